@@ -160,6 +160,94 @@ kda_status kda_decode(long long n_req, long long H, long long groups, float scal
                       const float* A_log, const float* dt_bias,
                       float* state, kda_bf16* o, void* stream);
 
+/* ------------------------------------------------ linear attention, one decay per head
+ *
+ * Per sequence n and value head h, with gamma_h = exp(log_decay[h]) and a value-first
+ * fp32 state S in R^{V x K} (K = V = 128):
+ *   S_t = gamma_h S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t
+ * (no normalisation of q and k, no gate, no delta rule: the cheaper token mixer next to
+ * kda_fwd / kda_bwd / kda_decode, with their layouts and conventions).
+ *
+ * log_decay is a fixed slope of the model, [H] fp32 in device memory: it gets no
+ * gradient. 0 is plain linear attention, -inf keeps no memory (o_t = scale (q_t.k_t) v_t).
+ * A positive value makes the state grow; nothing checks it.
+ * Rounding: products of bf16 inputs and all sums are taken in fp32; the decayed scores
+ * and, where a chunk reads it, the state are rounded to bf16 once each as operands of a
+ * product. The state itself and hT, dh0 are fp32-accurate.
+ * Inputs are expected to be finite. An infinity or NaN in a token reaches the outputs of
+ * its own sequence and head only, of tokens up to 127 before it among them (they share
+ * its chunk). */
+typedef struct {
+    int64_t B;      /* fixed-length batch rows; 1 when packed */
+    int64_t T;      /* tokens per row; total tokens when packed */
+    int64_t H;      /* value heads */
+    int64_t N;      /* sequences: B when cu_seqlens is NULL, else len(cu_seqlens) - 1 */
+    int32_t K;      /* key dimension, must be 128 */
+    int32_t V;      /* value dimension, must be 128 */
+    float scale;    /* output scale, finite and > 0 */
+    int32_t groups; /* value heads per query/key head, as in kda_shape (0 is read as 1) */
+} kda_linattn_shape;
+
+/* Bytes of workspace kda_linattn_fwd (backward = 0) or kda_linattn_bwd (backward = 1)
+ * needs for this shape; 0 for an invalid shape. The backward's size serves both. */
+size_t kda_linattn_workspace_size(const kda_linattn_shape* shape, int backward);
+
+/* Forward over whole prompts. q, k [B*T, H/G, 128], v [B*T, H, 128] bf16; h0 (NULL = 0)
+ * and hT (NULL = not wanted) [N, H, 128, 128] fp32; o [B*T, H, 128] bf16. The workspace
+ * holds nothing between calls. Host checks and their codes are those of kda_fwd; a
+ * malformed cu_seqlens or a wait that gave up is found on the device and reported by
+ * kda_get_device_status(workspace, stream). */
+kda_status kda_linattn_fwd(const kda_linattn_shape* shape,
+                           const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                           const float* log_decay, const float* h0, const int64_t* cu_seqlens,
+                           kda_bf16* o, float* hT,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_t <o_t, do_t> + <S_T, dhT> with respect to q, k, v and h0. It
+ * recomputes what it needs from the inputs: no call of kda_linattn_fwd has to come
+ * before it. dq, dk [B*T, H/G, 128] bf16 are the sums over each group of value heads
+ * (fixed order), dv [B*T, H, 128] bf16, dh0 [N, H, 128, 128] fp32 (NULL = not wanted).
+ * Bitwise reproducible. */
+kda_status kda_linattn_bwd(const kda_linattn_shape* shape,
+                           const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                           const float* log_decay, const float* h0, const int64_t* cu_seqlens,
+                           const kda_bf16* do_, const float* dhT,
+                           kda_bf16* dq, kda_bf16* dk, kda_bf16* dv, float* dh0,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of n_req requests: advances the state [n_req, H, 128, 128] fp32 in
+ * place and writes o [n_req, H, 128] bf16. q, k [n_req, H/groups, 128], v [n_req, H, 128]
+ * bf16. Checks and codes as in kda_decode. */
+kda_status kda_linattn_decode(long long n_req, long long H, long long groups, float scale,
+                              const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
+                              const float* log_decay, float* state, kda_bf16* o, void* stream);
+
+/* ---------------------------------------------------------------- layer norm over rows
+ *
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * x, y, dy, dx: [rows, width] contiguous, all KDA_BF16 or all KDA_FP32. weight, bias,
+ * dweight, dbias: [width] fp32; mean, rstd: [rows] fp32. weight = NULL reads as 1,
+ * bias = NULL as 0. Statistics and sums are fp32. Any width from 1 to 2^20; every
+ * pointer 16-byte aligned. */
+typedef enum { KDA_BF16 = 0, KDA_FP32 = 1 } kda_dtype;
+
+/* Forward. mean and rstd are written for the backward pass; NULL where not wanted. */
+kda_status kda_layernorm_fwd(long long rows, long long width, int dtype, float eps,
+                             const void* x, const float* weight, const float* bias,
+                             void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace kda_layernorm_bwd needs; 0 for an invalid size. */
+size_t kda_layernorm_workspace_size(long long rows, long long width);
+
+/* Backward, with the mean and rstd of the forward. dweight = sum_rows dy * xhat and
+ * dbias = sum_rows dy (NULL where not wanted) are written, not accumulated, summed in a
+ * fixed order. */
+kda_status kda_layernorm_bwd(long long rows, long long width, int dtype,
+                             const void* x, const void* dy, const float* weight,
+                             const float* mean, const float* rstd,
+                             void* dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream` and returns the device status word of `workspace`
  * (KDA_OK, KDA_ERR_OFFSETS, KDA_ERR_TIMEOUT or KDA_ERR_STALE_WORKSPACE), or
  * KDA_ERR_CUDA if the stream reported an error. Clears nothing. */

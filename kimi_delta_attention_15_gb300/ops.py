@@ -41,6 +41,12 @@ class Shape(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("chunk_size", ctypes.c_int32)]
 
 
+class LinattnShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("groups", ctypes.c_int32)]
+
+
 def lib_path() -> str:
     return _build.LIB
 
@@ -82,6 +88,20 @@ def load(build_if_missing: bool = True):
         lib.kda_diag_umma_selftest.restype = ctypes.c_int
         lib.kda_decode.argtypes = [ctypes.c_longlong] * 3 + [ctypes.c_float, ctypes.c_float] + [P] * 10
         lib.kda_decode.restype = ctypes.c_int
+        lib.kda_linattn_workspace_size.argtypes = [ctypes.POINTER(LinattnShape), ctypes.c_int]
+        lib.kda_linattn_workspace_size.restype = S
+        lib.kda_linattn_fwd.argtypes = [ctypes.POINTER(LinattnShape)] + [P] * 9 + [S, P]
+        lib.kda_linattn_fwd.restype = ctypes.c_int
+        lib.kda_linattn_bwd.argtypes = [ctypes.POINTER(LinattnShape)] + [P] * 13 + [S, P]
+        lib.kda_linattn_bwd.restype = ctypes.c_int
+        lib.kda_linattn_decode.argtypes = [ctypes.c_longlong] * 3 + [ctypes.c_float] + [P] * 7
+        lib.kda_linattn_decode.restype = ctypes.c_int
+        lib.kda_layernorm_fwd.argtypes = [ctypes.c_longlong] * 2 + [ctypes.c_int, ctypes.c_float] + [P] * 7
+        lib.kda_layernorm_fwd.restype = ctypes.c_int
+        lib.kda_layernorm_workspace_size.argtypes = [ctypes.c_longlong] * 2
+        lib.kda_layernorm_workspace_size.restype = S
+        lib.kda_layernorm_bwd.argtypes = [ctypes.c_longlong] * 2 + [ctypes.c_int] + [P] * 9 + [S, P]
+        lib.kda_layernorm_bwd.restype = ctypes.c_int
         lib.kda_diag_tf32_round.argtypes = [P, P, P, ctypes.c_longlong, P]
         lib.kda_diag_tf32_round.restype = ctypes.c_int
         _lib = lib
@@ -277,6 +297,159 @@ def decode(q, k, v, g_raw, beta_raw, A_log, dt_bias, state, *, o=None, scale: fl
                              _ptr(A_log), _ptr(dt_bias), _ptr(state), _ptr(o), _stream_handle(stream))
     _check(code, "kda_decode")
     return o
+
+
+def linattn_shape(T: int, H: int, N: int, B: int = 1, scale: float = SCALE, groups: int = 1) -> LinattnShape:
+    """Shape of the linear attention with a decay for each head; H counts value heads."""
+    return LinattnShape(B=B, T=T, H=H, N=N, K=128, V=128, scale=scale, groups=groups)
+
+
+def _linattn_shape_of(q, v, cu_seqlens, B, scale):
+    sh = _shape_of(q, v, cu_seqlens, B, scale, LOWER_BOUND)
+    return linattn_shape(sh.T, sh.H, sh.N, sh.B, scale, sh.groups)
+
+
+def linattn_workspace_size(shape: LinattnShape, backward: bool = False) -> int:
+    return int(load().kda_linattn_workspace_size(ctypes.byref(shape), int(backward)))
+
+
+def linattn_alloc_workspace(shape: LinattnShape, device, backward: bool = False) -> torch.Tensor:
+    return torch.empty(linattn_workspace_size(shape, backward), dtype=torch.uint8, device=device)
+
+
+def _linattn_specs(shape, q, k, v, log_decay, h0, cu_seqlens):
+    tok, H, N = shape.B * shape.T, shape.H, shape.N
+    Hqk = H // max(int(shape.groups), 1)
+    bf, f32 = torch.bfloat16, torch.float32
+    return [("q", q, tok * Hqk * 128, bf, False), ("k", k, tok * Hqk * 128, bf, False),
+            ("v", v, tok * H * 128, bf, False), ("log_decay", log_decay, H, f32, False),
+            ("h0", h0, N * H * 128 * 128, f32, True), ("cu_seqlens", cu_seqlens, N + 1, torch.int64, True)]
+
+
+def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, B: int = 1, scale: float = SCALE, workspace=None,
+                o=None, hT=None, want_hT: bool = True, stream=None):
+    """kda_linattn_fwd: S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t. Token tensors
+    [T, H, 128] bf16 (or [B, T, H, 128]; q, k may hold H / groups heads); log_decay [H] fp32.
+    Returns (o, hT, workspace)."""
+    lib = load()
+    shape = _linattn_shape_of(q, v, cu_seqlens, B, scale)
+    if workspace is None:
+        workspace = linattn_alloc_workspace(shape, q.device)
+    if o is None:
+        o = torch.empty_like(v)
+    if hT is None and want_hT:
+        hT = torch.empty(shape.N, shape.H, 128, 128, dtype=torch.float32, device=q.device)
+    _validate(_linattn_specs(shape, q, k, v, log_decay, h0, cu_seqlens)
+              + [("o", o, v.numel(), torch.bfloat16, False),
+                 ("hT", hT, shape.N * shape.H * 128 * 128, torch.float32, True),
+                 ("workspace", workspace, None, torch.uint8, False)])
+    code = lib.kda_linattn_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
+                               _ptr(cu_seqlens), _ptr(o), _ptr(hT), _ptr(workspace), workspace.numel(),
+                               _stream_handle(stream))
+    _check(code, "kda_linattn_fwd")
+    return o, hT, workspace
+
+
+def linattn_bwd(q, k, v, log_decay, do, workspace=None, h0=None, cu_seqlens=None, dhT=None, *, B: int = 1,
+                scale: float = SCALE, grads=None, want_dh0: bool = True, stream=None):
+    """kda_linattn_bwd: gradients of sum <o, do> + <hT, dhT>. It recomputes what it needs, so any
+    workspace of linattn_alloc_workspace(shape, device, backward=True) serves; pass one to read
+    device_status(workspace) afterwards. Returns a dict of dq, dk, dv and dh0."""
+    lib = load()
+    shape = _linattn_shape_of(q, v, cu_seqlens, B, scale)
+    if workspace is None:
+        workspace = linattn_alloc_workspace(shape, q.device, backward=True)
+    state = shape.N * shape.H * 128 * 128
+    bf, f32 = torch.bfloat16, torch.float32
+    if grads is None:
+        grads = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                     dh0=torch.empty(shape.N, shape.H, 128, 128, dtype=f32, device=q.device) if want_dh0 else None)
+    _validate(_linattn_specs(shape, q, k, v, log_decay, h0, cu_seqlens)
+              + [("do", do, v.numel(), bf, False), ("dhT", dhT, state, f32, True),
+                 ("dq", grads.get("dq"), q.numel(), bf, False), ("dk", grads.get("dk"), q.numel(), bf, False),
+                 ("dv", grads.get("dv"), v.numel(), bf, False), ("dh0", grads.get("dh0"), state, f32, True),
+                 ("workspace", workspace, None, torch.uint8, False)])
+    code = lib.kda_linattn_bwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
+                               _ptr(cu_seqlens), _ptr(do), _ptr(dhT), _ptr(grads["dq"]), _ptr(grads["dk"]),
+                               _ptr(grads["dv"]), _ptr(grads.get("dh0")), _ptr(workspace), workspace.numel(),
+                               _stream_handle(stream))
+    _check(code, "kda_linattn_bwd")
+    return grads
+
+
+def linattn_decode(q, k, v, log_decay, state, *, o=None, scale: float = SCALE, stream=None):
+    """kda_linattn_decode: one token per request. v [n_req, H, 128] bf16, q, k [n_req, H / groups, 128]
+    bf16; `state` [n_req, H, 128, 128] fp32 is updated in place. Returns o [n_req, H, 128] bf16."""
+    n_req, H, Hqk = int(v.shape[0]), int(v.shape[1]), int(q.shape[1])
+    if Hqk <= 0 or H % Hqk != 0:
+        raise ValueError(f"value heads ({H}) must be a multiple of query/key heads ({Hqk})")
+    if o is None:
+        o = torch.empty_like(v)
+    lib = load()
+    bf, f32 = torch.bfloat16, torch.float32
+    _validate([("q", q, n_req * Hqk * 128, bf, False), ("k", k, n_req * Hqk * 128, bf, False),
+               ("v", v, n_req * H * 128, bf, False), ("log_decay", log_decay, H, f32, False),
+               ("state", state, n_req * H * 128 * 128, f32, False), ("o", o, n_req * H * 128, bf, False)])
+    code = lib.kda_linattn_decode(n_req, H, H // Hqk, scale, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
+                                  _ptr(o), _stream_handle(stream))
+    _check(code, "kda_linattn_decode")
+    return o
+
+
+_NORM_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _norm_size(x):
+    if x.dtype not in _NORM_DTYPES:
+        raise ValueError(f"x: dtype {x.dtype}, expected bfloat16 or float32")
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"x: shape {tuple(x.shape)} has no row to normalise")
+    width = int(x.shape[-1])
+    return x.numel() // width, width
+
+
+def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, mean=None, rstd=None, stream=None):
+    """kda_layernorm_fwd over the last dimension. x bf16 or fp32, weight and bias [width] fp32 or
+    None. Returns (y, mean, rstd); mean and rstd [rows] fp32 are what layernorm_bwd reads."""
+    rows, width = _norm_size(x)
+    f32 = torch.float32
+    if y is None:
+        y = torch.empty_like(x)
+    if mean is None:
+        mean = torch.empty(rows, dtype=f32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=f32, device=x.device)
+    lib = load()
+    _validate([("x", x, None, None, False), ("weight", weight, width, f32, True), ("bias", bias, width, f32, True),
+               ("y", y, x.numel(), x.dtype, False), ("mean", mean, rows, f32, False), ("rstd", rstd, rows, f32, False)])
+    code = lib.kda_layernorm_fwd(rows, width, _NORM_DTYPES[x.dtype], eps, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                 _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    _check(code, "kda_layernorm_fwd")
+    return y, mean, rstd
+
+
+def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool = True, want_dbias: bool = True,
+                  workspace=None, stream=None):
+    """kda_layernorm_bwd with the mean and rstd of layernorm_fwd (weight None reads as 1). Returns a
+    dict of dx (dtype of x), dweight and dbias ([width] fp32)."""
+    rows, width = _norm_size(x)
+    f32 = torch.float32
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(int(lib.kda_layernorm_workspace_size(rows, width)), dtype=torch.uint8, device=x.device)
+    if grads is None:
+        grads = dict(dx=torch.empty_like(x),
+                     dweight=torch.empty(width, dtype=f32, device=x.device) if want_dweight else None,
+                     dbias=torch.empty(width, dtype=f32, device=x.device) if want_dbias else None)
+    _validate([("x", x, None, None, False), ("dy", dy, x.numel(), x.dtype, False), ("weight", weight, width, f32, True),
+               ("mean", mean, rows, f32, False), ("rstd", rstd, rows, f32, False),
+               ("dx", grads.get("dx"), x.numel(), x.dtype, False), ("dweight", grads.get("dweight"), width, f32, True),
+               ("dbias", grads.get("dbias"), width, f32, True), ("workspace", workspace, None, torch.uint8, False)])
+    code = lib.kda_layernorm_bwd(rows, width, _NORM_DTYPES[x.dtype], _ptr(x), _ptr(dy), _ptr(weight), _ptr(mean),
+                                 _ptr(rstd), _ptr(grads["dx"]), _ptr(grads.get("dweight")), _ptr(grads.get("dbias")),
+                                 _ptr(workspace), workspace.numel(), _stream_handle(stream))
+    _check(code, "kda_layernorm_bwd")
+    return grads
 
 
 def device_status(workspace, stream=None) -> int:
