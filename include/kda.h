@@ -194,7 +194,8 @@ size_t kda_linattn_workspace_size(const kda_linattn_shape* shape, int backward);
 
 /* Forward over whole prompts. q, k [B*T, H/G, 128], v [B*T, H, 128] bf16; h0 (NULL = 0)
  * and hT (NULL = not wanted) [N, H, 128, 128] fp32; o [B*T, H, 128] bf16. The workspace
- * holds nothing between calls. Host checks and their codes are those of kda_fwd; a
+ * holds nothing between calls. Host checks and their codes are those of kda_fwd, and
+ * N * H >= 2^28 gives KDA_ERR_SHAPE; a
  * malformed cu_seqlens or a wait that gave up is found on the device and reported by
  * kda_get_device_status(workspace, stream). */
 kda_status kda_linattn_fwd(const kda_linattn_shape* shape,

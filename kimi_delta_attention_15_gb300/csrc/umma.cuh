@@ -209,6 +209,16 @@ __device__ __forceinline__ void tmem_st32_issue(uint32_t taddr, const uint32_t (
         "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+// 32 lanes x 16 consecutive columns; the same rule for v until tmem_wait_st_all
+__device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st_all() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // wait for this thread's TMEM stores; r (the source of one of them) may change afterwards
 __device__ __forceinline__ void tmem_wait_st(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::st.sync.aligned;" : KDA_TMEM_REGS32(r) : : "memory");
@@ -260,6 +270,36 @@ __device__ __forceinline__ void umma_tf32_ta(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+// Instruction descriptor for kind::f16 with bf16 operands and fp32 accumulation.
+// a_mn / b_mn: 0 = operand is K-major, 1 = MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4)                       // D format: f32
+           | (1u << 7)                     // A format: bf16
+           | (1u << 10)                    // B format: bf16
+           | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A * B^T in bf16, one instruction (K = 16). Issued by one thread.
+__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in tensor memory: lane m holds row m, the 8 columns from a_tmem the 16 K
+// values of this step, two to a column.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive on the mbarrier once every previously issued MMA of this thread has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -302,5 +342,18 @@ __device__ __forceinline__ uint32_t tf32_round_bits(float x) {
     return (__float_as_uint(x) + (x != x ? 0u : 0x1000u)) & 0xffffe000u;
 }
 __device__ __forceinline__ float tf32_round(float x) { return __uint_as_float(tf32_round_bits(x)); }
+
+// bf16 operand tiles of R rows x 128 columns: panels of 64 columns (128 bytes per row), each
+// panel [R][64] contiguous with the same 128-byte swizzle. Byte offset of the 16-byte chunk
+// (8 columns) ch = 0 .. 15 of row r:
+__host__ __device__ __forceinline__ uint32_t panel_off_bf16(uint32_t r, uint32_t ch, uint32_t R) {
+    return (ch >> 3) * R * 128u + r * 128u + (((ch & 7u) ^ (r & 7u)) << 4);
+}
+// k-step s of such a tile as an operand [MN columns][K rows] (MN-major): rows 16 s .. 16 s + 15.
+// 64-column panels along MN are R * 128 bytes apart, 8-row groups along K 1024 bytes. (As a
+// K-major operand, [MN rows][K columns], its step s of 16 columns has desc_kmajor's descriptor.)
+__device__ __forceinline__ uint64_t desc_mnmajor_bf16(uint32_t tile_saddr, uint32_t R, uint32_t s) {
+    return sdesc_sw128(tile_saddr + s * 2048u, R * 128u, 1024u);
+}
 
 }  // namespace kda

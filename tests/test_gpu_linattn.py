@@ -123,6 +123,17 @@ def test_a_long_sequence_on_few_heads():
     check_all(d, run(d))
 
 
+@pytest.mark.parametrize("n,H,G", [(60, 8, 2), (3, 120, 1)])
+def test_more_units_than_multiprocessors(n, H, G):
+    """Each persistent block goes through several (sequence, head) pairs of one or two chunks, some empty."""
+    gen = torch.Generator().manual_seed(n)
+    lens = tuple(int(x) for x in torch.randint(0, 260, (n,), generator=gen))
+    d = O.make(lens, H, G, seed=n, h0=True, dhT=True)
+    check_all(d, run(d))
+    d = O.make(lens, H, G, seed=n)
+    check_all(d, run(d))
+
+
 def test_outputs_not_wanted():
     d = dev(O.make((130,), 2, seed=13))
     args = (d["q"], d["k"], d["v"], d["log_decay"])
