@@ -12,6 +12,7 @@
 //   reversed  S <- S + v k^T,  out = S q,   S <- gamma S
 #include <cmath>
 #include <cstdio>
+#include <cuda.h>
 #include "kda_internal.cuh"
 #include "umma.cuh"
 
@@ -31,8 +32,7 @@ constexpr uint32_t kTile = LC * D * 2;        // a bf16 operand tile [128][128],
 //   out_i = out_scale (sum_{j <= i} k_scale gamma^{i-j} (q_i . k_j) v_j + gamma^{i+e} S q_i)
 //   S    <- gamma^L S + sum_j k_scale gamma^{L-e-j} v_j k_j^T
 struct LinJob {
-    const uint16_t *q, *k, *v;   // [tokens, H / g?, 128]
-    int gq, gk, gv;              // value heads that share a head of each
+    int q, k, v;                 // which of LinArgs' tensors
     uint16_t* out;               // [tokens, H, 128] bf16, or
     float* share;                // [tokens, H, 128] fp32: each value head's share of a grouped sum
     const float* s_in;           // initial state [N, H, 128, 128], may be NULL
@@ -52,6 +52,8 @@ struct Slot {
 };
 
 struct LinArgs {
+    CUtensorMap map[4];          // [tokens, H / group, 128] bf16 in boxes of 128 tokens x 64 channels
+    int group[4];                // value heads that share a head of each
     LinJob job[3];
     int jobs;
     int state_only;              // the segments' own states to seg, nothing else
@@ -80,37 +82,48 @@ __device__ __forceinline__ Slot slot_of(const LinArgs& a, int i) {
     return s;
 }
 
+// Held by value: the kernel's loops store to shared memory, and a pointer into the parameters would
+// be read again after every store.
 struct Unit {
-    const LinJob* job;
     int64_t t0;
-    int len, h;
-    size_t seq_state, seg_state;   // element offsets of the (sequence, head) and (slot, head) states
+    int len, h, rev;
+    int q, k, v;                   // tensors
+    uint16_t* out;
+    float* share;
+    float k_scale, out_scale, g;   // g: log decay
+    int pieces;
     const float* s_in;             // where this unit's state comes from and goes to, NULL: zero, not wanted
     float* s_out;
     int s_in_t;
 };
 __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     const int per = a.jobs * a.H;
-    const int i = u / per, r = u - i * per;
+    const int i = u / per, r = u - i * per, ji = r / a.H;
     const Slot s = slot_of(a, i);
+    const LinJob j = a.job[ji];
     Unit x;
-    x.job = &a.job[r / a.H];
-    x.h = r % a.H;
+    x.h = r - ji * a.H;
     x.t0 = s.t0;
     x.len = s.len;
-    x.seq_state = ((size_t)s.seq * a.H + x.h) * D * D;
-    x.seg_state = ((size_t)i * a.H + x.h) * D * D;
-    const LinJob& j = *x.job;
+    x.rev = j.rev;
+    x.q = j.q; x.k = j.k; x.v = j.v;
+    x.out = j.out;
+    x.share = j.share;
+    x.k_scale = j.k_scale;
+    x.out_scale = j.out_scale;
+    x.g = a.log_decay[x.h];
+    x.pieces = j.pieces;
+    const size_t seq_state = ((size_t)s.seq * a.H + x.h) * D * D, seg_state = ((size_t)i * a.H + x.h) * D * D;
     const bool head = j.rev ? s.seg == s.nseg - 1 : s.seg == 0, tail = j.rev ? s.seg == 0 : s.seg == s.nseg - 1;
     if (a.state_only) {            // every segment but the last of its sequence starts from zero and leaves its sum
         x.s_in = nullptr;
         x.s_in_t = 0;
-        x.s_out = tail ? nullptr : j.seg + x.seg_state;
+        x.s_out = tail ? nullptr : j.seg + seg_state;
         if (tail) x.len = 0;
     } else {
-        x.s_in = head ? (j.s_in ? j.s_in + x.seq_state : nullptr) : j.seg + x.seg_state;
+        x.s_in = head ? (j.s_in ? j.s_in + seq_state : nullptr) : j.seg + seg_state;
         x.s_in_t = head ? j.s_in_t : j.seg_t;
-        x.s_out = tail && j.s_out ? j.s_out + x.seq_state : nullptr;
+        x.s_out = tail && j.s_out ? j.s_out + seq_state : nullptr;
     }
     return x;
 }
@@ -121,6 +134,22 @@ __device__ __forceinline__ int unit_at(int round) {
     return round * (int)gridDim.x + (int)((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+// Chunk c of a unit: rows are tokens t .. t + 127 in either direction, a reversed unit's chunks are
+// counted from its end; rows lo <= r < hi belong to the unit (fewer than 128 in its last chunk).
+struct Chunk {
+    int64_t t;
+    int lo, hi;
+};
+__device__ __forceinline__ Chunk chunk_of(const Unit& u, int c) {
+    const int left = u.len - c * LC;
+    Chunk x;
+    x.t = u.rev ? u.t0 + left - LC : u.t0 + (int64_t)c * LC;
+    x.lo = u.rev ? max(LC - left, 0) : 0;
+    x.hi = u.rev ? LC : min(left, LC);
+    return x;
+}
+__device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
+
 struct LinSmem {
     // operand tiles (bf16 panels, 1024-byte aligned)
     uint8_t K[2][kTile];     // keys by chunk parity; once scored, overwritten with the decayed keys' high parts
@@ -128,19 +157,23 @@ struct LinSmem {
     uint8_t V[kTile];
     uint8_t MID[kTile];      // the decayed keys' middle and low parts
     uint8_t LOW[kTile];
-    uint8_t S[kTile];        // the state [v][c] the chunk starts from, rounded to bf16
-    // full: operands in shared memory; qk, qs, pv, ds: MMA groups done; s, p, piece: operands written;
-    // o: accumulators read. Each completes one phase per chunk. A wait names a phase by its parity, so
-    // no waiter may be a whole phase behind: every wait comes before an arrival of the same thread
-    // (or an MMA that needs one) on which the barrier's next phase depends.
-    uint64_t full_qk, full_v, qk, qs, pv, ds, s, p, piece, o;
+    uint8_t S[kTile];        // the state [v][c] the chunk starts from, rounded to bf16; once read, the output rows
+    float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
+    // full: operands in shared memory; qk, qs, pv, ds: MMA groups done; s, p, piece: operands written.
+    // Each completes one phase per chunk (full_k: per two chunks).
+    // A wait names a phase by its parity, so no waiter may be a whole phase behind or ahead: every wait
+    // comes before an arrival of the same thread (or an MMA that needs one) on which the barrier's next
+    // phase depends, and after something that depends on the phase before.
+    uint64_t full_k[2], full_q, full_v, qk, qs, pv, ds, s, p, piece;
     uint32_t tmem;
 };
 
-// Warps 0-3: scores and outputs (thread = row of the chunk = TMEM lane). Warps 4-11: the state
-// (thread = half a row) and the decayed keys. Warps 12, 13: loads. Warp 14: MMAs.
-constexpr int kScoreWarps = 4, kStateWarps = 8, kLoadWarps = 2;
-constexpr int kLinThreads = 32 * (kScoreWarps + kStateWarps + kLoadWarps + 1);
+// Warps 0-3: scores (thread = row of the chunk = TMEM lane). Warps 4-11: the state, the decayed keys and
+// the outputs (thread = half a row). Warp 12: loads. Warp 13: MMAs. Warps 14, 15 complete a warpgroup,
+// the unit in which registers are handed over: 128 a thread at launch, 4 x (128 + 160 + 160 + 64) = 4 x 512.
+constexpr int kScoreWarps = 4, kMainWarps = 8;
+constexpr int kLinThreads = 512;
+constexpr int kMainRegs = 160, kIssueRegs = 64;
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, int n) {
     return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(n & 1)));
@@ -151,60 +184,80 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// two fp32 values in one 64-bit register, multiplied and added in one instruction
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 two(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 two(uint32_t a, uint32_t b) { return two(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f32x2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(f32x2 a) {
+    const float2 x = parts(a);
+    return pack_bf16(x.x, x.y);
+}
 
-// --- loads: cp.async, 16 bytes a thread, zeros for rows past the end of the segment
-__device__ void lin_load(const LinArgs& a, LinSmem& sm, int units) {
-    const int p = threadIdx.x - 32 * (kScoreWarps + kStateWarps);
-    const int ch = p & 15, r0 = p >> 4;      // its 16-byte chunk, rows r0 + 4 i
-    const uint32_t off[2] = {panel_off_bf16(r0, ch, LC), panel_off_bf16(r0 + 4, ch, LC)};
-    auto tile = [&](uint8_t* dst, const uint16_t* base, int heads, int head, const Unit& u, int c) {
-        const int64_t step = (u.job->rev ? -(int64_t)heads : (int64_t)heads) * D;
-        const int left = u.len - c * LC;
-        const int64_t first = u.job->rev ? u.t0 + u.len - 1 - c * LC : u.t0 + c * LC;
-        const uint16_t* src0 = base + (first * heads + head) * D + ch * 8;
-#pragma unroll
-        for (int i = 0; i < LC / 4; ++i) {
-            const int r = r0 + 4 * i;
-            cp_async16_zfill(dst + off[i & 1] + (i >> 1) * 1024, r < left ? src0 + r * step : base, r < left);
+// --- loads, one thread
+__device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int units) {
+    const bool state_only = a.state_only != 0;
+    struct At { int round, c, chunks; Unit u; bool more; };
+    auto settle = [&](At& x) {   // to the first unit from here on that has chunks
+        for (;; ++x.round) {
+            const int i = unit_at(x.round);
+            if (!(x.more = i < units)) return;
+            x.u = unit_of(a, i);
+            if ((x.chunks = chunks_of(x.u)) > 0) return;
         }
-        cp_async_commit();
     };
+    auto tile = [&](uint8_t* dst, int which, const At& x, uint64_t* bar) {
+        const Chunk k = chunk_of(x.u, x.c);
+        const int head = x.u.h / a.group[which];
+        mbar_arrive_expect_tx(bar, kTile);
+        tma_load_3d(dst, &a.map[which], 0, head, (int)k.t, bar);
+        tma_load_3d(dst + kTile / 2, &a.map[which], 64, head, (int)k.t, bar);
+    };
+    At x;
+    x.round = x.c = 0;
+    settle(x);
+    if (x.more) tile(sm.K[0], x.u.k, x, &sm.full_k[0]);
     bool ok = true;
     int n = 0;
-    bool have_k = false;      // this chunk's keys were requested with the chunk before
-    for (int round = 0; ok; ++round) {
-        const int at = unit_at(round);
-        if (at >= units) break;
-        const Unit u = unit_of(a, at);
-        const LinJob& j = *u.job;
-        const int chunks = (u.len + LC - 1) / LC;
-        const int hq = a.H / j.gq, hk = a.H / j.gk, hv = a.H / j.gv;
-        for (int c = 0; c < chunks; ++c, ++n) {
-            // K[n & 1] was last read by the state product of chunk n - 2, which this thread waited for
-            // with the V of chunk n - 1
-            if (!have_k) tile(sm.K[n & 1], j.k, hk, u.h / j.gk, u, c);
-            if (n > 0 && !wait_warp(&sm.qs, n - 1)) { ok = false; break; }
-            if (!a.state_only) tile(sm.Q, j.q, hq, u.h / j.gq, u, c);
-            cp_async_wait_all();
-            fence_async_smem();
-            mbar_arrive(&sm.full_qk);
-            if (n > 0 && !wait_warp(&sm.ds, n - 1)) { ok = false; break; }
-            tile(sm.V, j.v, hv, u.h / j.gv, u, c);
-            have_k = c + 1 < chunks;
-            if (have_k) tile(sm.K[(n + 1) & 1], j.k, hk, u.h / j.gk, u, c + 1);
-            if (have_k) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else cp_async_wait_all();
-            fence_async_smem();
-            mbar_arrive(&sm.full_v);
+    for (; x.more; ++n) {
+        if (n > 0 && !(ok = mbar_wait(&sm.qs, (uint32_t)((n - 1) & 1)))) break;
+        if (!state_only) tile(sm.Q, x.u.q, x, &sm.full_q);
+        else mbar_arrive(&sm.full_q);
+        if (n > 0 && !(ok = mbar_wait(&sm.ds, (uint32_t)((n - 1) & 1)))) break;
+        tile(sm.V, x.u.v, x, &sm.full_v);
+        if (++x.c == x.chunks) {
+            ++x.round;
+            x.c = 0;
+            settle(x);
         }
+        // K[(n + 1) & 1] was last read by the state product of chunk n - 1
+        if (x.more) tile(sm.K[(n + 1) & 1], x.u.k, x, &sm.full_k[(n + 1) & 1]);
     }
-    cp_async_wait_all();
     if (!ok) raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
 // --- MMAs, one thread. TMEM: scores (and their bf16 copy, two to a column), Q S^T, scores V, state sum
 constexpr uint32_t kColP = 0, kColQS = 128, kColPV = 256, kColDS = 384;
-__device__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+__device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+    const bool state_only = a.state_only != 0;
     constexpr uint32_t kk = idesc_bf16(128, 128, 0, 0), kn = idesc_bf16(128, 128, 0, 1), mn = idesc_bf16(128, 128, 1, 1);
     const uint32_t q = smem_u32(sm.Q), v = smem_u32(sm.V), st = smem_u32(sm.S);
     const uint32_t mid = smem_u32(sm.MID), low = smem_u32(sm.LOW);
@@ -214,29 +267,28 @@ __device__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
         const int at = unit_at(round);
         if (at >= units) break;
         const Unit u = unit_of(a, at);
-        const int chunks = (u.len + LC - 1) / LC;
+        const int chunks = chunks_of(u);
         for (int c = 0; c < chunks; ++c, ++n) {
             const uint32_t ph = (uint32_t)(n & 1), k = smem_u32(sm.K[n & 1]);
-            if (!(ok = mbar_wait(&sm.full_qk, ph))) break;
-            tc_fence_after();
-            if (!a.state_only)
+            if (!(ok = mbar_wait(&sm.full_k[n & 1], (uint32_t)((n >> 1) & 1)) && mbar_wait(&sm.full_q, ph))) break;
+            if (!state_only)
                 for (int s = 0; s < 8; ++s) umma_bf16(tm + kColP, desc_kmajor(q, LC, s), desc_kmajor(k, LC, s), kk, s > 0);
             umma_commit(&sm.qk);
-            if (!(ok = mbar_wait(&sm.s, ph) && (n == 0 || mbar_wait(&sm.o, ph ^ 1u)))) break;
+            if (!(ok = mbar_wait(&sm.s, ph))) break;   // and chunk n - 1's accumulators have been read
             tc_fence_after();
-            if (!a.state_only && (c > 0 || u.s_in))
+            if (!state_only && (c > 0 || u.s_in))
                 for (int s = 0; s < 8; ++s) umma_bf16(tm + kColQS, desc_kmajor(q, LC, s), desc_kmajor(st, LC, s), kk, s > 0);
             umma_commit(&sm.qs);
             if (!(ok = mbar_wait(&sm.p, ph) && mbar_wait(&sm.full_v, ph))) break;
             tc_fence_after();
-            if (!a.state_only)
+            if (!state_only)
                 for (int s = 0; s < 8; ++s) umma_bf16_ta(tm + kColPV, tm + kColP + 8 * s, desc_mnmajor_bf16(v, LC, s), kn, s > 0);
             umma_commit(&sm.pv);
             if (!(ok = mbar_wait(&sm.piece, ph))) break;
             tc_fence_after();
             if (c + 1 < chunks || u.s_out) {   // small parts first: the accumulator is rounded at its size
                 uint32_t acc = 0;
-                if (u.job->pieces > 2)
+                if (u.pieces > 2)
                     for (int s = 0; s < 8; ++s, acc = 1)
                         umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(low, LC, s), mn, acc);
                 for (int s = 0; s < 8; ++s, acc = 1)
@@ -254,207 +306,287 @@ __device__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     }
 }
 
-// --- scores -> decayed bf16 scores in TMEM; outputs
-__device__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+// --- scores -> decayed bf16 scores in TMEM
+__device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+    const bool state_only = a.state_only != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x;
-    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
+    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16) + kColP;
+    float* const diag = sm.diag[warp];
     bool ok = true;
     int n = 0;
     for (int round = 0; ok; ++round) {
         const int at = unit_at(round);
         if (at >= units) break;
         const Unit u = unit_of(a, at);
-        const LinJob& j = *u.job;
-        const int chunks = (u.len + LC - 1) / LC;
+        const int chunks = chunks_of(u);
         if (chunks == 0) continue;
-        const float g = a.log_decay[u.h];
-        // k_scale gamma^{row-j}: in the 32-column block left of the diagonal's by 32 m columns it is
-        // gamma^{32m-31} f[j mod 32], f[x] = k_scale gamma^{lane+31-x}: no exponent is negative
-        float f[32];
+        const float g = u.g;
+        const bool rev = u.rev != 0;
+        // k_scale gamma^{|row - col|}, row = 32 warp + lane, col = 32 b + x. Off the diagonal's block it is
+        // gamma^{32 |warp - b| - 31} f[x], f[x] = k_scale gamma^{31 + lane - x} (reversed: 31 - lane + x): no
+        // exponent is negative. On it, diag[lane - x + 31].
+        f32x2 f[16];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) f[x] = j.k_scale * decay_pow(g, lane + 31 - x);
-        const float own = j.k_scale * decay_pow(g, lane);
-        const float w_state = decay_pow(g, row + (j.rev ? 0 : 1));
+        for (int x = 0; x < 16; ++x)
+            f[x] = two(u.k_scale * decay_pow(g, 31 + (rev ? 2 * x - lane : lane - 2 * x)),
+                       u.k_scale * decay_pow(g, 31 + (rev ? 2 * x + 1 - lane : lane - 2 * x - 1)));
+        __syncwarp();
+        diag[31 + lane] = diag[31 - lane] = u.k_scale * decay_pow(g, lane);
+        __syncwarp();
+        const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // columns that count in its block
+        const float far1 = decay_pow(g, 1), far2 = decay_pow(g, 33), far3 = decay_pow(g, 65);
         for (int c = 0; c < chunks; ++c, ++n) {
             if (!(ok = wait_warp(&sm.qk, n))) break;
             tc_fence_after();
-            if (!a.state_only) {
-#pragma unroll
+            if (!state_only) {
+#pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     uint32_t w[16];
-                    if (b > warp) {
+                    const int away = rev ? b - warp : warp - b;
+                    if (away < 0) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) w[x] = 0u;
                     } else {
                         uint32_t r[32];
-                        tmem_ld32_issue(lanes + kColP + 32 * b, r);
-                        if (b < warp) {
-                            const float base = decay_pow(g, 32 * (warp - b) - 31);
+                        tmem_ld32_issue(lanes + 32 * b, r);
+                        if (away > 0) {
+                            const float base = away == 1 ? far1 : away == 2 ? far2 : far3;
+                            const f32x2 base2 = two(base, base);
                             tmem_wait_ld(r);
 #pragma unroll
-                            for (int x = 0; x < 32; x += 2)
-                                w[x >> 1] = pack_bf16(__uint_as_float(r[x]) * (base * f[x]), __uint_as_float(r[x + 1]) * (base * f[x + 1]));
+                            for (int x = 0; x < 16; ++x) w[x] = pack_bf16(mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x])));
                         } else {
+                            const float* const d = diag + 31 + lane;
                             tmem_wait_ld(r);
 #pragma unroll
-                            for (int x = 0; x < 32; x += 2) {
-                                const float d0 = __shfl_up_sync(0xffffffffu, own, x), d1 = __shfl_up_sync(0xffffffffu, own, x + 1);
-                                w[x >> 1] = pack_bf16(x <= lane ? __uint_as_float(r[x]) * d0 : 0.0f,
-                                                      x + 1 <= lane ? __uint_as_float(r[x + 1]) * d1 : 0.0f);
+                            for (int x = 0; x < 16; ++x) {
+                                const float p0 = __uint_as_float(r[2 * x]) * d[-2 * x], p1 = __uint_as_float(r[2 * x + 1]) * d[-2 * x - 1];
+                                w[x] = pack_bf16((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
                             }
                         }
                     }
-                    tmem_st16_issue(lanes + kColP + 16 * b, w);   // behind the columns still to be read
+                    tmem_st16_issue(lanes + 16 * b, w);   // behind the columns still to be read
                 }
                 tmem_wait_st_all();
             }
-            tc_fence_before();
-            mbar_arrive(&sm.p);
-            if (!(ok = wait_warp(&sm.pv, n))) break;
-            tc_fence_after();
-            if (!a.state_only) {
-                const bool carried = c > 0 || u.s_in;
-                const int idx = c * LC + row;
-                const int64_t t = j.rev ? u.t0 + u.len - 1 - idx : u.t0 + idx;
-                const size_t at_out = (size_t)(t * a.H + u.h) * D;
+            const Chunk k = chunk_of(u, c);
+            if (k.hi - k.lo < LC) {   // rows of a neighbour in V: their scores are zero, and zero times an infinity is not
+                if (!(ok = wait_warp(&sm.full_v, n))) break;
+                if (row < k.lo || row >= k.hi)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t x[32], y[32];
-                    tmem_ld32_issue(lanes + kColPV + 32 * b, x);
-                    if (carried) tmem_ld32_issue(lanes + kColQS + 32 * b, y);
-                    tmem_wait_ld(x);
-                    if (carried) {
-                        tmem_after_wait(y);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = __float_as_uint(j.out_scale * (__uint_as_float(x[i]) + w_state * __uint_as_float(y[i])));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(j.out_scale * __uint_as_float(x[i]));
-                    }
-                    if (idx < u.len) {
-                        if (j.share) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4*>(j.share + at_out + 32 * b + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) w[e] = pack_bf16(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1]));
-                                *reinterpret_cast<uint4*>(j.out + at_out + 32 * b + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
-                    }
-                }
+                    for (int ch = 0; ch < 16; ++ch)
+                        *reinterpret_cast<uint4*>(sm.V + panel_off_bf16(row, ch, LC)) = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
             }
             tc_fence_before();
-            mbar_arrive(&sm.o);
+            mbar_arrive(&sm.p);
         }
     }
     if (!ok && lane == 0) raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
-// --- state in registers, its bf16 copy for the next chunk; decayed keys in bf16 parts
-__device__ void lin_state(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
-    const int t = threadIdx.x - 32 * kScoreWarps, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = 32 * (warp & 3) + lane, half = t >> 7;       // state row, which 64 columns of it
-    const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16) + kColDS + 64 * half;
+// w x as a sum of bf16 parts: 16 significant bits in two, 24 in three. x: eight bf16 values.
+__device__ __forceinline__ void split_two(float w, const uint32_t (&x)[4], uint32_t (&hi)[4], uint32_t (&mi)[4]) {
+    // w = w1 + w2; w1 x = hi + e without error (e, the error of a rounded product, has 8 bits); mid = w2 x + e
+    const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
+    const __nv_bfloat162 a = __bfloat162bfloat162(w1), b = __bfloat162bfloat162(w2);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&x[d]);
+        const __nv_bfloat162 h = __hmul2_rn(a, v);
+        const __nv_bfloat162 m = __hfma2(b, v, __hfma2(a, v, __hneg2(h)));
+        hi[d] = *reinterpret_cast<const uint32_t*>(&h);
+        mi[d] = *reinterpret_cast<const uint32_t*>(&m);
+    }
+}
+__device__ __forceinline__ void split_three(float w, const uint32_t (&x)[4], uint32_t (&hi)[4], uint32_t (&mi)[4], uint32_t (&lo)[4]) {
+    const f32x2 w2 = two(w, w), minus = two(-1.0f, -1.0f);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        f32x2 p = mul2(w2, two(low_bf16(x[d]), high_bf16(x[d])));
+        hi[d] = pack_bf16(p);
+        p = fma2(minus, two(low_bf16(hi[d]), high_bf16(hi[d])), p);
+        mi[d] = pack_bf16(p);
+        p = fma2(minus, two(low_bf16(mi[d]), high_bf16(mi[d])), p);
+        lo[d] = pack_bf16(p);
+    }
+}
+
+// --- state in registers, its bf16 copy for the next chunk; decayed keys in bf16 parts; outputs
+__device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+    const bool state_only = a.state_only != 0;
+    const int heads = a.H;
+    const int t = threadIdx.x - 32 * kScoreWarps, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int row = 32 * warp + lane, half = t >> 7;             // state or output row, which 64 columns of it
+    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16) + 64 * half;
     const int ch = t & 15, r0 = t >> 4;                          // decayed keys: 16-byte chunk, rows r0 + 16 i
     const uint32_t off = panel_off_bf16(r0, ch, LC);
     bool ok = true;
     int n = 0;
-    float s[64];
+    f32x2 s[32];
     auto grow = [&](float decay) {   // s = decay s + the state sum of the last chunk
+        const f32x2 w = two(decay, decay);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             uint32_t r[32];
-            tmem_ld32_issue(lanes + 32 * b, r);
+            tmem_ld32_issue(lanes + kColDS + 32 * b, r);
             tmem_wait_ld(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[32 * b + i] = decay * s[32 * b + i] + __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) s[16 * b + i] = fma2(w, s[16 * b + i], two(r[2 * i], r[2 * i + 1]));
         }
     };
     for (int round = 0; ok; ++round) {
         const int at = unit_at(round);
         if (at >= units) break;
         const Unit u = unit_of(a, at);
-        const LinJob& j = *u.job;
-        const int chunks = (u.len + LC - 1) / LC;
-        const float g = a.log_decay[u.h];
+        const int chunks = chunks_of(u);
         if (u.s_in && u.s_in_t) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = u.s_in[(64 * half + i) * D + row];
+            for (int i = 0; i < 32; ++i) s[i] = two(u.s_in[(64 * half + 2 * i) * D + row], u.s_in[(64 * half + 2 * i + 1) * D + row]);
         } else if (u.s_in) {
 #pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(u.s_in + row * D + 64 * half + i);
-                s[i] = x.x; s[i + 1] = x.y; s[i + 2] = x.z; s[i + 3] = x.w;
+            for (int i = 0; i < 32; i += 2) {
+                const float4 x = *reinterpret_cast<const float4*>(u.s_in + row * D + 64 * half + 2 * i);
+                s[i] = two(x.x, x.y); s[i + 1] = two(x.z, x.w);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = 0.0f;
+            for (int i = 0; i < 32; ++i) s[i] = 0ull;
         }
-        const float whole = decay_pow(g, LC);
-        const int e = j.rev ? 0 : 1;
+        const float whole = decay_pow(u.g, LC);
+        const float w_state = u.out_scale * decay_pow(u.g, u.rev ? LC - 1 - row : row + 1);
+        const f32x2 w2 = two(w_state, w_state), sc2 = two(u.out_scale, u.out_scale);
+        float wk[8];   // decays of this thread's key rows in a whole chunk
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wk[i] = u.k_scale * decay_pow(u.g, u.rev ? r0 + 16 * i + 1 : LC - 1 - (r0 + 16 * i));
         for (int c = 0; c < chunks; ++c, ++n) {
             if (c > 0) {
                 if (!(ok = wait_warp(&sm.ds, n - 1))) break;
                 tc_fence_after();
                 grow(whole);
-                tc_fence_before();
             }
-            if (!a.state_only && (c > 0 || u.s_in)) {   // sm.S: last read by chunk n - 1, whose state product is done
+            const bool carried = c > 0 || u.s_in;
+            if (!state_only && carried) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(sm.S + panel_off_bf16(row, 8 * half + i, LC)) =
-                        make_uint4(pack_bf16(s[8 * i], s[8 * i + 1]), pack_bf16(s[8 * i + 2], s[8 * i + 3]),
-                                   pack_bf16(s[8 * i + 4], s[8 * i + 5]), pack_bf16(s[8 * i + 6], s[8 * i + 7]));
+                        make_uint4(pack_bf16(s[4 * i]), pack_bf16(s[4 * i + 1]), pack_bf16(s[4 * i + 2]), pack_bf16(s[4 * i + 3]));
                 fence_async_smem();
             }
-            // (before the arrival, without which Q of chunk n + 1 cannot complete the barrier's next phase)
-            if (!(ok = wait_warp(&sm.full_qk, n))) break;
+            tc_fence_before();
             mbar_arrive(&sm.s);
-            // k_scale gamma^{L-e-j} k_j as a sum of bf16 parts: 16 significant bits in two, 24 in three
-            if (!(ok = wait_warp(&sm.qk, n))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full_k[n & 1], (uint32_t)((n >> 1) & 1))) && wait_warp(&sm.qk, n))) break;
+            const Chunk k = chunk_of(u, c);
             if (c + 1 < chunks || u.s_out) {
-                const int L = min(LC, u.len - c * LC);
                 uint8_t* const key = sm.K[n & 1];
-#pragma unroll 2
-                for (int i = 0; i < LC / 16; ++i) {
-                    const float w = j.k_scale * decay_pow(g, max(L - e - (r0 + 16 * i), 0));
-                    const uint32_t o = off + i * 2048;
-                    const uint4 x = *reinterpret_cast<const uint4*>(key + o);
-                    uint32_t in[4] = {x.x, x.y, x.z, x.w}, hi[4], mi[4], lo[4];
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        float p = w * low_bf16(in[d]), q = w * high_bf16(in[d]);
-                        hi[d] = pack_bf16(p, q);
-                        p -= low_bf16(hi[d]); q -= high_bf16(hi[d]);
-                        mi[d] = pack_bf16(p, q);
-                        p -= low_bf16(mi[d]); q -= high_bf16(mi[d]);
-                        lo[d] = pack_bf16(p, q);
+                if (k.hi - k.lo < LC) {   // nothing of a neighbour's rows
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + 16 * i;
+                        const bool mine = r >= k.lo && r < k.hi;
+                        const float w = u.k_scale * decay_pow(u.g, mine ? (u.rev ? r + 1 - k.lo : k.hi - 1 - r) : 0);
+                        const uint32_t o = off + i * 2048;
+                        const uint4 y = mine ? *reinterpret_cast<const uint4*>(key + o) : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+                        uint32_t hi[4], mi[4], lo[4];
+                        split_three(w, x, hi, mi, lo);
+                        *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                        *reinterpret_cast<uint4*>(sm.LOW + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-                    if (j.pieces > 2) *reinterpret_cast<uint4*>(sm.LOW + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                } else if (u.pieces > 2) {
+#pragma unroll
+                    for (int i0 = 0; i0 < 8; i0 += 2) {   // two rows' chains side by side
+                        uint4 y[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) y[e] = *reinterpret_cast<const uint4*>(key + off + (i0 + e) * 2048);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t x[4] = {y[e].x, y[e].y, y[e].z, y[e].w}, o = off + (i0 + e) * 2048;
+                            uint32_t hi[4], mi[4], lo[4];
+                            split_three(wk[i0 + e], x, hi, mi, lo);
+                            *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                            *reinterpret_cast<uint4*>(sm.LOW + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i0 = 0; i0 < 8; i0 += 4) {
+                        uint4 y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const uint4*>(key + off + (i0 + e) * 2048);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t x[4] = {y[e].x, y[e].y, y[e].z, y[e].w}, o = off + (i0 + e) * 2048;
+                            uint32_t hi[4], mi[4];
+                            split_two(wk[i0 + e], x, hi, mi);
+                            *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                        }
+                    }
                 }
                 fence_async_smem();
             }
             mbar_arrive(&sm.piece);
+            if (!(ok = wait_warp(&sm.pv, n))) break;
+            if (state_only) continue;
+            // out_scale (scores V + gamma^{..} Q S^T), by way of shared memory (this warp's part of S) so
+            // that whole 128-byte lines leave: 64 bf16 columns, or 32 fp32 columns of a share at a time
+            tc_fence_after();
+            uint8_t* const stage = sm.S + half * (kTile / 2);
+            auto store = [&](uint8_t* base, size_t pitch) {
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 32 * warp + 4 * i + (lane >> 3), q = lane & 7;
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + panel_off_bf16(r, q, LC));
+                    if (r >= k.lo && r < k.hi) *reinterpret_cast<uint4*>(base + (size_t)((k.t + r) * heads + u.h) * pitch + q * 16) = x;
+                }
+                __syncwarp();
+            };
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t x[32];
+                f32x2 z[16];
+                tmem_ld32_issue(lanes + kColPV + 32 * b, x);
+                tmem_wait_ld(x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = mul2(sc2, two(x[2 * i], x[2 * i + 1]));
+                if (carried) {
+                    tmem_ld32_issue(lanes + kColQS + 32 * b, x);
+                    tmem_wait_ld(x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = fma2(w2, two(x[2 * i], x[2 * i + 1]), z[i]);
+                }
+                if (u.share) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 p = parts(z[2 * i]), q = parts(z[2 * i + 1]);
+                        *reinterpret_cast<float4*>(stage + panel_off_bf16(row, i, LC)) = make_float4(p.x, p.y, q.x, q.y);
+                    }
+                    store(reinterpret_cast<uint8_t*>(u.share + 64 * half + 32 * b), D * sizeof(float));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(stage + panel_off_bf16(row, 4 * b + i, LC)) =
+                            make_uint4(pack_bf16(z[4 * i]), pack_bf16(z[4 * i + 1]), pack_bf16(z[4 * i + 2]), pack_bf16(z[4 * i + 3]));
+                }
+            }
+            if (!u.share) store(reinterpret_cast<uint8_t*>(u.out + 64 * half), D * sizeof(uint16_t));
         }
         if (!ok) break;
         if (chunks > 0) {
             if (!(ok = wait_warp(&sm.ds, n - 1))) break;
             tc_fence_after();
-            if (u.s_out) grow(decay_pow(g, u.len - (chunks - 1) * LC));
-            tc_fence_before();
+            if (u.s_out) grow(decay_pow(u.g, u.len - (chunks - 1) * LC));
         }
         if (u.s_out) {
 #pragma unroll
-            for (int i = 0; i < 64; i += 4)
-                *reinterpret_cast<float4*>(u.s_out + row * D + 64 * half + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+            for (int i = 0; i < 32; i += 2) {
+                const float2 x = parts(s[i]), y = parts(s[i + 1]);
+                *reinterpret_cast<float4*>(u.s_out + row * D + 64 * half + 2 * i) = make_float4(x.x, x.y, y.x, y.y);
+            }
         }
     }
     if (!ok && lane == 0) raise_status(a.ws, KDA_ERR_TIMEOUT);
@@ -477,20 +609,28 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        mbar_init(&sm.full_qk, 32 * kLoadWarps); mbar_init(&sm.full_v, 32 * kLoadWarps);
+        mbar_init(&sm.full_k[0], 1); mbar_init(&sm.full_k[1], 1); mbar_init(&sm.full_q, 1); mbar_init(&sm.full_v, 1);
         mbar_init(&sm.qk, 1); mbar_init(&sm.qs, 1); mbar_init(&sm.pv, 1); mbar_init(&sm.ds, 1);
-        mbar_init(&sm.s, 32 * kStateWarps); mbar_init(&sm.piece, 32 * kStateWarps);
-        mbar_init(&sm.p, 32 * kScoreWarps); mbar_init(&sm.o, 32 * kScoreWarps);
+        mbar_init(&sm.s, 32 * kMainWarps); mbar_init(&sm.piece, 32 * kMainWarps);
+        mbar_init(&sm.p, 32 * kScoreWarps);
         fence_mbar_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sm.tmem;
-    if (warp < kScoreWarps) lin_scores(a, sm, units, tm);
-    else if (warp < kScoreWarps + kStateWarps) lin_state(a, sm, units, tm);
-    else if (warp < kScoreWarps + kStateWarps + kLoadWarps) lin_load(a, sm, units);
-    else if ((threadIdx.x & 31) == 0) lin_mma(a, sm, units, tm);
+    if (warp < kScoreWarps) {
+        lin_scores(a, sm, units, tm);
+    } else if (warp < kScoreWarps + kMainWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
+        lin_main(a, sm, units, tm);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if ((threadIdx.x & 31) == 0) {
+            if (warp == kScoreWarps + kMainWarps) lin_load(a, sm, units);
+            else if (warp == kScoreWarps + kMainWarps + 1) lin_mma(a, sm, units, tm);
+        }
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -723,9 +863,39 @@ kda_status common_checks(const kda_linattn_shape* sh, const int64_t* cu, const v
     return KDA_OK;
 }
 
+// The tensor map of a [tokens, heads, 128] bf16 tensor.
+kda_status make_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t heads) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) {
+        set_last_error_text("the driver has no cuTensorMapEncodeTiled");
+        return KDA_ERR_CUDA;
+    }
+    const cuuint64_t dims[3] = {D, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {D * 2, (cuuint64_t)heads * D * 2};
+    const cuuint32_t box[3] = {64, 1, LC}, step[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return KDA_OK;
+    char msg[96];
+    snprintf(msg, sizeof(msg), "cuTensorMapEncodeTiled: %d", (int)r);
+    set_last_error_text(msg);
+    return KDA_ERR_CUDA;
+}
+
 // Launches for `jobs` sums over the shape's tokens. seg[0], seg[1]: the segment states of job 0 and,
 // transposed for job 1, of job 2 (the backward's two reversed jobs sum the same state).
-kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, int jobs, const int64_t* cu, const float* log_decay, uint8_t* ws,
+kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (&tensors)[4], int jobs, const int64_t* cu, const float* log_decay, uint8_t* ws,
                     const LinLayout& lay, cudaStream_t s) {
     const Plan p = plan_of(sh, cu != nullptr, jobs);
     const cudaError_t e = cudaFuncSetAttribute(linattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
@@ -733,6 +903,12 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, int jobs, const int
         set_last_error_text(cudaGetErrorString(e));
         return KDA_ERR_CUDA;
     }
+    if (sh->B * sh->T > 0)
+        for (int i = 0; i < 4; ++i)
+            if (tensors[i]) {
+                const kda_status st = make_map(&a.map[i], tensors[i], sh->B * sh->T, sh->H / a.group[i]);
+                if (st != KDA_OK) return st;
+            }
     a.log_decay = log_decay;
     a.T = sh->T;
     a.H = (int)sh->H;
@@ -801,9 +977,10 @@ extern "C" kda_status kda_linattn_fwd(const kda_linattn_shape* shape, const kda_
     for (const void* p : ptrs)
         if (misaligned(p)) return KDA_ERR_ALIGN;
     const int G = groups_of(shape);
-    LinArgs a{};
-    a.job[0] = LinJob{q, k, v, G, G, 1, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT ? 3 : 2, 1.0f, shape->scale};
-    const kda_status rs = run_jobs(shape, a, 1, cu_seqlens, log_decay, static_cast<uint8_t*>(workspace),
+    LinArgs a{{}, {G, G, 1, 1}};
+    // parts of the decayed keys: three (fp32-accurate) where the state itself is an output
+    a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT ? 3 : 2, 1.0f, shape->scale};
+    const kda_status rs = run_jobs(shape, a, {q, k, v, nullptr}, 1, cu_seqlens, log_decay, static_cast<uint8_t*>(workspace),
                                    layout_of(shape, cu_seqlens != nullptr, false), static_cast<cudaStream_t>(stream));
     return rs != KDA_OK ? rs : launched("kda_linattn_fwd launch");
 }
@@ -827,12 +1004,11 @@ extern "C" kda_status kda_linattn_bwd(const kda_linattn_shape* shape, const kda_
     float* const share_q = G > 1 ? reinterpret_cast<float*>(ws + lay.share_q) : nullptr;
     float* const share_k = G > 1 ? reinterpret_cast<float*>(ws + lay.share_k) : nullptr;
     const float sc = shape->scale;
-    LinArgs a{};
-    // parts of the decayed keys: three (fp32-accurate) where the state itself is an output
-    a.job[0] = LinJob{do_, v, k, 1, 1, G, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 2, 1.0f, sc};
-    a.job[1] = LinJob{v, do_, q, 1, 1, G, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 2, sc, 1.0f};
-    a.job[2] = LinJob{k, q, do_, G, G, 1, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 ? 3 : 2, sc, 1.0f};
-    const kda_status rs = run_jobs(shape, a, 3, cu_seqlens, log_decay, ws, lay, s);
+    LinArgs a{{}, {G, G, 1, 1}};
+    a.job[0] = LinJob{3, 2, 1, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 2, 1.0f, sc};
+    a.job[1] = LinJob{2, 3, 0, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 2, sc, 1.0f};
+    a.job[2] = LinJob{1, 0, 3, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 ? 3 : 2, sc, 1.0f};
+    const kda_status rs = run_jobs(shape, a, {q, k, v, do_}, 3, cu_seqlens, log_decay, ws, lay, s);
     if (rs != KDA_OK) return rs;
     if (G > 1 && tokens > 0) {
         const int64_t n4 = tokens * (shape->H / G) * (D / 4);
