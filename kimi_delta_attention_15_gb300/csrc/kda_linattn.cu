@@ -40,7 +40,7 @@ struct LinJob {
     float* seg;                  // states of the segments [slots, H, 128, 128]
     int s_in_t, seg_t;           // s_in, seg are stored transposed
     int rev;                     // tokens from last to first
-    int pieces;                  // bf16 parts of the decayed k in the state's sum: 2 or 3
+    int exact;                   // the state is an output: fp32-accurate (else as good as its bf16 copy needs)
     float k_scale, out_scale;
 };
 
@@ -48,7 +48,8 @@ struct LinJob {
 struct Slot {
     int64_t t0;         // first token
     int32_t len, seq;
-    int32_t seg, nseg;  // its place among the sequence's segments
+    int32_t seg, nseg;  // its place among the sequence's segments,
+    int32_t before, after;   // and the sequence's tokens on either side of it
 };
 
 struct LinArgs {
@@ -79,6 +80,8 @@ __device__ __forceinline__ Slot slot_of(const LinArgs& a, int i) {
     const int64_t at = s.seg * a.seg_len, left = a.T - at;
     s.t0 = s.seq * a.T + at;
     s.len = (int32_t)(left < a.seg_len ? (left > 0 ? left : 0) : a.seg_len);
+    s.before = (int32_t)at;
+    s.after = (int32_t)(left - s.len);
     return s;
 }
 
@@ -91,7 +94,7 @@ struct Unit {
     uint16_t* out;
     float* share;
     float k_scale, out_scale, g;   // g: log decay
-    int pieces;
+    int exact, after;              // after: tokens of the sequence still to come after this unit
     const float* s_in;             // where this unit's state comes from and goes to, NULL: zero, not wanted
     float* s_out;
     int s_in_t;
@@ -112,7 +115,8 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     x.k_scale = j.k_scale;
     x.out_scale = j.out_scale;
     x.g = a.log_decay[x.h];
-    x.pieces = j.pieces;
+    x.exact = j.exact;
+    x.after = j.rev ? s.before : s.after;
     const size_t seq_state = ((size_t)s.seq * a.H + x.h) * D * D, seg_state = ((size_t)i * a.H + x.h) * D * D;
     const bool head = j.rev ? s.seg == s.nseg - 1 : s.seg == 0, tail = j.rev ? s.seg == 0 : s.seg == s.nseg - 1;
     if (a.state_only) {            // every segment but the last of its sequence starts from zero and leaves its sum
@@ -148,6 +152,13 @@ __device__ __forceinline__ Chunk chunk_of(const Unit& u, int c) {
     x.hi = u.rev ? LC : min(left, LC);
     return x;
 }
+// The decayed keys of a chunk go into the state's sum as two bf16 parts (16 significant bits), or as
+// three (24) where the state is an output and the tokens still to come will not have decayed this
+// chunk's share, and its error with it, by another 2^-8.
+__device__ __forceinline__ bool three_parts(const Unit& u, int c) {
+    const int left = u.after + max(u.len - (c + 1) * LC, 0);
+    return u.exact && (left == 0 || u.g * (float)left > -5.6f);
+}
 __device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
 
 struct LinSmem {
@@ -158,7 +169,8 @@ struct LinSmem {
     uint8_t MID[kTile];      // the decayed keys' middle and low parts
     uint8_t LOW[kTile];
     uint8_t S[kTile];        // the state [v][c] the chunk starts from, rounded to bf16; once read, the output rows
-    float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
+    float col[4][32];        // per score warp: decays along the columns of a 32 x 32 block,
+    float diag[4][64];       // and inside the diagonal's
     // full: operands in shared memory; qk, qs, pv, ds: MMA groups done; s, p, piece: operands written.
     // Each completes one phase per chunk (full_k: per two chunks).
     // A wait names a phase by its parity, so no waiter may be a whole phase behind or ahead: every wait
@@ -170,10 +182,10 @@ struct LinSmem {
 
 // Warps 0-3: scores (thread = row of the chunk = TMEM lane). Warps 4-11: the state, the decayed keys and
 // the outputs (thread = half a row). Warp 12: loads. Warp 13: MMAs. Warps 14, 15 complete a warpgroup,
-// the unit in which registers are handed over: 128 a thread at launch, 4 x (128 + 160 + 160 + 64) = 4 x 512.
+// the unit in which registers are handed over: 128 a thread at launch, 128 + 152 + 152 + 80 = 4 x 128.
 constexpr int kScoreWarps = 4, kMainWarps = 8;
 constexpr int kLinThreads = 512;
-constexpr int kMainRegs = 160, kIssueRegs = 64;
+constexpr int kMainRegs = 152, kIssueRegs = 80;
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, int n) {
     return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(n & 1)));
@@ -212,18 +224,34 @@ __device__ __forceinline__ uint32_t pack_bf16(f32x2 a) {
     return pack_bf16(x.x, x.y);
 }
 
+// The chunks of a CTA's units, one after another.
+struct At {
+    int round, c, chunks;
+    bool more;
+    Unit u;
+    __device__ __forceinline__ void settle(const LinArgs& a, int units) {   // the first unit from here on that has chunks
+        for (c = 0;; ++round) {
+            const int i = unit_at(round);
+            if (!(more = i < units)) return;
+            u = unit_of(a, i);
+            if ((chunks = chunks_of(u)) > 0) return;
+        }
+    }
+    __device__ __forceinline__ void first(const LinArgs& a, int units) {
+        round = 0;
+        settle(a, units);
+    }
+    __device__ __forceinline__ void next(const LinArgs& a, int units) {
+        if (++c == chunks) {
+            ++round;
+            settle(a, units);
+        }
+    }
+};
+
 // --- loads, one thread
 __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int units) {
     const bool state_only = a.state_only != 0;
-    struct At { int round, c, chunks; Unit u; bool more; };
-    auto settle = [&](At& x) {   // to the first unit from here on that has chunks
-        for (;; ++x.round) {
-            const int i = unit_at(x.round);
-            if (!(x.more = i < units)) return;
-            x.u = unit_of(a, i);
-            if ((x.chunks = chunks_of(x.u)) > 0) return;
-        }
-    };
     auto tile = [&](uint8_t* dst, int which, const At& x, uint64_t* bar) {
         const Chunk k = chunk_of(x.u, x.c);
         const int head = x.u.h / a.group[which];
@@ -232,8 +260,7 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
         tma_load_3d(dst + kTile / 2, &a.map[which], 64, head, (int)k.t, bar);
     };
     At x;
-    x.round = x.c = 0;
-    settle(x);
+    x.first(a, units);
     if (x.more) tile(sm.K[0], x.u.k, x, &sm.full_k[0]);
     bool ok = true;
     int n = 0;
@@ -243,11 +270,7 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
         else mbar_arrive(&sm.full_q);
         if (n > 0 && !(ok = mbar_wait(&sm.ds, (uint32_t)((n - 1) & 1)))) break;
         tile(sm.V, x.u.v, x, &sm.full_v);
-        if (++x.c == x.chunks) {
-            ++x.round;
-            x.c = 0;
-            settle(x);
-        }
+        x.next(a, units);
         // K[(n + 1) & 1] was last read by the state product of chunk n - 1
         if (x.more) tile(sm.K[(n + 1) & 1], x.u.k, x, &sm.full_k[(n + 1) & 1]);
     }
@@ -263,41 +286,46 @@ __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units
     const uint32_t mid = smem_u32(sm.MID), low = smem_u32(sm.LOW);
     bool ok = true;
     int n = 0;
-    for (int round = 0; ok; ++round) {
-        const int at = unit_at(round);
-        if (at >= units) break;
-        const Unit u = unit_of(a, at);
-        const int chunks = chunks_of(u);
-        for (int c = 0; c < chunks; ++c, ++n) {
-            const uint32_t ph = (uint32_t)(n & 1), k = smem_u32(sm.K[n & 1]);
-            if (!(ok = mbar_wait(&sm.full_k[n & 1], (uint32_t)((n >> 1) & 1)) && mbar_wait(&sm.full_q, ph))) break;
-            if (!state_only)
-                for (int s = 0; s < 8; ++s) umma_bf16(tm + kColP, desc_kmajor(q, LC, s), desc_kmajor(k, LC, s), kk, s > 0);
-            umma_commit(&sm.qk);
-            if (!(ok = mbar_wait(&sm.s, ph))) break;   // and chunk n - 1's accumulators have been read
-            tc_fence_after();
-            if (!state_only && (c > 0 || u.s_in))
-                for (int s = 0; s < 8; ++s) umma_bf16(tm + kColQS, desc_kmajor(q, LC, s), desc_kmajor(st, LC, s), kk, s > 0);
-            umma_commit(&sm.qs);
-            if (!(ok = mbar_wait(&sm.p, ph) && mbar_wait(&sm.full_v, ph))) break;
-            tc_fence_after();
-            if (!state_only)
-                for (int s = 0; s < 8; ++s) umma_bf16_ta(tm + kColPV, tm + kColP + 8 * s, desc_mnmajor_bf16(v, LC, s), kn, s > 0);
-            umma_commit(&sm.pv);
-            if (!(ok = mbar_wait(&sm.piece, ph))) break;
-            tc_fence_after();
-            if (c + 1 < chunks || u.s_out) {   // small parts first: the accumulator is rounded at its size
-                uint32_t acc = 0;
-                if (u.pieces > 2)
-                    for (int s = 0; s < 8; ++s, acc = 1)
-                        umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(low, LC, s), mn, acc);
+    At x;
+    x.first(a, units);
+    // scores of chunk m
+    auto score = [&](int m) {
+        if (!mbar_wait(&sm.full_k[m & 1], (uint32_t)((m >> 1) & 1)) || !mbar_wait(&sm.full_q, (uint32_t)(m & 1))) return false;
+        const uint32_t k = smem_u32(sm.K[m & 1]);
+        if (!state_only)
+            for (int s = 0; s < 8; ++s) umma_bf16(tm + kColP, desc_kmajor(q, LC, s), desc_kmajor(k, LC, s), kk, s > 0);
+        umma_commit(&sm.qk);
+        return true;
+    };
+    for (; ok && x.more; ++n) {
+        const uint32_t ph = (uint32_t)(n & 1), k = smem_u32(sm.K[n & 1]);
+        if (!(ok = score(n))) break;
+        if (!(ok = mbar_wait(&sm.s, ph))) break;   // chunk n - 1's accumulators have been read too
+        tc_fence_after();
+        if (!state_only && (x.c > 0 || x.u.s_in))
+            for (int s = 0; s < 8; ++s) umma_bf16(tm + kColQS, desc_kmajor(q, LC, s), desc_kmajor(st, LC, s), kk, s > 0);
+        umma_commit(&sm.qs);
+        if (!(ok = mbar_wait(&sm.p, ph) && mbar_wait(&sm.full_v, ph))) break;
+        tc_fence_after();
+        if (!state_only)
+            for (int s = 0; s < 8; ++s) umma_bf16_ta(tm + kColPV, tm + kColP + 8 * s, desc_mnmajor_bf16(v, LC, s), kn, s > 0);
+        umma_commit(&sm.pv);
+        if (!(ok = mbar_wait(&sm.piece, ph))) break;
+        tc_fence_after();
+        const bool sum = x.c + 1 < x.chunks || x.u.s_out;
+        if (sum) {   // small parts first: the accumulator is rounded at its size
+            uint32_t acc = 0;
+            if (three_parts(x.u, x.c))
                 for (int s = 0; s < 8; ++s, acc = 1)
-                    umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(mid, LC, s), mn, acc);
-                for (int s = 0; s < 8; ++s)
-                    umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(k, LC, s), mn, 1);
-            }
-            umma_commit(&sm.ds);
+                    umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(low, LC, s), mn, acc);
+            for (int s = 0; s < 8; ++s, acc = 1)
+                umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(mid, LC, s), mn, acc);
         }
+        if (sum)
+            for (int s = 0; s < 8; ++s)
+                umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(k, LC, s), mn, 1);
+        umma_commit(&sm.ds);
+        x.next(a, units);
     }
     if (!ok) {
         raise_status(a.ws, KDA_ERR_TIMEOUT);
@@ -322,50 +350,55 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
         if (chunks == 0) continue;
         const float g = u.g;
         const bool rev = u.rev != 0;
-        // k_scale gamma^{|row - col|}, row = 32 warp + lane, col = 32 b + x. Off the diagonal's block it is
-        // gamma^{32 |warp - b| - 31} f[x], f[x] = k_scale gamma^{31 + lane - x} (reversed: 31 - lane + x): no
+        // scale gamma^{|row - col|} with both scales, row = 32 warp + lane, col = 32 b + x. Off the diagonal's block it is
+        // gamma^{32 |warp - b| - 31} gamma^{lane} gamma^{31 - x} (reversed: gamma^{31 - lane} gamma^{x}): no
         // exponent is negative. On it, diag[lane - x + 31].
-        f32x2 f[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-            f[x] = two(u.k_scale * decay_pow(g, 31 + (rev ? 2 * x - lane : lane - 2 * x)),
-                       u.k_scale * decay_pow(g, 31 + (rev ? 2 * x + 1 - lane : lane - 2 * x - 1)));
         __syncwarp();
-        diag[31 + lane] = diag[31 - lane] = u.k_scale * decay_pow(g, lane);
+        const float scale = u.k_scale * u.out_scale;
+        diag[31 + lane] = diag[31 - lane] = scale * decay_pow(g, lane);
+        sm.col[warp][lane] = decay_pow(g, rev ? lane : 31 - lane);
         __syncwarp();
         const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // columns that count in its block
-        const float far1 = decay_pow(g, 1), far2 = decay_pow(g, 33), far3 = decay_pow(g, 65);
+        const float own = scale * decay_pow(g, rev ? 31 - lane : lane);
+        const float far1 = own * decay_pow(g, 1), far2 = own * decay_pow(g, 33), far3 = own * decay_pow(g, 65);
         for (int c = 0; c < chunks; ++c, ++n) {
             if (!(ok = wait_warp(&sm.qk, n))) break;
             tc_fence_after();
             if (!state_only) {
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t w[16];
-                    const int away = rev ? b - warp : warp - b;
-                    if (away < 0) {
+                for (int b0 = 0; b0 < 4; b0 += 2) {   // two blocks of 32 columns side by side
+                    uint32_t r[2][32];
+                    const int away0 = rev ? b0 - warp : warp - b0, away1 = rev ? away0 + 1 : away0 - 1;
+                    if (away0 >= 0) tmem_ld32_issue(lanes + 32 * b0, r[0]);
+                    if (away1 >= 0) tmem_ld32_issue(lanes + 32 * b0 + 32, r[1]);
+                    tmem_wait_ld(r[0]);
+                    tmem_after_wait(r[1]);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) w[x] = 0u;
-                    } else {
-                        uint32_t r[32];
-                        tmem_ld32_issue(lanes + 32 * b, r);
-                        if (away > 0) {
+                    for (int e = 0; e < 2; ++e) {
+                        const int away = e ? away1 : away0;
+                        uint32_t w[16];
+                        if (away < 0) {
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) w[x] = 0u;
+                        } else if (away > 0) {
                             const float base = away == 1 ? far1 : away == 2 ? far2 : far3;
                             const f32x2 base2 = two(base, base);
-                            tmem_wait_ld(r);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) w[x] = pack_bf16(mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x])));
+                            for (int x = 0; x < 16; x += 2) {
+                                const float4 f = *reinterpret_cast<const float4*>(&sm.col[warp][2 * x]);
+                                w[x] = pack_bf16(mul2(two(r[e][2 * x], r[e][2 * x + 1]), mul2(base2, two(f.x, f.y))));
+                                w[x + 1] = pack_bf16(mul2(two(r[e][2 * x + 2], r[e][2 * x + 3]), mul2(base2, two(f.z, f.w))));
+                            }
                         } else {
                             const float* const d = diag + 31 + lane;
-                            tmem_wait_ld(r);
 #pragma unroll
                             for (int x = 0; x < 16; ++x) {
-                                const float p0 = __uint_as_float(r[2 * x]) * d[-2 * x], p1 = __uint_as_float(r[2 * x + 1]) * d[-2 * x - 1];
+                                const float p0 = __uint_as_float(r[e][2 * x]) * d[-2 * x], p1 = __uint_as_float(r[e][2 * x + 1]) * d[-2 * x - 1];
                                 w[x] = pack_bf16((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
                             }
                         }
+                        tmem_st16_issue(lanes + 16 * (b0 + e), w);   // behind the columns still to be read
                     }
-                    tmem_st16_issue(lanes + 16 * b, w);   // behind the columns still to be read
                 }
                 tmem_wait_st_all();
             }
@@ -428,11 +461,14 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
         const f32x2 w = two(decay, decay);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            uint32_t r[32];
-            tmem_ld32_issue(lanes + kColDS + 32 * b, r);
-            tmem_wait_ld(r);
+            uint32_t r[2][16];
+            tmem_ld16_issue(lanes + kColDS + 32 * b, r[0]);
+            tmem_ld16_issue(lanes + kColDS + 32 * b + 16, r[1]);
+            tmem_wait_ld16(r[0]);
+            tmem_after_wait16(r[1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[16 * b + i] = fma2(w, s[16 * b + i], two(r[2 * i], r[2 * i + 1]));
+            for (int i = 0; i < 16; ++i)
+                s[16 * b + i] = fma2(w, s[16 * b + i], two(r[i >> 3][2 * (i & 7)], r[i >> 3][2 * (i & 7) + 1]));
         }
     };
     for (int round = 0; ok; ++round) {
@@ -455,7 +491,7 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
         }
         const float whole = decay_pow(u.g, LC);
         const float w_state = u.out_scale * decay_pow(u.g, u.rev ? LC - 1 - row : row + 1);
-        const f32x2 w2 = two(w_state, w_state), sc2 = two(u.out_scale, u.out_scale);
+        const f32x2 w2 = two(w_state, w_state);
         float wk[8];   // decays of this thread's key rows in a whole chunk
 #pragma unroll
         for (int i = 0; i < 8; ++i) wk[i] = u.k_scale * decay_pow(u.g, u.rev ? r0 + 16 * i + 1 : LC - 1 - (r0 + 16 * i));
@@ -479,11 +515,11 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             const Chunk k = chunk_of(u, c);
             if (c + 1 < chunks || u.s_out) {
                 uint8_t* const key = sm.K[n & 1];
-                if (k.hi - k.lo < LC) {   // nothing of a neighbour's rows
+                if (k.hi - k.lo < LC || three_parts(u, c)) {
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const int r = r0 + 16 * i;
-                        const bool mine = r >= k.lo && r < k.hi;
+                        const bool mine = r >= k.lo && r < k.hi;   // nothing of a neighbour's rows
                         const float w = u.k_scale * decay_pow(u.g, mine ? (u.rev ? r + 1 - k.lo : k.hi - 1 - r) : 0);
                         const uint32_t o = off + i * 2048;
                         const uint4 y = mine ? *reinterpret_cast<const uint4*>(key + o) : make_uint4(0u, 0u, 0u, 0u);
@@ -493,22 +529,6 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                         *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                         *reinterpret_cast<uint4*>(sm.LOW + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                } else if (u.pieces > 2) {
-#pragma unroll
-                    for (int i0 = 0; i0 < 8; i0 += 2) {   // two rows' chains side by side
-                        uint4 y[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) y[e] = *reinterpret_cast<const uint4*>(key + off + (i0 + e) * 2048);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t x[4] = {y[e].x, y[e].y, y[e].z, y[e].w}, o = off + (i0 + e) * 2048;
-                            uint32_t hi[4], mi[4], lo[4];
-                            split_three(wk[i0 + e], x, hi, mi, lo);
-                            *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-                            *reinterpret_cast<uint4*>(sm.LOW + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        }
                     }
                 } else {
 #pragma unroll
@@ -531,49 +551,53 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             mbar_arrive(&sm.piece);
             if (!(ok = wait_warp(&sm.pv, n))) break;
             if (state_only) continue;
-            // out_scale (scores V + gamma^{..} Q S^T), by way of shared memory (this warp's part of S) so
+            // scores V + out_scale gamma^{..} Q S^T, by way of shared memory (this warp's part of S) so
             // that whole 128-byte lines leave: 64 bf16 columns, or 32 fp32 columns of a share at a time
             tc_fence_after();
             uint8_t* const stage = sm.S + half * (kTile / 2);
-            auto store = [&](uint8_t* base, size_t pitch) {
+            const int first = 32 * warp + (lane >> 3);
+            auto store = [&](uint8_t* base, int pitch) {   // base: row 0 of the chunk at this head and part
                 __syncwarp();
-#pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 32 * warp + 4 * i + (lane >> 3), q = lane & 7;
-                    const uint4 x = *reinterpret_cast<const uint4*>(stage + panel_off_bf16(r, q, LC));
-                    if (r >= k.lo && r < k.hi) *reinterpret_cast<uint4*>(base + (size_t)((k.t + r) * heads + u.h) * pitch + q * 16) = x;
+                const int64_t step = (int64_t)heads * pitch;
+                uint8_t* p = base + (k.t + first) * step + (lane & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < 8; ++i, p += 4 * step) {
+                    const int r = first + 4 * i;
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + panel_off_bf16(r, lane & 7, LC));
+                    if (r >= k.lo && r < k.hi) *reinterpret_cast<uint4*>(p) = x;
                 }
                 __syncwarp();
             };
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t x[32];
-                f32x2 z[16];
-                tmem_ld32_issue(lanes + kColPV + 32 * b, x);
-                tmem_wait_ld(x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = mul2(sc2, two(x[2 * i], x[2 * i + 1]));
+            for (int b = 0; b < 4; ++b) {   // 16 columns at a time
+                uint32_t x[16], y[16];
+                tmem_ld16_issue(lanes + kColPV + 16 * b, x);
+                if (carried) tmem_ld16_issue(lanes + kColQS + 16 * b, y);
+                tmem_wait_ld16(x);
                 if (carried) {
-                    tmem_ld32_issue(lanes + kColQS + 32 * b, x);
-                    tmem_wait_ld(x);
+                    tmem_after_wait16(y);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = fma2(w2, two(x[2 * i], x[2 * i + 1]), z[i]);
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 z = parts(fma2(w2, two(y[i], y[i + 1]), two(x[i], x[i + 1])));
+                        x[i] = __float_as_uint(z.x);
+                        x[i + 1] = __float_as_uint(z.y);
+                    }
                 }
                 if (u.share) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 p = parts(z[2 * i]), q = parts(z[2 * i + 1]);
-                        *reinterpret_cast<float4*>(stage + panel_off_bf16(row, i, LC)) = make_float4(p.x, p.y, q.x, q.y);
-                    }
-                    store(reinterpret_cast<uint8_t*>(u.share + 64 * half + 32 * b), D * sizeof(float));
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(stage + panel_off_bf16(row, 4 * (b & 1) + i, LC)) =
+                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    if (b & 1) store(reinterpret_cast<uint8_t*>(u.share + (size_t)u.h * D + 64 * half + 16 * (b - 1)), D * (int)sizeof(float));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(stage + panel_off_bf16(row, 4 * b + i, LC)) =
-                            make_uint4(pack_bf16(z[4 * i]), pack_bf16(z[4 * i + 1]), pack_bf16(z[4 * i + 2]), pack_bf16(z[4 * i + 3]));
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4*>(stage + panel_off_bf16(row, 2 * b + i, LC)) =
+                            make_uint4(pack_bf16(two(x[8 * i], x[8 * i + 1])), pack_bf16(two(x[8 * i + 2], x[8 * i + 3])),
+                                       pack_bf16(two(x[8 * i + 4], x[8 * i + 5])), pack_bf16(two(x[8 * i + 6], x[8 * i + 7])));
                 }
             }
-            if (!u.share) store(reinterpret_cast<uint8_t*>(u.out + 64 * half), D * sizeof(uint16_t));
+            if (!u.share) store(reinterpret_cast<uint8_t*>(u.out + (size_t)u.h * D + 64 * half), D * (int)sizeof(uint16_t));
         }
         if (!ok) break;
         if (chunks > 0) {
@@ -708,7 +732,10 @@ __global__ void __launch_bounds__(1024)
         const int first = carry + scan[tid] - cnt;
         for (int k = 0; k < cnt; ++k) {
             const int64_t left = len - k * seg_len;
-            if (first + k < slots_max) table[first + k] = Slot{t0 + k * seg_len, (int32_t)(left < seg_len ? left : seg_len), n, k, cnt};
+            if (first + k < slots_max) {
+                const int32_t m = (int32_t)(left < seg_len ? left : seg_len);
+                table[first + k] = Slot{t0 + k * seg_len, m, n, k, cnt, (int32_t)(k * seg_len), (int32_t)(left - m)};
+            }
         }
         __syncthreads();
         if (tid == blockDim.x - 1) carry += scan[tid];
@@ -978,8 +1005,7 @@ extern "C" kda_status kda_linattn_fwd(const kda_linattn_shape* shape, const kda_
         if (misaligned(p)) return KDA_ERR_ALIGN;
     const int G = groups_of(shape);
     LinArgs a{{}, {G, G, 1, 1}};
-    // parts of the decayed keys: three (fp32-accurate) where the state itself is an output
-    a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT ? 3 : 2, 1.0f, shape->scale};
+    a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT != nullptr, 1.0f, shape->scale};
     const kda_status rs = run_jobs(shape, a, {q, k, v, nullptr}, 1, cu_seqlens, log_decay, static_cast<uint8_t*>(workspace),
                                    layout_of(shape, cu_seqlens != nullptr, false), static_cast<cudaStream_t>(stream));
     return rs != KDA_OK ? rs : launched("kda_linattn_fwd launch");
@@ -1005,9 +1031,9 @@ extern "C" kda_status kda_linattn_bwd(const kda_linattn_shape* shape, const kda_
     float* const share_k = G > 1 ? reinterpret_cast<float*>(ws + lay.share_k) : nullptr;
     const float sc = shape->scale;
     LinArgs a{{}, {G, G, 1, 1}};
-    a.job[0] = LinJob{3, 2, 1, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 2, 1.0f, sc};
-    a.job[1] = LinJob{2, 3, 0, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 2, sc, 1.0f};
-    a.job[2] = LinJob{1, 0, 3, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 ? 3 : 2, sc, 1.0f};
+    a.job[0] = LinJob{3, 2, 1, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 0, 1.0f, sc};
+    a.job[1] = LinJob{2, 3, 0, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 0, sc, 1.0f};
+    a.job[2] = LinJob{1, 0, 3, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 != nullptr, sc, 1.0f};
     const kda_status rs = run_jobs(shape, a, {q, k, v, do_}, 3, cu_seqlens, log_decay, ws, lay, s);
     if (rs != KDA_OK) return rs;
     if (G > 1 && tokens > 0) {
