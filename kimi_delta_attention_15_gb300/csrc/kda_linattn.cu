@@ -54,6 +54,7 @@ struct Slot {
 
 struct LinArgs {
     CUtensorMap map[4];          // [tokens, H / group, 128] bf16 in boxes of 128 tokens x 64 channels
+    CUtensorMap out_map[3];      // each job's out or share in boxes of 32 tokens x 128 bytes
     int group[4];                // value heads that share a head of each
     LinJob job[3];
     int jobs;
@@ -90,9 +91,9 @@ __device__ __forceinline__ Slot slot_of(const LinArgs& a, int i) {
 struct Unit {
     int64_t t0;
     int len, h, rev;
-    int q, k, v;                   // tensors
-    uint16_t* out;
-    float* share;
+    int job, q, k, v;              // tensors
+    uint8_t* out;                  // out or share
+    bool fp32;
     float k_scale, out_scale, g;   // g: log decay
     int exact, after;              // after: tokens of the sequence still to come after this unit
     const float* s_in;             // where this unit's state comes from and goes to, NULL: zero, not wanted
@@ -110,8 +111,9 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     x.len = s.len;
     x.rev = j.rev;
     x.q = j.q; x.k = j.k; x.v = j.v;
-    x.out = j.out;
-    x.share = j.share;
+    x.job = ji;
+    x.fp32 = j.share != nullptr;
+    x.out = x.fp32 ? reinterpret_cast<uint8_t*>(j.share) : reinterpret_cast<uint8_t*>(j.out);
     x.k_scale = j.k_scale;
     x.out_scale = j.out_scale;
     x.g = a.log_decay[x.h];
@@ -162,33 +164,31 @@ __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
 __device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
 
 struct LinSmem {
-    // operand tiles (bf16 panels, 1024-byte aligned)
-    uint8_t K[2][kTile];     // keys by chunk parity; once scored, overwritten with the decayed keys' high parts
-    uint8_t Q[kTile];
-    uint8_t V[kTile];
-    uint8_t MID[kTile];      // the decayed keys' middle and low parts
-    uint8_t LOW[kTile];
-    uint8_t S[kTile];        // the state [v][c] the chunk starts from, rounded to bf16; once read, the output rows
-    float col[4][32];        // per score warp: decays along the columns of a 32 x 32 block,
-    float diag[4][64];       // and inside the diagonal's
-    // full: operands in shared memory; qk, qs, pv, ds: MMA groups done; s, p, piece: operands written.
-    // Each completes one phase per chunk (full_k: per two chunks).
+    // operand tiles (bf16 panels, 1024-byte aligned), Q and V by chunk parity
+    uint8_t K[kTile], Q[2][kTile], V[2][kTile];
+    uint8_t S[kTile];        // the state the chunk starts from, [c][v], rounded to bf16
+    uint8_t stage[kTile];    // output rows on their way out
+    float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
+    // full: operands in shared memory; qk, qs, ds, pv: MMA groups done; s, p, piece, low, o: operands written
+    // (state, scores, decayed keys and their low parts, decayed Q S^T); k_free, r: keys, outputs read. Each completes one
+    // phase per chunk (full_q, full_v: one of the two; low: per chunk with three parts).
     // A wait names a phase by its parity, so no waiter may be a whole phase behind or ahead: every wait
-    // comes before an arrival of the same thread (or an MMA that needs one) on which the barrier's next
-    // phase depends, and after something that depends on the phase before.
-    uint64_t full_k[2], full_q, full_v, qk, qs, pv, ds, s, p, piece;
+    // comes before an arrival of the same thread on which the barrier's next phase depends, and after
+    // something that depends on the phase before. A thread that arrives twice on a barrier waits in between
+    // for something that depends on all the first arrivals.
+    uint64_t full_k, full_q[2], full_v[2], qk, qs, ds, pv, s, p, piece, low, k_free, o, r, end;
     uint32_t tmem;
 };
 
-// Warps 0-3: scores (thread = row of the chunk = TMEM lane). Warps 4-11: the state, the decayed keys and
-// the outputs (thread = half a row). Warp 12: loads. Warp 13: MMAs. Warps 14, 15 complete a warpgroup,
+// Warps 0-3: scores and outputs (thread = row of the chunk = TMEM lane). Warps 4-11: the state and the
+// decayed keys (thread = half a TMEM lane's columns). Warp 12: loads. Warp 13: MMAs. Warps 14, 15 complete a warpgroup,
 // the unit in which registers are handed over: 128 a thread at launch, 128 + 152 + 152 + 80 = 4 x 128.
 constexpr int kScoreWarps = 4, kMainWarps = 8;
 constexpr int kLinThreads = 512;
 constexpr int kMainRegs = 152, kIssueRegs = 80;
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, int n) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(n & 1)));
+    return __all_sync(0xffffffffu, mbar_wait_asleep(bar, (uint32_t)(n & 1)));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
@@ -259,87 +259,116 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
         tma_load_3d(dst, &a.map[which], 0, head, (int)k.t, bar);
         tma_load_3d(dst + kTile / 2, &a.map[which], 64, head, (int)k.t, bar);
     };
-    At x;
+    auto q_tile = [&](int b, const At& x) {
+        if (state_only) mbar_arrive(&sm.full_q[b]);
+        else tile(sm.Q[b], x.u.q, x, &sm.full_q[b]);
+    };
+    At x;   // the chunk after n
     x.first(a, units);
-    if (x.more) tile(sm.K[0], x.u.k, x, &sm.full_k[0]);
-    bool ok = true;
-    int n = 0;
-    for (; x.more; ++n) {
-        if (n > 0 && !(ok = mbar_wait(&sm.qs, (uint32_t)((n - 1) & 1)))) break;
-        if (!state_only) tile(sm.Q, x.u.q, x, &sm.full_q);
-        else mbar_arrive(&sm.full_q);
-        if (n > 0 && !(ok = mbar_wait(&sm.ds, (uint32_t)((n - 1) & 1)))) break;
-        tile(sm.V, x.u.v, x, &sm.full_v);
+    if (!x.more) return;
+    tile(sm.K, x.u.k, x, &sm.full_k);
+    q_tile(0, x);
+    tile(sm.V[0], x.u.v, x, &sm.full_v[0]);
+    x.next(a, units);
+    if (x.more) q_tile(1, x);
+    for (int n = 0; x.more; ++n) {
+        // Q S^T of chunk n done: so are its scores and everything of chunk n - 1. K is free with its decayed
+        // copies made, Q[n & 1] and V[(n + 1) & 1] are free.
+        if (!mbar_wait_asleep(&sm.k_free, (uint32_t)(n & 1)) || !mbar_wait_asleep(&sm.qs, (uint32_t)(n & 1))) {
+            raise_status(a.ws, KDA_ERR_TIMEOUT);
+            return;
+        }
+        tile(sm.K, x.u.k, x, &sm.full_k);
+        tile(sm.V[(n + 1) & 1], x.u.v, x, &sm.full_v[(n + 1) & 1]);
         x.next(a, units);
-        // K[(n + 1) & 1] was last read by the state product of chunk n - 1
-        if (x.more) tile(sm.K[(n + 1) & 1], x.u.k, x, &sm.full_k[(n + 1) & 1]);
+        if (x.more) q_tile(n & 1, x);
     }
-    if (!ok) raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
-// --- MMAs, one thread. TMEM: scores (and their bf16 copy, two to a column), Q S^T, scores V, state sum
-constexpr uint32_t kColP = 0, kColQS = 128, kColPV = 256, kColDS = 384;
+// --- MMAs, one thread. TMEM: scores and, in one half of their columns (two to a column), their bf16 copy,
+// in the other the decayed keys' low parts; outputs; state sum [c][v]; decayed keys [c][tokens], high and
+// middle parts (two to a column)
+constexpr uint32_t kColP = 0, kColO = 128, kColDS = 256, kColHi = 384, kColMid = 448;
+// the scores' copy goes behind the columns still to be read: forward from the left, reversed from the right
+__device__ __forceinline__ uint32_t copy_col(int rev) { return kColP + (rev ? 64u : 0u); }
+__device__ __forceinline__ uint32_t low_col(int rev) { return kColP + (rev ? 0u : 64u); }
+// A product over K = 128: eight MMAs, unrolled, descriptors a constant apart. (The thread that issues them is
+// what limits it otherwise: with descriptors built one by one an MMA of 128 x 128 x 16 took 130 to 190 cycles,
+// so it takes 65, the time to read its operands from shared memory.)
+__device__ __forceinline__ uint64_t k_step(uint64_t d, int s) { return d + (uint64_t)((s >> 2) * (kTile / 2 / 16) + (s & 3) * 2); }
+__device__ __forceinline__ uint64_t mn_step(uint64_t d, int s) { return d + (uint64_t)(s * 128); }
+template <bool kBmn>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) umma_bf16(d, k_step(a, s), kBmn ? mn_step(b, s) : k_step(b, s), idesc, s > 0);
+}
+template <bool kAdd>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) umma_bf16_ta(d, a + 8 * s, mn_step(b, s), idesc, kAdd || s > 0);
+}
 __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
-    constexpr uint32_t kk = idesc_bf16(128, 128, 0, 0), kn = idesc_bf16(128, 128, 0, 1), mn = idesc_bf16(128, 128, 1, 1);
-    const uint32_t q = smem_u32(sm.Q), v = smem_u32(sm.V), st = smem_u32(sm.S);
-    const uint32_t mid = smem_u32(sm.MID), low = smem_u32(sm.LOW);
+    constexpr uint32_t kk = idesc_bf16(128, 128, 0, 0), kn = idesc_bf16(128, 128, 0, 1);
+    const uint64_t dk = desc_kmajor(smem_u32(sm.K), LC, 0), ds = desc_mnmajor_bf16(smem_u32(sm.S), LC, 0);
+    const uint64_t dq0 = desc_kmajor(smem_u32(sm.Q[0]), LC, 0), dv0 = desc_mnmajor_bf16(smem_u32(sm.V[0]), LC, 0);
     bool ok = true;
-    int n = 0;
+    int n = 0, lows = 0;
     At x;
     x.first(a, units);
-    // scores of chunk m
-    auto score = [&](int m) {
-        if (!mbar_wait(&sm.full_k[m & 1], (uint32_t)((m >> 1) & 1)) || !mbar_wait(&sm.full_q, (uint32_t)(m & 1))) return false;
-        const uint32_t k = smem_u32(sm.K[m & 1]);
-        if (!state_only)
-            for (int s = 0; s < 8; ++s) umma_bf16(tm + kColP, desc_kmajor(q, LC, s), desc_kmajor(k, LC, s), kk, s > 0);
+    auto score = [&](int m) {   // scores of chunk m
+        if (!mbar_wait_asleep(&sm.full_k, (uint32_t)(m & 1)) || !mbar_wait_asleep(&sm.full_q[m & 1], (uint32_t)((m >> 1) & 1))) return false;
+        if (!state_only) product_ss<false>(tm + kColP, dq0 + (uint64_t)((m & 1) * (kTile / 16)), dk, kk);
         umma_commit(&sm.qk);
         return true;
     };
+    if (x.more) ok = score(0);
     for (; ok && x.more; ++n) {
-        const uint32_t ph = (uint32_t)(n & 1), k = smem_u32(sm.K[n & 1]);
-        if (!(ok = score(n))) break;
-        if (!(ok = mbar_wait(&sm.s, ph))) break;   // chunk n - 1's accumulators have been read too
+        const uint32_t ph = (uint32_t)(n & 1);
+        const uint64_t q = dq0 + (uint64_t)(ph * (kTile / 16)), v = dv0 + (uint64_t)(ph * (kTile / 16));
+        const bool carried = x.c > 0 || x.u.s_in, sum = x.c + 1 < x.chunks || x.u.s_out, three = sum && three_parts(x.u, x.c);
+        if (!(ok = mbar_wait_asleep(&sm.s, ph) && (n == 0 || mbar_wait_asleep(&sm.r, ph ^ 1u)))) break;
         tc_fence_after();
-        if (!state_only && (x.c > 0 || x.u.s_in))
-            for (int s = 0; s < 8; ++s) umma_bf16(tm + kColQS, desc_kmajor(q, LC, s), desc_kmajor(st, LC, s), kk, s > 0);
+        if (!state_only && carried) product_ss<true>(tm + kColO, q, ds, kn);
         umma_commit(&sm.qs);
-        if (!(ok = mbar_wait(&sm.p, ph) && mbar_wait(&sm.full_v, ph))) break;
+        if (!(ok = mbar_wait_asleep(&sm.piece, ph) && mbar_wait_asleep(&sm.full_v[n & 1], (uint32_t)((n >> 1) & 1)))) break;
         tc_fence_after();
-        if (!state_only)
-            for (int s = 0; s < 8; ++s) umma_bf16_ta(tm + kColPV, tm + kColP + 8 * s, desc_mnmajor_bf16(v, LC, s), kn, s > 0);
-        umma_commit(&sm.pv);
-        if (!(ok = mbar_wait(&sm.piece, ph))) break;
-        tc_fence_after();
-        const bool sum = x.c + 1 < x.chunks || x.u.s_out;
         if (sum) {   // small parts first: the accumulator is rounded at its size
-            uint32_t acc = 0;
-            if (three_parts(x.u, x.c))
-                for (int s = 0; s < 8; ++s, acc = 1)
-                    umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(low, LC, s), mn, acc);
-            for (int s = 0; s < 8; ++s, acc = 1)
-                umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(mid, LC, s), mn, acc);
+            product_ts<false>(tm + kColDS, tm + kColMid, v, kn);
+            product_ts<true>(tm + kColDS, tm + kColHi, v, kn);
         }
-        if (sum)
-            for (int s = 0; s < 8; ++s)
-                umma_bf16(tm + kColDS, desc_mnmajor_bf16(v, LC, s), desc_mnmajor_bf16(k, LC, s), mn, 1);
-        umma_commit(&sm.ds);
+        if (!three) umma_commit(&sm.ds);
+        if (!(ok = mbar_wait_asleep(&sm.o, ph) && mbar_wait_asleep(&sm.p, ph))) break;
+        tc_fence_after();
+        if (!state_only) {
+            if (carried) product_ts<true>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
+            else product_ts<false>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
+        }
+        umma_commit(&sm.pv);
+        if (three) {
+            if (!(ok = mbar_wait_asleep(&sm.low, (uint32_t)(lows++ & 1)))) break;
+            tc_fence_after();
+            product_ts<true>(tm + kColDS, tm + low_col(x.u.rev), v, kn);
+            umma_commit(&sm.ds);
+        }
         x.next(a, units);
+        // the next chunk's scores now: they and their decays need no state
+        if (x.more) ok = score(n + 1);
     }
-    if (!ok) {
-        raise_status(a.ws, KDA_ERR_TIMEOUT);
-        umma_commit(&sm.ds);                   // MMAs still in flight end before the tensor memory is freed
-        mbar_wait(&sm.ds, (uint32_t)(n & 1));
-    }
+    if (!ok) raise_status(a.ws, KDA_ERR_TIMEOUT);
+    umma_commit(&sm.end);   // no MMA is in flight when the tensor memory is freed
+    mbar_wait_asleep(&sm.end, 0);
 }
 
-// --- scores -> decayed bf16 scores in TMEM
+// --- scores -> decayed bf16 scores in TMEM; outputs -> shared memory -> global, a warp's 32 rows by TMA (or,
+// in a chunk with rows of a neighbour, row by row)
 __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x;
-    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16) + kColP;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
     float* const diag = sm.diag[warp];
+    uint8_t* const stage = sm.stage + warp * 4096;   // rows 32 warp .. of the tile
+    const int heads = a.H;
     bool ok = true;
     int n = 0;
     for (int round = 0; ok; ++round) {
@@ -350,127 +379,153 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
         if (chunks == 0) continue;
         const float g = u.g;
         const bool rev = u.rev != 0;
-        // scale gamma^{|row - col|} with both scales, row = 32 warp + lane, col = 32 b + x. Off the diagonal's block it is
-        // gamma^{32 |warp - b| - 31} gamma^{lane} gamma^{31 - x} (reversed: gamma^{31 - lane} gamma^{x}): no
-        // exponent is negative. On it, diag[lane - x + 31].
-        __syncwarp();
+        // scale gamma^{|row - col|} with both scales, row = 32 warp + lane, col = 32 b + x. Off the diagonal's
+        // block it is gamma^{32 |warp - b| - 31} f[x], f[x] = scale gamma^{31 + lane - x} (reversed:
+        // 31 - lane + x): no exponent is negative. On it, diag[lane - x + 31].
         const float scale = u.k_scale * u.out_scale;
+        f32x2 f[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+            f[x] = two(scale * decay_pow(g, 31 + (rev ? 2 * x - lane : lane - 2 * x)),
+                       scale * decay_pow(g, 31 + (rev ? 2 * x + 1 - lane : lane - 2 * x - 1)));
+        __syncwarp();
         diag[31 + lane] = diag[31 - lane] = scale * decay_pow(g, lane);
-        sm.col[warp][lane] = decay_pow(g, rev ? lane : 31 - lane);
         __syncwarp();
         const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // columns that count in its block
-        const float own = scale * decay_pow(g, rev ? 31 - lane : lane);
-        const float far1 = own * decay_pow(g, 1), far2 = own * decay_pow(g, 33), far3 = own * decay_pow(g, 65);
+        const float far1 = decay_pow(g, 1), far2 = decay_pow(g, 33), far3 = decay_pow(g, 65);
         for (int c = 0; c < chunks; ++c, ++n) {
             if (!(ok = wait_warp(&sm.qk, n))) break;
             tc_fence_after();
             if (!state_only) {
+                // from the far end to the diagonal's block, so that its table is read when Q S^T, which leaves
+                // shared memory no read cycles, is over; zeros beyond it
 #pragma unroll 1
-                for (int b0 = 0; b0 < 4; b0 += 2) {   // two blocks of 32 columns side by side
-                    uint32_t r[2][32];
-                    const int away0 = rev ? b0 - warp : warp - b0, away1 = rev ? away0 + 1 : away0 - 1;
-                    if (away0 >= 0) tmem_ld32_issue(lanes + 32 * b0, r[0]);
-                    if (away1 >= 0) tmem_ld32_issue(lanes + 32 * b0 + 32, r[1]);
-                    tmem_wait_ld(r[0]);
-                    tmem_after_wait(r[1]);
+                for (int i = 0; i < 4; ++i) {
+                    const int b = rev ? 3 - i : i, away = rev ? b - warp : warp - b;
+                    uint32_t w[16];
+                    if (away < 0) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int away = e ? away1 : away0;
-                        uint32_t w[16];
-                        if (away < 0) {
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) w[x] = 0u;
-                        } else if (away > 0) {
+                        for (int x = 0; x < 16; ++x) w[x] = 0u;
+                    } else {
+                        uint32_t r[32];
+                        tmem_ld32_issue(lanes + kColP + 32 * b, r);
+                        if (away > 0) {
                             const float base = away == 1 ? far1 : away == 2 ? far2 : far3;
                             const f32x2 base2 = two(base, base);
+                            tmem_wait_ld(r);
 #pragma unroll
-                            for (int x = 0; x < 16; x += 2) {
-                                const float4 f = *reinterpret_cast<const float4*>(&sm.col[warp][2 * x]);
-                                w[x] = pack_bf16(mul2(two(r[e][2 * x], r[e][2 * x + 1]), mul2(base2, two(f.x, f.y))));
-                                w[x + 1] = pack_bf16(mul2(two(r[e][2 * x + 2], r[e][2 * x + 3]), mul2(base2, two(f.z, f.w))));
-                            }
+                            for (int x = 0; x < 16; ++x) w[x] = pack_bf16(mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x])));
                         } else {
                             const float* const d = diag + 31 + lane;
+                            tmem_wait_ld(r);
 #pragma unroll
                             for (int x = 0; x < 16; ++x) {
-                                const float p0 = __uint_as_float(r[e][2 * x]) * d[-2 * x], p1 = __uint_as_float(r[e][2 * x + 1]) * d[-2 * x - 1];
+                                const float p0 = __uint_as_float(r[2 * x]) * d[-2 * x], p1 = __uint_as_float(r[2 * x + 1]) * d[-2 * x - 1];
                                 w[x] = pack_bf16((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
                             }
                         }
-                        tmem_st16_issue(lanes + 16 * (b0 + e), w);   // behind the columns still to be read
                     }
+                    tmem_st16_issue(lanes + copy_col(rev) + 16 * b, w);   // columns that have been read
                 }
                 tmem_wait_st_all();
             }
-            const Chunk k = chunk_of(u, c);
-            if (k.hi - k.lo < LC) {   // rows of a neighbour in V: their scores are zero, and zero times an infinity is not
-                if (!(ok = wait_warp(&sm.full_v, n))) break;
-                if (row < k.lo || row >= k.hi)
-#pragma unroll
-                    for (int ch = 0; ch < 16; ++ch)
-                        *reinterpret_cast<uint4*>(sm.V + panel_off_bf16(row, ch, LC)) = make_uint4(0u, 0u, 0u, 0u);
-                fence_async_smem();
-            }
             tc_fence_before();
             mbar_arrive(&sm.p);
+            if (!(ok = wait_warp(&sm.pv, n))) break;
+            tc_fence_after();
+            if (state_only) {
+                mbar_arrive(&sm.r);
+                continue;
+            }
+            const Chunk k = chunk_of(u, c);
+            const int r0 = 32 * warp;
+            const bool all = r0 >= k.lo && r0 + 32 <= k.hi;
+            // a tile of 32 rows x 128 bytes at a time, 32 or 64 columns; two are staged at once
+            auto send = [&](int tile, int slot) {
+                uint8_t* const from = stage + slot * (kTile / 2);
+                if (all) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(from, &a.out_map[u.job], tile * (u.fp32 ? 32 : 64), u.h, (int)k.t + r0);
+                        bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+                    const int64_t pitch = (int64_t)heads * D * (u.fp32 ? 4 : 2);
+#pragma unroll 1
+                    for (int i = lane >> 3; i < 32; i += 4)
+                        if (r0 + i >= k.lo && r0 + i < k.hi)
+                            *reinterpret_cast<uint4*>(u.out + (k.t + r0 + i) * pitch + (int64_t)u.h * D * (u.fp32 ? 4 : 2) + tile * 128 +
+                                                      (lane & 7) * 16) =
+                                *reinterpret_cast<const uint4*>(from + panel_off_bf16(i, lane & 7, LC));
+                }
+            };
+            auto staged = [&] {   // what was staged before has been read
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+            };
+            staged();
+            if (!u.fp32) {
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t x[32], y[32];
+                    tmem_ld32_issue(lanes + kColO + 64 * t, x);
+                    tmem_ld32_issue(lanes + kColO + 64 * t + 32, y);
+                    tmem_wait_ld(x);
+                    tmem_after_wait(y);
+                    if (t == 1) {
+                        tc_fence_before();
+                        mbar_arrive(&sm.r);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        *reinterpret_cast<uint4*>(stage + t * (kTile / 2) + panel_off_bf16(lane, i, LC)) =
+                            make_uint4(pack_bf16(two(x[8 * i], x[8 * i + 1])), pack_bf16(two(x[8 * i + 2], x[8 * i + 3])),
+                                       pack_bf16(two(x[8 * i + 4], x[8 * i + 5])), pack_bf16(two(x[8 * i + 6], x[8 * i + 7])));
+                        *reinterpret_cast<uint4*>(stage + t * (kTile / 2) + panel_off_bf16(lane, 4 + i, LC)) =
+                            make_uint4(pack_bf16(two(y[8 * i], y[8 * i + 1])), pack_bf16(two(y[8 * i + 2], y[8 * i + 3])),
+                                       pack_bf16(two(y[8 * i + 4], y[8 * i + 5])), pack_bf16(two(y[8 * i + 6], y[8 * i + 7])));
+                    }
+                    send(t, t);
+                }
+            } else {
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    if (t == 2) staged();
+                    uint32_t x[32];
+                    tmem_ld32_issue(lanes + kColO + 32 * t, x);
+                    tmem_wait_ld(x);
+                    if (t == 3) {
+                        tc_fence_before();
+                        mbar_arrive(&sm.r);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(stage + (t & 1) * (kTile / 2) + panel_off_bf16(lane, i, LC)) =
+                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    send(t, t & 1);
+                }
+            }
         }
     }
+    if (lane == 0) bulk_wait_all();
     if (!ok && lane == 0) raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
-// w x as a sum of bf16 parts: 16 significant bits in two, 24 in three. x: eight bf16 values.
-__device__ __forceinline__ void split_two(float w, const uint32_t (&x)[4], uint32_t (&hi)[4], uint32_t (&mi)[4]) {
-    // w = w1 + w2; w1 x = hi + e without error (e, the error of a rounded product, has 8 bits); mid = w2 x + e
-    const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
-    const __nv_bfloat162 a = __bfloat162bfloat162(w1), b = __bfloat162bfloat162(w2);
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&x[d]);
-        const __nv_bfloat162 h = __hmul2_rn(a, v);
-        const __nv_bfloat162 m = __hfma2(b, v, __hfma2(a, v, __hneg2(h)));
-        hi[d] = *reinterpret_cast<const uint32_t*>(&h);
-        mi[d] = *reinterpret_cast<const uint32_t*>(&m);
-    }
-}
-__device__ __forceinline__ void split_three(float w, const uint32_t (&x)[4], uint32_t (&hi)[4], uint32_t (&mi)[4], uint32_t (&lo)[4]) {
-    const f32x2 w2 = two(w, w), minus = two(-1.0f, -1.0f);
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        f32x2 p = mul2(w2, two(low_bf16(x[d]), high_bf16(x[d])));
-        hi[d] = pack_bf16(p);
-        p = fma2(minus, two(low_bf16(hi[d]), high_bf16(hi[d])), p);
-        mi[d] = pack_bf16(p);
-        p = fma2(minus, two(low_bf16(mi[d]), high_bf16(mi[d])), p);
-        lo[d] = pack_bf16(p);
-    }
-}
-
-// --- state in registers, its bf16 copy for the next chunk; decayed keys in bf16 parts; outputs
+// --- state in registers and its bf16 copy for the next chunk; decayed keys as bf16 parts; Q S^T decayed by row
 __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
-    const int heads = a.H;
-    const int t = threadIdx.x - 32 * kScoreWarps, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-    const int row = 32 * warp + lane, half = t >> 7;             // state or output row, which 64 columns of it
-    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16) + 64 * half;
-    const int ch = t & 15, r0 = t >> 4;                          // decayed keys: 16-byte chunk, rows r0 + 16 i
-    const uint32_t off = panel_off_bf16(r0, ch, LC);
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, half = (threadIdx.x - 32 * kScoreWarps) >> 7;
+    const int row = 32 * warp + lane;              // TMEM lane: output row, or key channel of the state
+    const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16), wide = lanes + 64 * half;
+    // decayed keys: this warp's channels 32 warp + .., tokens 64 half + ..; ldmatrix row of this thread
+    const int jl = 64 * half + 8 * (lane >> 4) + (lane & 7), cl = 4 * warp + ((lane >> 3) & 1);
+    const int jr = 64 * half + 2 * (lane & 3);     // first token of its fragment register 0
+    const uint32_t key = smem_u32(sm.K);
     bool ok = true;
     int n = 0;
-    f32x2 s[32];
-    auto grow = [&](float decay) {   // s = decay s + the state sum of the last chunk
-        const f32x2 w = two(decay, decay);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            uint32_t r[2][16];
-            tmem_ld16_issue(lanes + kColDS + 32 * b, r[0]);
-            tmem_ld16_issue(lanes + kColDS + 32 * b + 16, r[1]);
-            tmem_wait_ld16(r[0]);
-            tmem_after_wait16(r[1]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[16 * b + i] = fma2(w, s[16 * b + i], two(r[i >> 3][2 * (i & 7)], r[i >> 3][2 * (i & 7) + 1]));
-        }
-    };
+    f32x2 s[32];                                   // S[v][row], v = 64 half + ..
     for (int round = 0; ok; ++round) {
         const int at = unit_at(round);
         if (at >= units) break;
@@ -478,31 +533,128 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
         const int chunks = chunks_of(u);
         if (u.s_in && u.s_in_t) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = two(u.s_in[(64 * half + 2 * i) * D + row], u.s_in[(64 * half + 2 * i + 1) * D + row]);
-        } else if (u.s_in) {
-#pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 const float4 x = *reinterpret_cast<const float4*>(u.s_in + row * D + 64 * half + 2 * i);
                 s[i] = two(x.x, x.y); s[i + 1] = two(x.z, x.w);
             }
+        } else if (u.s_in) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = two(u.s_in[(64 * half + 2 * i) * D + row], u.s_in[(64 * half + 2 * i + 1) * D + row]);
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[i] = 0ull;
         }
-        const float whole = decay_pow(u.g, LC);
         const float w_state = u.out_scale * decay_pow(u.g, u.rev ? LC - 1 - row : row + 1);
         const f32x2 w2 = two(w_state, w_state);
-        float wk[8];   // decays of this thread's key rows in a whole chunk
+        const float whole_decay = decay_pow(u.g, LC);
+        // the decays k_scale gamma^{..} of tokens jr + 8 i and the next in a whole chunk, as w = w1 + w2 in bf16
+        uint32_t wk1[8], wk2[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wk[i] = u.k_scale * decay_pow(u.g, u.rev ? r0 + 16 * i + 1 : LC - 1 - (r0 + 16 * i));
-        for (int c = 0; c < chunks; ++c, ++n) {
-            if (c > 0) {
+        for (int i = 0; i < 8; ++i) {
+            const int j = jr + 8 * i;
+            const float x = u.k_scale * decay_pow(u.g, u.rev ? j + 1 : LC - 1 - j), y = u.k_scale * decay_pow(u.g, u.rev ? j + 2 : LC - 2 - j);
+            wk1[i] = pack_bf16(x, y);
+            wk2[i] = pack_bf16(x - low_bf16(wk1[i]), y - high_bf16(wk1[i]));
+        }
+        for (int c = 0; ok && chunks > 0; ++c) {
+            if (c > 0) {   // the state sum of chunk c - 1 is there, its decayed keys are no longer needed
                 if (!(ok = wait_warp(&sm.ds, n - 1))) break;
                 tc_fence_after();
-                grow(whole);
             }
-            const bool carried = c > 0 || u.s_in;
-            if (!state_only && carried) {
+            const bool carried = c > 0 || u.s_in, sum = c + 1 < chunks || (c < chunks && u.s_out), three = sum && three_parts(u, c);
+            auto parts_fp32 = [&](const Chunk& k, bool low) {
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t x[8], hi[8], mi[8], lo[8];
+                    const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
+                    ldmatrix4_trans(key + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
+                    ldmatrix4_trans(key + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const int t = jr + 32 * (g >> 1) + 8 * m;
+                        const bool mine0 = t >= k.lo && t < k.hi, mine1 = t + 1 >= k.lo && t + 1 < k.hi;
+                        const int e = u.rev ? t + 1 - k.lo : k.hi - 1 - t, d = u.rev ? 1 : -1;
+                        const f32x2 w = two(u.k_scale * decay_pow(u.g, mine0 ? e : 0), u.k_scale * decay_pow(u.g, mine1 ? e + d : 0));
+                        const uint32_t mask = (mine0 ? 0xffffu : 0u) | (mine1 ? 0xffff0000u : 0u);
+                        const f32x2 minus = two(-1.0f, -1.0f);
+#pragma unroll
+                        for (int i = 2 * m; i < 2 * m + 2; ++i) {
+                            x[i] &= mask;
+                            f32x2 p = mul2(w, two(low_bf16(x[i]), high_bf16(x[i])));
+                            hi[i] = pack_bf16(p);
+                            p = fma2(minus, two(low_bf16(hi[i]), high_bf16(hi[i])), p);
+                            mi[i] = pack_bf16(p);
+                            p = fma2(minus, two(low_bf16(mi[i]), high_bf16(mi[i])), p);
+                            lo[i] = pack_bf16(p);
+                        }
+                    }
+                    const uint32_t at_t = lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1);
+                    if (low) {
+                        tmem_st_frag_issue(at_t + low_col(u.rev), lo);
+                    } else {
+                        tmem_st_frag_issue(at_t + kColMid, mi);
+                        tmem_st_frag_issue(at_t + kColHi, hi);
+                    }
+                }
+            };
+            if (c < chunks) {
+                // decayed keys, transposed to [channel][token], to tensor memory: first, while the scores and
+                // outputs of chunk c - 1 leave shared memory read cycles
+                if (!(ok = wait_warp(&sm.full_k, n))) break;
+                const Chunk k = chunk_of(u, c);
+                const bool whole = k.hi - k.lo == LC;
+                if (!whole) {   // rows of a neighbour in V: their scores are zero, and zero times an infinity is not
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(&sm.full_v[n & 1], (uint32_t)((n >> 1) & 1))))) break;
+                    if (row < k.lo || row >= k.hi)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(sm.V[n & 1] + panel_off_bf16(row, 8 * half + i, LC)) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_async_smem();
+                }
+                if (sum && whole && !three) {
+                    // w1 x = hi + e without error (the error of a rounded product has 8 bits), mid = w2 x + e
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {   // 32 tokens x 16 channels
+                        uint32_t x[8], hi[8], mi[8];
+                        const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
+                        ldmatrix4_trans(key + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
+                        ldmatrix4_trans(key + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int w = 4 * (g >> 1) + (i >> 1);
+                            const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&x[i]);
+                            const __nv_bfloat162 w1 = *reinterpret_cast<const __nv_bfloat162*>(&wk1[w]);
+                            const __nv_bfloat162 h = __hmul2_rn(w1, y);
+                            const __nv_bfloat162 m = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&wk2[w]), y, __hfma2(w1, y, __hneg2(h)));
+                            hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+                            mi[i] = *reinterpret_cast<const uint32_t*>(&m);
+                        }
+                        const uint32_t at_t = lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1);
+                        tmem_st_frag_issue(at_t + kColMid, mi);
+                        tmem_st_frag_issue(at_t + kColHi, hi);
+                    }
+                } else if (sum) {   // three parts, or rows of a neighbour among the tokens: in fp32
+                    parts_fp32(k, false);
+                }
+                tmem_wait_st_all();
+                tc_fence_before();
+                mbar_arrive(&sm.piece);
+                if (!three) mbar_arrive(&sm.k_free);
+            }
+            if (c > 0 && (c < chunks || u.s_out)) {   // the state after chunk c - 1
+                const float w = c < chunks ? whole_decay : decay_pow(u.g, u.len - (c - 1) * LC);
+                const f32x2 decay = two(w, w);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t r[32];
+                    tmem_ld32_issue(wide + kColDS + 32 * b, r);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[16 * b + i] = fma2(decay, s[16 * b + i], two(r[2 * i], r[2 * i + 1]));
+                }
+            }
+            if (c == chunks) break;
+            if (!state_only && carried) {   // sm.S was last read before the state sum just waited for
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(sm.S + panel_off_bf16(row, 8 * half + i, LC)) =
@@ -511,105 +663,45 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             }
             tc_fence_before();
             mbar_arrive(&sm.s);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full_k[n & 1], (uint32_t)((n >> 1) & 1))) && wait_warp(&sm.qk, n))) break;
-            const Chunk k = chunk_of(u, c);
-            if (c + 1 < chunks || u.s_out) {
-                uint8_t* const key = sm.K[n & 1];
-                if (k.hi - k.lo < LC || three_parts(u, c)) {
-#pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r0 + 16 * i;
-                        const bool mine = r >= k.lo && r < k.hi;   // nothing of a neighbour's rows
-                        const float w = u.k_scale * decay_pow(u.g, mine ? (u.rev ? r + 1 - k.lo : k.hi - 1 - r) : 0);
-                        const uint32_t o = off + i * 2048;
-                        const uint4 y = mine ? *reinterpret_cast<const uint4*>(key + o) : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
-                        uint32_t hi[4], mi[4], lo[4];
-                        split_three(w, x, hi, mi, lo);
-                        *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-                        *reinterpret_cast<uint4*>(sm.LOW + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                } else {
+            // out_scale gamma^{..} Q S^T, the rows' decays, before the scores' part is added to it
+            if (!(ok = wait_warp(&sm.qs, n))) break;
+            if (!state_only && carried) {
+                tc_fence_after();
 #pragma unroll
-                    for (int i0 = 0; i0 < 8; i0 += 4) {
-                        uint4 y[4];
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t x[32];
+                    tmem_ld32_issue(wide + kColO + 32 * b, x);
+                    tmem_wait_ld(x);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const uint4*>(key + off + (i0 + e) * 2048);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t x[4] = {y[e].x, y[e].y, y[e].z, y[e].w}, o = off + (i0 + e) * 2048;
-                            uint32_t hi[4], mi[4];
-                            split_two(wk[i0 + e], x, hi, mi);
-                            *reinterpret_cast<uint4*>(key + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(sm.MID + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-                        }
-                    }
-                }
-                fence_async_smem();
-            }
-            mbar_arrive(&sm.piece);
-            if (!(ok = wait_warp(&sm.pv, n))) break;
-            if (state_only) continue;
-            // scores V + out_scale gamma^{..} Q S^T, by way of shared memory (this warp's part of S) so
-            // that whole 128-byte lines leave: 64 bf16 columns, or 32 fp32 columns of a share at a time
-            tc_fence_after();
-            uint8_t* const stage = sm.S + half * (kTile / 2);
-            const int first = 32 * warp + (lane >> 3);
-            auto store = [&](uint8_t* base, int pitch) {   // base: row 0 of the chunk at this head and part
-                __syncwarp();
-                const int64_t step = (int64_t)heads * pitch;
-                uint8_t* p = base + (k.t + first) * step + (lane & 7) * 16;
-#pragma unroll
-                for (int i = 0; i < 8; ++i, p += 4 * step) {
-                    const int r = first + 4 * i;
-                    const uint4 x = *reinterpret_cast<const uint4*>(stage + panel_off_bf16(r, lane & 7, LC));
-                    if (r >= k.lo && r < k.hi) *reinterpret_cast<uint4*>(p) = x;
-                }
-                __syncwarp();
-            };
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {   // 16 columns at a time
-                uint32_t x[16], y[16];
-                tmem_ld16_issue(lanes + kColPV + 16 * b, x);
-                if (carried) tmem_ld16_issue(lanes + kColQS + 16 * b, y);
-                tmem_wait_ld16(x);
-                if (carried) {
-                    tmem_after_wait16(y);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 z = parts(fma2(w2, two(y[i], y[i + 1]), two(x[i], x[i + 1])));
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 z = parts(mul2(w2, two(x[i], x[i + 1])));
                         x[i] = __float_as_uint(z.x);
                         x[i + 1] = __float_as_uint(z.y);
                     }
+                    tmem_st32_issue(wide + kColO + 32 * b, x);
                 }
-                if (u.share) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(stage + panel_off_bf16(row, 4 * (b & 1) + i, LC)) =
-                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    if (b & 1) store(reinterpret_cast<uint8_t*>(u.share + (size_t)u.h * D + 64 * half + 16 * (b - 1)), D * (int)sizeof(float));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint4*>(stage + panel_off_bf16(row, 2 * b + i, LC)) =
-                            make_uint4(pack_bf16(two(x[8 * i], x[8 * i + 1])), pack_bf16(two(x[8 * i + 2], x[8 * i + 3])),
-                                       pack_bf16(two(x[8 * i + 4], x[8 * i + 5])), pack_bf16(two(x[8 * i + 6], x[8 * i + 7])));
-                }
+                tmem_wait_st_all();
+                tc_fence_before();
             }
-            if (!u.share) store(reinterpret_cast<uint8_t*>(u.out + (size_t)u.h * D + 64 * half), D * (int)sizeof(uint16_t));
+            mbar_arrive(&sm.o);
+            if (three) {   // the low parts: beside the scores' bf16 copy, once that is made
+                if (!(ok = wait_warp(&sm.p, n))) break;
+                tc_fence_after();
+                parts_fp32(chunk_of(u, c), true);
+                tmem_wait_st_all();
+                tc_fence_before();
+                mbar_arrive(&sm.k_free);
+                mbar_arrive(&sm.low);
+            }
+            ++n;
         }
         if (!ok) break;
-        if (chunks > 0) {
-            if (!(ok = wait_warp(&sm.ds, n - 1))) break;
-            tc_fence_after();
-            if (u.s_out) grow(decay_pow(u.g, u.len - (chunks - 1) * LC));
-        }
         if (u.s_out) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const float2 x = parts(s[i]), y = parts(s[i + 1]);
-                *reinterpret_cast<float4*>(u.s_out + row * D + 64 * half + 2 * i) = make_float4(x.x, x.y, y.x, y.y);
+            for (int i = 0; i < 32; ++i) {
+                const float2 x = parts(s[i]);
+                u.s_out[(64 * half + 2 * i) * D + row] = x.x;
+                u.s_out[(64 * half + 2 * i + 1) * D + row] = x.y;
             }
         }
     }
@@ -633,10 +725,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        mbar_init(&sm.full_k[0], 1); mbar_init(&sm.full_k[1], 1); mbar_init(&sm.full_q, 1); mbar_init(&sm.full_v, 1);
-        mbar_init(&sm.qk, 1); mbar_init(&sm.qs, 1); mbar_init(&sm.pv, 1); mbar_init(&sm.ds, 1);
-        mbar_init(&sm.s, 32 * kMainWarps); mbar_init(&sm.piece, 32 * kMainWarps);
+        uint64_t* const one[] = {&sm.full_k, &sm.full_q[0], &sm.full_q[1], &sm.full_v[0], &sm.full_v[1],
+                                 &sm.qk, &sm.qs, &sm.ds, &sm.pv, &sm.end};
+        for (uint64_t* bar : one) mbar_init(bar, 1);
+        uint64_t* const all_main[] = {&sm.s, &sm.piece, &sm.low, &sm.k_free, &sm.o};
+        for (uint64_t* bar : all_main) mbar_init(bar, 32 * kMainWarps);
         mbar_init(&sm.p, 32 * kScoreWarps);
+        mbar_init(&sm.r, 32 * kScoreWarps);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -890,8 +985,8 @@ kda_status common_checks(const kda_linattn_shape* sh, const int64_t* cu, const v
     return KDA_OK;
 }
 
-// The tensor map of a [tokens, heads, 128] bf16 tensor.
-kda_status make_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t heads) {
+// The tensor map of a [tokens, heads, 128] bf16 (or fp32) tensor in boxes of `rows` tokens x 128 bytes.
+kda_status make_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t heads, int rows, bool fp32 = false) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -908,9 +1003,9 @@ kda_status make_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t hea
         return KDA_ERR_CUDA;
     }
     const cuuint64_t dims[3] = {D, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {D * 2, (cuuint64_t)heads * D * 2};
-    const cuuint32_t box[3] = {64, 1, LC}, step[3] = {1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
+    const cuuint64_t size = fp32 ? 4 : 2, strides[2] = {D * size, (cuuint64_t)heads * D * size};
+    const cuuint32_t box[3] = {fp32 ? 32u : 64u, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
+    const CUresult r = encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) return KDA_OK;
@@ -930,12 +1025,15 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
         set_last_error_text(cudaGetErrorString(e));
         return KDA_ERR_CUDA;
     }
-    if (sh->B * sh->T > 0)
-        for (int i = 0; i < 4; ++i)
-            if (tensors[i]) {
-                const kda_status st = make_map(&a.map[i], tensors[i], sh->B * sh->T, sh->H / a.group[i]);
-                if (st != KDA_OK) return st;
-            }
+    const int64_t tokens = sh->B * sh->T;
+    kda_status st = KDA_OK;
+    for (int i = 0; i < 4 && tokens > 0 && st == KDA_OK; ++i)
+        if (tensors[i]) st = make_map(&a.map[i], tensors[i], tokens, sh->H / a.group[i], LC);
+    for (int i = 0; i < jobs && tokens > 0 && st == KDA_OK; ++i) {
+        const LinJob& j = a.job[i];
+        st = make_map(&a.out_map[i], j.share ? static_cast<void*>(j.share) : j.out, tokens, sh->H, 32, j.share != nullptr);
+    }
+    if (st != KDA_OK) return st;
     a.log_decay = log_decay;
     a.T = sh->T;
     a.H = (int)sh->H;
@@ -1004,7 +1102,7 @@ extern "C" kda_status kda_linattn_fwd(const kda_linattn_shape* shape, const kda_
     for (const void* p : ptrs)
         if (misaligned(p)) return KDA_ERR_ALIGN;
     const int G = groups_of(shape);
-    LinArgs a{{}, {G, G, 1, 1}};
+    LinArgs a{{}, {}, {G, G, 1, 1}};
     a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT != nullptr, 1.0f, shape->scale};
     const kda_status rs = run_jobs(shape, a, {q, k, v, nullptr}, 1, cu_seqlens, log_decay, static_cast<uint8_t*>(workspace),
                                    layout_of(shape, cu_seqlens != nullptr, false), static_cast<cudaStream_t>(stream));
@@ -1030,7 +1128,7 @@ extern "C" kda_status kda_linattn_bwd(const kda_linattn_shape* shape, const kda_
     float* const share_q = G > 1 ? reinterpret_cast<float*>(ws + lay.share_q) : nullptr;
     float* const share_k = G > 1 ? reinterpret_cast<float*>(ws + lay.share_k) : nullptr;
     const float sc = shape->scale;
-    LinArgs a{{}, {G, G, 1, 1}};
+    LinArgs a{{}, {}, {G, G, 1, 1}};
     a.job[0] = LinJob{3, 2, 1, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 0, 1.0f, sc};
     a.job[1] = LinJob{2, 3, 0, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 0, sc, 1.0f};
     a.job[2] = LinJob{1, 0, 3, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 != nullptr, sc, 1.0f};

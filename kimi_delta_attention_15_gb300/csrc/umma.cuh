@@ -61,6 +61,28 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
 }
 
+// The same for kernels whose waiting warps share an SM's issue slots with working ones: the thread may
+// sleep in the hardware for up to 20 us at a time and is woken when the phase completes.
+__device__ __forceinline__ bool mbar_try_wait_asleep(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+    if (mbar_try_wait_asleep(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (mbar_try_wait_asleep(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
 // ------------------------------------------------------ bulk (TMA) copies
 // global -> shared, completion counted in bytes on an mbarrier.
 // dst, src 16-byte aligned; bytes a multiple of 16.
@@ -93,6 +115,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
         "[%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+// shared -> a box of a 3-D tensor, tracked by bulk async-groups. No coordinate may be negative.
+__device__ __forceinline__ void tma_store_3d(const void* src, const void* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
 }
 
 // 16-byte asynchronous global -> shared copy (L2 only), grouped by commit.
@@ -244,6 +273,22 @@ __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+// 16 lanes (the first or second half of the warp's 32, by the address) x 16 consecutive columns from
+// ldmatrix fragments: register 2 m + e of thread t holds column 4 m + t % 4 of lane 8 e + t / 4
+__device__ __forceinline__ void tmem_st_frag_issue(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+        "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
+// four 8x8 matrices of 16-bit values, transposed: lanes 8 i .. 8 i + 7 give the row addresses of matrix
+// i; register i of thread t holds elements (2 (t % 4), t / 4) and (2 (t % 4) + 1, t / 4) of it
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(saddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st_all() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // wait for this thread's TMEM stores; r (the source of one of them) may change afterwards
