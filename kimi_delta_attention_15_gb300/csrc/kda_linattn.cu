@@ -29,8 +29,9 @@ constexpr uint32_t kTile = LC * D * 2;        // a bf16 operand tile [128][128],
 
 // One sum over tokens in the roles' names. Row i of a chunk of L rows, with the state S the
 // chunk starts from (e = 1 forward, 0 reversed: a token's decay applies before or after its read):
-//   out_i = out_scale (sum_{j <= i} k_scale gamma^{i-j} (q_i . k_j) v_j + gamma^{i+e} S q_i)
-//   S    <- gamma^L S + sum_j k_scale gamma^{L-e-j} v_j k_j^T
+//   out_i = scale (sum_{j <= i} gamma^{i-j} (q_i . k_j) v_j + gamma^{i+e} S q_i)
+//   S    <- gamma^L S + sum_j gamma^{L-e-j} v_j k_j^T
+// The adjoint state of a reversed job is scale times its S: s_in is divided and s_out multiplied by it.
 struct LinJob {
     int q, k, v;                 // which of LinArgs' tensors
     uint16_t* out;               // [tokens, H, 128] bf16, or
@@ -41,7 +42,7 @@ struct LinJob {
     int s_in_t, seg_t;           // s_in, seg are stored transposed
     int rev;                     // tokens from last to first
     int exact;                   // the state is an output: fp32-accurate (else as good as its bf16 copy needs)
-    float k_scale, out_scale;
+    float s_scale;               // of s_in and s_out over S: 1, or scale
 };
 
 // A slot is a segment of a sequence; a sequence has one at least, an empty one too.
@@ -66,6 +67,7 @@ struct LinArgs {
     int nseg;
     int64_t seg_len, T;
     const float* log_decay;
+    float scale;
     int H;
     uint8_t* ws;
 };
@@ -94,7 +96,8 @@ struct Unit {
     int job, q, k, v;              // tensors
     uint8_t* out;                  // out or share
     bool fp32;
-    float k_scale, out_scale, g;   // g: log decay
+    float scale, g;                // g: log decay
+    float in_scale, out_scale;     // what the state is multiplied with on its way in and out
     int exact, after;              // after: tokens of the sequence still to come after this unit
     const float* s_in;             // where this unit's state comes from and goes to, NULL: zero, not wanted
     float* s_out;
@@ -114,8 +117,8 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     x.job = ji;
     x.fp32 = j.share != nullptr;
     x.out = x.fp32 ? reinterpret_cast<uint8_t*>(j.share) : reinterpret_cast<uint8_t*>(j.out);
-    x.k_scale = j.k_scale;
-    x.out_scale = j.out_scale;
+    x.scale = a.scale;
+    x.in_scale = x.out_scale = 1.0f;
     x.g = a.log_decay[x.h];
     x.exact = j.exact;
     x.after = j.rev ? s.before : s.after;
@@ -129,6 +132,10 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     } else {
         x.s_in = head ? (j.s_in ? j.s_in + seq_state : nullptr) : j.seg + seg_state;
         x.s_in_t = head ? j.s_in_t : j.seg_t;
+        if (x.len > 0) {           // an empty sequence's state passes through unchanged
+            if (head) x.in_scale = 1.0f / j.s_scale;
+            x.out_scale = j.s_scale;
+        }
         x.s_out = tail && j.s_out ? j.s_out + seq_state : nullptr;
     }
     return x;
@@ -156,10 +163,10 @@ __device__ __forceinline__ Chunk chunk_of(const Unit& u, int c) {
 }
 // The decayed keys of a chunk go into the state's sum as two bf16 parts (16 significant bits), or as
 // three (24) where the state is an output and the tokens still to come will not have decayed this
-// chunk's share, and its error with it, by another 2^-8.
+// chunk's share, and its error with it, by another 2^-8. (Without any decay one part is exact.)
 __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
     const int left = u.after + max(u.len - (c + 1) * LC, 0);
-    return u.exact && (left == 0 || u.g * (float)left > -5.6f);
+    return u.exact && u.g != 0.0f && (left == 0 || u.g * (float)left > -5.6f);
 }
 __device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
 
@@ -169,6 +176,7 @@ struct LinSmem {
     uint8_t S[kTile];        // the state the chunk starts from, [c][v], rounded to bf16
     uint8_t stage[kTile];    // output rows on their way out
     float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
+    float decay[LC];         // of the keys of a whole chunk
     // full: operands in shared memory; qk, qs, ds, pv: MMA groups done; s, p, piece, low, o: operands written
     // (state, scores, decayed keys and their low parts, decayed Q S^T); k_free, r: keys, outputs read. Each completes one
     // phase per chunk (full_q, full_v: one of the two; low: per chunk with three parts).
@@ -263,6 +271,12 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
         if (state_only) mbar_arrive(&sm.full_q[b]);
         else tile(sm.Q[b], x.u.q, x, &sm.full_q[b]);
     };
+    auto ahead = [&](int which, const At& x) {
+        const Chunk k = chunk_of(x.u, x.c);
+        const int head = x.u.h / a.group[which];
+        tma_prefetch_3d(&a.map[which], 0, head, (int)k.t);
+        tma_prefetch_3d(&a.map[which], 64, head, (int)k.t);
+    };
     At x;   // the chunk after n
     x.first(a, units);
     if (!x.more) return;
@@ -270,7 +284,11 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
     q_tile(0, x);
     tile(sm.V[0], x.u.v, x, &sm.full_v[0]);
     x.next(a, units);
-    if (x.more) q_tile(1, x);
+    if (x.more) {
+        q_tile(1, x);
+        ahead(x.u.k, x);
+        ahead(x.u.v, x);
+    }
     for (int n = 0; x.more; ++n) {
         // Q S^T of chunk n done: so are its scores and everything of chunk n - 1. K is free with its decayed
         // copies made, Q[n & 1] and V[(n + 1) & 1] are free.
@@ -281,7 +299,11 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
         tile(sm.K, x.u.k, x, &sm.full_k);
         tile(sm.V[(n + 1) & 1], x.u.v, x, &sm.full_v[(n + 1) & 1]);
         x.next(a, units);
-        if (x.more) q_tile(n & 1, x);
+        if (x.more) {
+            q_tile(n & 1, x);
+            ahead(x.u.k, x);   // K and V of chunk n + 2 on their way into L2: from there they arrive in time
+            ahead(x.u.v, x);
+        }
     }
 }
 
@@ -379,10 +401,10 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
         if (chunks == 0) continue;
         const float g = u.g;
         const bool rev = u.rev != 0;
-        // scale gamma^{|row - col|} with both scales, row = 32 warp + lane, col = 32 b + x. Off the diagonal's
+        // scale gamma^{|row - col|}, row = 32 warp + lane, col = 32 b + x. Off the diagonal's
         // block it is gamma^{32 |warp - b| - 31} f[x], f[x] = scale gamma^{31 + lane - x} (reversed:
         // 31 - lane + x): no exponent is negative. On it, diag[lane - x + 31].
-        const float scale = u.k_scale * u.out_scale;
+        const float scale = u.scale;
         f32x2 f[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x)
@@ -535,24 +557,30 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 const float4 x = *reinterpret_cast<const float4*>(u.s_in + row * D + 64 * half + 2 * i);
-                s[i] = two(x.x, x.y); s[i + 1] = two(x.z, x.w);
+                s[i] = two(u.in_scale * x.x, u.in_scale * x.y); s[i + 1] = two(u.in_scale * x.z, u.in_scale * x.w);
             }
         } else if (u.s_in) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = two(u.s_in[(64 * half + 2 * i) * D + row], u.s_in[(64 * half + 2 * i + 1) * D + row]);
+            for (int i = 0; i < 32; ++i)
+                s[i] = two(u.in_scale * u.s_in[(64 * half + 2 * i) * D + row], u.in_scale * u.s_in[(64 * half + 2 * i + 1) * D + row]);
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[i] = 0ull;
         }
-        const float w_state = u.out_scale * decay_pow(u.g, u.rev ? LC - 1 - row : row + 1);
+        const float w_state = u.scale * decay_pow(u.g, u.rev ? LC - 1 - row : row + 1);
         const f32x2 w2 = two(w_state, w_state);
         const float whole_decay = decay_pow(u.g, LC);
-        // the decays k_scale gamma^{..} of tokens jr + 8 i and the next in a whole chunk, as w = w1 + w2 in bf16
+        // the decays of the tokens of a whole chunk in fp32 (every warp writes the same values; none is still
+        // reading another unit's: its last state sum has been waited for), and those of tokens jr + 8 i and the
+        // next as w = w1 + w2 in bf16
+#pragma unroll
+        for (int i = 0; i < LC; i += 32) sm.decay[lane + i] = decay_pow(u.g, u.rev ? lane + i + 1 : LC - 1 - (lane + i));
+        __syncwarp();
         uint32_t wk1[8], wk2[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int j = jr + 8 * i;
-            const float x = u.k_scale * decay_pow(u.g, u.rev ? j + 1 : LC - 1 - j), y = u.k_scale * decay_pow(u.g, u.rev ? j + 2 : LC - 2 - j);
+            const float x = sm.decay[j], y = sm.decay[j + 1];
             wk1[i] = pack_bf16(x, y);
             wk2[i] = pack_bf16(x - low_bf16(wk1[i]), y - high_bf16(wk1[i]));
         }
@@ -573,8 +601,9 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                     for (int m = 0; m < 4; ++m) {
                         const int t = jr + 32 * (g >> 1) + 8 * m;
                         const bool mine0 = t >= k.lo && t < k.hi, mine1 = t + 1 >= k.lo && t + 1 < k.hi;
-                        const int e = u.rev ? t + 1 - k.lo : k.hi - 1 - t, d = u.rev ? 1 : -1;
-                        const f32x2 w = two(u.k_scale * decay_pow(u.g, mine0 ? e : 0), u.k_scale * decay_pow(u.g, mine1 ? e + d : 0));
+                        // gamma^{L-1-t} (reversed, counted from the end: gamma^{t+1-lo}) is at t + 128 - L (t - lo)
+                        const int e = u.rev ? t - k.lo : t + LC - k.hi;
+                        const f32x2 w = two(sm.decay[mine0 ? e : 0], sm.decay[mine1 ? e + 1 : 0]);
                         const uint32_t mask = (mine0 ? 0xffffu : 0u) | (mine1 ? 0xffff0000u : 0u);
                         const f32x2 minus = two(-1.0f, -1.0f);
 #pragma unroll
@@ -644,14 +673,13 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             if (c > 0 && (c < chunks || u.s_out)) {   // the state after chunk c - 1
                 const float w = c < chunks ? whole_decay : decay_pow(u.g, u.len - (c - 1) * LC);
                 const f32x2 decay = two(w, w);
+                uint32_t r[2][32];
+                tmem_ld32_issue(wide + kColDS, r[0]);
+                tmem_ld32_issue(wide + kColDS + 32, r[1]);
+                tmem_wait_ld(r[0]);
+                tmem_after_wait(r[1]);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t r[32];
-                    tmem_ld32_issue(wide + kColDS + 32 * b, r);
-                    tmem_wait_ld(r);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[16 * b + i] = fma2(decay, s[16 * b + i], two(r[2 * i], r[2 * i + 1]));
-                }
+                for (int i = 0; i < 32; ++i) s[i] = fma2(decay, s[i], two(r[i >> 4][2 * (i & 15)], r[i >> 4][2 * (i & 15) + 1]));
             }
             if (c == chunks) break;
             if (!state_only && carried) {   // sm.S was last read before the state sum just waited for
@@ -663,7 +691,7 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             }
             tc_fence_before();
             mbar_arrive(&sm.s);
-            // out_scale gamma^{..} Q S^T, the rows' decays, before the scores' part is added to it
+            // scale gamma^{..} Q S^T, the rows' decays, before the scores' part is added to it
             if (!(ok = wait_warp(&sm.qs, n))) break;
             if (!state_only && carried) {
                 tc_fence_after();
@@ -700,8 +728,8 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const float2 x = parts(s[i]);
-                u.s_out[(64 * half + 2 * i) * D + row] = x.x;
-                u.s_out[(64 * half + 2 * i + 1) * D + row] = x.y;
+                u.s_out[(64 * half + 2 * i) * D + row] = u.out_scale * x.x;
+                u.s_out[(64 * half + 2 * i + 1) * D + row] = u.out_scale * x.y;
             }
         }
     }
@@ -778,6 +806,8 @@ __global__ void __launch_bounds__(256) linattn_carry_kernel(const __grid_constan
         } else {
             x = *reinterpret_cast<const float4*>(j.s_in + seq + e);
         }
+        const float over = 1.0f / j.s_scale;
+        x.x *= over; x.y *= over; x.z *= over; x.w *= over;
     }
     for (int k = 0; k < s.nseg; ++k) {
         const int at = j.rev ? i + s.nseg - 1 - k : i + k;
@@ -1035,6 +1065,7 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
     }
     if (st != KDA_OK) return st;
     a.log_decay = log_decay;
+    a.scale = sh->scale;
     a.T = sh->T;
     a.H = (int)sh->H;
     a.ws = ws;
@@ -1103,7 +1134,7 @@ extern "C" kda_status kda_linattn_fwd(const kda_linattn_shape* shape, const kda_
         if (misaligned(p)) return KDA_ERR_ALIGN;
     const int G = groups_of(shape);
     LinArgs a{{}, {}, {G, G, 1, 1}};
-    a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT != nullptr, 1.0f, shape->scale};
+    a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT != nullptr, 1.0f};
     const kda_status rs = run_jobs(shape, a, {q, k, v, nullptr}, 1, cu_seqlens, log_decay, static_cast<uint8_t*>(workspace),
                                    layout_of(shape, cu_seqlens != nullptr, false), static_cast<cudaStream_t>(stream));
     return rs != KDA_OK ? rs : launched("kda_linattn_fwd launch");
@@ -1129,9 +1160,9 @@ extern "C" kda_status kda_linattn_bwd(const kda_linattn_shape* shape, const kda_
     float* const share_k = G > 1 ? reinterpret_cast<float*>(ws + lay.share_k) : nullptr;
     const float sc = shape->scale;
     LinArgs a{{}, {}, {G, G, 1, 1}};
-    a.job[0] = LinJob{3, 2, 1, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 0, 1.0f, sc};
-    a.job[1] = LinJob{2, 3, 0, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 0, sc, 1.0f};
-    a.job[2] = LinJob{1, 0, 3, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 != nullptr, sc, 1.0f};
+    a.job[0] = LinJob{3, 2, 1, dq, share_q, h0, nullptr, nullptr, 1, 0, 0, 0, 1.0f};
+    a.job[1] = LinJob{2, 3, 0, dk, share_k, dhT, nullptr, nullptr, 1, 1, 1, 0, sc};
+    a.job[2] = LinJob{1, 0, 3, dv, nullptr, dhT, dh0, nullptr, 0, 0, 1, dh0 != nullptr, sc};
     const kda_status rs = run_jobs(shape, a, {q, k, v, do_}, 3, cu_seqlens, log_decay, ws, lay, s);
     if (rs != KDA_OK) return rs;
     if (G > 1 && tokens > 0) {

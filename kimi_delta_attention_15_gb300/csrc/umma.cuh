@@ -117,6 +117,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
         : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const void* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 // shared -> a box of a 3-D tensor, tracked by bulk async-groups. No coordinate may be negative.
 __device__ __forceinline__ void tma_store_3d(const void* src, const void* map, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
