@@ -2,113 +2,581 @@
 //   y  = (x - mean) rstd w + b
 //   dx = rstd (a - mean(a) - xh mean(a xh)),  a = dy w,  xh = (x - mean) rstd
 //   dw = sum_rows dy xh,  db = sum_rows dy
+// A few operations per byte: HBM bounds all of it, so every input is read once and kept in
+// registers between the row's sums and its outputs, and dw, db are summed on the same pass, each
+// thread over the rows it meets for columns of its own, in registers. Three forms, by width:
+//  - narrow (up to 64 units a row): rows by warps, several at a time, sums by shuffles;
+//  - wide (up to 16384 columns): persistent blocks, a row at a time, rows arriving in shared memory
+//    by bulk copies some rows ahead;
+//  - beyond: a block for each row that reads it again for every step.
+// A unit is 16 bytes where the width is a multiple of it, a single element otherwise (bulk copies
+// then bring the aligned span around the row, and elements are read one by one from shared memory).
 #include <cmath>
 #include <cstdio>
 #include "kda_internal.cuh"
+#include "umma.cuh"
 
 namespace kda {
 void set_last_error_text(const char* msg);
 
 namespace {
 constexpr int kThreads = 256;
-constexpr int kPartRows = 304;   // most row blocks of the partial sums of dw, db
+constexpr int kSMs = 152;
+constexpr int kWideMost = 16384;       // columns of the wide form
+constexpr int kNarrowUnits = 64;       // units of the narrow form with 16-byte units
+constexpr int kNarrowColumns = 512;    // and with single elements
 
-template <typename T> __device__ __forceinline__ float ld(const T* p, size_t i);
-template <> __device__ __forceinline__ float ld<uint16_t>(const uint16_t* p, size_t i) { return bf2f(p[i]); }
-template <> __device__ __forceinline__ float ld<float>(const float* p, size_t i) { return p[i]; }
-__device__ __forceinline__ void st(uint16_t* p, size_t i, float x) { p[i] = f2bf(x); }
-__device__ __forceinline__ void st(float* p, size_t i, float x) { p[i] = x; }
+__device__ __forceinline__ float get(const uint16_t* p) { return bf2f(*p); }
+__device__ __forceinline__ float get(const float* p) { return *p; }
+__device__ __forceinline__ void put(uint16_t* p, float x) { *p = f2bf(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
 
-// sum over the block, the same value in every thread
-__device__ __forceinline__ float block_sum(float x, float* buf) {
+// A unit in registers as it is stored, and as fp32.
+template <typename T, int V> struct Unit;
+template <> struct Unit<uint16_t, 8> {
+    uint4 r;
+    __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load_stream(const uint16_t* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float at(int i) const {
+        const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
+        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    __device__ static __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
+        uint32_t w[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float s = 0.0f;
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) s += buf[i];
-    return s;
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+};
+template <> struct Unit<float, 4> {
+    float4 r;
+    __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void load_stream(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void zero() { r = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ float at(int i) const { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
+    __device__ static __forceinline__ void store(float* p, const float (&f)[4]) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    }
+};
+template <typename T> struct Unit<T, 1> {
+    float r;
+    __device__ __forceinline__ void load(const T* p) { r = get(p); }
+    __device__ __forceinline__ void load_stream(const T* p) { r = get(p); }
+    __device__ __forceinline__ void zero() { r = 0.0f; }
+    __device__ __forceinline__ float at(int) const { return r; }
+    __device__ static __forceinline__ void store(T* p, const float (&f)[1]) { put(p, f[0]); }
+};
+// the parameters of a unit's columns, `other` without one
+template <int V>
+__device__ __forceinline__ void params(const float* p, int c, float other, float (&f)[V]) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = other;
+    } else if constexpr (V == 1) {
+        f[0] = __ldg(p + c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + c + i));
+            f[i] = x.x; f[i + 1] = x.y; f[i + 2] = x.z; f[i + 3] = x.w;
+        }
+    }
 }
 
-// One row for each block, read three times (from the cache after the first).
-template <typename T>
+// A thread's columns are its own for all rows, so their parameters stay in registers, up to 24 columns
+// (they are as long as two or four bf16 rows: fetched for every row, 96 KB of them at a width of 12288
+// came from L2 each time and held the forward at 3.1 of 6.7 TB/s).
+template <int NV, int V> struct Params {
+    static constexpr bool kept = NV * V <= 24;
+    const float* p;
+    float other;
+    float f[kept ? NV : 1][V];
+    __device__ __forceinline__ void init(const float* from, float without, int first, int step, int units) {
+        p = from;
+        other = without;
+        if constexpr (kept)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) params<V>(first + step * k < units ? p : nullptr, (first + step * k) * V, other, f[k]);
+    }
+    __device__ __forceinline__ void at(int k, int i, float (&o)[V]) const {   // unit k of the thread, unit i of the row
+        if constexpr (kept)
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = f[k][e];
+        else params<V>(p, i * V, other, o);
+    }
+};
+
+// ---------------------------------------------------------------------------------- narrow
+// Lanes lpr * s .. lpr * (s + 1) - 1 of a warp hold row s of its 32 / lpr rows, lane l of them units
+// l, l + 32, .. (lpr < 32: one unit).
+__device__ __forceinline__ float lanes_sum(float x, int lpr) {
+    for (int o = lpr >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads)
-    layernorm_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b,
-                         T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width,
-                         float eps) {
-    __shared__ float buf[32];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* xr = x + r * width;
+    norm_fwd_narrow_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
+                           float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int units, int lpr,
+                           float eps) {
+    const int lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const float inv = 1.0f / (float)width;
+    Params<NV, V> pw, pb;
+    pw.init(w, 1.0f, l, 32, units);
+    pb.init(b, 0.0f, l, 32, units);
+    for (int64_t r0 = first * rpw; r0 < rows; r0 += warps * rpw) {
+        const int64_t r = r0 + sub;
+        const bool in = r < rows;
+        Unit<T, V> u[NV];
         float s = 0.0f;
-        for (int c = threadIdx.x; c < width; c += kThreads) s += ld(xr, c);
-        const float mu = block_sum(s, buf) / (float)width;
-        s = 0.0f;
-        for (int c = threadIdx.x; c < width; c += kThreads) {
-            const float d = ld(xr, c) - mu;
-            s += d * d;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = l + 32 * k;
+            if (in && i < units) u[k].load_stream(x + r * width + i * V);
+            else u[k].zero();
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += u[k].at(e);
         }
-        const float rs = rsqrtf(block_sum(s, buf) / (float)width + eps);
-        for (int c = threadIdx.x; c < width; c += kThreads)
-            st(y + r * width, c, (ld(xr, c) - mu) * rs * (w ? w[c] : 1.0f) + (b ? b[c] : 0.0f));
-        if (threadIdx.x == 0) {
+        const float mu = lanes_sum(s, lpr) * inv;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (l + 32 * k < units)
+#pragma unroll
+                for (int e = 0; e < V; ++e) s += (u[k].at(e) - mu) * (u[k].at(e) - mu);
+        const float rs = rsqrtf(lanes_sum(s, lpr) * inv + eps);
+        if (!in) continue;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = l + 32 * k;
+            if (i < units) {
+                float wv[V], bv[V], o[V];
+                pw.at(k, i, wv);
+                pb.at(k, i, bv);
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = (u[k].at(e) - mu) * rs * wv[e] + bv[e];
+                Unit<T, V>::store(y + r * width + i * V, o);
+            }
+        }
+        if (l == 0) {
             if (mean) mean[r] = mu;
             if (rstd) rstd[r] = rs;
         }
     }
 }
 
-template <typename T>
+template <typename T, int V, int NV, int R>   // R: row groups in flight
 __global__ void __launch_bounds__(kThreads)
-    layernorm_dx_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
-                        const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx, int64_t rows,
-                        int width) {
-    __shared__ float buf[32];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const float mu = mean[r], rs = rstd[r];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int c = threadIdx.x; c < width; c += kThreads) {
-            const float a = ld(dy, r * width + c) * (w ? w[c] : 1.0f);
-            s1 += a;
-            s2 += a * ((ld(x, r * width + c) - mu) * rs);
+    norm_bwd_narrow_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
+                           const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
+                           float* __restrict__ part, int64_t rows, int width, int units, int lpr) {
+    extern __shared__ float acc[];   // [warps][2][width]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), first = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const float inv = 1.0f / (float)width;
+    float wv[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        params<V>(w, l + 32 * k < units ? (l + 32 * k) * V : 0, 1.0f, wv[k]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
+    }
+    for (int64_t r0 = first * rpw; r0 < rows; r0 += R * warps * rpw) {
+        Unit<T, V> ux[R][NV], ug[R][NV];
+        float mu[R], rs[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = r0 + q * warps * rpw + sub;
+            const bool in = r < rows;
+            mu[q] = in ? mean[r] : 0.0f;
+            rs[q] = in ? rstd[r] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int i = l + 32 * k;
+                if (in && i < units) {
+                    ux[q][k].load_stream(x + r * width + i * V);
+                    ug[q][k].load_stream(dy + r * width + i * V);
+                } else {
+                    ux[q][k].zero();
+                    ug[q][k].zero();
+                }
+            }
         }
-        s1 = block_sum(s1, buf) / (float)width;
-        s2 = block_sum(s2, buf) / (float)width;
-        for (int c = threadIdx.x; c < width; c += kThreads) {
-            const float a = ld(dy, r * width + c) * (w ? w[c] : 1.0f);
-            st(dx + r * width, c, rs * (a - s1 - (ld(x, r * width + c) - mu) * rs * s2));
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = r0 + q * warps * rpw + sub;
+            float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float g = ug[q][k].at(e), h = (ux[q][k].at(e) - mu[q]) * rs[q], a = g * wv[k][e];
+                    s1 += a;
+                    s2 += a * h;
+                    dw[k][e] += g * h;
+                    db[k][e] += g;
+                }
+            s1 = lanes_sum(s1, lpr) * inv;
+            s2 = lanes_sum(s2, lpr) * inv;
+            if (r < rows)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int i = l + 32 * k;
+                    if (i < units) {
+                        float o[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            o[e] = rs[q] * (ug[q][k].at(e) * wv[k][e] - s1 - (ux[q][k].at(e) - mu[q]) * rs[q] * s2);
+                        Unit<T, V>::store(dx + r * width + i * V, o);
+                    }
+                }
+        }
+    }
+    if (!part) return;
+    // the warp's rows by lane, then the block's warps in order
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            for (int o = lpr; o < 32; o <<= 1) {
+                dw[k][e] += __shfl_xor_sync(0xffffffffu, dw[k][e], o);
+                db[k][e] += __shfl_xor_sync(0xffffffffu, db[k][e], o);
+            }
+    if (sub == 0)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (l + 32 * k < units)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    acc[(size_t)(2 * warp) * width + (l + 32 * k) * V + e] = dw[k][e];
+                    acc[(size_t)(2 * warp + 1) * width + (l + 32 * k) * V + e] = db[k][e];
+                }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * width; c += kThreads) {
+        float s = 0.0f;
+        for (int i = 0; i < kThreads / 32; ++i) s += acc[(size_t)2 * i * width + c];
+        part[(size_t)blockIdx.x * 2 * width + c] = s;
+    }
+}
+
+// ------------------------------------------------------------------------------------ wide
+// sums over the block, the same values in every thread; buf: 2 x 32 pairs used in turn, one barrier
+__device__ __forceinline__ float2 block_sums(float a, float b, float2* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    float2 s = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+        const float2 p = buf[i];
+        s.x += p.x;
+        s.y += p.y;
+    }
+    return s;
+}
+
+// Rows on their way to shared memory: the aligned span of row r of each input, `stages` rows ahead.
+// The last bytes of a tensor whose size is no multiple of 16 are not copied: read them with tail().
+struct Rows {
+    uint8_t* at;             // [stages][inputs][pitch]
+    uint64_t* full;          // [stages]
+    size_t row_bytes, most;  // most: the tensor's size rounded down to 16 bytes
+    int pitch, stages, inputs;
+    __device__ __forceinline__ void issue(int64_t r, int stage, const void* a, const void* b) const {
+        const size_t p = (size_t)r * row_bytes, from = p & ~(size_t)15;
+        size_t to = (p + row_bytes + 15) & ~(size_t)15;
+        if (to > most) to = most;
+        const uint32_t n = to > from ? (uint32_t)(to - from) : 0u;
+        mbar_arrive_expect_tx(&full[stage], n * (uint32_t)inputs);
+        if (n == 0) return;
+        bulk_g2s(at + (size_t)stage * inputs * pitch, static_cast<const uint8_t*>(a) + from, n, &full[stage]);
+        if (inputs > 1) bulk_g2s(at + ((size_t)stage * inputs + 1) * pitch, static_cast<const uint8_t*>(b) + from, n, &full[stage]);
+    }
+    // element c of row r of an input in shared memory
+    template <typename T>
+    __device__ __forceinline__ const T* row(int64_t r, int stage, int input) const {
+        return reinterpret_cast<const T*>(at + ((size_t)stage * inputs + input) * pitch + (((size_t)r * row_bytes) & 15));
+    }
+};
+// a unit of the row from shared memory, or from global memory past the copied part
+template <typename T, int V>
+__device__ __forceinline__ void take(Unit<T, V>& u, const Rows& m, const T* in_smem, const T* in_global, int64_t r, int c) {
+    if (V == 1 && (size_t)r * m.row_bytes + (size_t)(c + 1) * sizeof(T) > m.most) u.load(in_global + c);
+    else u.load(in_smem + c);
+}
+__device__ __forceinline__ Rows rows_of(uint8_t* smem, size_t row_bytes, int64_t rows, int pitch, int stages, int inputs) {
+    Rows m;
+    m.full = reinterpret_cast<uint64_t*>(smem);
+    m.at = smem + 64;
+    m.row_bytes = row_bytes;
+    m.most = (row_bytes * (size_t)rows) & ~(size_t)15;
+    m.pitch = pitch;
+    m.stages = stages;
+    m.inputs = inputs;
+    return m;
+}
+
+// Persistent blocks: row blockIdx.x, + gridDim.x, ..; thread t holds units t, t + blockDim.x, .. A wait that
+// gives up (2 s) ends the block without writing that row: there is no workspace to report it in, so the
+// forward writes NaN into the row's outputs.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512)
+    norm_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
+                         float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int units, int pitch,
+                         int stages, float eps) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 buf[2][32];
+    const Rows m = rows_of(smem, (size_t)width * sizeof(T), rows, pitch, stages, 1);
+    const int t = threadIdx.x, nt = blockDim.x;
+    const float inv = 1.0f / (float)width;
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&m.full[i], 1);
+        fence_mbar_init();
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + (int64_t)i * gridDim.x < rows) m.issue(blockIdx.x + (int64_t)i * gridDim.x, i, x, nullptr);
+    }
+    __syncthreads();
+    Params<NV, V> pw, pb;
+    pw.init(w, 1.0f, t, nt, units);
+    pb.init(b, 0.0f, t, nt, units);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const bool ok = mbar_wait(&m.full[stage], phase);
+        const T* row = m.row<T>(r, stage, 0);
+        Unit<T, V> u[NV];
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = t + nt * k;
+            if (i < units) take(u[k], m, row, x + r * width, r, i * V);
+            else u[k].zero();
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += u[k].at(e);
+        }
+        const float mu = block_sums(ok ? s : __int_as_float(0x7fffffff), 0.0f, buf[0]).x * inv;
+        // every thread has its part of the row in registers: the stage takes a later one
+        const int64_t next = r + (int64_t)stages * gridDim.x;
+        if (t == 0 && next < rows) m.issue(next, stage, x, nullptr);
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + nt * k < units)
+#pragma unroll
+                for (int e = 0; e < V; ++e) s += (u[k].at(e) - mu) * (u[k].at(e) - mu);
+        const float rs = rsqrtf(block_sums(s, 0.0f, buf[1]).x * inv + eps);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = t + nt * k;
+            if (i < units) {
+                float wv[V], bv[V], o[V];
+                pw.at(k, i, wv);
+                pb.at(k, i, bv);
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = (u[k].at(e) - mu) * rs * wv[e] + bv[e];
+                Unit<T, V>::store(y + r * width + i * V, o);
+            }
+        }
+        if (t == 0) {
+            if (mean) mean[r] = mu;
+            if (rstd) rstd[r] = rs;
+        }
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
         }
     }
 }
 
-// Partial sums of dw and db: block (i, j) takes 256 columns and every gridDim.y-th row.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512)
+    norm_bwd_wide_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
+                         const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
+                         float* __restrict__ part, int64_t rows, int width, int units, int pitch, int stages) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 buf[2][32];
+    const Rows m = rows_of(smem, (size_t)width * sizeof(T), rows, pitch, stages, 2);
+    const int t = threadIdx.x, nt = blockDim.x;
+    const float inv = 1.0f / (float)width;
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&m.full[i], 1);
+        fence_mbar_init();
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + (int64_t)i * gridDim.x < rows) m.issue(blockIdx.x + (int64_t)i * gridDim.x, i, x, dy);
+    }
+    __syncthreads();
+    float dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
+    Params<NV, V> pw;
+    pw.init(w, 1.0f, t, nt, units);
+    int stage = 0, turn = 0;
+    uint32_t phase = 0;
+    float mu_next = blockIdx.x < rows ? mean[blockIdx.x] : 0.0f, rs_next = blockIdx.x < rows ? rstd[blockIdx.x] : 0.0f;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const float mu = mu_next, rs = rs_next;
+        if (r + gridDim.x < rows) {
+            mu_next = mean[r + gridDim.x];
+            rs_next = rstd[r + gridDim.x];
+        }
+        const bool ok = mbar_wait(&m.full[stage], phase);
+        const T *rx = m.row<T>(r, stage, 0), *rg = m.row<T>(r, stage, 1);
+        Unit<T, V> ux[NV], ug[NV];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = t + nt * k;
+            if (i < units) {
+                float wv[V];
+                pw.at(k, i, wv);
+                take(ux[k], m, rx, x + r * width, r, i * V);
+                take(ug[k], m, rg, dy + r * width, r, i * V);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float g = ug[k].at(e), h = (ux[k].at(e) - mu) * rs, a = g * wv[e];
+                    s1 += a;
+                    s2 += a * h;
+                    dw[k][e] += g * h;
+                    db[k][e] += g;
+                }
+            }
+        }
+        const float2 s = block_sums(ok ? s1 : __int_as_float(0x7fffffff), s2, buf[turn]);
+        turn ^= 1;
+        s1 = s.x * inv;
+        s2 = s.y * inv;
+        const int64_t next = r + (int64_t)stages * gridDim.x;
+        if (t == 0 && next < rows) m.issue(next, stage, x, dy);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = t + nt * k;
+            if (i < units) {
+                float wv[V], o[V];
+                pw.at(k, i, wv);
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = rs * (ug[k].at(e) * wv[e] - s1 - (ux[k].at(e) - mu) * rs * s2);
+                Unit<T, V>::store(dx + r * width + i * V, o);
+            }
+        }
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = t + nt * k;
+        if (i < units)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                part[(size_t)blockIdx.x * 2 * width + i * V + e] = dw[k][e];
+                part[((size_t)blockIdx.x * 2 + 1) * width + i * V + e] = db[k][e];
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------- any width
+// One row for each block, read three times (from the cache after the first).
+__device__ __forceinline__ float block_sum(float x, float2* buf) {
+    const float s = block_sums(x, 0.0f, buf).x;
+    __syncthreads();
+    return s;
+}
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    layernorm_dw_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ mean,
-                        const float* __restrict__ rstd, float* __restrict__ part, int64_t rows, int width) {
+    norm_fwd_any_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
+                        float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, float eps) {
+    __shared__ float2 buf[32];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T* xr = x + r * width;
+        float s = 0.0f;
+        for (int c = threadIdx.x; c < width; c += kThreads) s += get(xr + c);
+        const float mu = block_sum(s, buf) / (float)width;
+        s = 0.0f;
+        for (int c = threadIdx.x; c < width; c += kThreads) {
+            const float d = get(xr + c) - mu;
+            s += d * d;
+        }
+        const float rs = rsqrtf(block_sum(s, buf) / (float)width + eps);
+        for (int c = threadIdx.x; c < width; c += kThreads)
+            put(y + r * width + c, (get(xr + c) - mu) * rs * (w ? w[c] : 1.0f) + (b ? b[c] : 0.0f));
+        if (threadIdx.x == 0) {
+            if (mean) mean[r] = mu;
+            if (rstd) rstd[r] = rs;
+        }
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    norm_dx_any_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
+                       const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx, int64_t rows,
+                       int width) {
+    __shared__ float2 buf[2][32];
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
+        const float mu = mean[r], rs = rstd[r];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int c = threadIdx.x; c < width; c += kThreads) {
+            const float a = get(dy + r * width + c) * (w ? w[c] : 1.0f);
+            s1 += a;
+            s2 += a * ((get(x + r * width + c) - mu) * rs);
+        }
+        const float2 s = block_sums(s1, s2, buf[turn]);
+        s1 = s.x / (float)width;
+        s2 = s.y / (float)width;
+        for (int c = threadIdx.x; c < width; c += kThreads) {
+            const float a = get(dy + r * width + c) * (w ? w[c] : 1.0f);
+            put(dx + r * width + c, rs * (a - s1 - (get(x + r * width + c) - mu) * rs * s2));
+        }
+    }
+}
+// block (i, j): 256 columns, every gridDim.y-th row
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    norm_dw_any_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ mean,
+                       const float* __restrict__ rstd, float* __restrict__ part, int64_t rows, int width) {
     const int c = blockIdx.x * kThreads + threadIdx.x;
     if (c >= width) return;
     float dw = 0.0f, db = 0.0f;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-        const float g = ld(dy, r * width + c);
-        dw += g * ((ld(x, r * width + c) - mean[r]) * rstd[r]);
+        const float g = get(dy + r * width + c);
+        dw += g * ((get(x + r * width + c) - mean[r]) * rstd[r]);
         db += g;
     }
     part[((size_t)blockIdx.y * 2) * width + c] = dw;
     part[((size_t)blockIdx.y * 2 + 1) * width + c] = db;
 }
 
-__global__ void __launch_bounds__(kThreads)
-    layernorm_reduce_kernel(const float* __restrict__ part, int n, int width, float* __restrict__ dw, float* __restrict__ db) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= width) return;
-    float a = 0.0f, b = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        a += part[((size_t)i * 2) * width + c];
-        b += part[((size_t)i * 2 + 1) * width + c];
+// dw and db from the n blocks' sums: 32 columns a block, 32 row groups that each add every 32nd partial,
+// then the groups in order.
+__global__ void __launch_bounds__(1024)
+    norm_reduce_kernel(const float* __restrict__ part, int n, int width, float* __restrict__ dw, float* __restrict__ db) {
+    __shared__ float s[32][33];
+    float* const out = blockIdx.y ? db : dw;
+    if (!out) return;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float a = 0.0f;
+    if (c < width)
+#pragma unroll 4
+        for (int i = threadIdx.y; i < n; i += 32) a += part[((size_t)i * 2 + blockIdx.y) * width + c];
+    s[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < width) {
+        a = 0.0f;
+        for (int i = 0; i < 32; ++i) a += s[i][threadIdx.x];
+        out[c] = a;
     }
-    if (dw) dw[c] = a;
-    if (db) db[c] = b;
 }
 
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -126,24 +594,173 @@ bool valid_size(long long rows, long long width) {
     return rows >= 0 && width >= 1 && width <= (1LL << 20) && rows <= (1LL << 40) / width;
 }
 
-unsigned part_rows(long long rows) { return (unsigned)(rows < kPartRows ? rows : kPartRows); }
-
-template <typename T>
-void fwd(long long rows, int width, float eps, const void* x, const float* w, const float* b, void* y, float* mean,
-         float* rstd, cudaStream_t s) {
-    const unsigned grid = (unsigned)(rows < (1LL << 30) ? rows : (1LL << 30));
-    layernorm_fwd_kernel<T><<<grid, kThreads, 0, s>>>(static_cast<const T*>(x), w, b, static_cast<T*>(y), mean, rstd, rows,
-                                                      width, eps);
+// Most blocks whose sums of dw and db are kept: eight on an SM, and no more than about 32 MB of sums.
+int most_parts(long long width) {
+    const long long n = (32LL << 20) / (8 * width);
+    return (int)(n < kSMs ? kSMs : n > 8 * kSMs ? 8 * kSMs : n);
 }
 
+// Which form a width takes, and its launch.
+struct Form {
+    int units, lpr, nv;      // lpr: lanes of a row (narrow), 0: wide or any
+    bool vec, wide;
+    int threads, pitch, stages, per_sm;
+    size_t smem;
+};
+Form form_of(long long width, size_t size, int inputs) {
+    Form f{};
+    const int v = (int)(16 / size);
+    f.vec = width % v == 0;
+    f.units = (int)(f.vec ? width / v : width);
+    if (f.vec ? f.units <= kNarrowUnits : width <= kNarrowColumns) {
+        f.lpr = 1;
+        while (f.lpr < f.units && f.lpr < 32) f.lpr *= 2;
+        const int need = (f.units + 31) / 32;
+        f.nv = 1;
+        while (f.nv < need) f.nv *= 2;
+        return f;
+    }
+    if (width > kWideMost) return f;
+    f.wide = true;
+    // as few units a thread as 256 threads (512 from two units on) allow
+    const int most[] = {1, 2, 3, 4, 8, 16, 32};
+    for (int nv : most) {
+        f.nv = nv;
+        if (f.units <= nv * (nv > 1 ? 512 : 256)) break;
+    }
+    f.threads = ((f.units + f.nv - 1) / f.nv + 31) / 32 * 32;
+    f.pitch = (int)((width * size + 31) / 16 * 16);
+    const int stage = f.pitch * inputs;
+    // threads on an SM: the parameters and the backward's sums take registers
+    const int columns = f.nv * (f.vec ? v : 1);
+    const int room = columns * (inputs + 1) >= 48 ? 512 : 1024;
+    f.per_sm = room / f.threads < 1 ? 1 : room / f.threads;
+    if (f.per_sm > 8) f.per_sm = 8;
+    // up to four rows ahead, within the SM's shared memory; fewer blocks rather than none ahead
+    for (;; --f.per_sm) {
+        f.stages = (int)(((size_t)216 * 1024 / f.per_sm - 1024 - 64) / stage);
+        if (f.stages >= 3 || f.per_sm == 1) break;
+    }
+    if (f.stages > 4) f.stages = 4;
+    if (f.stages < 1) f.stages = 1;
+    f.smem = 64 + (size_t)stage * f.stages;
+    return f;
+}
+
+unsigned blocks(long long rows, long long most) { return (unsigned)(rows < most ? rows : most); }
+
+template <typename T, int V, int NV>
+kda_status fwd_wide(const Form& f, long long rows, int width, float eps, const T* x, const float* w, const float* b, T* y,
+                    float* mean, float* rstd, cudaStream_t s) {
+    auto k = norm_fwd_wide_kernel<T, V, NV>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_fwd");
+    k<<<blocks(rows, (long long)kSMs * f.per_sm), f.threads, f.smem, s>>>(x, w, b, y, mean, rstd, rows, width, f.units, f.pitch,
+                                                                       f.stages, eps);
+    return launched("kda_layernorm_fwd launch");
+}
+template <typename T, int V, int NV>
+kda_status fwd_narrow(const Form& f, long long rows, int width, float eps, const T* x, const float* w, const float* b, T* y,
+                      float* mean, float* rstd, cudaStream_t s) {
+    const long long rpb = (long long)(kThreads / 32) * (32 / f.lpr);
+    norm_fwd_narrow_kernel<T, V, NV><<<blocks((rows + rpb - 1) / rpb, 8LL * kSMs), kThreads, 0, s>>>(x, w, b, y, mean, rstd, rows,
+                                                                                                     width, f.units, f.lpr, eps);
+    return launched("kda_layernorm_fwd launch");
+}
 template <typename T>
-void bwd(long long rows, int width, const void* x, const void* dy, const float* w, const float* mean, const float* rstd,
-         void* dx, float* part, cudaStream_t s) {
-    const unsigned grid = (unsigned)(rows < (1LL << 30) ? rows : (1LL << 30));
-    layernorm_dx_kernel<T><<<grid, kThreads, 0, s>>>(static_cast<const T*>(x), static_cast<const T*>(dy), w, mean, rstd,
-                                                     static_cast<T*>(dx), rows, width);
-    layernorm_dw_kernel<T><<<dim3((unsigned)((width + kThreads - 1) / kThreads), part_rows(rows)), kThreads, 0, s>>>(
-        static_cast<const T*>(x), static_cast<const T*>(dy), mean, rstd, part, rows, width);
+kda_status fwd(long long rows, int width, float eps, const void* xv, const float* w, const float* b, void* yv, float* mean,
+               float* rstd, cudaStream_t s) {
+    const T* x = static_cast<const T*>(xv);
+    T* y = static_cast<T*>(yv);
+    constexpr int V = 16 / sizeof(T);
+    const Form f = form_of(width, sizeof(T), 1);
+#define KDA_NORM(fn, v, n) return fn<T, v, n>(f, rows, width, eps, x, w, b, y, mean, rstd, s)
+    if (f.lpr && f.vec) {
+        if (f.nv == 1) KDA_NORM(fwd_narrow, V, 1);
+        KDA_NORM(fwd_narrow, V, 2);
+    }
+    if (f.lpr) {
+        if (f.nv <= 2) KDA_NORM(fwd_narrow, 1, 2);
+        if (f.nv <= 4) KDA_NORM(fwd_narrow, 1, 4);
+        if (f.nv <= 8) KDA_NORM(fwd_narrow, 1, 8);
+        KDA_NORM(fwd_narrow, 1, 16);
+    }
+    if (f.wide && f.vec) {
+        if (f.nv == 1) KDA_NORM(fwd_wide, V, 1);
+        if (f.nv == 2) KDA_NORM(fwd_wide, V, 2);
+        if (f.nv == 3) KDA_NORM(fwd_wide, V, 3);
+        if (f.nv == 4) KDA_NORM(fwd_wide, V, 4);
+        if constexpr (V == 4) KDA_NORM(fwd_wide, V, 8);
+    }
+    if (f.wide) {
+        if (f.nv <= 4) KDA_NORM(fwd_wide, 1, 4);
+        if (f.nv <= 8) KDA_NORM(fwd_wide, 1, 8);
+        if (f.nv <= 16) KDA_NORM(fwd_wide, 1, 16);
+        KDA_NORM(fwd_wide, 1, 32);
+    }
+#undef KDA_NORM
+    norm_fwd_any_kernel<T><<<blocks(rows, 1 << 30), kThreads, 0, s>>>(x, w, b, y, mean, rstd, rows, width, eps);
+    return launched("kda_layernorm_fwd launch");
+}
+
+template <typename T, int V, int NV>
+kda_status bwd_wide(const Form& f, long long rows, int width, const T* x, const T* dy, const float* w, const float* mean,
+                    const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
+    auto k = norm_bwd_wide_kernel<T, V, NV>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_bwd");
+    const long long most = (long long)kSMs * f.per_sm;
+    *parts = (int)blocks(rows, most < most_parts(width) ? most : most_parts(width));
+    k<<<*parts, f.threads, f.smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.units, f.pitch, f.stages);
+    return launched("kda_layernorm_bwd launch");
+}
+template <typename T, int V, int NV>
+kda_status bwd_narrow(const Form& f, long long rows, int width, const T* x, const T* dy, const float* w, const float* mean,
+                      const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
+    constexpr int R = V * NV <= 8 ? 2 : 1;
+    const long long rpb = (long long)(kThreads / 32) * (32 / f.lpr);
+    *parts = (int)blocks((rows + rpb - 1) / rpb, most_parts(width));
+    norm_bwd_narrow_kernel<T, V, NV, R><<<*parts, kThreads, (size_t)(kThreads / 32) * 2 * width * sizeof(float), s>>>(
+        x, dy, w, mean, rstd, dx, part, rows, width, f.units, f.lpr);
+    return launched("kda_layernorm_bwd launch");
+}
+// dx and, to part where it is given, the sums of `parts` blocks
+template <typename T>
+kda_status bwd(long long rows, int width, const void* xv, const void* dyv, const float* w, const float* mean, const float* rstd,
+               void* dxv, float* part, int* parts, cudaStream_t s) {
+    const T *x = static_cast<const T*>(xv), *dy = static_cast<const T*>(dyv);
+    T* dx = static_cast<T*>(dxv);
+    constexpr int V = 16 / sizeof(T);
+    const Form f = form_of(width, sizeof(T), 2);
+#define KDA_NORM(fn, v, n) return fn<T, v, n>(f, rows, width, x, dy, w, mean, rstd, dx, part, parts, s)
+    if (f.lpr && f.vec) {
+        if (f.nv == 1) KDA_NORM(bwd_narrow, V, 1);
+        KDA_NORM(bwd_narrow, V, 2);
+    }
+    if (f.lpr) {
+        if (f.nv <= 2) KDA_NORM(bwd_narrow, 1, 2);
+        if (f.nv <= 4) KDA_NORM(bwd_narrow, 1, 4);
+        if (f.nv <= 8) KDA_NORM(bwd_narrow, 1, 8);
+        KDA_NORM(bwd_narrow, 1, 16);
+    }
+    if (f.wide && f.vec) {
+        if (f.nv == 1) KDA_NORM(bwd_wide, V, 1);
+        if (f.nv == 2) KDA_NORM(bwd_wide, V, 2);
+        if (f.nv == 3) KDA_NORM(bwd_wide, V, 3);
+        if (f.nv == 4) KDA_NORM(bwd_wide, V, 4);
+        if constexpr (V == 4) KDA_NORM(bwd_wide, V, 8);
+    }
+    if (f.wide) {
+        if (f.nv <= 4) KDA_NORM(bwd_wide, 1, 4);
+        if (f.nv <= 8) KDA_NORM(bwd_wide, 1, 8);
+        if (f.nv <= 16) KDA_NORM(bwd_wide, 1, 16);
+        KDA_NORM(bwd_wide, 1, 32);
+    }
+#undef KDA_NORM
+    norm_dx_any_kernel<T><<<blocks(rows, 1 << 30), kThreads, 0, s>>>(x, dy, w, mean, rstd, dx, rows, width);
+    *parts = (int)blocks(rows, kSMs);
+    if (part)
+        norm_dw_any_kernel<T><<<dim3((unsigned)((width + kThreads - 1) / kThreads), (unsigned)*parts), kThreads, 0, s>>>(
+            x, dy, mean, rstd, part, rows, width);
+    return launched("kda_layernorm_bwd launch");
 }
 
 }  // namespace
@@ -163,14 +780,13 @@ extern "C" kda_status kda_layernorm_fwd(long long rows, long long width, int dty
     for (const void* p : ptrs)
         if (misaligned(p)) return KDA_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == KDA_BF16) fwd<uint16_t>(rows, (int)width, eps, x, weight, bias, y, mean, rstd, s);
-    else fwd<float>(rows, (int)width, eps, x, weight, bias, y, mean, rstd, s);
-    return launched("kda_layernorm_fwd launch");
+    return dtype == KDA_BF16 ? fwd<uint16_t>(rows, (int)width, eps, x, weight, bias, y, mean, rstd, s)
+                             : fwd<float>(rows, (int)width, eps, x, weight, bias, y, mean, rstd, s);
 }
 
 extern "C" size_t kda_layernorm_workspace_size(long long rows, long long width) {
     if (!valid_size(rows, width)) return 0;
-    return align_up((size_t)kPartRows * 2 * (size_t)width * sizeof(float), 1024);
+    return align_up((size_t)most_parts(width) * 2 * (size_t)width * sizeof(float), 1024);
 }
 
 extern "C" kda_status kda_layernorm_bwd(long long rows, long long width, int dtype, const void* x, const void* dy,
@@ -185,13 +801,17 @@ extern "C" kda_status kda_layernorm_bwd(long long rows, long long width, int dty
     for (const void* p : ptrs)
         if (misaligned(p)) return KDA_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    float* part = static_cast<float*>(workspace);
+    const bool sums = dweight || dbias;
+    float* part = sums ? static_cast<float*>(workspace) : nullptr;
+    int parts = 0;
     if (rows > 0) {
-        if (dtype == KDA_BF16) bwd<uint16_t>(rows, (int)width, x, dy, weight, mean, rstd, dx, part, s);
-        else bwd<float>(rows, (int)width, x, dy, weight, mean, rstd, dx, part, s);
+        const kda_status st = dtype == KDA_BF16
+                                  ? bwd<uint16_t>(rows, (int)width, x, dy, weight, mean, rstd, dx, part, &parts, s)
+                                  : bwd<float>(rows, (int)width, x, dy, weight, mean, rstd, dx, part, &parts, s);
+        if (st != KDA_OK) return st;
     }
-    if (dweight || dbias)
-        layernorm_reduce_kernel<<<(unsigned)((width + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-            part, (int)part_rows(rows), (int)width, dweight, dbias);
+    if (sums)
+        norm_reduce_kernel<<<dim3((unsigned)((width + 31) / 32), 2), dim3(32, 32), 0, s>>>(static_cast<const float*>(workspace),
+                                                                                          parts, (int)width, dweight, dbias);
     return launched("kda_layernorm_bwd launch");
 }

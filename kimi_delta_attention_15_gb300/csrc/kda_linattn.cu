@@ -990,11 +990,13 @@ Plan plan_of(const kda_linattn_shape* sh, bool packed, int jobs) {
 }
 
 struct LinLayout {
+    Plan plan;
     size_t table, seg[2], share_q, share_k, total;
 };
 LinLayout layout_of(const kda_linattn_shape* sh, bool packed, bool backward) {
     const Plan p = plan_of(sh, packed, backward ? 3 : 1);
     LinLayout l;
+    l.plan = p;
     size_t o = 1024;   // the status word, at byte 64 the number of slots
     l.table = o; o += packed ? align_up((size_t)p.slots * sizeof(Slot), 1024) : 0;
     const size_t states = p.nseg > 1 ? (size_t)p.slots * sh->H * D * D * sizeof(float) : 0;
@@ -1007,10 +1009,12 @@ LinLayout layout_of(const kda_linattn_shape* sh, bool packed, bool backward) {
     return l;
 }
 
-kda_status common_checks(const kda_linattn_shape* sh, const int64_t* cu, const void* ws, size_t bytes, bool backward) {
+kda_status common_checks(const kda_linattn_shape* sh, const int64_t* cu, const void* ws, size_t bytes, bool backward,
+                         LinLayout* lay) {
     const kda_status st = check_shape(sh, cu != nullptr);
     if (st != KDA_OK) return st;
-    if (!ws || bytes < layout_of(sh, cu != nullptr, backward).total) return KDA_ERR_WORKSPACE;
+    *lay = layout_of(sh, cu != nullptr, backward);
+    if (!ws || bytes < lay->total) return KDA_ERR_WORKSPACE;
     if (misaligned(ws) || (reinterpret_cast<uintptr_t>(cu) & 7u)) return KDA_ERR_ALIGN;
     return KDA_OK;
 }
@@ -1049,7 +1053,7 @@ kda_status make_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t hea
 // transposed for job 1, of job 2 (the backward's two reversed jobs sum the same state).
 kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (&tensors)[4], int jobs, const int64_t* cu, const float* log_decay, uint8_t* ws,
                     const LinLayout& lay, cudaStream_t s) {
-    const Plan p = plan_of(sh, cu != nullptr, jobs);
+    const Plan p = lay.plan;
     const cudaError_t e = cudaFuncSetAttribute(linattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
     if (e != cudaSuccess) {
         set_last_error_text(cudaGetErrorString(e));
@@ -1113,11 +1117,11 @@ extern "C" size_t kda_linattn_workspace_size(const kda_linattn_shape* shape, int
     size_t most = 0;
     for (int packed = 0; packed < 2; ++packed)
         if (check_shape(shape, packed != 0) == KDA_OK) {
-            const size_t b = layout_of(shape, packed != 0, backward != 0).total;
+            const LinLayout l = layout_of(shape, packed != 0, backward != 0);
+            // the backward's workspace serves the forward too, beside the grouped gradients' shares
+            const size_t share = l.total - l.share_q, f = layout_of(shape, packed != 0, false).total;
+            const size_t b = (l.share_q > f ? l.share_q : f) + share;
             if (b > most) most = b;
-            // the backward's workspace serves the forward too
-            const size_t f = backward ? layout_of(shape, packed != 0, false).total : 0;
-            if (f > most) most = f;
         }
     return most;
 }
@@ -1126,7 +1130,8 @@ extern "C" kda_status kda_linattn_fwd(const kda_linattn_shape* shape, const kda_
                                       const kda_bf16* v, const float* log_decay, const float* h0,
                                       const int64_t* cu_seqlens, kda_bf16* o, float* hT, void* workspace,
                                       size_t workspace_bytes, void* stream) {
-    const kda_status st = common_checks(shape, cu_seqlens, workspace, workspace_bytes, false);
+    LinLayout lay;
+    const kda_status st = common_checks(shape, cu_seqlens, workspace, workspace_bytes, false, &lay);
     if (st != KDA_OK) return st;
     if ((shape->B * shape->T > 0 && (!q || !k || !v || !o)) || !log_decay) return KDA_ERR_NULL;
     const void* ptrs[] = {q, k, v, log_decay, h0, o, hT};
@@ -1136,7 +1141,7 @@ extern "C" kda_status kda_linattn_fwd(const kda_linattn_shape* shape, const kda_
     LinArgs a{{}, {}, {G, G, 1, 1}};
     a.job[0] = LinJob{0, 1, 2, o, nullptr, h0, hT, nullptr, 0, 0, 0, hT != nullptr, 1.0f};
     const kda_status rs = run_jobs(shape, a, {q, k, v, nullptr}, 1, cu_seqlens, log_decay, static_cast<uint8_t*>(workspace),
-                                   layout_of(shape, cu_seqlens != nullptr, false), static_cast<cudaStream_t>(stream));
+                                   lay, static_cast<cudaStream_t>(stream));
     return rs != KDA_OK ? rs : launched("kda_linattn_fwd launch");
 }
 
@@ -1145,7 +1150,8 @@ extern "C" kda_status kda_linattn_bwd(const kda_linattn_shape* shape, const kda_
                                       const int64_t* cu_seqlens, const kda_bf16* do_, const float* dhT, kda_bf16* dq,
                                       kda_bf16* dk, kda_bf16* dv, float* dh0, void* workspace, size_t workspace_bytes,
                                       void* stream) {
-    const kda_status st = common_checks(shape, cu_seqlens, workspace, workspace_bytes, true);
+    LinLayout lay;
+    const kda_status st = common_checks(shape, cu_seqlens, workspace, workspace_bytes, true, &lay);
     if (st != KDA_OK) return st;
     const int64_t tokens = shape->B * shape->T;
     if ((tokens > 0 && (!q || !k || !v || !do_ || !dq || !dk || !dv)) || !log_decay) return KDA_ERR_NULL;
@@ -1155,7 +1161,6 @@ extern "C" kda_status kda_linattn_bwd(const kda_linattn_shape* shape, const kda_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int G = groups_of(shape);
-    const LinLayout lay = layout_of(shape, cu_seqlens != nullptr, true);
     float* const share_q = G > 1 ? reinterpret_cast<float*>(ws + lay.share_q) : nullptr;
     float* const share_k = G > 1 ? reinterpret_cast<float*>(ws + lay.share_k) : nullptr;
     const float sc = shape->scale;

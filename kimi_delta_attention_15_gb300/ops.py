@@ -304,26 +304,56 @@ def linattn_shape(T: int, H: int, N: int, B: int = 1, scale: float = SCALE, grou
     return LinattnShape(B=B, T=T, H=H, N=N, K=128, V=128, scale=scale, groups=groups)
 
 
+def _ready(specs):
+    """_validate for calls whose latency counts: the same checks on (name, tensor, count, dtype,
+    optional) specs, in as few operations as a valid call needs; _validate words the refusals.
+    Returns the tensors' device."""
+    dev = -1
+    for _, t, numel, dtype, optional in specs:
+        if t is None:
+            if optional:
+                continue
+        elif t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+            d = t.get_device()
+            if d == dev:
+                continue
+            if dev < 0 <= d:
+                dev = d
+                continue
+        _validate(specs)
+        raise ValueError(f"every tensor must be on one CUDA device (cuda:{dev})")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _linattn_shape_of(q, v, cu_seqlens, B, scale):
-    sh = _shape_of(q, v, cu_seqlens, B, scale, LOWER_BOUND)
-    return linattn_shape(sh.T, sh.H, sh.N, sh.B, scale, sh.groups)
+    """Shape from the token tensors: H = value heads (v); q, k may hold H / groups heads."""
+    H, Hqk = v.shape[-2], q.shape[-2]
+    if Hqk <= 0 or H % Hqk != 0:
+        raise ValueError(f"value heads ({H}) must be a multiple of query/key heads ({Hqk})")
+    if cu_seqlens is not None:
+        return LinattnShape(1, q.shape[0], H, cu_seqlens.numel() - 1, 128, 128, scale, H // Hqk)
+    if q.dim() == 4:
+        return LinattnShape(q.shape[0], q.shape[1], H, q.shape[0], 128, 128, scale, H // Hqk)
+    return LinattnShape(B, q.shape[0] // B, H, B, 128, 128, scale, H // Hqk)
 
 
 def linattn_workspace_size(shape: LinattnShape, backward: bool = False) -> int:
-    return int(load().kda_linattn_workspace_size(ctypes.byref(shape), int(backward)))
+    return int((_lib or load()).kda_linattn_workspace_size(ctypes.byref(shape), int(backward)))
 
 
 def linattn_alloc_workspace(shape: LinattnShape, device, backward: bool = False) -> torch.Tensor:
     return torch.empty(linattn_workspace_size(shape, backward), dtype=torch.uint8, device=device)
 
 
-def _linattn_specs(shape, q, k, v, log_decay, h0, cu_seqlens):
-    tok, H, N = shape.B * shape.T, shape.H, shape.N
-    Hqk = H // max(int(shape.groups), 1)
-    bf, f32 = torch.bfloat16, torch.float32
-    return [("q", q, tok * Hqk * 128, bf, False), ("k", k, tok * Hqk * 128, bf, False),
-            ("v", v, tok * H * 128, bf, False), ("log_decay", log_decay, H, f32, False),
-            ("h0", h0, N * H * 128 * 128, f32, True), ("cu_seqlens", cu_seqlens, N + 1, torch.int64, True)]
+_BF, _F32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.uint8
 
 
 def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, B: int = 1, scale: float = SCALE, workspace=None,
@@ -331,22 +361,26 @@ def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, B: int = 1, sca
     """kda_linattn_fwd: S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t. Token tensors
     [T, H, 128] bf16 (or [B, T, H, 128]; q, k may hold H / groups heads); log_decay [H] fp32.
     Returns (o, hT, workspace)."""
-    lib = load()
+    lib = _lib or load()
     shape = _linattn_shape_of(q, v, cu_seqlens, B, scale)
+    H, N = shape.H, shape.N
+    tok = shape.B * shape.T * 128
+    qk, state = tok * (H // shape.groups), N * H * 16384
     if workspace is None:
         workspace = linattn_alloc_workspace(shape, q.device)
     if o is None:
         o = torch.empty_like(v)
     if hT is None and want_hT:
-        hT = torch.empty(shape.N, shape.H, 128, 128, dtype=torch.float32, device=q.device)
-    _validate(_linattn_specs(shape, q, k, v, log_decay, h0, cu_seqlens)
-              + [("o", o, v.numel(), torch.bfloat16, False),
-                 ("hT", hT, shape.N * shape.H * 128 * 128, torch.float32, True),
-                 ("workspace", workspace, None, torch.uint8, False)])
-    code = lib.kda_linattn_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
-                               _ptr(cu_seqlens), _ptr(o), _ptr(hT), _ptr(workspace), workspace.numel(),
-                               _stream_handle(stream))
-    _check(code, "kda_linattn_fwd")
+        hT = torch.empty((N, H, 128, 128), dtype=_F32, device=q.device)
+    dev = _ready((("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, tok * H, _BF, False),
+                  ("log_decay", log_decay, H, _F32, False), ("h0", h0, state, _F32, True),
+                  ("cu_seqlens", cu_seqlens, N + 1, _I64, True), ("o", o, tok * H, _BF, False), ("hT", hT, state, _F32, True),
+                  ("workspace", workspace, workspace.numel(), _U8, False)))
+    code = lib.kda_linattn_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                               _address(h0), _address(cu_seqlens), o.data_ptr(), _address(hT), workspace.data_ptr(),
+                               workspace.numel(), _raw_stream(stream, dev))
+    if code:
+        _check(code, "kda_linattn_fwd")
     return o, hT, workspace
 
 
@@ -355,44 +389,47 @@ def linattn_bwd(q, k, v, log_decay, do, workspace=None, h0=None, cu_seqlens=None
     """kda_linattn_bwd: gradients of sum <o, do> + <hT, dhT>. It recomputes what it needs, so any
     workspace of linattn_alloc_workspace(shape, device, backward=True) serves; pass one to read
     device_status(workspace) afterwards. Returns a dict of dq, dk, dv and dh0."""
-    lib = load()
+    lib = _lib or load()
     shape = _linattn_shape_of(q, v, cu_seqlens, B, scale)
+    H, N = shape.H, shape.N
+    tok = shape.B * shape.T * 128
+    qk, state = tok * (H // shape.groups), N * H * 16384
     if workspace is None:
         workspace = linattn_alloc_workspace(shape, q.device, backward=True)
-    state = shape.N * shape.H * 128 * 128
-    bf, f32 = torch.bfloat16, torch.float32
     if grads is None:
         grads = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-                     dh0=torch.empty(shape.N, shape.H, 128, 128, dtype=f32, device=q.device) if want_dh0 else None)
-    _validate(_linattn_specs(shape, q, k, v, log_decay, h0, cu_seqlens)
-              + [("do", do, v.numel(), bf, False), ("dhT", dhT, state, f32, True),
-                 ("dq", grads.get("dq"), q.numel(), bf, False), ("dk", grads.get("dk"), q.numel(), bf, False),
-                 ("dv", grads.get("dv"), v.numel(), bf, False), ("dh0", grads.get("dh0"), state, f32, True),
-                 ("workspace", workspace, None, torch.uint8, False)])
-    code = lib.kda_linattn_bwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
-                               _ptr(cu_seqlens), _ptr(do), _ptr(dhT), _ptr(grads["dq"]), _ptr(grads["dk"]),
-                               _ptr(grads["dv"]), _ptr(grads.get("dh0")), _ptr(workspace), workspace.numel(),
-                               _stream_handle(stream))
-    _check(code, "kda_linattn_bwd")
+                     dh0=torch.empty((N, H, 128, 128), dtype=_F32, device=q.device) if want_dh0 else None)
+    dq, dk, dv, dh0 = grads.get("dq"), grads.get("dk"), grads.get("dv"), grads.get("dh0")
+    dev = _ready((("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, tok * H, _BF, False),
+                  ("log_decay", log_decay, H, _F32, False), ("h0", h0, state, _F32, True),
+                  ("cu_seqlens", cu_seqlens, N + 1, _I64, True), ("do", do, tok * H, _BF, False),
+                  ("dhT", dhT, state, _F32, True), ("dq", dq, qk, _BF, False), ("dk", dk, qk, _BF, False),
+                  ("dv", dv, tok * H, _BF, False), ("dh0", dh0, state, _F32, True),
+                  ("workspace", workspace, workspace.numel(), _U8, False)))
+    code = lib.kda_linattn_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                               _address(h0), _address(cu_seqlens), do.data_ptr(), _address(dhT), dq.data_ptr(), dk.data_ptr(),
+                               dv.data_ptr(), _address(dh0), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if code:
+        _check(code, "kda_linattn_bwd")
     return grads
 
 
 def linattn_decode(q, k, v, log_decay, state, *, o=None, scale: float = SCALE, stream=None):
     """kda_linattn_decode: one token per request. v [n_req, H, 128] bf16, q, k [n_req, H / groups, 128]
     bf16; `state` [n_req, H, 128, 128] fp32 is updated in place. Returns o [n_req, H, 128] bf16."""
-    n_req, H, Hqk = int(v.shape[0]), int(v.shape[1]), int(q.shape[1])
+    n_req, H, Hqk = v.shape[0], v.shape[1], q.shape[1]
     if Hqk <= 0 or H % Hqk != 0:
         raise ValueError(f"value heads ({H}) must be a multiple of query/key heads ({Hqk})")
     if o is None:
         o = torch.empty_like(v)
-    lib = load()
-    bf, f32 = torch.bfloat16, torch.float32
-    _validate([("q", q, n_req * Hqk * 128, bf, False), ("k", k, n_req * Hqk * 128, bf, False),
-               ("v", v, n_req * H * 128, bf, False), ("log_decay", log_decay, H, f32, False),
-               ("state", state, n_req * H * 128 * 128, f32, False), ("o", o, n_req * H * 128, bf, False)])
-    code = lib.kda_linattn_decode(n_req, H, H // Hqk, scale, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
-                                  _ptr(o), _stream_handle(stream))
-    _check(code, "kda_linattn_decode")
+    lib = _lib or load()
+    qk, n = n_req * Hqk * 128, n_req * H * 128
+    dev = _ready((("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, n, _BF, False),
+                  ("log_decay", log_decay, H, _F32, False), ("state", state, n * 128, _F32, False), ("o", o, n, _BF, False)))
+    code = lib.kda_linattn_decode(n_req, H, H // Hqk, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                  state.data_ptr(), o.data_ptr(), _raw_stream(stream, dev))
+    if code:
+        _check(code, "kda_linattn_decode")
     return o
 
 
@@ -404,27 +441,27 @@ def _norm_size(x):
         raise ValueError(f"x: dtype {x.dtype}, expected bfloat16 or float32")
     if x.dim() < 1 or x.shape[-1] == 0:
         raise ValueError(f"x: shape {tuple(x.shape)} has no row to normalise")
-    width = int(x.shape[-1])
-    return x.numel() // width, width
+    n, width = x.numel(), x.shape[-1]
+    return n, n // width, width
 
 
 def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, mean=None, rstd=None, stream=None):
     """kda_layernorm_fwd over the last dimension. x bf16 or fp32, weight and bias [width] fp32 or
     None. Returns (y, mean, rstd); mean and rstd [rows] fp32 are what layernorm_bwd reads."""
-    rows, width = _norm_size(x)
-    f32 = torch.float32
+    n, rows, width = _norm_size(x)
     if y is None:
         y = torch.empty_like(x)
     if mean is None:
-        mean = torch.empty(rows, dtype=f32, device=x.device)
+        mean = torch.empty(rows, dtype=_F32, device=x.device)
     if rstd is None:
-        rstd = torch.empty(rows, dtype=f32, device=x.device)
-    lib = load()
-    _validate([("x", x, None, None, False), ("weight", weight, width, f32, True), ("bias", bias, width, f32, True),
-               ("y", y, x.numel(), x.dtype, False), ("mean", mean, rows, f32, False), ("rstd", rstd, rows, f32, False)])
-    code = lib.kda_layernorm_fwd(rows, width, _NORM_DTYPES[x.dtype], eps, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                 _ptr(mean), _ptr(rstd), _stream_handle(stream))
-    _check(code, "kda_layernorm_fwd")
+        rstd = torch.empty(rows, dtype=_F32, device=x.device)
+    lib = _lib or load()
+    dev = _ready((("x", x, n, x.dtype, False), ("weight", weight, width, _F32, True), ("bias", bias, width, _F32, True),
+                  ("y", y, n, x.dtype, False), ("mean", mean, rows, _F32, False), ("rstd", rstd, rows, _F32, False)))
+    code = lib.kda_layernorm_fwd(rows, width, _NORM_DTYPES[x.dtype], eps, x.data_ptr(), _address(weight), _address(bias),
+                                 y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev))
+    if code:
+        _check(code, "kda_layernorm_fwd")
     return y, mean, rstd
 
 
@@ -432,23 +469,23 @@ def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool =
                   workspace=None, stream=None):
     """kda_layernorm_bwd with the mean and rstd of layernorm_fwd (weight None reads as 1). Returns a
     dict of dx (dtype of x), dweight and dbias ([width] fp32)."""
-    rows, width = _norm_size(x)
-    f32 = torch.float32
-    lib = load()
+    n, rows, width = _norm_size(x)
+    lib = _lib or load()
     if workspace is None:
-        workspace = torch.empty(int(lib.kda_layernorm_workspace_size(rows, width)), dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(lib.kda_layernorm_workspace_size(rows, width), dtype=_U8, device=x.device)
     if grads is None:
-        grads = dict(dx=torch.empty_like(x),
-                     dweight=torch.empty(width, dtype=f32, device=x.device) if want_dweight else None,
-                     dbias=torch.empty(width, dtype=f32, device=x.device) if want_dbias else None)
-    _validate([("x", x, None, None, False), ("dy", dy, x.numel(), x.dtype, False), ("weight", weight, width, f32, True),
-               ("mean", mean, rows, f32, False), ("rstd", rstd, rows, f32, False),
-               ("dx", grads.get("dx"), x.numel(), x.dtype, False), ("dweight", grads.get("dweight"), width, f32, True),
-               ("dbias", grads.get("dbias"), width, f32, True), ("workspace", workspace, None, torch.uint8, False)])
-    code = lib.kda_layernorm_bwd(rows, width, _NORM_DTYPES[x.dtype], _ptr(x), _ptr(dy), _ptr(weight), _ptr(mean),
-                                 _ptr(rstd), _ptr(grads["dx"]), _ptr(grads.get("dweight")), _ptr(grads.get("dbias")),
-                                 _ptr(workspace), workspace.numel(), _stream_handle(stream))
-    _check(code, "kda_layernorm_bwd")
+        grads = dict(dx=torch.empty_like(x), dweight=torch.empty(width, dtype=_F32, device=x.device) if want_dweight else None,
+                     dbias=torch.empty(width, dtype=_F32, device=x.device) if want_dbias else None)
+    dx, dweight, dbias = grads.get("dx"), grads.get("dweight"), grads.get("dbias")
+    dev = _ready((("x", x, n, x.dtype, False), ("dy", dy, n, x.dtype, False), ("weight", weight, width, _F32, True),
+                  ("mean", mean, rows, _F32, False), ("rstd", rstd, rows, _F32, False), ("dx", dx, n, x.dtype, False),
+                  ("dweight", dweight, width, _F32, True), ("dbias", dbias, width, _F32, True),
+                  ("workspace", workspace, workspace.numel(), _U8, False)))
+    code = lib.kda_layernorm_bwd(rows, width, _NORM_DTYPES[x.dtype], x.data_ptr(), dy.data_ptr(), _address(weight),
+                                 mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _address(dweight), _address(dbias),
+                                 workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if code:
+        _check(code, "kda_layernorm_bwd")
     return grads
 
 
