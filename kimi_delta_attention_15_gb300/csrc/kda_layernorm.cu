@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename T, int V, int NV, int R>   // R: row groups in flight
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, V * NV <= 8 ? 4 : 2)
     norm_bwd_narrow_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                            const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                            float* __restrict__ part, int64_t rows, int width, int units, int lpr) {
@@ -265,114 +265,157 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------------------------ wide
-// sums over the block, the same values in every thread; buf: 2 x 32 pairs used in turn, one barrier
-__device__ __forceinline__ float2 block_sums(float a, float b, float2* buf) {
+__device__ __forceinline__ float2 warp_sums(float a, float b) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
         b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
+    return make_float2(a, b);
+}
+// the sum of the block's warps' pairs, four at a time; what lies past them in the 32 does not count
+__device__ __forceinline__ float2 sum_of(const float2 (&buf)[32]) {
     float2 s = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) {
-        const float2 p = buf[i];
-        s.x += p.x;
-        s.y += p.y;
+    const int n = blockDim.x >> 5;
+    for (int i = 0; i < n; i += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(&buf[i]), q = *reinterpret_cast<const float4*>(&buf[i + 2]);
+        s.x += (p.x + (i + 1 < n ? p.z : 0.0f)) + ((i + 2 < n ? q.x : 0.0f) + (i + 3 < n ? q.z : 0.0f));
+        s.y += (p.y + (i + 1 < n ? p.w : 0.0f)) + ((i + 2 < n ? q.y : 0.0f) + (i + 3 < n ? q.w : 0.0f));
     }
     return s;
 }
+// sums over the block, the same values in every thread, with one barrier (the caller uses two buffers in turn)
+__device__ __forceinline__ float2 block_sums(float a, float b, float2 (&buf)[32]) {
+    const float2 p = warp_sums(a, b);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = p;
+    __syncthreads();
+    return sum_of(buf);
+}
+// rows at a time of the backward, by a thread's columns (single elements take a register each)
+__host__ __device__ constexpr int bwd_rows(int columns, bool vec) { return columns <= (vec ? 16 : 8) ? 2 : 1; }
 
-// Rows on their way to shared memory: the aligned span of row r of each input, `stages` rows ahead.
-// The last bytes of a tensor whose size is no multiple of 16 are not copied: read them with tail().
+// Rows on their way to shared memory: a step of R rows (r, r + stride, ..) of each input, `stages` steps
+// ahead, of each row the aligned span around it. The last bytes of a tensor whose size is no multiple of
+// 16 are not copied: take() reads them from global memory.
+template <int R>
 struct Rows {
-    uint8_t* at;             // [stages][inputs][pitch]
+    uint8_t* at;             // [stages][inputs][R][pitch]
     uint64_t* full;          // [stages]
     size_t row_bytes, most;  // most: the tensor's size rounded down to 16 bytes
-    int pitch, stages, inputs;
-    __device__ __forceinline__ void issue(int64_t r, int stage, const void* a, const void* b) const {
-        const size_t p = (size_t)r * row_bytes, from = p & ~(size_t)15;
-        size_t to = (p + row_bytes + 15) & ~(size_t)15;
-        if (to > most) to = most;
-        const uint32_t n = to > from ? (uint32_t)(to - from) : 0u;
-        mbar_arrive_expect_tx(&full[stage], n * (uint32_t)inputs);
-        if (n == 0) return;
-        bulk_g2s(at + (size_t)stage * inputs * pitch, static_cast<const uint8_t*>(a) + from, n, &full[stage]);
-        if (inputs > 1) bulk_g2s(at + ((size_t)stage * inputs + 1) * pitch, static_cast<const uint8_t*>(b) + from, n, &full[stage]);
+    int64_t rows, stride;
+    int pitch, inputs;
+    __device__ __forceinline__ void issue(int64_t r0, int stage, const void* a, const void* b) const {
+        uint32_t n[R], sum = 0;
+        size_t from[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = r0 + q * stride;
+            const size_t p = (size_t)r * row_bytes;
+            size_t to = (p + row_bytes + 15) & ~(size_t)15;
+            from[q] = p & ~(size_t)15;
+            if (to > most) to = most;
+            n[q] = r < rows && to > from[q] ? (uint32_t)(to - from[q]) : 0u;
+            sum += n[q];
+        }
+        mbar_arrive_expect_tx(&full[stage], sum * (uint32_t)inputs);
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (n[q]) {
+                bulk_g2s(slot(stage, 0, q), static_cast<const uint8_t*>(a) + from[q], n[q], &full[stage]);
+                if (inputs > 1) bulk_g2s(slot(stage, 1, q), static_cast<const uint8_t*>(b) + from[q], n[q], &full[stage]);
+            }
     }
-    // element c of row r of an input in shared memory
+    __device__ __forceinline__ uint8_t* slot(int stage, int input, int q) const {
+        return at + ((size_t)(stage * inputs + input) * R + q) * pitch;
+    }
+    // element 0 of row r, the q-th of its step, of an input in shared memory
     template <typename T>
-    __device__ __forceinline__ const T* row(int64_t r, int stage, int input) const {
-        return reinterpret_cast<const T*>(at + ((size_t)stage * inputs + input) * pitch + (((size_t)r * row_bytes) & 15));
+    __device__ __forceinline__ const T* row(int64_t r, int stage, int input, int q) const {
+        return reinterpret_cast<const T*>(slot(stage, input, q) + (((size_t)r * row_bytes) & 15));
     }
 };
 // a unit of the row from shared memory, or from global memory past the copied part
-template <typename T, int V>
-__device__ __forceinline__ void take(Unit<T, V>& u, const Rows& m, const T* in_smem, const T* in_global, int64_t r, int c) {
+template <typename T, int V, int R>
+__device__ __forceinline__ void take(Unit<T, V>& u, const Rows<R>& m, const T* in_smem, const T* in_global, int64_t r, int c) {
     if (V == 1 && (size_t)r * m.row_bytes + (size_t)(c + 1) * sizeof(T) > m.most) u.load(in_global + c);
     else u.load(in_smem + c);
 }
-__device__ __forceinline__ Rows rows_of(uint8_t* smem, size_t row_bytes, int64_t rows, int pitch, int stages, int inputs) {
-    Rows m;
+template <int R>
+__device__ __forceinline__ Rows<R> rows_of(uint8_t* smem, size_t row_bytes, int64_t rows, int pitch, int inputs) {
+    Rows<R> m;
     m.full = reinterpret_cast<uint64_t*>(smem);
     m.at = smem + 64;
     m.row_bytes = row_bytes;
     m.most = (row_bytes * (size_t)rows) & ~(size_t)15;
+    m.rows = rows;
+    m.stride = gridDim.x;
     m.pitch = pitch;
-    m.stages = stages;
     m.inputs = inputs;
     return m;
 }
 
-// Persistent blocks: row blockIdx.x, + gridDim.x, ..; thread t holds units t, t + blockDim.x, .. A wait that
-// gives up (2 s) ends the block without writing that row: there is no workspace to report it in, so the
-// forward writes NaN into the row's outputs.
+// Persistent blocks: rows blockIdx.x, + gridDim.x, .., two at a time (their sums share the barriers, and one's
+// arithmetic runs in the other's waits: one row at a time took 81 instead of .. us at 8192 x 12288); thread t
+// holds units t, t + blockDim.x, .. A copy that has not arrived after 2 s leaves NaN in its rows' outputs
+// (there is no workspace to report it in).
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(512)
     norm_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                          float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int units, int pitch,
                          int stages, float eps) {
+    constexpr int R = 2;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 buf[2][32];
-    const Rows m = rows_of(smem, (size_t)width * sizeof(T), rows, pitch, stages, 1);
+    __shared__ __align__(16) float2 buf[2][32];
+    const Rows<R> m = rows_of<R>(smem, (size_t)width * sizeof(T), rows, pitch, 1);
     const int t = threadIdx.x, nt = blockDim.x;
+    const int64_t step = (int64_t)R * gridDim.x;
     const float inv = 1.0f / (float)width;
     if (t == 0) {
         for (int i = 0; i < stages; ++i) mbar_init(&m.full[i], 1);
         fence_mbar_init();
         for (int i = 0; i < stages; ++i)
-            if (blockIdx.x + (int64_t)i * gridDim.x < rows) m.issue(blockIdx.x + (int64_t)i * gridDim.x, i, x, nullptr);
+            if (blockIdx.x + i * step < rows) m.issue(blockIdx.x + i * step, i, x, nullptr);
     }
-    __syncthreads();
     Params<NV, V> pw, pb;
     pw.init(w, 1.0f, t, nt, units);
     pb.init(b, 0.0f, t, nt, units);
+    __syncthreads();
     int stage = 0;
     uint32_t phase = 0;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    for (int64_t r = blockIdx.x; r < rows; r += step) {
         const bool ok = mbar_wait(&m.full[stage], phase);
-        const T* row = m.row<T>(r, stage, 0);
-        Unit<T, V> u[NV];
-        float s = 0.0f;
+        Unit<T, V> u[R][NV];
+        float s[R];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int i = t + nt * k;
-            if (i < units) take(u[k], m, row, x + r * width, r, i * V);
-            else u[k].zero();
+        for (int q = 0; q < R; ++q) {
+            const int64_t rq = r + q * m.stride;
+            const T* row = m.template row<T>(rq, stage, 0, q);
+            s[q] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) s += u[k].at(e);
+            for (int k = 0; k < NV; ++k) {
+                const int i = t + nt * k;
+                if (i < units && rq < rows) take(u[q][k], m, row, x + rq * width, rq, i * V);
+                else u[q][k].zero();
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[q] += u[q][k].at(e);
+            }
         }
-        const float mu = block_sums(ok ? s : __int_as_float(0x7fffffff), 0.0f, buf[0]).x * inv;
-        // every thread has its part of the row in registers: the stage takes a later one
-        const int64_t next = r + (int64_t)stages * gridDim.x;
+        const float2 mu2 = block_sums(ok ? s[0] : __int_as_float(0x7fffffff), ok ? s[1] : __int_as_float(0x7fffffff), buf[0]);
+        const float mu[R] = {mu2.x * inv, mu2.y * inv};
+        // every thread has its part of the rows in registers: the stage takes later ones
+        const int64_t next = r + stages * step;
         if (t == 0 && next < rows) m.issue(next, stage, x, nullptr);
-        s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (t + nt * k < units)
+        for (int q = 0; q < R; ++q) {
+            s[q] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < V; ++e) s += (u[k].at(e) - mu) * (u[k].at(e) - mu);
-        const float rs = rsqrtf(block_sums(s, 0.0f, buf[1]).x * inv + eps);
+            for (int k = 0; k < NV; ++k)
+                if (t + nt * k < units)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[q] += (u[q][k].at(e) - mu[q]) * (u[q][k].at(e) - mu[q]);
+        }
+        const float2 var = block_sums(s[0], s[1], buf[1]);
+        const float rs[R] = {rsqrtf(var.x * inv + eps), rsqrtf(var.y * inv + eps)};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = t + nt * k;
@@ -381,13 +424,17 @@ __global__ void __launch_bounds__(512)
                 pw.at(k, i, wv);
                 pb.at(k, i, bv);
 #pragma unroll
-                for (int e = 0; e < V; ++e) o[e] = (u[k].at(e) - mu) * rs * wv[e] + bv[e];
-                Unit<T, V>::store(y + r * width + i * V, o);
+                for (int q = 0; q < R; ++q) {
+                    const int64_t rq = r + q * m.stride;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[e] = (u[q][k].at(e) - mu[q]) * rs[q] * wv[e] + bv[e];
+                    if (rq < rows) Unit<T, V>::store(y + rq * width + i * V, o);
+                }
             }
         }
-        if (t == 0) {
-            if (mean) mean[r] = mu;
-            if (rstd) rstd[r] = rs;
+        if (t < R && r + t * m.stride < rows) {
+            if (mean) mean[r + t * m.stride] = t == 0 ? mu[0] : mu[1];
+            if (rstd) rstd[r + t * m.stride] = t == 0 ? rs[0] : rs[1];
         }
         if (++stage == stages) {
             stage = 0;
@@ -396,23 +443,26 @@ __global__ void __launch_bounds__(512)
     }
 }
 
+// The same for the backward, with dw and db of a thread's columns in registers; two rows at a time where
+// registers allow.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(512)
     norm_bwd_wide_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                          const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                          float* __restrict__ part, int64_t rows, int width, int units, int pitch, int stages) {
+    constexpr int R = bwd_rows(NV * V, V > 1);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 buf[2][32];
-    const Rows m = rows_of(smem, (size_t)width * sizeof(T), rows, pitch, stages, 2);
+    __shared__ __align__(16) float2 buf[2][R][32];
+    const Rows<R> m = rows_of<R>(smem, (size_t)width * sizeof(T), rows, pitch, 2);
     const int t = threadIdx.x, nt = blockDim.x;
+    const int64_t step = (int64_t)R * gridDim.x;
     const float inv = 1.0f / (float)width;
     if (t == 0) {
         for (int i = 0; i < stages; ++i) mbar_init(&m.full[i], 1);
         fence_mbar_init();
         for (int i = 0; i < stages; ++i)
-            if (blockIdx.x + (int64_t)i * gridDim.x < rows) m.issue(blockIdx.x + (int64_t)i * gridDim.x, i, x, dy);
+            if (blockIdx.x + i * step < rows) m.issue(blockIdx.x + i * step, i, x, dy);
     }
-    __syncthreads();
     float dw[NV][V], db[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -420,42 +470,67 @@ __global__ void __launch_bounds__(512)
         for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
     Params<NV, V> pw;
     pw.init(w, 1.0f, t, nt, units);
+    __syncthreads();
     int stage = 0, turn = 0;
     uint32_t phase = 0;
-    float mu_next = blockIdx.x < rows ? mean[blockIdx.x] : 0.0f, rs_next = blockIdx.x < rows ? rstd[blockIdx.x] : 0.0f;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const float mu = mu_next, rs = rs_next;
-        if (r + gridDim.x < rows) {
-            mu_next = mean[r + gridDim.x];
-            rs_next = rstd[r + gridDim.x];
+    float mu_next[R], rs_next[R];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t rq = r + q * m.stride;
+            mu_next[q] = rq < rows ? mean[rq] : 0.0f;
+            rs_next[q] = rq < rows ? rstd[rq] : 0.0f;
         }
+    };
+    fetch(blockIdx.x);
+    for (int64_t r = blockIdx.x; r < rows; r += step) {
+        float mu[R], rs[R], s1[R], s2[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            mu[q] = mu_next[q];
+            rs[q] = rs_next[q];
+            s1[q] = s2[q] = 0.0f;
+        }
+        fetch(r + step);
         const bool ok = mbar_wait(&m.full[stage], phase);
-        const T *rx = m.row<T>(r, stage, 0), *rg = m.row<T>(r, stage, 1);
-        Unit<T, V> ux[NV], ug[NV];
-        float s1 = 0.0f, s2 = 0.0f;
+        Unit<T, V> ux[R][NV], ug[R][NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = t + nt * k;
-            if (i < units) {
-                float wv[V];
-                pw.at(k, i, wv);
-                take(ux[k], m, rx, x + r * width, r, i * V);
-                take(ug[k], m, rg, dy + r * width, r, i * V);
+            float wv[V];
+            if (i < units) pw.at(k, i, wv);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float g = ug[k].at(e), h = (ux[k].at(e) - mu) * rs, a = g * wv[e];
-                    s1 += a;
-                    s2 += a * h;
-                    dw[k][e] += g * h;
-                    db[k][e] += g;
+            for (int q = 0; q < R; ++q) {
+                const int64_t rq = r + q * m.stride;
+                if (i < units && rq < rows) {
+                    take(ux[q][k], m, m.template row<T>(rq, stage, 0, q), x + rq * width, rq, i * V);
+                    take(ug[q][k], m, m.template row<T>(rq, stage, 1, q), dy + rq * width, rq, i * V);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float g = ug[q][k].at(e), h = (ux[q][k].at(e) - mu[q]) * rs[q], a = g * wv[e];
+                        s1[q] += a;
+                        s2[q] += a * h;
+                        dw[k][e] += g * h;
+                        db[k][e] += g;
+                    }
                 }
             }
         }
-        const float2 s = block_sums(ok ? s1 : __int_as_float(0x7fffffff), s2, buf[turn]);
+        // one barrier for the sums of all rows of the step
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const float2 p = warp_sums(ok ? s1[q] : __int_as_float(0x7fffffff), s2[q]);
+            if ((t & 31) == 0) buf[turn][q][t >> 5] = p;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const float2 p = sum_of(buf[turn][q]);
+            s1[q] = p.x * inv;
+            s2[q] = p.y * inv;
+        }
         turn ^= 1;
-        s1 = s.x * inv;
-        s2 = s.y * inv;
-        const int64_t next = r + (int64_t)stages * gridDim.x;
+        const int64_t next = r + stages * step;
         if (t == 0 && next < rows) m.issue(next, stage, x, dy);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -464,8 +539,13 @@ __global__ void __launch_bounds__(512)
                 float wv[V], o[V];
                 pw.at(k, i, wv);
 #pragma unroll
-                for (int e = 0; e < V; ++e) o[e] = rs * (ug[k].at(e) * wv[e] - s1 - (ux[k].at(e) - mu) * rs * s2);
-                Unit<T, V>::store(dx + r * width + i * V, o);
+                for (int q = 0; q < R; ++q) {
+                    const int64_t rq = r + q * m.stride;
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        o[e] = rs[q] * (ug[q][k].at(e) * wv[e] - s1[q] - (ux[q][k].at(e) - mu[q]) * rs[q] * s2[q]);
+                    if (rq < rows) Unit<T, V>::store(dx + rq * width + i * V, o);
+                }
             }
         }
         if (++stage == stages) {
@@ -488,7 +568,7 @@ __global__ void __launch_bounds__(512)
 
 // ---------------------------------------------------------------------------- any width
 // One row for each block, read three times (from the cache after the first).
-__device__ __forceinline__ float block_sum(float x, float2* buf) {
+__device__ __forceinline__ float block_sum(float x, float2 (&buf)[32]) {
     const float s = block_sums(x, 0.0f, buf).x;
     __syncthreads();
     return s;
@@ -497,7 +577,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads)
     norm_fwd_any_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                         float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, float eps) {
-    __shared__ float2 buf[32];
+    __shared__ __align__(16) float2 buf[32];
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T* xr = x + r * width;
         float s = 0.0f;
@@ -522,7 +602,7 @@ __global__ void __launch_bounds__(kThreads)
     norm_dx_any_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                        const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx, int64_t rows,
                        int width) {
-    __shared__ float2 buf[2][32];
+    __shared__ __align__(16) float2 buf[2][32];
     int turn = 0;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
         const float mu = mean[r], rs = rstd[r];
@@ -568,7 +648,7 @@ __global__ void __launch_bounds__(1024)
     const int c = blockIdx.x * 32 + threadIdx.x;
     float a = 0.0f;
     if (c < width)
-#pragma unroll 4
+#pragma unroll 8
         for (int i = threadIdx.y; i < n; i += 32) a += part[((size_t)i * 2 + blockIdx.y) * width + c];
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
@@ -594,10 +674,12 @@ bool valid_size(long long rows, long long width) {
     return rows >= 0 && width >= 1 && width <= (1LL << 20) && rows <= (1LL << 40) / width;
 }
 
-// Most blocks whose sums of dw and db are kept: eight on an SM, and no more than about 32 MB of sums.
-int most_parts(long long width) {
-    const long long n = (32LL << 20) / (8 * width);
-    return (int)(n < kSMs ? kSMs : n > 8 * kSMs ? 8 * kSMs : n);
+// Most blocks whose sums of dw and db are kept: four on an SM, and one for every SM at least. Their sums are
+// written and read again, so they stay below about a twentieth of what the rows themselves move.
+constexpr int kMostParts = 4 * kSMs;
+int most_parts(long long rows, size_t size) {
+    const long long n = rows * (long long)size / 54;
+    return (int)(n < kSMs ? kSMs : n > kMostParts ? kMostParts : n);
 }
 
 // Which form a width takes, and its launch.
@@ -622,24 +704,24 @@ Form form_of(long long width, size_t size, int inputs) {
     }
     if (width > kWideMost) return f;
     f.wide = true;
-    // as few units a thread as 256 threads (512 from two units on) allow
-    const int most[] = {1, 2, 3, 4, 8, 16, 32};
+    // 16 bf16 or 8 fp32 columns a thread and small blocks, so that many rows are in flight; more columns
+    // where 512 threads do not hold the row
+    const int most[] = {2, 3, 4, 8, 16, 32};
     for (int nv : most) {
         f.nv = nv;
-        if (f.units <= nv * (nv > 1 ? 512 : 256)) break;
+        if ((f.vec || nv >= 8) && f.units <= nv * 512) break;
     }
     f.threads = ((f.units + f.nv - 1) / f.nv + 31) / 32 * 32;
     f.pitch = (int)((width * size + 31) / 16 * 16);
-    const int stage = f.pitch * inputs;
-    // threads on an SM: the parameters and the backward's sums take registers
     const int columns = f.nv * (f.vec ? v : 1);
-    const int room = columns * (inputs + 1) >= 48 ? 512 : 1024;
+    const int stage = f.pitch * inputs * (inputs == 1 ? 2 : bwd_rows(columns, f.vec));
+    const int room = columns * (inputs + 1) >= 48 ? 512 : 1024;   // threads on an SM, by registers
     f.per_sm = room / f.threads < 1 ? 1 : room / f.threads;
-    if (f.per_sm > 8) f.per_sm = 8;
-    // up to four rows ahead, within the SM's shared memory; fewer blocks rather than none ahead
+    if (f.per_sm > 16) f.per_sm = 16;
+    // up to four steps ahead, within the SM's shared memory; fewer blocks rather than none ahead
     for (;; --f.per_sm) {
         f.stages = (int)(((size_t)216 * 1024 / f.per_sm - 1024 - 64) / stage);
-        if (f.stages >= 3 || f.per_sm == 1) break;
+        if (f.stages >= 2 || f.per_sm == 1) break;
     }
     if (f.stages > 4) f.stages = 4;
     if (f.stages < 1) f.stages = 1;
@@ -685,14 +767,12 @@ kda_status fwd(long long rows, int width, float eps, const void* xv, const float
         KDA_NORM(fwd_narrow, 1, 16);
     }
     if (f.wide && f.vec) {
-        if (f.nv == 1) KDA_NORM(fwd_wide, V, 1);
         if (f.nv == 2) KDA_NORM(fwd_wide, V, 2);
         if (f.nv == 3) KDA_NORM(fwd_wide, V, 3);
         if (f.nv == 4) KDA_NORM(fwd_wide, V, 4);
         if constexpr (V == 4) KDA_NORM(fwd_wide, V, 8);
     }
     if (f.wide) {
-        if (f.nv <= 4) KDA_NORM(fwd_wide, 1, 4);
         if (f.nv <= 8) KDA_NORM(fwd_wide, 1, 8);
         if (f.nv <= 16) KDA_NORM(fwd_wide, 1, 16);
         KDA_NORM(fwd_wide, 1, 32);
@@ -707,8 +787,8 @@ kda_status bwd_wide(const Form& f, long long rows, int width, const T* x, const 
                     const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
     auto k = norm_bwd_wide_kernel<T, V, NV>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_bwd");
-    const long long most = (long long)kSMs * f.per_sm;
-    *parts = (int)blocks(rows, most < most_parts(width) ? most : most_parts(width));
+    const long long most = (long long)kSMs * f.per_sm, keep = most_parts(rows, sizeof(T));
+    *parts = (int)blocks(rows, most < keep ? most : keep);
     k<<<*parts, f.threads, f.smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.units, f.pitch, f.stages);
     return launched("kda_layernorm_bwd launch");
 }
@@ -717,7 +797,7 @@ kda_status bwd_narrow(const Form& f, long long rows, int width, const T* x, cons
                       const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
     constexpr int R = V * NV <= 8 ? 2 : 1;
     const long long rpb = (long long)(kThreads / 32) * (32 / f.lpr);
-    *parts = (int)blocks((rows + rpb - 1) / rpb, most_parts(width));
+    *parts = (int)blocks((rows + rpb - 1) / rpb, (V * NV <= 8 ? 4 : 2) * kSMs);   // as many as are resident
     norm_bwd_narrow_kernel<T, V, NV, R><<<*parts, kThreads, (size_t)(kThreads / 32) * 2 * width * sizeof(float), s>>>(
         x, dy, w, mean, rstd, dx, part, rows, width, f.units, f.lpr);
     return launched("kda_layernorm_bwd launch");
@@ -742,14 +822,12 @@ kda_status bwd(long long rows, int width, const void* xv, const void* dyv, const
         KDA_NORM(bwd_narrow, 1, 16);
     }
     if (f.wide && f.vec) {
-        if (f.nv == 1) KDA_NORM(bwd_wide, V, 1);
         if (f.nv == 2) KDA_NORM(bwd_wide, V, 2);
         if (f.nv == 3) KDA_NORM(bwd_wide, V, 3);
         if (f.nv == 4) KDA_NORM(bwd_wide, V, 4);
         if constexpr (V == 4) KDA_NORM(bwd_wide, V, 8);
     }
     if (f.wide) {
-        if (f.nv <= 4) KDA_NORM(bwd_wide, 1, 4);
         if (f.nv <= 8) KDA_NORM(bwd_wide, 1, 8);
         if (f.nv <= 16) KDA_NORM(bwd_wide, 1, 16);
         KDA_NORM(bwd_wide, 1, 32);
@@ -786,7 +864,7 @@ extern "C" kda_status kda_layernorm_fwd(long long rows, long long width, int dty
 
 extern "C" size_t kda_layernorm_workspace_size(long long rows, long long width) {
     if (!valid_size(rows, width)) return 0;
-    return align_up((size_t)most_parts(width) * 2 * (size_t)width * sizeof(float), 1024);
+    return align_up((size_t)(rows < kMostParts ? rows + 1 : kMostParts) * 2 * (size_t)width * sizeof(float), 1024);
 }
 
 extern "C" kda_status kda_layernorm_bwd(long long rows, long long width, int dtype, const void* x, const void* dy,

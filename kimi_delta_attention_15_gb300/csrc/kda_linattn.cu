@@ -161,12 +161,13 @@ __device__ __forceinline__ Chunk chunk_of(const Unit& u, int c) {
     x.hi = u.rev ? LC : min(left, LC);
     return x;
 }
-// The decayed keys of a chunk go into the state's sum as two bf16 parts (16 significant bits), or as
-// three (24) where the state is an output and the tokens still to come will not have decayed this
-// chunk's share, and its error with it, by another 2^-8. (Without any decay one part is exact.)
+// The decayed keys of a chunk go into the state's sum as two bf16 parts (16 significant bits, 2.2e-6 of
+// their size in the mean square), or as three (24) where the state is an output and the tokens still to
+// come will not have decayed this chunk's share, and its error with it, by another e^-1: an output state
+// is within 1e-6 of its size. (Without any decay one part is exact.)
 __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
     const int left = u.after + max(u.len - (c + 1) * LC, 0);
-    return u.exact && u.g != 0.0f && (left == 0 || u.g * (float)left > -5.6f);
+    return u.exact && u.g != 0.0f && (left == 0 || u.g * (float)left > -1.0f);
 }
 __device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
 
@@ -590,41 +591,17 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                 tc_fence_after();
             }
             const bool carried = c > 0 || u.s_in, sum = c + 1 < chunks || (c < chunks && u.s_out), three = sum && three_parts(u, c);
-            auto parts_fp32 = [&](const Chunk& k, bool low) {
-#pragma unroll 1
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t x[8], hi[8], mi[8], lo[8];
-                    const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
-                    ldmatrix4_trans(key + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
-                    ldmatrix4_trans(key + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int t = jr + 32 * (g >> 1) + 8 * m;
-                        const bool mine0 = t >= k.lo && t < k.hi, mine1 = t + 1 >= k.lo && t + 1 < k.hi;
-                        // gamma^{L-1-t} (reversed, counted from the end: gamma^{t+1-lo}) is at t + 128 - L (t - lo)
-                        const int e = u.rev ? t - k.lo : t + LC - k.hi;
-                        const f32x2 w = two(sm.decay[mine0 ? e : 0], sm.decay[mine1 ? e + 1 : 0]);
-                        const uint32_t mask = (mine0 ? 0xffffu : 0u) | (mine1 ? 0xffff0000u : 0u);
-                        const f32x2 minus = two(-1.0f, -1.0f);
-#pragma unroll
-                        for (int i = 2 * m; i < 2 * m + 2; ++i) {
-                            x[i] &= mask;
-                            f32x2 p = mul2(w, two(low_bf16(x[i]), high_bf16(x[i])));
-                            hi[i] = pack_bf16(p);
-                            p = fma2(minus, two(low_bf16(hi[i]), high_bf16(hi[i])), p);
-                            mi[i] = pack_bf16(p);
-                            p = fma2(minus, two(low_bf16(mi[i]), high_bf16(mi[i])), p);
-                            lo[i] = pack_bf16(p);
-                        }
-                    }
-                    const uint32_t at_t = lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1);
-                    if (low) {
-                        tmem_st_frag_issue(at_t + low_col(u.rev), lo);
-                    } else {
-                        tmem_st_frag_issue(at_t + kColMid, mi);
-                        tmem_st_frag_issue(at_t + kColHi, hi);
-                    }
-                }
+            // 32 tokens x 16 channels of K, the g-th of this warp's four blocks
+            auto fragments = [&](int g, uint32_t (&x)[8]) {
+                const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
+                ldmatrix4_trans(key + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
+                ldmatrix4_trans(key + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
+            };
+            auto place = [&](int g) { return lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1); };
+            // where a thread's low parts of block g wait: the block's own bytes of K, which nothing else reads
+            // once it is in fragments and the scores are done
+            auto wait_place = [&](int g, int e) {
+                return sm.K + panel_off_bf16(64 * half + 32 * (g >> 1) + lane, 4 * warp + 2 * (g & 1) + e, LC);
             };
             if (c < chunks) {
                 // decayed keys, transposed to [channel][token], to tensor memory: first, while the scores and
@@ -643,11 +620,9 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                 if (sum && whole && !three) {
                     // w1 x = hi + e without error (the error of a rounded product has 8 bits), mid = w2 x + e
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {   // 32 tokens x 16 channels
+                    for (int g = 0; g < 4; ++g) {
                         uint32_t x[8], hi[8], mi[8];
-                        const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
-                        ldmatrix4_trans(key + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
-                        ldmatrix4_trans(key + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
+                        fragments(g, x);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int w = 4 * (g >> 1) + (i >> 1);
@@ -658,12 +633,42 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                             hi[i] = *reinterpret_cast<const uint32_t*>(&h);
                             mi[i] = *reinterpret_cast<const uint32_t*>(&m);
                         }
-                        const uint32_t at_t = lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1);
-                        tmem_st_frag_issue(at_t + kColMid, mi);
-                        tmem_st_frag_issue(at_t + kColHi, hi);
+                        tmem_st_frag_issue(place(g) + kColMid, mi);
+                        tmem_st_frag_issue(place(g) + kColHi, hi);
                     }
                 } else if (sum) {   // three parts, or rows of a neighbour among the tokens: in fp32
-                    parts_fp32(k, false);
+                    if (three && !(ok = wait_warp(&sm.qk, n))) break;
+#pragma unroll 1
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t x[8], hi[8], mi[8], lo[8];
+                        fragments(g, x);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const int t = jr + 32 * (g >> 1) + 8 * m;
+                            const bool mine0 = t >= k.lo && t < k.hi, mine1 = t + 1 >= k.lo && t + 1 < k.hi;
+                            // gamma^{L-1-t} (reversed, counted from the end: gamma^{t+1-lo}) is at t + 128 - L (t - lo)
+                            const int e = u.rev ? t - k.lo : t + LC - k.hi;
+                            const f32x2 w = two(sm.decay[mine0 ? e : 0], sm.decay[mine1 ? e + 1 : 0]);
+                            const uint32_t mask = (mine0 ? 0xffffu : 0u) | (mine1 ? 0xffff0000u : 0u);
+                            const f32x2 minus = two(-1.0f, -1.0f);
+#pragma unroll
+                            for (int i = 2 * m; i < 2 * m + 2; ++i) {
+                                x[i] &= mask;
+                                f32x2 p = mul2(w, two(low_bf16(x[i]), high_bf16(x[i])));
+                                hi[i] = pack_bf16(p);
+                                p = fma2(minus, two(low_bf16(hi[i]), high_bf16(hi[i])), p);
+                                mi[i] = pack_bf16(p);
+                                p = fma2(minus, two(low_bf16(mi[i]), high_bf16(mi[i])), p);
+                                lo[i] = pack_bf16(p);
+                            }
+                        }
+                        tmem_st_frag_issue(place(g) + kColMid, mi);
+                        tmem_st_frag_issue(place(g) + kColHi, hi);
+                        if (three) {
+                            *reinterpret_cast<uint4*>(wait_place(g, 0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            *reinterpret_cast<uint4*>(wait_place(g, 1)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                        }
+                    }
                 }
                 tmem_wait_st_all();
                 tc_fence_before();
@@ -715,9 +720,15 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             if (three) {   // the low parts: beside the scores' bf16 copy, once that is made
                 if (!(ok = wait_warp(&sm.p, n))) break;
                 tc_fence_after();
-                parts_fp32(chunk_of(u, c), true);
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(wait_place(g, 0)), y = *reinterpret_cast<const uint4*>(wait_place(g, 1));
+                    const uint32_t lo[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                    tmem_st_frag_issue(place(g) + low_col(u.rev), lo);
+                }
                 tmem_wait_st_all();
                 tc_fence_before();
+                fence_async_smem();   // K's next tile comes by TMA
                 mbar_arrive(&sm.k_free);
                 mbar_arrive(&sm.low);
             }
@@ -809,13 +820,24 @@ __global__ void __launch_bounds__(256) linattn_carry_kernel(const __grid_constan
         const float over = 1.0f / j.s_scale;
         x.x *= over; x.y *= over; x.z *= over; x.w *= over;
     }
-    for (int k = 0; k < s.nseg; ++k) {
-        const int at = j.rev ? i + s.nseg - 1 - k : i + k;
-        float4* p = reinterpret_cast<float4*>(j.seg + ((size_t)at * a.H + h) * D * D + e);
-        const float4 y = k + 1 < s.nseg ? *p : x;
-        *p = x;
-        const float w = expf(g * (float)slot_of(a, at).len);
-        x = make_float4(w * x.x + y.x, w * x.y + y.y, w * x.z + y.z, w * x.w + y.w);
+    // segments in the job's order, eight loads in flight; all but the last in time have seg_len tokens
+    const int64_t step = (j.rev ? -1 : 1) * (int64_t)a.H * D * D;
+    float* p = j.seg + ((size_t)(j.rev ? i + s.nseg - 1 : i) * a.H + h) * D * D + e;
+    const float whole = expf(g * (float)a.seg_len), last = expf(g * (float)(s.after - (int64_t)(s.nseg - 2) * a.seg_len));
+    for (int k0 = 0; k0 < s.nseg; k0 += 8, p += 8 * step) {
+        float4 y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)   // the sum of the last segment in order is not there and not needed
+            if (k0 + k + 1 < s.nseg) y[k] = *reinterpret_cast<const float4*>(p + k * step);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < s.nseg) {
+                *reinterpret_cast<float4*>(p + k * step) = x;
+                if (k0 + k + 1 < s.nseg) {
+                    const float w = j.rev && k0 + k == 0 ? last : whole;
+                    x = make_float4(w * x.x + y[k].x, w * x.y + y[k].y, w * x.z + y[k].z, w * x.w + y[k].w);
+                }
+            }
     }
 }
 
