@@ -196,6 +196,8 @@ constexpr int kScoreWarps = 4, kMainWarps = 8;
 constexpr int kLinThreads = 512;
 constexpr int kMainRegs = 152, kIssueRegs = 80;
 
+// the same value in every lane of the warp, and known to be (uniform registers)
+template <typename X> __device__ __forceinline__ X uniform(X x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, int n) {
     return __all_sync(0xffffffffu, mbar_wait_asleep(bar, (uint32_t)(n & 1)));
 }
@@ -539,7 +541,7 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
 // --- state in registers and its bf16 copy for the next chunk; decayed keys as bf16 parts; Q S^T decayed by row
 __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
-    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, half = (threadIdx.x - 32 * kScoreWarps) >> 7;
+    const int warp = uniform((int)((threadIdx.x >> 5) & 3)), lane = threadIdx.x & 31, half = uniform((int)((threadIdx.x - 32 * kScoreWarps) >> 7));
     const int row = 32 * warp + lane;              // TMEM lane: output row, or key channel of the state
     const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16), wide = lanes + 64 * half;
     // decayed keys: this warp's channels 32 warp + .., tokens 64 half + ..; ldmatrix row of this thread
@@ -758,7 +760,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
         return;
     }
     const int units = units_of(a);
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform((int)(threadIdx.x >> 5));
     if (warp == 0) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = sm.tmem;
+    const uint32_t tm = uniform(sm.tmem);
     if (warp < kScoreWarps) {
         lin_scores(a, sm, units, tm);
     } else if (warp < kScoreWarps + kMainWarps) {
@@ -892,6 +894,17 @@ __global__ void __launch_bounds__(1024)
         *slots = carry;
         *reinterpret_cast<int*>(ws) = 0;
     }
+    // Whole sequences, few of them: longest first. A block's rounds come from opposite ends of the list in turn,
+    // which evens them out (lengths 1300, 547, 2048, 963, 271, 3063 with 96 heads on 152 SMs: at most 46 chunks
+    // on an SM instead of 59, with 43 in the mean).
+    if (seg_len < T_total || N > (int)blockDim.x) return;
+    const Slot own = tid < N ? table[tid] : Slot{};
+    scan[tid] = own.len;
+    __syncthreads();
+    if (tid >= N) return;
+    int rank = 0;
+    for (int m = 0; m < N; ++m) rank += scan[m] > own.len || (scan[m] == own.len && m < tid);
+    table[rank] = own;
 }
 
 // dq, dk of a query/key head: the sum of its G value heads' shares, in head order.

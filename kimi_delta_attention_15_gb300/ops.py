@@ -315,9 +315,7 @@ def _ready(specs):
                 continue
         elif t.dtype is dtype and t.numel() == numel and t.is_contiguous():
             d = t.get_device()
-            if d == dev:
-                continue
-            if dev < 0 <= d:
+            if d >= 0 and (d == dev or dev < 0):
                 dev = d
                 continue
         _validate(specs)
@@ -366,16 +364,25 @@ def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, B: int = 1, sca
     H, N = shape.H, shape.N
     tok = shape.B * shape.T * 128
     qk, state = tok * (H // shape.groups), N * H * 16384
+    specs = [("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, tok * H, _BF, False),
+             ("log_decay", log_decay, H, _F32, False)]
+    if h0 is not None:
+        specs.append(("h0", h0, state, _F32, True))
+    if cu_seqlens is not None:
+        specs.append(("cu_seqlens", cu_seqlens, N + 1, _I64, True))
+    if o is not None:
+        specs.append(("o", o, tok * H, _BF, False))
+    if hT is not None:
+        specs.append(("hT", hT, state, _F32, True))
+    if workspace is not None:
+        specs.append(("workspace", workspace, workspace.numel(), _U8, False))
+    dev = _ready(specs)
     if workspace is None:
         workspace = linattn_alloc_workspace(shape, q.device)
     if o is None:
         o = torch.empty_like(v)
     if hT is None and want_hT:
         hT = torch.empty((N, H, 128, 128), dtype=_F32, device=q.device)
-    dev = _ready((("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, tok * H, _BF, False),
-                  ("log_decay", log_decay, H, _F32, False), ("h0", h0, state, _F32, True),
-                  ("cu_seqlens", cu_seqlens, N + 1, _I64, True), ("o", o, tok * H, _BF, False), ("hT", hT, state, _F32, True),
-                  ("workspace", workspace, workspace.numel(), _U8, False)))
     code = lib.kda_linattn_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                _address(h0), _address(cu_seqlens), o.data_ptr(), _address(hT), workspace.data_ptr(),
                                workspace.numel(), _raw_stream(stream, dev))
@@ -394,21 +401,29 @@ def linattn_bwd(q, k, v, log_decay, do, workspace=None, h0=None, cu_seqlens=None
     H, N = shape.H, shape.N
     tok = shape.B * shape.T * 128
     qk, state = tok * (H // shape.groups), N * H * 16384
+    specs = [("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, tok * H, _BF, False),
+             ("log_decay", log_decay, H, _F32, False), ("do", do, tok * H, _BF, False)]
+    if h0 is not None:
+        specs.append(("h0", h0, state, _F32, True))
+    if cu_seqlens is not None:
+        specs.append(("cu_seqlens", cu_seqlens, N + 1, _I64, True))
+    if dhT is not None:
+        specs.append(("dhT", dhT, state, _F32, True))
+    if workspace is not None:
+        specs.append(("workspace", workspace, workspace.numel(), _U8, False))
+    if grads is not None:
+        specs += [("dq", grads.get("dq"), qk, _BF, False), ("dk", grads.get("dk"), qk, _BF, False),
+                  ("dv", grads.get("dv"), tok * H, _BF, False), ("dh0", grads.get("dh0"), state, _F32, True)]
+    dev = _ready(specs)
     if workspace is None:
         workspace = linattn_alloc_workspace(shape, q.device, backward=True)
     if grads is None:
         grads = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                      dh0=torch.empty((N, H, 128, 128), dtype=_F32, device=q.device) if want_dh0 else None)
-    dq, dk, dv, dh0 = grads.get("dq"), grads.get("dk"), grads.get("dv"), grads.get("dh0")
-    dev = _ready((("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, tok * H, _BF, False),
-                  ("log_decay", log_decay, H, _F32, False), ("h0", h0, state, _F32, True),
-                  ("cu_seqlens", cu_seqlens, N + 1, _I64, True), ("do", do, tok * H, _BF, False),
-                  ("dhT", dhT, state, _F32, True), ("dq", dq, qk, _BF, False), ("dk", dk, qk, _BF, False),
-                  ("dv", dv, tok * H, _BF, False), ("dh0", dh0, state, _F32, True),
-                  ("workspace", workspace, workspace.numel(), _U8, False)))
     code = lib.kda_linattn_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                               _address(h0), _address(cu_seqlens), do.data_ptr(), _address(dhT), dq.data_ptr(), dk.data_ptr(),
-                               dv.data_ptr(), _address(dh0), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+                               _address(h0), _address(cu_seqlens), do.data_ptr(), _address(dhT), grads["dq"].data_ptr(),
+                               grads["dk"].data_ptr(), grads["dv"].data_ptr(), _address(grads.get("dh0")),
+                               workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if code:
         _check(code, "kda_linattn_bwd")
     return grads
@@ -417,15 +432,19 @@ def linattn_bwd(q, k, v, log_decay, do, workspace=None, h0=None, cu_seqlens=None
 def linattn_decode(q, k, v, log_decay, state, *, o=None, scale: float = SCALE, stream=None):
     """kda_linattn_decode: one token per request. v [n_req, H, 128] bf16, q, k [n_req, H / groups, 128]
     bf16; `state` [n_req, H, 128, 128] fp32 is updated in place. Returns o [n_req, H, 128] bf16."""
-    n_req, H, Hqk = v.shape[0], v.shape[1], q.shape[1]
+    n_req, H, _ = v.shape
+    Hqk = q.shape[1]
     if Hqk <= 0 or H % Hqk != 0:
         raise ValueError(f"value heads ({H}) must be a multiple of query/key heads ({Hqk})")
-    if o is None:
-        o = torch.empty_like(v)
     lib = _lib or load()
     qk, n = n_req * Hqk * 128, n_req * H * 128
-    dev = _ready((("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, n, _BF, False),
-                  ("log_decay", log_decay, H, _F32, False), ("state", state, n * 128, _F32, False), ("o", o, n, _BF, False)))
+    specs = [("q", q, qk, _BF, False), ("k", k, qk, _BF, False), ("v", v, n, _BF, False),
+             ("log_decay", log_decay, H, _F32, False), ("state", state, n * 128, _F32, False)]
+    if o is not None:
+        specs.append(("o", o, n, _BF, False))
+    dev = _ready(specs)
+    if o is None:
+        o = torch.empty_like(v)
     code = lib.kda_linattn_decode(n_req, H, H // Hqk, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                   state.data_ptr(), o.data_ptr(), _raw_stream(stream, dev))
     if code:
@@ -449,16 +468,27 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, mean=
     """kda_layernorm_fwd over the last dimension. x bf16 or fp32, weight and bias [width] fp32 or
     None. Returns (y, mean, rstd); mean and rstd [rows] fp32 are what layernorm_bwd reads."""
     n, rows, width = _norm_size(x)
+    dtype = x.dtype
+    lib = _lib or load()
+    specs = [("x", x, n, dtype, False)]
+    if weight is not None:
+        specs.append(("weight", weight, width, _F32, True))
+    if bias is not None:
+        specs.append(("bias", bias, width, _F32, True))
+    if y is not None:
+        specs.append(("y", y, n, dtype, False))
+    if mean is not None:
+        specs.append(("mean", mean, rows, _F32, False))
+    if rstd is not None:
+        specs.append(("rstd", rstd, rows, _F32, False))
+    dev = _ready(specs)
     if y is None:
         y = torch.empty_like(x)
     if mean is None:
         mean = torch.empty(rows, dtype=_F32, device=x.device)
     if rstd is None:
         rstd = torch.empty(rows, dtype=_F32, device=x.device)
-    lib = _lib or load()
-    dev = _ready((("x", x, n, x.dtype, False), ("weight", weight, width, _F32, True), ("bias", bias, width, _F32, True),
-                  ("y", y, n, x.dtype, False), ("mean", mean, rows, _F32, False), ("rstd", rstd, rows, _F32, False)))
-    code = lib.kda_layernorm_fwd(rows, width, _NORM_DTYPES[x.dtype], eps, x.data_ptr(), _address(weight), _address(bias),
+    code = lib.kda_layernorm_fwd(rows, width, _NORM_DTYPES[dtype], eps, x.data_ptr(), _address(weight), _address(bias),
                                  y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev))
     if code:
         _check(code, "kda_layernorm_fwd")
@@ -470,20 +500,27 @@ def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool =
     """kda_layernorm_bwd with the mean and rstd of layernorm_fwd (weight None reads as 1). Returns a
     dict of dx (dtype of x), dweight and dbias ([width] fp32)."""
     n, rows, width = _norm_size(x)
+    dtype = x.dtype
     lib = _lib or load()
+    specs = [("x", x, n, dtype, False), ("dy", dy, n, dtype, False), ("mean", mean, rows, _F32, False),
+             ("rstd", rstd, rows, _F32, False)]
+    if weight is not None:
+        specs.append(("weight", weight, width, _F32, True))
+    if workspace is not None:
+        specs.append(("workspace", workspace, workspace.numel(), _U8, False))
+    if grads is not None:
+        specs += [("dx", grads.get("dx"), n, dtype, False), ("dweight", grads.get("dweight"), width, _F32, True),
+                  ("dbias", grads.get("dbias"), width, _F32, True)]
+    dev = _ready(specs)
     if workspace is None:
         workspace = torch.empty(lib.kda_layernorm_workspace_size(rows, width), dtype=_U8, device=x.device)
     if grads is None:
         grads = dict(dx=torch.empty_like(x), dweight=torch.empty(width, dtype=_F32, device=x.device) if want_dweight else None,
                      dbias=torch.empty(width, dtype=_F32, device=x.device) if want_dbias else None)
-    dx, dweight, dbias = grads.get("dx"), grads.get("dweight"), grads.get("dbias")
-    dev = _ready((("x", x, n, x.dtype, False), ("dy", dy, n, x.dtype, False), ("weight", weight, width, _F32, True),
-                  ("mean", mean, rows, _F32, False), ("rstd", rstd, rows, _F32, False), ("dx", dx, n, x.dtype, False),
-                  ("dweight", dweight, width, _F32, True), ("dbias", dbias, width, _F32, True),
-                  ("workspace", workspace, workspace.numel(), _U8, False)))
-    code = lib.kda_layernorm_bwd(rows, width, _NORM_DTYPES[x.dtype], x.data_ptr(), dy.data_ptr(), _address(weight),
-                                 mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _address(dweight), _address(dbias),
-                                 workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    dweight, dbias = grads.get("dweight"), grads.get("dbias")
+    code = lib.kda_layernorm_bwd(rows, width, _NORM_DTYPES[dtype], x.data_ptr(), dy.data_ptr(), _address(weight),
+                                 mean.data_ptr(), rstd.data_ptr(), grads["dx"].data_ptr(), _address(dweight),
+                                 _address(dbias), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if code:
         _check(code, "kda_layernorm_bwd")
     return grads
