@@ -172,20 +172,20 @@ __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
 __device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
 
 struct LinSmem {
-    // operand tiles (bf16 panels, 1024-byte aligned), Q and V by chunk parity
-    uint8_t K[kTile], Q[2][kTile], V[2][kTile];
+    // operand tiles (bf16 panels, 1024-byte aligned), K and V by chunk parity
+    uint8_t K[2][kTile], V[2][kTile], Q[kTile];
     uint8_t S[kTile];        // the state the chunk starts from, [c][v], rounded to bf16
     uint8_t stage[kTile];    // output rows on their way out
     float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
     float decay[LC];         // of the keys of a whole chunk
-    // full: operands in shared memory; qk, qs, ds, pv: MMA groups done; s, p, piece, low, o: operands written
-    // (state, scores, decayed keys and their low parts, decayed Q S^T); k_free, r: keys, outputs read. Each completes one
-    // phase per chunk (full_q, full_v: one of the two; low: per chunk with three parts).
+    // full: operands in shared memory; qk, qs, ds, pv: MMA groups done, all: of the chunk; s, p, piece, low, o:
+    // operands written (state, scores, decayed keys and their low parts, decayed Q S^T); r: outputs read. Each
+    // completes one phase per chunk (full_k, full_v, all: one of the two; low: per chunk with three parts).
     // A wait names a phase by its parity, so no waiter may be a whole phase behind or ahead: every wait
     // comes before an arrival of the same thread on which the barrier's next phase depends, and after
     // something that depends on the phase before. A thread that arrives twice on a barrier waits in between
     // for something that depends on all the first arrivals.
-    uint64_t full_k, full_q[2], full_v[2], qk, qs, ds, pv, s, p, piece, low, k_free, o, r, end;
+    uint64_t full_k[2], full_q, full_v[2], all[2], qk, qs, ds, pv, s, p, piece, low, o, r, end;
     uint32_t tmem;
 };
 
@@ -263,51 +263,42 @@ struct At {
 // --- loads, one thread
 __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int units) {
     const bool state_only = a.state_only != 0;
-    auto tile = [&](uint8_t* dst, int which, const At& x, uint64_t* bar) {
-        const Chunk k = chunk_of(x.u, x.c);
-        const int head = x.u.h / a.group[which];
+    struct Place { int q, k, v, h, t; };
+    auto place = [](const At& x) { return Place{x.u.q, x.u.k, x.u.v, x.u.h, (int)chunk_of(x.u, x.c).t}; };
+    auto tile = [&](uint8_t* dst, int which, const Place& x, uint64_t* bar) {
+        const int head = x.h / a.group[which];
         mbar_arrive_expect_tx(bar, kTile);
-        tma_load_3d(dst, &a.map[which], 0, head, (int)k.t, bar);
-        tma_load_3d(dst + kTile / 2, &a.map[which], 64, head, (int)k.t, bar);
+        tma_load_3d(dst, &a.map[which], 0, head, x.t, bar);
+        tma_load_3d(dst + kTile / 2, &a.map[which], 64, head, x.t, bar);
     };
-    auto q_tile = [&](int b, const At& x) {
-        if (state_only) mbar_arrive(&sm.full_q[b]);
-        else tile(sm.Q[b], x.u.q, x, &sm.full_q[b]);
+    auto q_tile = [&](const Place& x) {
+        if (state_only) mbar_arrive(&sm.full_q);
+        else tile(sm.Q, x.q, x, &sm.full_q);
     };
-    auto ahead = [&](int which, const At& x) {
-        const Chunk k = chunk_of(x.u, x.c);
-        const int head = x.u.h / a.group[which];
-        tma_prefetch_3d(&a.map[which], 0, head, (int)k.t);
-        tma_prefetch_3d(&a.map[which], 64, head, (int)k.t);
+    auto ahead = [&](int which, const Place& x) {
+        const int head = x.h / a.group[which];
+        tma_prefetch_3d(&a.map[which], 0, head, x.t);
+        tma_prefetch_3d(&a.map[which], 64, head, x.t);
     };
-    At x;   // the chunk after n
+    At x;
     x.first(a, units);
     if (!x.more) return;
-    tile(sm.K, x.u.k, x, &sm.full_k);
-    q_tile(0, x);
-    tile(sm.V[0], x.u.v, x, &sm.full_v[0]);
-    x.next(a, units);
-    if (x.more) {
-        q_tile(1, x);
-        ahead(x.u.k, x);
-        ahead(x.u.v, x);
-    }
-    for (int n = 0; x.more; ++n) {
-        // Q S^T of chunk n done: so are its scores and everything of chunk n - 1. K is free with its decayed
-        // copies made, Q[n & 1] and V[(n + 1) & 1] are free.
-        if (!mbar_wait_asleep(&sm.k_free, (uint32_t)(n & 1)) || !mbar_wait_asleep(&sm.qs, (uint32_t)(n & 1))) {
-            raise_status(a.ws, KDA_ERR_TIMEOUT);
-            return;
-        }
-        tile(sm.K, x.u.k, x, &sm.full_k);
-        tile(sm.V[(n + 1) & 1], x.u.v, x, &sm.full_v[(n + 1) & 1]);
+    Place next = place(x);
+    tile(sm.K[0], next.k, next, &sm.full_k[0]);
+    tile(sm.V[0], next.v, next, &sm.full_v[0]);
+    q_tile(next);
+    for (int n = 0;; ++n) {
         x.next(a, units);
-        if (x.more) {
-            q_tile(n & 1, x);
-            ahead(x.u.k, x);   // K and V of chunk n + 2 on their way into L2: from there they arrive in time
-            ahead(x.u.v, x);
-        }
+        if (!x.more) return;
+        next = place(x);   // chunk n + 1: its keys and values once chunk n - 1 is done
+        if (n > 0 && !mbar_wait_asleep(&sm.all[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1))) break;
+        tile(sm.K[(n + 1) & 1], next.k, next, &sm.full_k[(n + 1) & 1]);
+        tile(sm.V[(n + 1) & 1], next.v, next, &sm.full_v[(n + 1) & 1]);
+        if (!state_only) ahead(next.q, next);   // on their way into L2: from there they arrive in time
+        if (!mbar_wait_asleep(&sm.qs, (uint32_t)(n & 1))) break;
+        q_tile(next);
     }
+    raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
 // --- MMAs, one thread. TMEM: scores and, in one half of their columns (two to a column), their bf16 copy,
@@ -335,22 +326,22 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, u
 __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     constexpr uint32_t kk = idesc_bf16(128, 128, 0, 0), kn = idesc_bf16(128, 128, 0, 1);
-    const uint64_t dk = desc_kmajor(smem_u32(sm.K), LC, 0), ds = desc_mnmajor_bf16(smem_u32(sm.S), LC, 0);
-    const uint64_t dq0 = desc_kmajor(smem_u32(sm.Q[0]), LC, 0), dv0 = desc_mnmajor_bf16(smem_u32(sm.V[0]), LC, 0);
+    const uint64_t dk0 = desc_kmajor(smem_u32(sm.K[0]), LC, 0), ds = desc_mnmajor_bf16(smem_u32(sm.S), LC, 0);
+    const uint64_t q = desc_kmajor(smem_u32(sm.Q), LC, 0), dv0 = desc_mnmajor_bf16(smem_u32(sm.V[0]), LC, 0);
     bool ok = true;
     int n = 0, lows = 0;
     At x;
     x.first(a, units);
     auto score = [&](int m) {   // scores of chunk m
-        if (!mbar_wait_asleep(&sm.full_k, (uint32_t)(m & 1)) || !mbar_wait_asleep(&sm.full_q[m & 1], (uint32_t)((m >> 1) & 1))) return false;
-        if (!state_only) product_ss<false>(tm + kColP, dq0 + (uint64_t)((m & 1) * (kTile / 16)), dk, kk);
+        if (!mbar_wait_asleep(&sm.full_k[m & 1], (uint32_t)((m >> 1) & 1)) || !mbar_wait_asleep(&sm.full_q, (uint32_t)(m & 1))) return false;
+        if (!state_only) product_ss<false>(tm + kColP, q, dk0 + (uint64_t)((m & 1) * (kTile / 16)), kk);
         umma_commit(&sm.qk);
         return true;
     };
     if (x.more) ok = score(0);
     for (; ok && x.more; ++n) {
         const uint32_t ph = (uint32_t)(n & 1);
-        const uint64_t q = dq0 + (uint64_t)(ph * (kTile / 16)), v = dv0 + (uint64_t)(ph * (kTile / 16));
+        const uint64_t v = dv0 + (uint64_t)(ph * (kTile / 16));
         const bool carried = x.c > 0 || x.u.s_in, sum = x.c + 1 < x.chunks || x.u.s_out, three = sum && three_parts(x.u, x.c);
         if (!(ok = mbar_wait_asleep(&sm.s, ph) && (n == 0 || mbar_wait_asleep(&sm.r, ph ^ 1u)))) break;
         tc_fence_after();
@@ -376,6 +367,7 @@ __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units
             product_ts<true>(tm + kColDS, tm + low_col(x.u.rev), v, kn);
             umma_commit(&sm.ds);
         }
+        umma_commit(&sm.all[n & 1]);
         x.next(a, units);
         // the next chunk's scores now: they and their decays need no state
         if (x.more) ok = score(n + 1);
@@ -547,7 +539,7 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
     // decayed keys: this warp's channels 32 warp + .., tokens 64 half + ..; ldmatrix row of this thread
     const int jl = 64 * half + 8 * (lane >> 4) + (lane & 7), cl = 4 * warp + ((lane >> 3) & 1);
     const int jr = 64 * half + 2 * (lane & 3);     // first token of its fragment register 0
-    const uint32_t key = smem_u32(sm.K);
+    const uint32_t key0 = smem_u32(sm.K[0]);
     bool ok = true;
     int n = 0;
     f32x2 s[32];                                   // S[v][row], v = 64 half + ..
@@ -596,19 +588,19 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             // 32 tokens x 16 channels of K, the g-th of this warp's four blocks
             auto fragments = [&](int g, uint32_t (&x)[8]) {
                 const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
-                ldmatrix4_trans(key + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
-                ldmatrix4_trans(key + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
+                ldmatrix4_trans(key0 + (uint32_t)(n & 1) * kTile + panel_off_bf16(j, cc, LC), x[0], x[1], x[2], x[3]);
+                ldmatrix4_trans(key0 + (uint32_t)(n & 1) * kTile + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
             };
             auto place = [&](int g) { return lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1); };
             // where a thread's low parts of block g wait: the block's own bytes of K, which nothing else reads
             // once it is in fragments and the scores are done
             auto wait_place = [&](int g, int e) {
-                return sm.K + panel_off_bf16(64 * half + 32 * (g >> 1) + lane, 4 * warp + 2 * (g & 1) + e, LC);
+                return sm.K[n & 1] + panel_off_bf16(64 * half + 32 * (g >> 1) + lane, 4 * warp + 2 * (g & 1) + e, LC);
             };
             if (c < chunks) {
                 // decayed keys, transposed to [channel][token], to tensor memory: first, while the scores and
                 // outputs of chunk c - 1 leave shared memory read cycles
-                if (!(ok = wait_warp(&sm.full_k, n))) break;
+                if (!(ok = wait_warp(&sm.full_k[n & 1], n >> 1))) break;
                 const Chunk k = chunk_of(u, c);
                 const bool whole = k.hi - k.lo == LC;
                 if (!whole) {   // rows of a neighbour in V: their scores are zero, and zero times an infinity is not
@@ -675,7 +667,6 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                 tmem_wait_st_all();
                 tc_fence_before();
                 mbar_arrive(&sm.piece);
-                if (!three) mbar_arrive(&sm.k_free);
             }
             if (c > 0 && (c < chunks || u.s_out)) {   // the state after chunk c - 1
                 const float w = c < chunks ? whole_decay : decay_pow(u.g, u.len - (c - 1) * LC);
@@ -731,7 +722,6 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
                 tmem_wait_st_all();
                 tc_fence_before();
                 fence_async_smem();   // K's next tile comes by TMA
-                mbar_arrive(&sm.k_free);
                 mbar_arrive(&sm.low);
             }
             ++n;
@@ -766,10 +756,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        uint64_t* const one[] = {&sm.full_k, &sm.full_q[0], &sm.full_q[1], &sm.full_v[0], &sm.full_v[1],
+        uint64_t* const one[] = {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_v[0], &sm.full_v[1], &sm.all[0], &sm.all[1],
                                  &sm.qk, &sm.qs, &sm.ds, &sm.pv, &sm.end};
         for (uint64_t* bar : one) mbar_init(bar, 1);
-        uint64_t* const all_main[] = {&sm.s, &sm.piece, &sm.low, &sm.k_free, &sm.o};
+        uint64_t* const all_main[] = {&sm.s, &sm.piece, &sm.low, &sm.o};
         for (uint64_t* bar : all_main) mbar_init(bar, 32 * kMainWarps);
         mbar_init(&sm.p, 32 * kScoreWarps);
         mbar_init(&sm.r, 32 * kScoreWarps);
