@@ -10,6 +10,8 @@
 // whether the decay of a token applies before or after its read:
 //   forward   S <- gamma S + v k^T,         out = S q
 //   reversed  S <- S + v k^T,  out = S q,   S <- gamma S
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cuda.h>
@@ -61,9 +63,10 @@ struct LinArgs {
     int jobs;
     int state_only;              // the segments' own states to seg, nothing else
     int first;                   // the first kernel of the call on this workspace: clears its status word
-    const Slot* table;           // packed: slots and their number, written by linattn_table_kernel
+    Slot* table;                 // packed: slots and their number, written by linattn_table_kernel, or
     const int* slots_dev;
-    int slots;                   // fixed length: nseg segments of seg_len tokens per sequence
+    const int64_t* cu;           // the offsets of few whole sequences, from which each block writes the slot of its unit
+    int slots;                   // fixed length: nseg segments of seg_len tokens per sequence; with cu: N
     int nseg;
     int64_t seg_len, T;
     const float* log_decay;
@@ -140,7 +143,7 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     }
     return x;
 }
-__device__ __forceinline__ int units_of(const LinArgs& a) { return (a.table ? *a.slots_dev : a.slots) * a.H * a.jobs; }
+__device__ __forceinline__ int units_of(const LinArgs& a) { return (a.slots_dev ? *a.slots_dev : a.slots) * a.H * a.jobs; }
 // the units of a CTA: every round of gridDim.x units in turn from the other end, so that with slots in
 // order of falling length no CTA gets the longer one each time
 __device__ __forceinline__ int unit_at(int round) {
@@ -739,13 +742,29 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
     if (!ok && lane == 0) raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
+// Few sequences, one unit a block at most: each block checks the offsets itself (cu[0] = 0, non-decreasing,
+// cu[N] = T) and writes the slot it reads; blocks of one sequence write the same values. (A kernel of its own
+// for it takes 5 us, against 15 for lengths 17, 33, 65 with 4 heads.)
+__device__ __forceinline__ bool own_slot(const LinArgs& a) {
+    const int N = a.slots, n = threadIdx.x;
+    bool bad = false;
+    if (n < N) {
+        const int64_t from = a.cu[n], to = a.cu[n + 1];
+        bad = to < from || (n == 0 && from != 0) || (n == N - 1 && to != a.T);
+        if (n == (int)blockIdx.x / (a.jobs * a.H)) a.table[n] = Slot{from, (int32_t)(to - from), n, 0, 1, 0, 0};
+    }
+    return !__syncthreads_or(bad);
+}
+
 __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_constant__ LinArgs a) {
     extern __shared__ uint8_t smem_raw[];
     LinSmem& sm = *reinterpret_cast<LinSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // A fixed-length call's first kernel clears the status word here, long before any wait of
-    // another CTA can give up (2 s) and write to it.
+    // A call's first kernel sets the status word here, long before any wait of another CTA can give up
+    // (2 s) and write to it.
     if (a.first) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int*>(a.ws) = 0;
+        const bool bad = a.cu && !own_slot(a);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int*>(a.ws) = bad ? KDA_ERR_OFFSETS : 0;
+        if (bad) return;
     } else if (read_status(a.ws) != 0) {
         return;
     }
@@ -793,43 +812,45 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
 __global__ void __launch_bounds__(256) linattn_carry_kernel(const __grid_constant__ LinArgs a) {
     if (read_status(a.ws) != 0) return;
     const LinJob& j = a.job[blockIdx.z];
-    const int i = blockIdx.x / 16, h = blockIdx.y, e = ((blockIdx.x & 15) * 256 + threadIdx.x) * 4;
-    const int slots = a.table ? *a.slots_dev : a.slots;
-    if (i >= slots) return;
-    const Slot s = slot_of(a, i);
-    if (s.seg != 0 || s.nseg == 1) return;
+    const int h = blockIdx.y, e = ((blockIdx.x & 15) * 256 + threadIdx.x) * 4;
+    const int slots = a.slots_dev ? *a.slots_dev : a.slots;
     const float g = a.log_decay[h];
-    const size_t seq = ((size_t)s.seq * a.H + h) * D * D;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (j.s_in) {
-        if (j.s_in_t) {
-            const int r = e / D, c = e % D;
-            x = make_float4(j.s_in[seq + c * D + r], j.s_in[seq + (c + 1) * D + r], j.s_in[seq + (c + 2) * D + r],
-                            j.s_in[seq + (c + 3) * D + r]);
-        } else {
-            x = *reinterpret_cast<const float4*>(j.s_in + seq + e);
-        }
-        const float over = 1.0f / j.s_scale;
-        x.x *= over; x.y *= over; x.z *= over; x.w *= over;
-    }
-    // segments in the job's order, eight loads in flight; all but the last in time have seg_len tokens
-    const int64_t step = (j.rev ? -1 : 1) * (int64_t)a.H * D * D;
-    float* p = j.seg + ((size_t)(j.rev ? i + s.nseg - 1 : i) * a.H + h) * D * D + e;
-    const float whole = expf(g * (float)a.seg_len), last = expf(g * (float)(s.after - (int64_t)(s.nseg - 2) * a.seg_len));
-    for (int k0 = 0; k0 < s.nseg; k0 += 8, p += 8 * step) {
-        float4 y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)   // the sum of the last segment in order is not there and not needed
-            if (k0 + k + 1 < s.nseg) y[k] = *reinterpret_cast<const float4*>(p + k * step);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k0 + k < s.nseg) {
-                *reinterpret_cast<float4*>(p + k * step) = x;
-                if (k0 + k + 1 < s.nseg) {
-                    const float w = j.rev && k0 + k == 0 ? last : whole;
-                    x = make_float4(w * x.x + y[k].x, w * x.y + y[k].y, w * x.z + y[k].z, w * x.w + y[k].w);
-                }
+    for (int i = blockIdx.x / 16; i < slots; i += gridDim.x / 16) {
+        const Slot s = slot_of(a, i);
+        if (s.nseg == 1) return;   // sequences of several segments come first
+        if (s.seg != 0) continue;
+        const size_t seq = ((size_t)s.seq * a.H + h) * D * D;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j.s_in) {
+            if (j.s_in_t) {
+                const int r = e / D, c = e % D;
+                x = make_float4(j.s_in[seq + c * D + r], j.s_in[seq + (c + 1) * D + r], j.s_in[seq + (c + 2) * D + r],
+                                j.s_in[seq + (c + 3) * D + r]);
+            } else {
+                x = *reinterpret_cast<const float4*>(j.s_in + seq + e);
             }
+            const float over = 1.0f / j.s_scale;
+            x.x *= over; x.y *= over; x.z *= over; x.w *= over;
+        }
+        // segments in the job's order, eight loads in flight; all but the last in time have seg_len tokens
+        const int64_t step = (j.rev ? -1 : 1) * (int64_t)a.H * D * D;
+        float* p = j.seg + ((size_t)(j.rev ? i + s.nseg - 1 : i) * a.H + h) * D * D + e;
+        const float whole = expf(g * (float)a.seg_len), last = expf(g * (float)(s.after - (int64_t)(s.nseg - 2) * a.seg_len));
+        for (int k0 = 0; k0 < s.nseg; k0 += 8, p += 8 * step) {
+            float4 y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)   // the sum of the last segment in order is not there and not needed
+                if (k0 + k + 1 < s.nseg) y[k] = *reinterpret_cast<const float4*>(p + k * step);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k0 + k < s.nseg) {
+                    *reinterpret_cast<float4*>(p + k * step) = x;
+                    if (k0 + k + 1 < s.nseg) {
+                        const float w = j.rev && k0 + k == 0 ? last : whole;
+                        x = make_float4(w * x.x + y[k].x, w * x.y + y[k].y, w * x.z + y[k].z, w * x.w + y[k].w);
+                    }
+                }
+        }
     }
 }
 
@@ -856,29 +877,37 @@ __global__ void __launch_bounds__(1024)
         }
         return;
     }
-    for (int b = 0; b < N; b += blockDim.x) {
-        const int n = b + tid;
-        const int64_t t0 = n < N ? cu[n] : 0, len = n < N ? cu[n + 1] - t0 : 0;
-        const int cnt = n < N ? (len > 0 ? (int)((len + seg_len - 1) / seg_len) : 1) : 0;
-        scan[tid] = cnt;
-        __syncthreads();
-        for (int o = 1; o < (int)blockDim.x; o <<= 1) {
-            const int x = tid >= o ? scan[tid - o] : 0;
-            __syncthreads();
-            scan[tid] += x;
-            __syncthreads();
-        }
-        const int first = carry + scan[tid] - cnt;
-        for (int k = 0; k < cnt; ++k) {
-            const int64_t left = len - k * seg_len;
-            if (first + k < slots_max) {
-                const int32_t m = (int32_t)(left < seg_len ? left : seg_len);
-                table[first + k] = Slot{t0 + k * seg_len, m, n, k, cnt, (int32_t)(k * seg_len), (int32_t)(left - m)};
+    // sequences of several segments first, so that the states of segments take up the first places
+    const int warp = tid >> 5, lane = tid & 31;
+    for (int pass = seg_len < T_total ? 0 : 1; pass < 2; ++pass) {
+        for (int b = 0; b < N; b += blockDim.x) {
+            const int n = b + tid;
+            const int64_t t0 = n < N ? cu[n] : 0, len = n < N ? cu[n + 1] - t0 : 0;
+            const int cnt = n < N && (len > seg_len) == (pass == 0) ? (len > 0 ? (int)((len + seg_len - 1) / seg_len) : 1) : 0;
+            int before = cnt;   // sums of the warp, then of the warps before it
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += x;
             }
+            if (lane == 31) scan[warp] = before;
+            __syncthreads();
+            int first = carry + before - cnt, sum = 0;
+            for (int w = 0; w < 32; ++w) {
+                if (w == warp) first += sum;
+                sum += scan[w];
+            }
+            for (int k = 0; k < cnt; ++k) {
+                const int64_t left = len - k * seg_len;
+                if (first + k < slots_max) {
+                    const int32_t m = (int32_t)(left < seg_len ? left : seg_len);
+                    table[first + k] = Slot{t0 + k * seg_len, m, n, k, cnt, (int32_t)(k * seg_len), (int32_t)(left - m)};
+                }
+            }
+            __syncthreads();
+            if (tid == 0) carry += sum;
+            __syncthreads();
         }
-        __syncthreads();
-        if (tid == blockDim.x - 1) carry += scan[tid];
-        __syncthreads();
     }
     if (tid == 0) {
         *slots = carry;
@@ -993,6 +1022,7 @@ struct Plan {
     int64_t seg_len;   // tokens, a multiple of the chunk
     int nseg;          // segments of a fixed-length sequence (packed: of T_total tokens at most)
     int slots;         // fixed: slots; packed: most slots
+    int kept;          // the first of them, whose states are kept in the workspace
 };
 Plan plan_of(const kda_linattn_shape* sh, bool packed, int jobs) {
     const int64_t chunks = (sh->T + LC - 1) / LC;
@@ -1011,6 +1041,8 @@ Plan plan_of(const kda_linattn_shape* sh, bool packed, int jobs) {
     if (p.seg_len < LC) p.seg_len = LC;
     p.nseg = (int)(chunks > 0 ? (sh->T + p.seg_len - 1) / p.seg_len : 1);
     p.slots = packed ? (int)(sh->N + sh->T / p.seg_len) : (int)(sh->B * p.nseg);
+    // of those, segments of sequences of several: no more than 2 (length / seg_len), rounded down, of each sequence
+    p.kept = p.nseg == 1 ? 0 : packed ? (int)std::min<int64_t>(p.slots, 2 * (sh->T / p.seg_len)) : p.slots;
     return p;
 }
 
@@ -1024,7 +1056,7 @@ LinLayout layout_of(const kda_linattn_shape* sh, bool packed, bool backward) {
     l.plan = p;
     size_t o = 1024;   // the status word, at byte 64 the number of slots
     l.table = o; o += packed ? align_up((size_t)p.slots * sizeof(Slot), 1024) : 0;
-    const size_t states = p.nseg > 1 ? (size_t)p.slots * sh->H * D * D * sizeof(float) : 0;
+    const size_t states = (size_t)p.kept * sh->H * D * D * sizeof(float);
     l.seg[0] = o; o += states;
     l.seg[1] = o; o += backward ? states : 0;
     const size_t share = backward && groups_of(sh) > 1 ? align_up((size_t)(sh->B * sh->T * sh->H) * D * sizeof(float), 1024) : 0;
@@ -1079,7 +1111,14 @@ kda_status make_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t hea
 kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (&tensors)[4], int jobs, const int64_t* cu, const float* log_decay, uint8_t* ws,
                     const LinLayout& lay, cudaStream_t s) {
     const Plan p = lay.plan;
-    const cudaError_t e = cudaFuncSetAttribute(linattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
+    static std::atomic<uint64_t> allowed{0};   // devices on which the kernel may use its shared memory
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (e == cudaSuccess && !(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(linattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
+        if (e == cudaSuccess && device < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) {
         set_last_error_text(cudaGetErrorString(e));
         return KDA_ERR_CUDA;
@@ -1107,8 +1146,12 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
         a.job[i].seg = reinterpret_cast<float*>(ws + lay.seg[i > 0]);
         a.job[i].seg_t = i == 1;
     }
-    if (cu) {
-        Slot* const table = reinterpret_cast<Slot*>(ws + lay.table);
+    Slot* const table = reinterpret_cast<Slot*>(ws + lay.table);
+    if (cu && p.nseg == 1 && sh->N * sh->H * jobs <= kSMs) {
+        a.cu = cu;
+        a.table = table;
+        a.slots = (int)sh->N;
+    } else if (cu) {
         int* const slots = reinterpret_cast<int*>(ws + 64);
         linattn_table_kernel<<<1, 1024, 0, s>>>(cu, (int)sh->N, sh->T, p.seg_len, p.slots, table, slots, ws);
         a.table = table;
@@ -1116,7 +1159,7 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
         a.first = 0;
     }
     auto launch = [&](const LinArgs& x) {
-        const int64_t units = (int64_t)p.slots * sh->H * x.jobs;
+        const int64_t units = (int64_t)x.slots * sh->H * x.jobs;
         linattn_kernel<<<(unsigned)(units < kSMs ? units : kSMs), kLinThreads, sizeof(LinSmem) + 1024, s>>>(x);
     };
     if (p.nseg > 1) {
@@ -1125,7 +1168,7 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
         if (jobs > 1) { b.jobs = 2; b.job[1] = a.job[2]; }
         launch(b);
         b.first = a.first = 0;
-        linattn_carry_kernel<<<dim3((unsigned)p.slots * 16, (unsigned)sh->H, (unsigned)b.jobs), 256, 0, s>>>(b);
+        linattn_carry_kernel<<<dim3((unsigned)std::min(p.slots, 64) * 16, (unsigned)sh->H, (unsigned)b.jobs), 256, 0, s>>>(b);
     }
     if (p.slots > 0) launch(a);
     return KDA_OK;

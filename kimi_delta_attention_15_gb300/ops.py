@@ -8,6 +8,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -323,8 +324,15 @@ def _ready(specs):
     return dev
 
 
-def _raw_stream(stream, dev):
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+def _on_stream(call):
+    """A call with `stream` runs with it as the current one, so that what it allocates is the stream's."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on
 
 
 def _address(t):
@@ -354,6 +362,7 @@ def linattn_alloc_workspace(shape: LinattnShape, device, backward: bool = False)
 _BF, _F32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.uint8
 
 
+@_on_stream
 def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, B: int = 1, scale: float = SCALE, workspace=None,
                 o=None, hT=None, want_hT: bool = True, stream=None):
     """kda_linattn_fwd: S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t. Token tensors
@@ -385,12 +394,13 @@ def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, B: int = 1, sca
         hT = torch.empty((N, H, 128, 128), dtype=_F32, device=q.device)
     code = lib.kda_linattn_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                _address(h0), _address(cu_seqlens), o.data_ptr(), _address(hT), workspace.data_ptr(),
-                               workspace.numel(), _raw_stream(stream, dev))
+                               workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if code:
         _check(code, "kda_linattn_fwd")
     return o, hT, workspace
 
 
+@_on_stream
 def linattn_bwd(q, k, v, log_decay, do, workspace=None, h0=None, cu_seqlens=None, dhT=None, *, B: int = 1,
                 scale: float = SCALE, grads=None, want_dh0: bool = True, stream=None):
     """kda_linattn_bwd: gradients of sum <o, do> + <hT, dhT>. It recomputes what it needs, so any
@@ -423,12 +433,13 @@ def linattn_bwd(q, k, v, log_decay, do, workspace=None, h0=None, cu_seqlens=None
     code = lib.kda_linattn_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                _address(h0), _address(cu_seqlens), do.data_ptr(), _address(dhT), grads["dq"].data_ptr(),
                                grads["dk"].data_ptr(), grads["dv"].data_ptr(), _address(grads.get("dh0")),
-                               workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+                               workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if code:
         _check(code, "kda_linattn_bwd")
     return grads
 
 
+@_on_stream
 def linattn_decode(q, k, v, log_decay, state, *, o=None, scale: float = SCALE, stream=None):
     """kda_linattn_decode: one token per request. v [n_req, H, 128] bf16, q, k [n_req, H / groups, 128]
     bf16; `state` [n_req, H, 128, 128] fp32 is updated in place. Returns o [n_req, H, 128] bf16."""
@@ -446,7 +457,7 @@ def linattn_decode(q, k, v, log_decay, state, *, o=None, scale: float = SCALE, s
     if o is None:
         o = torch.empty_like(v)
     code = lib.kda_linattn_decode(n_req, H, H // Hqk, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                  state.data_ptr(), o.data_ptr(), _raw_stream(stream, dev))
+                                  state.data_ptr(), o.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
     if code:
         _check(code, "kda_linattn_decode")
     return o
@@ -464,6 +475,7 @@ def _norm_size(x):
     return n, n // width, width
 
 
+@_on_stream
 def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, mean=None, rstd=None, stream=None):
     """kda_layernorm_fwd over the last dimension. x bf16 or fp32, weight and bias [width] fp32 or
     None. Returns (y, mean, rstd); mean and rstd [rows] fp32 are what layernorm_bwd reads."""
@@ -489,12 +501,13 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, mean=
     if rstd is None:
         rstd = torch.empty(rows, dtype=_F32, device=x.device)
     code = lib.kda_layernorm_fwd(rows, width, _NORM_DTYPES[dtype], eps, x.data_ptr(), _address(weight), _address(bias),
-                                 y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev))
+                                 y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
     if code:
         _check(code, "kda_layernorm_fwd")
     return y, mean, rstd
 
 
+@_on_stream
 def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool = True, want_dbias: bool = True,
                   workspace=None, stream=None):
     """kda_layernorm_bwd with the mean and rstd of layernorm_fwd (weight None reads as 1). Returns a
@@ -520,7 +533,7 @@ def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool =
     dweight, dbias = grads.get("dweight"), grads.get("dbias")
     code = lib.kda_layernorm_bwd(rows, width, _NORM_DTYPES[dtype], x.data_ptr(), dy.data_ptr(), _address(weight),
                                  mean.data_ptr(), rstd.data_ptr(), grads["dx"].data_ptr(), _address(dweight),
-                                 _address(dbias), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+                                 _address(dbias), workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if code:
         _check(code, "kda_layernorm_bwd")
     return grads

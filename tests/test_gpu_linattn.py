@@ -234,6 +234,45 @@ def test_malformed_offsets_set_the_device_status(bad):
     check_all(good, run(good))
 
 
+@pytest.mark.parametrize("N,H,lens", [(160, 1, (100,)), (3, 1, (4000,)), (1100, 1, (1500,))])
+def test_malformed_offsets_of_many_or_long_sequences(N, H, lens):
+    """The same where a kernel of its own lists the sequences: many of them, or long ones that are split."""
+    T = N - 1 + lens[0]
+    x = torch.ones(T, H, 128, dtype=torch.bfloat16, device="cuda")
+    log_decay = torch.full((H,), -0.1, device="cuda")
+    cu = torch.tensor(list(range(N)) + [T], dtype=torch.int64)
+    for at, value in ((0, 1), (N // 2, T + 1), (N, T - 1)):
+        bad = cu.clone()
+        bad[at] = value
+        o, hT = torch.full_like(x, 7.0), torch.full((N, H, 128, 128), 7.0, device="cuda")
+        _, _, ws = ops.linattn_fwd(x, x, x, log_decay, cu_seqlens=bad.cuda(), o=o, hT=hT)
+        assert ops.device_status(ws) == 6
+        assert (o == 7.0).all() and (hT == 7.0).all()
+
+
+def test_many_short_sequences_beside_long_ones():
+    """More sequences than the listing kernel takes at a time; the long ones are split, among the others."""
+    lens = [2, 0, 1] * 380
+    lens[5], lens[700], lens[-1] = 1900, 2300, 1500
+    d = O.make(tuple(lens), 1, seed=21, h0=True, dhT=True)
+    check_all(d, run(d))
+
+
+def test_calls_given_a_stream():
+    """`stream`: the call's own tensors belong to it too, so that their memory is not handed out while it runs."""
+    d = O.make((300, 45), 4, 2, seed=22, h0=True, dhT=True)
+    a, c, side = run(d), dev(d), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    args = (c["q"], c["k"], c["v"], c["log_decay"])
+    for _ in range(20):
+        b = ops.linattn_bwd(*args, c["do"], h0=c["h0"], cu_seqlens=c["cu_seqlens"], dhT=c["dhT"], stream=side)
+        o, hT, ws = ops.linattn_fwd(*args, h0=c["h0"], cu_seqlens=c["cu_seqlens"], stream=side)
+        torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")      # what the current stream allocates meanwhile
+    side.synchronize()
+    for k, x in dict(o=o, hT=hT, **b).items():
+        assert torch.equal(x, a[k]), k
+
+
 def test_gradient_against_differences_of_the_loss():
     """<gradient, step> against the central difference of the 64-bit loss along the step: bf16 gradients
     carry at most u each, and n independent errors add up to that times |grad| |step| / sqrt(n)

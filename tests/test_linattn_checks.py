@@ -66,6 +66,13 @@ def test_linattn_workspace_size(lib):
     assert ops.linattn_workspace_size(ops.linattn_shape(1000, 8, 1, groups=3)) == 0
 
 
+def test_workspace_of_many_sequences(lib):
+    """Only segments of sequences of several keep states (64 KB each): with n segments' length of tokens between n and
+    2 n of them, whatever the number of sequences."""
+    few, many = (ops.linattn_workspace_size(ops.linattn_shape(100000, 4, n), True) for n in (10, 65535))
+    assert many <= 2 * few + 65535 * 64
+
+
 def test_linattn_decode_status_codes(lib):
     def call(n=2, H=3, groups=1, scale=0.1, ptr=16, bad=None):
         p = [ctypes.c_void_p(ptr) for _ in range(6)]
