@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, V * NV <= 8 ? 4 : 2)
                            const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                            float* __restrict__ part, int64_t rows, int width, int units, int lpr) {
     extern __shared__ float acc[];   // [warps][2][width]
+    grid_launch_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), first = (int64_t)blockIdx.x * (kThreads / 32) + warp;
     const float inv = 1.0f / (float)width;
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(512)
                          const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                          float* __restrict__ part, int64_t rows, int width, int units, int pitch, int stages) {
     constexpr int R = bwd_rows(NV * V, V > 1);
+    grid_launch_next();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float2 buf[2][R][32];
     const Rows<R> m = rows_of<R>(smem, (size_t)width * sizeof(T), rows, pitch, 2);
@@ -642,6 +644,7 @@ __global__ void __launch_bounds__(kThreads)
 // then the groups in order.
 __global__ void __launch_bounds__(1024)
     norm_reduce_kernel(const float* __restrict__ part, int n, int width, float* __restrict__ dw, float* __restrict__ db) {
+    grid_wait_before();
     __shared__ float s[32][33];
     float* const out = blockIdx.y ? db : dw;
     if (!out) return;
@@ -889,7 +892,7 @@ extern "C" kda_status kda_layernorm_bwd(long long rows, long long width, int dty
         if (st != KDA_OK) return st;
     }
     if (sums)
-        norm_reduce_kernel<<<dim3((unsigned)((width + 31) / 32), 2), dim3(32, 32), 0, s>>>(static_cast<const float*>(workspace),
-                                                                                          parts, (int)width, dweight, dbias);
+        launch_kernel(norm_reduce_kernel, dim3((unsigned)((width + 31) / 32), 2), dim3(32, 32), 0, s, parts > 0,
+                      static_cast<const float*>(workspace), parts, (int)width, dweight, dbias);
     return launched("kda_layernorm_bwd launch");
 }
