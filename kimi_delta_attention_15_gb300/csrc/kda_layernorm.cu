@@ -9,8 +9,10 @@
 //  - wide (up to 16384 columns): persistent blocks, a row at a time, rows arriving in shared memory
 //    by bulk copies some rows ahead;
 //  - beyond: a block for each row that reads it again for every step.
-// A unit is 16 bytes where the width is a multiple of it, a single element otherwise (bulk copies
-// then bring the aligned span around the row, and elements are read one by one from shared memory).
+// A unit is 16 aligned bytes. Where the width is no multiple of it, rows start inside a unit, each at one of
+// eight (bf16) or four (fp32) places; a thread meets only rows that start at the same place, so that its columns
+// stay its own, and its first and last unit of a row hold elements of the neighbours, which do not count.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include "kda_internal.cuh"
@@ -23,17 +25,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSMs = 152;
 constexpr int kWideMost = 16384;       // columns of the wide form
-constexpr int kNarrowUnits = 64;       // units of the narrow form with 16-byte units
-constexpr int kNarrowColumns = 512;    // and with single elements
+constexpr int kNarrowUnits = 64;       // units of the narrow form
 
 __device__ __forceinline__ float get(const uint16_t* p) { return bf2f(*p); }
 __device__ __forceinline__ float get(const float* p) { return *p; }
 __device__ __forceinline__ void put(uint16_t* p, float x) { *p = f2bf(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 
-// A unit in registers as it is stored, and as fp32.
-template <typename T, int V> struct Unit;
-template <> struct Unit<uint16_t, 8> {
+// A unit, 16 bytes, in registers as it is stored, and as fp32.
+template <typename T> struct Unit;
+template <> struct Unit<uint16_t> {
+    static constexpr int V = 8;
     uint4 r;
     __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void load_stream(const uint16_t* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
@@ -41,6 +43,18 @@ template <> struct Unit<uint16_t, 8> {
     __device__ __forceinline__ float at(int i) const {
         const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
         return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    __device__ __forceinline__ void keep(uint32_t ok) {   // the elements of these bits, zero elsewhere
+        r.x &= ((ok & 1u) ? 0xffffu : 0u) | ((ok & 2u) ? 0xffff0000u : 0u);
+        r.y &= ((ok & 4u) ? 0xffffu : 0u) | ((ok & 8u) ? 0xffff0000u : 0u);
+        r.z &= ((ok & 16u) ? 0xffffu : 0u) | ((ok & 32u) ? 0xffff0000u : 0u);
+        r.w &= ((ok & 64u) ? 0xffffu : 0u) | ((ok & 128u) ? 0xffff0000u : 0u);
+    }
+    __device__ __forceinline__ void load_some(const uint16_t* p, uint32_t ok) {
+        uint32_t e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = (ok >> i) & 1u ? p[i] : 0u;
+        r = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
     }
     __device__ static __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
         uint32_t w[4];
@@ -51,157 +65,262 @@ template <> struct Unit<uint16_t, 8> {
         }
         __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
     }
+    // the first or last elements of a unit (ok) in as few stores as their number has bits, others one by one
+    __device__ static __forceinline__ void store_some(uint16_t* p, const float (&f)[8], uint32_t ok) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if ((ok & 15u) == 15u) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        if ((ok >> 4) == 15u) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
+        const bool upper = (ok & 15u) == 0u || (ok & 15u) == 15u;    // the half that is not done
+        const uint32_t a = upper ? w[2] : w[0], b = upper ? w[3] : w[1], r = upper ? ok >> 4 : ok & 15u;
+        if (!upper && ok >> 4 && ok >> 4 != 15u) {                   // a row inside a unit
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((ok >> (4 + i)) & 1u) put(p + 4 + i, f[4 + i]);
+        }
+        if (r == 15u) return;
+        uint16_t* const h = p + (upper ? 4 : 0);
+        if ((r & 3u) == 3u) *reinterpret_cast<uint32_t*>(h) = a;
+        if ((r & 12u) == 12u) *reinterpret_cast<uint32_t*>(h + 2) = b;
+        if ((r & 3u) == 1u) h[0] = (uint16_t)a;
+        if ((r & 3u) == 2u) h[1] = (uint16_t)(a >> 16);
+        if ((r & 12u) == 4u) h[2] = (uint16_t)b;
+        if ((r & 12u) == 8u) h[3] = (uint16_t)(b >> 16);
+    }
 };
-template <> struct Unit<float, 4> {
+template <> struct Unit<float> {
+    static constexpr int V = 4;
     float4 r;
     __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void load_stream(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void zero() { r = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ float at(int i) const { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
+    __device__ __forceinline__ void keep(uint32_t ok) {
+        r = make_float4((ok & 1u) ? r.x : 0.0f, (ok & 2u) ? r.y : 0.0f, (ok & 4u) ? r.z : 0.0f, (ok & 8u) ? r.w : 0.0f);
+    }
+    __device__ __forceinline__ void load_some(const float* p, uint32_t ok) {
+        r = make_float4((ok & 1u) ? p[0] : 0.0f, (ok & 2u) ? p[1] : 0.0f, (ok & 4u) ? p[2] : 0.0f, (ok & 8u) ? p[3] : 0.0f);
+    }
     __device__ static __forceinline__ void store(float* p, const float (&f)[4]) {
         __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
     }
-};
-template <typename T> struct Unit<T, 1> {
-    float r;
-    __device__ __forceinline__ void load(const T* p) { r = get(p); }
-    __device__ __forceinline__ void load_stream(const T* p) { r = get(p); }
-    __device__ __forceinline__ void zero() { r = 0.0f; }
-    __device__ __forceinline__ float at(int) const { return r; }
-    __device__ static __forceinline__ void store(T* p, const float (&f)[1]) { put(p, f[0]); }
-};
-// the parameters of a unit's columns, `other` without one
-template <int V>
-__device__ __forceinline__ void params(const float* p, int c, float other, float (&f)[V]) {
-    if (!p) {
+    __device__ static __forceinline__ void store_some(float* p, const float (&f)[4], uint32_t ok) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = other;
-    } else if constexpr (V == 1) {
-        f[0] = __ldg(p + c);
-    } else {
+        for (int i = 0; i < 4; ++i)
+            if ((ok >> i) & 1u) p[i] = f[i];
+    }
+};
+
+// The columns of a thread's NV units of every row it meets: units first, first + step, .. of the row, counted
+// from the aligned address at or before its start, `off` elements before it. Rows whose distance is a multiple
+// of V have the same off, and a thread meets only such rows, so that a width that is no multiple of V (kRagged)
+// differs only in the edge units: bits of `ok` say which elements of a unit are the row's.
+template <typename T, int NV, bool kRagged> struct Columns {
+    static constexpr int V = Unit<T>::V;
+    static constexpr uint32_t kAll = (1u << V) - 1u;
+    int first, step, off, units;
+    uint32_t bits[kRagged ? NV : 1];
+    __device__ __forceinline__ void init(int first_, int step_, int64_t row, int width) {
+        first = first_;
+        step = step_;
+        off = kRagged ? (int)((row * width) % V) : 0;
+        units = (off + width + V - 1) / V;
+        if constexpr (kRagged)
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p + c + i));
-            f[i] = x.x; f[i + 1] = x.y; f[i + 2] = x.z; f[i + 3] = x.w;
+            for (int k = 0; k < NV; ++k) {
+                bits[k] = 0u;
+#pragma unroll
+                for (int e = 0; e < V; ++e) bits[k] |= (unsigned)(column(k) + e) < (unsigned)width ? 1u << e : 0u;
+            }
+    }
+    __device__ __forceinline__ int unit(int k) const { return first + step * k; }
+    __device__ __forceinline__ bool in(int k) const { return unit(k) < units; }
+    __device__ __forceinline__ int column(int k) const { return unit(k) * V - off; }    // of its element 0
+    __device__ __forceinline__ uint32_t ok(int k) const { return kRagged ? bits[kRagged ? k : 0] : kAll; }
+    __device__ __forceinline__ bool whole(int k) const { return !kRagged || ok(k) == kAll; }
+    // row: element 0 of the row; left: elements from there to the tensor's end. The elements that are not the
+    // row's are still to be taken out (keep), when no more loads wait to be issued.
+    __device__ __forceinline__ void load(Unit<T>& u, int k, const T* row, int64_t left) const {
+        if (kRagged && column(k) + V > left) u.load_some(row + column(k), ok(k));
+        else u.load_stream(row + column(k));
+    }
+    __device__ __forceinline__ void keep(Unit<T>& u, int k) const {
+        if (!whole(k)) u.keep(ok(k));
+    }
+    __device__ __forceinline__ void store(T* row, int k, const float (&f)[V]) const {
+        if (whole(k)) {
+            Unit<T>::store(row + column(k), f);
+        } else {
+            Unit<T>::store_some(row + column(k), f, ok(k));
         }
     }
-}
+    // sum of (x - mu)^2 over the unit's elements that are the row's
+    __device__ __forceinline__ float squares(const Unit<T>& u, int k, float mu) const {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float d = (ok(k) >> e) & 1u ? u.at(e) - mu : 0.0f;
+            s += d * d;
+        }
+        return s;
+    }
+    // the parameters of unit k, `other` without them
+    __device__ __forceinline__ void params(const float* p, int k, float other, float (&f)[V]) const {
+        if (!p || !in(k)) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = other;
+        } else if constexpr (kRagged) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = (ok(k) >> e) & 1u ? __ldg(p + column(k) + e) : other;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(p + column(k) + e));
+                f[e] = x.x; f[e + 1] = x.y; f[e + 2] = x.z; f[e + 3] = x.w;
+            }
+        }
+    }
+};
 
 // A thread's columns are its own for all rows, so their parameters stay in registers, up to 24 columns
 // (they are as long as two or four bf16 rows: fetched for every row, 96 KB of them at a width of 12288
 // came from L2 each time and held the forward at 3.1 of 6.7 TB/s).
-template <int NV, int V> struct Params {
+template <typename T, int NV, bool kRagged> struct Params {
+    static constexpr int V = Unit<T>::V;
     static constexpr bool kept = NV * V <= 24;
     const float* p;
     float other;
     float f[kept ? NV : 1][V];
-    __device__ __forceinline__ void init(const float* from, float without, int first, int step, int units) {
+    __device__ __forceinline__ void init(const Columns<T, NV, kRagged>& c, const float* from, float without) {
         p = from;
         other = without;
         if constexpr (kept)
 #pragma unroll
-            for (int k = 0; k < NV; ++k) params<V>(first + step * k < units ? p : nullptr, (first + step * k) * V, other, f[k]);
+            for (int k = 0; k < NV; ++k) c.params(p, k, other, f[k]);
     }
-    __device__ __forceinline__ void at(int k, int i, float (&o)[V]) const {   // unit k of the thread, unit i of the row
+    __device__ __forceinline__ void at(const Columns<T, NV, kRagged>& c, int k, float (&o)[V]) const {
         if constexpr (kept)
 #pragma unroll
             for (int e = 0; e < V; ++e) o[e] = f[k][e];
-        else params<V>(p, i * V, other, o);
+        else c.params(p, k, other, o);
     }
 };
 
 // ---------------------------------------------------------------------------------- narrow
 // Lanes lpr * s .. lpr * (s + 1) - 1 of a warp hold row s of its 32 / lpr rows, lane l of them units
-// l, l + 32, .. (lpr < 32: one unit).
+// l, l + 32, .. (lpr < 32: one unit). A block has eight warps and all rows of a step lie a multiple of eight
+// apart from the step's before.
 __device__ __forceinline__ float lanes_sum(float x, int lpr) {
     for (int o = lpr >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-template <typename T, int V, int NV>
+// rows in flight and blocks on an SM of the forward, by a thread's columns (bf16: 131072 x 128 19.5 us with (2, 4), 24.5
+// with (1, 6); 32768 x 512 20.7 and 17.9; 32768 x 501 32 and 35)
+__host__ __device__ constexpr int fwd_rows(int columns, bool ragged) { return columns <= 8 || ragged ? 2 : 1; }
+template <typename T, int NV, bool kRagged>
 __global__ void __launch_bounds__(kThreads)
     norm_fwd_narrow_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
-                           float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int units, int lpr,
-                           float eps) {
+                           float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int lpr, float eps) {
+    constexpr int V = Unit<T>::V, R = fwd_rows(V * NV, kRagged);
     const int lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * rpw;
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * rpw;
     const float inv = 1.0f / (float)width;
-    Params<NV, V> pw, pb;
-    pw.init(w, 1.0f, l, 32, units);
-    pb.init(b, 0.0f, l, 32, units);
-    for (int64_t r0 = first * rpw; r0 < rows; r0 += warps * rpw) {
-        const int64_t r = r0 + sub;
-        const bool in = r < rows;
-        Unit<T, V> u[NV];
-        float s = 0.0f;
+    Columns<T, NV, kRagged> c;
+    c.init(l, 32, first + sub, width);
+    Params<T, NV, kRagged> pw, pb;
+    pw.init(c, w, 1.0f);
+    pb.init(c, b, 0.0f);
+    for (int64_t r0 = first; r0 < rows; r0 += R * step) {
+        Unit<T> u[R][NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int i = l + 32 * k;
-            if (in && i < units) u[k].load_stream(x + r * width + i * V);
-            else u[k].zero();
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = r0 + q * step + sub;
 #pragma unroll
-            for (int e = 0; e < V; ++e) s += u[k].at(e);
-        }
-        const float mu = lanes_sum(s, lpr) * inv;
-        s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (l + 32 * k < units)
-#pragma unroll
-                for (int e = 0; e < V; ++e) s += (u[k].at(e) - mu) * (u[k].at(e) - mu);
-        const float rs = rsqrtf(lanes_sum(s, lpr) * inv + eps);
-        if (!in) continue;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int i = l + 32 * k;
-            if (i < units) {
-                float wv[V], bv[V], o[V];
-                pw.at(k, i, wv);
-                pb.at(k, i, bv);
-#pragma unroll
-                for (int e = 0; e < V; ++e) o[e] = (u[k].at(e) - mu) * rs * wv[e] + bv[e];
-                Unit<T, V>::store(y + r * width + i * V, o);
+            for (int k = 0; k < NV; ++k) {
+                if (r < rows && c.in(k)) c.load(u[q][k], k, x + r * width, (rows - r) * width);
+                else u[q][k].zero();
             }
         }
-        if (l == 0) {
-            if (mean) mean[r] = mu;
-            if (rstd) rstd[r] = rs;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = r0 + q * step + sub;
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                c.keep(u[q][k], k);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s += u[q][k].at(e);
+            }
+            const float mu = lanes_sum(s, lpr) * inv;
+            s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (c.in(k)) s += c.squares(u[q][k], k, mu);
+            const float rs = rsqrtf(lanes_sum(s, lpr) * inv + eps);
+            if (r >= rows) continue;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (c.in(k)) {
+                    float wv[V], bv[V], o[V];
+                    pw.at(c, k, wv);
+                    pb.at(c, k, bv);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[e] = (u[q][k].at(e) - mu) * rs * wv[e] + bv[e];
+                    c.store(y + r * width, k, o);
+                }
+            if (l == 0) {
+                if (mean) mean[r] = mu;
+                if (rstd) rstd[r] = rs;
+            }
         }
     }
 }
 
-template <typename T, int V, int NV, int R>   // R: row groups in flight
-__global__ void __launch_bounds__(kThreads, V * NV <= 8 ? 4 : 2)
+// rows in flight and blocks on an SM of the backward (131072 x 128 bf16 27.8 us with (2, 3), 29.6 with (3, 2); 65536 x
+// 256 fp32 35 us with (3, 2), 38 with (2, 3); 32768 x 512 bf16 25 us with (2, 2), 40 with (2, 3), 33 with (1, 2))
+__host__ __device__ constexpr int bwd_narrow_rows(int nv, int columns) { return nv > 1 && columns <= 8 ? 3 : 2; }
+__host__ __device__ constexpr int bwd_narrow_blocks(int nv) { return nv == 1 ? 3 : 2; }
+template <typename T, int NV, bool kRagged>
+__global__ void __launch_bounds__(kThreads, bwd_narrow_blocks(NV))
     norm_bwd_narrow_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                            const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
-                           float* __restrict__ part, int64_t rows, int width, int units, int lpr) {
-    extern __shared__ float acc[];   // [warps][2][width]
+                           float* __restrict__ part, int64_t rows, int width, int lpr) {
+    constexpr int V = Unit<T>::V, R = bwd_narrow_rows(NV, V * NV);
+    extern __shared__ float acc[];   // [warps, or warps * rpw][2][width]
     grid_launch_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), first = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * rpw;
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * rpw;
     const float inv = 1.0f / (float)width;
+    Columns<T, NV, kRagged> c;
+    c.init(l, 32, first + sub, width);
     float wv[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        params<V>(w, l + 32 * k < units ? (l + 32 * k) * V : 0, 1.0f, wv[k]);
+        c.params(w, k, 1.0f, wv[k]);
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
     }
-    for (int64_t r0 = first * rpw; r0 < rows; r0 += R * warps * rpw) {
-        Unit<T, V> ux[R][NV], ug[R][NV];
+    for (int64_t r0 = first; r0 < rows; r0 += R * step) {
+        Unit<T> ux[R][NV], ug[R][NV];
         float mu[R], rs[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t r = r0 + q * warps * rpw + sub;
+            const int64_t r = r0 + q * step + sub;
             const bool in = r < rows;
             mu[q] = in ? mean[r] : 0.0f;
             rs[q] = in ? rstd[r] : 0.0f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int i = l + 32 * k;
-                if (in && i < units) {
-                    ux[q][k].load_stream(x + r * width + i * V);
-                    ug[q][k].load_stream(dy + r * width + i * V);
+                if (in && c.in(k)) {
+                    c.load(ux[q][k], k, x + r * width, (rows - r) * width);
+                    c.load(ug[q][k], k, dy + r * width, (rows - r) * width);
                 } else {
                     ux[q][k].zero();
                     ug[q][k].zero();
@@ -210,10 +329,12 @@ __global__ void __launch_bounds__(kThreads, V * NV <= 8 ? 4 : 2)
         }
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t r = r0 + q * warps * rpw + sub;
+            const int64_t r = r0 + q * step + sub;
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k) {
+                c.keep(ux[q][k], k);
+                c.keep(ug[q][k], k);   // zero where the element is not the row's: it adds nothing
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float g = ug[q][k].at(e), h = (ux[q][k].at(e) - mu[q]) * rs[q], a = g * wv[k][e];
@@ -222,46 +343,52 @@ __global__ void __launch_bounds__(kThreads, V * NV <= 8 ? 4 : 2)
                     dw[k][e] += g * h;
                     db[k][e] += g;
                 }
+            }
             s1 = lanes_sum(s1, lpr) * inv;
             s2 = lanes_sum(s2, lpr) * inv;
             if (r < rows)
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int i = l + 32 * k;
-                    if (i < units) {
+                for (int k = 0; k < NV; ++k)
+                    if (c.in(k)) {
                         float o[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e)
                             o[e] = rs[q] * (ug[q][k].at(e) * wv[k][e] - s1 - (ux[q][k].at(e) - mu[q]) * rs[q] * s2);
-                        Unit<T, V>::store(dx + r * width + i * V, o);
+                        c.store(dx + r * width, k, o);
                     }
-                }
         }
     }
     if (!part) return;
-    // the warp's rows by lane, then the block's warps in order
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            for (int o = lpr; o < 32; o <<= 1) {
-                dw[k][e] += __shfl_xor_sync(0xffffffffu, dw[k][e], o);
-                db[k][e] += __shfl_xor_sync(0xffffffffu, db[k][e], o);
-            }
-    if (sub == 0)
+    // The sums of the warp's rows, of the block's warps in order. (Rows of a warp that start at different places
+    // have different columns in a lane.)
+    int at = warp * rpw + sub, parts = kThreads / 32 * rpw;
+    if constexpr (!kRagged) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (l + 32 * k < units)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    acc[(size_t)(2 * warp) * width + (l + 32 * k) * V + e] = dw[k][e];
-                    acc[(size_t)(2 * warp + 1) * width + (l + 32 * k) * V + e] = db[k][e];
+            for (int e = 0; e < V; ++e)
+                for (int o = lpr; o < 32; o <<= 1) {
+                    dw[k][e] += __shfl_xor_sync(0xffffffffu, dw[k][e], o);
+                    db[k][e] += __shfl_xor_sync(0xffffffffu, db[k][e], o);
                 }
+        at = warp;
+        parts = kThreads / 32;
+    }
+    if (kRagged || sub == 0)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (c.in(k))
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if ((c.ok(k) >> e) & 1u) {
+                        acc[(size_t)(2 * at) * width + c.column(k) + e] = dw[k][e];
+                        acc[(size_t)(2 * at + 1) * width + c.column(k) + e] = db[k][e];
+                    }
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * width; c += kThreads) {
+    for (int i = threadIdx.x; i < 2 * width; i += kThreads) {
         float s = 0.0f;
-        for (int i = 0; i < kThreads / 32; ++i) s += acc[(size_t)2 * i * width + c];
-        part[(size_t)blockIdx.x * 2 * width + c] = s;
+        for (int j = 0; j < parts; ++j) s += acc[(size_t)2 * j * width + i];
+        part[(size_t)blockIdx.x * 2 * width + i] = s;
     }
 }
 
@@ -292,8 +419,9 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float2 (&buf)[32]
     __syncthreads();
     return sum_of(buf);
 }
-// rows at a time of the backward, by a thread's columns (single elements take a register each)
-__host__ __device__ constexpr int bwd_rows(int columns, bool vec) { return columns <= (vec ? 16 : 8) ? 2 : 1; }
+// rows at a time of the backward, by a thread's columns: 4099 x 4096 fp32 (8 columns) 41 us, 45 with one;
+// 8192 x 4096 bf16 (16 columns) 54 us with one, 57 with two
+__host__ __device__ constexpr int bwd_rows(int columns) { return columns <= 8 ? 2 : 1; }
 
 // Rows on their way to shared memory: a step of R rows (r, r + stride, ..) of each input, `stages` steps
 // ahead, of each row the aligned span around it. The last bytes of a tensor whose size is no multiple of
@@ -329,17 +457,17 @@ struct Rows {
     __device__ __forceinline__ uint8_t* slot(int stage, int input, int q) const {
         return at + ((size_t)(stage * inputs + input) * R + q) * pitch;
     }
-    // element 0 of row r, the q-th of its step, of an input in shared memory
-    template <typename T>
-    __device__ __forceinline__ const T* row(int64_t r, int stage, int input, int q) const {
-        return reinterpret_cast<const T*>(slot(stage, input, q) + (((size_t)r * row_bytes) & 15));
-    }
 };
-// a unit of the row from shared memory, or from global memory past the copied part
-template <typename T, int V, int R>
-__device__ __forceinline__ void take(Unit<T, V>& u, const Rows<R>& m, const T* in_smem, const T* in_global, int64_t r, int c) {
-    if (V == 1 && (size_t)r * m.row_bytes + (size_t)(c + 1) * sizeof(T) > m.most) u.load(in_global + c);
-    else u.load(in_smem + c);
+// unit k of a row from shared memory, or from global memory past the copied part
+template <typename T, int NV, bool kRagged, int R>
+__device__ __forceinline__ void take(Unit<T>& u, const Rows<R>& m, const Columns<T, NV, kRagged>& c, int k, const uint8_t* slot,
+                                     const T* row, int64_t r) {
+    if (kRagged && (size_t)r * m.row_bytes + (size_t)(c.column(k) + Unit<T>::V) * sizeof(T) > m.most) {
+        u.load_some(row + c.column(k), c.ok(k));
+    } else {
+        u.load(reinterpret_cast<const T*>(slot + 16 * c.unit(k)));
+        if (!c.whole(k)) u.keep(c.ok(k));
+    }
 }
 template <int R>
 __device__ __forceinline__ Rows<R> rows_of(uint8_t* smem, size_t row_bytes, int64_t rows, int pitch, int inputs) {
@@ -356,15 +484,15 @@ __device__ __forceinline__ Rows<R> rows_of(uint8_t* smem, size_t row_bytes, int6
 }
 
 // Persistent blocks: rows blockIdx.x, + gridDim.x, .., two at a time (their sums share the barriers, and one's
-// arithmetic runs in the other's waits: one row at a time took 81 instead of .. us at 8192 x 12288); thread t
+// arithmetic runs in the other's waits: one row at a time took 81 instead of 72 us at 8192 x 12288); thread t
 // holds units t, t + blockDim.x, .. A copy that has not arrived after 2 s leaves NaN in its rows' outputs
 // (there is no workspace to report it in).
-template <typename T, int V, int NV>
+template <typename T, int NV, bool kRagged>
 __global__ void __launch_bounds__(512)
     norm_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
-                         float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int units, int pitch,
-                         int stages, float eps) {
-    constexpr int R = 2;
+                         float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int pitch, int stages,
+                         float eps) {
+    constexpr int R = 2, V = Unit<T>::V;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float2 buf[2][32];
     const Rows<R> m = rows_of<R>(smem, (size_t)width * sizeof(T), rows, pitch, 1);
@@ -377,25 +505,25 @@ __global__ void __launch_bounds__(512)
         for (int i = 0; i < stages; ++i)
             if (blockIdx.x + i * step < rows) m.issue(blockIdx.x + i * step, i, x, nullptr);
     }
-    Params<NV, V> pw, pb;
-    pw.init(w, 1.0f, t, nt, units);
-    pb.init(b, 0.0f, t, nt, units);
+    Columns<T, NV, kRagged> c;
+    c.init(t, nt, blockIdx.x, width);
+    Params<T, NV, kRagged> pw, pb;
+    pw.init(c, w, 1.0f);
+    pb.init(c, b, 0.0f);
     __syncthreads();
     int stage = 0;
     uint32_t phase = 0;
     for (int64_t r = blockIdx.x; r < rows; r += step) {
         const bool ok = mbar_wait(&m.full[stage], phase);
-        Unit<T, V> u[R][NV];
+        Unit<T> u[R][NV];
         float s[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             const int64_t rq = r + q * m.stride;
-            const T* row = m.template row<T>(rq, stage, 0, q);
             s[q] = 0.0f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int i = t + nt * k;
-                if (i < units && rq < rows) take(u[q][k], m, row, x + rq * width, rq, i * V);
+                if (c.in(k) && rq < rows) take(u[q][k], m, c, k, m.slot(stage, 0, q), x + rq * width, rq);
                 else u[q][k].zero();
 #pragma unroll
                 for (int e = 0; e < V; ++e) s[q] += u[q][k].at(e);
@@ -411,25 +539,22 @@ __global__ void __launch_bounds__(512)
             s[q] = 0.0f;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (t + nt * k < units)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) s[q] += (u[q][k].at(e) - mu[q]) * (u[q][k].at(e) - mu[q]);
+                if (c.in(k)) s[q] += c.squares(u[q][k], k, mu[q]);
         }
         const float2 var = block_sums(s[0], s[1], buf[1]);
         const float rs[R] = {rsqrtf(var.x * inv + eps), rsqrtf(var.y * inv + eps)};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int i = t + nt * k;
-            if (i < units) {
+            if (c.in(k)) {
                 float wv[V], bv[V], o[V];
-                pw.at(k, i, wv);
-                pb.at(k, i, bv);
+                pw.at(c, k, wv);
+                pb.at(c, k, bv);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
                     const int64_t rq = r + q * m.stride;
 #pragma unroll
                     for (int e = 0; e < V; ++e) o[e] = (u[q][k].at(e) - mu[q]) * rs[q] * wv[e] + bv[e];
-                    if (rq < rows) Unit<T, V>::store(y + rq * width + i * V, o);
+                    if (rq < rows) c.store(y + rq * width, k, o);
                 }
             }
         }
@@ -446,12 +571,12 @@ __global__ void __launch_bounds__(512)
 
 // The same for the backward, with dw and db of a thread's columns in registers; two rows at a time where
 // registers allow.
-template <typename T, int V, int NV>
+template <typename T, int NV, bool kRagged>
 __global__ void __launch_bounds__(512)
     norm_bwd_wide_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                          const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
-                         float* __restrict__ part, int64_t rows, int width, int units, int pitch, int stages) {
-    constexpr int R = bwd_rows(NV * V, V > 1);
+                         float* __restrict__ part, int64_t rows, int width, int pitch, int stages) {
+    constexpr int V = Unit<T>::V, R = bwd_rows(NV * V);
     grid_launch_next();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float2 buf[2][R][32];
@@ -470,8 +595,10 @@ __global__ void __launch_bounds__(512)
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
-    Params<NV, V> pw;
-    pw.init(w, 1.0f, t, nt, units);
+    Columns<T, NV, kRagged> c;
+    c.init(t, nt, blockIdx.x, width);
+    Params<T, NV, kRagged> pw;
+    pw.init(c, w, 1.0f);
     __syncthreads();
     int stage = 0, turn = 0;
     uint32_t phase = 0;
@@ -495,18 +622,17 @@ __global__ void __launch_bounds__(512)
         }
         fetch(r + step);
         const bool ok = mbar_wait(&m.full[stage], phase);
-        Unit<T, V> ux[R][NV], ug[R][NV];
+        Unit<T> ux[R][NV], ug[R][NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int i = t + nt * k;
             float wv[V];
-            if (i < units) pw.at(k, i, wv);
+            if (c.in(k)) pw.at(c, k, wv);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 const int64_t rq = r + q * m.stride;
-                if (i < units && rq < rows) {
-                    take(ux[q][k], m, m.template row<T>(rq, stage, 0, q), x + rq * width, rq, i * V);
-                    take(ug[q][k], m, m.template row<T>(rq, stage, 1, q), dy + rq * width, rq, i * V);
+                if (c.in(k) && rq < rows) {
+                    take(ux[q][k], m, c, k, m.slot(stage, 0, q), x + rq * width, rq);
+                    take(ug[q][k], m, c, k, m.slot(stage, 1, q), dy + rq * width, rq);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float g = ug[q][k].at(e), h = (ux[q][k].at(e) - mu[q]) * rs[q], a = g * wv[e];
@@ -536,17 +662,16 @@ __global__ void __launch_bounds__(512)
         if (t == 0 && next < rows) m.issue(next, stage, x, dy);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int i = t + nt * k;
-            if (i < units) {
+            if (c.in(k)) {
                 float wv[V], o[V];
-                pw.at(k, i, wv);
+                pw.at(c, k, wv);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
                     const int64_t rq = r + q * m.stride;
 #pragma unroll
                     for (int e = 0; e < V; ++e)
                         o[e] = rs[q] * (ug[q][k].at(e) * wv[e] - s1[q] - (ux[q][k].at(e) - mu[q]) * rs[q] * s2[q]);
-                    if (rq < rows) Unit<T, V>::store(dx + rq * width + i * V, o);
+                    if (rq < rows) c.store(dx + rq * width, k, o);
                 }
             }
         }
@@ -558,13 +683,13 @@ __global__ void __launch_bounds__(512)
     if (!part) return;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int i = t + nt * k;
-        if (i < units)
+        if (c.in(k))
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                part[(size_t)blockIdx.x * 2 * width + i * V + e] = dw[k][e];
-                part[((size_t)blockIdx.x * 2 + 1) * width + i * V + e] = db[k][e];
-            }
+            for (int e = 0; e < V; ++e)
+                if ((c.ok(k) >> e) & 1u) {
+                    part[(size_t)blockIdx.x * 2 * width + c.column(k) + e] = dw[k][e];
+                    part[((size_t)blockIdx.x * 2 + 1) * width + c.column(k) + e] = db[k][e];
+                }
     }
 }
 
@@ -677,163 +802,126 @@ bool valid_size(long long rows, long long width) {
     return rows >= 0 && width >= 1 && width <= (1LL << 20) && rows <= (1LL << 40) / width;
 }
 
-// Most blocks whose sums of dw and db are kept: four on an SM, and one for every SM at least. Their sums are
-// written and read again, so they stay below about a twentieth of what the rows themselves move.
-constexpr int kMostParts = 4 * kSMs;
-int most_parts(long long rows, size_t size) {
-    const long long n = rows * (long long)size / 54;
-    return (int)(n < kSMs ? kSMs : n > kMostParts ? kMostParts : n);
-}
+constexpr int kMostParts = 4 * kSMs;   // blocks whose sums of dw and db are kept
 
 // Which form a width takes, and its launch.
 struct Form {
-    int units, lpr, nv;      // lpr: lanes of a row (narrow), 0: wide or any
-    bool vec, wide;
+    int units, lpr, nv;      // most units of a row; lpr: lanes of a row (narrow), 0: wide or any
+    bool ragged, wide;
     int threads, pitch, stages, per_sm;
     size_t smem;
 };
 Form form_of(long long width, size_t size, int inputs) {
     Form f{};
     const int v = (int)(16 / size);
-    f.vec = width % v == 0;
-    f.units = (int)(f.vec ? width / v : width);
-    if (f.vec ? f.units <= kNarrowUnits : width <= kNarrowColumns) {
+    f.ragged = width % v != 0;
+    f.units = (int)((width + (f.ragged ? v - 1 : 0) + v - 1) / v);
+    if (f.units <= kNarrowUnits) {
         f.lpr = 1;
         while (f.lpr < f.units && f.lpr < 32) f.lpr *= 2;
-        const int need = (f.units + 31) / 32;
-        f.nv = 1;
-        while (f.nv < need) f.nv *= 2;
+        f.nv = f.units <= 32 ? 1 : 2;
         return f;
     }
     if (width > kWideMost) return f;
     f.wide = true;
-    // 16 bf16 or 8 fp32 columns a thread and small blocks, so that many rows are in flight; more columns
-    // where 512 threads do not hold the row
-    const int most[] = {2, 3, 4, 8, 16, 32};
-    for (int nv : most) {
-        f.nv = nv;
-        if ((f.vec || nv >= 8) && f.units <= nv * 512) break;
-    }
-    f.threads = ((f.units + f.nv - 1) / f.nv + 31) / 32 * 32;
     f.pitch = (int)((width * size + 31) / 16 * 16);
-    const int columns = f.nv * (f.vec ? v : 1);
-    const int stage = f.pitch * inputs * (inputs == 1 ? 2 : bwd_rows(columns, f.vec));
-    const int room = columns * (inputs + 1) >= 48 ? 512 : 1024;   // threads on an SM, by registers
-    f.per_sm = room / f.threads < 1 ? 1 : room / f.threads;
-    if (f.per_sm > 16) f.per_sm = 16;
+    // Two units a thread and small blocks, so that many rows are in flight; more units where 512 threads do not hold
+    // the row; one in the backward of short rows, whose blocks are limited by kMostParts (20000 x 777 bf16 43 us,
+    // 54 with two).
+    // Threads on an SM, by registers: 512 with 24 columns (backward: 16), 1024 otherwise (8192 x 12288 backward
+    // 140 us, 156 with 1024; 4099 x 4096 fp32 forward 27 us, 32 with 512).
+    f.nv = inputs == 2 && f.units <= 128 ? 1 : 2;
+    while (f.units > f.nv * 512) f.nv = f.nv == 4 ? 8 : f.nv + 1;
+    f.threads = ((f.units + f.nv - 1) / f.nv + 31) / 32 * 32;
+    const int fit = (f.nv * v * (inputs + 1) >= 48 ? 512 : 1024) / f.threads;
+    f.per_sm = std::min(std::max(fit, 1), inputs == 1 ? 16 : kMostParts / kSMs);
+    const int stage = f.pitch * inputs * (inputs == 1 ? 2 : bwd_rows(f.nv * v));
     // up to four steps ahead, within the SM's shared memory; fewer blocks rather than none ahead
     for (;; --f.per_sm) {
         f.stages = (int)(((size_t)216 * 1024 / f.per_sm - 1024 - 64) / stage);
         if (f.stages >= 2 || f.per_sm == 1) break;
     }
-    if (f.stages > 4) f.stages = 4;
-    if (f.stages < 1) f.stages = 1;
+    f.stages = std::clamp(f.stages, 1, 4);
     f.smem = 64 + (size_t)stage * f.stages;
     return f;
 }
 
 unsigned blocks(long long rows, long long most) { return (unsigned)(rows < most ? rows : most); }
 
-template <typename T, int V, int NV>
+template <typename T, int NV, bool kRagged>
 kda_status fwd_wide(const Form& f, long long rows, int width, float eps, const T* x, const float* w, const float* b, T* y,
                     float* mean, float* rstd, cudaStream_t s) {
-    auto k = norm_fwd_wide_kernel<T, V, NV>;
+    auto k = norm_fwd_wide_kernel<T, NV, kRagged>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_fwd");
-    k<<<blocks(rows, (long long)kSMs * f.per_sm), f.threads, f.smem, s>>>(x, w, b, y, mean, rstd, rows, width, f.units, f.pitch,
-                                                                       f.stages, eps);
+    k<<<blocks(rows, (long long)kSMs * f.per_sm), f.threads, f.smem, s>>>(x, w, b, y, mean, rstd, rows, width, f.pitch, f.stages, eps);
     return launched("kda_layernorm_fwd launch");
 }
-template <typename T, int V, int NV>
+template <typename T, int NV, bool kRagged>
 kda_status fwd_narrow(const Form& f, long long rows, int width, float eps, const T* x, const float* w, const float* b, T* y,
                       float* mean, float* rstd, cudaStream_t s) {
     const long long rpb = (long long)(kThreads / 32) * (32 / f.lpr);
-    norm_fwd_narrow_kernel<T, V, NV><<<blocks((rows + rpb - 1) / rpb, 8LL * kSMs), kThreads, 0, s>>>(x, w, b, y, mean, rstd, rows,
-                                                                                                     width, f.units, f.lpr, eps);
+    constexpr int per_sm = fwd_rows(Unit<T>::V * NV, kRagged) == 2 ? 4 : 6;
+    norm_fwd_narrow_kernel<T, NV, kRagged><<<blocks((rows + rpb - 1) / rpb, per_sm * kSMs), kThreads, 0, s>>>(
+        x, w, b, y, mean, rstd, rows, width, f.lpr, eps);
     return launched("kda_layernorm_fwd launch");
 }
-template <typename T>
-kda_status fwd(long long rows, int width, float eps, const void* xv, const float* w, const float* b, void* yv, float* mean,
-               float* rstd, cudaStream_t s) {
+template <typename T, bool kRagged>
+kda_status fwd(const Form& f, long long rows, int width, float eps, const void* xv, const float* w, const float* b, void* yv,
+               float* mean, float* rstd, cudaStream_t s) {
     const T* x = static_cast<const T*>(xv);
     T* y = static_cast<T*>(yv);
-    constexpr int V = 16 / sizeof(T);
-    const Form f = form_of(width, sizeof(T), 1);
-#define KDA_NORM(fn, v, n) return fn<T, v, n>(f, rows, width, eps, x, w, b, y, mean, rstd, s)
-    if (f.lpr && f.vec) {
-        if (f.nv == 1) KDA_NORM(fwd_narrow, V, 1);
-        KDA_NORM(fwd_narrow, V, 2);
-    }
+#define KDA_NORM(fn, n) return fn<T, n, kRagged>(f, rows, width, eps, x, w, b, y, mean, rstd, s)
     if (f.lpr) {
-        if (f.nv <= 2) KDA_NORM(fwd_narrow, 1, 2);
-        if (f.nv <= 4) KDA_NORM(fwd_narrow, 1, 4);
-        if (f.nv <= 8) KDA_NORM(fwd_narrow, 1, 8);
-        KDA_NORM(fwd_narrow, 1, 16);
-    }
-    if (f.wide && f.vec) {
-        if (f.nv == 2) KDA_NORM(fwd_wide, V, 2);
-        if (f.nv == 3) KDA_NORM(fwd_wide, V, 3);
-        if (f.nv == 4) KDA_NORM(fwd_wide, V, 4);
-        if constexpr (V == 4) KDA_NORM(fwd_wide, V, 8);
+        if (f.nv == 1) KDA_NORM(fwd_narrow, 1);
+        KDA_NORM(fwd_narrow, 2);
     }
     if (f.wide) {
-        if (f.nv <= 8) KDA_NORM(fwd_wide, 1, 8);
-        if (f.nv <= 16) KDA_NORM(fwd_wide, 1, 16);
-        KDA_NORM(fwd_wide, 1, 32);
+        if (f.nv == 2) KDA_NORM(fwd_wide, 2);
+        if (f.nv == 3) KDA_NORM(fwd_wide, 3);
+        if (f.nv == 4) KDA_NORM(fwd_wide, 4);
+        if constexpr (sizeof(T) == 4) KDA_NORM(fwd_wide, 8);
     }
 #undef KDA_NORM
     norm_fwd_any_kernel<T><<<blocks(rows, 1 << 30), kThreads, 0, s>>>(x, w, b, y, mean, rstd, rows, width, eps);
     return launched("kda_layernorm_fwd launch");
 }
 
-template <typename T, int V, int NV>
+template <typename T, int NV, bool kRagged>
 kda_status bwd_wide(const Form& f, long long rows, int width, const T* x, const T* dy, const float* w, const float* mean,
                     const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
-    auto k = norm_bwd_wide_kernel<T, V, NV>;
+    auto k = norm_bwd_wide_kernel<T, NV, kRagged>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_bwd");
-    const long long most = (long long)kSMs * f.per_sm, keep = most_parts(rows, sizeof(T));
-    *parts = (int)blocks(rows, most < keep ? most : keep);
-    k<<<*parts, f.threads, f.smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.units, f.pitch, f.stages);
+    *parts = (int)blocks(rows, (long long)kSMs * f.per_sm);
+    k<<<*parts, f.threads, f.smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.pitch, f.stages);
     return launched("kda_layernorm_bwd launch");
 }
-template <typename T, int V, int NV>
+template <typename T, int NV, bool kRagged>
 kda_status bwd_narrow(const Form& f, long long rows, int width, const T* x, const T* dy, const float* w, const float* mean,
                       const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
-    constexpr int R = V * NV <= 8 ? 2 : 1;
-    const long long rpb = (long long)(kThreads / 32) * (32 / f.lpr);
-    *parts = (int)blocks((rows + rpb - 1) / rpb, (V * NV <= 8 ? 4 : 2) * kSMs);   // as many as are resident
-    norm_bwd_narrow_kernel<T, V, NV, R><<<*parts, kThreads, (size_t)(kThreads / 32) * 2 * width * sizeof(float), s>>>(
-        x, dy, w, mean, rstd, dx, part, rows, width, f.units, f.lpr);
+    const int rpw = 32 / f.lpr;
+    const long long rpb = (long long)(kThreads / 32) * rpw;
+    const size_t smem = (size_t)rpb * 2 * width * sizeof(float);
+    *parts = (int)blocks((rows + rpb - 1) / rpb, bwd_narrow_blocks(NV) * kSMs);   // as many as are resident
+    norm_bwd_narrow_kernel<T, NV, kRagged><<<*parts, kThreads, smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.lpr);
     return launched("kda_layernorm_bwd launch");
 }
 // dx and, to part where it is given, the sums of `parts` blocks
-template <typename T>
-kda_status bwd(long long rows, int width, const void* xv, const void* dyv, const float* w, const float* mean, const float* rstd,
-               void* dxv, float* part, int* parts, cudaStream_t s) {
+template <typename T, bool kRagged>
+kda_status bwd(const Form& f, long long rows, int width, const void* xv, const void* dyv, const float* w, const float* mean,
+               const float* rstd, void* dxv, float* part, int* parts, cudaStream_t s) {
     const T *x = static_cast<const T*>(xv), *dy = static_cast<const T*>(dyv);
     T* dx = static_cast<T*>(dxv);
-    constexpr int V = 16 / sizeof(T);
-    const Form f = form_of(width, sizeof(T), 2);
-#define KDA_NORM(fn, v, n) return fn<T, v, n>(f, rows, width, x, dy, w, mean, rstd, dx, part, parts, s)
-    if (f.lpr && f.vec) {
-        if (f.nv == 1) KDA_NORM(bwd_narrow, V, 1);
-        KDA_NORM(bwd_narrow, V, 2);
-    }
+#define KDA_NORM(fn, n) return fn<T, n, kRagged>(f, rows, width, x, dy, w, mean, rstd, dx, part, parts, s)
     if (f.lpr) {
-        if (f.nv <= 2) KDA_NORM(bwd_narrow, 1, 2);
-        if (f.nv <= 4) KDA_NORM(bwd_narrow, 1, 4);
-        if (f.nv <= 8) KDA_NORM(bwd_narrow, 1, 8);
-        KDA_NORM(bwd_narrow, 1, 16);
-    }
-    if (f.wide && f.vec) {
-        if (f.nv == 2) KDA_NORM(bwd_wide, V, 2);
-        if (f.nv == 3) KDA_NORM(bwd_wide, V, 3);
-        if (f.nv == 4) KDA_NORM(bwd_wide, V, 4);
-        if constexpr (V == 4) KDA_NORM(bwd_wide, V, 8);
+        if (f.nv == 1) KDA_NORM(bwd_narrow, 1);
+        KDA_NORM(bwd_narrow, 2);
     }
     if (f.wide) {
-        if (f.nv <= 8) KDA_NORM(bwd_wide, 1, 8);
-        if (f.nv <= 16) KDA_NORM(bwd_wide, 1, 16);
-        KDA_NORM(bwd_wide, 1, 32);
+        if (f.nv == 1) KDA_NORM(bwd_wide, 1);
+        if (f.nv == 2) KDA_NORM(bwd_wide, 2);
+        if (f.nv == 3) KDA_NORM(bwd_wide, 3);
+        if (f.nv == 4) KDA_NORM(bwd_wide, 4);
+        if constexpr (sizeof(T) == 4) KDA_NORM(bwd_wide, 8);
     }
 #undef KDA_NORM
     norm_dx_any_kernel<T><<<blocks(rows, 1 << 30), kThreads, 0, s>>>(x, dy, w, mean, rstd, dx, rows, width);
@@ -861,8 +949,9 @@ extern "C" kda_status kda_layernorm_fwd(long long rows, long long width, int dty
     for (const void* p : ptrs)
         if (misaligned(p)) return KDA_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == KDA_BF16 ? fwd<uint16_t>(rows, (int)width, eps, x, weight, bias, y, mean, rstd, s)
-                             : fwd<float>(rows, (int)width, eps, x, weight, bias, y, mean, rstd, s);
+    const Form f = form_of(width, dtype == KDA_BF16 ? 2 : 4, 1);
+    auto run = dtype == KDA_BF16 ? (f.ragged ? fwd<uint16_t, true> : fwd<uint16_t, false>) : (f.ragged ? fwd<float, true> : fwd<float, false>);
+    return run(f, rows, (int)width, eps, x, weight, bias, y, mean, rstd, s);
 }
 
 extern "C" size_t kda_layernorm_workspace_size(long long rows, long long width) {
@@ -886,9 +975,9 @@ extern "C" kda_status kda_layernorm_bwd(long long rows, long long width, int dty
     float* part = sums ? static_cast<float*>(workspace) : nullptr;
     int parts = 0;
     if (rows > 0) {
-        const kda_status st = dtype == KDA_BF16
-                                  ? bwd<uint16_t>(rows, (int)width, x, dy, weight, mean, rstd, dx, part, &parts, s)
-                                  : bwd<float>(rows, (int)width, x, dy, weight, mean, rstd, dx, part, &parts, s);
+        const Form f = form_of(width, dtype == KDA_BF16 ? 2 : 4, 2);
+        auto run = dtype == KDA_BF16 ? (f.ragged ? bwd<uint16_t, true> : bwd<uint16_t, false>) : (f.ragged ? bwd<float, true> : bwd<float, false>);
+        const kda_status st = run(f, rows, (int)width, x, dy, weight, mean, rstd, dx, part, &parts, s);
         if (st != KDA_OK) return st;
     }
     if (sums)
