@@ -27,6 +27,10 @@ constexpr int LC = 128;                       // tokens of a chunk
 constexpr int kSMs = 152;                     // of a GB300; one persistent CTA on each
 // the cost model of the split, in chunk times of a full unit
 constexpr double kStateOnly = 0.5, kUnitChunks = 1.0, kSplitChunks = 4.0;
+// Calls of up to so many tokens have their scores in two bf16 parts (16 significant bits). Rounded once, a score is off
+// by up to 2^-8 of itself; over many scores that is 1.4 times the outputs' own rounding in the mean square, but in the few
+// outputs of a short call it was up to 1.7 times, wherever a single score makes up a row.
+constexpr int kFineTokens = 512;
 constexpr uint32_t kTile = LC * D * 2;        // a bf16 operand tile [128][128], two 64-column panels
 
 // One sum over tokens in the roles' names. Row i of a chunk of L rows, with the state S the
@@ -238,6 +242,11 @@ __device__ __forceinline__ uint32_t pack_bf16(f32x2 a) {
     return pack_bf16(x.x, x.y);
 }
 
+// what bf16 leaves of a pair, itself in bf16
+__device__ __forceinline__ uint32_t low_part(f32x2 p, uint32_t high) {
+    return pack_bf16(fma2(two(-1.0f, -1.0f), two(low_bf16(high), high_bf16(high)), p));
+}
+
 // The chunks of a CTA's units, one after another.
 struct At {
     int round, c, chunks;
@@ -311,6 +320,8 @@ constexpr uint32_t kColP = 0, kColO = 128, kColDS = 256, kColHi = 384, kColMid =
 // the scores' copy goes behind the columns still to be read: forward from the left, reversed from the right
 __device__ __forceinline__ uint32_t copy_col(int rev) { return kColP + (rev ? 64u : 0u); }
 __device__ __forceinline__ uint32_t low_col(int rev) { return kColP + (rev ? 0u : 64u); }
+// in two parts each block of 32 columns holds its own: of the MMA step s, the high part here, the low part 16 columns on
+__device__ __forceinline__ uint32_t fine_col(int s) { return kColP + 32 * (s >> 1) + 8 * (s & 1); }
 // A product over K = 128: eight MMAs, unrolled, descriptors a constant apart. (The thread that issues them is
 // what limits it otherwise: with descriptors built one by one an MMA of 128 x 128 x 16 took 130 to 190 cycles,
 // so it takes 65, the time to read its operands from shared memory.)
@@ -326,7 +337,7 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, u
 #pragma unroll
     for (int s = 0; s < 8; ++s) umma_bf16_ta(d, a + 8 * s, mn_step(b, s), idesc, kAdd || s > 0);
 }
-__device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     constexpr uint32_t kk = idesc_bf16(128, 128, 0, 0), kn = idesc_bf16(128, 128, 0, 1);
     const uint64_t dk0 = desc_kmajor(smem_u32(sm.K[0]), LC, 0), ds = desc_mnmajor_bf16(smem_u32(sm.S), LC, 0);
@@ -360,8 +371,15 @@ __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units
         if (!(ok = mbar_wait_asleep(&sm.o, ph) && mbar_wait_asleep(&sm.p, ph))) break;
         tc_fence_after();
         if (!state_only) {
-            if (carried) product_ts<true>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
-            else product_ts<false>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
+            if (kFine) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    umma_bf16_ta(tm + kColO, tm + fine_col(i >> 1) + 16 * (i & 1), mn_step(v, i >> 1), kn, carried || i > 0);
+            } else if (carried) {
+                product_ts<true>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
+            } else {
+                product_ts<false>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
+            }
         }
         umma_commit(&sm.pv);
         if (three) {
@@ -382,7 +400,7 @@ __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units
 
 // --- scores -> decayed bf16 scores in TMEM; outputs -> shared memory -> global, a warp's 32 rows by TMA (or,
 // in a chunk with rows of a neighbour, row by row)
-__device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
@@ -422,10 +440,10 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     const int b = rev ? 3 - i : i, away = rev ? b - warp : warp - b;
-                    uint32_t w[16];
+                    uint32_t w[16], low[16];
                     if (away < 0) {
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) w[x] = 0u;
+                        for (int x = 0; x < 16; ++x) w[x] = low[x] = 0u;
                     } else {
                         uint32_t r[32];
                         tmem_ld32_issue(lanes + kColP + 32 * b, r);
@@ -434,18 +452,25 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
                             const f32x2 base2 = two(base, base);
                             tmem_wait_ld(r);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) w[x] = pack_bf16(mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x])));
+                            for (int x = 0; x < 16; ++x) {
+                                const f32x2 p = mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x]));
+                                w[x] = pack_bf16(p);
+                                if (kFine) low[x] = low_part(p, w[x]);
+                            }
                         } else {
                             const float* const d = diag + 31 + lane;
                             tmem_wait_ld(r);
 #pragma unroll
                             for (int x = 0; x < 16; ++x) {
                                 const float p0 = __uint_as_float(r[2 * x]) * d[-2 * x], p1 = __uint_as_float(r[2 * x + 1]) * d[-2 * x - 1];
-                                w[x] = pack_bf16((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
+                                const f32x2 p = two((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
+                                w[x] = pack_bf16(p);
+                                if (kFine) low[x] = low_part(p, w[x]);
                             }
                         }
                     }
-                    tmem_st16_issue(lanes + copy_col(rev) + 16 * b, w);   // columns that have been read
+                    tmem_st16_issue(lanes + (kFine ? kColP + 32 * b : copy_col(rev) + 16 * b), w);   // columns that have been read
+                    if (kFine) tmem_st16_issue(lanes + kColP + 32 * b + 16, low);
                 }
                 tmem_wait_st_all();
             }
@@ -534,7 +559,7 @@ __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int un
 }
 
 // --- state in registers and its bf16 copy for the next chunk; decayed keys as bf16 parts; Q S^T decayed by row
-__device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     const int warp = uniform((int)((threadIdx.x >> 5) & 3)), lane = threadIdx.x & 31, half = uniform((int)((threadIdx.x - 32 * kScoreWarps) >> 7));
     const int row = 32 * warp + lane;              // TMEM lane: output row, or key channel of the state
@@ -714,7 +739,7 @@ __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int unit
             }
             mbar_arrive(&sm.o);
             if (three) {   // the low parts: beside the scores' bf16 copy, once that is made
-                if (!(ok = wait_warp(&sm.p, n))) break;
+                if (!(ok = wait_warp(kFine ? &sm.pv : &sm.p, n))) break;   // (qs: pv of the chunk before is over)
                 tc_fence_after();
 #pragma unroll 1
                 for (int g = 0; g < 4; ++g) {
@@ -756,7 +781,7 @@ __device__ __forceinline__ bool own_slot(const LinArgs& a) {
     return !__syncthreads_or(bad);
 }
 
-__global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_constant__ LinArgs a) {
+template <bool kFine> __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_constant__ LinArgs a) {
     extern __shared__ uint8_t smem_raw[];
     LinSmem& sm = *reinterpret_cast<LinSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // A call's first kernel sets the status word here, long before any wait of another CTA can give up
@@ -789,15 +814,15 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tm = uniform(sm.tmem);
     if (warp < kScoreWarps) {
-        lin_scores(a, sm, units, tm);
+        lin_scores<kFine>(a, sm, units, tm);
     } else if (warp < kScoreWarps + kMainWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
-        lin_main(a, sm, units, tm);
+        lin_main<kFine>(a, sm, units, tm);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if ((threadIdx.x & 31) == 0) {
             if (warp == kScoreWarps + kMainWarps) lin_load(a, sm, units);
-            else if (warp == kScoreWarps + kMainWarps + 1) lin_mma(a, sm, units, tm);
+            else if (warp == kScoreWarps + kMainWarps + 1) lin_mma<kFine>(a, sm, units, tm);
         }
     }
     __syncwarp();
@@ -1116,7 +1141,9 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
     cudaError_t e = cudaGetDevice(&device);
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (e == cudaSuccess && !(allowed.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(linattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
+        e = cudaFuncSetAttribute(linattn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(linattn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
         if (e == cudaSuccess && device < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
     if (e != cudaSuccess) {
@@ -1160,7 +1187,8 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
     }
     auto launch = [&](const LinArgs& x) {
         const int64_t units = (int64_t)x.slots * sh->H * x.jobs;
-        linattn_kernel<<<(unsigned)(units < kSMs ? units : kSMs), kLinThreads, sizeof(LinSmem) + 1024, s>>>(x);
+        auto kernel = tokens <= kFineTokens ? linattn_kernel<true> : linattn_kernel<false>;
+        kernel<<<(unsigned)(units < kSMs ? units : kSMs), kLinThreads, sizeof(LinSmem) + 1024, s>>>(x);
     };
     if (p.nseg > 1) {
         LinArgs b = a;
