@@ -6,9 +6,13 @@
 // registers between the row's sums and its outputs, and dw, db are summed on the same pass, each
 // thread over the rows it meets for columns of its own, in registers. Three forms, by width:
 //  - narrow (up to 64 units a row): rows by warps, several at a time, sums by shuffles;
-//  - wide (up to 16384 columns): persistent blocks, a row at a time, rows arriving in shared memory
-//    by bulk copies some rows ahead;
+//  - wide (up to 16384 columns): persistent blocks, one or two rows at a time, rows arriving in shared
+//    memory by bulk copies some rows ahead;
 //  - beyond: a block for each row that reads it again for every step.
+// Measured, of what is read and written once: forward 8192 x 12288 bf16 72 us (5.6 TB/s, of 6.7 that a copy reaches),
+// 131072 x 128 bf16 19.6 us (3.4); backward 4099 x 4096 fp32 40 us (5.0), of which 5 are the sum over blocks, 131072 x
+// 128 bf16 28 us (3.6). Short rows are bound by instructions as much (62% of the issue slots): bf16 in and out,
+// two sums by shuffles, and in the backward about ten operations an element.
 // A unit is 16 aligned bytes. Where the width is no multiple of it, rows start inside a unit, each at one of
 // eight (bf16) or four (fp32) places; a thread meets only rows that start at the same place, so that its columns
 // stay its own, and its first and last unit of a row hold elements of the neighbours, which do not count.
@@ -569,8 +573,7 @@ __global__ void __launch_bounds__(512)
     }
 }
 
-// The same for the backward, with dw and db of a thread's columns in registers; two rows at a time where
-// registers allow.
+// The same for the backward, with dw and db of a thread's columns in registers; one or two rows at a time (bwd_rows).
 template <typename T, int NV, bool kRagged>
 __global__ void __launch_bounds__(512)
     norm_bwd_wide_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // dw and db from the n blocks' sums: 32 columns a block, 32 row groups that each add every 32nd partial,
-// then the groups in order.
+// then the groups in order. 5 us; launched under the kernel before it (131072 x 128 bf16 in all 29 us, 31.5 without).
 __global__ void __launch_bounds__(1024)
     norm_reduce_kernel(const float* __restrict__ part, int n, int width, float* __restrict__ dw, float* __restrict__ db) {
     grid_wait_before();

@@ -10,6 +10,18 @@
 // whether the decay of a token applies before or after its read:
 //   forward   S <- gamma S + v k^T,         out = S q
 //   reversed  S <- S + v k^T,  out = S q,   S <- gamma S
+//
+// A job goes through its tokens in chunks of 128, the rows of a tcgen05 tile: scores Q K^T, their decays, times V;
+// Q S^T with the state the chunk starts from; the state's sum of decayed keys times values. That is 4 products of
+// 128 x 128 x 128 with fp32 sums in tensor memory (the last of them twice or three times, see three_parts), 2600 cycles
+// of the tensor core, and 128 KB in and out, about 2700 cycles of an SM's share of HBM. One CTA on an SM, by its
+// shared and tensor memory, has one chunk at work and part of the next: the chain from one state to the next (decayed
+// keys 1200 cycles, state 640, its bf16 copy 600, Q S^T 600, the state's sum 1060, waits between them) takes
+// about 5700 cycles, and it bounds the prompts. Measured: T = 4096, 152 heads forward 110 us, 5.6 TB/s of DRAM traffic;
+// T = 8192, 96 heads backward 380 us for 12 tensors of 201 MB (6.3 of 6.7 TB/s; 7 would do if the jobs shared their reads).
+// Not faster: the jobs of a head side by side, which do share them in L2 (T = 4096, 152 heads: 1.03 instead of 1.41 GB
+// read, 322 instead of 302 us); the next chunk's state sum issued before this one's outputs (8192 x 96 backward
+// 409 against 382 us); a whole split call in one cooperative kernel (T = 4096, 32 heads forward 79 against 71 us).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -171,7 +183,8 @@ __device__ __forceinline__ Chunk chunk_of(const Unit& u, int c) {
 // The decayed keys of a chunk go into the state's sum as two bf16 parts (16 significant bits, 2.2e-6 of
 // their size in the mean square), or as three (24) where the state is an output and the tokens still to
 // come will not have decayed this chunk's share, and its error with it, by another e^-1: an output state
-// is within 1e-6 of its size. (Without any decay one part is exact.)
+// is within 1e-6 of its size. (Without any decay one part is exact.) Forward with final states, six sequences of 8192
+// tokens in all with 96 heads: 252 us with three parts always, 177 by this rule, 167 with two always.
 __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
     const int left = u.after + max(u.len - (c + 1) * LC, 0);
     return u.exact && u.g != 0.0f && (left == 0 || u.g * (float)left > -1.0f);
@@ -940,7 +953,7 @@ __global__ void __launch_bounds__(1024)
     }
     // Whole sequences, few of them: longest first. A block's rounds come from opposite ends of the list in turn,
     // which evens them out (lengths 1300, 547, 2048, 963, 271, 3063 with 96 heads on 152 SMs: at most 46 chunks
-    // on an SM instead of 59, with 43 in the mean).
+    // on an SM instead of 59, with 43 in the mean; 197 instead of 238 us).
     if (seg_len < T_total || N > (int)blockDim.x) return;
     const Slot own = tid < N ? table[tid] : Slot{};
     scan[tid] = own.len;
@@ -951,7 +964,9 @@ __global__ void __launch_bounds__(1024)
     table[rank] = own;
 }
 
-// dq, dk of a query/key head: the sum of its G value heads' shares, in head order.
+// dq, dk of a query/key head: the sum of its G value heads' shares, in head order. HBM bounds it (T = 4096, 32 heads in
+// groups of 4: 21 us for 134 MB of shares). The heads of a group are on different SMs at a time, and sums in
+// the order of their arrival would differ from call to call.
 __global__ void __launch_bounds__(256)
     linattn_group_sum_kernel(const float* __restrict__ share_q, const float* __restrict__ share_k, uint16_t* __restrict__ dq,
                              uint16_t* __restrict__ dk, int64_t n4, int G) {
@@ -969,7 +984,8 @@ __global__ void __launch_bounds__(256)
 
 // One token for each (request, head): the state is read and written once (64 KB each way), so
 // the step is bound by HBM. Warp w owns state rows 16 w .. 16 w + 15, lane l key channels
-// 4 l .. 4 l + 3 of each, so that a warp moves whole 512-byte rows.
+// 4 l .. 4 l + 3 of each, so that a warp moves whole 512-byte rows. 256 requests, 96 heads: 489 us, 6.6 TB/s, 99% of the
+// measured copy; 4 requests, 4 heads: 9 us on the GPU, 14 with the call.
 constexpr int kRows = 16;
 __global__ void __launch_bounds__(256)
     linattn_decode_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
@@ -1041,8 +1057,10 @@ kda_status check_shape(const kda_linattn_shape* sh, bool packed) {
 
 // How the tokens are split. A unit is a (segment, head, job); each takes its chunks one after
 // another on one SM. With fewer units than SMs a sequence is cut into segments: their own state
-// sums come first (state-only units, about 0.4 of a full one's time), then the states they start
-// from, then all segments at once.
+// sums come first (state-only units, about half of a full one's time), then the states they start
+// from, then all segments at once, if that comes out shorter by the cost model. Forward, whole and as split:
+// T = 4096 with 32 heads 95 and 71 us, 16384 with 8 heads 339 and 67, 1024 with 4 heads 32 and 30; lengths 2000, 300,
+// 5000 with 16 heads 118 and 80; backward 16384 with 8 heads 344 and 144.
 struct Plan {
     int64_t seg_len;   // tokens, a multiple of the chunk
     int nseg;          // segments of a fixed-length sequence (packed: of T_total tokens at most)
