@@ -67,7 +67,7 @@ MEASURED_TRAFFIC = {
 
 
 # files that do not build the kernels of the forward + backward step
-_NOT_STEP_SOURCES = ("kda_decode.cu", "kda_diag.cu", "kda_noalloc.cu")
+_NOT_STEP_SOURCES = ("kda_decode.cu", "kda_diag.cu", "kda_layernorm.cu", "kda_linattn.cu", "kda_noalloc.cu", "umma_bf16.cuh")
 
 
 def _sources_hash():

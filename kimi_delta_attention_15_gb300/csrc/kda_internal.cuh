@@ -3,7 +3,6 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
-#include <utility>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -93,23 +92,6 @@ struct Layout {
     int64_t G;           // value heads per query/key head
     // (kept at 14 fields: kernels that take the layout by value spill registers once it grows)
 };
-
-// A launch; with `overlap` the kernel may start before the one before it on the stream has finished, and waits for
-// it (grid_wait_before) ahead of anything it reads or writes in global memory.
-template <typename... P, typename... A>
-inline void launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool overlap, A&&... args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = grid;
-    c.blockDim = block;
-    c.dynamicSmemBytes = smem;
-    c.stream = stream;
-    c.attrs = &at;
-    c.numAttrs = overlap ? 1 : 0;
-    cudaLaunchKernelEx(&c, kernel, std::forward<A>(args)...);   // an error is left for cudaGetLastError
-}
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

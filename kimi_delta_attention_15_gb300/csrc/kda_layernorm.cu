@@ -20,7 +20,7 @@
 #include <cmath>
 #include <cstdio>
 #include "kda_internal.cuh"
-#include "umma.cuh"
+#include "umma_bf16.cuh"
 
 namespace kda {
 void set_last_error_text(const char* msg);

@@ -28,7 +28,7 @@
 #include <cstdio>
 #include <cuda.h>
 #include "kda_internal.cuh"
-#include "umma.cuh"
+#include "umma_bf16.cuh"
 
 namespace kda {
 void set_last_error_text(const char* msg);
