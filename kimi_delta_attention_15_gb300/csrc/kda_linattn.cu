@@ -316,11 +316,11 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
         x.next(a, units);
         if (!x.more) return;
         next = place(x);   // chunk n + 1: its keys and values once chunk n - 1 is done
-        if (n > 0 && !mbar_wait_asleep(&sm.all[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1))) break;
+        if (n > 0 && !mbar_wait(&sm.all[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1))) break;
         tile(sm.K[(n + 1) & 1], next.k, next, &sm.full_k[(n + 1) & 1]);
         tile(sm.V[(n + 1) & 1], next.v, next, &sm.full_v[(n + 1) & 1]);
         if (!state_only) ahead(next.q, next);   // on their way into L2: from there they arrive in time
-        if (!mbar_wait_asleep(&sm.qs, (uint32_t)(n & 1))) break;
+        if (!mbar_wait(&sm.qs, (uint32_t)(n & 1))) break;
         q_tile(next);
     }
     raise_status(a.ws, KDA_ERR_TIMEOUT);
@@ -360,7 +360,7 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
     At x;
     x.first(a, units);
     auto score = [&](int m) {   // scores of chunk m
-        if (!mbar_wait_asleep(&sm.full_k[m & 1], (uint32_t)((m >> 1) & 1)) || !mbar_wait_asleep(&sm.full_q, (uint32_t)(m & 1))) return false;
+        if (!mbar_wait(&sm.full_k[m & 1], (uint32_t)((m >> 1) & 1)) || !mbar_wait(&sm.full_q, (uint32_t)(m & 1))) return false;
         if (!state_only) product_ss<false>(tm + kColP, q, dk0 + (uint64_t)((m & 1) * (kTile / 16)), kk);
         umma_commit(&sm.qk);
         return true;
@@ -370,18 +370,18 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
         const uint32_t ph = (uint32_t)(n & 1);
         const uint64_t v = dv0 + (uint64_t)(ph * (kTile / 16));
         const bool carried = x.c > 0 || x.u.s_in, sum = x.c + 1 < x.chunks || x.u.s_out, three = sum && three_parts(x.u, x.c);
-        if (!(ok = mbar_wait_asleep(&sm.s, ph) && (n == 0 || mbar_wait_asleep(&sm.r, ph ^ 1u)))) break;
+        if (!(ok = mbar_wait(&sm.s, ph) && (n == 0 || mbar_wait(&sm.r, ph ^ 1u)))) break;
         tc_fence_after();
         if (!state_only && carried) product_ss<true>(tm + kColO, q, ds, kn);
         umma_commit(&sm.qs);
-        if (!(ok = mbar_wait_asleep(&sm.piece, ph) && mbar_wait_asleep(&sm.full_v[n & 1], (uint32_t)((n >> 1) & 1)))) break;
+        if (!(ok = mbar_wait(&sm.piece, ph) && mbar_wait(&sm.full_v[n & 1], (uint32_t)((n >> 1) & 1)))) break;
         tc_fence_after();
         if (sum) {   // small parts first: the accumulator is rounded at its size
             product_ts<false>(tm + kColDS, tm + kColMid, v, kn);
             product_ts<true>(tm + kColDS, tm + kColHi, v, kn);
         }
         if (!three) umma_commit(&sm.ds);
-        if (!(ok = mbar_wait_asleep(&sm.o, ph) && mbar_wait_asleep(&sm.p, ph))) break;
+        if (!(ok = mbar_wait(&sm.o, ph) && mbar_wait(&sm.p, ph))) break;
         tc_fence_after();
         if (!state_only) {
             if (kFine) {
@@ -396,7 +396,7 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
         }
         umma_commit(&sm.pv);
         if (three) {
-            if (!(ok = mbar_wait_asleep(&sm.low, (uint32_t)(lows++ & 1)))) break;
+            if (!(ok = mbar_wait(&sm.low, (uint32_t)(lows++ & 1)))) break;
             tc_fence_after();
             product_ts<true>(tm + kColDS, tm + low_col(x.u.rev), v, kn);
             umma_commit(&sm.ds);
@@ -408,7 +408,7 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
     }
     if (!ok) raise_status(a.ws, KDA_ERR_TIMEOUT);
     umma_commit(&sm.end);   // no MMA is in flight when the tensor memory is freed
-    mbar_wait_asleep(&sm.end, 0);
+    mbar_wait(&sm.end, 0);
 }
 
 // --- scores -> decayed bf16 scores in TMEM; outputs -> shared memory -> global, a warp's 32 rows by TMA (or,
