@@ -37,8 +37,9 @@ namespace {
 
 constexpr int LC = 128;                       // tokens of a chunk
 constexpr int kSMs = 152;                     // of a GB300; one persistent CTA on each
-// the cost model of the split, in chunk times of a full unit
-constexpr double kStateOnly = 0.5, kUnitChunks = 1.0, kSplitChunks = 4.0;
+// the cost model of the split, in chunk times of a full unit (2.7 us): a state-only chunk, the start of a unit, the two more
+// launches, and each state that is carried (fitted to T = 512 .. 16384 with 1 .. 64 heads cut into 1 .. 64 segments)
+constexpr double kStateOnly = 0.55, kUnitChunks = 1.0, kSplitChunks = 4.5, kCarried = 1.0 / 40;
 // Calls of up to so many tokens have their scores in two bf16 parts (16 significant bits). Rounded once, a score is off
 // by up to 2^-8 of itself; over many scores that is 1.4 times the outputs' own rounding in the mean square, but in the few
 // outputs of a short call it was up to 1.7 times, wherever a single score makes up a row.
@@ -1059,8 +1060,8 @@ kda_status check_shape(const kda_linattn_shape* sh, bool packed) {
 // another on one SM. With fewer units than SMs a sequence is cut into segments: their own state
 // sums come first (state-only units, about half of a full one's time), then the states they start
 // from, then all segments at once, if that comes out shorter by the cost model. Forward, whole and as split:
-// T = 4096 with 32 heads 95 and 71 us, 16384 with 8 heads 339 and 67, 1024 with 4 heads 32 and 30; lengths 2000, 300,
-// 5000 with 16 heads 118 and 80; backward 16384 with 8 heads 344 and 144.
+// T = 4096 with 32 heads 92 and 70 us, 16384 with 8 heads 328 and 65, 1024 with 4 heads 32 and 30 (not split: 1024
+// with 16 heads, 32 and 34; 4096 with 64 heads, 93 and 109); backward 16384 with 8 heads 332 and 142.
 struct Plan {
     int64_t seg_len;   // tokens, a multiple of the chunk
     int nseg;          // segments of a fixed-length sequence (packed: of T_total tokens at most)
@@ -1076,7 +1077,7 @@ Plan plan_of(const kda_linattn_shape* sh, bool packed, int jobs) {
     for (int s = 1; s <= 64 && s <= (chunks > 0 ? chunks : 1); ++s) {
         const double len = (double)((chunks + s - 1) / s);
         double t = (double)((rows * s + kSMs - 1) / kSMs) * (len + kUnitChunks);
-        if (s > 1) t += (double)((pre * (s - 1) + kSMs - 1) / kSMs) * (kStateOnly * len + kUnitChunks) + kSplitChunks;
+        if (s > 1) t += (double)((pre * (s - 1) + kSMs - 1) / kSMs) * (kStateOnly * len + kUnitChunks) + kSplitChunks + kCarried * (double)(rows * s);
         if (s == 1 || t < least) { least = t; best = s; }
     }
     Plan p;
