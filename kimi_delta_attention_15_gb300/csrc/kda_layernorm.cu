@@ -10,8 +10,8 @@
 //    memory by bulk copies some rows ahead;
 //  - beyond: a block for each row that reads it again for every step.
 // Measured, of what is read and written once: forward 8192 x 12288 bf16 72 us (5.6 TB/s, of 6.7 that a copy reaches),
-// 131072 x 128 bf16 19.6 us (3.4); backward 4099 x 4096 fp32 40 us (5.0), of which 5 are the sum over blocks, 131072 x
-// 128 bf16 28 us (3.6). Short rows are bound by instructions as much (62% of the issue slots): bf16 in and out,
+// 131072 x 128 bf16 18.7 us (3.6); backward 4099 x 4096 fp32 40 us (5.0), of which 5 are the sum over blocks, 131072 x
+// 128 bf16 24.7 us (4.1). Short rows are bound by instructions as much (62% of the issue slots): bf16 in and out,
 // two sums by shuffles, and in the backward about ten operations an element.
 // A unit is 16 aligned bytes. Where the width is no multiple of it, rows start inside a unit, each at one of
 // eight (bf16) or four (fp32) places; a thread meets only rows that start at the same place, so that its columns
@@ -215,16 +215,18 @@ template <typename T, int NV, bool kRagged> struct Params {
 };
 
 // ---------------------------------------------------------------------------------- narrow
-// Lanes lpr * s .. lpr * (s + 1) - 1 of a warp hold row s of its 32 / lpr rows, lane l of them units
-// l, l + 32, .. (lpr < 32: one unit). A block has eight warps and all rows of a step lie a multiple of eight
-// apart from the step's before.
+// Lanes lpr * s .. lpr * (s + 1) - 1 of a warp hold row s of its 32 / lpr rows, lane l of them units l and l + lpr
+// (with one unit a lane and twice the lanes the sums' shuffles cost as much for half the rows: backward 131072 x 128
+// bf16 28 instead of 24.7 us, forward 161374 x 128 fp32 39 instead of 30). A block has eight warps, and the rows of a
+// step lie a multiple of eight from those of the step before.
+constexpr int kNarrowNV = 2;
 __device__ __forceinline__ float lanes_sum(float x, int lpr) {
     for (int o = lpr >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// rows in flight and blocks on an SM of the forward, by a thread's columns (bf16: 131072 x 128 19.5 us with (2, 4), 24.5
-// with (1, 6); 32768 x 512 20.7 and 17.9; 32768 x 501 32 and 35)
+// rows in flight of the forward, by a thread's columns, and blocks on an SM (32768 x 512 bf16 17.9 us with (1, 6), 20.7 with
+// (2, 4); 32768 x 501 35 and 30)
 __host__ __device__ constexpr int fwd_rows(int columns, bool ragged) { return columns <= 8 || ragged ? 2 : 1; }
 template <typename T, int NV, bool kRagged>
 __global__ void __launch_bounds__(kThreads)
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * rpw;
     const float inv = 1.0f / (float)width;
     Columns<T, NV, kRagged> c;
-    c.init(l, 32, first + sub, width);
+    c.init(l, lpr, first + sub, width);
     Params<T, NV, kRagged> pw, pb;
     pw.init(c, w, 1.0f);
     pb.init(c, b, 0.0f);
@@ -286,16 +288,16 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// rows in flight and blocks on an SM of the backward (131072 x 128 bf16 27.8 us with (2, 3), 29.6 with (3, 2); 65536 x
-// 256 fp32 35 us with (3, 2), 38 with (2, 3); 32768 x 512 bf16 25 us with (2, 2), 40 with (2, 3), 33 with (1, 2))
-__host__ __device__ constexpr int bwd_narrow_rows(int nv, int columns) { return nv > 1 && columns <= 8 ? 3 : 2; }
-__host__ __device__ constexpr int bwd_narrow_blocks(int nv) { return nv == 1 ? 3 : 2; }
+// rows in flight of the backward, two blocks on an SM (65536 x 256 fp32 35 us, with two rows 38; 32768 x 512 bf16 25 us,
+// with one 33; three blocks of two rows 40)
+__host__ __device__ constexpr int bwd_narrow_rows(int columns) { return columns <= 8 ? 3 : 2; }
+constexpr int kNarrowBlocks = 2;
 template <typename T, int NV, bool kRagged>
-__global__ void __launch_bounds__(kThreads, bwd_narrow_blocks(NV))
+__global__ void __launch_bounds__(kThreads, kNarrowBlocks)
     norm_bwd_narrow_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                            const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                            float* __restrict__ part, int64_t rows, int width, int lpr) {
-    constexpr int V = Unit<T>::V, R = bwd_narrow_rows(NV, V * NV);
+    constexpr int V = Unit<T>::V, R = bwd_narrow_rows(V * NV);
     extern __shared__ float acc[];   // [warps, or warps * rpw][2][width]
     grid_launch_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, bwd_narrow_blocks(NV))
     const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * rpw;
     const float inv = 1.0f / (float)width;
     Columns<T, NV, kRagged> c;
-    c.init(l, 32, first + sub, width);
+    c.init(l, lpr, first + sub, width);
     float wv[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -427,6 +429,14 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float2 (&buf)[32]
 // 8192 x 4096 bf16 (16 columns) 54 us with one, 57 with two
 __host__ __device__ constexpr int bwd_rows(int columns) { return columns <= 8 ? 2 : 1; }
 
+// Registers of a thread in the forward (inputs 1) and the backward (2), by its units and columns: fewer leave room for more
+// rows on an SM, and too few spill (forward 8192 x 4097 bf16 46 us with 96, 54 with 80, 67 with 112; 8192 x 4096 bf16 29.5
+// with 80, 31.5 with 96; backward 16384 x 1024 bf16 32.5 with 96, 35.7 with 112; 4099 x 4096 fp32 41 with 112, 51 with 80).
+__host__ __device__ constexpr int wide_regs(int inputs, int nv, int columns, bool ragged) {
+    return inputs == 1 ? (columns <= 8 ? 64 : columns < 16 || (columns == 16 && !ragged) ? 80 : columns == 16 ? 96 : 128)
+                       : (columns <= 8 ? (nv == 1 ? 96 : 112) : 128);
+}
+
 // Rows on their way to shared memory: a step of R rows (r, r + stride, ..) of each input, `stages` steps
 // ahead, of each row the aligned span around it. The last bytes of a tensor whose size is no multiple of
 // 16 are not copied: take() reads them from global memory.
@@ -492,7 +502,7 @@ __device__ __forceinline__ Rows<R> rows_of(uint8_t* smem, size_t row_bytes, int6
 // holds units t, t + blockDim.x, .. A copy that has not arrived after 2 s leaves NaN in its rows' outputs
 // (there is no workspace to report it in).
 template <typename T, int NV, bool kRagged>
-__global__ void __launch_bounds__(512)
+__global__ void __maxnreg__(wide_regs(1, NV, NV * Unit<T>::V, kRagged))
     norm_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                          float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int pitch, int stages,
                          float eps) {
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(512)
 
 // The same for the backward, with dw and db of a thread's columns in registers; one or two rows at a time (bwd_rows).
 template <typename T, int NV, bool kRagged>
-__global__ void __launch_bounds__(512)
+__global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
     norm_bwd_wide_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                          const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                          float* __restrict__ part, int64_t rows, int width, int pitch, int stages) {
@@ -769,7 +779,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // dw and db from the n blocks' sums: 32 columns a block, 32 row groups that each add every 32nd partial,
-// then the groups in order. 5 us; launched under the kernel before it (131072 x 128 bf16 in all 29 us, 31.5 without).
+// then the groups in order. 5 us; launched under the kernel before it (4099 x 4096 fp32 in all 41 us, 44 without).
 __global__ void __launch_bounds__(1024)
     norm_reduce_kernel(const float* __restrict__ part, int n, int width, float* __restrict__ dw, float* __restrict__ db) {
     grid_wait_before();
@@ -809,7 +819,7 @@ constexpr int kMostParts = 4 * kSMs;   // blocks whose sums of dw and db are kep
 
 // Which form a width takes, and its launch.
 struct Form {
-    int units, lpr, nv;      // most units of a row; lpr: lanes of a row (narrow), 0: wide or any
+    int units, lpr, nv;      // most units of a row; lpr: lanes of a row (narrow), 0: wide or any; units a thread (wide)
     bool ragged, wide;
     int threads, pitch, stages, per_sm;
     size_t smem;
@@ -821,8 +831,7 @@ Form form_of(long long width, size_t size, int inputs) {
     f.units = (int)((width + (f.ragged ? v - 1 : 0) + v - 1) / v);
     if (f.units <= kNarrowUnits) {
         f.lpr = 1;
-        while (f.lpr < f.units && f.lpr < 32) f.lpr *= 2;
-        f.nv = f.units <= 32 ? 1 : 2;
+        while (kNarrowNV * f.lpr < f.units) f.lpr *= 2;
         return f;
     }
     if (width > kWideMost) return f;
@@ -831,12 +840,11 @@ Form form_of(long long width, size_t size, int inputs) {
     // Two units a thread and small blocks, so that many rows are in flight; more units where 512 threads do not hold
     // the row; one in the backward of short rows, whose blocks are limited by kMostParts (20000 x 777 bf16 43 us,
     // 54 with two).
-    // Threads on an SM, by registers: 512 with 24 columns (backward: 16), 1024 otherwise (8192 x 12288 backward
-    // 140 us, 156 with 1024; 4099 x 4096 fp32 forward 27 us, 32 with 512).
     f.nv = inputs == 2 && f.units <= 128 ? 1 : 2;
     while (f.units > f.nv * 512) f.nv = f.nv == 4 ? 8 : f.nv + 1;
     f.threads = ((f.units + f.nv - 1) / f.nv + 31) / 32 * 32;
-    const int fit = (f.nv * v * (inputs + 1) >= 48 ? 512 : 1024) / f.threads;
+    // warps that an SM's registers hold, in four quarters
+    const int fit = 4 * (65536 / 4 / (32 * wide_regs(inputs, f.nv, f.nv * v, f.ragged))) / (f.threads / 32);
     f.per_sm = std::min(std::max(fit, 1), inputs == 1 ? 16 : kMostParts / kSMs);
     const int stage = f.pitch * inputs * (inputs == 1 ? 2 : bwd_rows(f.nv * v));
     // up to four steps ahead, within the SM's shared memory; fewer blocks rather than none ahead
@@ -874,10 +882,7 @@ kda_status fwd(const Form& f, long long rows, int width, float eps, const void* 
     const T* x = static_cast<const T*>(xv);
     T* y = static_cast<T*>(yv);
 #define KDA_NORM(fn, n) return fn<T, n, kRagged>(f, rows, width, eps, x, w, b, y, mean, rstd, s)
-    if (f.lpr) {
-        if (f.nv == 1) KDA_NORM(fwd_narrow, 1);
-        KDA_NORM(fwd_narrow, 2);
-    }
+    if (f.lpr) KDA_NORM(fwd_narrow, kNarrowNV);
     if (f.wide) {
         if (f.nv == 2) KDA_NORM(fwd_wide, 2);
         if (f.nv == 3) KDA_NORM(fwd_wide, 3);
@@ -904,7 +909,7 @@ kda_status bwd_narrow(const Form& f, long long rows, int width, const T* x, cons
     const int rpw = 32 / f.lpr;
     const long long rpb = (long long)(kThreads / 32) * rpw;
     const size_t smem = (size_t)rpb * 2 * width * sizeof(float);
-    *parts = (int)blocks((rows + rpb - 1) / rpb, bwd_narrow_blocks(NV) * kSMs);   // as many as are resident
+    *parts = (int)blocks((rows + rpb - 1) / rpb, kNarrowBlocks * kSMs);   // as many as are resident
     norm_bwd_narrow_kernel<T, NV, kRagged><<<*parts, kThreads, smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.lpr);
     return launched("kda_layernorm_bwd launch");
 }
@@ -915,10 +920,7 @@ kda_status bwd(const Form& f, long long rows, int width, const void* xv, const v
     const T *x = static_cast<const T*>(xv), *dy = static_cast<const T*>(dyv);
     T* dx = static_cast<T*>(dxv);
 #define KDA_NORM(fn, n) return fn<T, n, kRagged>(f, rows, width, x, dy, w, mean, rstd, dx, part, parts, s)
-    if (f.lpr) {
-        if (f.nv == 1) KDA_NORM(bwd_narrow, 1);
-        KDA_NORM(bwd_narrow, 2);
-    }
+    if (f.lpr) KDA_NORM(bwd_narrow, kNarrowNV);
     if (f.wide) {
         if (f.nv == 1) KDA_NORM(bwd_wide, 1);
         if (f.nv == 2) KDA_NORM(bwd_wide, 2);
