@@ -36,17 +36,17 @@ __device__ __forceinline__ float get(const float* p) { return *p; }
 __device__ __forceinline__ void put(uint16_t* p, float x) { *p = f2bf(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 
-// A unit, 16 bytes, in registers as it is stored, and as fp32.
+// A unit, 16 bytes, in registers as it is stored, and as P pairs of fp32 (packed arithmetic: half the instructions).
 template <typename T> struct Unit;
 template <> struct Unit<uint16_t> {
-    static constexpr int V = 8;
+    static constexpr int V = 8, P = 4;
     uint4 r;
     __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void load_stream(const uint16_t* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ float at(int i) const {
-        const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
-        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    __device__ __forceinline__ f32x2 at(int i) const {   // elements 2 i and 2 i + 1
+        const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+        return two(w << 16, w & 0xffff0000u);
     }
     __device__ __forceinline__ void keep(uint32_t ok) {   // the elements of these bits, zero elsewhere
         r.x &= ((ok & 1u) ? 0xffffu : 0u) | ((ok & 2u) ? 0xffff0000u : 0u);
@@ -60,23 +60,17 @@ template <> struct Unit<uint16_t> {
         for (int i = 0; i < 8; ++i) e[i] = (ok >> i) & 1u ? p[i] : 0u;
         r = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
     }
-    __device__ static __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    __device__ static __forceinline__ uint32_t pack(f32x2 f) {
+        const float2 x = parts(f);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ static __forceinline__ void store(uint16_t* p, const f32x2 (&f)[4]) {
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack(f[0]), pack(f[1]), pack(f[2]), pack(f[3])));
     }
     // the first or last elements of a unit (ok) in as few stores as their number has bits, others one by one
-    __device__ static __forceinline__ void store_some(uint16_t* p, const float (&f)[8], uint32_t ok) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+    __device__ static __forceinline__ void store_some(uint16_t* p, const f32x2 (&f)[4], uint32_t ok) {
+        const uint32_t w[4] = {pack(f[0]), pack(f[1]), pack(f[2]), pack(f[3])};
         if ((ok & 15u) == 15u) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         if ((ok >> 4) == 15u) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
         const bool upper = (ok & 15u) == 0u || (ok & 15u) == 15u;    // the half that is not done
@@ -84,7 +78,7 @@ template <> struct Unit<uint16_t> {
         if (!upper && ok >> 4 && ok >> 4 != 15u) {                   // a row inside a unit
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if ((ok >> (4 + i)) & 1u) put(p + 4 + i, f[4 + i]);
+                if ((ok >> (4 + i)) & 1u) p[4 + i] = (uint16_t)(i & 1 ? w[2 + i / 2] >> 16 : w[2 + i / 2]);
         }
         if (r == 15u) return;
         uint16_t* const h = p + (upper ? 4 : 0);
@@ -97,25 +91,28 @@ template <> struct Unit<uint16_t> {
     }
 };
 template <> struct Unit<float> {
-    static constexpr int V = 4;
+    static constexpr int V = 4, P = 2;
     float4 r;
     __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void load_stream(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void zero() { r = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-    __device__ __forceinline__ float at(int i) const { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
+    __device__ __forceinline__ f32x2 at(int i) const { return i == 0 ? two(r.x, r.y) : two(r.z, r.w); }
     __device__ __forceinline__ void keep(uint32_t ok) {
         r = make_float4((ok & 1u) ? r.x : 0.0f, (ok & 2u) ? r.y : 0.0f, (ok & 4u) ? r.z : 0.0f, (ok & 8u) ? r.w : 0.0f);
     }
     __device__ __forceinline__ void load_some(const float* p, uint32_t ok) {
         r = make_float4((ok & 1u) ? p[0] : 0.0f, (ok & 2u) ? p[1] : 0.0f, (ok & 4u) ? p[2] : 0.0f, (ok & 8u) ? p[3] : 0.0f);
     }
-    __device__ static __forceinline__ void store(float* p, const float (&f)[4]) {
-        __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __device__ static __forceinline__ void store(float* p, const f32x2 (&f)[2]) {
+        const float2 a = parts(f[0]), b = parts(f[1]);
+        __stcs(reinterpret_cast<float4*>(p), make_float4(a.x, a.y, b.x, b.y));
     }
-    __device__ static __forceinline__ void store_some(float* p, const float (&f)[4], uint32_t ok) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if ((ok >> i) & 1u) p[i] = f[i];
+    __device__ static __forceinline__ void store_some(float* p, const f32x2 (&f)[2], uint32_t ok) {
+        const float2 a = parts(f[0]), b = parts(f[1]);
+        if (ok & 1u) p[0] = a.x;
+        if (ok & 2u) p[1] = a.y;
+        if (ok & 4u) p[2] = b.x;
+        if (ok & 8u) p[3] = b.y;
     }
 };
 
@@ -124,7 +121,7 @@ template <> struct Unit<float> {
 // of V have the same off, and a thread meets only such rows, so that a width that is no multiple of V (kRagged)
 // differs only in the edge units: bits of `ok` say which elements of a unit are the row's.
 template <typename T, int NV, bool kRagged> struct Columns {
-    static constexpr int V = Unit<T>::V;
+    static constexpr int V = Unit<T>::V, P = V / 2;
     static constexpr uint32_t kAll = (1u << V) - 1u;
     int first, step, off, units;
     uint32_t bits[kRagged ? NV : 1];
@@ -155,36 +152,50 @@ template <typename T, int NV, bool kRagged> struct Columns {
     __device__ __forceinline__ void keep(Unit<T>& u, int k) const {
         if (!whole(k)) u.keep(ok(k));
     }
-    __device__ __forceinline__ void store(T* row, int k, const float (&f)[V]) const {
+    __device__ __forceinline__ void store(T* row, int k, const f32x2 (&f)[P]) const {
         if (whole(k)) {
             Unit<T>::store(row + column(k), f);
         } else {
             Unit<T>::store_some(row + column(k), f, ok(k));
         }
     }
-    // sum of (x - mu)^2 over the unit's elements that are the row's
-    __device__ __forceinline__ float squares(const Unit<T>& u, int k, float mu) const {
-        float s = 0.0f;
+    // the same for fp32 sums of the columns, at any alignment
+    __device__ __forceinline__ void leave(float* sums, int k, const f32x2 (&f)[P]) const {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float d = (ok(k) >> e) & 1u ? u.at(e) - mu : 0.0f;
-            s += d * d;
+        for (int i = 0; i < P; ++i) {
+            const float2 x = parts(f[i]);
+            if ((ok(k) >> (2 * i)) & 1u) sums[column(k) + 2 * i] = x.x;
+            if ((ok(k) >> (2 * i + 1)) & 1u) sums[column(k) + 2 * i + 1] = x.y;
         }
-        return s;
+    }
+    // adds (x - mu)^2 of the unit's elements that are the row's to a pair of sums
+    __device__ __forceinline__ void squares(f32x2& s, const Unit<T>& u, int k, f32x2 minus_mu) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            f32x2 d = add2(u.at(i), minus_mu);
+            if constexpr (kRagged) {
+                const float2 x = parts(d);
+                d = two((ok(k) >> (2 * i)) & 1u ? x.x : 0.0f, (ok(k) >> (2 * i + 1)) & 1u ? x.y : 0.0f);
+            }
+            s = fma2(d, d, s);
+        }
     }
     // the parameters of unit k, `other` without them
-    __device__ __forceinline__ void params(const float* p, int k, float other, float (&f)[V]) const {
+    __device__ __forceinline__ void params(const float* p, int k, float other, f32x2 (&f)[P]) const {
         if (!p || !in(k)) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = other;
+            for (int i = 0; i < P; ++i) f[i] = two(other, other);
         } else if constexpr (kRagged) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = (ok(k) >> e) & 1u ? __ldg(p + column(k) + e) : other;
+            for (int i = 0; i < P; ++i)
+                f[i] = two((ok(k) >> (2 * i)) & 1u ? __ldg(p + column(k) + 2 * i) : other,
+                           (ok(k) >> (2 * i + 1)) & 1u ? __ldg(p + column(k) + 2 * i + 1) : other);
         } else {
 #pragma unroll
-            for (int e = 0; e < V; e += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(p + column(k) + e));
-                f[e] = x.x; f[e + 1] = x.y; f[e + 2] = x.z; f[e + 3] = x.w;
+            for (int i = 0; i < P; i += 2) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(p + column(k) + 2 * i));
+                f[i] = two(x.x, x.y);
+                f[i + 1] = two(x.z, x.w);
             }
         }
     }
@@ -194,11 +205,11 @@ template <typename T, int NV, bool kRagged> struct Columns {
 // (they are as long as two or four bf16 rows: fetched for every row, 96 KB of them at a width of 12288
 // came from L2 each time and held the forward at 3.1 of 6.7 TB/s).
 template <typename T, int NV, bool kRagged> struct Params {
-    static constexpr int V = Unit<T>::V;
-    static constexpr bool kept = NV * V <= 24;
+    static constexpr int P = Unit<T>::P;
+    static constexpr bool kept = NV * Unit<T>::V <= 24;
     const float* p;
     float other;
-    float f[kept ? NV : 1][V];
+    f32x2 f[kept ? NV : 1][P];
     __device__ __forceinline__ void init(const Columns<T, NV, kRagged>& c, const float* from, float without) {
         p = from;
         other = without;
@@ -206,13 +217,23 @@ template <typename T, int NV, bool kRagged> struct Params {
 #pragma unroll
             for (int k = 0; k < NV; ++k) c.params(p, k, other, f[k]);
     }
-    __device__ __forceinline__ void at(const Columns<T, NV, kRagged>& c, int k, float (&o)[V]) const {
+    __device__ __forceinline__ void at(const Columns<T, NV, kRagged>& c, int k, f32x2 (&o)[P]) const {
         if constexpr (kept)
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = f[k][e];
+            for (int i = 0; i < P; ++i) o[i] = f[k][i];
         else c.params(p, k, other, o);
     }
 };
+
+__device__ __forceinline__ float both(f32x2 x) {
+    const float2 p = parts(x);
+    return p.x + p.y;
+}
+// y of a pair, and dx of a pair: xh and a = dy w, then rstd (a - s1 - xh s2)
+__device__ __forceinline__ f32x2 norm_y(f32x2 x, f32x2 minus_mu, f32x2 rs, f32x2 w, f32x2 b) { return fma2(mul2(add2(x, minus_mu), rs), w, b); }
+__device__ __forceinline__ f32x2 norm_dx(f32x2 xh, f32x2 a, f32x2 rs, f32x2 minus_s1, f32x2 minus_s2) {
+    return mul2(rs, fma2(xh, minus_s2, add2(a, minus_s1)));
+}
 
 // ---------------------------------------------------------------------------------- narrow
 // Lanes lpr * s .. lpr * (s + 1) - 1 of a warp hold row s of its 32 / lpr rows, lane l of them units l and l + lpr
@@ -232,7 +253,7 @@ template <typename T, int NV, bool kRagged>
 __global__ void __launch_bounds__(kThreads)
     norm_fwd_narrow_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                            float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int lpr, float eps) {
-    constexpr int V = Unit<T>::V, R = fwd_rows(V * NV, kRagged);
+    constexpr int P = Unit<T>::P, R = fwd_rows(2 * P * NV, kRagged);
     const int lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * rpw;
     const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * rpw;
@@ -256,28 +277,30 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             const int64_t r = r0 + q * step + sub;
-            float s = 0.0f;
+            f32x2 s = 0ull;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 c.keep(u[q][k], k);
 #pragma unroll
-                for (int e = 0; e < V; ++e) s += u[q][k].at(e);
+                for (int i = 0; i < P; ++i) s = add2(s, u[q][k].at(i));
             }
-            const float mu = lanes_sum(s, lpr) * inv;
-            s = 0.0f;
+            const float mu = lanes_sum(both(s), lpr) * inv;
+            const f32x2 minus_mu = two(-mu, -mu);
+            s = 0ull;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (c.in(k)) s += c.squares(u[q][k], k, mu);
-            const float rs = rsqrtf(lanes_sum(s, lpr) * inv + eps);
+                if (c.in(k)) c.squares(s, u[q][k], k, minus_mu);
+            const float rs = rsqrtf(lanes_sum(both(s), lpr) * inv + eps);
+            const f32x2 rs2 = two(rs, rs);
             if (r >= rows) continue;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (c.in(k)) {
-                    float wv[V], bv[V], o[V];
+                    f32x2 wv[P], bv[P], o[P];
                     pw.at(c, k, wv);
                     pb.at(c, k, bv);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] = (u[q][k].at(e) - mu) * rs * wv[e] + bv[e];
+                    for (int i = 0; i < P; ++i) o[i] = norm_y(u[q][k].at(i), minus_mu, rs2, wv[i], bv[i]);
                     c.store(y + r * width, k, o);
                 }
             if (l == 0) {
@@ -297,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, kNarrowBlocks)
     norm_bwd_narrow_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                            const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                            float* __restrict__ part, int64_t rows, int width, int lpr) {
-    constexpr int V = Unit<T>::V, R = bwd_narrow_rows(V * NV);
+    constexpr int P = Unit<T>::P, R = bwd_narrow_rows(2 * P * NV);
     extern __shared__ float acc[];   // [warps, or warps * rpw][2][width]
     grid_launch_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / lpr, l = lane % lpr, rpw = 32 / lpr;
@@ -306,12 +329,12 @@ __global__ void __launch_bounds__(kThreads, kNarrowBlocks)
     const float inv = 1.0f / (float)width;
     Columns<T, NV, kRagged> c;
     c.init(l, lpr, first + sub, width);
-    float wv[NV][V], dw[NV][V], db[NV][V];
+    f32x2 wv[NV][P], dw[NV][P], db[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         c.params(w, k, 1.0f, wv[k]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
+        for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = 0ull;
     }
     for (int64_t r0 = first; r0 < rows; r0 += R * step) {
         Unit<T> ux[R][NV], ug[R][NV];
@@ -336,30 +359,30 @@ __global__ void __launch_bounds__(kThreads, kNarrowBlocks)
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             const int64_t r = r0 + q * step + sub;
-            float s1 = 0.0f, s2 = 0.0f;
+            f32x2 s1 = 0ull, s2 = 0ull;
+            const f32x2 minus_mu = two(-mu[q], -mu[q]), rs2 = two(rs[q], rs[q]);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 c.keep(ux[q][k], k);
                 c.keep(ug[q][k], k);   // zero where the element is not the row's: it adds nothing
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float g = ug[q][k].at(e), h = (ux[q][k].at(e) - mu[q]) * rs[q], a = g * wv[k][e];
-                    s1 += a;
-                    s2 += a * h;
-                    dw[k][e] += g * h;
-                    db[k][e] += g;
+                for (int i = 0; i < P; ++i) {
+                    const f32x2 g = ug[q][k].at(i), h = mul2(add2(ux[q][k].at(i), minus_mu), rs2), a = mul2(g, wv[k][i]);
+                    s1 = add2(s1, a);
+                    s2 = fma2(a, h, s2);
+                    dw[k][i] = fma2(g, h, dw[k][i]);
+                    db[k][i] = add2(db[k][i], g);
                 }
             }
-            s1 = lanes_sum(s1, lpr) * inv;
-            s2 = lanes_sum(s2, lpr) * inv;
+            const float t1 = -lanes_sum(both(s1), lpr) * inv, t2 = -lanes_sum(both(s2), lpr) * inv;
             if (r < rows)
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
                     if (c.in(k)) {
-                        float o[V];
+                        f32x2 o[P];
 #pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            o[e] = rs[q] * (ug[q][k].at(e) * wv[k][e] - s1 - (ux[q][k].at(e) - mu[q]) * rs[q] * s2);
+                        for (int i = 0; i < P; ++i)
+                            o[i] = norm_dx(mul2(add2(ux[q][k].at(i), minus_mu), rs2), mul2(ug[q][k].at(i), wv[k][i]), rs2, two(t1, t1), two(t2, t2));
                         c.store(dx + r * width, k, o);
                     }
         }
@@ -367,33 +390,30 @@ __global__ void __launch_bounds__(kThreads, kNarrowBlocks)
     if (!part) return;
     // The sums of the warp's rows, of the block's warps in order. (Rows of a warp that start at different places
     // have different columns in a lane.)
-    int at = warp * rpw + sub, parts = kThreads / 32 * rpw;
+    int at = warp * rpw + sub, n = kThreads / 32 * rpw;
     if constexpr (!kRagged) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
+            for (int i = 0; i < P; ++i)
                 for (int o = lpr; o < 32; o <<= 1) {
-                    dw[k][e] += __shfl_xor_sync(0xffffffffu, dw[k][e], o);
-                    db[k][e] += __shfl_xor_sync(0xffffffffu, db[k][e], o);
+                    dw[k][i] = add2(dw[k][i], __shfl_xor_sync(0xffffffffu, dw[k][i], o));
+                    db[k][i] = add2(db[k][i], __shfl_xor_sync(0xffffffffu, db[k][i], o));
                 }
         at = warp;
-        parts = kThreads / 32;
+        n = kThreads / 32;
     }
     if (kRagged || sub == 0)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (c.in(k))
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if ((c.ok(k) >> e) & 1u) {
-                        acc[(size_t)(2 * at) * width + c.column(k) + e] = dw[k][e];
-                        acc[(size_t)(2 * at + 1) * width + c.column(k) + e] = db[k][e];
-                    }
+            if (c.in(k)) {
+                c.leave(acc + (size_t)(2 * at) * width, k, dw[k]);
+                c.leave(acc + (size_t)(2 * at + 1) * width, k, db[k]);
+            }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * width; i += kThreads) {
         float s = 0.0f;
-        for (int j = 0; j < parts; ++j) s += acc[(size_t)2 * j * width + i];
+        for (int j = 0; j < n; ++j) s += acc[(size_t)2 * j * width + i];
         part[(size_t)blockIdx.x * 2 * width + i] = s;
     }
 }
@@ -506,7 +526,7 @@ __global__ void __maxnreg__(wide_regs(1, NV, NV * Unit<T>::V, kRagged))
     norm_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, T* __restrict__ y,
                          float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width, int pitch, int stages,
                          float eps) {
-    constexpr int R = 2, V = Unit<T>::V;
+    constexpr int R = 2, P = Unit<T>::P;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float2 buf[2][32];
     const Rows<R> m = rows_of<R>(smem, (size_t)width * sizeof(T), rows, pitch, 1);
@@ -530,44 +550,45 @@ __global__ void __maxnreg__(wide_regs(1, NV, NV * Unit<T>::V, kRagged))
     for (int64_t r = blockIdx.x; r < rows; r += step) {
         const bool ok = mbar_wait(&m.full[stage], phase);
         Unit<T> u[R][NV];
-        float s[R];
+        f32x2 s[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             const int64_t rq = r + q * m.stride;
-            s[q] = 0.0f;
+            s[q] = 0ull;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 if (c.in(k) && rq < rows) take(u[q][k], m, c, k, m.slot(stage, 0, q), x + rq * width, rq);
                 else u[q][k].zero();
 #pragma unroll
-                for (int e = 0; e < V; ++e) s[q] += u[q][k].at(e);
+                for (int i = 0; i < P; ++i) s[q] = add2(s[q], u[q][k].at(i));
             }
         }
-        const float2 mu2 = block_sums(ok ? s[0] : __int_as_float(0x7fffffff), ok ? s[1] : __int_as_float(0x7fffffff), buf[0]);
+        const float2 mu2 = block_sums(ok ? both(s[0]) : __int_as_float(0x7fffffff), ok ? both(s[1]) : __int_as_float(0x7fffffff), buf[0]);
         const float mu[R] = {mu2.x * inv, mu2.y * inv};
+        const f32x2 minus_mu[R] = {two(-mu[0], -mu[0]), two(-mu[1], -mu[1])};
         // every thread has its part of the rows in registers: the stage takes later ones
         const int64_t next = r + stages * step;
         if (t == 0 && next < rows) m.issue(next, stage, x, nullptr);
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            s[q] = 0.0f;
+            s[q] = 0ull;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (c.in(k)) s[q] += c.squares(u[q][k], k, mu[q]);
+                if (c.in(k)) c.squares(s[q], u[q][k], k, minus_mu[q]);
         }
-        const float2 var = block_sums(s[0], s[1], buf[1]);
+        const float2 var = block_sums(both(s[0]), both(s[1]), buf[1]);
         const float rs[R] = {rsqrtf(var.x * inv + eps), rsqrtf(var.y * inv + eps)};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (c.in(k)) {
-                float wv[V], bv[V], o[V];
+                f32x2 wv[P], bv[P], o[P];
                 pw.at(c, k, wv);
                 pb.at(c, k, bv);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
                     const int64_t rq = r + q * m.stride;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] = (u[q][k].at(e) - mu[q]) * rs[q] * wv[e] + bv[e];
+                    for (int i = 0; i < P; ++i) o[i] = norm_y(u[q][k].at(i), minus_mu[q], two(rs[q], rs[q]), wv[i], bv[i]);
                     if (rq < rows) c.store(y + rq * width, k, o);
                 }
             }
@@ -589,7 +610,7 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
     norm_bwd_wide_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ w,
                          const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
                          float* __restrict__ part, int64_t rows, int width, int pitch, int stages) {
-    constexpr int V = Unit<T>::V, R = bwd_rows(NV * V);
+    constexpr int P = Unit<T>::P, R = bwd_rows(2 * P * NV);
     grid_launch_next();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float2 buf[2][R][32];
@@ -603,11 +624,11 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
         for (int i = 0; i < stages; ++i)
             if (blockIdx.x + i * step < rows) m.issue(blockIdx.x + i * step, i, x, dy);
     }
-    float dw[NV][V], db[NV][V];
+    f32x2 dw[NV][P], db[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.0f;
+        for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = 0ull;
     Columns<T, NV, kRagged> c;
     c.init(t, nt, blockIdx.x, width);
     Params<T, NV, kRagged> pw;
@@ -626,19 +647,19 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
     };
     fetch(blockIdx.x);
     for (int64_t r = blockIdx.x; r < rows; r += step) {
-        float mu[R], rs[R], s1[R], s2[R];
+        f32x2 minus_mu[R], rs[R], s1[R], s2[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            mu[q] = mu_next[q];
-            rs[q] = rs_next[q];
-            s1[q] = s2[q] = 0.0f;
+            minus_mu[q] = two(-mu_next[q], -mu_next[q]);
+            rs[q] = two(rs_next[q], rs_next[q]);
+            s1[q] = s2[q] = 0ull;
         }
         fetch(r + step);
         const bool ok = mbar_wait(&m.full[stage], phase);
         Unit<T> ux[R][NV], ug[R][NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float wv[V];
+            f32x2 wv[P];
             if (c.in(k)) pw.at(c, k, wv);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
@@ -647,12 +668,12 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
                     take(ux[q][k], m, c, k, m.slot(stage, 0, q), x + rq * width, rq);
                     take(ug[q][k], m, c, k, m.slot(stage, 1, q), dy + rq * width, rq);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float g = ug[q][k].at(e), h = (ux[q][k].at(e) - mu[q]) * rs[q], a = g * wv[e];
-                        s1[q] += a;
-                        s2[q] += a * h;
-                        dw[k][e] += g * h;
-                        db[k][e] += g;
+                    for (int i = 0; i < P; ++i) {
+                        const f32x2 g = ug[q][k].at(i), h = mul2(add2(ux[q][k].at(i), minus_mu[q]), rs[q]), a = mul2(g, wv[i]);
+                        s1[q] = add2(s1[q], a);
+                        s2[q] = fma2(a, h, s2[q]);
+                        dw[k][i] = fma2(g, h, dw[k][i]);
+                        db[k][i] = add2(db[k][i], g);
                     }
                 }
             }
@@ -660,15 +681,15 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
         // one barrier for the sums of all rows of the step
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const float2 p = warp_sums(ok ? s1[q] : __int_as_float(0x7fffffff), s2[q]);
+            const float2 p = warp_sums(ok ? both(s1[q]) : __int_as_float(0x7fffffff), both(s2[q]));
             if ((t & 31) == 0) buf[turn][q][t >> 5] = p;
         }
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             const float2 p = sum_of(buf[turn][q]);
-            s1[q] = p.x * inv;
-            s2[q] = p.y * inv;
+            s1[q] = two(-p.x * inv, -p.x * inv);
+            s2[q] = two(-p.y * inv, -p.y * inv);
         }
         turn ^= 1;
         const int64_t next = r + stages * step;
@@ -676,14 +697,14 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (c.in(k)) {
-                float wv[V], o[V];
+                f32x2 wv[P], o[P];
                 pw.at(c, k, wv);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
                     const int64_t rq = r + q * m.stride;
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        o[e] = rs[q] * (ug[q][k].at(e) * wv[e] - s1[q] - (ux[q][k].at(e) - mu[q]) * rs[q] * s2[q]);
+                    for (int i = 0; i < P; ++i)
+                        o[i] = norm_dx(mul2(add2(ux[q][k].at(i), minus_mu[q]), rs[q]), mul2(ug[q][k].at(i), wv[i]), rs[q], s1[q], s2[q]);
                     if (rq < rows) c.store(dx + rq * width, k, o);
                 }
             }
@@ -696,13 +717,10 @@ __global__ void __maxnreg__(wide_regs(2, NV, NV * Unit<T>::V, kRagged))
     if (!part) return;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        if (c.in(k))
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if ((c.ok(k) >> e) & 1u) {
-                    part[(size_t)blockIdx.x * 2 * width + c.column(k) + e] = dw[k][e];
-                    part[((size_t)blockIdx.x * 2 + 1) * width + c.column(k) + e] = db[k][e];
-                }
+        if (c.in(k)) {
+            c.leave(part + (size_t)blockIdx.x * 2 * width, k, dw[k]);
+            c.leave(part + ((size_t)blockIdx.x * 2 + 1) * width, k, db[k]);
+        }
     }
 }
 

@@ -125,6 +125,36 @@ __device__ __forceinline__ uint64_t desc_mnmajor_bf16(uint32_t tile_saddr, uint3
     return sdesc_sw128(tile_saddr + s * 2048u, R * 128u, 1024u);
 }
 
+// ------------------------------------------------------------- packed fp32
+// two fp32 values in one 64-bit register, multiplied and added in one instruction
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 two(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 two(uint32_t a, uint32_t b) { return two(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f32x2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+
 // ---------------------------------------------------------------- launches
 // Overlap of a kernel's launch with the kernel before it (launch_kernel with `overlap`): the kernel before allows
 // it to start, and it waits until that one has finished and its writes can be read. Neither does anything in a
