@@ -11,8 +11,8 @@
 //  - beyond: a block for each row that reads it again for every step.
 // Measured, of what is read and written once: forward 8192 x 12288 bf16 72 us (5.6 TB/s, of 6.7 that a copy reaches),
 // 131072 x 128 bf16 18.7 us (3.6); backward 4099 x 4096 fp32 40 us (5.0), of which 5 are the sum over blocks, 131072 x
-// 128 bf16 24.7 us (4.1). Short rows are bound by instructions as much (62% of the issue slots): bf16 in and out,
-// two sums by shuffles, and in the backward about ten operations an element.
+// 128 bf16 23.2 us (4.3). Short rows are bound by instructions as much (62% of the issue slots): bf16 in and out,
+// two sums by shuffles, and in the backward about ten operations an element, taken two elements at a time.
 // A unit is 16 aligned bytes. Where the width is no multiple of it, rows start inside a unit, each at one of
 // eight (bf16) or four (fp32) places; a thread meets only rows that start at the same place, so that its columns
 // stay its own, and its first and last unit of a row hold elements of the neighbours, which do not count.
@@ -237,8 +237,8 @@ __device__ __forceinline__ f32x2 norm_dx(f32x2 xh, f32x2 a, f32x2 rs, f32x2 minu
 
 // ---------------------------------------------------------------------------------- narrow
 // Lanes lpr * s .. lpr * (s + 1) - 1 of a warp hold row s of its 32 / lpr rows, lane l of them units l and l + lpr
-// (with one unit a lane and twice the lanes the sums' shuffles cost as much for half the rows: backward 131072 x 128
-// bf16 28 instead of 24.7 us, forward 161374 x 128 fp32 39 instead of 30). A block has eight warps, and the rows of a
+// (with one unit a lane and twice the lanes the sums' shuffles cost as much for half the rows, which took 13% to 30%
+// more: backward 131072 x 128 bf16 28 instead of 24.7 us, forward 161374 x 128 fp32 39 instead of 30). A block has eight warps, and the rows of a
 // step lie a multiple of eight from those of the step before.
 constexpr int kNarrowNV = 2;
 __device__ __forceinline__ float lanes_sum(float x, int lpr) {
