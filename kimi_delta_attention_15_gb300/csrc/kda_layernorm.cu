@@ -852,7 +852,7 @@ Form form_of(long long width, size_t size, int inputs) {
         while (kNarrowNV * f.lpr < f.units) f.lpr *= 2;
         return f;
     }
-    if (width > kWideMost) return f;
+    if (f.units > kWideMost / v) return f;   // (a row of that many columns spans one unit more where it starts inside one)
     f.wide = true;
     f.pitch = (int)((width * size + 31) / 16 * 16);
     // Two units a thread and small blocks, so that many rows are in flight; more units where 512 threads do not hold

@@ -132,6 +132,36 @@ def test_non_finite_rows_stay_alone():
     assert torch.isnan(y[4]).all() and torch.isnan(y[6]).all()
 
 
+ODD = [(40, 1), (40, 3), (50, 5), (41, 9), (64, 17), (33, 65), (70, 131), (300, 201), (20, 333), (25, 501), (17, 607), (19, 1001),
+       (9, 2049), (13, 4097), (12, 7777), (11, 9733), (10, 12289), (9, 16383)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,width", ODD)
+def test_rows_that_start_anywhere(rows, width, dtype):
+    """Widths that are no multiple of 16 bytes: rows share 16-byte units with their neighbours, of which nothing may
+    leak in (rows of NaN and infinity change no other row's outputs) and nothing may be overwritten."""
+    x, dy, w, b = make(rows, width, dtype, seed=width)
+    _, mean, rstd = check_forward(x, w, b)
+    check_backward(x, dy, w, mean, rstd)
+    x, dy, w, b = x.cuda(), dy.cuda(), w.cuda(), b.cuda()
+    y, mean, rstd = ops.layernorm_fwd(x, w, b)
+    g = ops.layernorm_bwd(x, dy, w, mean, rstd)
+    bad, dbad = x.clone(), dy.clone()
+    bad[1], bad[rows // 2], bad[-1] = float("nan"), float("inf"), float("nan")
+    dbad[1], dbad[rows // 2], dbad[-1] = float("inf"), float("nan"), float("nan")
+    keep = [r for r in range(rows) if r not in (1, rows // 2, rows - 1)]
+    pad = 64
+    room = [torch.full((rows * width + 2 * pad,), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    out = [t[pad:-pad].view(rows, width) for t in room]
+    y2, mean2, rstd2 = ops.layernorm_fwd(bad, w, b, y=out[0])
+    ops.layernorm_bwd(bad, dbad, w, mean2, rstd2, grads=dict(dx=out[1]))
+    assert torch.equal(y2[keep], y[keep]) and torch.equal(out[1][keep], g["dx"][keep])
+    assert torch.equal(mean2[keep], mean[keep]) and torch.equal(rstd2[keep], rstd[keep])
+    for t in room:
+        assert (t[:pad] == 7).all() and (t[-pad:] == 7).all()
+
+
 def test_gradients_not_wanted_and_guards():
     x, dy, w, b = (t.cuda() for t in make(50, 1000, torch.bfloat16, seed=6))
     _, mean, rstd = ops.layernorm_fwd(x, w, b)
