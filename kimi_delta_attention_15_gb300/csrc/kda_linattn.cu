@@ -40,9 +40,9 @@ constexpr int kSMs = 152;                     // of a GB300; one persistent CTA 
 // the cost model of the split, in chunk times of a full unit (2.7 us): a state-only chunk, the start of a unit, the two more
 // launches, and each state that is carried (fitted to T = 512 .. 16384 with 1 .. 64 heads cut into 1 .. 64 segments)
 constexpr double kStateOnly = 0.55, kUnitChunks = 1.0, kSplitChunks = 4.5, kCarried = 1.0 / 40;
-// Calls of up to so many tokens have their scores in two bf16 parts (16 significant bits). Rounded once, a score is off
-// by up to 2^-8 of itself; over many scores that is 1.4 times the outputs' own rounding in the mean square, but in the few
-// outputs of a short call it was up to 1.7 times, wherever a single score makes up a row.
+// Calls of up to so many tokens (kFine) have their scores, and the state that a chunk reads, in two bf16 parts (16
+// significant bits). Rounded once, they put the outputs off by 1.4 times the outputs' own rounding in the mean square, but
+// the few outputs of a short call by up to 1.7 times, wherever a single score makes up a row.
 constexpr int kFineTokens = 512;
 constexpr uint32_t kTile = LC * D * 2;        // a bf16 operand tile [128][128], two 64-column panels
 
@@ -196,7 +196,7 @@ struct LinSmem {
     // operand tiles (bf16 panels, 1024-byte aligned), K and V by chunk parity
     uint8_t K[2][kTile], V[2][kTile], Q[kTile];
     uint8_t S[kTile];        // the state the chunk starts from, [c][v], rounded to bf16
-    uint8_t stage[kTile];    // output rows on their way out
+    uint8_t stage[kTile];    // output rows on their way out; before them (kFine) the low part of S
     float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
     float decay[LC];         // of the keys of a whole chunk
     // full: operands in shared memory; qk, qs, ds, pv: MMA groups done, all: of the chunk; s, p, piece, low, o:
@@ -350,7 +350,15 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
         const bool carried = x.c > 0 || x.u.s_in, sum = x.c + 1 < x.chunks || x.u.s_out, three = sum && three_parts(x.u, x.c);
         if (!(ok = mbar_wait(&sm.s, ph) && (n == 0 || mbar_wait(&sm.r, ph ^ 1u)))) break;
         tc_fence_after();
-        if (!state_only && carried) product_ss<true>(tm + kColO, q, ds, kn);
+        if (!state_only && carried) {
+            if constexpr (kFine) {
+                product_ss<true>(tm + kColO, q, desc_mnmajor_bf16(smem_u32(sm.stage), LC, 0), kn);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) umma_bf16(tm + kColO, k_step(q, i), mn_step(ds, i), kn, 1);
+            } else {
+                product_ss<true>(tm + kColO, q, ds, kn);
+            }
+        }
         umma_commit(&sm.qs);
         if (!(ok = mbar_wait(&sm.piece, ph) && mbar_wait(&sm.full_v[n & 1], (uint32_t)((n >> 1) & 1)))) break;
         tc_fence_after();
@@ -512,7 +520,7 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
                     tmem_after_wait(y);
                     if (t == 1) {
                         tc_fence_before();
-                        mbar_arrive(&sm.r);
+                        if (!kFine) mbar_arrive(&sm.r);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -534,7 +542,7 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
                     tmem_wait_ld(x);
                     if (t == 3) {
                         tc_fence_before();
-                        mbar_arrive(&sm.r);
+                        if (!kFine) mbar_arrive(&sm.r);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -542,6 +550,10 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
                             make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     send(t, t & 1);
                 }
+            }
+            if constexpr (kFine) {   // the stage takes the next state's low part
+                staged();
+                mbar_arrive(&sm.r);
             }
         }
     }
@@ -704,6 +716,16 @@ template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a,
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(sm.S + panel_off_bf16(row, 8 * half + i, LC)) =
                         make_uint4(pack_bf16(s[4 * i]), pack_bf16(s[4 * i + 1]), pack_bf16(s[4 * i + 2]), pack_bf16(s[4 * i + 3]));
+                if constexpr (kFine) {   // its low part where the outputs are staged later
+                    if (n > 0 && !(ok = wait_warp(&sm.r, n - 1))) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = low_part(s[4 * i + e], pack_bf16(s[4 * i + e]));
+                        *reinterpret_cast<uint4*>(sm.stage + panel_off_bf16(row, 8 * half + i, LC)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
                 fence_async_smem();
             }
             tc_fence_before();

@@ -104,6 +104,17 @@ def test_short_calls_round_their_outputs_only(lens, H, G):
         assert ((x - r.reshape(x.shape)).norm() / r.norm()).item() <= 0.51 * U, k
 
 
+@pytest.mark.parametrize("lens,H,G", [((1,), 1, 1), ((0, 1, 3), 2, 1), ((40, 130), 3, 1), ((300, 1, 211), 2, 2), ((512,), 1, 1)])
+def test_short_calls_with_states_round_their_outputs_only(lens, H, G):
+    """The same for every chunk of a call of up to 512 tokens, with states carried in."""
+    d = O.make(lens, H, G, seed=33 + len(lens), h0=True, dhT=True)
+    out, ref = run(d), {**O.forward(d), **O.backward(d)}
+    check_all(d, out)
+    for k in ("o", "dq", "dk", "dv"):
+        x, r = out[k].double().cpu(), ref[k].double()
+        assert ((x - r.reshape(x.shape)).norm() / r.norm()).item() <= 0.51 * U, k
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.01])
 def test_scale(scale):
     d = O.make((200,), 2, seed=8, h0=True, dhT=True)
