@@ -596,19 +596,22 @@ template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a,
         const float w_state = u.scale * decay_pow(u.g, u.rev ? LC - 1 - row : row + 1);
         const f32x2 w2 = two(w_state, w_state);
         const float whole_decay = decay_pow(u.g, LC);
-        // the decays of the tokens of a whole chunk in fp32 (every warp writes the same values; none is still
-        // reading another unit's: its last state sum has been waited for), and those of tokens jr + 8 i and the
-        // next as w = w1 + w2 in bf16
-#pragma unroll
-        for (int i = 0; i < LC; i += 32) sm.decay[lane + i] = decay_pow(u.g, u.rev ? lane + i + 1 : LC - 1 - (lane + i));
-        __syncwarp();
+        // the decays of the tokens of a whole chunk in fp32 (every warp writes the same values), and those of tokens
+        // jr + 8 i and the next as w = w1 + w2 in bf16. Only for a unit with chunks: the last state sum of the one
+        // before has been waited for, which every warp's last read of its decays comes before. A unit without chunks
+        // has nothing to wait for: its decays, written by a warp that is behind, would replace the next unit's.
         uint32_t wk1[8], wk2[8];
+        if (chunks > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = jr + 8 * i;
-            const float x = sm.decay[j], y = sm.decay[j + 1];
-            wk1[i] = pack_bf16(x, y);
-            wk2[i] = pack_bf16(x - low_bf16(wk1[i]), y - high_bf16(wk1[i]));
+            for (int i = 0; i < LC; i += 32) sm.decay[lane + i] = decay_pow(u.g, u.rev ? lane + i + 1 : LC - 1 - (lane + i));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = jr + 8 * i;
+                const float x = sm.decay[j], y = sm.decay[j + 1];
+                wk1[i] = pack_bf16(x, y);
+                wk2[i] = pack_bf16(x - low_bf16(wk1[i]), y - high_bf16(wk1[i]));
+            }
         }
         for (int c = 0; ok && chunks > 0; ++c) {
             if (c > 0) {   // the state sum of chunk c - 1 is there, its decayed keys are no longer needed
