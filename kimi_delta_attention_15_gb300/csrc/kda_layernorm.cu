@@ -17,6 +17,7 @@
 // eight (bf16) or four (fp32) places; a thread meets only rows that start at the same place, so that its columns
 // stay its own, and its first and last unit of a row hold elements of the neighbours, which do not count.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include "kda_internal.cuh"
@@ -834,6 +835,7 @@ bool valid_size(long long rows, long long width) {
 }
 
 constexpr int kMostParts = 4 * kSMs;   // blocks whose sums of dw and db are kept
+constexpr size_t kSharedOfSM = 216 * 1024;   // for the rows of the wide form's blocks; 1 KB of each block's share is left free
 
 // Which form a width takes, and its launch.
 struct Form {
@@ -867,12 +869,25 @@ Form form_of(long long width, size_t size, int inputs) {
     const int stage = f.pitch * inputs * (inputs == 1 ? 2 : bwd_rows(f.nv * v));
     // up to four steps ahead, within the SM's shared memory; fewer blocks rather than none ahead
     for (;; --f.per_sm) {
-        f.stages = (int)(((size_t)216 * 1024 / f.per_sm - 1024 - 64) / stage);
+        f.stages = (int)((kSharedOfSM / f.per_sm - 1024 - 64) / stage);
         if (f.stages >= 2 || f.per_sm == 1) break;
     }
     f.stages = std::clamp(f.stages, 1, 4);
     f.smem = 64 + (size_t)stage * f.stages;
     return f;
+}
+
+// Allows a wide kernel as much shared memory as form_of can ask for, once for each device (`done` is the kernel's own): the
+// limit is the kernel's, not the launch's, and a call that set it to its own size could take it from under a launch
+// of another thread.
+kda_status allow_shared(const void* kernel, std::atomic<uint64_t>& done, const char* where) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return launched(where);
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return KDA_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSharedOfSM - 1024)) != cudaSuccess) return launched(where);
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return KDA_OK;
 }
 
 unsigned blocks(long long rows, long long most) { return (unsigned)(rows < most ? rows : most); }
@@ -881,7 +896,9 @@ template <typename T, int NV, bool kRagged>
 kda_status fwd_wide(const Form& f, long long rows, int width, float eps, const T* x, const float* w, const float* b, T* y,
                     float* mean, float* rstd, cudaStream_t s) {
     auto k = norm_fwd_wide_kernel<T, NV, kRagged>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_fwd");
+    static std::atomic<uint64_t> allowed{0};
+    const kda_status st = allow_shared(reinterpret_cast<const void*>(k), allowed, "kda_layernorm_fwd");
+    if (st != KDA_OK) return st;
     k<<<blocks(rows, (long long)kSMs * f.per_sm), f.threads, f.smem, s>>>(x, w, b, y, mean, rstd, rows, width, f.pitch, f.stages, eps);
     return launched("kda_layernorm_fwd launch");
 }
@@ -916,7 +933,9 @@ template <typename T, int NV, bool kRagged>
 kda_status bwd_wide(const Form& f, long long rows, int width, const T* x, const T* dy, const float* w, const float* mean,
                     const float* rstd, T* dx, float* part, int* parts, cudaStream_t s) {
     auto k = norm_bwd_wide_kernel<T, NV, kRagged>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem) != cudaSuccess) return launched("kda_layernorm_bwd");
+    static std::atomic<uint64_t> allowed{0};
+    const kda_status st = allow_shared(reinterpret_cast<const void*>(k), allowed, "kda_layernorm_bwd");
+    if (st != KDA_OK) return st;
     *parts = (int)blocks(rows, (long long)kSMs * f.per_sm);
     k<<<*parts, f.threads, f.smem, s>>>(x, dy, w, mean, rstd, dx, part, rows, width, f.pitch, f.stages);
     return launched("kda_layernorm_bwd launch");
