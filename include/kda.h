@@ -34,7 +34,8 @@
  *  - Nullable inputs (h0, dhT) mean zero. Nullable outputs (hT, dh0) are
  *    skipped.
  *  - `stream` is a cudaStream_t. Calls are asynchronous: nothing is
- *    synchronised or allocated inside the launch path.
+ *    synchronised or allocated inside the launch path. They launch on the
+ *    current device, which has to be the stream's and the pointers' own.
  *
  * Ownership: the caller owns every buffer, including the workspace. kda_fwd
  * stores its per-chunk intermediates and state checkpoints in the workspace;

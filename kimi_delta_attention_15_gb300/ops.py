@@ -193,6 +193,48 @@ def alloc_workspace(shape: Shape, device) -> torch.Tensor:
     return torch.empty(workspace_size(shape), dtype=torch.uint8, device=device)
 
 
+def _elsewhere(t, stream):
+    """The device of the call's first tensor, where it is not the current one; None where it is."""
+    dev = t.get_device() if t is not None else -1
+    if dev < 0:
+        return None       # not on a GPU: refused by the call itself
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream: on cuda:{stream.device_index}; the tensors are on cuda:{dev}")
+    return None if dev == torch._C._cuda_getDevice() else dev
+
+
+def _on_device(call):
+    """A call runs with its tensors' device as the current one: the library launches there."""
+    first = call.__code__.co_varnames[0]
+
+    @functools.wraps(call)
+    def on(*args, **kw):
+        dev = _elsewhere(args[0] if args else kw.get(first), kw.get("stream"))
+        if dev is None:
+            return call(*args, **kw)
+        with torch.cuda.device(dev):
+            return call(*args, **kw)
+    return on
+
+
+def _on_stream(call):
+    """The same for calls to which `stream` is the current one, so that what they allocate is the stream's."""
+    first = call.__code__.co_varnames[0]
+
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        dev = _elsewhere(args[0] if args else kw.get(first), stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):     # which makes its device current too
+                return call(*args, **kw)
+        if dev is None:
+            return call(*args, **kw)
+        with torch.cuda.device(dev):
+            return call(*args, **kw)
+    return on
+
+
+@_on_device
 def fwd(q, k, v, g_raw, beta_raw, A_log, dt_bias, h0=None, cu_seqlens=None, *, B: int = 1,
         scale: float = SCALE, lower_bound: float = LOWER_BOUND, workspace=None, o=None,
         hT=None, want_hT: bool = True, stream=None, chunk_size: int = 64):
@@ -219,6 +261,7 @@ def fwd(q, k, v, g_raw, beta_raw, A_log, dt_bias, h0=None, cu_seqlens=None, *, B
 STATIC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
+@_on_device
 def fwd_static_scratch(q, k, v, g_raw, beta_raw, A_log, dt_bias, h0=None, cu_seqlens=None, *, B: int = 1,
                        scale: float = SCALE, lower_bound: float = LOWER_BOUND, o=None, hT=None,
                        want_hT: bool = True, stream=None):
@@ -243,6 +286,7 @@ def fwd_static_scratch(q, k, v, g_raw, beta_raw, A_log, dt_bias, h0=None, cu_seq
     return o, hT
 
 
+@_on_device
 def bwd(q, k, v, g_raw, beta_raw, A_log, dt_bias, do, workspace, h0=None, cu_seqlens=None,
         dhT=None, *, B: int = 1, scale: float = SCALE, lower_bound: float = LOWER_BOUND,
         grads=None, want_dh0: bool = True, stream=None, chunk_size: int = 64):
@@ -276,6 +320,7 @@ def bwd(q, k, v, g_raw, beta_raw, A_log, dt_bias, do, workspace, h0=None, cu_seq
     return grads
 
 
+@_on_device
 def decode(q, k, v, g_raw, beta_raw, A_log, dt_bias, state, *, o=None, scale: float = SCALE,
            lower_bound: float = LOWER_BOUND, stream=None):
     """kda_decode: one token per request. v, g_raw [n_req, H, 128] bf16,
@@ -322,17 +367,6 @@ def _ready(specs):
         _validate(specs)
         raise ValueError(f"every tensor must be on one CUDA device (cuda:{dev})")
     return dev
-
-
-def _on_stream(call):
-    """A call with `stream` runs with it as the current one, so that what it allocates is the stream's."""
-    @functools.wraps(call)
-    def on(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return on
 
 
 def _address(t):
@@ -539,6 +573,7 @@ def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool =
     return grads
 
 
+@_on_device
 def device_status(workspace, stream=None) -> int:
     return int(load().kda_get_device_status(_ptr(workspace), _stream_handle(stream)))
 
