@@ -174,8 +174,9 @@ kda_status kda_decode(long long n_req, long long H, long long groups, float scal
  * A positive value makes the state grow; nothing checks it.
  * Rounding: products of bf16 inputs and all sums are taken in fp32; the decayed scores
  * and, where a chunk of 128 tokens reads it, the state are rounded to bf16 once each as
- * operands of a product (calls of up to 512 tokens keep both in two bf16 parts, 16
- * bits). The state itself is kept in fp32, and hT and dh0 are within 1e-6 of their size.
+ * operands of a product; in chunks that start within the first 512 tokens of a sequence
+ * (o, dq; for dk, dv the last 512) both are kept in two bf16 parts, 16 bits. The state
+ * itself is kept in fp32, and hT and dh0 are within 1e-6 of their size.
  * Inputs are expected to be finite. An infinity or NaN in a token reaches the outputs of
  * its own sequence and head only, of tokens up to 127 before it among them (they share
  * its chunk). */

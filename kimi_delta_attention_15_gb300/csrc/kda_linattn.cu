@@ -26,6 +26,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 #include <cuda.h>
 #include "kda_internal.cuh"
 #include "umma_bf16.cuh"
@@ -40,9 +41,13 @@ constexpr int kSMs = 152;                     // of a GB300; one persistent CTA 
 // the cost model of the split, in chunk times of a full unit (2.7 us): a state-only chunk, the start of a unit, the two more
 // launches, and each state that is carried (fitted to T = 512 .. 16384 with 1 .. 64 heads cut into 1 .. 64 segments)
 constexpr double kStateOnly = 0.55, kUnitChunks = 1.0, kSplitChunks = 4.5, kCarried = 1.0 / 40;
-// Calls of up to so many tokens (kFine) have their scores, and the state that a chunk reads, in two bf16 parts (16
-// significant bits). Rounded once, they put the outputs off by 1.4 times the outputs' own rounding in the mean square, but
-// the few outputs of a short call by up to 1.7 times, wherever a single score makes up a row.
+// The chunks that start within so many tokens of where a sequence starts, in the job's direction, have their scores, and
+// the state that they read, in two bf16 parts (16 significant bits). Rounded once, these put an output off by 1.4 times
+// its own rounding in the mean square where many scores make up a row, but by up to 2.5 times where a single one does, as
+// in the first rows. It goes by a row's place in its sequence alone, so that a sequence has the same precision
+// whatever shares its call. (By the call's tokens, short calls in two parts and others in one: T = 8192, 96 heads backward 396
+// us, packed six with 96 heads forward 187; by place 417 and 215; two parts throughout 556 and 244, and as much with
+// two parts for heads that decay by e^-0.5 a token too, whose rows are few scores everywhere: they hold up the rest.)
 constexpr int kFineTokens = 512;
 constexpr uint32_t kTile = LC * D * 2;        // a bf16 operand tile [128][128], two 64-column panels
 
@@ -118,7 +123,7 @@ struct Unit {
     bool fp32;
     float scale, g;                // g: log decay
     float in_scale, out_scale;     // what the state is multiplied with on its way in and out
-    int exact, after;              // after: tokens of the sequence still to come after this unit
+    int exact, after, done;        // tokens of the sequence, in the unit's order, still to come after it and before it
     const float* s_in;             // where this unit's state comes from and goes to, NULL: zero, not wanted
     float* s_out;
     int s_in_t;
@@ -142,6 +147,7 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
     x.g = a.log_decay[x.h];
     x.exact = j.exact;
     x.after = j.rev ? s.before : s.after;
+    x.done = j.rev ? s.after : s.before;
     const size_t seq_state = ((size_t)s.seq * a.H + x.h) * D * D, seg_state = ((size_t)i * a.H + x.h) * D * D;
     const bool head = j.rev ? s.seg == s.nseg - 1 : s.seg == 0, tail = j.rev ? s.seg == 0 : s.seg == s.nseg - 1;
     if (a.state_only) {            // every segment but the last of its sequence starts from zero and leaves its sum
@@ -190,13 +196,14 @@ __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
     const int left = u.after + max(u.len - (c + 1) * LC, 0);
     return u.exact && u.g != 0.0f && (left == 0 || u.g * (float)left > -1.0f);
 }
+__device__ __forceinline__ bool in_two_parts(const Unit& u, int c) { return u.done + c * LC < kFineTokens; }
 __device__ __forceinline__ int chunks_of(const Unit& u) { return (u.len + LC - 1) / LC; }
 
 struct LinSmem {
     // operand tiles (bf16 panels, 1024-byte aligned), K and V by chunk parity
     uint8_t K[2][kTile], V[2][kTile], Q[kTile];
     uint8_t S[kTile];        // the state the chunk starts from, [c][v], rounded to bf16
-    uint8_t stage[kTile];    // output rows on their way out; before them (kFine) the low part of S
+    uint8_t stage[kTile];    // output rows on their way out; before them, in two parts, the low part of S
     float diag[4][64];       // per score warp: decays inside the diagonal's 32 x 32 block
     float decay[LC];         // of the keys of a whole chunk
     // full: operands in shared memory; qk, qs, ds, pv: MMA groups done, all: of the chunk; s, p, piece, low, o:
@@ -304,31 +311,27 @@ __device__ __forceinline__ void lin_load(const LinArgs& a, LinSmem& sm, int unit
     raise_status(a.ws, KDA_ERR_TIMEOUT);
 }
 
-// --- MMAs, one thread. TMEM: scores and, in one half of their columns (two to a column), their bf16 copy,
-// in the other the decayed keys' low parts; outputs; state sum [c][v]; decayed keys [c][tokens], high and
-// middle parts (two to a column)
-constexpr uint32_t kColP = 0, kColO = 128, kColDS = 256, kColHi = 384, kColMid = 448;
-// the scores' copy goes behind the columns still to be read: forward from the left, reversed from the right
-__device__ __forceinline__ uint32_t copy_col(int rev) { return kColP + (rev ? 64u : 0u); }
-__device__ __forceinline__ uint32_t low_col(int rev) { return kColP + (rev ? 0u : 64u); }
-// in two parts each block of 32 columns holds its own: of the MMA step s, the high part here, the low part 16 columns on
-__device__ __forceinline__ uint32_t fine_col(int s) { return kColP + 32 * (s >> 1) + 8 * (s & 1); }
+// --- MMAs, one thread. TMEM: scores and, in the first half of each block of 32 columns, its bf16 copy (two to a
+// column), in the second half the copy's low part or, after that, the decayed keys' low parts; outputs; state sum
+// [c][v]; decayed keys [c][tokens], high and middle parts (two to a column)
+constexpr uint32_t kColP = 0, kColLow = 16, kColO = 128, kColDS = 256, kColHi = 384, kColMid = 448;
 // A product over K = 128: eight MMAs, unrolled, descriptors a constant apart. (The thread that issues them is
 // what limits it otherwise: with descriptors built one by one an MMA of 128 x 128 x 16 took 130 to 190 cycles,
 // so it takes 65, the time to read its operands from shared memory.)
 __device__ __forceinline__ uint64_t k_step(uint64_t d, int s) { return d + (uint64_t)((s >> 2) * (kTile / 2 / 16) + (s & 3) * 2); }
 __device__ __forceinline__ uint64_t mn_step(uint64_t d, int s) { return d + (uint64_t)(s * 128); }
 template <bool kBmn>
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add = false) {
 #pragma unroll
-    for (int s = 0; s < 8; ++s) umma_bf16(d, k_step(a, s), kBmn ? mn_step(b, s) : k_step(b, s), idesc, s > 0);
+    for (int s = 0; s < 8; ++s) umma_bf16(d, k_step(a, s), kBmn ? mn_step(b, s) : k_step(b, s), idesc, add || s > 0);
 }
-template <bool kAdd>
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+// A in tensor memory, `add` to what the accumulator holds; kBlocks: in the halves of blocks, else in 64 columns one after another
+template <bool kBlocks>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
 #pragma unroll
-    for (int s = 0; s < 8; ++s) umma_bf16_ta(d, a + 8 * s, mn_step(b, s), idesc, kAdd || s > 0);
+    for (int s = 0; s < 8; ++s) umma_bf16_ta(d, a + 8 * s + (kBlocks ? 16 * (s >> 1) : 0), mn_step(b, s), idesc, add || s > 0);
 }
-template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+__device__ __forceinline__ void lin_mma(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     constexpr uint32_t kk = idesc_bf16(128, 128, 0, 0), kn = idesc_bf16(128, 128, 0, 1);
     const uint64_t dk0 = desc_kmajor(smem_u32(sm.K[0]), LC, 0), ds = desc_mnmajor_bf16(smem_u32(sm.S), LC, 0);
@@ -348,43 +351,32 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
         const uint32_t ph = (uint32_t)(n & 1);
         const uint64_t v = dv0 + (uint64_t)(ph * (kTile / 16));
         const bool carried = x.c > 0 || x.u.s_in, sum = x.c + 1 < x.chunks || x.u.s_out, three = sum && three_parts(x.u, x.c);
+        const bool fine = in_two_parts(x.u, x.c);
         if (!(ok = mbar_wait(&sm.s, ph) && (n == 0 || mbar_wait(&sm.r, ph ^ 1u)))) break;
         tc_fence_after();
         if (!state_only && carried) {
-            if constexpr (kFine) {
-                product_ss<true>(tm + kColO, q, desc_mnmajor_bf16(smem_u32(sm.stage), LC, 0), kn);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) umma_bf16(tm + kColO, k_step(q, i), mn_step(ds, i), kn, 1);
-            } else {
-                product_ss<true>(tm + kColO, q, ds, kn);
-            }
+            if (fine) product_ss<true>(tm + kColO, q, ds + (uint64_t)(kTile / 16), kn);   // its low part, in the stage
+            product_ss<true>(tm + kColO, q, ds, kn, fine);
         }
         umma_commit(&sm.qs);
         if (!(ok = mbar_wait(&sm.piece, ph) && mbar_wait(&sm.full_v[n & 1], (uint32_t)((n >> 1) & 1)))) break;
         tc_fence_after();
         if (sum) {   // small parts first: the accumulator is rounded at its size
-            product_ts<false>(tm + kColDS, tm + kColMid, v, kn);
-            product_ts<true>(tm + kColDS, tm + kColHi, v, kn);
+            product_ts<false>(tm + kColDS, tm + kColMid, v, kn, false);
+            product_ts<false>(tm + kColDS, tm + kColHi, v, kn, true);
         }
         if (!three) umma_commit(&sm.ds);
         if (!(ok = mbar_wait(&sm.o, ph) && mbar_wait(&sm.p, ph))) break;
         tc_fence_after();
         if (!state_only) {
-            if (kFine) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    umma_bf16_ta(tm + kColO, tm + fine_col(i >> 1) + 16 * (i & 1), mn_step(v, i >> 1), kn, carried || i > 0);
-            } else if (carried) {
-                product_ts<true>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
-            } else {
-                product_ts<false>(tm + kColO, tm + copy_col(x.u.rev), v, kn);
-            }
+            if (fine) product_ts<true>(tm + kColO, tm + kColP + kColLow, v, kn, carried);
+            product_ts<true>(tm + kColO, tm + kColP, v, kn, carried || fine);
         }
         umma_commit(&sm.pv);
         if (three) {
             if (!(ok = mbar_wait(&sm.low, (uint32_t)(lows++ & 1)))) break;
             tc_fence_after();
-            product_ts<true>(tm + kColDS, tm + low_col(x.u.rev), v, kn);
+            product_ts<true>(tm + kColDS, tm + kColP + kColLow, v, kn, true);
             umma_commit(&sm.ds);
         }
         umma_commit(&sm.all[n & 1]);
@@ -399,7 +391,7 @@ template <bool kFine> __device__ __forceinline__ void lin_mma(const LinArgs& a, 
 
 // --- scores -> decayed bf16 scores in TMEM; outputs -> shared memory -> global, a warp's 32 rows by TMA (or,
 // in a chunk with rows of a neighbour, row by row)
-template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+__device__ __forceinline__ void lin_scores(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
@@ -430,47 +422,53 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
         __syncwarp();
         const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // columns that count in its block
         const float far1 = decay_pow(g, 1), far2 = decay_pow(g, 33), far3 = decay_pow(g, 65);
+        // from the far end to the diagonal's block, so that its table is read when Q S^T, which leaves
+        // shared memory no read cycles, is over; zeros beyond it
+        auto copy = [&](auto in_parts) {
+            constexpr bool kFine = decltype(in_parts)::value;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const int b = rev ? 3 - i : i, away = rev ? b - warp : warp - b;
+                uint32_t w[16], low[16];
+                if (away < 0) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) w[x] = low[x] = 0u;
+                } else {
+                    uint32_t r[32];
+                    tmem_ld32_issue(lanes + kColP + 32 * b, r);
+                    if (away > 0) {
+                        const float base = away == 1 ? far1 : away == 2 ? far2 : far3;
+                        const f32x2 base2 = two(base, base);
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const f32x2 p = mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x]));
+                            w[x] = pack_bf16(p);
+                            if (kFine) low[x] = low_part(p, w[x]);
+                        }
+                    } else {
+                        const float* const d = diag + 31 + lane;
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float p0 = __uint_as_float(r[2 * x]) * d[-2 * x], p1 = __uint_as_float(r[2 * x + 1]) * d[-2 * x - 1];
+                            const f32x2 p = two((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
+                            w[x] = pack_bf16(p);
+                            if (kFine) low[x] = low_part(p, w[x]);
+                        }
+                    }
+                }
+                tmem_st16_issue(lanes + kColP + 32 * b, w);   // columns that have been read
+                if (kFine) tmem_st16_issue(lanes + kColP + 32 * b + kColLow, low);
+            }
+        };
         for (int c = 0; c < chunks; ++c, ++n) {
             if (!(ok = wait_warp(&sm.qk, n))) break;
             tc_fence_after();
+            const bool fine = in_two_parts(u, c);
             if (!state_only) {
-                // from the far end to the diagonal's block, so that its table is read when Q S^T, which leaves
-                // shared memory no read cycles, is over; zeros beyond it
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int b = rev ? 3 - i : i, away = rev ? b - warp : warp - b;
-                    uint32_t w[16], low[16];
-                    if (away < 0) {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) w[x] = low[x] = 0u;
-                    } else {
-                        uint32_t r[32];
-                        tmem_ld32_issue(lanes + kColP + 32 * b, r);
-                        if (away > 0) {
-                            const float base = away == 1 ? far1 : away == 2 ? far2 : far3;
-                            const f32x2 base2 = two(base, base);
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const f32x2 p = mul2(two(r[2 * x], r[2 * x + 1]), mul2(base2, f[x]));
-                                w[x] = pack_bf16(p);
-                                if (kFine) low[x] = low_part(p, w[x]);
-                            }
-                        } else {
-                            const float* const d = diag + 31 + lane;
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const float p0 = __uint_as_float(r[2 * x]) * d[-2 * x], p1 = __uint_as_float(r[2 * x + 1]) * d[-2 * x - 1];
-                                const f32x2 p = two((keep >> (2 * x)) & 1u ? p0 : 0.0f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.0f);
-                                w[x] = pack_bf16(p);
-                                if (kFine) low[x] = low_part(p, w[x]);
-                            }
-                        }
-                    }
-                    tmem_st16_issue(lanes + (kFine ? kColP + 32 * b : copy_col(rev) + 16 * b), w);   // columns that have been read
-                    if (kFine) tmem_st16_issue(lanes + kColP + 32 * b + 16, low);
-                }
+                if (fine) copy(std::true_type{});
+                else copy(std::false_type{});
                 tmem_wait_st_all();
             }
             tc_fence_before();
@@ -483,6 +481,9 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
             }
             const Chunk k = chunk_of(u, c);
             const int r0 = 32 * warp;
+            // the outputs' columns are free once read, the stage, where the next chunk may want it for the low part of
+            // its state, once it has been sent
+            const bool late = fine || c + 1 == chunks;
             const bool all = r0 >= k.lo && r0 + 32 <= k.hi;
             // a tile of 32 rows x 128 bytes at a time, 32 or 64 columns; two are staged at once
             auto send = [&](int tile, int slot) {
@@ -520,7 +521,7 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
                     tmem_after_wait(y);
                     if (t == 1) {
                         tc_fence_before();
-                        if (!kFine) mbar_arrive(&sm.r);
+                        if (!late) mbar_arrive(&sm.r);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -542,7 +543,7 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
                     tmem_wait_ld(x);
                     if (t == 3) {
                         tc_fence_before();
-                        if (!kFine) mbar_arrive(&sm.r);
+                        if (!late) mbar_arrive(&sm.r);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -551,7 +552,7 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
                     send(t, t & 1);
                 }
             }
-            if constexpr (kFine) {   // the stage takes the next state's low part
+            if (late) {
                 staged();
                 mbar_arrive(&sm.r);
             }
@@ -562,7 +563,7 @@ template <bool kFine> __device__ __forceinline__ void lin_scores(const LinArgs& 
 }
 
 // --- state in registers and its bf16 copy for the next chunk; decayed keys as bf16 parts; Q S^T decayed by row
-template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
+__device__ __forceinline__ void lin_main(const LinArgs& a, LinSmem& sm, int units, uint32_t tm) {
     const bool state_only = a.state_only != 0;
     const int warp = uniform((int)((threadIdx.x >> 5) & 3)), lane = threadIdx.x & 31, half = uniform((int)((threadIdx.x - 32 * kScoreWarps) >> 7));
     const int row = 32 * warp + lane;              // TMEM lane: output row, or key channel of the state
@@ -619,6 +620,7 @@ template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a,
                 tc_fence_after();
             }
             const bool carried = c > 0 || u.s_in, sum = c + 1 < chunks || (c < chunks && u.s_out), three = sum && three_parts(u, c);
+            const bool fine = in_two_parts(u, c);
             // 32 tokens x 16 channels of K, the g-th of this warp's four blocks
             auto fragments = [&](int g, uint32_t (&x)[8]) {
                 const int j = jl + 32 * (g >> 1), cc = cl + 2 * (g & 1);
@@ -626,6 +628,7 @@ template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a,
                 ldmatrix4_trans(key0 + (uint32_t)(n & 1) * kTile + panel_off_bf16(j + 16, cc, LC), x[4], x[5], x[6], x[7]);
             };
             auto place = [&](int g) { return lanes + ((uint32_t)(16 * (g & 1)) << 16) + 32 * half + 16 * (g >> 1); };
+            auto low_place = [&](int g) { return lanes + ((uint32_t)(16 * (g & 1)) << 16) + kColP + 64 * half + 32 * (g >> 1) + kColLow; };
             // where a thread's low parts of block g wait: the block's own bytes of K, which nothing else reads
             // once it is in fragments and the scores are done
             auto wait_place = [&](int g, int e) {
@@ -719,7 +722,7 @@ template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a,
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(sm.S + panel_off_bf16(row, 8 * half + i, LC)) =
                         make_uint4(pack_bf16(s[4 * i]), pack_bf16(s[4 * i + 1]), pack_bf16(s[4 * i + 2]), pack_bf16(s[4 * i + 3]));
-                if constexpr (kFine) {   // its low part where the outputs are staged later
+                if (fine) {   // its low part where the outputs are staged later
                     if (n > 0 && !(ok = wait_warp(&sm.r, n - 1))) break;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -755,13 +758,13 @@ template <bool kFine> __device__ __forceinline__ void lin_main(const LinArgs& a,
             }
             mbar_arrive(&sm.o);
             if (three) {   // the low parts: beside the scores' bf16 copy, once that is made
-                if (!(ok = wait_warp(kFine ? &sm.pv : &sm.p, n))) break;   // (qs: pv of the chunk before is over)
+                if (!(ok = wait_warp(fine ? &sm.pv : &sm.p, n))) break;   // (qs: pv of the chunk before is over)
                 tc_fence_after();
 #pragma unroll 1
                 for (int g = 0; g < 4; ++g) {
                     const uint4 x = *reinterpret_cast<const uint4*>(wait_place(g, 0)), y = *reinterpret_cast<const uint4*>(wait_place(g, 1));
                     const uint32_t lo[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                    tmem_st_frag_issue(place(g) + low_col(u.rev), lo);
+                    tmem_st_frag_issue(low_place(g), lo);
                 }
                 tmem_wait_st_all();
                 tc_fence_before();
@@ -797,7 +800,7 @@ __device__ __forceinline__ bool own_slot(const LinArgs& a) {
     return !__syncthreads_or(bad);
 }
 
-template <bool kFine> __global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_constant__ LinArgs a) {
+__global__ void __launch_bounds__(kLinThreads, 1) linattn_kernel(const __grid_constant__ LinArgs a) {
     extern __shared__ uint8_t smem_raw[];
     LinSmem& sm = *reinterpret_cast<LinSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // A call's first kernel sets the status word here, long before any wait of another CTA can give up
@@ -830,15 +833,15 @@ template <bool kFine> __global__ void __launch_bounds__(kLinThreads, 1) linattn_
     tc_fence_after();
     const uint32_t tm = uniform(sm.tmem);
     if (warp < kScoreWarps) {
-        lin_scores<kFine>(a, sm, units, tm);
+        lin_scores(a, sm, units, tm);
     } else if (warp < kScoreWarps + kMainWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
-        lin_main<kFine>(a, sm, units, tm);
+        lin_main(a, sm, units, tm);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if ((threadIdx.x & 31) == 0) {
             if (warp == kScoreWarps + kMainWarps) lin_load(a, sm, units);
-            else if (warp == kScoreWarps + kMainWarps + 1) lin_mma<kFine>(a, sm, units, tm);
+            else if (warp == kScoreWarps + kMainWarps + 1) lin_mma(a, sm, units, tm);
         }
     }
     __syncwarp();
@@ -1162,9 +1165,7 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
     cudaError_t e = cudaGetDevice(&device);
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (e == cudaSuccess && !(allowed.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(linattn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(linattn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
+        e = cudaFuncSetAttribute(linattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LinSmem) + 1024);
         if (e == cudaSuccess && device < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
     if (e != cudaSuccess) {
@@ -1208,8 +1209,7 @@ kda_status run_jobs(const kda_linattn_shape* sh, LinArgs& a, const void* const (
     }
     auto launch = [&](const LinArgs& x) {
         const int64_t units = (int64_t)x.slots * sh->H * x.jobs;
-        auto kernel = tokens <= kFineTokens ? linattn_kernel<true> : linattn_kernel<false>;
-        kernel<<<(unsigned)(units < kSMs ? units : kSMs), kLinThreads, sizeof(LinSmem) + 1024, s>>>(x);
+        linattn_kernel<<<(unsigned)(units < kSMs ? units : kSMs), kLinThreads, sizeof(LinSmem) + 1024, s>>>(x);
     };
     if (p.nseg > 1) {
         LinArgs b = a;
