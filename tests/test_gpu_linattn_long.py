@@ -5,6 +5,7 @@ import torch
 
 import linattn_oracle as O
 import linattn_products as P
+from kimi_delta_attention_15_gb300 import ops
 from test_gpu_linattn import check, dev, run
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +48,63 @@ def test_the_first_rows_of_every_sequence_round_their_outputs_only(lens, H, G, s
             at = slice(first, first + most) if k in ("o", "dq") else slice(first + length - most, first + length)
             x, r = out[k][at].double(), ref[k][at]
             assert ((x - r).norm() / r.norm()).item() <= 0.51 * 2.0 ** -8, (k, n)
+
+
+# fixed and packed lengths that are split into segments, the last one short, shared heads among them; with decays under which a
+# wrong weight of a segment's state shows
+@pytest.mark.parametrize("lens,H,G", [((2950,), 4, 1), ((3000,), 8, 4), ((2100, 0, 900, 131), 6, 3), ((4099, 1), 8, 8), ((1, 1700, 260), 5, 1)])
+@pytest.mark.parametrize("states", [False, True])
+def test_split_sequences(lens, H, G, states):
+    against_products(lens, H, G, seed=len(lens) + H, states=states)
+
+
+# no segments: units of up to 24 chunks, and blocks that go through several of them
+@pytest.mark.parametrize("lens,H,G", [((3001,), 152, 1), ((1000,), 120, 4), ((1000, 900, 1), 100, 2), ((1000, 900, 1, 300), 60, 1)])
+def test_long_units_one_after_another(lens, H, G):
+    against_products(lens, H, G, seed=H)
+
+
+@pytest.mark.parametrize("B,T,H,G", [(3, 1500, 4, 1), (2, 2500, 8, 4), (3, 700, 64, 2)])
+def test_batches_of_long_sequences(B, T, H, G):
+    d = O.make((T,) * B, H, G, seed=B, h0=True, dhT=True, log_decay=P.slow_decays(H))
+    c = dev(d)
+    four = {k: c[k].view(B, T, -1, 128) for k in ("q", "k", "v", "do")}
+    o, hT, _ = ops.linattn_fwd(four["q"], four["k"], four["v"], c["log_decay"], h0=c["h0"])
+    g = ops.linattn_bwd(four["q"], four["k"], four["v"], c["log_decay"], four["do"], h0=c["h0"], dhT=c["dhT"])
+    ref = P.reference(c)
+    for k, x in dict(o=o, hT=hT, **g).items():
+        check(k, x, ref[k])
+
+
+@pytest.mark.parametrize("lens", [(3000,), (1900, 0, 700)])
+def test_split_calls_in_a_graph(lens):
+    """Three dependent launches a call (four when packed), shared heads: captured and replayed."""
+    d = O.make(lens, 8, 4, seed=6, h0=True, dhT=True, log_decay=P.slow_decays(8))
+    c, ref = dev(d), P.reference(dev(d))
+    cu = c["cu_seqlens"] if len(lens) > 1 else None
+    args = (c["q"], c["k"], c["v"], c["log_decay"])
+    ws = ops.linattn_alloc_workspace(ops._linattn_shape_of(c["q"], c["v"], cu, 1, ops.SCALE), "cuda", backward=True)
+    o, hT = torch.empty_like(c["v"]), torch.empty_like(c["h0"])
+    g = dict(dq=torch.empty_like(c["q"]), dk=torch.empty_like(c["k"]), dv=torch.empty_like(c["v"]), dh0=torch.empty_like(hT))
+
+    def step():
+        ops.linattn_fwd(*args, h0=c["h0"], cu_seqlens=cu, workspace=ws, o=o, hT=hT)
+        ops.linattn_bwd(*args, c["do"], ws, h0=c["h0"], cu_seqlens=cu, dhT=c["dhT"], grads=g)
+
+    step()
+    torch.cuda.synchronize()
+    outs = dict(o=o, hT=hT, **g)
+    eager = {k: x.clone() for k, x in outs.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for x in outs.values():
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ops.device_status(ws) == 0
+        for k, x in outs.items():
+            assert torch.equal(x, eager[k]), k
+    for k, x in outs.items():
+        check(k, x, ref[k])
