@@ -232,7 +232,8 @@ kda_status kda_linattn_decode(long long n_req, long long H, long long groups, fl
  * x, y, dy, dx: [rows, width] contiguous, all KDA_BF16 or all KDA_FP32. weight, bias,
  * dweight, dbias: [width] fp32; mean, rstd: [rows] fp32. weight = NULL reads as 1,
  * bias = NULL as 0. Statistics and sums are fp32. Any width from 1 to 2^20; every
- * pointer 16-byte aligned. */
+ * pointer 16-byte aligned; eps finite and > 0 (0 gives KDA_ERR_UNSUPPORTED). In place: y
+ * may be x, and dx may be x or dy; outputs that overlap inputs otherwise are not allowed. */
 typedef enum { KDA_BF16 = 0, KDA_FP32 = 1 } kda_dtype;
 
 /* Forward. mean and rstd are written for the backward pass; NULL where not wanted. */

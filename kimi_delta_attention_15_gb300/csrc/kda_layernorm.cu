@@ -966,11 +966,11 @@ kda_status bwd(const Form& f, long long rows, int width, const void* xv, const v
         if constexpr (sizeof(T) == 4) KDA_NORM(bwd_wide, 8);
     }
 #undef KDA_NORM
-    norm_dx_any_kernel<T><<<blocks(rows, 1 << 30), kThreads, 0, s>>>(x, dy, w, mean, rstd, dx, rows, width);
     *parts = (int)blocks(rows, kSMs);
-    if (part)
+    if (part)   // before dx, which may take the place of x or dy
         norm_dw_any_kernel<T><<<dim3((unsigned)((width + kThreads - 1) / kThreads), (unsigned)*parts), kThreads, 0, s>>>(
             x, dy, mean, rstd, part, rows, width);
+    norm_dx_any_kernel<T><<<blocks(rows, 1 << 30), kThreads, 0, s>>>(x, dy, w, mean, rstd, dx, rows, width);
     return launched("kda_layernorm_bwd launch");
 }
 
