@@ -197,10 +197,10 @@ size_t kda_linattn_workspace_size(const kda_linattn_shape* shape, int backward);
 
 /* Forward over whole prompts. q, k [B*T, H/G, 128], v [B*T, H, 128] bf16; h0 (NULL = 0)
  * and hT (NULL = not wanted) [N, H, 128, 128] fp32; o [B*T, H, 128] bf16. The workspace
- * holds nothing between calls. Host checks and their codes are those of kda_fwd, and
- * N * H >= 2^28 gives KDA_ERR_SHAPE; a
- * malformed cu_seqlens or a wait that gave up is found on the device and reported by
- * kda_get_device_status(workspace, stream). */
+ * holds nothing between calls. hT may be h0 (the states advance in place); outputs that
+ * overlap inputs otherwise are not allowed. Host checks and their codes are those of
+ * kda_fwd, and N * H >= 2^28 gives KDA_ERR_SHAPE; a malformed cu_seqlens or a wait that
+ * gave up is found on the device and reported by kda_get_device_status(workspace, stream). */
 kda_status kda_linattn_fwd(const kda_linattn_shape* shape,
                            const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
                            const float* log_decay, const float* h0, const int64_t* cu_seqlens,
@@ -211,7 +211,8 @@ kda_status kda_linattn_fwd(const kda_linattn_shape* shape,
  * recomputes what it needs from the inputs: no call of kda_linattn_fwd has to come
  * before it. dq, dk [B*T, H/G, 128] bf16 are the sums over each group of value heads
  * (fixed order), dv [B*T, H, 128] bf16, dh0 [N, H, 128, 128] fp32 (NULL = not wanted).
- * Bitwise reproducible. */
+ * Bitwise reproducible. No output may overlap an input, dh0 not dhT either. The adjoint
+ * state is kept divided by scale, so dhT / scale has to be within fp32's range. */
 kda_status kda_linattn_bwd(const kda_linattn_shape* shape,
                            const kda_bf16* q, const kda_bf16* k, const kda_bf16* v,
                            const float* log_decay, const float* h0, const int64_t* cu_seqlens,

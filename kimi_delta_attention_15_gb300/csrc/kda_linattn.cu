@@ -156,10 +156,12 @@ __device__ __forceinline__ Unit unit_of(const LinArgs& a, int u) {
         x.s_out = tail ? nullptr : j.seg + seg_state;
         if (tail) x.len = 0;
     } else {
-        x.s_in = head ? (j.s_in ? j.s_in + seq_state : nullptr) : j.seg + seg_state;
-        x.s_in_t = head ? j.s_in_t : j.seg_t;
+        // the first segment of several reads its copy too: a final state that takes the initial one's place may be there already
+        const bool given = head && (s.nseg == 1 || !j.s_in);
+        x.s_in = given ? (j.s_in ? j.s_in + seq_state : nullptr) : j.seg + seg_state;
+        x.s_in_t = given ? j.s_in_t : j.seg_t;
         if (x.len > 0) {           // an empty sequence's state passes through unchanged
-            if (head) x.in_scale = 1.0f / j.s_scale;
+            if (given) x.in_scale = 1.0f / j.s_scale;
             x.out_scale = j.s_scale;
         }
         x.s_out = tail && j.s_out ? j.s_out + seq_state : nullptr;

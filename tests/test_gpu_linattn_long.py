@@ -108,3 +108,17 @@ def test_split_calls_in_a_graph(lens):
             assert torch.equal(x, eager[k]), k
     for k, x in outs.items():
         check(k, x, ref[k])
+
+
+@pytest.mark.parametrize("lens,H", [((700,), 4), ((3000,), 8), ((512, 0, 821, 1, 1, 419, 725), 21), ((2500, 130, 2500, 257), 20), ((60, 5), 2)])
+def test_final_states_in_the_place_of_the_initial_ones(lens, H):
+    """Segments of one sequence run at the same time: the last writes the state while the first may not have read it yet."""
+    d = dev(O.make(lens, H, seed=H, h0=True, log_decay=P.slow_decays(H)))
+    cu = d["cu_seqlens"] if len(lens) > 1 else None
+    args = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, hT, _ = ops.linattn_fwd(*args, h0=d["h0"], cu_seqlens=cu)
+    for _ in range(5):
+        state = d["h0"].clone()
+        o2, same, ws = ops.linattn_fwd(*args, h0=state, hT=state, cu_seqlens=cu)
+        assert same is state and ops.device_status(ws) == 0
+        assert torch.equal(o2, o) and torch.equal(state, hT)
