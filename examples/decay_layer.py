@@ -120,7 +120,7 @@ def train(layer, teacher, lengths, steps, lr=2e-3, seed=1):
 
 
 def generate(layer, x, cu_seqlens, tokens):
-    """The prompts in one pass, then `tokens` more for each sequence, every output the next input."""
+    """The prompts (of one token at least) in one pass, then `tokens` more for each sequence, every output the next input."""
     with torch.no_grad():
         y, state = layer(x, cu_seqlens)
     last, out = y[cu_seqlens[1:] - 1], []

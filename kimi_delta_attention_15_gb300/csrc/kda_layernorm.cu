@@ -2,7 +2,7 @@
 //   y  = (x - mean) rstd w + b
 //   dx = rstd (a - mean(a) - xh mean(a xh)),  a = dy w,  xh = (x - mean) rstd
 //   dw = sum_rows dy xh,  db = sum_rows dy
-// A few operations per byte: HBM bounds all of it, so every input is read once and kept in
+// A few operations per byte: HBM is the floor of all of it, so every input is read once and kept in
 // registers between the row's sums and its outputs, and dw, db are summed on the same pass, each
 // thread over the rows it meets for columns of its own, in registers. Three forms, by width:
 //  - narrow (up to 64 units a row): rows by warps, several at a time, sums by shuffles;
@@ -10,9 +10,13 @@
 //    memory by bulk copies some rows ahead;
 //  - beyond: a block for each row that reads it again for every step.
 // Measured, of what is read and written once: forward 8192 x 12288 bf16 72 us (5.6 TB/s, of 6.7 that a copy reaches),
-// 131072 x 128 bf16 18.7 us (3.6); backward 4099 x 4096 fp32 40 us (5.0), of which 5 are the sum over blocks, 131072 x
-// 128 bf16 23.2 us (4.3). Short rows are bound by instructions as much (62% of the issue slots): bf16 in and out,
-// two sums by shuffles, and in the backward about ten operations an element, taken two elements at a time.
+// 131072 x 128 bf16 19.7 us (3.4); backward 4099 x 4096 fp32 40 us (5.0), of which 5 are the sum over blocks, 131072 x
+// 128 bf16 24 us (4.2), 8192 x 4096 bf16 54 us (3.8), 16384 x 1024 bf16 32 us (3.2); ragged widths take two to four times
+// their floor (forward 8192 x 4097 bf16 46 us, 32768 x 501 31; backward 100000 x 131 48). What bounds them is not HBM (14% to
+// 62% of its peak in the kernels): the registers that rows are held in leave 16 of 64 warps on an SM, and these issue in
+// half of the cycles (45% to 57%) and wait in the others, for the row's sums (barriers, shuffles) and for loads.
+// dw and db are sums of a thread's rows in turn, of up to 608 blocks' by 32 groups, of the groups': in fp32 1.5e-7 of their
+// size off at 4099 x 4096 (elementary tensor operations: 1.2e-7), 1.6e-7 at 131072 x 128 in bf16 (3.7e-7).
 // A unit is 16 aligned bytes. Where the width is no multiple of it, rows start inside a unit, each at one of
 // eight (bf16) or four (fp32) places; a thread meets only rows that start at the same place, so that its columns
 // stay its own, and its first and last unit of a row hold elements of the neighbours, which do not count.

@@ -17,11 +17,13 @@
 // of the tensor core, and 128 KB in and out, about 2700 cycles of an SM's share of HBM. One CTA on an SM, by its
 // shared and tensor memory, has one chunk at work and part of the next: the chain from one state to the next (decayed
 // keys 1200 cycles, state 640, its bf16 copy 600, Q S^T 600, the state's sum 1060, waits between them) takes
-// about 5700 cycles, and it bounds the prompts. Measured: T = 4096, 152 heads forward 110 us, 5.6 TB/s of DRAM traffic;
-// T = 8192, 96 heads backward 380 us for 12 tensors of 201 MB (6.3 of 6.7 TB/s; 7 would do if the jobs shared their reads).
-// Not faster: the jobs of a head side by side, which do share them in L2 (T = 4096, 152 heads: 1.03 instead of 1.41 GB
-// read, 322 instead of 302 us); the next chunk's state sum issued before this one's outputs (8192 x 96 backward
-// 409 against 382 us); a whole split call in one cooperative kernel (T = 4096, 32 heads forward 79 against 71 us).
+// about 5700 cycles, and it bounds the prompts. A chunk with two parts (kFineTokens) has two products more and takes 1.4
+// times as long. Measured: T = 4096, 152 heads forward 118 us, 5.2 TB/s of DRAM traffic; T = 8192, 96 heads backward 414 to 427
+// us by the clocks, for 12 tensors of 201 MB (5.7 of 6.7 TB/s; 7 would do if the jobs shared their reads).
+// Not faster, each against the code of its time: the jobs of a head side by side, which do share them in L2 (T = 4096,
+// 152 heads: 1.03 instead of 1.41 GB read, 322 instead of 302 us); the next chunk's state sum issued before this one's
+// outputs (8192 x 96 backward 409 against 382 us); a whole split call in one cooperative kernel (T = 4096, 32 heads forward 79
+// against 71 us); chunks of one and of two parts as two instances of the roles' code (T = 4096, 32 heads 77 against 70 us).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -192,8 +194,8 @@ __device__ __forceinline__ Chunk chunk_of(const Unit& u, int c) {
 // The decayed keys of a chunk go into the state's sum as two bf16 parts (16 significant bits, 2.2e-6 of
 // their size in the mean square), or as three (24) where the state is an output and the tokens still to
 // come will not have decayed this chunk's share, and its error with it, by another e^-1: an output state
-// is within 1e-6 of its size. (Without any decay one part is exact.) Forward with final states, six sequences of 8192
-// tokens in all with 96 heads: 252 us with three parts always, 177 by this rule, 167 with two always.
+// is within 1e-6 of its size. (Without any decay one part is exact.) Forward with states, six sequences of 8192
+// tokens in all with 96 heads: 289 us with three parts always, 215 by this rule, 197 with two always.
 __device__ __forceinline__ bool three_parts(const Unit& u, int c) {
     const int left = u.after + max(u.len - (c + 1) * LC, 0);
     return u.exact && u.g != 0.0f && (left == 0 || u.g * (float)left > -1.0f);
@@ -961,7 +963,7 @@ __global__ void __launch_bounds__(1024)
     }
     // Whole sequences, few of them: longest first. A block's rounds come from opposite ends of the list in turn,
     // which evens them out (lengths 1300, 547, 2048, 963, 271, 3063 with 96 heads on 152 SMs: at most 46 chunks
-    // on an SM instead of 59, with 43 in the mean; 197 instead of 238 us).
+    // on an SM instead of 59, with 43 in the mean; 215 instead of 252 us).
     if (seg_len < T_total || N > (int)blockDim.x) return;
     const Slot own = tid < N ? table[tid] : Slot{};
     scan[tid] = own.len;
@@ -1067,8 +1069,8 @@ kda_status check_shape(const kda_linattn_shape* sh, bool packed) {
 // another on one SM. With fewer units than SMs a sequence is cut into segments: their own state
 // sums come first (state-only units, about half of a full one's time), then the states they start
 // from, then all segments at once, if that comes out shorter by the cost model. Forward, whole and as split:
-// T = 4096 with 32 heads 92 and 70 us, 16384 with 8 heads 328 and 65, 1024 with 4 heads 32 and 30 (not split: 1024
-// with 16 heads, 32 and 34; 4096 with 64 heads, 93 and 109); backward 16384 with 8 heads 332 and 142.
+// T = 4096 with 32 heads 98 and 71 us, 16384 with 8 heads 340 and 68, 1024 with 4 heads 35 and 29 (not split: 1024
+// with 16 heads, 36 and 35; 4096 with 64 heads, 100 and 112); backward 16384 with 8 heads 346 and 135.
 struct Plan {
     int64_t seg_len;   // tokens, a multiple of the chunk
     int nseg;          // segments of a fixed-length sequence (packed: of T_total tokens at most)
