@@ -254,6 +254,108 @@ kda_status kda_layernorm_bwd(long long rows, long long width, int dtype,
                              void* dx, float* dweight, float* dbias,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- gated recurrence over channels
+ *
+ * Per sequence and channel, a state h that each token's gates decay and write to:
+ *   u_t = exp(A_log) * sigmoid(g_raw_t),  a_t = exp(-u_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) * sigmoid(i_raw_t) * x_t,   y_t = h_t
+ * (a vector state of D channels: the layer that models alternate with those of the matrix
+ * states above, in their packed layout). x, g_raw, i_raw, y and their gradients are
+ * [B*T, D], all KDA_BF16 or all KDA_FP32, rows at the strides of the shape, so that they may
+ * be columns of one buffer; aligned to an element (16 bytes, and strides that are multiples of
+ * them, are faster). A_log, dA_log [D], h0, hT, dhT, dh0 [N, D] fp32, 16-byte aligned.
+ * Gates, decays, states and sums are fp32; 1 - a_t is computed as it is, not from a rounded
+ * a_t, so long memories keep fp32's precision. Inputs are expected to be finite; an
+ * infinity or NaN in a token reaches its own sequence and channel only. */
+#define KDA_RECURRENCE_BLOCK 64
+
+typedef struct {
+    int64_t B;        /* fixed-length batch rows; 1 when packed */
+    int64_t T;        /* tokens per row; total tokens when packed */
+    int64_t D;        /* channels, 1 .. 2^20 */
+    int64_t N;        /* sequences: B when cu_seqlens is NULL, else len(cu_seqlens) - 1 */
+    int32_t dtype;    /* kda_dtype of the token tensors */
+    int32_t reserved; /* 0 */
+    /* elements from one token's row to the next, at least D; 0 is read as D. y_stride is y's
+     * in the forward and dy's in the backward. */
+    int64_t x_stride, g_stride, i_stride, y_stride, dx_stride, dg_stride, di_stride;
+} kda_recurrence_shape;
+
+/* Bytes of workspace kda_recurrence_fwd (backward = 0) or kda_recurrence_bwd (backward = 1)
+ * needs for this shape; 0 for an invalid shape. The backward's size serves both. The strides
+ * do not count. */
+size_t kda_recurrence_workspace_size(const kda_recurrence_shape* shape, int backward);
+
+/* Forward. h0 (NULL = 0), hT (NULL = not wanted). kept (NULL = not wanted) is for the
+ * backward: [ceil(B*T / KDA_RECURRENCE_BLOCK), D] fp32, row j the state after token
+ * j * KDA_RECURRENCE_BLOCK - 1 of the flattened tokens, whichever sequence holds it (row 0:
+ * zeros). The workspace holds nothing between calls. y may be x, g_raw or i_raw (same
+ * stride); outputs that overlap inputs otherwise, hT and h0 among them, are not allowed
+ * (hT = h0 gives KDA_ERR_UNSUPPORTED). A malformed cu_seqlens is found on the device and reported by
+ * kda_get_device_status(workspace, stream); the outputs are then not defined. */
+kda_status kda_recurrence_fwd(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,
+                              const float* A_log, const float* h0, const int64_t* cu_seqlens, void* y, float* hT,
+                              float* kept, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_t <y_t, dy_t> + <hT, dhT> with the forward's inputs and `kept`: dx, dg_raw,
+ * di_raw in the tokens' type, dA_log [D] (NULL = not wanted; written, not accumulated, summed in a
+ * fixed order), dh0 [N, D] (NULL = not wanted). Bitwise reproducible. dx, dg_raw, di_raw may be
+ * any of x, g_raw, i_raw, dy (same stride, each another one); otherwise outputs that overlap
+ * inputs are not allowed (dh0 = dhT gives KDA_ERR_UNSUPPORTED). */
+kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,
+                              const float* A_log, const float* h0, const int64_t* cu_seqlens, const void* dy,
+                              const float* dhT, const float* kept, void* dx, void* dg_raw, void* di_raw, float* dA_log,
+                              float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each request: the shape has T = 1 and B = N = requests, x, g_raw, i_raw, y are
+ * [requests, D]; state [requests, D] fp32 is updated in place. y may be x, g_raw or i_raw. */
+kda_status kda_recurrence_decode(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,
+                                 const float* A_log, float* state, void* y, void* stream);
+
+/* -------------------------- norm of queries and keys by heads, with the position rotation
+ *
+ * For every token and head of q and k, with the weight of q or of k:
+ *   z_c = x_c * weight_c / sqrt(mean_c(x_c^2) + eps)
+ *   (y_a, y_b) = (z_a cos t - z_b sin t, z_b cos t + z_a sin t),  t = position * inv_freq[j]
+ * for the pairs j of the first rotary_dim columns, (j, j + rotary_dim / 2) or, interleaved,
+ * (2 j, 2 j + 1); y_c = z_c beyond. The angle is reduced exactly, whatever the position.
+ * q, k and their outputs and gradients: [tokens, heads, head_dim], all KDA_BF16 or all KDA_FP32, a
+ * token's heads together and tokens at the strides of the shape (multiples of 16 bytes), so
+ * that they may be columns of one projection; all pointers 16-byte aligned. The outputs
+ * are what kda_linattn_fwd and kda_linattn_bwd read. Weights [head_dim] fp32 (NULL reads as 1),
+ * inv_freq [rotary_dim / 2] fp32, finite, positions [tokens] int64, any value. Sums, norms and
+ * rotations are fp32, rounded once to the outputs' type. */
+typedef struct {
+    int64_t tokens;
+    int32_t q_heads, k_heads;   /* at least one of q; k may have none (its pointers are then not read) */
+    int32_t head_dim;           /* a multiple of 8 up to 256 */
+    int32_t rotary_dim;         /* a multiple of 8 up to head_dim; 0: the norm alone */
+    int32_t interleaved;        /* 0: pairs (j, j + rotary_dim / 2); 1: (2 j, 2 j + 1) */
+    int32_t dtype;              /* kda_dtype of q and k */
+    float eps;                  /* finite and > 0 */
+    /* elements from a token to the next, 0 read as heads * head_dim. q_out_stride, k_out_stride:
+     * of the forward's outputs and of dq_out, dk_out */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride, dq_stride, dk_stride;
+} kda_qknorm_shape;
+
+/* Forward. In place: q_out may be q and k_out may be k (same stride); outputs that overlap
+ * inputs otherwise are not allowed. */
+kda_status kda_qknorm_fwd(const kda_qknorm_shape* shape, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const int64_t* positions, const float* inv_freq, void* q_out,
+                          void* k_out, void* stream);
+
+/* Bytes of workspace kda_qknorm_bwd needs; 0 for an invalid shape. */
+size_t kda_qknorm_workspace_size(const kda_qknorm_shape* shape);
+
+/* Gradients from the forward's inputs and the outputs' adjoints dq_out, dk_out: dq, dk in their
+ * type, dq_weight, dk_weight [head_dim] fp32 (NULL = not wanted; written, not accumulated,
+ * summed over tokens and heads in a fixed order). dq may be dq_out or q, dk dk_out or k (same
+ * stride); outputs that overlap inputs otherwise are not allowed. */
+kda_status kda_qknorm_bwd(const kda_qknorm_shape* shape, const void* q, const void* k, const void* dq_out,
+                          const void* dk_out, const float* q_weight, const float* k_weight, const int64_t* positions,
+                          const float* inv_freq, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream` and returns the device status word of `workspace`
  * (KDA_OK, KDA_ERR_OFFSETS, KDA_ERR_TIMEOUT or KDA_ERR_STALE_WORKSPACE), or
  * KDA_ERR_CUDA if the stream reported an error. Clears nothing. */

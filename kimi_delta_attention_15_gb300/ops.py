@@ -48,6 +48,19 @@ class LinattnShape(ctypes.Structure):
                 ("scale", ctypes.c_float), ("groups", ctypes.c_int32)]
 
 
+class RecurrenceShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)] + \
+               [(n + "_stride", ctypes.c_int64) for n in ("x", "g", "i", "y", "dx", "dg", "di")]
+
+
+class QknormShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "rotary_dim", "interleaved", "dtype")] + \
+               [("eps", ctypes.c_float)] + \
+               [(n + "_stride", ctypes.c_int64) for n in ("q", "k", "q_out", "k_out", "dq", "dk")]
+
+
 def lib_path() -> str:
     return _build.LIB
 
@@ -103,6 +116,20 @@ def load(build_if_missing: bool = True):
         lib.kda_layernorm_workspace_size.restype = S
         lib.kda_layernorm_bwd.argtypes = [ctypes.c_longlong] * 2 + [ctypes.c_int] + [P] * 9 + [S, P]
         lib.kda_layernorm_bwd.restype = ctypes.c_int
+        lib.kda_recurrence_workspace_size.argtypes = [ctypes.POINTER(RecurrenceShape), ctypes.c_int]
+        lib.kda_recurrence_workspace_size.restype = S
+        lib.kda_recurrence_fwd.argtypes = [ctypes.POINTER(RecurrenceShape)] + [P] * 10 + [S, P]
+        lib.kda_recurrence_fwd.restype = ctypes.c_int
+        lib.kda_recurrence_bwd.argtypes = [ctypes.POINTER(RecurrenceShape)] + [P] * 15 + [S, P]
+        lib.kda_recurrence_bwd.restype = ctypes.c_int
+        lib.kda_recurrence_decode.argtypes = [ctypes.POINTER(RecurrenceShape)] + [P] * 7
+        lib.kda_recurrence_decode.restype = ctypes.c_int
+        lib.kda_qknorm_fwd.argtypes = [ctypes.POINTER(QknormShape)] + [P] * 9
+        lib.kda_qknorm_fwd.restype = ctypes.c_int
+        lib.kda_qknorm_workspace_size.argtypes = [ctypes.POINTER(QknormShape)]
+        lib.kda_qknorm_workspace_size.restype = S
+        lib.kda_qknorm_bwd.argtypes = [ctypes.POINTER(QknormShape)] + [P] * 13 + [S, P]
+        lib.kda_qknorm_bwd.restype = ctypes.c_int
         lib.kda_diag_tf32_round.argtypes = [P, P, P, ctypes.c_longlong, P]
         lib.kda_diag_tf32_round.restype = ctypes.c_int
         _lib = lib
@@ -570,6 +597,293 @@ def layernorm_bwd(x, dy, weight, mean, rstd, *, grads=None, want_dweight: bool =
                                  _address(dbias), workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if code:
         _check(code, "kda_layernorm_bwd")
+    return grads
+
+
+def _rows(name, t, rows, inner, dtype, dev):
+    """The elements from one row to the next of a tensor of `rows` rows of `inner` contiguous elements, whose rows may
+    lie apart (columns of a wider buffer). Checks count, dtype, layout and device."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.numel() != rows * inner:
+        raise ValueError(f"{name}: {t.numel()} elements {tuple(t.shape)}, expected {rows * inner}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: on {t.device}; every tensor must be on one CUDA device"
+                         + (f" (cuda:{dev})" if dev >= 0 else ""))
+    if t.is_contiguous():
+        return inner
+    size, stride, d, run = t.shape, t.stride(), t.dim() - 1, 1
+    while run < inner:
+        if size[d] != 1 and stride[d] != run:
+            raise ValueError(f"{name}: the {inner} elements of a row must be contiguous")
+        run *= size[d]
+        d -= 1
+    step, run = inner, 1
+    for e in range(d, -1, -1):
+        if size[e] == 1:
+            continue
+        if run == 1:
+            step = stride[e]
+        elif stride[e] != step * run:
+            raise ValueError(f"{name}: rows must be evenly spaced")
+        run *= size[e]
+    if rows > 1 and step < inner:
+        raise ValueError(f"{name}: rows overlap")
+    return step
+
+
+RECURRENCE_BLOCK = 64
+
+
+def recurrence_shape(T: int, D: int, N: int, B: int = 1, dtype=torch.bfloat16) -> RecurrenceShape:
+    """Shape of the gated recurrence over D channels."""
+    return RecurrenceShape(B=B, T=T, D=D, N=N, dtype=_NORM_DTYPES[dtype])
+
+
+def recurrence_workspace_size(shape: RecurrenceShape, backward: bool = False) -> int:
+    return int((_lib or load()).kda_recurrence_workspace_size(ctypes.byref(shape), int(backward)))
+
+
+def recurrence_alloc_workspace(shape: RecurrenceShape, device, backward: bool = False) -> torch.Tensor:
+    return torch.empty(recurrence_workspace_size(shape, backward), dtype=torch.uint8, device=device)
+
+
+def _recurrence_shape_of(x, cu_seqlens, B):
+    if x.dtype not in _NORM_DTYPES:
+        raise ValueError(f"x: dtype {x.dtype}, expected bfloat16 or float32")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, D] or [B, T, D]")
+    D, dtype = x.shape[-1], _NORM_DTYPES[x.dtype]
+    if cu_seqlens is not None:
+        if x.dim() != 2:
+            raise ValueError(f"x: shape {tuple(x.shape)}, packed tokens are [T, D]")
+        return RecurrenceShape(1, x.shape[0], D, cu_seqlens.numel() - 1, dtype)
+    if x.dim() == 3:
+        return RecurrenceShape(x.shape[0], x.shape[1], D, x.shape[0], dtype)
+    if B < 1 or x.shape[0] % B:
+        raise ValueError(f"B: {x.shape[0]} tokens are no {B} sequences of one length")
+    return RecurrenceShape(B, x.shape[0] // B, D, B, dtype)
+
+
+@_on_stream
+def recurrence_fwd(x, g_raw, i_raw, A_log, h0=None, cu_seqlens=None, *, B: int = 1, workspace=None, y=None, hT=None, kept=None,
+                   want_hT: bool = True, want_kept: bool = False, stream=None):
+    """kda_recurrence_fwd: h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_raw_t) x_t, a_t = exp(-exp(A_log) sigmoid(g_raw_t)),
+    y = h. Token tensors [T, D] (or [B, T, D]) bf16 or fp32, rows evenly spaced; A_log [D], states [N, D] fp32. `kept`
+    (want_kept) is what recurrence_bwd reads. Returns (y, hT, kept, workspace)."""
+    lib = _lib or load()
+    shape = _recurrence_shape_of(x, cu_seqlens, B)
+    D, N, dtype = shape.D, shape.N, x.dtype
+    T = shape.B * shape.T
+    blocks = (T + RECURRENCE_BLOCK - 1) // RECURRENCE_BLOCK
+    specs = [("A_log", A_log, D, _F32, False)]
+    if h0 is not None:
+        specs.append(("h0", h0, N * D, _F32, True))
+    if cu_seqlens is not None:
+        specs.append(("cu_seqlens", cu_seqlens, N + 1, _I64, True))
+    if hT is not None:
+        specs.append(("hT", hT, N * D, _F32, True))
+    if kept is not None:
+        specs.append(("kept", kept, blocks * D, _F32, True))
+    if workspace is not None:
+        specs.append(("workspace", workspace, workspace.numel(), _U8, False))
+    dev = _ready(specs)
+    shape.x_stride = _rows("x", x, T, D, dtype, dev)
+    shape.g_stride = _rows("g_raw", g_raw, T, D, dtype, dev)
+    shape.i_stride = _rows("i_raw", i_raw, T, D, dtype, dev)
+    if y is not None:
+        shape.y_stride = _rows("y", y, T, D, dtype, dev)
+    if workspace is None:
+        workspace = recurrence_alloc_workspace(shape, x.device)
+    if y is None:
+        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    if hT is None and want_hT:
+        hT = torch.empty((N, D), dtype=_F32, device=x.device)
+    if kept is None and want_kept:
+        kept = torch.empty((blocks, D), dtype=_F32, device=x.device)
+    code = lib.kda_recurrence_fwd(ctypes.byref(shape), x.data_ptr(), g_raw.data_ptr(), i_raw.data_ptr(), A_log.data_ptr(),
+                                  _address(h0), _address(cu_seqlens), y.data_ptr(), _address(hT), _address(kept),
+                                  workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        _check(code, "kda_recurrence_fwd")
+    return y, hT, kept, workspace
+
+
+@_on_stream
+def recurrence_bwd(x, g_raw, i_raw, A_log, dy, kept, workspace=None, h0=None, cu_seqlens=None, dhT=None, *, B: int = 1,
+                   grads=None, want_dA_log: bool = True, want_dh0: bool = True, stream=None):
+    """kda_recurrence_bwd: gradients of sum <y, dy> + <hT, dhT>, with the forward's inputs and its `kept`. Any workspace of
+    recurrence_alloc_workspace(shape, device, backward=True) serves; pass one to read device_status(workspace)
+    afterwards. Returns a dict of dx, dg_raw, di_raw (in `grads` they may be columns of one buffer), dA_log and dh0."""
+    lib = _lib or load()
+    shape = _recurrence_shape_of(x, cu_seqlens, B)
+    D, N, dtype = shape.D, shape.N, x.dtype
+    T = shape.B * shape.T
+    specs = [("A_log", A_log, D, _F32, False),
+             ("kept", kept, (T + RECURRENCE_BLOCK - 1) // RECURRENCE_BLOCK * D, _F32, False)]
+    if h0 is not None:
+        specs.append(("h0", h0, N * D, _F32, True))
+    if cu_seqlens is not None:
+        specs.append(("cu_seqlens", cu_seqlens, N + 1, _I64, True))
+    if dhT is not None:
+        specs.append(("dhT", dhT, N * D, _F32, True))
+    if workspace is not None:
+        specs.append(("workspace", workspace, workspace.numel(), _U8, False))
+    if grads is not None:
+        specs += [("dA_log", grads.get("dA_log"), D, _F32, True), ("dh0", grads.get("dh0"), N * D, _F32, True)]
+    dev = _ready(specs)
+    shape.x_stride = _rows("x", x, T, D, dtype, dev)
+    shape.g_stride = _rows("g_raw", g_raw, T, D, dtype, dev)
+    shape.i_stride = _rows("i_raw", i_raw, T, D, dtype, dev)
+    shape.y_stride = _rows("dy", dy, T, D, dtype, dev)
+    if workspace is None:
+        workspace = recurrence_alloc_workspace(shape, x.device, backward=True)
+    if grads is None:
+        dx, dg, di = (torch.empty(x.shape, dtype=dtype, device=x.device) for _ in range(3))
+        grads = dict(dx=dx, dg_raw=dg, di_raw=di, dA_log=torch.empty(D, dtype=_F32, device=x.device) if want_dA_log else None,
+                     dh0=torch.empty((N, D), dtype=_F32, device=x.device) if want_dh0 else None)
+    else:
+        dx, dg, di = (grads.get(n) for n in ("dx", "dg_raw", "di_raw"))
+        for name, t in (("dx", dx), ("dg_raw", dg), ("di_raw", di)):
+            if t is None:
+                raise ValueError(f"{name} is required")
+        shape.dx_stride = _rows("dx", dx, T, D, dtype, dev)
+        shape.dg_stride = _rows("dg_raw", dg, T, D, dtype, dev)
+        shape.di_stride = _rows("di_raw", di, T, D, dtype, dev)
+    code = lib.kda_recurrence_bwd(ctypes.byref(shape), x.data_ptr(), g_raw.data_ptr(), i_raw.data_ptr(), A_log.data_ptr(),
+                                  _address(h0), _address(cu_seqlens), dy.data_ptr(), _address(dhT), kept.data_ptr(),
+                                  dx.data_ptr(), dg.data_ptr(), di.data_ptr(), _address(grads.get("dA_log")),
+                                  _address(grads.get("dh0")), workspace.data_ptr(), workspace.numel(),
+                                  torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        _check(code, "kda_recurrence_bwd")
+    return grads
+
+
+@_on_stream
+def recurrence_decode(x, g_raw, i_raw, A_log, state, *, y=None, stream=None):
+    """kda_recurrence_decode: one token per request. x, g_raw, i_raw [requests, D] bf16 or fp32, rows evenly spaced;
+    `state` [requests, D] fp32 is updated in place. Returns y [requests, D]."""
+    dtype = x.dtype
+    if dtype not in _NORM_DTYPES:
+        raise ValueError(f"x: dtype {dtype}, expected bfloat16 or float32")
+    n, D = x.shape
+    lib = _lib or load()
+    dev = _ready([("A_log", A_log, D, _F32, False), ("state", state, n * D, _F32, False)])
+    shape = RecurrenceShape(n, 1, D, n, _NORM_DTYPES[dtype], 0, _rows("x", x, n, D, dtype, dev),
+                            _rows("g_raw", g_raw, n, D, dtype, dev), _rows("i_raw", i_raw, n, D, dtype, dev))
+    if y is None:
+        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    else:
+        shape.y_stride = _rows("y", y, n, D, dtype, dev)
+    code = lib.kda_recurrence_decode(ctypes.byref(shape), x.data_ptr(), g_raw.data_ptr(), i_raw.data_ptr(), A_log.data_ptr(),
+                                     state.data_ptr(), y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        _check(code, "kda_recurrence_decode")
+    return y
+
+
+def _qknorm_shape_of(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, more):
+    """Shape, device and checks of the inputs; `more` are (name, tensor, count, dtype, optional) specs besides."""
+    dtype = q.dtype
+    if dtype not in _NORM_DTYPES:
+        raise ValueError(f"q: dtype {dtype}, expected bfloat16 or float32")
+    if q.dim() < 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [T, heads, head_dim]")
+    head, Hq = q.shape[-1], q.shape[-2]
+    if head == 0 or Hq == 0:
+        raise ValueError(f"q: shape {tuple(q.shape)} has no heads to normalise")
+    T, Hk = q.numel() // (Hq * head), 0
+    if k is not None:
+        if k.dim() < 3 or k.shape[-1] != head:
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected [T, heads, {head}]")
+        Hk = k.shape[-2]
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    specs = more
+    if q_weight is not None:
+        specs.append(("q_weight", q_weight, head, _F32, True))
+    if k_weight is not None:
+        specs.append(("k_weight", k_weight, head, _F32, True))
+    if pairs:
+        specs += [("positions", positions, T, _I64, False), ("inv_freq", inv_freq, pairs, _F32, False)]
+    dev = q.get_device()
+    if specs and _ready(specs) not in (dev, -1):
+        raise ValueError(f"q: on {q.device}; every tensor must be on one CUDA device")
+    shape = QknormShape(T, Hq, Hk, head, 2 * pairs, int(interleaved), _NORM_DTYPES[dtype], eps,
+                        _rows("q", q, T, Hq * head, dtype, dev),
+                        _rows("k", k, T, Hk * head, dtype, dev) if k is not None else 0)
+    return shape, dev
+
+
+@_on_stream
+def qknorm_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, eps: float = 1e-6,
+               interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """kda_qknorm_fwd: every head of q and k [T, heads, head_dim] (or [B, T, heads, head_dim]; bf16 or fp32, tokens evenly
+    spaced) divided by its root mean square, times its weight [head_dim] fp32 (None reads as 1), its first
+    2 * len(inv_freq) columns rotated by positions [T] int64 * inv_freq fp32 (None: not rotated), pairs half of them apart or,
+    interleaved, neighbours. Returns (q_out, k_out)."""
+    lib = _lib or load()
+    shape, dev = _qknorm_shape_of(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, [])
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        shape.q_out_stride = _rows("q_out", q_out, shape.tokens, shape.q_heads * shape.head_dim, q.dtype, dev)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    else:
+        shape.k_out_stride = _rows("k_out", k_out, shape.tokens, shape.k_heads * shape.head_dim, q.dtype, dev)
+    code = lib.kda_qknorm_fwd(ctypes.byref(shape), q.data_ptr(), _address(k), _address(q_weight), _address(k_weight),
+                              _address(positions), _address(inv_freq), q_out.data_ptr(), _address(k_out),
+                              torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        _check(code, "kda_qknorm_fwd")
+    return q_out, k_out
+
+
+@_on_stream
+def qknorm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, eps: float = 1e-6,
+               interleaved: bool = False, grads=None, want_dweight: bool = True, workspace=None, stream=None):
+    """kda_qknorm_bwd with the forward's inputs and the outputs' adjoints. Returns a dict of dq, dk (in `grads` they may
+    be columns of one buffer), dq_weight and dk_weight ([head_dim] fp32)."""
+    lib = _lib or load()
+    more = []
+    if workspace is not None:
+        more.append(("workspace", workspace, workspace.numel(), _U8, False))
+    if grads is not None:
+        more += [("dq_weight", grads.get("dq_weight"), q.shape[-1], _F32, True),
+                 ("dk_weight", grads.get("dk_weight"), q.shape[-1], _F32, True)]
+    shape, dev = _qknorm_shape_of(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, more)
+    T, wq, wk = shape.tokens, shape.q_heads * shape.head_dim, shape.k_heads * shape.head_dim
+    shape.q_out_stride = _rows("dq_out", dq_out, T, wq, q.dtype, dev)
+    if k is not None:
+        if dk_out is None:
+            raise ValueError("dk_out is required")
+        shape.k_out_stride = _rows("dk_out", dk_out, T, wk, q.dtype, dev)
+    if workspace is None:
+        workspace = torch.empty(lib.kda_qknorm_workspace_size(ctypes.byref(shape)), dtype=_U8, device=q.device)
+    if grads is None:
+        def weight(wanted):
+            return torch.empty(shape.head_dim, dtype=_F32, device=q.device) if wanted else None
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+        grads = dict(dq=dq, dk=dk, dq_weight=weight(want_dweight), dk_weight=weight(want_dweight and k is not None))
+    else:
+        dq, dk = grads.get("dq"), grads.get("dk")
+        if dq is None or (dk is None and k is not None):
+            raise ValueError(f"{'dq' if dq is None else 'dk'} is required")
+        shape.dq_stride = _rows("dq", dq, T, wq, q.dtype, dev)
+        if k is not None:
+            shape.dk_stride = _rows("dk", dk, T, wk, q.dtype, dev)
+    code = lib.kda_qknorm_bwd(ctypes.byref(shape), q.data_ptr(), _address(k), dq_out.data_ptr(),
+                              _address(dk_out) if k is not None else None, _address(q_weight), _address(k_weight), _address(positions),
+                              _address(inv_freq), dq.data_ptr(), _address(dk) if k is not None else None,
+                              _address(grads.get("dq_weight")),
+                              _address(grads.get("dk_weight")), workspace.data_ptr(), workspace.numel(),
+                              torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        _check(code, "kda_qknorm_bwd")
     return grads
 
 

@@ -1,0 +1,213 @@
+"""Refusals of the gated recurrence and of the norm with rotation (CPU): the C ABI's status codes before any CUDA
+call, and the binding's checks of sizes, dtypes and layout."""
+import ctypes
+
+import pytest
+import torch
+
+from kimi_delta_attention_15_gb300 import build, ops
+
+DEVICE_MSG = "one CUDA device"
+BF, F32, I64 = torch.bfloat16, torch.float32, torch.int64
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return ops.load()
+
+
+def pointers(n, ptr, bad, by=8):
+    p = [ctypes.c_void_p(ptr + 64 * i if ptr else 0) for i in range(n)]
+    if bad is not None:
+        p[bad] = ctypes.c_void_p(ptr + 64 * bad + by)
+    return p
+
+
+def fwd(lib, shape, ptr=1 << 12, ws_bytes=1 << 40, cu=None, ws=1024, bad=None, by=8, same=False):
+    p = pointers(8, ptr, bad, by)                                   # x g_raw i_raw A_log h0 | y hT kept
+    if same:
+        p[6] = p[4]
+    return lib.kda_recurrence_fwd(ctypes.byref(shape), *p[:5], cu, *p[5:], ctypes.c_void_p(ws), ws_bytes, None)
+
+
+def bwd(lib, shape, ptr=1 << 12, ws_bytes=1 << 40, cu=None, ws=1024, bad=None, by=8, same=False):
+    p = pointers(13, ptr, bad, by)                                  # x g_raw i_raw A_log h0 | dy dhT kept dx dg di dA_log dh0
+    if same:
+        p[12] = p[6]
+    return lib.kda_recurrence_bwd(ctypes.byref(shape), *p[:5], cu, *p[5:], ctypes.c_void_p(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("call,states,tokens", [(fwd, (3, 4, 6, 7), (0, 1, 2, 5)), (bwd, (3, 4, 6, 7, 11, 12), (0, 1, 2, 5, 8, 9, 10))])
+def test_recurrence_status_codes(lib, call, states, tokens):
+    s = ops.recurrence_shape(64, 16, 1)
+    assert call(lib, s, ptr=0) == 1
+    for i in states:
+        assert call(lib, s, bad=i) == 2, i                          # states and parameters 16-byte aligned
+    for i in tokens:
+        assert call(lib, s, bad=i, by=1) == 2, i                    # tokens to an element
+    assert call(lib, s, same=True) == 4                             # hT = h0, dh0 = dhT
+    assert call(lib, s, ws_bytes=16) == 5 and call(lib, s, ws=0) == 5
+    assert call(lib, s, ws=1032) == 2
+    assert call(lib, s, cu=ctypes.c_void_p(20)) == 2
+    u = ops.recurrence_shape(64, 16, 1)
+    u.dtype = 2
+    assert call(lib, u) == 4
+    for bad in (ops.recurrence_shape(64, 0, 1), ops.recurrence_shape(-1, 16, 1), ops.recurrence_shape(64, 16, 3),
+                ops.recurrence_shape(64, (1 << 20) + 1, 1), ops.recurrence_shape(1 << 31, 16, 1),
+                ops.recurrence_shape(1 << 16, 16, 1 << 15, B=1 << 15)):
+        assert call(lib, bad) == 3
+    assert call(lib, ops.recurrence_shape(64, 16, 2, B=2), cu=ctypes.c_void_p(16)) == 3
+    assert call(lib, ops.recurrence_shape(64, 16, 0), cu=ctypes.c_void_p(16)) == 3      # tokens of no sequence
+    for name in ("x", "g", "i", "y", "dx", "dg", "di"):
+        for stride in (15, -16, 1 << 41):
+            u = ops.recurrence_shape(64, 16, 1)
+            setattr(u, name + "_stride", stride)
+            assert call(lib, u) == 3, (name, stride)
+    u = ops.recurrence_shape(64, 16, 1, dtype=F32)
+    for i in tokens:
+        assert call(lib, u, bad=i, by=2) == 2
+
+
+def test_recurrence_null_shape_and_workspace(lib):
+    null = ctypes.POINTER(ops.RecurrenceShape)()
+    assert lib.kda_recurrence_workspace_size(null, 0) == 0
+    assert lib.kda_recurrence_fwd(null, *[None] * 10, 0, None) == 1
+    assert lib.kda_recurrence_bwd(null, *[None] * 15, 0, None) == 1
+    assert lib.kda_recurrence_decode(null, *[None] * 7) == 1
+    f, b = (ops.recurrence_workspace_size(ops.recurrence_shape(1000, 64, 1), x) for x in (False, True))
+    assert 0 < f <= b
+    assert ops.recurrence_workspace_size(ops.recurrence_shape(1000, 0, 1)) == 0
+
+
+def test_recurrence_decode_status_codes(lib):
+    def call(n=2, D=16, T=1, ptr=1 << 12, bad=None, by=8, **kw):
+        s = ops.recurrence_shape(T, D, n, n)
+        for k, v in kw.items():
+            setattr(s, k, v)
+        p = pointers(6, ptr, bad, by)                               # x g_raw i_raw A_log state y
+        return lib.kda_recurrence_decode(ctypes.byref(s), *p, None)
+    assert call(n=-1) == 3 and call(D=0) == 3 and call(T=2) == 3 and call(N=3) == 3 and call(x_stride=8) == 3
+    assert call(dtype=7) == 4
+    assert call(ptr=0) == 1
+    for i in (3, 4):
+        assert call(bad=i) == 2
+    for i in (0, 1, 2, 5):
+        assert call(bad=i, by=1) == 2
+    assert call(n=0, ptr=0) == 0
+
+
+def qk_shape(T=5, Hq=4, Hk=2, head=64, rotary=64, interleaved=0, dtype=0, eps=1e-6, **kw):
+    s = ops.QknormShape(T, Hq, Hk, head, rotary, interleaved, dtype, eps)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def qk_fwd(lib, shape, ptr=1 << 12, bad=None, by=8, none=()):
+    p = pointers(8, ptr, bad, by)                                   # q k q_weight k_weight positions inv_freq q_out k_out
+    for i in none:
+        p[i] = None
+    return lib.kda_qknorm_fwd(ctypes.byref(shape), *p, None)
+
+
+def qk_bwd(lib, shape, ptr=1 << 12, bad=None, by=8, none=(), ws=1024, ws_bytes=1 << 40):
+    p = pointers(12, ptr, bad, by)                  # q k dq_out dk_out q_weight k_weight positions inv_freq dq dk dq_weight dk_weight
+    for i in none:
+        p[i] = None
+    return lib.kda_qknorm_bwd(ctypes.byref(shape), *p, ctypes.c_void_p(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("call,n,at,needed", [(qk_fwd, 8, 4, (0, 1, 4, 5, 6, 7)), (qk_bwd, 12, 6, (0, 1, 2, 3, 6, 7, 8, 9))])
+def test_qknorm_status_codes(lib, call, n, at, needed):
+    for i in needed:
+        assert call(lib, qk_shape(), none=(i,)) == 1, i
+    for i in range(n):
+        assert call(lib, qk_shape(), bad=i, by=4 if i == at else 8) == 2, i
+    for kw in (dict(T=-1), dict(T=1 << 31), dict(Hq=0), dict(Hk=-1), dict(Hq=1 << 21), dict(q_stride=255 - 7), dict(k_stride=64),
+               dict(dk_stride=-128), dict(q_out_stride=1 << 41)):
+        assert call(lib, qk_shape(**kw)) == 3, kw
+    for kw in (dict(head=0), dict(head=264), dict(head=60), dict(rotary=72), dict(rotary=4), dict(rotary=-8), dict(interleaved=2),
+               dict(dtype=2), dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf"))):
+        assert call(lib, qk_shape(**kw)) == 4, kw
+    assert call(lib, qk_shape(q_stride=260)) == 2                    # rows on 16 bytes
+    assert call(lib, qk_shape(dtype=1, q_stride=258)) == 2
+
+
+def test_qknorm_workspace(lib):
+    assert qk_bwd(lib, qk_shape(), ws=0) == 5 and qk_bwd(lib, qk_shape(), ws_bytes=16) == 5 and qk_bwd(lib, qk_shape(), ws=1032) == 2
+    assert lib.kda_qknorm_workspace_size(ctypes.byref(qk_shape())) > 0
+    assert lib.kda_qknorm_workspace_size(ctypes.byref(qk_shape(head=12))) == 0
+    null = ctypes.POINTER(ops.QknormShape)()
+    assert lib.kda_qknorm_workspace_size(null) == 0
+    assert lib.kda_qknorm_fwd(null, *[None] * 9) == 1 and lib.kda_qknorm_bwd(null, *[None] * 13, 0, None) == 1
+    assert qk_fwd(lib, qk_shape(T=0), ptr=0) == 0
+
+
+def test_binding_refuses(lib):
+    x, A = torch.zeros(8, 16, dtype=BF), torch.zeros(16)
+    with pytest.raises(ValueError, match=DEVICE_MSG):
+        ops.recurrence_fwd(x, x, x, A)
+    with pytest.raises(ValueError, match=DEVICE_MSG):
+        ops.recurrence_bwd(x, x, x, A, x, torch.zeros(1, 16))
+    with pytest.raises(ValueError, match=DEVICE_MSG):
+        ops.recurrence_decode(x, x, x, A, torch.zeros(8, 16))
+    with pytest.raises(ValueError, match=DEVICE_MSG):
+        ops.qknorm_fwd(torch.zeros(2, 3, 8))
+    with pytest.raises(ValueError, match=DEVICE_MSG):
+        ops.qknorm_bwd(torch.zeros(2, 3, 8), None, torch.zeros(2, 3, 8), None)
+    with pytest.raises(ValueError, match="x: dtype torch.float16"):
+        ops.recurrence_fwd(x.half(), x, x, A)
+    with pytest.raises(ValueError, match="x: shape"):
+        ops.recurrence_fwd(x.view(-1), x, x, A)
+    with pytest.raises(ValueError, match="B: 8 tokens are no 3 sequences"):
+        ops.recurrence_fwd(x, x, x, A, B=3)
+    with pytest.raises(ValueError, match="A_log: 15 elements"):
+        ops.recurrence_fwd(x, x, x, A[:15].clone())
+    with pytest.raises(ValueError, match="A_log: dtype"):
+        ops.recurrence_decode(x, x, x, A.double(), torch.zeros(8, 16))
+    with pytest.raises(ValueError, match="kept: 32 elements"):
+        ops.recurrence_bwd(x, x, x, A, x, torch.zeros(2, 16))
+    with pytest.raises(ValueError, match="q: dtype"):
+        ops.qknorm_fwd(torch.zeros(2, 3, 8, dtype=torch.float64))
+    with pytest.raises(ValueError, match="k: shape"):
+        ops.qknorm_fwd(torch.zeros(2, 3, 8), torch.zeros(2, 3, 16))
+    with pytest.raises(ValueError, match="positions is required"):
+        ops.qknorm_fwd(torch.zeros(2, 3, 8), inv_freq=torch.zeros(4))
+    with pytest.raises(ValueError, match="q: shape"):
+        ops.qknorm_fwd(torch.zeros(2, 8))
+
+
+class OnGpu:
+    """A tensor's layout on a pretended device 0."""
+
+    def __init__(self, t):
+        self.t, self.dtype, self.shape, self.device = t, t.dtype, t.shape, torch.device("cuda", 0)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return 0
+
+
+def test_rows_of_wider_buffers():
+    rows = lambda t, n, inner: ops._rows("t", OnGpu(t), n, inner, t.dtype, 0)
+    buf = torch.zeros(6, 40)
+    assert rows(buf, 6, 40) == 40
+    assert rows(buf[:, 8:24], 6, 16) == 40
+    assert rows(buf[:, 8:24].unflatten(1, (2, 8)), 6, 16) == 40
+    assert rows(buf[::2, :16], 3, 16) == 80
+    assert rows(buf[1:2, :16], 1, 16) == 16
+    assert rows(buf.view(2, 3, 40)[..., :16], 6, 16) == 40
+    assert rows(torch.zeros(0, 16), 0, 16) == 16
+    for t, n, inner, match in ((buf[:, ::2], 6, 20, "contiguous"), (buf.t()[:6], 6, 6, "contiguous"),
+                               (buf[:1].expand(6, 40), 6, 40, "overlap"), (buf.view(2, 3, 40)[:, :2, :16], 4, 16, "evenly"),
+                               (buf[:, :16].view(6, 2, 8).transpose(1, 2), 6, 16, "contiguous"),
+                               (torch.zeros(60).as_strided((6, 16), (8, 1)), 6, 16, "overlap"), (buf, 5, 40, "elements")):
+        with pytest.raises(ValueError, match=match):
+            rows(t, n, inner)
+    with pytest.raises(ValueError, match=DEVICE_MSG):
+        ops._rows("t", buf, 6, 40, F32, 0)
+    with pytest.raises(ValueError, match="dtype"):
+        ops._rows("t", OnGpu(buf), 6, 40, BF, 0)
