@@ -272,7 +272,7 @@ kda_status kda_layernorm_bwd(long long rows, long long width, int dtype,
 typedef struct {
     int64_t B;        /* fixed-length batch rows; 1 when packed */
     int64_t T;        /* tokens per row; total tokens when packed */
-    int64_t D;        /* channels, 1 .. 2^20 */
+    int64_t D;        /* channels, 1 .. 2^20; B*T, N at most 2^31 - 2^16 */
     int64_t N;        /* sequences: B when cu_seqlens is NULL, else len(cu_seqlens) - 1 */
     int32_t dtype;    /* kda_dtype of the token tensors */
     int32_t reserved; /* 0 */

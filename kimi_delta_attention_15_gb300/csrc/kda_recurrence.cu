@@ -6,16 +6,25 @@
 //   du u = G (i x a^2 u / m - u a h_{t-1}),  dg_raw = du u (1 - s),  dA_log = sum du u
 // em = 1 - a is what the arithmetic holds: -expm1(-u), a series for small u, so that h += b - em h keeps
 // fp32's precision over memories of any length, and m = sqrt(em (2 - em)) has no cancellation.
-// Simple form: a thread takes a channel of a sequence, token after token.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 #include "kda_internal.cuh"
+#include "umma_bf16.cuh"
 
 namespace kda {
 void set_last_error_text(const char* msg);
 
 namespace {
 constexpr int kBlock = KDA_RECURRENCE_BLOCK;
+constexpr int kCh = 64;              // channels of a block, two to a lane
+constexpr int kTok = 8;              // tokens of a warp
+constexpr int kWarps = kBlock / kTok;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMostRanks = 8;
+constexpr int kMostSegs = 64;
+constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float get(const uint16_t* p) { return bf2f(*p); }
@@ -23,40 +32,38 @@ __device__ __forceinline__ float get(const float* p) { return *p; }
 __device__ __forceinline__ void put(uint16_t* p, float x) { *p = f2bf(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 
+__device__ __forceinline__ float exp2_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float inverse(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // sigmoid(x) and 1 - sigmoid(x), without cancellation at either end
 struct Sigmoid {
     float s, c;
 };
+__device__ __forceinline__ float exp_minus(float x) { return exp2_of(fminf(-x * kLog2e, 126.0f)); }   // finite
 __device__ __forceinline__ Sigmoid sigmoid2(float x) {
-    const float e = exp2f(fminf(-x * kLog2e, 126.0f));   // finite, so that e * s is
-    const float s = 1.0f / (1.0f + e);
+    const float e = exp_minus(x), s = inverse(1.0f + e);
     return {s, e * s};
 }
 
 // 1 - exp(-u) for u >= 0: below 1/4 the series u - u^2/2 + u^3/6 .. u^6/720 (the next term is 5e-8 of the sum), above
 // it 1 - exp(-u), which loses two bits at most there
 __device__ __forceinline__ float one_minus_exp(float u) {
-    const float p = u * (1.0f + u * (-1.0f / 2 + u * (1.0f / 6 + u * (-1.0f / 24 + u * (1.0f / 120 + u * (-1.0f / 720))))));
-    return u < 0.25f ? p : 1.0f - exp2f(-u * kLog2e);
+    const float p = u * fmaf(u, fmaf(u, fmaf(u, fmaf(u, fmaf(u, -1.0f / 720, 1.0f / 120), -1.0f / 24), 1.0f / 6), -0.5f), 1.0f);
+    return u < 0.25f ? p : 1.0f - exp2_of(-u * kLog2e);
 }
-
-// [first, last) of sequence n, within the tokens whatever the offsets hold
-__device__ __forceinline__ void range_of(const int64_t* cu, int64_t T, int64_t total, int64_t n, int64_t& first, int64_t& last) {
-    first = cu ? cu[n] : n * T;
-    last = cu ? cu[n + 1] : (n + 1) * T;
-    first = first < 0 ? 0 : first > total ? total : first;
-    last = last < first ? first : last > total ? total : last;
-}
-
-// the first block checks the offsets and writes the status word
-__device__ __forceinline__ void check_offsets(const int64_t* cu, int64_t N, int64_t total, uint8_t* ws) {
-    int bad = 0;
-    if (cu) {
-        for (int64_t n = threadIdx.x; n < N; n += blockDim.x) bad |= cu[n] > cu[n + 1];
-        bad |= cu[0] != 0 || cu[N] != total;
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *reinterpret_cast<int*>(ws) = bad ? KDA_ERR_OFFSETS : KDA_OK;
+// 1 / sqrt(x), 0 at 0
+__device__ __forceinline__ float rsqrt_or_0(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return x > 1.2e-38f ? r : 0.0f;
 }
 
 struct RecArgs {
@@ -65,86 +72,561 @@ struct RecArgs {
     const int64_t* cu;
     void *y, *dx, *dg, *di;
     float *hT, *kept, *dh0, *part;
+    float4* seg;         // [segments][channel pairs] what each segment does to a state: a0, b0, a1, b1
     uint8_t* ws;
-    int64_t total, T, D, N, sx, sg, si, sy, sdx, sdg, sdi;
+    int64_t D, sx, sg, si, sy, sdx, sdg, sdi;
+    int total, T, N, chunks, seg_chunks, ranks;
 };
 
-template <typename T> __global__ void __launch_bounds__(128) rec_fwd_kernel(const RecArgs a) {
-    if (blockIdx.x == 0) check_offsets(a.cu, a.N, a.total, a.ws);
-    const int64_t tiles = (a.D + 127) / 128, c = (blockIdx.x % tiles) * 128 + threadIdx.x, n = blockIdx.x / tiles;
-    if (c >= a.D) return;
-    int64_t first, last;
-    range_of(a.cu, a.T, a.total, n, first, last);
-    float h = a.h0 ? a.h0[n * a.D + c] : 0.0f;
-    const float lam = expf(a.A_log[c]);
-    if (a.kept && first == 0 && last > 0) a.kept[c] = 0.0f;
-    for (int64_t t = first; t < last; ++t) {
-        const Sigmoid s = sigmoid2(get(static_cast<const T*>(a.g) + t * a.sg + c));
-        const Sigmoid i = sigmoid2(get(static_cast<const T*>(a.i) + t * a.si + c));
-        const float em = one_minus_exp(lam * s.s);
-        const float b = sqrtf(em * (2.0f - em)) * i.s * get(static_cast<const T*>(a.x) + t * a.sx + c);
-        h += b - em * h;
-        put(static_cast<T*>(a.y) + t * a.sy + c, h);
-        if (a.kept && (t + 1) % kBlock == 0 && t + 1 < a.total) a.kept[(t + 1) / kBlock * a.D + c] = h;
-    }
-    if (a.hT) a.hT[n * a.D + c] = h;
+// ---------------------------------------------------------------- two channels of a lane
+struct F2 {
+    float v[2];
+};
+// What a run of tokens does to a state that comes to it: a h + b; a < 0 where a sequence starts in it, which leaves b
+// whatever h is, also where that is no number.
+__device__ __forceinline__ float over(float a, float b, float h) { return a < 0.0f ? b : fmaf(a, h, b); }
+__device__ __forceinline__ void over2(const float4& s, F2& h) {
+    h.v[0] = over(s.x, s.y, h.v[0]);
+    h.v[1] = over(s.z, s.w, h.v[1]);
+}
+// first s, then t
+__device__ __forceinline__ float4 then(const float4& s, const float4& t) {
+    return make_float4(t.x < 0.0f || s.x < 0.0f ? -1.0f : t.x * s.x, over(t.x, t.y, s.y),
+                       t.z < 0.0f || s.z < 0.0f ? -1.0f : t.z * s.z, over(t.z, t.w, s.w));
 }
 
-template <typename T> __global__ void __launch_bounds__(128) rec_bwd_kernel(const RecArgs a) {
-    if (blockIdx.x == 0) check_offsets(a.cu, a.N, a.total, a.ws);
-    const int64_t tiles = (a.D + 127) / 128, c = (blockIdx.x % tiles) * 128 + threadIdx.x, n = blockIdx.x / tiles;
-    if (c >= a.D) return;
-    int64_t first, last;
-    range_of(a.cu, a.T, a.total, n, first, last);
-    const float lam = expf(a.A_log[c]);
-    float acc = 0.0f, G = a.dhT ? a.dhT[n * a.D + c] : 0.0f;
-    float before[kBlock];
-    for (int64_t j = (last - 1) / kBlock; last > first && j >= first / kBlock; --j) {
-        const int64_t t0 = j * kBlock > first ? j * kBlock : first, t1 = (j + 1) * kBlock < last ? (j + 1) * kBlock : last;
-        float h = t0 == first ? (a.h0 ? a.h0[n * a.D + c] : 0.0f) : a.kept[j * a.D + c];
-        for (int64_t t = t0; t < t1; ++t) {
-            before[t - t0] = h;
-            const float em = one_minus_exp(lam * sigmoid2(get(static_cast<const T*>(a.g) + t * a.sg + c)).s);
-            const float i = sigmoid2(get(static_cast<const T*>(a.i) + t * a.si + c)).s;
-            h += sqrtf(em * (2.0f - em)) * i * get(static_cast<const T*>(a.x) + t * a.sx + c) - em * h;
-        }
-        for (int64_t t = t1 - 1; t >= t0; --t) {
-            const Sigmoid s = sigmoid2(get(static_cast<const T*>(a.g) + t * a.sg + c));
-            const Sigmoid i = sigmoid2(get(static_cast<const T*>(a.i) + t * a.si + c));
-            const float x = get(static_cast<const T*>(a.x) + t * a.sx + c);
-            const float u = lam * s.s, em = one_minus_exp(u), m2 = em * (2.0f - em), m = sqrtf(m2), d = 1.0f - em;
-            G += get(static_cast<const T*>(a.dy) + t * a.sy + c);
-            const float duu = G * (i.s * x * d * d * (m > 0.0f ? u / m : 0.0f) - u * d * before[t - t0]);
-            acc += duu;
-            put(static_cast<T*>(a.dx) + t * a.sdx + c, G * m * i.s);
-            put(static_cast<T*>(a.dg) + t * a.sdg + c, duu * s.c);
-            put(static_cast<T*>(a.di) + t * a.sdi + c, G * m * x * i.s * i.c);
-            G -= em * G;
-        }
+template <typename T> __device__ __forceinline__ F2 pair_at(const T* p);
+template <> __device__ __forceinline__ F2 pair_at<uint16_t>(const uint16_t* p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+}
+template <> __device__ __forceinline__ F2 pair_at<float>(const float* p) {
+    const float2 w = *reinterpret_cast<const float2*>(p);
+    return {w.x, w.y};
+}
+__device__ __forceinline__ void put_pair(uint16_t* p, const F2& f) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.v[0], f.v[1]);
+    __stcs(reinterpret_cast<uint32_t*>(p), *reinterpret_cast<const uint32_t*>(&h));
+}
+__device__ __forceinline__ void put_pair(float* p, const F2& f) { __stcs(reinterpret_cast<float2*>(p), make_float2(f.v[0], f.v[1])); }
+
+// The lane's channels c, c + 1 of a row, where they exist (kVec: rows and widths are whole 16-byte units)
+template <bool kVec, typename T> __device__ __forceinline__ void store_pair(T* row, int64_t c, int64_t D, const F2& f) {
+    if constexpr (kVec) {
+        if (c < D) put_pair(row + c, f);
+    } else {
+        if (c < D) put(row + c, f.v[0]);
+        if (c + 1 < D) put(row + c + 1, f.v[1]);
     }
-    if (a.dh0) a.dh0[n * a.D + c] = G;
-    if (a.part) a.part[n * a.D + c] = acc;
+}
+template <bool kVec> __device__ __forceinline__ F2 load_state(const float* p, int64_t row, int64_t c, int64_t D) {
+    if (!p) return {0.0f, 0.0f};
+    p += row * D;
+    if constexpr (kVec) {
+        if (c >= D) return {0.0f, 0.0f};
+        return pair_at(p + c);
+    } else {
+        return {c < D ? p[c] : 0.0f, c + 1 < D ? p[c + 1] : 0.0f};
+    }
+}
+template <bool kVec> __device__ __forceinline__ void store_state(float* p, int64_t row, int64_t c, int64_t D, const F2& f) {
+    store_pair<kVec>(p + row * D, c, D, f);
 }
 
-__global__ void __launch_bounds__(128) rec_sum_kernel(const float* part, int64_t parts, int64_t D, float* out) {
-    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (c >= D) return;
+// A warp's kTok rows of one token tensor into its own shared memory, [kTok][kCh], zeros outside the tensor
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_rows(T* dst, const void* src, int64_t stride, int t0, int total, int64_t c0, int64_t D) {
+    const int lane = threadIdx.x & 31;
+    const T* const from = static_cast<const T*>(src);
+    if constexpr (kVec) {
+        constexpr int V = 16 / sizeof(T), units = kCh / V, rows = 32 / units;
+        const int u = lane % units;
+#pragma unroll
+        for (int j = 0; j < kTok / rows; ++j) {
+            const int r = j * rows + lane / units;
+            const bool in = t0 + r < total && c0 + u * V < D;
+            const T* p = from + (in ? (int64_t)(t0 + r) * stride + c0 + u * V : 0);
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * kCh + u * V);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(in ? 16 : 0) : "memory");
+        }
+    } else {
+        const int64_t c = c0 + 2 * lane;
+        T a[kTok], b[kTok];
+#pragma unroll
+        for (int r = 0; r < kTok; ++r) {
+            const bool in = t0 + r < total;
+            const T* p = from + (int64_t)(t0 + r) * stride + c;
+            a[r] = in && c < D ? p[0] : T(0);
+            b[r] = in && c + 1 < D ? p[1] : T(0);
+        }
+#pragma unroll
+        for (int r = 0; r < kTok; ++r) {
+            dst[r * kCh + 2 * lane] = a[r];
+            dst[r * kCh + 2 * lane + 1] = b[r];
+        }
+    }
+}
+__device__ __forceinline__ void loads_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void loads_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+// -------------------------------------------------------------------------- sequences
+// The last sequence that starts at or before token t (0 where there is none, so that any offsets at all give
+// a sequence of the N), by the whole warp.
+__device__ __forceinline__ int64_t start_of(const RecArgs& a, int n) { return a.cu ? a.cu[n] : (int64_t)n * a.T; }
+__device__ __forceinline__ int sequence_at(const RecArgs& a, int t) {
+    if (!a.cu) return t / a.T;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.N;            // the count of starts cu[0 .. N - 1] <= t is between
+    while (hi > lo) {
+        const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi) - 1;
+        const int n = __popc(__ballot_sync(0xffffffffu, lo + lane * step < hi && a.cu[at] <= t));
+        hi = min(hi, lo + (n + 1) * step - 1);
+        lo = min(hi, lo + n * step);
+    }
+    return max(lo - 1, 0);
+}
+
+// Starts and ends of sequences among a warp's tokens t0 .. t0 + kTok - 1, one bit each; the sequence of token t0 + j is lane
+// j's. Remembers the sequence between calls.
+struct Events {
+    uint32_t starts = 0, ends = 0;
+    int n = -1;
+    int64_t first = 0, last = 0;
+    int seq = 0;
+    __device__ __forceinline__ bool find(const RecArgs& a, int t0) {
+        starts = ends = 0;
+        if (t0 >= a.total) return false;
+        if (n < 0 || t0 < first || t0 >= last) {
+            n = sequence_at(a, t0);
+            first = start_of(a, n);
+            last = start_of(a, n + 1);
+        }
+        if (first < t0 && last > t0 + kTok) return false;
+        const int lane = threadIdx.x & 31, t = t0 + lane;
+        const bool in = lane < kTok && t < a.total;
+        int lo = n, hi = a.N - 1;    // the last sequence from n on that starts at or before t
+        if (in) {
+            if (!a.cu) lo = t / a.T;
+            else
+                while (lo < hi) {
+                    const int mid = lo + (hi - lo + 1) / 2;
+                    if (a.cu[mid] <= t) lo = mid;
+                    else hi = mid - 1;
+                }
+        }
+        seq = lo;
+        starts = __ballot_sync(0xffffffffu, in && start_of(a, lo) == t);
+        ends = __ballot_sync(0xffffffffu, in && start_of(a, lo + 1) == t + 1);
+        return (starts | ends) != 0;
+    }
+    __device__ __forceinline__ int of(int j) const { return __shfl_sync(0xffffffffu, seq, j); }
+};
+
+// The states of sequences without tokens go through as they are, a share of the sequences for each warp of the blocks
+// along the tokens.
+template <bool kVec>
+__device__ __forceinline__ void pass_empty(const RecArgs& a, float* out, const float* in, int64_t c) {
+    if (!out) return;
+    const int lane = threadIdx.x & 31, warps = gridDim.x * kWarps;
+    for (int64_t n0 = (int64_t)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * 32; n0 < a.N; n0 += (int64_t)warps * 32) {
+        const int64_t n = n0 + lane;
+        uint32_t left = __ballot_sync(0xffffffffu, n < a.N && start_of(a, (int)min(n, (int64_t)a.N - 1)) == start_of(a, (int)min(n, (int64_t)a.N - 1) + 1));
+        while (left) {
+            const int j = __ffs(left) - 1;
+            left &= left - 1;
+            store_state<kVec>(out, n0 + j, c, a.D, load_state<kVec>(in, n0 + j, c, a.D));
+        }
+    }
+}
+
+// The first block checks the offsets and writes the status word.
+__device__ __forceinline__ void check_offsets(const RecArgs& a) {
+    int bad = 0;
+    if (a.cu) {
+#pragma unroll 4
+        for (int n = threadIdx.x; n < a.N; n += kThreads) bad |= a.cu[n] > a.cu[n + 1];
+        bad |= a.cu[0] != 0 || a.cu[a.N] != a.total;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *reinterpret_cast<int*>(a.ws) = bad ? KDA_ERR_OFFSETS : KDA_OK;
+}
+
+// ------------------------------------------------------------------ blocks of a cluster
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ void store_at_rank(float4* p, int rank, const float4& v) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
+    float4 warp[2][kWarps][32];
+    float4 rank[2][kMostRanks][32];
+};
+
+// After a step's own sums: the state (adjoint) that comes to this warp, and in `carry` the one that leaves the step.
+// Warps and ranks follow one another in the order of the scan, `w` and `r` their places in it.
+template <bool kTotal>
+__device__ __forceinline__ F2 exchange(Shares& sh, int parity, int ranks, int r, int w, const float4& own, F2& carry, float4& total) {
+    const int lane = threadIdx.x & 31;
+    sh.warp[parity][w][lane] = own;
+    __syncthreads();
+    F2 at = carry;
+    if (ranks > 1) {
+        if (w == 0) {
+            float4 s = sh.warp[parity][0][lane];
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v) s = then(s, sh.warp[parity][v][lane]);
+            for (int k = 0; k < ranks; ++k) store_at_rank(&sh.rank[parity][r][lane], k, s);
+        }
+        cluster_arrive();
+        cluster_wait();
+        for (int k = 0; k < ranks; ++k) {
+            if (k == r) at = carry;
+            const float4 s = sh.rank[parity][k][lane];
+            if constexpr (kTotal) total = then(total, s);
+            else over2(s, carry);
+        }
+        if constexpr (!kTotal)
+            for (int v = 0; v < w; ++v) over2(sh.warp[parity][v][lane], at);
+    } else {
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+            if (v == w) at = carry;
+            if constexpr (kTotal) total = then(total, sh.warp[parity][v][lane]);
+            else over2(sh.warp[parity][v][lane], carry);
+        }
+    }
+    return at;
+}
+
+// The state that comes to segment `seg`, in the order of the scan, from what those before it did
+__device__ __forceinline__ F2 into_segment(const RecArgs& a, int seg, int64_t c) {
+    F2 h{0.0f, 0.0f};
+    const int64_t pairs = (a.D + 1) / 2;
+    if (c < a.D)
+        for (int s = 0; s < seg; ++s) over2(a.seg[s * pairs + c / 2], h);
+    return h;
+}
+
+// Grid: x segments x ranks of a cluster, y tiles of kCh channels. A cluster takes a segment's chunks of kBlock
+// tokens, its blocks the chunks of a step next to one another, a warp kTok tokens of a chunk, a lane two channels.
+// kTotal: only what the segment does to a state, for the segments after it.
+template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kernel(const RecArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shares& sh = *reinterpret_cast<Shares*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    T* const rows = reinterpret_cast<T*>(smem + sizeof(Shares)) + warp * (3 * kTok * kCh);
+    const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
+    const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
+    const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);
+    const int steps = (last - first + a.ranks - 1) / a.ranks;
+    auto load = [&](int step) {
+        const int chunk = first + step * a.ranks + r;
+        const int t0 = chunk < last ? chunk * kBlock + warp * kTok : a.total;     // zeros beyond the segment
+        load_rows<kVec>(rows, a.x, a.sx, t0, a.total, c0, a.D);
+        load_rows<kVec>(rows + kTok * kCh, a.g, a.sg, t0, a.total, c0, a.D);
+        load_rows<kVec>(rows + 2 * kTok * kCh, a.i, a.si, t0, a.total, c0, a.D);
+    };
+    load(0);
+    loads_done();
+    if (a.ranks > 1) cluster_arrive();
+    F2 lam;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) lam.v[e] = c + e < a.D ? expf(a.A_log[c + e]) : 0.0f;
+    F2 carry = kTotal ? F2{0.0f, 0.0f} : into_segment(a, seg, c);
+    float4 total = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    if constexpr (!kTotal) {
+        if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
+        pass_empty<kVec>(a, a.hT, a.h0, c);
+    }
+    if (a.ranks > 1) cluster_wait();       // the cluster's blocks all run, before one writes into another
+    Events ev;
+    for (int step = 0; step < steps; ++step) {
+        const int chunk = first + step * a.ranks + r;
+        const bool some = chunk < last;
+        const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;   // tokens of the warp
+        const bool events = some && ev.find(a, t0);
+        loads_wait<0>();
+        __syncwarp();
+        float em[kTok][2], b[kTok][2];
+        F2 h{0.0f, 0.0f}, sum{0.0f, 0.0f};
+        bool fresh = false;
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            const F2 x = pair_at(rows + j * kCh + 2 * lane), g = pair_at(rows + (kTok + j) * kCh + 2 * lane),
+                     i = pair_at(rows + (2 * kTok + j) * kCh + 2 * lane);
+            if (events && (ev.starts >> j & 1)) {
+                h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                fresh = true;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float u = j < left ? lam.v[e] * sigmoid2(g.v[e]).s : 0.0f;
+                em[j][e] = one_minus_exp(u);
+                const float m2 = em[j][e] * (2.0f - em[j][e]);
+                b[j][e] = m2 * rsqrt_or_0(m2) * sigmoid2(i.v[e]).s * x.v[e];
+                h.v[e] += fmaf(-em[j][e], h.v[e], b[j][e]);
+                sum.v[e] += u;
+            }
+        }
+        __syncwarp();
+        if (step + 1 < steps) load(step + 1);
+        loads_done();
+        const float4 own = make_float4(fresh ? -1.0f : exp2_of(-sum.v[0] * kLog2e), h.v[0], fresh ? -1.0f : exp2_of(-sum.v[1] * kLog2e), h.v[1]);
+        h = exchange<kTotal>(sh, step & 1, a.ranks, r, warp, own, carry, total);
+        if constexpr (!kTotal) {
+            if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
+            T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.sy;
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) {
+                if (events && (ev.starts >> j & 1)) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) h.v[e] += fmaf(-em[j][e], h.v[e], b[j][e]);
+                if (j < left) store_pair<kVec>(y + j * a.sy, c, a.D, h);
+                if (events && (ev.ends >> j & 1)) {
+                    const int n = ev.of(j);
+                    if (a.hT) store_state<kVec>(a.hT, n, c, a.D, h);
+                }
+            }
+        }
+    }
+    if constexpr (kTotal)
+        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = total;
+}
+
+// The same grid, tokens from the last to the first: chunks, ranks and warps in that order.
+template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const RecArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shares& sh = *reinterpret_cast<Shares*>(smem);
+    float4 (*const ahead)[32] = reinterpret_cast<float4 (*)[32]>(smem + sizeof(Shares));     // [2 kWarps][32] the states' way forwards
+    constexpr int kTensors = kTotal ? 2 : 4, kStages = sizeof(T) == 2 && !kTotal ? 2 : 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    T* const base = reinterpret_cast<T*>(smem + sizeof(Shares) + 2 * kWarps * 32 * sizeof(float4)) + warp * (kStages * kTensors * kTok * kCh);
+    const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
+    const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
+    const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);   // counted from the last chunk
+    const int steps = (last - first + a.ranks - 1) / a.ranks;
+    auto load = [&](int step) {
+        const int at = first + step * a.ranks + r;
+        T* const rows = base + (kStages == 2 ? (step & 1) * kTensors * kTok * kCh : 0);
+        const int t0 = at < last ? (a.chunks - 1 - at) * kBlock + warp * kTok : a.total;
+        load_rows<kVec>(rows, a.g, a.sg, t0, a.total, c0, a.D);
+        load_rows<kVec>(rows + kTok * kCh, a.dy, a.sy, t0, a.total, c0, a.D);
+        if constexpr (!kTotal) {
+            load_rows<kVec>(rows + 2 * kTok * kCh, a.x, a.sx, t0, a.total, c0, a.D);
+            load_rows<kVec>(rows + 3 * kTok * kCh, a.i, a.si, t0, a.total, c0, a.D);
+        }
+    };
+    load(0);
+    loads_done();
+    if (a.ranks > 1) cluster_arrive();
+    F2 lam;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) lam.v[e] = c + e < a.D ? expf(a.A_log[c + e]) : 0.0f;
+    F2 carry = kTotal ? F2{0.0f, 0.0f} : into_segment(a, seg, c);
+    float4 total = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    if constexpr (!kTotal) {
+        if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
+        pass_empty<kVec>(a, a.dh0, a.dhT, c);
+    }
+    if (a.ranks > 1) cluster_wait();
+    Events ev;
+    F2 acc{0.0f, 0.0f};
+    for (int step = 0; step < steps; ++step) {
+        const int at = first + step * a.ranks + r, chunk = a.chunks - 1 - at;
+        const bool some = at < last;
+        const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;
+        const bool events = some && ev.find(a, t0);
+        T* const rows = base + (kStages == 2 ? (step & 1) * kTensors * kTok * kCh : 0) + 2 * lane;
+        if constexpr (kStages == 2) {
+            __syncwarp();          // the last lane's reads of the step before last
+            if (step + 1 < steps) load(step + 1);
+            loads_done();
+            loads_wait<1>();
+        } else {
+            loads_wait<0>();
+        }
+        __syncwarp();
+        float s[kTok][2], em[kTok][2], si[kTok][2], rs[kTok][2];
+        F2 h{0.0f, 0.0f}, sum{0.0f, 0.0f}, G{0.0f, 0.0f};
+        bool fresh = false, ended = false;
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            const F2 g = pair_at(rows + j * kCh);
+            F2 x{0.0f, 0.0f}, i{0.0f, 0.0f};
+            if constexpr (!kTotal) {
+                x = pair_at(rows + (2 * kTok + j) * kCh);
+                i = pair_at(rows + (3 * kTok + j) * kCh);
+                if (events && (ev.starts >> j & 1)) {
+                    h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                    fresh = true;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                s[j][e] = j < left ? sigmoid2(g.v[e]).s : 0.0f;
+                const float u = lam.v[e] * s[j][e];
+                em[j][e] = one_minus_exp(u);
+                sum.v[e] += u;
+                if constexpr (!kTotal) {
+                    const float m2 = em[j][e] * (2.0f - em[j][e]);
+                    rs[j][e] = rsqrt_or_0(m2);
+                    si[j][e] = sigmoid2(i.v[e]).s;
+                    h.v[e] += fmaf(-em[j][e], h.v[e], m2 * rs[j][e] * si[j][e] * x.v[e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = kTok - 1; j >= 0; --j) {
+            if (events && (ev.ends >> j & 1)) {
+                G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
+                ended = true;
+            }
+            const F2 dy = pair_at(rows + (kTok + j) * kCh);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float t = G.v[e] + dy.v[e];
+                G.v[e] = fmaf(-em[j][e], t, t);
+            }
+        }
+        const float a0 = exp2_of(-sum.v[0] * kLog2e), a1 = exp2_of(-sum.v[1] * kLog2e);
+        if constexpr (!kTotal) ahead[(step & 1) * kWarps + warp][lane] = make_float4(fresh ? -1.0f : a0, h.v[0], fresh ? -1.0f : a1, h.v[1]);
+        const float4 own = make_float4(ended ? -1.0f : a0, G.v[0], ended ? -1.0f : a1, G.v[1]);
+        if constexpr (!kTotal) h = some ? load_state<kVec>(a.kept, chunk, c, a.D) : F2{0.0f, 0.0f};
+        G = exchange<kTotal>(sh, step & 1, a.ranks, r, kWarps - 1 - warp, own, carry, total);
+        if constexpr (kTotal) {
+            __syncwarp();
+            if (step + 1 < steps) load(step + 1);
+            loads_done();
+        } else {
+            for (int v = 0; v < warp; ++v) over2(ahead[(step & 1) * kWarps + v][lane], h);
+            float before[kTok][2];
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) {
+                if (events && (ev.starts >> j & 1)) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                const F2 x = pair_at(rows + (2 * kTok + j) * kCh);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    before[j][e] = h.v[e];
+                    const float m2 = em[j][e] * (2.0f - em[j][e]);
+                    h.v[e] += fmaf(-em[j][e], h.v[e], m2 * rs[j][e] * si[j][e] * x.v[e]);
+                }
+            }
+#pragma unroll
+            for (int j = kTok - 1; j >= 0; --j) {
+                if (events && (ev.ends >> j & 1)) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
+                const F2 g = pair_at(rows + j * kCh), dy = pair_at(rows + (kTok + j) * kCh), x = pair_at(rows + (2 * kTok + j) * kCh),
+                         i = pair_at(rows + (3 * kTok + j) * kCh);
+                F2 dx, dg, di;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float t = G.v[e] + dy.v[e], u = lam.v[e] * s[j][e], d = 1.0f - em[j][e], m2 = em[j][e] * (2.0f - em[j][e]);
+                    const float tm = t * (m2 * rs[j][e]), ix = si[j][e] * x.v[e];
+                    const float duu = t * (u * (ix * d * d * rs[j][e] - d * before[j][e]));
+                    acc.v[e] += j < left ? duu : 0.0f;
+                    dx.v[e] = tm * si[j][e];
+                    dg.v[e] = duu * (exp_minus(g.v[e]) * s[j][e]);
+                    di.v[e] = tm * ix * (exp_minus(i.v[e]) * si[j][e]);
+                    G.v[e] = fmaf(-em[j][e], t, t);
+                }
+                if (j < left) {
+                    store_pair<kVec>(static_cast<T*>(a.dx) + (t0 + j) * a.sdx, c, a.D, dx);
+                    store_pair<kVec>(static_cast<T*>(a.dg) + (t0 + j) * a.sdg, c, a.D, dg);
+                    store_pair<kVec>(static_cast<T*>(a.di) + (t0 + j) * a.sdi, c, a.D, di);
+                }
+                if (events && (ev.starts >> j & 1)) {
+                    const int n = ev.of(j);
+                    if (a.dh0) store_state<kVec>(a.dh0, n, c, a.D, G);
+                }
+            }
+            if constexpr (kStages == 1) {
+                __syncwarp();
+                if (step + 1 < steps) load(step + 1);
+                loads_done();
+            }
+        }
+    }
+    if constexpr (kTotal) {
+        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = total;
+    } else if (a.part) {
+        grid_launch_next();
+        // the block's share of dA_log: its warps in turn
+        __syncthreads();
+        F2* const sums = reinterpret_cast<F2*>(ahead);
+        sums[warp * 32 + lane] = acc;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v) {
+                acc.v[0] += sums[v * 32 + lane].v[0];
+                acc.v[1] += sums[v * 32 + lane].v[1];
+            }
+            store_state<kVec>(a.part, blockIdx.x, c, a.D, acc);
+        }
+    }
+}
+
+// dA_log from the blocks' shares, in their order: 32 columns by 8 threads
+__global__ void __launch_bounds__(256) rec_sum_kernel(const float* part, int parts, int64_t D, float* out) {
+    grid_wait_before();
+    __shared__ float sums[8][32];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
-    for (int64_t p = 0; p < parts; ++p) s += part[p * D + c];
-    out[c] = s;
+    if (c < D)
+        for (int p = threadIdx.y; p < parts; p += 8) s += part[p * D + c];
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < D) {
+        for (int v = 1; v < 8; ++v) s += sums[v][threadIdx.x];
+        out[c] = s;
+    }
 }
 
-template <typename T> __global__ void __launch_bounds__(256) rec_decode_kernel(const RecArgs a) {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= a.N * a.D) return;
-    const int64_t t = at / a.D, c = at % a.D;
-    const float em = one_minus_exp(expf(a.A_log[c]) * sigmoid2(get(static_cast<const T*>(a.g) + t * a.sg + c)).s);
-    const float b = sqrtf(em * (2.0f - em)) * sigmoid2(get(static_cast<const T*>(a.i) + t * a.si + c)).s *
-                    get(static_cast<const T*>(a.x) + t * a.sx + c);
-    float h = a.hT[at];
-    h += b - em * h;
-    a.hT[at] = h;
-    put(static_cast<T*>(a.y) + t * a.sy + c, h);
+// A token of every request: kVec 4 channels to a thread, else one.
+template <typename T, bool kVec> __global__ void __launch_bounds__(256) rec_decode_kernel(const RecArgs a) {
+    constexpr int V = kVec ? 4 : 1;
+    const int64_t units = a.D / V, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= a.N * units) return;
+    const int64_t t = at < (int64_t(1) << 32) ? (uint32_t)at / (uint32_t)units : at / units, c = (at - t * units) * V;
+    const T *x = static_cast<const T*>(a.x) + t * a.sx + c, *g = static_cast<const T*>(a.g) + t * a.sg + c,
+            *i = static_cast<const T*>(a.i) + t * a.si + c;
+    T* y = static_cast<T*>(a.y) + t * a.sy + c;
+    float* state = a.hT + t * a.D + c;
+    float xv[V], gv[V], iv[V], hv[V], lam[V];
+    if constexpr (kVec) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const F2 p = pair_at(x + 2 * k), q = pair_at(g + 2 * k), r = pair_at(i + 2 * k);
+            xv[2 * k] = p.v[0]; xv[2 * k + 1] = p.v[1];
+            gv[2 * k] = q.v[0]; gv[2 * k + 1] = q.v[1];
+            iv[2 * k] = r.v[0]; iv[2 * k + 1] = r.v[1];
+        }
+        const float4 h = *reinterpret_cast<const float4*>(state), A = *reinterpret_cast<const float4*>(a.A_log + c);
+        hv[0] = h.x; hv[1] = h.y; hv[2] = h.z; hv[3] = h.w;
+        lam[0] = A.x; lam[1] = A.y; lam[2] = A.z; lam[3] = A.w;
+    } else {
+        xv[0] = get(x); gv[0] = get(g); iv[0] = get(i); hv[0] = state[0]; lam[0] = a.A_log[c];
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const float em = one_minus_exp(expf(lam[k]) * sigmoid2(gv[k]).s), m2 = em * (2.0f - em);
+        hv[k] += fmaf(-em, hv[k], m2 * rsqrt_or_0(m2) * sigmoid2(iv[k]).s * xv[k]);
+    }
+    if constexpr (kVec) {
+        *reinterpret_cast<float4*>(state) = make_float4(hv[0], hv[1], hv[2], hv[3]);
+        put_pair(y, F2{hv[0], hv[1]});
+        put_pair(y + 2, F2{hv[2], hv[3]});
+    } else {
+        state[0] = hv[0];
+        put(y, hv[0]);
+    }
 }
 
 bool misaligned(const void* p, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
@@ -163,7 +645,7 @@ kda_status check_shape(const kda_recurrence_shape* sh, bool packed) {
     if (sh->dtype != KDA_BF16 && sh->dtype != KDA_FP32) return KDA_ERR_UNSUPPORTED;
     if (sh->B < 0 || sh->T < 0 || sh->N < 0 || sh->D <= 0 || sh->D > (1 << 20)) return KDA_ERR_SHAPE;
     if (packed ? sh->B != 1 : sh->N != sh->B) return KDA_ERR_SHAPE;
-    const int64_t most = (int64_t(1) << 31) - 1;
+    const int64_t most = (int64_t(1) << 31) - (1 << 16);     // a token's number and some chunks more are ints
     if (sh->B > most || sh->T > most || sh->N > most || (sh->T > 0 && sh->B > most / sh->T)) return KDA_ERR_SHAPE;
     if (sh->B * sh->T > 0 && sh->N == 0) return KDA_ERR_SHAPE;
     const int64_t strides[] = {sh->x_stride, sh->g_stride, sh->i_stride, sh->y_stride, sh->dx_stride, sh->dg_stride, sh->di_stride};
@@ -172,17 +654,119 @@ kda_status check_shape(const kda_recurrence_shape* sh, bool packed) {
     return KDA_OK;
 }
 
+// How the tokens are cut: clusters of `ranks` blocks for each tile of channels, each over one of `segs` segments.
+// Blocks of a cluster take chunks next to one another and exchange what they did over distributed shared memory,
+// one pass over the data; only where the channels are too few to fill the GPU with clusters of eight are there
+// segments, which read the inputs of a scan twice (once to find what each does to a state).
+struct Plan {
+    int tiles, chunks, ranks, segs, seg_chunks;
+};
+Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
+    Plan p;
+    const int64_t slots = (int64_t)kSMs * (backward || sh->dtype == KDA_FP32 ? 2 : 3);
+    p.tiles = (int)((sh->D + kCh - 1) / kCh);
+    p.chunks = (int)((sh->B * sh->T + kBlock - 1) / kBlock);
+    p.ranks = 1;
+    while (p.ranks < kMostRanks && 2 * p.ranks * p.tiles <= slots && 2 * p.ranks <= p.chunks) p.ranks *= 2;
+    const int steps = (p.chunks + p.ranks - 1) / p.ranks;
+    int64_t segs = slots / ((int64_t)p.tiles * p.ranks);
+    if (segs > steps / 4) segs = steps / 4;
+    if (segs > kMostSegs) segs = kMostSegs;
+    if (segs < 2) segs = 1;
+    p.seg_chunks = (int)((steps + segs - 1) / segs) * p.ranks;
+    p.segs = p.chunks ? (p.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
+    return p;
+}
+size_t seg_bytes(const Plan& p, int64_t D) {
+    return p.segs > 1 ? align_up((size_t)p.segs * ((D + 1) / 2) * sizeof(float4), 1024) : 0;
+}
 size_t bytes_of(const kda_recurrence_shape* sh, bool backward) {
-    return 1024 + (backward ? align_up((size_t)sh->N * sh->D * sizeof(float), 1024) : 0);
+    const size_t f = seg_bytes(plan_of(sh, false), sh->D);
+    if (!backward) return 1024 + f;
+    const Plan p = plan_of(sh, true);
+    const size_t b = seg_bytes(p, sh->D) + align_up((size_t)p.segs * p.ranks * sh->D * sizeof(float), 1024);
+    return 1024 + (f > b ? f : b);
 }
 
 RecArgs args_of(const kda_recurrence_shape* sh) {
     RecArgs a{};
     auto st = [&](int64_t s) { return s ? s : sh->D; };
-    a.total = sh->B * sh->T; a.T = sh->T; a.D = sh->D; a.N = sh->N;
+    a.total = (int)(sh->B * sh->T); a.T = (int)sh->T; a.D = sh->D; a.N = (int)sh->N;
     a.sx = st(sh->x_stride); a.sg = st(sh->g_stride); a.si = st(sh->i_stride); a.sy = st(sh->y_stride);
     a.sdx = st(sh->dx_stride); a.sdg = st(sh->dg_stride); a.sdi = st(sh->di_stride);
     return a;
+}
+
+// Token tensors in whole 16-byte units?
+bool whole_units(const kda_recurrence_shape* sh, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> strides) {
+    const int unit = sh->dtype == KDA_BF16 ? 8 : 4;
+    bool ok = sh->D % 8 == 0;
+    for (const void* p : ptrs) ok = ok && !misaligned(p);
+    for (const int64_t s : strides) ok = ok && s % unit == 0;
+    return ok;
+}
+
+using Kernel = void (*)(RecArgs);
+template <bool kBwd, typename T, bool kVec, bool kTotal> Kernel kernel_of() {
+    if constexpr (kBwd) return rec_bwd_kernel<T, kVec, kTotal>;
+    else return rec_fwd_kernel<T, kVec, kTotal>;
+}
+template <bool kBwd> Kernel pick(bool bf16, bool vec, bool total) {
+    if (bf16) return vec ? (total ? kernel_of<kBwd, uint16_t, true, true>() : kernel_of<kBwd, uint16_t, true, false>())
+                         : (total ? kernel_of<kBwd, uint16_t, false, true>() : kernel_of<kBwd, uint16_t, false, false>());
+    return vec ? (total ? kernel_of<kBwd, float, true, true>() : kernel_of<kBwd, float, true, false>())
+               : (total ? kernel_of<kBwd, float, false, true>() : kernel_of<kBwd, float, false, false>());
+}
+
+constexpr size_t smem_of(bool backward, size_t element, bool total) {
+    const size_t rows = (size_t)kWarps * kTok * kCh * element;
+    if (!backward) return sizeof(Shares) + 3 * rows;
+    return sizeof(Shares) + 2 * kWarps * 32 * sizeof(float4) + (total ? 2 : element == 2 ? 8 : 4) * rows;
+}
+
+// The kernels' limits on shared memory are set once for each device.
+kda_status allow_shared(const char* where) {
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return launched(where);
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return KDA_OK;
+    for (int k = 0; k < 16; ++k) {
+        const bool bwd = k & 1, bf16 = k & 2, vec = k & 4, total = k & 8;
+        const Kernel f = bwd ? pick<true>(bf16, vec, total) : pick<false>(bf16, vec, total);
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_of(bwd, bf16 ? 2 : 4, total)) != cudaSuccess)
+            return launched(where);
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return KDA_OK;
+}
+
+void launch_clusters(Kernel f, const Plan& p, int segs, size_t smem, cudaStream_t s, const RecArgs& a) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)p.ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(segs * p.ranks), (unsigned)p.tiles);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = p.ranks > 1 ? 1 : 0;
+    cudaLaunchKernelEx(&c, f, a);   // an error is left for cudaGetLastError
+}
+
+template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, bool vec, cudaStream_t s, const char* where) {
+    const kda_status st = allow_shared(where);
+    if (st != KDA_OK) return st;
+    const Plan p = plan_of(sh, kBwd);
+    const bool bf16 = sh->dtype == KDA_BF16;
+    a.chunks = p.chunks; a.seg_chunks = p.seg_chunks; a.ranks = p.ranks;
+    a.seg = reinterpret_cast<float4*>(a.ws + 1024);
+    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a);
+    launch_clusters(pick<kBwd>(bf16, vec, false), p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a);
+    return launched(where);
 }
 
 kda_status common_checks(const kda_recurrence_shape* sh, const int64_t* cu, const void* ws, size_t bytes, bool backward) {
@@ -214,16 +798,11 @@ extern "C" kda_status kda_recurrence_fwd(const kda_recurrence_shape* shape, cons
     for (const float* p : {A_log, h0, static_cast<const float*>(hT), static_cast<const float*>(kept)})
         if (misaligned(p)) return KDA_ERR_ALIGN;
     if (hT && hT == h0) return KDA_ERR_UNSUPPORTED;
-    if (shape->N == 0) return KDA_OK;
     RecArgs a = args_of(shape);
     a.x = x; a.g = g_raw; a.i = i_raw; a.y = y; a.A_log = A_log; a.h0 = h0; a.cu = cu_seqlens; a.hT = hT; a.kept = kept;
     a.ws = static_cast<uint8_t*>(workspace);
-    const int64_t blocks = (a.D + 127) / 128 * a.N;
-    if (blocks >= (int64_t(1) << 31)) return KDA_ERR_SHAPE;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (shape->dtype == KDA_BF16) rec_fwd_kernel<uint16_t><<<(unsigned)blocks, 128, 0, s>>>(a);
-    else rec_fwd_kernel<float><<<(unsigned)blocks, 128, 0, s>>>(a);
-    return launched("kda_recurrence_fwd launch");
+    const bool vec = whole_units(shape, {x, g_raw, i_raw, y}, {a.sx, a.sg, a.si, a.sy});
+    return run<false>(shape, a, vec, static_cast<cudaStream_t>(stream), "kda_recurrence_fwd launch");
 }
 
 extern "C" kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,
@@ -244,15 +823,15 @@ extern "C" kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, cons
     a.x = x; a.g = g_raw; a.i = i_raw; a.dy = dy; a.A_log = A_log; a.h0 = h0; a.dhT = dhT; a.cu = cu_seqlens;
     a.kept = const_cast<float*>(kept); a.dx = dx; a.dg = dg_raw; a.di = di_raw; a.dh0 = dh0;
     a.ws = static_cast<uint8_t*>(workspace);
-    a.part = reinterpret_cast<float*>(a.ws + 1024);
-    const int64_t blocks = (a.D + 127) / 128 * a.N;
-    if (blocks >= (int64_t(1) << 31)) return KDA_ERR_SHAPE;
+    const Plan p = plan_of(shape, true);
+    const int parts = p.segs * p.ranks;
+    float* const shares = reinterpret_cast<float*>(a.ws + 1024 + seg_bytes(p, a.D));
+    a.part = !dA_log || parts == 1 ? dA_log : shares;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (blocks > 0) {
-        if (shape->dtype == KDA_BF16) rec_bwd_kernel<uint16_t><<<(unsigned)blocks, 128, 0, s>>>(a);
-        else rec_bwd_kernel<float><<<(unsigned)blocks, 128, 0, s>>>(a);
-    }
-    if (dA_log) rec_sum_kernel<<<(unsigned)((a.D + 127) / 128), 128, 0, s>>>(a.part, a.N, a.D, dA_log);
+    const bool vec = whole_units(shape, {x, g_raw, i_raw, dy, dx, dg_raw, di_raw}, {a.sx, a.sg, a.si, a.sy, a.sdx, a.sdg, a.sdi});
+    const kda_status rs = run<true>(shape, a, vec, s, "kda_recurrence_bwd launch");
+    if (rs != KDA_OK || !dA_log || parts == 1) return rs;
+    launch_kernel(rec_sum_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(32, 8), 0, s, true, static_cast<const float*>(shares), parts, a.D, dA_log);
     return launched("kda_recurrence_bwd launch");
 }
 
@@ -269,10 +848,11 @@ extern "C" kda_status kda_recurrence_decode(const kda_recurrence_shape* shape, c
     if (misaligned(A_log) || misaligned(state)) return KDA_ERR_ALIGN;
     RecArgs a = args_of(shape);
     a.x = x; a.g = g_raw; a.i = i_raw; a.A_log = A_log; a.hT = state; a.y = y;
-    const int64_t blocks = (a.N * a.D + 255) / 256;
+    const bool vec = whole_units(shape, {x, g_raw, i_raw, y}, {a.sx, a.sg, a.si, a.sy});
+    const int64_t blocks = (a.N * (vec ? a.D / 4 : a.D) + 255) / 256;
     if (blocks >= (int64_t(1) << 31)) return KDA_ERR_SHAPE;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (shape->dtype == KDA_BF16) rec_decode_kernel<uint16_t><<<(unsigned)blocks, 256, 0, s>>>(a);
-    else rec_decode_kernel<float><<<(unsigned)blocks, 256, 0, s>>>(a);
+    const Kernel f = shape->dtype == KDA_BF16 ? (vec ? rec_decode_kernel<uint16_t, true> : rec_decode_kernel<uint16_t, false>)
+                                              : (vec ? rec_decode_kernel<float, true> : rec_decode_kernel<float, false>);
+    f<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return launched("kda_recurrence_decode launch");
 }
