@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdio>
 #include <initializer_list>
+#include <type_traits>
 #include "kda_internal.cuh"
 #include "umma_bf16.cuh"
 
@@ -42,29 +43,50 @@ __device__ __forceinline__ float inverse(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
-// sigmoid(x) and 1 - sigmoid(x), without cancellation at either end
-struct Sigmoid {
-    float s, c;
-};
-__device__ __forceinline__ float exp_minus(float x) { return exp2_of(fminf(-x * kLog2e, 126.0f)); }   // finite
-__device__ __forceinline__ Sigmoid sigmoid2(float x) {
-    const float e = exp_minus(x), s = inverse(1.0f + e);
-    return {s, e * s};
+__device__ __forceinline__ float root(float x) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-
-// 1 - exp(-u) for u >= 0: below 1/4 the series u - u^2/2 + u^3/6 .. u^6/720 (the next term is 5e-8 of the sum), above
-// it 1 - exp(-u), which loses two bits at most there
-__device__ __forceinline__ float one_minus_exp(float u) {
-    const float p = u * fmaf(u, fmaf(u, fmaf(u, fmaf(u, fmaf(u, -1.0f / 720, 1.0f / 120), -1.0f / 24), 1.0f / 6), -0.5f), 1.0f);
-    return u < 0.25f ? p : 1.0f - exp2_of(-u * kLog2e);
-}
-// 1 / sqrt(x), 0 at 0
-__device__ __forceinline__ float rsqrt_or_0(float x) {
+__device__ __forceinline__ float inverse_root(float x) {
     float r;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return x > 1.2e-38f ? r : 0.0f;
+    return r;
 }
+
+// exp(A_log), finite: times a closed gate it is 0
+__device__ __forceinline__ float rate(float A_log) {
+    const float r = expf(A_log);
+    return r > 2e38f ? 2e38f : r;
+}
+
+// Two channels at a time, in packed arithmetic where it exists
+__device__ __forceinline__ f32x2 both(float x) { return two(x, x); }
+__device__ __forceinline__ f32x2 exp2_of(f32x2 x) { const float2 p = parts(x); return two(exp2_of(p.x), exp2_of(p.y)); }
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
+    const float2 d = parts(add2(exp2_of(mul2(x, both(-kLog2e))), both(1.0f)));
+    return two(inverse(d.x), inverse(d.y));
+}
+// exp(-x), finite: times sigmoid(x) it is 1 - sigmoid(x) without cancellation
+__device__ __forceinline__ f32x2 exp_minus(f32x2 x) {
+    const float2 p = parts(mul2(x, both(-kLog2e)));
+    return two(exp2_of(fminf(p.x, 126.0f)), exp2_of(fminf(p.y, 126.0f)));
+}
+// exp(-u) - 1 for u >= 0, v = -u log2(e): below 1/4 the series -u + u^2/2 - u^3/6 .. + u^6/720 (the next term is 5e-8 of
+// the sum), above it exp(-u) - 1, which loses two bits at most there
+__device__ __forceinline__ f32x2 minus_decayed(f32x2 u, f32x2 v) {
+    f32x2 p = fma2(u, both(1.0f / 720), both(-1.0f / 120));
+    p = fma2(u, p, both(1.0f / 24));
+    p = fma2(u, p, both(-1.0f / 6));
+    p = fma2(u, p, both(0.5f));
+    p = mul2(u, fma2(u, p, both(-1.0f)));
+    const float2 small = parts(p), large = parts(add2(exp2_of(v), both(-1.0f))), at = parts(u);
+    return two(at.x < 0.25f ? small.x : large.x, at.y < 0.25f ? small.y : large.y);
+}
+// m^2 = (1 - a) (1 + a) of n = a - 1
+__device__ __forceinline__ f32x2 written2(f32x2 n) { return mul2(n, fma2(n, both(-1.0f), both(-2.0f))); }
+// h + n h + b: the sum of a step as a change of h, so that a's own rounding does not count
+__device__ __forceinline__ f32x2 advance(f32x2 h, f32x2 n, f32x2 b) { return add2(h, fma2(n, h, b)); }
 
 struct RecArgs {
     const void *x, *g, *i, *dy;
@@ -72,65 +94,58 @@ struct RecArgs {
     const int64_t* cu;
     void *y, *dx, *dg, *di;
     float *hT, *kept, *dh0, *part;
-    float4* seg;         // [segments][channel pairs] what each segment does to a state: a0, b0, a1, b1
+    float4* seg;         // [segments][channel pairs] what each segment does to a state
+    int* seg_fresh;      // [segments] whether a sequence starts (ends, backwards) in it
     uint8_t* ws;
     int64_t D, sx, sg, si, sy, sdx, sdg, sdi;
     int total, T, N, chunks, seg_chunks, ranks;
 };
 
 // ---------------------------------------------------------------- two channels of a lane
-struct F2 {
-    float v[2];
+// What a run of tokens does to a state that comes to it: a h + b. Where a sequence starts in it, which is the same for all
+// channels, b alone (not 0 h + b: a state that is no number ends with its sequence).
+struct Run {
+    f32x2 a, b;
 };
-// What a run of tokens does to a state that comes to it: a h + b; a < 0 where a sequence starts in it, which leaves b
-// whatever h is, also where that is no number.
-__device__ __forceinline__ float over(float a, float b, float h) { return a < 0.0f ? b : fmaf(a, h, b); }
-__device__ __forceinline__ void over2(const float4& s, F2& h) {
-    h.v[0] = over(s.x, s.y, h.v[0]);
-    h.v[1] = over(s.z, s.w, h.v[1]);
+__device__ __forceinline__ Run run_of(const float4& s) { return {two(s.x, s.y), two(s.z, s.w)}; }
+__device__ __forceinline__ float4 held(const Run& r) {
+    const float2 a = parts(r.a), b = parts(r.b);
+    return make_float4(a.x, a.y, b.x, b.y);
 }
-// first s, then t
-__device__ __forceinline__ float4 then(const float4& s, const float4& t) {
-    return make_float4(t.x < 0.0f || s.x < 0.0f ? -1.0f : t.x * s.x, over(t.x, t.y, s.y),
-                       t.z < 0.0f || s.z < 0.0f ? -1.0f : t.z * s.z, over(t.z, t.w, s.w));
-}
+__device__ __forceinline__ f32x2 over(const Run& r, bool fresh, f32x2 h) { return fresh ? r.b : fma2(r.a, h, r.b); }
+// first s, then t; `fresh` is t's
+__device__ __forceinline__ Run then(const Run& s, const Run& t, bool fresh) { return {fresh ? t.a : mul2(s.a, t.a), over(t, fresh, s.b)}; }
 
-template <typename T> __device__ __forceinline__ F2 pair_at(const T* p);
-template <> __device__ __forceinline__ F2 pair_at<uint16_t>(const uint16_t* p) {
+__device__ __forceinline__ f32x2 pair_at(const uint16_t* p) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+    return two(w << 16, w & 0xffff0000u);
 }
-template <> __device__ __forceinline__ F2 pair_at<float>(const float* p) {
-    const float2 w = *reinterpret_cast<const float2*>(p);
-    return {w.x, w.y};
-}
-__device__ __forceinline__ void put_pair(uint16_t* p, const F2& f) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f.v[0], f.v[1]);
+__device__ __forceinline__ f32x2 pair_at(const float* p) { return *reinterpret_cast<const f32x2*>(p); }
+__device__ __forceinline__ void put_pair(uint16_t* p, f32x2 f) {
+    const float2 v = parts(f);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     __stcs(reinterpret_cast<uint32_t*>(p), *reinterpret_cast<const uint32_t*>(&h));
 }
-__device__ __forceinline__ void put_pair(float* p, const F2& f) { __stcs(reinterpret_cast<float2*>(p), make_float2(f.v[0], f.v[1])); }
+__device__ __forceinline__ void put_pair(float* p, f32x2 f) { __stcs(reinterpret_cast<float2*>(p), parts(f)); }
 
-// The lane's channels c, c + 1 of a row, where they exist (kVec: rows and widths are whole 16-byte units)
-template <bool kVec, typename T> __device__ __forceinline__ void store_pair(T* row, int64_t c, int64_t D, const F2& f) {
+// The lane's channels c, c + 1 at p, where they exist (kVec: rows and widths are whole 16-byte units)
+template <bool kVec, typename T> __device__ __forceinline__ void store_pair(T* p, int64_t c, int64_t D, f32x2 f) {
     if constexpr (kVec) {
-        if (c < D) put_pair(row + c, f);
+        if (c < D) put_pair(p, f);
     } else {
-        if (c < D) put(row + c, f.v[0]);
-        if (c + 1 < D) put(row + c + 1, f.v[1]);
+        const float2 v = parts(f);
+        if (c < D) put(p, v.x);
+        if (c + 1 < D) put(p + 1, v.y);
     }
 }
-template <bool kVec> __device__ __forceinline__ F2 load_state(const float* p, int64_t row, int64_t c, int64_t D) {
-    if (!p) return {0.0f, 0.0f};
-    p += row * D;
-    if constexpr (kVec) {
-        if (c >= D) return {0.0f, 0.0f};
-        return pair_at(p + c);
-    } else {
-        return {c < D ? p[c] : 0.0f, c + 1 < D ? p[c + 1] : 0.0f};
-    }
+template <bool kVec> __device__ __forceinline__ f32x2 load_state(const float* p, int64_t row, int64_t c, int64_t D) {
+    if (!p || c >= D) return 0;
+    p += row * D + c;
+    if constexpr (kVec) return pair_at(p);
+    else return two(p[0], c + 1 < D ? p[1] : 0.0f);
 }
-template <bool kVec> __device__ __forceinline__ void store_state(float* p, int64_t row, int64_t c, int64_t D, const F2& f) {
-    store_pair<kVec>(p + row * D, c, D, f);
+template <bool kVec> __device__ __forceinline__ void store_state(float* p, int64_t row, int64_t c, int64_t D, f32x2 f) {
+    store_pair<kVec>(p + row * D + c, c, D, f);
 }
 
 // A warp's kTok rows of one token tensor into its own shared memory, [kTok][kCh], zeros outside the tensor
@@ -166,6 +181,9 @@ __device__ __forceinline__ void load_rows(T* dst, const void* src, int64_t strid
         }
     }
 }
+// Rows of the decay's gate that are no tokens: a closed gate, which decays and writes nothing.
+__device__ __forceinline__ void closed(uint16_t* p) { *reinterpret_cast<uint32_t*>(p) = 0xff80ff80u; }
+__device__ __forceinline__ void closed(float* p) { *reinterpret_cast<uint64_t*>(p) = 0xff800000ff800000ull; }
 __device__ __forceinline__ void loads_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft> __device__ __forceinline__ void loads_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
@@ -265,53 +283,88 @@ __device__ __forceinline__ void store_at_rank(float4* p, int rank, const float4&
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
+__device__ __forceinline__ void flag_at_rank(uint8_t* p, int rank, uint32_t v) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+}
+
 struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
-    float4 warp[2][kWarps][32];
-    float4 rank[2][kMostRanks][32];
+    float4 warp[2][8][32];
+    float4 rank[2][8][32];
+    uint8_t warp_fresh[2][8], rank_fresh[2][8];
 };
+static_assert(kWarps == 8 && kMostRanks == 8, "a flag for each in eight bytes");
+
+struct Ahead {           // what the warps' tokens do to a state, in the backward
+    float4 warp[2][8][32];
+    uint8_t fresh[2][8];
+};
+constexpr size_t kSharesBytes = (sizeof(Shares) + 127) / 128 * 128, kAheadBytes = (sizeof(Ahead) + 127) / 128 * 128;
+
+// h through the runs from `from` to `to`
+__device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint64_t fresh, int from, int to, f32x2 h) {
+    const int lane = threadIdx.x & 31;
+    if (fresh == 0) {
+#pragma unroll 2
+        for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), false, h);
+    } else {
+        for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), (fresh >> (8 * k) & 1) != 0, h);
+    }
+    return h;
+}
 
 // After a step's own sums: the state (adjoint) that comes to this warp, and in `carry` the one that leaves the step.
-// Warps and ranks follow one another in the order of the scan, `w` and `r` their places in it.
+// Warps and ranks follow one another in the order of the scan, `w` and `r` their places in it. kTotal: only what all
+// the steps so far do, in `total`.
 template <bool kTotal>
-__device__ __forceinline__ F2 exchange(Shares& sh, int parity, int ranks, int r, int w, const float4& own, F2& carry, float4& total) {
+__device__ __forceinline__ f32x2 exchange(Shares& sh, int parity, int ranks, int r, int w, const Run& own, bool fresh, f32x2& carry,
+                                          Run& total, bool& total_fresh) {
     const int lane = threadIdx.x & 31;
-    sh.warp[parity][w][lane] = own;
+    sh.warp[parity][w][lane] = held(own);
+    if (lane == 0) sh.warp_fresh[parity][w] = fresh;
     __syncthreads();
-    F2 at = carry;
+    const uint64_t warps = *reinterpret_cast<const uint64_t*>(sh.warp_fresh[parity]);
     if (ranks > 1) {
         if (w == 0) {
-            float4 s = sh.warp[parity][0][lane];
+            Run s = own;
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) s = then(s, sh.warp[parity][v][lane]);
-            for (int k = 0; k < ranks; ++k) store_at_rank(&sh.rank[parity][r][lane], k, s);
+            for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), (warps >> (8 * v) & 1) != 0);
+            const float4 f = held(s);
+            for (int k = 0; k < ranks; ++k) store_at_rank(&sh.rank[parity][r][lane], k, f);
+            if (lane < ranks) flag_at_rank(&sh.rank_fresh[parity][r], lane, warps != 0);
         }
         cluster_arrive();
         cluster_wait();
-        for (int k = 0; k < ranks; ++k) {
-            if (k == r) at = carry;
-            const float4 s = sh.rank[parity][k][lane];
-            if constexpr (kTotal) total = then(total, s);
-            else over2(s, carry);
-        }
-        if constexpr (!kTotal)
-            for (int v = 0; v < w; ++v) over2(sh.warp[parity][v][lane], at);
-    } else {
-#pragma unroll
-        for (int v = 0; v < kWarps; ++v) {
-            if (v == w) at = carry;
-            if constexpr (kTotal) total = then(total, sh.warp[parity][v][lane]);
-            else over2(sh.warp[parity][v][lane], carry);
-        }
     }
+    if constexpr (kTotal) {
+        const uint64_t all = ranks > 1 ? *reinterpret_cast<const uint64_t*>(sh.rank_fresh[parity]) : warps;
+        const int count = ranks > 1 ? ranks : kWarps;
+        for (int k = 0; k < count; ++k) {
+            const bool f = (all >> (8 * k) & 1) != 0;
+            total = then(total, run_of((ranks > 1 ? sh.rank : sh.warp)[parity][k][lane]), f);
+            total_fresh = total_fresh || f;
+        }
+        return 0;
+    }
+    if (ranks > 1) {
+        uint64_t all = *reinterpret_cast<const uint64_t*>(sh.rank_fresh[parity]);
+        if (ranks < 8) all &= (uint64_t(1) << (8 * ranks)) - 1;
+        const f32x2 block = through(sh.rank[parity], all, 0, r, carry);
+        carry = through(sh.rank[parity], all, r, ranks, block);
+        return through(sh.warp[parity], warps, 0, w, block);
+    }
+    const f32x2 at = through(sh.warp[parity], warps, 0, w, carry);
+    carry = through(sh.warp[parity], warps, w, kWarps, at);
     return at;
 }
 
 // The state that comes to segment `seg`, in the order of the scan, from what those before it did
-__device__ __forceinline__ F2 into_segment(const RecArgs& a, int seg, int64_t c) {
-    F2 h{0.0f, 0.0f};
+__device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t c) {
+    f32x2 h = 0;
     const int64_t pairs = (a.D + 1) / 2;
     if (c < a.D)
-        for (int s = 0; s < seg; ++s) over2(a.seg[s * pairs + c / 2], h);
+        for (int s = 0; s < seg; ++s) h = over(run_of(a.seg[s * pairs + c / 2]), a.seg_fresh[s] != 0, h);
     return h;
 }
 
@@ -322,7 +375,8 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
     extern __shared__ __align__(16) uint8_t smem[];
     Shares& sh = *reinterpret_cast<Shares*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* const rows = reinterpret_cast<T*>(smem + sizeof(Shares)) + warp * (3 * kTok * kCh);
+    T* const rows = reinterpret_cast<T*>(smem + kSharesBytes) + warp * (3 * kTok * kCh);
+    T *const mine = rows + 2 * lane, *const xs = mine, *const gs = mine + kTok * kCh, *const is = mine + 2 * kTok * kCh;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);
@@ -337,11 +391,10 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
     load(0);
     loads_done();
     if (a.ranks > 1) cluster_arrive();
-    F2 lam;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) lam.v[e] = c + e < a.D ? expf(a.A_log[c + e]) : 0.0f;
-    F2 carry = kTotal ? F2{0.0f, 0.0f} : into_segment(a, seg, c);
-    float4 total = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    const f32x2 lam = two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), lam2 = mul2(lam, both(-kLog2e));
+    f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
+    Run total{both(1.0f), 0};
+    bool total_fresh = false;
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
         pass_empty<kVec>(a, a.hT, a.h0, c);
@@ -352,70 +405,74 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
         const int chunk = first + step * a.ranks + r;
         const bool some = chunk < last;
         const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;   // tokens of the warp
-        const bool events = some && ev.find(a, t0);
+        const bool events = ev.find(a, some ? t0 : a.total);
         loads_wait<0>();
         __syncwarp();
-        float em[kTok][2], b[kTok][2];
-        F2 h{0.0f, 0.0f}, sum{0.0f, 0.0f};
-        bool fresh = false;
+        for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
+        f32x2 n[kTok], b[kTok], h = 0, sum = 0;
+        auto gates = [&](auto with) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            const F2 x = pair_at(rows + j * kCh + 2 * lane), g = pair_at(rows + (kTok + j) * kCh + 2 * lane),
-                     i = pair_at(rows + (2 * kTok + j) * kCh + 2 * lane);
-            if (events && (ev.starts >> j & 1)) {
-                h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                fresh = true;
+            for (int j = 0; j < kTok; ++j) {
+                const f32x2 s = sigmoid2(pair_at(gs + j * kCh)), v = mul2(lam2, s);
+                n[j] = minus_decayed(mul2(lam, s), v);
+                const float2 m2 = parts(written2(n[j]));
+                b[j] = mul2(mul2(two(root(m2.x), root(m2.y)), sigmoid2(pair_at(is + j * kCh))), pair_at(xs + j * kCh));
+                if constexpr (with.value)
+                    if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                h = advance(h, n[j], b[j]);
+                sum = add2(sum, v);
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float u = j < left ? lam.v[e] * sigmoid2(g.v[e]).s : 0.0f;
-                em[j][e] = one_minus_exp(u);
-                const float m2 = em[j][e] * (2.0f - em[j][e]);
-                b[j][e] = m2 * rsqrt_or_0(m2) * sigmoid2(i.v[e]).s * x.v[e];
-                h.v[e] += fmaf(-em[j][e], h.v[e], b[j][e]);
-                sum.v[e] += u;
-            }
-        }
+        };
+        if (events) gates(std::true_type());
+        else gates(std::false_type());
         __syncwarp();
         if (step + 1 < steps) load(step + 1);
         loads_done();
-        const float4 own = make_float4(fresh ? -1.0f : exp2_of(-sum.v[0] * kLog2e), h.v[0], fresh ? -1.0f : exp2_of(-sum.v[1] * kLog2e), h.v[1]);
-        h = exchange<kTotal>(sh, step & 1, a.ranks, r, warp, own, carry, total);
+        h = exchange<kTotal>(sh, step & 1, a.ranks, r, warp, Run{exp2_of(sum), h}, events && ev.starts, carry, total, total_fresh);
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
-            T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.sy;
+            T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.sy + c;
+            if (!events && left == kTok) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                if (events && (ev.starts >> j & 1)) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                for (int j = 0; j < kTok; ++j, y += a.sy) {
+                    h = advance(h, n[j], b[j]);
+                    store_pair<kVec>(y, c, a.D, h);
+                }
+            } else {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) h.v[e] += fmaf(-em[j][e], h.v[e], b[j][e]);
-                if (j < left) store_pair<kVec>(y + j * a.sy, c, a.D, h);
-                if (events && (ev.ends >> j & 1)) {
-                    const int n = ev.of(j);
-                    if (a.hT) store_state<kVec>(a.hT, n, c, a.D, h);
+                for (int j = 0; j < kTok; ++j, y += a.sy) {
+                    if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                    h = advance(h, n[j], b[j]);
+                    if (j < left) store_pair<kVec>(y, c, a.D, h);
+                    if (ev.ends >> j & 1) {
+                        const int q = ev.of(j);
+                        if (a.hT) store_state<kVec>(a.hT, q, c, a.D, h);
+                    }
                 }
             }
         }
     }
-    if constexpr (kTotal)
-        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = total;
+    if constexpr (kTotal) {
+        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
+        if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
+    }
 }
 
 // The same grid, tokens from the last to the first: chunks, ranks and warps in that order.
 template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const RecArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shares& sh = *reinterpret_cast<Shares*>(smem);
-    float4 (*const ahead)[32] = reinterpret_cast<float4 (*)[32]>(smem + sizeof(Shares));     // [2 kWarps][32] the states' way forwards
-    constexpr int kTensors = kTotal ? 2 : 4, kStages = sizeof(T) == 2 && !kTotal ? 2 : 1;
+    Ahead& ahead = *reinterpret_cast<Ahead*>(smem + kSharesBytes);      // the states' way, forwards
+    constexpr int kTensors = kTotal ? 2 : 4, kStages = sizeof(T) == 2 && !kTotal ? 2 : 1, kStage = kTensors * kTok * kCh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* const base = reinterpret_cast<T*>(smem + sizeof(Shares) + 2 * kWarps * 32 * sizeof(float4)) + warp * (kStages * kTensors * kTok * kCh);
+    T* const base = reinterpret_cast<T*>(smem + kSharesBytes + kAheadBytes) + warp * (kStages * kStage);
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);   // counted from the last chunk
     const int steps = (last - first + a.ranks - 1) / a.ranks;
     auto load = [&](int step) {
         const int at = first + step * a.ranks + r;
-        T* const rows = base + (kStages == 2 ? (step & 1) * kTensors * kTok * kCh : 0);
+        T* const rows = base + (kStages == 2 ? (step & 1) * kStage : 0);
         const int t0 = at < last ? (a.chunks - 1 - at) * kBlock + warp * kTok : a.total;
         load_rows<kVec>(rows, a.g, a.sg, t0, a.total, c0, a.D);
         load_rows<kVec>(rows + kTok * kCh, a.dy, a.sy, t0, a.total, c0, a.D);
@@ -427,24 +484,24 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
     load(0);
     loads_done();
     if (a.ranks > 1) cluster_arrive();
-    F2 lam;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) lam.v[e] = c + e < a.D ? expf(a.A_log[c + e]) : 0.0f;
-    F2 carry = kTotal ? F2{0.0f, 0.0f} : into_segment(a, seg, c);
-    float4 total = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    const f32x2 lam = two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), lam2 = mul2(lam, both(-kLog2e));
+    f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
+    Run total{both(1.0f), 0};
+    bool total_fresh = false;
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
         pass_empty<kVec>(a, a.dh0, a.dhT, c);
     }
     if (a.ranks > 1) cluster_wait();
     Events ev;
-    F2 acc{0.0f, 0.0f};
+    f32x2 acc = 0;
     for (int step = 0; step < steps; ++step) {
         const int at = first + step * a.ranks + r, chunk = a.chunks - 1 - at;
         const bool some = at < last;
         const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;
-        const bool events = some && ev.find(a, t0);
-        T* const rows = base + (kStages == 2 ? (step & 1) * kTensors * kTok * kCh : 0) + 2 * lane;
+        const bool events = ev.find(a, some ? t0 : a.total);
+        T *const gs = base + (kStages == 2 ? (step & 1) * kStage : 0) + 2 * lane, *const dys = gs + kTok * kCh, *const xs = gs + 2 * kTok * kCh,
+                 *const is = gs + 3 * kTok * kCh;
         if constexpr (kStages == 2) {
             __syncwarp();          // the last lane's reads of the step before last
             if (step + 1 < steps) load(step + 1);
@@ -454,98 +511,83 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
             loads_wait<0>();
         }
         __syncwarp();
-        float s[kTok][2], em[kTok][2], si[kTok][2], rs[kTok][2];
-        F2 h{0.0f, 0.0f}, sum{0.0f, 0.0f}, G{0.0f, 0.0f};
-        bool fresh = false, ended = false;
+        for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
+        f32x2 s[kTok], n[kTok], si[kTok], rs[kTok], h = 0, sum = 0, G = 0;
+        auto sums = [&](auto with) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            const F2 g = pair_at(rows + j * kCh);
-            F2 x{0.0f, 0.0f}, i{0.0f, 0.0f};
-            if constexpr (!kTotal) {
-                x = pair_at(rows + (2 * kTok + j) * kCh);
-                i = pair_at(rows + (3 * kTok + j) * kCh);
-                if (events && (ev.starts >> j & 1)) {
-                    h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                    fresh = true;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                s[j][e] = j < left ? sigmoid2(g.v[e]).s : 0.0f;
-                const float u = lam.v[e] * s[j][e];
-                em[j][e] = one_minus_exp(u);
-                sum.v[e] += u;
+            for (int j = 0; j < kTok; ++j) {
+                s[j] = sigmoid2(pair_at(gs + j * kCh));
+                const f32x2 v = mul2(lam2, s[j]);
+                n[j] = minus_decayed(mul2(lam, s[j]), v);
+                sum = add2(sum, v);
                 if constexpr (!kTotal) {
-                    const float m2 = em[j][e] * (2.0f - em[j][e]);
-                    rs[j][e] = rsqrt_or_0(m2);
-                    si[j][e] = sigmoid2(i.v[e]).s;
-                    h.v[e] += fmaf(-em[j][e], h.v[e], m2 * rs[j][e] * si[j][e] * x.v[e]);
+                    const f32x2 m2 = written2(n[j]);
+                    const float2 p = parts(add2(m2, both(0x1p-125f)));      // no infinity at 0
+                    rs[j] = two(inverse_root(p.x), inverse_root(p.y));
+                    si[j] = sigmoid2(pair_at(is + j * kCh));
+                    if constexpr (with.value)
+                        if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                    h = advance(h, n[j], mul2(mul2(m2, rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
                 }
             }
-        }
 #pragma unroll
-        for (int j = kTok - 1; j >= 0; --j) {
-            if (events && (ev.ends >> j & 1)) {
-                G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
-                ended = true;
+            for (int j = kTok - 1; j >= 0; --j) {
+                if constexpr (with.value)
+                    if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
+                const f32x2 t = add2(G, pair_at(dys + j * kCh));
+                G = fma2(n[j], t, t);
             }
-            const F2 dy = pair_at(rows + (kTok + j) * kCh);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float t = G.v[e] + dy.v[e];
-                G.v[e] = fmaf(-em[j][e], t, t);
-            }
+        };
+        if (events) sums(std::true_type());
+        else sums(std::false_type());
+        const f32x2 decay = exp2_of(sum);
+        if constexpr (!kTotal) {
+            ahead.warp[step & 1][warp][lane] = held(Run{decay, h});
+            if (lane == 0) ahead.fresh[step & 1][warp] = events && ev.starts;
+            h = some ? load_state<kVec>(a.kept, chunk, c, a.D) : 0;
         }
-        const float a0 = exp2_of(-sum.v[0] * kLog2e), a1 = exp2_of(-sum.v[1] * kLog2e);
-        if constexpr (!kTotal) ahead[(step & 1) * kWarps + warp][lane] = make_float4(fresh ? -1.0f : a0, h.v[0], fresh ? -1.0f : a1, h.v[1]);
-        const float4 own = make_float4(ended ? -1.0f : a0, G.v[0], ended ? -1.0f : a1, G.v[1]);
-        if constexpr (!kTotal) h = some ? load_state<kVec>(a.kept, chunk, c, a.D) : F2{0.0f, 0.0f};
-        G = exchange<kTotal>(sh, step & 1, a.ranks, r, kWarps - 1 - warp, own, carry, total);
+        G = exchange<kTotal>(sh, step & 1, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends, carry, total, total_fresh);
         if constexpr (kTotal) {
             __syncwarp();
             if (step + 1 < steps) load(step + 1);
             loads_done();
         } else {
-            for (int v = 0; v < warp; ++v) over2(ahead[(step & 1) * kWarps + v][lane], h);
-            float before[kTok][2];
+            h = through(ahead.warp[step & 1], *reinterpret_cast<const uint64_t*>(ahead.fresh[step & 1]), 0, warp, h);
+            f32x2 before[kTok];
+            T *dx = static_cast<T*>(a.dx) + (int64_t)(t0 + kTok - 1) * a.sdx + c, *dg = static_cast<T*>(a.dg) + (int64_t)(t0 + kTok - 1) * a.sdg + c,
+              *di = static_cast<T*>(a.di) + (int64_t)(t0 + kTok - 1) * a.sdi + c;
+            auto grads = [&](auto with) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                if (events && (ev.starts >> j & 1)) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                const F2 x = pair_at(rows + (2 * kTok + j) * kCh);
+                for (int j = 0; j < kTok; ++j) {
+                    if constexpr (with.value)
+                        if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                    before[j] = h;
+                    h = advance(h, n[j], mul2(mul2(written2(n[j]), rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
+                }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    before[j][e] = h.v[e];
-                    const float m2 = em[j][e] * (2.0f - em[j][e]);
-                    h.v[e] += fmaf(-em[j][e], h.v[e], m2 * rs[j][e] * si[j][e] * x.v[e]);
+                for (int j = kTok - 1; j >= 0; --j, dx -= a.sdx, dg -= a.sdg, di -= a.sdi) {
+                    if constexpr (with.value)
+                        if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
+                    const f32x2 t = add2(G, pair_at(dys + j * kCh)), ix = mul2(si[j], pair_at(xs + j * kCh)), d = add2(n[j], both(1.0f));
+                    const f32x2 tm = mul2(t, mul2(written2(n[j]), rs[j]));
+                    const f32x2 q = fma2(before[j], both(-1.0f), mul2(mul2(rs[j], ix), d));       // over d: m' - h
+                    const f32x2 duu = mul2(mul2(t, mul2(lam, s[j])), mul2(d, q));
+                    acc = add2(acc, duu);
+                    G = fma2(n[j], t, t);
+                    if (!with.value || j < left) {
+                        store_pair<kVec>(dx, c, a.D, mul2(tm, si[j]));
+                        store_pair<kVec>(dg, c, a.D, mul2(duu, mul2(exp_minus(pair_at(gs + j * kCh)), s[j])));
+                        store_pair<kVec>(di, c, a.D, mul2(mul2(tm, ix), mul2(exp_minus(pair_at(is + j * kCh)), si[j])));
+                    }
+                    if constexpr (with.value)
+                        if (ev.starts >> j & 1) {
+                            const int q0 = ev.of(j);
+                            if (a.dh0) store_state<kVec>(a.dh0, q0, c, a.D, G);
+                        }
                 }
-            }
-#pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if (events && (ev.ends >> j & 1)) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
-                const F2 g = pair_at(rows + j * kCh), dy = pair_at(rows + (kTok + j) * kCh), x = pair_at(rows + (2 * kTok + j) * kCh),
-                         i = pair_at(rows + (3 * kTok + j) * kCh);
-                F2 dx, dg, di;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float t = G.v[e] + dy.v[e], u = lam.v[e] * s[j][e], d = 1.0f - em[j][e], m2 = em[j][e] * (2.0f - em[j][e]);
-                    const float tm = t * (m2 * rs[j][e]), ix = si[j][e] * x.v[e];
-                    const float duu = t * (u * (ix * d * d * rs[j][e] - d * before[j][e]));
-                    acc.v[e] += j < left ? duu : 0.0f;
-                    dx.v[e] = tm * si[j][e];
-                    dg.v[e] = duu * (exp_minus(g.v[e]) * s[j][e]);
-                    di.v[e] = tm * ix * (exp_minus(i.v[e]) * si[j][e]);
-                    G.v[e] = fmaf(-em[j][e], t, t);
-                }
-                if (j < left) {
-                    store_pair<kVec>(static_cast<T*>(a.dx) + (t0 + j) * a.sdx, c, a.D, dx);
-                    store_pair<kVec>(static_cast<T*>(a.dg) + (t0 + j) * a.sdg, c, a.D, dg);
-                    store_pair<kVec>(static_cast<T*>(a.di) + (t0 + j) * a.sdi, c, a.D, di);
-                }
-                if (events && (ev.starts >> j & 1)) {
-                    const int n = ev.of(j);
-                    if (a.dh0) store_state<kVec>(a.dh0, n, c, a.D, G);
-                }
-            }
+            };
+            if (events || left < kTok) grads(std::true_type());
+            else grads(std::false_type());
             if constexpr (kStages == 1) {
                 __syncwarp();
                 if (step + 1 < steps) load(step + 1);
@@ -554,20 +596,18 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
         }
     }
     if constexpr (kTotal) {
-        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = total;
+        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
+        if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
     } else if (a.part) {
         grid_launch_next();
         // the block's share of dA_log: its warps in turn
         __syncthreads();
-        F2* const sums = reinterpret_cast<F2*>(ahead);
-        sums[warp * 32 + lane] = acc;
+        f32x2* const shares = reinterpret_cast<f32x2*>(&ahead);
+        shares[warp * 32 + lane] = acc;
         __syncthreads();
         if (warp == 0) {
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) {
-                acc.v[0] += sums[v * 32 + lane].v[0];
-                acc.v[1] += sums[v * 32 + lane].v[1];
-            }
+            for (int v = 1; v < kWarps; ++v) acc = add2(acc, shares[v * 32 + lane]);
             store_state<kVec>(a.part, blockIdx.x, c, a.D, acc);
         }
     }
@@ -599,33 +639,22 @@ template <typename T, bool kVec> __global__ void __launch_bounds__(256) rec_deco
             *i = static_cast<const T*>(a.i) + t * a.si + c;
     T* y = static_cast<T*>(a.y) + t * a.sy + c;
     float* state = a.hT + t * a.D + c;
-    float xv[V], gv[V], iv[V], hv[V], lam[V];
+    auto step = [](f32x2 h, f32x2 x, f32x2 g, f32x2 i, f32x2 lam) {
+        const f32x2 s = sigmoid2(g), n = minus_decayed(mul2(lam, s), mul2(mul2(lam, both(-kLog2e)), s));
+        const float2 m2 = parts(written2(n));
+        return advance(h, n, mul2(mul2(two(root(m2.x), root(m2.y)), sigmoid2(i)), x));
+    };
     if constexpr (kVec) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const F2 p = pair_at(x + 2 * k), q = pair_at(g + 2 * k), r = pair_at(i + 2 * k);
-            xv[2 * k] = p.v[0]; xv[2 * k + 1] = p.v[1];
-            gv[2 * k] = q.v[0]; gv[2 * k + 1] = q.v[1];
-            iv[2 * k] = r.v[0]; iv[2 * k + 1] = r.v[1];
-        }
         const float4 h = *reinterpret_cast<const float4*>(state), A = *reinterpret_cast<const float4*>(a.A_log + c);
-        hv[0] = h.x; hv[1] = h.y; hv[2] = h.z; hv[3] = h.w;
-        lam[0] = A.x; lam[1] = A.y; lam[2] = A.z; lam[3] = A.w;
+        const f32x2 lo = step(two(h.x, h.y), pair_at(x), pair_at(g), pair_at(i), two(rate(A.x), rate(A.y)));
+        const f32x2 hi = step(two(h.z, h.w), pair_at(x + 2), pair_at(g + 2), pair_at(i + 2), two(rate(A.z), rate(A.w)));
+        *reinterpret_cast<float4*>(state) = held(Run{lo, hi});
+        put_pair(y, lo);
+        put_pair(y + 2, hi);
     } else {
-        xv[0] = get(x); gv[0] = get(g); iv[0] = get(i); hv[0] = state[0]; lam[0] = a.A_log[c];
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const float em = one_minus_exp(expf(lam[k]) * sigmoid2(gv[k]).s), m2 = em * (2.0f - em);
-        hv[k] += fmaf(-em, hv[k], m2 * rsqrt_or_0(m2) * sigmoid2(iv[k]).s * xv[k]);
-    }
-    if constexpr (kVec) {
-        *reinterpret_cast<float4*>(state) = make_float4(hv[0], hv[1], hv[2], hv[3]);
-        put_pair(y, F2{hv[0], hv[1]});
-        put_pair(y + 2, F2{hv[2], hv[3]});
-    } else {
-        state[0] = hv[0];
-        put(y, hv[0]);
+        const float2 h = parts(step(two(state[0], 0.0f), two(get(x), 0.0f), two(get(g), 0.0f), two(get(i), 0.0f), two(rate(a.A_log[c]), 0.0f)));
+        state[0] = h.x;
+        put(y, h.x);
     }
 }
 
@@ -720,8 +749,8 @@ template <bool kBwd> Kernel pick(bool bf16, bool vec, bool total) {
 
 constexpr size_t smem_of(bool backward, size_t element, bool total) {
     const size_t rows = (size_t)kWarps * kTok * kCh * element;
-    if (!backward) return sizeof(Shares) + 3 * rows;
-    return sizeof(Shares) + 2 * kWarps * 32 * sizeof(float4) + (total ? 2 : element == 2 ? 8 : 4) * rows;
+    if (!backward) return kSharesBytes + 3 * rows;
+    return kSharesBytes + kAheadBytes + (total ? 2 : element == 2 ? 8 : 4) * rows;
 }
 
 // The kernels' limits on shared memory are set once for each device.
@@ -764,6 +793,7 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
     const bool bf16 = sh->dtype == KDA_BF16;
     a.chunks = p.chunks; a.seg_chunks = p.seg_chunks; a.ranks = p.ranks;
     a.seg = reinterpret_cast<float4*>(a.ws + 1024);
+    a.seg_fresh = reinterpret_cast<int*>(a.ws + 64);       // kMostSegs of them
     if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a);
     launch_clusters(pick<kBwd>(bf16, vec, false), p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a);
     return launched(where);
