@@ -9,6 +9,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <cuda.h>
 #include <initializer_list>
 #include <type_traits>
 #include "kda_internal.cuh"
@@ -72,16 +73,15 @@ __device__ __forceinline__ f32x2 exp_minus(f32x2 x) {
     const float2 p = parts(mul2(x, both(-kLog2e)));
     return two(exp2_of(fminf(p.x, 126.0f)), exp2_of(fminf(p.y, 126.0f)));
 }
-// exp(-u) - 1 for u >= 0, v = -u log2(e): below 1/4 the series -u + u^2/2 - u^3/6 .. + u^6/720 (the next term is 5e-8 of
-// the sum), above it exp(-u) - 1, which loses two bits at most there
-__device__ __forceinline__ f32x2 minus_decayed(f32x2 u, f32x2 v) {
-    f32x2 p = fma2(u, both(1.0f / 720), both(-1.0f / 120));
-    p = fma2(u, p, both(1.0f / 24));
-    p = fma2(u, p, both(-1.0f / 6));
-    p = fma2(u, p, both(0.5f));
-    p = mul2(u, fma2(u, p, both(-1.0f)));
-    const float2 small = parts(p), large = parts(add2(exp2_of(v), both(-1.0f))), at = parts(u);
-    return two(at.x < 0.25f ? small.x : large.x, at.y < 0.25f ? small.y : large.y);
+// 2^v - 1 for v <= 0: from -1/2 on v times the polynomial of degree 4 with the least relative error there (1.3e-8, by
+// Remez exchange), below it 2^v - 1, which loses two bits at most
+__device__ __forceinline__ f32x2 minus_decayed(f32x2 v) {
+    f32x2 p = fma2(v, both(0.00115445226866f), both(0.00954128107951f));
+    p = fma2(v, p, both(0.0554904064448f));
+    p = fma2(v, p, both(0.240225642792f));
+    p = mul2(v, fma2(v, p, both(0.693147171737f)));
+    const float2 small = parts(p), large = parts(add2(exp2_of(v), both(-1.0f))), at = parts(v);
+    return two(at.x > -0.5f ? small.x : large.x, at.y > -0.5f ? small.y : large.y);
 }
 // m^2 = (1 - a) (1 + a) of n = a - 1
 __device__ __forceinline__ f32x2 written2(f32x2 n) { return mul2(n, fma2(n, both(-1.0f), both(-2.0f))); }
@@ -148,44 +148,51 @@ template <bool kVec> __device__ __forceinline__ void store_state(float* p, int64
     store_pair<kVec>(p + row * D + c, c, D, f);
 }
 
-// A warp's kTok rows of one token tensor into its own shared memory, [kTok][kCh], zeros outside the tensor
-template <bool kVec, typename T>
-__device__ __forceinline__ void load_rows(T* dst, const void* src, int64_t stride, int t0, int total, int64_t c0, int64_t D) {
-    const int lane = threadIdx.x & 31;
-    const T* const from = static_cast<const T*>(src);
-    if constexpr (kVec) {
-        constexpr int V = 16 / sizeof(T), units = kCh / V, rows = 32 / units;
-        const int u = lane % units;
+// The lane's channels of a warp's kTok rows of one token tensor, to rows of kCh in shared memory; zeros outside the tensor
+template <typename T>
+__device__ __forceinline__ void load_own(T* dst, const void* src, int64_t stride, int t0, int left, int64_t c, int64_t D) {
+    const T* p = static_cast<const T*>(src) + (int64_t)t0 * stride + c;
+    T a[kTok], b[kTok];
 #pragma unroll
-        for (int j = 0; j < kTok / rows; ++j) {
-            const int r = j * rows + lane / units;
-            const bool in = t0 + r < total && c0 + u * V < D;
-            const T* p = from + (in ? (int64_t)(t0 + r) * stride + c0 + u * V : 0);
-            const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * kCh + u * V);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(in ? 16 : 0) : "memory");
-        }
-    } else {
-        const int64_t c = c0 + 2 * lane;
-        T a[kTok], b[kTok];
+    for (int r = 0; r < kTok; ++r, p += stride) {
+        a[r] = r < left && c < D ? p[0] : T(0);
+        b[r] = r < left && c + 1 < D ? p[1] : T(0);
+    }
 #pragma unroll
-        for (int r = 0; r < kTok; ++r) {
-            const bool in = t0 + r < total;
-            const T* p = from + (int64_t)(t0 + r) * stride + c;
-            a[r] = in && c < D ? p[0] : T(0);
-            b[r] = in && c + 1 < D ? p[1] : T(0);
-        }
-#pragma unroll
-        for (int r = 0; r < kTok; ++r) {
-            dst[r * kCh + 2 * lane] = a[r];
-            dst[r * kCh + 2 * lane + 1] = b[r];
-        }
+    for (int r = 0; r < kTok; ++r) {
+        dst[r * kCh] = a[r];
+        dst[r * kCh + 1] = b[r];
     }
 }
 // Rows of the decay's gate that are no tokens: a closed gate, which decays and writes nothing.
 __device__ __forceinline__ void closed(uint16_t* p) { *reinterpret_cast<uint32_t*>(p) = 0xff80ff80u; }
 __device__ __forceinline__ void closed(float* p) { *reinterpret_cast<uint64_t*>(p) = 0xff800000ff800000ull; }
-__device__ __forceinline__ void loads_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft> __device__ __forceinline__ void loads_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+template <typename T> __device__ __forceinline__ void close_rows(T* gs, int left) {
+    for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
+    if (left < kTok) fence_async_smem();       // a later tensor load writes there
+}
+__device__ __forceinline__ void put_shared(uint16_t* p, f32x2 f) {
+    const float2 v = parts(f);
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ void put_shared(float* p, f32x2 f) { *reinterpret_cast<f32x2*>(p) = f; }
+
+// Waits for a stage's loads. A wait that gave up is reported and not repeated: the rest of the call computes what it finds.
+struct Waits {
+    bool lost = false;
+    __device__ __forceinline__ void full(uint64_t* bar, int parity, uint8_t* ws) {
+        if (lost) return;
+        if (!mbar_wait(bar, parity)) {
+            lost = true;
+            raise_status(ws, KDA_ERR_TIMEOUT);
+        }
+    }
+    // before the block ends: loads that may still be on their way
+    __device__ __forceinline__ void rest(uint64_t* bars, int steps, int stages) {
+        if (!lost) return;
+        for (int s = max(steps - stages, 0); s < steps; ++s) mbar_wait(&bars[s % stages], s / stages & 1);
+    }
+};
 
 // -------------------------------------------------------------------------- sequences
 // The last sequence that starts at or before token t (0 where there is none, so that any offsets at all give
@@ -204,20 +211,20 @@ __device__ __forceinline__ int sequence_at(const RecArgs& a, int t) {
     return max(lo - 1, 0);
 }
 
+__device__ __forceinline__ int bounded(int64_t t) { return (int)max(min(t, (int64_t)0x7fffffff), (int64_t)-1); }
+
 // Starts and ends of sequences among a warp's tokens t0 .. t0 + kTok - 1, one bit each; the sequence of token t0 + j is lane
 // j's. Remembers the sequence between calls.
 struct Events {
     uint32_t starts = 0, ends = 0;
-    int n = -1;
-    int64_t first = 0, last = 0;
-    int seq = 0;
+    int n = -1, first = 0, last = 0, seq = 0;
     __device__ __forceinline__ bool find(const RecArgs& a, int t0) {
         starts = ends = 0;
         if (t0 >= a.total) return false;
         if (n < 0 || t0 < first || t0 >= last) {
             n = sequence_at(a, t0);
-            first = start_of(a, n);
-            last = start_of(a, n + 1);
+            first = bounded(start_of(a, n));
+            last = bounded(start_of(a, n + 1));
         }
         if (first < t0 && last > t0 + kTok) return false;
         const int lane = threadIdx.x & 31, t = t0 + lane;
@@ -293,6 +300,7 @@ struct Shares {          // what the warps of a block and the blocks of a cluste
     float4 warp[2][8][32];
     float4 rank[2][8][32];
     uint8_t warp_fresh[2][8], rank_fresh[2][8];
+    uint64_t full[2];    // the stages' loads
 };
 static_assert(kWarps == 8 && kMostRanks == 8, "a flag for each in eight bytes");
 
@@ -368,30 +376,48 @@ __device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t
     return h;
 }
 
+// The tensor maps of the inputs (boxes of a block's chunk) and outputs (boxes of a warp's rows)
+struct Maps {
+    CUtensorMap x, g, i, dy, out[3];      // out: y, or dx, dg_raw, di_raw
+};
+constexpr int kTile = kBlock * kCh;
+
 // Grid: x segments x ranks of a cluster, y tiles of kCh channels. A cluster takes a segment's chunks of kBlock
-// tokens, its blocks the chunks of a step next to one another, a warp kTok tokens of a chunk, a lane two channels.
+// tokens, its blocks the chunks of a step next to one another, a warp kTok tokens of a chunk, a lane two channels. kVec: rows
+// in whole 16-byte units, which arrive and leave by tensor copies; else every lane moves its own channels.
 // kTotal: only what the segment does to a state, for the segments after it.
-template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kernel(const RecArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+template <typename T> constexpr int kFwdStages = sizeof(T) == 2 ? 2 : 1;
+template <typename T, bool kVec, bool kTotal>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t smem[];
     Shares& sh = *reinterpret_cast<Shares*>(smem);
+    constexpr int kStages = kFwdStages<T>;
+    T* const tiles = reinterpret_cast<T*>(smem + kSharesBytes);          // kStages of x, g, i, then y
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* const rows = reinterpret_cast<T*>(smem + kSharesBytes) + warp * (3 * kTok * kCh);
-    T *const mine = rows + 2 * lane, *const xs = mine, *const gs = mine + kTok * kCh, *const is = mine + 2 * kTok * kCh;
+    const int own_at = warp * kTok * kCh + 2 * lane;
+    T* const out = tiles + kStages * 3 * kTile;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);
     const int steps = (last - first + a.ranks - 1) / a.ranks;
-    auto load = [&](int step) {
+    auto load = [&](int step) {          // by one thread
         const int chunk = first + step * a.ranks + r;
-        const int t0 = chunk < last ? chunk * kBlock + warp * kTok : a.total;     // zeros beyond the segment
-        load_rows<kVec>(rows, a.x, a.sx, t0, a.total, c0, a.D);
-        load_rows<kVec>(rows + kTok * kCh, a.g, a.sg, t0, a.total, c0, a.D);
-        load_rows<kVec>(rows + 2 * kTok * kCh, a.i, a.si, t0, a.total, c0, a.D);
+        if (step >= steps || chunk >= last) return;
+        const int st = step % kStages;
+        T* const to = tiles + st * 3 * kTile;
+        uint64_t* const bar = &sh.full[st];
+        mbar_arrive_expect_tx(bar, 3 * kTile * sizeof(T));
+        tma_load_3d(to, &maps.x, (int)c0, chunk * kBlock, 0, bar);
+        tma_load_3d(to + kTile, &maps.g, (int)c0, chunk * kBlock, 0, bar);
+        tma_load_3d(to + 2 * kTile, &maps.i, (int)c0, chunk * kBlock, 0, bar);
     };
-    load(0);
-    loads_done();
+    if (kVec && threadIdx.x == 0) {
+        for (int st = 0; st < kStages; ++st) mbar_init(&sh.full[st], 1);
+        fence_mbar_init();
+        for (int st = 0; st < kStages; ++st) load(st);
+    }
     if (a.ranks > 1) cluster_arrive();
-    const f32x2 lam = two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), lam2 = mul2(lam, both(-kLog2e));
+    const f32x2 lam2 = mul2(two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), both(-kLog2e));
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
     Run total{both(1.0f), 0};
     bool total_fresh = false;
@@ -400,89 +426,123 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
         pass_empty<kVec>(a, a.hT, a.h0, c);
     }
     if (a.ranks > 1) cluster_wait();       // the cluster's blocks all run, before one writes into another
+    __syncthreads();
     Events ev;
+    Waits wait;
     for (int step = 0; step < steps; ++step) {
         const int chunk = first + step * a.ranks + r;
         const bool some = chunk < last;
         const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;   // tokens of the warp
         const bool events = ev.find(a, some ? t0 : a.total);
-        loads_wait<0>();
-        __syncwarp();
-        for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
+        const T *const xs = tiles + (step % kStages) * 3 * kTile + own_at, *const is = xs + 2 * kTile;
+        T* const gs = const_cast<T*>(xs) + kTile;
         f32x2 n[kTok], b[kTok], h = 0, sum = 0;
-        auto gates = [&](auto with) {
-#pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                const f32x2 s = sigmoid2(pair_at(gs + j * kCh)), v = mul2(lam2, s);
-                n[j] = minus_decayed(mul2(lam, s), v);
-                const float2 m2 = parts(written2(n[j]));
-                b[j] = mul2(mul2(two(root(m2.x), root(m2.y)), sigmoid2(pair_at(is + j * kCh))), pair_at(xs + j * kCh));
-                if constexpr (with.value)
-                    if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                h = advance(h, n[j], b[j]);
-                sum = add2(sum, v);
+        if (some) {
+            if constexpr (kVec) {
+                wait.full(&sh.full[step % kStages], step / kStages & 1, a.ws);
+            } else {
+                load_own(const_cast<T*>(xs), a.x, a.sx, t0, left, c, a.D);
+                load_own(gs, a.g, a.sg, t0, left, c, a.D);
+                load_own(const_cast<T*>(is), a.i, a.si, t0, left, c, a.D);
             }
-        };
-        if (events) gates(std::true_type());
-        else gates(std::false_type());
-        __syncwarp();
-        if (step + 1 < steps) load(step + 1);
-        loads_done();
+            if (left < kTok) close_rows(gs, left);
+            auto gates = [&](auto with) {
+#pragma unroll
+                for (int j = 0; j < kTok; ++j) {
+                    const f32x2 v = mul2(lam2, sigmoid2(pair_at(gs + j * kCh)));
+                    n[j] = minus_decayed(v);
+                    const float2 m2 = parts(written2(n[j]));
+                    b[j] = mul2(mul2(two(root(m2.x), root(m2.y)), sigmoid2(pair_at(is + j * kCh))), pair_at(xs + j * kCh));
+                    if constexpr (with.value)
+                        if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                    h = advance(h, n[j], b[j]);
+                    sum = add2(sum, v);
+                }
+            };
+            if (events) gates(std::true_type());
+            else gates(std::false_type());
+        }
         h = exchange<kTotal>(sh, step & 1, a.ranks, r, warp, Run{exp2_of(sum), h}, events && ev.starts, carry, total, total_fresh);
+        if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);     // every warp has read the stage
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
-            T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.sy + c;
-            if (!events && left == kTok) {
-#pragma unroll
-                for (int j = 0; j < kTok; ++j, y += a.sy) {
-                    h = advance(h, n[j], b[j]);
-                    store_pair<kVec>(y, c, a.D, h);
+            if (left > 0) {
+                if constexpr (kVec) {
+                    if (lane == 0) bulk_wait_read_all();        // the step before has left
+                    __syncwarp();
                 }
-            } else {
+                T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.sy + c;
+                auto states = [&](auto with) {
 #pragma unroll
-                for (int j = 0; j < kTok; ++j, y += a.sy) {
-                    if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                    h = advance(h, n[j], b[j]);
-                    if (j < left) store_pair<kVec>(y, c, a.D, h);
-                    if (ev.ends >> j & 1) {
-                        const int q = ev.of(j);
-                        if (a.hT) store_state<kVec>(a.hT, q, c, a.D, h);
+                    for (int j = 0; j < kTok; ++j) {
+                        if constexpr (with.value)
+                            if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                        h = advance(h, n[j], b[j]);
+                        if constexpr (kVec) put_shared(out + own_at + j * kCh, h);
+                        else if (j < left) store_pair<kVec>(y + j * a.sy, c, a.D, h);
+                        if constexpr (with.value)
+                            if (ev.ends >> j & 1) {
+                                const int q = ev.of(j);
+                                if (a.hT) store_state<kVec>(a.hT, q, c, a.D, h);
+                            }
+                    }
+                };
+                if (events) states(std::true_type());
+                else states(std::false_type());
+                if constexpr (kVec) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(out + warp * kTok * kCh, &maps.out[0], (int)c0, t0, 0);
+                        bulk_commit();
                     }
                 }
             }
         }
     }
+    if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, kStages);
     if constexpr (kTotal) {
         if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
         if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
+    } else if (kVec) {
+        if (lane == 0) bulk_wait_all();
     }
 }
 
-// The same grid, tokens from the last to the first: chunks, ranks and warps in that order.
-template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const RecArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+// The same grid, tokens from the last to the first: chunks, ranks and warps in that order. The gradients take the inputs'
+// places in shared memory.
+template <typename T, bool kTotal> constexpr int kBwdStages = sizeof(T) == 2 ? 2 : 1;
+template <typename T, bool kVec, bool kTotal>
+__global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t smem[];
     Shares& sh = *reinterpret_cast<Shares*>(smem);
     Ahead& ahead = *reinterpret_cast<Ahead*>(smem + kSharesBytes);      // the states' way, forwards
-    constexpr int kTensors = kTotal ? 2 : 4, kStages = sizeof(T) == 2 && !kTotal ? 2 : 1, kStage = kTensors * kTok * kCh;
+    constexpr int kTensors = kTotal ? 2 : 4, kStages = kBwdStages<T, kTotal>;
+    T* const tiles = reinterpret_cast<T*>(smem + kSharesBytes + kAheadBytes);       // kStages of g, dy, x, i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* const base = reinterpret_cast<T*>(smem + kSharesBytes + kAheadBytes) + warp * (kStages * kStage);
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);   // counted from the last chunk
     const int steps = (last - first + a.ranks - 1) / a.ranks;
-    auto load = [&](int step) {
+    auto load = [&](int step) {          // by one thread
         const int at = first + step * a.ranks + r;
-        T* const rows = base + (kStages == 2 ? (step & 1) * kStage : 0);
-        const int t0 = at < last ? (a.chunks - 1 - at) * kBlock + warp * kTok : a.total;
-        load_rows<kVec>(rows, a.g, a.sg, t0, a.total, c0, a.D);
-        load_rows<kVec>(rows + kTok * kCh, a.dy, a.sy, t0, a.total, c0, a.D);
+        if (step >= steps || at >= last) return;
+        const int st = step % kStages, t0 = (a.chunks - 1 - at) * kBlock;
+        T* const to = tiles + st * kTensors * kTile;
+        uint64_t* const bar = &sh.full[st];
+        mbar_arrive_expect_tx(bar, kTensors * kTile * sizeof(T));
+        tma_load_3d(to, &maps.g, (int)c0, t0, 0, bar);
+        tma_load_3d(to + kTile, &maps.dy, (int)c0, t0, 0, bar);
         if constexpr (!kTotal) {
-            load_rows<kVec>(rows + 2 * kTok * kCh, a.x, a.sx, t0, a.total, c0, a.D);
-            load_rows<kVec>(rows + 3 * kTok * kCh, a.i, a.si, t0, a.total, c0, a.D);
+            tma_load_3d(to + 2 * kTile, &maps.x, (int)c0, t0, 0, bar);
+            tma_load_3d(to + 3 * kTile, &maps.i, (int)c0, t0, 0, bar);
         }
     };
-    load(0);
-    loads_done();
+    if (kVec && threadIdx.x == 0) {
+        for (int st = 0; st < kStages; ++st) mbar_init(&sh.full[st], 1);
+        fence_mbar_init();
+        for (int st = 0; st < kStages; ++st) load(st);
+    }
     if (a.ranks > 1) cluster_arrive();
     const f32x2 lam = two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), lam2 = mul2(lam, both(-kLog2e));
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
@@ -493,123 +553,150 @@ template <typename T, bool kVec, bool kTotal> __global__ void __launch_bounds__(
         pass_empty<kVec>(a, a.dh0, a.dhT, c);
     }
     if (a.ranks > 1) cluster_wait();
+    __syncthreads();
     Events ev;
+    Waits wait;
     f32x2 acc = 0;
     for (int step = 0; step < steps; ++step) {
         const int at = first + step * a.ranks + r, chunk = a.chunks - 1 - at;
         const bool some = at < last;
         const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;
         const bool events = ev.find(a, some ? t0 : a.total);
-        T *const gs = base + (kStages == 2 ? (step & 1) * kStage : 0) + 2 * lane, *const dys = gs + kTok * kCh, *const xs = gs + 2 * kTok * kCh,
-                 *const is = gs + 3 * kTok * kCh;
-        if constexpr (kStages == 2) {
-            __syncwarp();          // the last lane's reads of the step before last
-            if (step + 1 < steps) load(step + 1);
-            loads_done();
-            loads_wait<1>();
-        } else {
-            loads_wait<0>();
-        }
-        __syncwarp();
-        for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
+        T* const own = tiles + (step % kStages) * kTensors * kTile + warp * kTok * kCh;
+        T *const gs = own + 2 * lane, *const dys = gs + kTile, *const xs = gs + 2 * kTile, *const is = gs + 3 * kTile;
         f32x2 s[kTok], n[kTok], si[kTok], rs[kTok], h = 0, sum = 0, G = 0;
-        auto sums = [&](auto with) {
-#pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                s[j] = sigmoid2(pair_at(gs + j * kCh));
-                const f32x2 v = mul2(lam2, s[j]);
-                n[j] = minus_decayed(mul2(lam, s[j]), v);
-                sum = add2(sum, v);
+        if (some) {
+            if constexpr (kVec) {
+                wait.full(&sh.full[step % kStages], step / kStages & 1, a.ws);
+            } else {
+                load_own(gs, a.g, a.sg, t0, left, c, a.D);
+                load_own(dys, a.dy, a.sy, t0, left, c, a.D);
                 if constexpr (!kTotal) {
-                    const f32x2 m2 = written2(n[j]);
-                    const float2 p = parts(add2(m2, both(0x1p-125f)));      // no infinity at 0
-                    rs[j] = two(inverse_root(p.x), inverse_root(p.y));
-                    si[j] = sigmoid2(pair_at(is + j * kCh));
-                    if constexpr (with.value)
-                        if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                    h = advance(h, n[j], mul2(mul2(m2, rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
+                    load_own(xs, a.x, a.sx, t0, left, c, a.D);
+                    load_own(is, a.i, a.si, t0, left, c, a.D);
                 }
             }
+            if (left < kTok) close_rows(gs, left);
+            auto sums = [&](auto with) {
 #pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if constexpr (with.value)
-                    if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
-                const f32x2 t = add2(G, pair_at(dys + j * kCh));
-                G = fma2(n[j], t, t);
-            }
-        };
-        if (events) sums(std::true_type());
-        else sums(std::false_type());
+                for (int j = 0; j < kTok; ++j) {
+                    s[j] = sigmoid2(pair_at(gs + j * kCh));
+                    const f32x2 v = mul2(lam2, s[j]);
+                    n[j] = minus_decayed(v);
+                    sum = add2(sum, v);
+                    if constexpr (!kTotal) {
+                        const f32x2 m2 = written2(n[j]);
+                        const float2 p = parts(add2(m2, both(0x1p-125f)));      // no infinity at 0
+                        rs[j] = two(inverse_root(p.x), inverse_root(p.y));
+                        si[j] = sigmoid2(pair_at(is + j * kCh));
+                        if constexpr (with.value)
+                            if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                        h = advance(h, n[j], mul2(mul2(m2, rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
+                    }
+                }
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) {
+                    if constexpr (with.value)
+                        if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
+                    const f32x2 t = add2(G, pair_at(dys + j * kCh));
+                    G = fma2(n[j], t, t);
+                }
+            };
+            if (events) sums(std::true_type());
+            else sums(std::false_type());
+        }
         const f32x2 decay = exp2_of(sum);
         if constexpr (!kTotal) {
             ahead.warp[step & 1][warp][lane] = held(Run{decay, h});
-            if (lane == 0) ahead.fresh[step & 1][warp] = events && ev.starts;
+            if (lane == 0) {
+                ahead.fresh[step & 1][warp] = events && ev.starts;
+                if (kVec) bulk_wait_read_all();      // the gradients of the step before have left
+            }
             h = some ? load_state<kVec>(a.kept, chunk, c, a.D) : 0;
         }
         G = exchange<kTotal>(sh, step & 1, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends, carry, total, total_fresh);
         if constexpr (kTotal) {
-            __syncwarp();
-            if (step + 1 < steps) load(step + 1);
-            loads_done();
+            if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);
         } else {
-            h = through(ahead.warp[step & 1], *reinterpret_cast<const uint64_t*>(ahead.fresh[step & 1]), 0, warp, h);
-            f32x2 before[kTok];
-            T *dx = static_cast<T*>(a.dx) + (int64_t)(t0 + kTok - 1) * a.sdx + c, *dg = static_cast<T*>(a.dg) + (int64_t)(t0 + kTok - 1) * a.sdg + c,
-              *di = static_cast<T*>(a.di) + (int64_t)(t0 + kTok - 1) * a.sdi + c;
-            auto grads = [&](auto with) {
+            if (kVec && kStages == 2 && threadIdx.x == 0 && !wait.lost && step > 0) load(step + 1);    // into the other stage, which all have left
+            if (left > 0) {
+                h = through(ahead.warp[step & 1], *reinterpret_cast<const uint64_t*>(ahead.fresh[step & 1]), 0, warp, h);
+                f32x2 before[kTok];
+                auto grads = [&](auto with) {
 #pragma unroll
-                for (int j = 0; j < kTok; ++j) {
-                    if constexpr (with.value)
-                        if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                    before[j] = h;
-                    h = advance(h, n[j], mul2(mul2(written2(n[j]), rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
-                }
-#pragma unroll
-                for (int j = kTok - 1; j >= 0; --j, dx -= a.sdx, dg -= a.sdg, di -= a.sdi) {
-                    if constexpr (with.value)
-                        if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
-                    const f32x2 t = add2(G, pair_at(dys + j * kCh)), ix = mul2(si[j], pair_at(xs + j * kCh)), d = add2(n[j], both(1.0f));
-                    const f32x2 tm = mul2(t, mul2(written2(n[j]), rs[j]));
-                    const f32x2 q = fma2(before[j], both(-1.0f), mul2(mul2(rs[j], ix), d));       // over d: m' - h
-                    const f32x2 duu = mul2(mul2(t, mul2(lam, s[j])), mul2(d, q));
-                    acc = add2(acc, duu);
-                    G = fma2(n[j], t, t);
-                    if (!with.value || j < left) {
-                        store_pair<kVec>(dx, c, a.D, mul2(tm, si[j]));
-                        store_pair<kVec>(dg, c, a.D, mul2(duu, mul2(exp_minus(pair_at(gs + j * kCh)), s[j])));
-                        store_pair<kVec>(di, c, a.D, mul2(mul2(tm, ix), mul2(exp_minus(pair_at(is + j * kCh)), si[j])));
+                    for (int j = 0; j < kTok; ++j) {
+                        if constexpr (with.value)
+                            if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                        before[j] = h;
+                        h = advance(h, n[j], mul2(mul2(written2(n[j]), rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
                     }
-                    if constexpr (with.value)
-                        if (ev.starts >> j & 1) {
-                            const int q0 = ev.of(j);
-                            if (a.dh0) store_state<kVec>(a.dh0, q0, c, a.D, G);
+#pragma unroll
+                    for (int j = kTok - 1; j >= 0; --j) {
+                        if constexpr (with.value)
+                            if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
+                        const f32x2 t = add2(G, pair_at(dys + j * kCh)), ix = mul2(si[j], pair_at(xs + j * kCh)), d = add2(n[j], both(1.0f));
+                        const f32x2 tm = mul2(t, mul2(written2(n[j]), rs[j]));
+                        const f32x2 q = fma2(before[j], both(-1.0f), mul2(mul2(rs[j], ix), d));       // i x a / m - h, times u a below
+                        const f32x2 duu = mul2(mul2(t, mul2(lam, s[j])), mul2(d, q));
+                        acc = add2(acc, duu);
+                        G = fma2(n[j], t, t);
+                        const f32x2 dx = mul2(tm, si[j]), dg = mul2(duu, mul2(exp_minus(pair_at(gs + j * kCh)), s[j])),
+                                    di = mul2(mul2(tm, ix), mul2(exp_minus(pair_at(is + j * kCh)), si[j]));
+                        if constexpr (kVec) {
+                            put_shared(xs + j * kCh, dx);
+                            put_shared(gs + j * kCh, dg);
+                            put_shared(is + j * kCh, di);
+                        } else if (j < left) {
+                            store_pair<kVec>(static_cast<T*>(a.dx) + (int64_t)(t0 + j) * a.sdx + c, c, a.D, dx);
+                            store_pair<kVec>(static_cast<T*>(a.dg) + (int64_t)(t0 + j) * a.sdg + c, c, a.D, dg);
+                            store_pair<kVec>(static_cast<T*>(a.di) + (int64_t)(t0 + j) * a.sdi + c, c, a.D, di);
                         }
+                        if constexpr (with.value)
+                            if (ev.starts >> j & 1) {
+                                const int q0 = ev.of(j);
+                                if (a.dh0) store_state<kVec>(a.dh0, q0, c, a.D, G);
+                            }
+                    }
+                };
+                if (events) grads(std::true_type());
+                else grads(std::false_type());
+                if constexpr (kVec) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(own + 2 * kTile, &maps.out[0], (int)c0, t0, 0);
+                        tma_store_3d(own, &maps.out[1], (int)c0, t0, 0);
+                        tma_store_3d(own + 3 * kTile, &maps.out[2], (int)c0, t0, 0);
+                        bulk_commit();
+                    }
                 }
-            };
-            if (events || left < kTok) grads(std::true_type());
-            else grads(std::false_type());
-            if constexpr (kStages == 1) {
-                __syncwarp();
-                if (step + 1 < steps) load(step + 1);
-                loads_done();
+            }
+            if constexpr (kVec && kStages == 1) {
+                if (lane == 0) bulk_wait_read_all();
+                __syncthreads();
+                if (threadIdx.x == 0 && !wait.lost) load(step + 1);
             }
         }
     }
+    if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, kStages);
     if constexpr (kTotal) {
         if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
         if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
-    } else if (a.part) {
-        grid_launch_next();
-        // the block's share of dA_log: its warps in turn
-        __syncthreads();
-        f32x2* const shares = reinterpret_cast<f32x2*>(&ahead);
-        shares[warp * 32 + lane] = acc;
-        __syncthreads();
-        if (warp == 0) {
+    } else {
+        if (a.part) {
+            grid_launch_next();
+            // the block's share of dA_log: its warps in turn
+            __syncthreads();
+            f32x2* const shares = reinterpret_cast<f32x2*>(&ahead);
+            shares[warp * 32 + lane] = acc;
+            __syncthreads();
+            if (warp == 0) {
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) acc = add2(acc, shares[v * 32 + lane]);
-            store_state<kVec>(a.part, blockIdx.x, c, a.D, acc);
+                for (int v = 1; v < kWarps; ++v) acc = add2(acc, shares[v * 32 + lane]);
+                store_state<kVec>(a.part, blockIdx.x, c, a.D, acc);
+            }
         }
+        if (kVec && lane == 0) bulk_wait_all();
     }
 }
 
@@ -640,7 +727,7 @@ template <typename T, bool kVec> __global__ void __launch_bounds__(256) rec_deco
     T* y = static_cast<T*>(a.y) + t * a.sy + c;
     float* state = a.hT + t * a.D + c;
     auto step = [](f32x2 h, f32x2 x, f32x2 g, f32x2 i, f32x2 lam) {
-        const f32x2 s = sigmoid2(g), n = minus_decayed(mul2(lam, s), mul2(mul2(lam, both(-kLog2e)), s));
+        const f32x2 s = sigmoid2(g), n = minus_decayed(mul2(mul2(lam, both(-kLog2e)), s));
         const float2 m2 = parts(written2(n));
         return advance(h, n, mul2(mul2(two(root(m2.x), root(m2.y)), sigmoid2(i)), x));
     };
@@ -731,11 +818,11 @@ bool whole_units(const kda_recurrence_shape* sh, std::initializer_list<const voi
     const int unit = sh->dtype == KDA_BF16 ? 8 : 4;
     bool ok = sh->D % 8 == 0;
     for (const void* p : ptrs) ok = ok && !misaligned(p);
-    for (const int64_t s : strides) ok = ok && s % unit == 0;
+    for (const int64_t s : strides) ok = ok && s % unit == 0 && s < (int64_t(1) << 36);    // of tensor maps: 2^40 bytes
     return ok;
 }
 
-using Kernel = void (*)(RecArgs);
+using Kernel = void (*)(RecArgs, Maps);
 template <bool kBwd, typename T, bool kVec, bool kTotal> Kernel kernel_of() {
     if constexpr (kBwd) return rec_bwd_kernel<T, kVec, kTotal>;
     else return rec_fwd_kernel<T, kVec, kTotal>;
@@ -748,9 +835,9 @@ template <bool kBwd> Kernel pick(bool bf16, bool vec, bool total) {
 }
 
 constexpr size_t smem_of(bool backward, size_t element, bool total) {
-    const size_t rows = (size_t)kWarps * kTok * kCh * element;
-    if (!backward) return kSharesBytes + 3 * rows;
-    return kSharesBytes + kAheadBytes + (total ? 2 : element == 2 ? 8 : 4) * rows;
+    const size_t tile = kTile * element, stages = element == 2 ? 2 : 1;
+    if (!backward) return kSharesBytes + (3 * stages + 1) * tile;
+    return kSharesBytes + kAheadBytes + (total ? 2 : 4) * stages * tile;
 }
 
 // The kernels' limits on shared memory are set once for each device.
@@ -771,7 +858,7 @@ kda_status allow_shared(const char* where) {
     return KDA_OK;
 }
 
-void launch_clusters(Kernel f, const Plan& p, int segs, size_t smem, cudaStream_t s, const RecArgs& a) {
+void launch_clusters(Kernel f, const Plan& p, int segs, size_t smem, cudaStream_t s, const RecArgs& a, const Maps& m) {
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = (unsigned)p.ranks;
@@ -783,7 +870,36 @@ void launch_clusters(Kernel f, const Plan& p, int segs, size_t smem, cudaStream_
     c.stream = s;
     c.attrs = &at;
     c.numAttrs = p.ranks > 1 ? 1 : 0;
-    cudaLaunchKernelEx(&c, f, a);   // an error is left for cudaGetLastError
+    cudaLaunchKernelEx(&c, f, a, m);   // an error is left for cudaGetLastError
+}
+
+// The tensor map of a [tokens, D] tensor in boxes of `rows` tokens x kCh channels
+kda_status row_map(CUtensorMap* map, const void* p, int64_t D, int64_t tokens, int64_t stride, int rows, int element) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) {
+        set_last_error_text("the driver has no cuTensorMapEncodeTiled");
+        return KDA_ERR_CUDA;
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)tokens, 1}, strides[2] = {(cuuint64_t)(stride * element), (cuuint64_t)(stride * element)};
+    const cuuint32_t box[3] = {kCh, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+    const CUresult r = encode(map, element == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p),
+                              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return KDA_OK;
+    char msg[96];
+    snprintf(msg, sizeof(msg), "cuTensorMapEncodeTiled: %d", (int)r);
+    set_last_error_text(msg);
+    return KDA_ERR_CUDA;
 }
 
 template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, bool vec, cudaStream_t s, const char* where) {
@@ -794,8 +910,21 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
     a.chunks = p.chunks; a.seg_chunks = p.seg_chunks; a.ranks = p.ranks;
     a.seg = reinterpret_cast<float4*>(a.ws + 1024);
     a.seg_fresh = reinterpret_cast<int*>(a.ws + 64);       // kMostSegs of them
-    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a);
-    launch_clusters(pick<kBwd>(bf16, vec, false), p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a);
+    Maps m{};
+    if (vec && a.total > 0) {
+        const int e = bf16 ? 2 : 4;
+        auto map = [&](CUtensorMap* to, const void* p, int64_t stride, int rows) { return row_map(to, p, sh->D, a.total, stride, rows, e); };
+        kda_status ms = map(&m.x, a.x, a.sx, kBlock);
+        if (ms == KDA_OK) ms = map(&m.g, a.g, a.sg, kBlock);
+        if (ms == KDA_OK) ms = map(&m.i, a.i, a.si, kBlock);
+        if (kBwd && ms == KDA_OK) ms = map(&m.dy, a.dy, a.sy, kBlock);
+        if (ms == KDA_OK) ms = kBwd ? map(&m.out[0], a.dx, a.sdx, kTok) : map(&m.out[0], a.y, a.sy, kTok);
+        if (kBwd && ms == KDA_OK) ms = map(&m.out[1], a.dg, a.sdg, kTok);
+        if (kBwd && ms == KDA_OK) ms = map(&m.out[2], a.di, a.sdi, kTok);
+        if (ms != KDA_OK) return ms;
+    }
+    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a, m);
+    launch_clusters(pick<kBwd>(bf16, vec, false), p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a, m);
     return launched(where);
 }
 
@@ -881,7 +1010,7 @@ extern "C" kda_status kda_recurrence_decode(const kda_recurrence_shape* shape, c
     const bool vec = whole_units(shape, {x, g_raw, i_raw, y}, {a.sx, a.sg, a.si, a.sy});
     const int64_t blocks = (a.N * (vec ? a.D / 4 : a.D) + 255) / 256;
     if (blocks >= (int64_t(1) << 31)) return KDA_ERR_SHAPE;
-    const Kernel f = shape->dtype == KDA_BF16 ? (vec ? rec_decode_kernel<uint16_t, true> : rec_decode_kernel<uint16_t, false>)
+    const auto f = shape->dtype == KDA_BF16 ? (vec ? rec_decode_kernel<uint16_t, true> : rec_decode_kernel<uint16_t, false>)
                                               : (vec ? rec_decode_kernel<float, true> : rec_decode_kernel<float, false>);
     f<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return launched("kda_recurrence_decode launch");
