@@ -21,9 +21,7 @@ void set_last_error_text(const char* msg);
 namespace {
 constexpr int kBlock = KDA_RECURRENCE_BLOCK;
 constexpr int kCh = 64;              // channels of a block, two to a lane
-constexpr int kTok = 8;              // tokens of a warp
-constexpr int kWarps = kBlock / kTok;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kMostWarps = 8;
 constexpr int kMostRanks = 8;
 constexpr int kMostSegs = 64;
 constexpr int kSMs = 152;
@@ -149,7 +147,7 @@ template <bool kVec> __device__ __forceinline__ void store_state(float* p, int64
 }
 
 // The lane's channels of a warp's kTok rows of one token tensor, to rows of kCh in shared memory; zeros outside the tensor
-template <typename T>
+template <int kTok, typename T>
 __device__ __forceinline__ void load_own(T* dst, const void* src, int64_t stride, int t0, int left, int64_t c, int64_t D) {
     const T* p = static_cast<const T*>(src) + (int64_t)t0 * stride + c;
     T a[kTok], b[kTok];
@@ -167,7 +165,7 @@ __device__ __forceinline__ void load_own(T* dst, const void* src, int64_t stride
 // Rows of the decay's gate that are no tokens: a closed gate, which decays and writes nothing.
 __device__ __forceinline__ void closed(uint16_t* p) { *reinterpret_cast<uint32_t*>(p) = 0xff80ff80u; }
 __device__ __forceinline__ void closed(float* p) { *reinterpret_cast<uint64_t*>(p) = 0xff800000ff800000ull; }
-template <typename T> __device__ __forceinline__ void close_rows(T* gs, int left) {
+template <int kTok, typename T> __device__ __forceinline__ void close_rows(T* gs, int left) {
     for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
     if (left < kTok) fence_async_smem();       // a later tensor load writes there
 }
@@ -215,7 +213,7 @@ __device__ __forceinline__ int bounded(int64_t t) { return (int)max(min(t, (int6
 
 // Starts and ends of sequences among a warp's tokens t0 .. t0 + kTok - 1, one bit each; the sequence of token t0 + j is lane
 // j's. Remembers the sequence between calls.
-struct Events {
+template <int kTok> struct Events {
     uint32_t starts = 0, ends = 0;
     int n = -1, first = 0, last = 0, seq = 0;
     __device__ __forceinline__ bool find(const RecArgs& a, int t0) {
@@ -249,7 +247,7 @@ struct Events {
 
 // The states of sequences without tokens go through as they are, a share of the sequences for each warp of the blocks
 // along the tokens.
-template <bool kVec>
+template <int kWarps, bool kVec>
 __device__ __forceinline__ void pass_empty(const RecArgs& a, float* out, const float* in, int64_t c) {
     if (!out) return;
     const int lane = threadIdx.x & 31, warps = gridDim.x * kWarps;
@@ -269,7 +267,7 @@ __device__ __forceinline__ void check_offsets(const RecArgs& a) {
     int bad = 0;
     if (a.cu) {
 #pragma unroll 4
-        for (int n = threadIdx.x; n < a.N; n += kThreads) bad |= a.cu[n] > a.cu[n + 1];
+        for (int n = threadIdx.x; n < a.N; n += (int)blockDim.x) bad |= a.cu[n] > a.cu[n + 1];
         bad |= a.cu[0] != 0 || a.cu[a.N] != a.total;
     }
     bad = __syncthreads_or(bad);
@@ -277,87 +275,108 @@ __device__ __forceinline__ void check_offsets(const RecArgs& a) {
 }
 
 // ------------------------------------------------------------------ blocks of a cluster
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ int cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return (int)r;
 }
-__device__ __forceinline__ void store_at_rank(float4* p, int rank, const float4& v) {
+// Stores into a block of the cluster, counted in bytes on a barrier of that block
+__device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
     uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(p)), "r"(rank));
+    return to;
 }
-
-__device__ __forceinline__ void flag_at_rank(uint8_t* p, int rank, uint32_t v) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+__device__ __forceinline__ void send(uint32_t to, const float4& v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t to, uint32_t v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(bar) : "memory");
 }
 
 struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
-    float4 warp[2][8][32];
-    float4 rank[2][8][32];
-    uint8_t warp_fresh[2][8], rank_fresh[2][8];
+    float4 warp[2][kMostWarps][32];
+    float4 rank[2][kMostRanks][32];
+    uint8_t warp_fresh[2][kMostWarps];
+    uint32_t rank_fresh[2][kMostRanks];
     uint64_t full[2];    // the stages' loads
+    uint64_t sent[2];    // the ranks' sums
 };
-static_assert(kWarps == 8 && kMostRanks == 8, "a flag for each in eight bytes");
+static_assert(kMostWarps == 8 && kMostRanks == 8, "a flag for each in eight bytes");
 
-struct Ahead {           // what the warps' tokens do to a state, in the backward
-    float4 warp[2][8][32];
-    uint8_t fresh[2][8];
-};
-constexpr size_t kSharesBytes = (sizeof(Shares) + 127) / 128 * 128, kAheadBytes = (sizeof(Ahead) + 127) / 128 * 128;
-
-// h through the runs from `from` to `to`
-__device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint64_t fresh, int from, int to, f32x2 h) {
+// h through the runs from `from` to `to`; fresh: a bit for each
+__device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint32_t fresh, int from, int to, f32x2 h) {
     const int lane = threadIdx.x & 31;
     if (fresh == 0) {
-#pragma unroll 2
-        for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), false, h);
+#pragma unroll 4
+        for (int k = from; k < to; ++k) {
+            const Run s = run_of(runs[k][lane]);
+            h = fma2(s.a, h, s.b);
+        }
     } else {
-        for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), (fresh >> (8 * k) & 1) != 0, h);
+        for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), (fresh >> k & 1) != 0, h);
     }
     return h;
+}
+// kCount bytes that are 0 or 1, as bits (byte k times 2^(56 - 7 k) is bit k of the product's highest byte)
+template <int kCount> __device__ __forceinline__ uint32_t bits_of(const uint8_t* p) {
+    static_assert(kCount == 8 || kCount == 4, "one load");
+    const uint64_t v = kCount == 8 ? *reinterpret_cast<const uint64_t*>(p) : *reinterpret_cast<const uint32_t*>(p);
+    return (uint32_t)(v * 0x0102040810204080ull >> 56);
 }
 
 // After a step's own sums: the state (adjoint) that comes to this warp, and in `carry` the one that leaves the step.
 // Warps and ranks follow one another in the order of the scan, `w` and `r` their places in it. kTotal: only what all
-// the steps so far do, in `total`.
-template <bool kTotal>
-__device__ __forceinline__ f32x2 exchange(Shares& sh, int parity, int ranks, int r, int w, const Run& own, bool fresh, f32x2& carry,
-                                          Run& total, bool& total_fresh) {
-    const int lane = threadIdx.x & 31;
+// the steps so far do, in `total`. The blocks' sums travel over distributed shared memory with their own
+// completion: a barrier of the cluster would make every thread wait for all its stores (a third of the time).
+// Two steps' sums are kept, and nobody sends a third before all have read the first: a block's sum of the step between
+// left it after that.
+template <int kWarps, bool kTotal>
+__device__ __forceinline__ f32x2 exchange(Shares& sh, int step, int ranks, int r, int w, const Run& own, bool fresh, f32x2& carry,
+                                          Run& total, bool& total_fresh, Waits& wait, uint8_t* ws) {
+    const int lane = threadIdx.x & 31, parity = step & 1;
     sh.warp[parity][w][lane] = held(own);
     if (lane == 0) sh.warp_fresh[parity][w] = fresh;
     __syncthreads();
-    const uint64_t warps = *reinterpret_cast<const uint64_t*>(sh.warp_fresh[parity]);
+    const uint32_t warps = bits_of<kWarps>(sh.warp_fresh[parity]);
+    uint32_t all = warps;
     if (ranks > 1) {
         if (w == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(&sh.sent[parity], (uint32_t)ranks * (32 * sizeof(float4) + 4));
             Run s = own;
+            if (warps == 0) {
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), (warps >> (8 * v) & 1) != 0);
+                for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), false);
+            } else {
+#pragma unroll
+                for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), (warps >> v & 1) != 0);
+            }
             const float4 f = held(s);
-            for (int k = 0; k < ranks; ++k) store_at_rank(&sh.rank[parity][r][lane], k, f);
-            if (lane < ranks) flag_at_rank(&sh.rank_fresh[parity][r], lane, warps != 0);
+            for (int k = 0; k < ranks; ++k) {
+                const uint32_t bar = at_rank(&sh.sent[parity], k);
+                send(at_rank(&sh.rank[parity][r][lane], k), f, bar);
+                if (lane == 0) send(at_rank(&sh.rank_fresh[parity][r], k), warps != 0 ? 1u : 0u, bar);
+            }
         }
-        cluster_arrive();
-        cluster_wait();
+        wait.full(&sh.sent[parity], step >> 1 & 1, ws);
+        all = __ballot_sync(0xffffffffu, lane < ranks && sh.rank_fresh[parity][lane & (kMostRanks - 1)] != 0);
     }
     if constexpr (kTotal) {
-        const uint64_t all = ranks > 1 ? *reinterpret_cast<const uint64_t*>(sh.rank_fresh[parity]) : warps;
         const int count = ranks > 1 ? ranks : kWarps;
         for (int k = 0; k < count; ++k) {
-            const bool f = (all >> (8 * k) & 1) != 0;
+            const bool f = (all >> k & 1) != 0;
             total = then(total, run_of((ranks > 1 ? sh.rank : sh.warp)[parity][k][lane]), f);
             total_fresh = total_fresh || f;
         }
         return 0;
     }
     if (ranks > 1) {
-        uint64_t all = *reinterpret_cast<const uint64_t*>(sh.rank_fresh[parity]);
-        if (ranks < 8) all &= (uint64_t(1) << (8 * ranks)) - 1;
         const f32x2 block = through(sh.rank[parity], all, 0, r, carry);
         carry = through(sh.rank[parity], all, r, ranks, block);
         return through(sh.warp[parity], warps, 0, w, block);
@@ -366,6 +385,12 @@ __device__ __forceinline__ f32x2 exchange(Shares& sh, int parity, int ranks, int
     carry = through(sh.warp[parity], warps, w, kWarps, at);
     return at;
 }
+
+struct Ahead {           // what the warps' tokens do to a state, in the backward
+    float4 warp[2][kMostWarps][32];
+    uint8_t fresh[2][kMostWarps];
+};
+constexpr size_t kSharesBytes = (sizeof(Shares) + 127) / 128 * 128, kAheadBytes = (sizeof(Ahead) + 127) / 128 * 128;
 
 // The state that comes to segment `seg`, in the order of the scan, from what those before it did
 __device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t c) {
@@ -387,13 +412,14 @@ constexpr int kTile = kBlock * kCh;
 // in whole 16-byte units, which arrive and leave by tensor copies; else every lane moves its own channels.
 // kTotal: only what the segment does to a state, for the segments after it.
 template <typename T> constexpr int kFwdStages = sizeof(T) == 2 ? 2 : 1;
+constexpr int kFwdTok = 16, kFwdThreads = kBlock / kFwdTok * 32;      // tokens of a warp
 template <typename T, bool kVec, bool kTotal>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
     Shares& sh = *reinterpret_cast<Shares*>(smem);
-    constexpr int kStages = kFwdStages<T>;
+    constexpr int kStages = kFwdStages<T>, kTok = kFwdTok, kWarps = kBlock / kTok;
     T* const tiles = reinterpret_cast<T*>(smem + kSharesBytes);          // kStages of x, g, i, then y
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;      // the warp's, as the compiler may know
     const int own_at = warp * kTok * kCh + 2 * lane;
     T* const out = tiles + kStages * 3 * kTile;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
@@ -411,10 +437,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kern
         tma_load_3d(to + kTile, &maps.g, (int)c0, chunk * kBlock, 0, bar);
         tma_load_3d(to + 2 * kTile, &maps.i, (int)c0, chunk * kBlock, 0, bar);
     };
-    if (kVec && threadIdx.x == 0) {
-        for (int st = 0; st < kStages; ++st) mbar_init(&sh.full[st], 1);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&sh.full[k], 1);
+            mbar_init(&sh.sent[k], 1);
+        }
         fence_mbar_init();
-        for (int st = 0; st < kStages; ++st) load(st);
+        if constexpr (kVec)
+            for (int st = 0; st < kStages; ++st) load(st);
     }
     if (a.ranks > 1) cluster_arrive();
     const f32x2 lam2 = mul2(two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), both(-kLog2e));
@@ -423,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kern
     bool total_fresh = false;
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
-        pass_empty<kVec>(a, a.hT, a.h0, c);
+        pass_empty<kWarps, kVec>(a, a.hT, a.h0, c);
     }
     if (a.ranks > 1) cluster_wait();       // the cluster's blocks all run, before one writes into another
     __syncthreads();
-    Events ev;
+    Events<kTok> ev;
     Waits wait;
     for (int step = 0; step < steps; ++step) {
         const int chunk = first + step * a.ranks + r;
@@ -441,11 +471,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kern
             if constexpr (kVec) {
                 wait.full(&sh.full[step % kStages], step / kStages & 1, a.ws);
             } else {
-                load_own(const_cast<T*>(xs), a.x, a.sx, t0, left, c, a.D);
-                load_own(gs, a.g, a.sg, t0, left, c, a.D);
-                load_own(const_cast<T*>(is), a.i, a.si, t0, left, c, a.D);
+                load_own<kTok>(const_cast<T*>(xs), a.x, a.sx, t0, left, c, a.D);
+                load_own<kTok>(gs, a.g, a.sg, t0, left, c, a.D);
+                load_own<kTok>(const_cast<T*>(is), a.i, a.si, t0, left, c, a.D);
             }
-            if (left < kTok) close_rows(gs, left);
+            if (left < kTok) close_rows<kTok>(gs, left);
             auto gates = [&](auto with) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
@@ -462,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kern
             if (events) gates(std::true_type());
             else gates(std::false_type());
         }
-        h = exchange<kTotal>(sh, step & 1, a.ranks, r, warp, Run{exp2_of(sum), h}, events && ev.starts, carry, total, total_fresh);
+        h = exchange<kWarps, kTotal>(sh, step, a.ranks, r, warp, Run{exp2_of(sum), h}, events && ev.starts, carry, total, total_fresh, wait, a.ws);
         if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);     // every warp has read the stage
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
@@ -501,25 +531,28 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rec_fwd_kern
         }
     }
     if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, kStages);
+    if (a.ranks > 1) cluster_arrive();     // no block ends before the others have sent it all
     if constexpr (kTotal) {
         if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
         if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
     } else if (kVec) {
         if (lane == 0) bulk_wait_all();
     }
+    if (a.ranks > 1) cluster_wait();
 }
 
 // The same grid, tokens from the last to the first: chunks, ranks and warps in that order. The gradients take the inputs'
 // places in shared memory.
 template <typename T, bool kTotal> constexpr int kBwdStages = sizeof(T) == 2 ? 2 : 1;
+constexpr int kBwdTok = 8, kBwdThreads = kBlock / kBwdTok * 32;
 template <typename T, bool kVec, bool kTotal>
-__global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
     Shares& sh = *reinterpret_cast<Shares*>(smem);
     Ahead& ahead = *reinterpret_cast<Ahead*>(smem + kSharesBytes);      // the states' way, forwards
-    constexpr int kTensors = kTotal ? 2 : 4, kStages = kBwdStages<T, kTotal>;
+    constexpr int kTensors = kTotal ? 2 : 4, kStages = kBwdStages<T, kTotal>, kTok = kBwdTok, kWarps = kBlock / kTok;
     T* const tiles = reinterpret_cast<T*>(smem + kSharesBytes + kAheadBytes);       // kStages of g, dy, x, i
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);   // counted from the last chunk
@@ -538,10 +571,14 @@ __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_const
             tma_load_3d(to + 3 * kTile, &maps.i, (int)c0, t0, 0, bar);
         }
     };
-    if (kVec && threadIdx.x == 0) {
-        for (int st = 0; st < kStages; ++st) mbar_init(&sh.full[st], 1);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&sh.full[k], 1);
+            mbar_init(&sh.sent[k], 1);
+        }
         fence_mbar_init();
-        for (int st = 0; st < kStages; ++st) load(st);
+        if constexpr (kVec)
+            for (int st = 0; st < kStages; ++st) load(st);
     }
     if (a.ranks > 1) cluster_arrive();
     const f32x2 lam = two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), lam2 = mul2(lam, both(-kLog2e));
@@ -550,11 +587,11 @@ __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_const
     bool total_fresh = false;
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
-        pass_empty<kVec>(a, a.dh0, a.dhT, c);
+        pass_empty<kWarps, kVec>(a, a.dh0, a.dhT, c);
     }
     if (a.ranks > 1) cluster_wait();
     __syncthreads();
-    Events ev;
+    Events<kTok> ev;
     Waits wait;
     f32x2 acc = 0;
     for (int step = 0; step < steps; ++step) {
@@ -569,14 +606,14 @@ __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_const
             if constexpr (kVec) {
                 wait.full(&sh.full[step % kStages], step / kStages & 1, a.ws);
             } else {
-                load_own(gs, a.g, a.sg, t0, left, c, a.D);
-                load_own(dys, a.dy, a.sy, t0, left, c, a.D);
+                load_own<kTok>(gs, a.g, a.sg, t0, left, c, a.D);
+                load_own<kTok>(dys, a.dy, a.sy, t0, left, c, a.D);
                 if constexpr (!kTotal) {
-                    load_own(xs, a.x, a.sx, t0, left, c, a.D);
-                    load_own(is, a.i, a.si, t0, left, c, a.D);
+                    load_own<kTok>(xs, a.x, a.sx, t0, left, c, a.D);
+                    load_own<kTok>(is, a.i, a.si, t0, left, c, a.D);
                 }
             }
-            if (left < kTok) close_rows(gs, left);
+            if (left < kTok) close_rows<kTok>(gs, left);
             auto sums = [&](auto with) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
@@ -614,13 +651,13 @@ __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_const
             }
             h = some ? load_state<kVec>(a.kept, chunk, c, a.D) : 0;
         }
-        G = exchange<kTotal>(sh, step & 1, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends, carry, total, total_fresh);
+        G = exchange<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends, carry, total, total_fresh, wait, a.ws);
         if constexpr (kTotal) {
             if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);
         } else {
             if (kVec && kStages == 2 && threadIdx.x == 0 && !wait.lost && step > 0) load(step + 1);    // into the other stage, which all have left
             if (left > 0) {
-                h = through(ahead.warp[step & 1], *reinterpret_cast<const uint64_t*>(ahead.fresh[step & 1]), 0, warp, h);
+                h = through(ahead.warp[step & 1], bits_of<kWarps>(ahead.fresh[step & 1]), 0, warp, h);
                 f32x2 before[kTok];
                 auto grads = [&](auto with) {
 #pragma unroll
@@ -679,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_const
         }
     }
     if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, kStages);
+    if (a.ranks > 1) cluster_arrive();     // no block ends before the others have sent it all
     if constexpr (kTotal) {
         if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
         if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
@@ -698,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_bwd_kernel(const __grid_const
         }
         if (kVec && lane == 0) bulk_wait_all();
     }
+    if (a.ranks > 1) cluster_wait();
 }
 
 // dA_log from the blocks' shares, in their order: 32 columns by 8 threads
@@ -858,14 +897,14 @@ kda_status allow_shared(const char* where) {
     return KDA_OK;
 }
 
-void launch_clusters(Kernel f, const Plan& p, int segs, size_t smem, cudaStream_t s, const RecArgs& a, const Maps& m) {
+void launch_clusters(Kernel f, int threads, const Plan& p, int segs, size_t smem, cudaStream_t s, const RecArgs& a, const Maps& m) {
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = (unsigned)p.ranks;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(segs * p.ranks), (unsigned)p.tiles);
-    c.blockDim = dim3(kThreads);
+    c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
     c.attrs = &at;
@@ -918,13 +957,14 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
         if (ms == KDA_OK) ms = map(&m.g, a.g, a.sg, kBlock);
         if (ms == KDA_OK) ms = map(&m.i, a.i, a.si, kBlock);
         if (kBwd && ms == KDA_OK) ms = map(&m.dy, a.dy, a.sy, kBlock);
-        if (ms == KDA_OK) ms = kBwd ? map(&m.out[0], a.dx, a.sdx, kTok) : map(&m.out[0], a.y, a.sy, kTok);
-        if (kBwd && ms == KDA_OK) ms = map(&m.out[1], a.dg, a.sdg, kTok);
-        if (kBwd && ms == KDA_OK) ms = map(&m.out[2], a.di, a.sdi, kTok);
+        if (ms == KDA_OK) ms = kBwd ? map(&m.out[0], a.dx, a.sdx, kBwdTok) : map(&m.out[0], a.y, a.sy, kFwdTok);
+        if (kBwd && ms == KDA_OK) ms = map(&m.out[1], a.dg, a.sdg, kBwdTok);
+        if (kBwd && ms == KDA_OK) ms = map(&m.out[2], a.di, a.sdi, kBwdTok);
         if (ms != KDA_OK) return ms;
     }
-    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a, m);
-    launch_clusters(pick<kBwd>(bf16, vec, false), p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a, m);
+    const int threads = kBwd ? kBwdThreads : kFwdThreads;
+    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), threads, p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a, m);
+    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a, m);
     return launched(where);
 }
 
