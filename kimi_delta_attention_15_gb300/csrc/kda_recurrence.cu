@@ -21,7 +21,6 @@ void set_last_error_text(const char* msg);
 namespace {
 constexpr int kBlock = KDA_RECURRENCE_BLOCK;
 constexpr int kCh = 64;              // channels of a block, two to a lane
-constexpr int kMostWarps = 8;
 constexpr int kMostRanks = 8;
 constexpr int kMostSegs = 64;
 constexpr int kSMs = 152;
@@ -300,15 +299,14 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t v, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(bar) : "memory");
 }
 
-struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
-    float4 warp[2][kMostWarps][32];
+template <int kWarps> struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
+    float4 warp[2][kWarps][32];
     float4 rank[2][kMostRanks][32];
-    uint8_t warp_fresh[2][kMostWarps];
+    uint8_t warp_fresh[2][8];
     uint32_t rank_fresh[2][kMostRanks];
     uint64_t full[2];    // the stages' loads
     uint64_t sent[2];    // the ranks' sums
 };
-static_assert(kMostWarps == 8 && kMostRanks == 8, "a flag for each in eight bytes");
 
 // h through the runs from `from` to `to`; fresh: a bit for each
 __device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint32_t fresh, int from, int to, f32x2 h) {
@@ -338,7 +336,7 @@ template <int kCount> __device__ __forceinline__ uint32_t bits_of(const uint8_t*
 // Two steps' sums are kept, and nobody sends a third before all have read the first: a block's sum of the step between
 // left it after that.
 template <int kWarps, bool kTotal>
-__device__ __forceinline__ f32x2 exchange(Shares& sh, int step, int ranks, int r, int w, const Run& own, bool fresh, f32x2& carry,
+__device__ __forceinline__ f32x2 exchange(Shares<kWarps>& sh, int step, int ranks, int r, int w, const Run& own, bool fresh, f32x2& carry,
                                           Run& total, bool& total_fresh, Waits& wait, uint8_t* ws) {
     const int lane = threadIdx.x & 31, parity = step & 1;
     sh.warp[parity][w][lane] = held(own);
@@ -371,7 +369,7 @@ __device__ __forceinline__ f32x2 exchange(Shares& sh, int step, int ranks, int r
         const int count = ranks > 1 ? ranks : kWarps;
         for (int k = 0; k < count; ++k) {
             const bool f = (all >> k & 1) != 0;
-            total = then(total, run_of((ranks > 1 ? sh.rank : sh.warp)[parity][k][lane]), f);
+            total = then(total, run_of((ranks > 1 ? &sh.rank[parity][0] : &sh.warp[parity][0])[k][lane]), f);
             total_fresh = total_fresh || f;
         }
         return 0;
@@ -386,11 +384,11 @@ __device__ __forceinline__ f32x2 exchange(Shares& sh, int step, int ranks, int r
     return at;
 }
 
-struct Ahead {           // what the warps' tokens do to a state, in the backward
-    float4 warp[2][kMostWarps][32];
-    uint8_t fresh[2][kMostWarps];
+template <int kWarps> struct Ahead {           // what the warps' tokens do to a state, in the backward
+    float4 warp[2][kWarps][32];
+    uint8_t fresh[2][8];
 };
-constexpr size_t kSharesBytes = (sizeof(Shares) + 127) / 128 * 128, kAheadBytes = (sizeof(Ahead) + 127) / 128 * 128;
+template <typename S> constexpr size_t kBytes = (sizeof(S) + 127) / 128 * 128;
 
 // The state that comes to segment `seg`, in the order of the scan, from what those before it did
 __device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t c) {
@@ -411,31 +409,36 @@ constexpr int kTile = kBlock * kCh;
 // tokens, its blocks the chunks of a step next to one another, a warp kTok tokens of a chunk, a lane two channels. kVec: rows
 // in whole 16-byte units, which arrive and leave by tensor copies; else every lane moves its own channels.
 // kTotal: only what the segment does to a state, for the segments after it.
-template <typename T> constexpr int kFwdStages = sizeof(T) == 2 ? 2 : 1;
 constexpr int kFwdTok = 16, kFwdThreads = kBlock / kFwdTok * 32;      // tokens of a warp
 template <typename T, bool kVec, bool kTotal>
 __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
-    Shares& sh = *reinterpret_cast<Shares*>(smem);
-    constexpr int kStages = kFwdStages<T>, kTok = kFwdTok, kWarps = kBlock / kTok;
-    T* const tiles = reinterpret_cast<T*>(smem + kSharesBytes);          // kStages of x, g, i, then y
+    constexpr int kTok = kFwdTok, kWarps = kBlock / kTok;
+    Shares<kWarps>& sh = *reinterpret_cast<Shares<kWarps>*>(smem);
+    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps>>);          // x, g, i, then y
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;      // the warp's, as the compiler may know
     const int own_at = warp * kTok * kCh + 2 * lane;
-    T* const out = tiles + kStages * 3 * kTile;
+    T* const out = tiles + 3 * kTile;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);
     const int steps = (last - first + a.ranks - 1) / a.ranks;
     auto load = [&](int step) {          // by one thread
         const int chunk = first + step * a.ranks + r;
-        if (step >= steps || chunk >= last) return;
-        const int st = step % kStages;
-        T* const to = tiles + st * 3 * kTile;
-        uint64_t* const bar = &sh.full[st];
-        mbar_arrive_expect_tx(bar, 3 * kTile * sizeof(T));
-        tma_load_3d(to, &maps.x, (int)c0, chunk * kBlock, 0, bar);
-        tma_load_3d(to + kTile, &maps.g, (int)c0, chunk * kBlock, 0, bar);
-        tma_load_3d(to + 2 * kTile, &maps.i, (int)c0, chunk * kBlock, 0, bar);
+        if (chunk < last) {
+            mbar_arrive_expect_tx(&sh.full[0], 3 * kTile * sizeof(T));
+            tma_load_3d(tiles, &maps.x, (int)c0, chunk * kBlock, 0, &sh.full[0]);
+            tma_load_3d(tiles + kTile, &maps.g, (int)c0, chunk * kBlock, 0, &sh.full[0]);
+            tma_load_3d(tiles + 2 * kTile, &maps.i, (int)c0, chunk * kBlock, 0, &sh.full[0]);
+        }
+    };
+    auto fetch = [&](int step) {         // into L2, ahead of load
+        const int chunk = first + step * a.ranks + r;
+        if (chunk < last) {
+            tma_prefetch_3d(&maps.x, (int)c0, chunk * kBlock, 0);
+            tma_prefetch_3d(&maps.g, (int)c0, chunk * kBlock, 0);
+            tma_prefetch_3d(&maps.i, (int)c0, chunk * kBlock, 0);
+        }
     };
     if (threadIdx.x == 0) {
         for (int k = 0; k < 2; ++k) {
@@ -443,11 +446,12 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
             mbar_init(&sh.sent[k], 1);
         }
         fence_mbar_init();
-        if constexpr (kVec)
-            for (int st = 0; st < kStages; ++st) load(st);
+        if constexpr (kVec) load(0);
     }
     if (a.ranks > 1) cluster_arrive();
     const f32x2 lam2 = mul2(two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), both(-kLog2e));
+    if constexpr (kTotal) grid_launch_next();
+    else grid_wait_before();           // the pass that found what segments do, where there is one
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
     Run total{both(1.0f), 0};
     bool total_fresh = false;
@@ -464,12 +468,13 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
         const bool some = chunk < last;
         const int t0 = chunk * kBlock + warp * kTok, left = some ? min(a.total - t0, kTok) : 0;   // tokens of the warp
         const bool events = ev.find(a, some ? t0 : a.total);
-        const T *const xs = tiles + (step % kStages) * 3 * kTile + own_at, *const is = xs + 2 * kTile;
+        const T *const xs = tiles + own_at, *const is = xs + 2 * kTile;
         T* const gs = const_cast<T*>(xs) + kTile;
+        if (kVec && threadIdx.x == 0) fetch(step + 1);
         f32x2 n[kTok], b[kTok], h = 0, sum = 0;
         if (some) {
             if constexpr (kVec) {
-                wait.full(&sh.full[step % kStages], step / kStages & 1, a.ws);
+                wait.full(&sh.full[0], step & 1, a.ws);
             } else {
                 load_own<kTok>(const_cast<T*>(xs), a.x, a.sx, t0, left, c, a.D);
                 load_own<kTok>(gs, a.g, a.sg, t0, left, c, a.D);
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
             else gates(std::false_type());
         }
         h = exchange<kWarps, kTotal>(sh, step, a.ranks, r, warp, Run{exp2_of(sum), h}, events && ev.starts, carry, total, total_fresh, wait, a.ws);
-        if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);     // every warp has read the stage
+        if (kVec && threadIdx.x == 0 && !wait.lost) load(step + 1);     // every warp has read this step's
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
             if (left > 0) {
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
             }
         }
     }
-    if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, kStages);
+    if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, 1);
     if (a.ranks > 1) cluster_arrive();     // no block ends before the others have sent it all
     if constexpr (kTotal) {
         if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
@@ -548,10 +553,10 @@ constexpr int kBwdTok = 8, kBwdThreads = kBlock / kBwdTok * 32;
 template <typename T, bool kVec, bool kTotal>
 __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
-    Shares& sh = *reinterpret_cast<Shares*>(smem);
-    Ahead& ahead = *reinterpret_cast<Ahead*>(smem + kSharesBytes);      // the states' way, forwards
     constexpr int kTensors = kTotal ? 2 : 4, kStages = kBwdStages<T, kTotal>, kTok = kBwdTok, kWarps = kBlock / kTok;
-    T* const tiles = reinterpret_cast<T*>(smem + kSharesBytes + kAheadBytes);       // kStages of g, dy, x, i
+    Shares<kWarps>& sh = *reinterpret_cast<Shares<kWarps>*>(smem);
+    Ahead<kWarps>& ahead = *reinterpret_cast<Ahead<kWarps>*>(smem + kBytes<Shares<kWarps>>);      // the states' way, forwards
+    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps>> + kBytes<Ahead<kWarps>>);       // kStages of g, dy, x, i
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
@@ -582,6 +587,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     }
     if (a.ranks > 1) cluster_arrive();
     const f32x2 lam = two(c < a.D ? rate(a.A_log[c]) : 0.0f, c + 1 < a.D ? rate(a.A_log[c + 1]) : 0.0f), lam2 = mul2(lam, both(-kLog2e));
+    if constexpr (kTotal) grid_launch_next();
+    else grid_wait_before();           // the pass that found what segments do, where there is one
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
     Run total{both(1.0f), 0};
     bool total_fresh = false;
@@ -811,25 +818,49 @@ kda_status check_shape(const kda_recurrence_shape* sh, bool packed) {
 
 // How the tokens are cut: clusters of `ranks` blocks for each tile of channels, each over one of `segs` segments.
 // Blocks of a cluster take chunks next to one another and exchange what they did over distributed shared memory,
-// one pass over the data; only where the channels are too few to fill the GPU with clusters of eight are there
-// segments, which read the inputs of a scan twice (once to find what each does to a state).
+// one pass over the data; where the channels are too few to fill the GPU with clusters of eight, segments may, which
+// read the inputs of a scan twice (once to find what each does to a state).
 struct Plan {
     int tiles, chunks, ranks, segs, seg_chunks;
 };
+// A step of m blocks on an SM takes about (m = 1) + (m - 1) more + the exchange, in us, as fitted to measured times
+// (T = 8192, D = 12288 bf16 forward: 1, 2, 3, 4 ranks 249, 189, 161, 190 us, by this 276, 198, 165, 215; D = 1024 with 8
+// ranks and 1, 2, 4 segments 51, 53, 40 us, by this 47, 57, 41).
+struct Cost {
+    float step, more, rank, passes;      // passes: what two of them take, in times of one
+    int per_sm;
+};
+float wave(const Cost& c, int64_t blocks, int ranks) {
+    const int64_t full = (int64_t)kSMs * c.per_sm, rest = blocks % full, m = (rest + kSMs - 1) / kSMs;
+    const float one = c.step + (ranks > 1 ? 0.5f + c.rank * (float)(ranks - 1) : 0.0f);
+    return (float)(blocks / full) * (one + c.more * (c.per_sm - 1)) + (m ? one + c.more * (float)(m - 1) : 0.0f);
+}
 Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
+    const bool bf16 = sh->dtype == KDA_BF16;
+    const Cost cost = backward ? (bf16 ? Cost{2.55f, 1.2f, 0.2f, 1.45f, 2} : Cost{3.75f, 1.2f, 0.2f, 1.45f, 2})
+                               : (bf16 ? Cost{1.6f, 0.55f, 0.06f, 2.0f, 4} : Cost{1.7f, 0.9f, 0.06f, 2.0f, 2});
+    constexpr float kPass = 5.0f;
     Plan p;
-    const int64_t slots = (int64_t)kSMs * (backward || sh->dtype == KDA_FP32 ? 2 : 3);
     p.tiles = (int)((sh->D + kCh - 1) / kCh);
     p.chunks = (int)((sh->B * sh->T + kBlock - 1) / kBlock);
-    p.ranks = 1;
-    while (p.ranks < kMostRanks && 2 * p.ranks * p.tiles <= slots && 2 * p.ranks <= p.chunks) p.ranks *= 2;
+    p.ranks = p.segs = 1;
+    float least = 0.0f;
+    for (int r = 1; r <= kMostRanks && r <= (p.chunks > 1 ? p.chunks : 1); ++r) {
+        const int steps = (p.chunks + r - 1) / r;
+        const float t = kPass + (float)steps * wave(cost, (int64_t)p.tiles * r, r);
+        if (r == 1 || t < least) { least = t; p.ranks = r; }
+    }
+    const int64_t slots = (int64_t)kSMs * cost.per_sm, clusters = (int64_t)p.tiles * kMostRanks;
+    for (const int s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+        const int steps = (p.chunks + s * kMostRanks - 1) / (s * kMostRanks);
+        if (s * clusters > slots || steps < 2) break;
+        const float t = cost.passes * (kPass + (float)steps * wave(cost, clusters * s, kMostRanks));
+        if (t < least) { least = t; p.ranks = kMostRanks; p.segs = s; }
+    }
     const int steps = (p.chunks + p.ranks - 1) / p.ranks;
-    int64_t segs = slots / ((int64_t)p.tiles * p.ranks);
-    if (segs > steps / 4) segs = steps / 4;
-    if (segs > kMostSegs) segs = kMostSegs;
-    if (segs < 2) segs = 1;
-    p.seg_chunks = (int)((steps + segs - 1) / segs) * p.ranks;
+    p.seg_chunks = (steps + p.segs - 1) / p.segs * p.ranks;
     p.segs = p.chunks ? (p.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
+    if (p.chunks == 0) p.seg_chunks = 1;
     return p;
 }
 size_t seg_bytes(const Plan& p, int64_t D) {
@@ -874,9 +905,10 @@ template <bool kBwd> Kernel pick(bool bf16, bool vec, bool total) {
 }
 
 constexpr size_t smem_of(bool backward, size_t element, bool total) {
-    const size_t tile = kTile * element, stages = element == 2 ? 2 : 1;
-    if (!backward) return kSharesBytes + (3 * stages + 1) * tile;
-    return kSharesBytes + kAheadBytes + (total ? 2 : 4) * stages * tile;
+    const size_t tile = kTile * element;
+    constexpr int fwd = kBlock / kFwdTok, bwd = kBlock / kBwdTok;
+    if (!backward) return kBytes<Shares<fwd>> + 4 * tile;
+    return kBytes<Shares<bwd>> + kBytes<Ahead<bwd>> + (total ? 2 : 4) * (element == 2 ? 2 : 1) * tile;
 }
 
 // The kernels' limits on shared memory are set once for each device.
@@ -897,18 +929,27 @@ kda_status allow_shared(const char* where) {
     return KDA_OK;
 }
 
-void launch_clusters(Kernel f, int threads, const Plan& p, int segs, size_t smem, cudaStream_t s, const RecArgs& a, const Maps& m) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)p.ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+void launch_clusters(Kernel f, int threads, const Plan& p, int segs, size_t smem, bool overlap, cudaStream_t s, const RecArgs& a, const Maps& m) {
+    cudaLaunchAttribute at[2] = {};
+    int n = 0;
+    if (p.ranks > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = (unsigned)p.ranks;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (overlap) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(segs * p.ranks), (unsigned)p.tiles);
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
-    c.attrs = &at;
-    c.numAttrs = p.ranks > 1 ? 1 : 0;
+    c.attrs = at;
+    c.numAttrs = (unsigned)n;
     cudaLaunchKernelEx(&c, f, a, m);   // an error is left for cudaGetLastError
 }
 
@@ -963,8 +1004,8 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
         if (ms != KDA_OK) return ms;
     }
     const int threads = kBwd ? kBwdThreads : kFwdThreads;
-    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), threads, p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), s, a, m);
-    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), s, a, m);
+    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), threads, p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), false, s, a, m);
+    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), p.segs > 1, s, a, m);
     return launched(where);
 }
 
