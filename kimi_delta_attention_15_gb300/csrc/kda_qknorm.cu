@@ -1,12 +1,15 @@
 // Norm of queries and keys by heads with the position rotation in the same pass, forward and backward.
 //   r = 1 / sqrt(mean(x^2) + eps),  z = x r w,  y = z turned by position * inv_freq in pairs
 //   gz = dy turned back,  dw = sum gz x r,  dx = r (gz w - x r^2 mean(gz w x))
-// A few operations per byte: HBM is the floor. A lane holds 8 columns of a row in registers, the two sides of four
-// pairs, so that a rotation needs no exchange: columns 4 p .. 4 p + 3 and rotary/2 + 4 p .. of unit p where pairs are half of
-// the rotated columns apart, 8 p .. 8 p + 7 elsewhere; only the row's sums go through shuffles. A warp takes a
-// token (or a share of its heads, where tokens are few), so that sines and cosines are computed once for many heads.
+// A few operations per byte: HBM is the floor. Every warp keeps a ring of blocks of rows (heads of one token, side by
+// side in memory) on their way to shared memory by bulk copies, so that loads never wait for the arithmetic. A lane
+// takes 8 columns of a row, the two sides of four pairs, so that a rotation needs no exchange: columns 4 p .. 4 p + 3
+// and rotary/2 + 4 p .. of unit p where pairs are half of the rotated columns apart, 8 p .. 8 p + 7 elsewhere; only the
+// row's sums go through shuffles. A warp takes a token (or a share of its heads, where tokens are few), so that sines and
+// cosines are computed once for many heads.
 // An angle is a fraction of a turn in 64-bit fixed point: inv_freq / 2 pi comes from its 24 bits and a 128-bit
 // constant, and position times that, modulo 2^64, is exact at any position.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include "kda_internal.cuh"
@@ -19,8 +22,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSMs = 152;
-constexpr int kRows = 4;         // rows of a lane in flight
-constexpr int kBlocksPerSM = 4;
+constexpr int kRing = 8192;      // bytes of a warp's ring
+template <bool kBwd> constexpr int kBlocksPerSM = kBwd ? 2 : 3;
+// rows of a lane in a block, blocks in a ring: 8 columns of 32 lanes each, of x and, backwards, dy
+template <bool kBwd> constexpr int kRows = kBwd ? 2 : 4;
+template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
+constexpr int kZeros = 32;       // bytes of zeros that lanes without columns read
 
 // inv_freq / 2 pi as a 64-bit fraction of a turn, truncated at 2^-64: the significand times 1 / 2 pi in 128 bits, shifted
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
@@ -39,25 +46,56 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
     return bits >> 31 ? 0 - r : r;
 }
 
-// four consecutive columns
-__device__ __forceinline__ void load4(const uint16_t* p, float* v) {
-    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(p));
-    v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
-    v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
+// A lane's 8 columns as four pairs, two to a register: a the first of each, b the second
+struct Pairs {
+    f32x2 a[2], b[2];
+};
+// columns 0 .. 3 at p and 0 .. 3 at q
+template <bool kInterleaved> __device__ __forceinline__ Pairs load(const uint16_t* p, const uint16_t* q) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p), v = *reinterpret_cast<const uint2*>(q);
+    constexpr uint32_t kHigh = 0xffff0000u;
+    if constexpr (kInterleaved)
+        return {{two(u.x << 16, u.y << 16), two(v.x << 16, v.y << 16)}, {two(u.x & kHigh, u.y & kHigh), two(v.x & kHigh, v.y & kHigh)}};
+    else
+        return {{two(u.x << 16, u.x & kHigh), two(u.y << 16, u.y & kHigh)}, {two(v.x << 16, v.x & kHigh), two(v.y << 16, v.y & kHigh)}};
 }
-__device__ __forceinline__ void load4(const float* p, float* v) {
-    const float4 w = __ldcs(reinterpret_cast<const float4*>(p));
-    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+template <bool kInterleaved> __device__ __forceinline__ Pairs load(const float* p, const float* q) {
+    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(q);
+    if constexpr (kInterleaved) return {{two(u.x, u.z), two(v.x, v.z)}, {two(u.y, u.w), two(v.y, v.w)}};
+    else return {{two(u.x, u.y), two(u.z, u.w)}, {two(v.x, v.y), two(v.z, v.w)}};
 }
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
-    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack(v[0], v[1]), pack(v[2], v[3])));
+template <bool kInterleaved> __device__ __forceinline__ void columns(const Pairs& v, float4& u, float4& w) {
+    const float2 a0 = parts(v.a[0]), a1 = parts(v.a[1]), b0 = parts(v.b[0]), b1 = parts(v.b[1]);
+    u = kInterleaved ? make_float4(a0.x, b0.x, a0.y, b0.y) : make_float4(a0.x, a0.y, a1.x, a1.y);
+    w = kInterleaved ? make_float4(a1.x, b1.x, a1.y, b1.y) : make_float4(b0.x, b0.y, b1.x, b1.y);
 }
-__device__ __forceinline__ void store4(float* p, const float* v) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+template <bool kInterleaved> __device__ __forceinline__ void store(uint16_t* p, uint16_t* q, const Pairs& v) {
+    float4 u, w;
+    columns<kInterleaved>(v, u, w);
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack(u.x, u.y), pack(u.z, u.w)));
+    __stcs(reinterpret_cast<uint2*>(q), make_uint2(pack(w.x, w.y), pack(w.z, w.w)));
+}
+template <bool kInterleaved> __device__ __forceinline__ void store(float* p, float* q, const Pairs& v) {
+    float4 u, w;
+    columns<kInterleaved>(v, u, w);
+    __stcs(reinterpret_cast<float4*>(p), u);
+    __stcs(reinterpret_cast<float4*>(q), w);
+}
+__device__ __forceinline__ f32x2 both(float x) { return two(x, x); }
+__device__ __forceinline__ f32x2 minus(f32x2 x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float sum_of(f32x2 x) { const float2 p = parts(x); return p.x + p.y; }
+__device__ __forceinline__ f32x2 dot(const Pairs& x, const Pairs& y) {
+    return add2(fma2(x.a[0], y.a[0], mul2(x.a[1], y.a[1])), fma2(x.b[0], y.b[0], mul2(x.b[1], y.b[1])));
+}
+__device__ __forceinline__ Pairs times(const Pairs& x, const Pairs& y) {
+    return {{mul2(x.a[0], y.a[0]), mul2(x.a[1], y.a[1])}, {mul2(x.b[0], y.b[0]), mul2(x.b[1], y.b[1])}};
+}
+__device__ __forceinline__ Pairs times(const Pairs& x, f32x2 y) {
+    return {{mul2(x.a[0], y), mul2(x.a[1], y)}, {mul2(x.b[0], y), mul2(x.b[1], y)}};
 }
 
 struct Side {            // q or k
@@ -65,7 +103,7 @@ struct Side {            // q or k
     void* out;           // y, or dx in the backward
     const float* w;
     int64_t sx, sdy, sout;
-    int heads, blocks;   // blocks of kRows rows of each group of lanes
+    int heads, blocks;
 };
 struct QkArgs {
     Side side[2];
@@ -73,14 +111,14 @@ struct QkArgs {
     const float* inv_freq;
     float* part;         // [blocks of the grid][2][head] sums of the weights' gradients, or NULL
     int64_t tokens;
-    int head, rotary, lanes, splits;   // lanes: of a row, a power of two
+    int head, rotary, lanes, share, shares;   // lanes of a row, a power of two; blocks to a share of a token, shares to a token
     float eps, inv_head;
 };
 
 // What a lane keeps between tokens
 struct Lane {
     int unit, group, groups, c1, c2;
-    bool on, turned;
+    bool on;
     uint64_t f[4];
     __device__ __forceinline__ Lane(const QkArgs& a, bool interleaved) {
         const int lane = threadIdx.x & 31;
@@ -88,171 +126,229 @@ struct Lane {
         group = lane / a.lanes;
         groups = 32 / a.lanes;
         on = 8 * unit < a.head;
-        turned = 8 * unit < a.rotary;
-        const bool half = turned && !interleaved;
+        const bool turned = 8 * unit < a.rotary, half = turned && !interleaved;
         c1 = half ? 4 * unit : 8 * unit;
         c2 = half ? a.rotary / 2 + 4 * unit : 8 * unit + 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = turned ? turn_fraction(a.inv_freq[4 * unit + j]) : 0;
     }
-    __device__ __forceinline__ void weights(const float* w, float* v) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = w && on ? w[c1 + j] : 1.0f;
-            v[4 + j] = w && on ? w[c2 + j] : 1.0f;
-        }
+    template <bool kInterleaved> __device__ __forceinline__ Pairs weights(const float* w) const {
+        if (!w || !on) return {{both(1.0f), both(1.0f)}, {both(1.0f), both(1.0f)}};
+        return load<kInterleaved>(w + c1, w + c2);
     }
-    __device__ __forceinline__ void angles(int64_t position, float* cs, float* sn) const {
+    __device__ __forceinline__ void angles(int64_t position, f32x2* cs, f32x2* sn) const {
+        float c[4], s[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int32_t top = (int32_t)((f[j] * (uint64_t)position) >> 32);   // of a turn, from -1/2 to 1/2
-            sincospif((float)top * 0x1p-31f, &sn[j], &cs[j]);
+            sincospif((float)top * 0x1p-31f, &s[j], &c[j]);
         }
+        cs[0] = two(c[0], c[1]); cs[1] = two(c[2], c[3]);
+        sn[0] = two(s[0], s[1]); sn[1] = two(s[2], s[3]);
     }
 };
 
-template <bool kInterleaved> __device__ __forceinline__ void turn(float* v, const float* cs, const float* sn) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float &a = v[kInterleaved ? 2 * j : j], &b = v[kInterleaved ? 2 * j + 1 : 4 + j];
-        const float x = a * cs[j] - b * sn[j];
-        b = b * cs[j] + a * sn[j];
-        a = x;
+// A warp's blocks in turn: shares of tokens, it, it + step, .., and the blocks of each
+struct Walk {
+    int64_t it, t;
+    int b, end;
+    __device__ __forceinline__ void start(const QkArgs& a, int64_t item) {
+        it = item;
+        if (a.shares == 1) {
+            t = it;
+            b = 0;
+        } else {
+            t = it / a.shares;
+            b = (int)(it - t * a.shares) * a.share;
+        }
+        end = min(b + a.share, a.side[0].blocks + a.side[1].blocks);
     }
-}
+    __device__ __forceinline__ bool next(const QkArgs& a, int64_t step) {      // whether another share begins
+        if (++b < end) return false;
+        start(a, it + step);
+        return true;
+    }
+};
 
-template <typename T, bool kInterleaved> __global__ void __launch_bounds__(kThreads) qknorm_fwd_kernel(const QkArgs a) {
-    const Lane l(a, kInterleaved);
-    float w[2][8];
-    l.weights(a.side[0].w, w[0]);
-    l.weights(a.side[1].w, w[1]);
-    const int64_t items = a.tokens * a.splits, step = (int64_t)gridDim.x * kWarps;
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-        const int64_t t = it / a.splits;
-        float cs[4], sn[4];
-        l.angles(a.rotary ? a.positions[t] : 0, cs, sn);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const Side& s = a.side[k];
-            const int first = (int)(it % a.splits) - (k ? a.side[0].blocks : 0);
-            for (int b = first < 0 ? first + (-first + a.splits - 1) / a.splits * a.splits : first; b < s.blocks; b += a.splits) {
-                float v[kRows][8];
-                const int h0 = b * kRows * l.groups + l.group;
-                const T* x = static_cast<const T*>(s.x) + t * s.sx;
-                T* y = static_cast<T*>(s.out) + t * s.sout;
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    const int h = h0 + i * l.groups;
-                    if (l.on && h < s.heads) {
-                        load4(x + h * a.head + l.c1, v[i]);
-                        load4(x + h * a.head + l.c2, v[i] + 4);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    float ss = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
-                    for (int o = a.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float r = rsqrtf(ss * a.inv_head + a.eps);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] *= r * w[k][j];
-                    turn<kInterleaved>(v[i], cs, sn);
-                    const int h = h0 + i * l.groups;
-                    if (l.on && h < s.heads) {
-                        store4(y + h * a.head + l.c1, v[i]);
-                        store4(y + h * a.head + l.c2, v[i] + 4);
-                    }
-                }
-            }
-        }
+template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bounds__(kThreads, kBlocksPerSM<kBwd>) qknorm_kernel(const QkArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kN = kStages<T>, kR = kRows<kBwd>, kStage = kRing / kN, kHalf = kStage / 2;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    uint8_t* const ring = smem + warp * kRing;
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kWarps * kRing) + warp * kN;
+    const T* const zeros = reinterpret_cast<const T*>(smem + kWarps * kRing + kWarps * kN * sizeof(uint64_t));
+    const int rows = kR * (32 / a.lanes);            // of a block
+    const int64_t items = a.tokens * a.shares, step = (int64_t)gridDim.x * kWarps, mine = (int64_t)blockIdx.x * kWarps + warp;
+    Walk ahead;
+    ahead.start(a, mine);
+    auto fetch = [&](int stage) {        // by one lane: the block that `ahead` stands at
+        const int k = ahead.b >= a.side[0].blocks, b = ahead.b - (k ? a.side[0].blocks : 0);
+        const Side& s = a.side[k];
+        const int count = min(rows, s.heads - b * rows);
+        const uint32_t bytes = (uint32_t)(count * a.head) * sizeof(T);
+        const int64_t at = (int64_t)b * rows * a.head;
+        uint8_t* const to = ring + stage * kStage;
+        mbar_arrive_expect_tx(&bars[stage], kBwd ? 2 * bytes : bytes);
+        bulk_g2s(to, static_cast<const T*>(s.x) + ahead.t * s.sx + at, bytes, &bars[stage]);
+        if constexpr (kBwd) bulk_g2s(to + kHalf, static_cast<const T*>(s.dy) + ahead.t * s.sdy + at, bytes, &bars[stage]);
+    };
+    if (threadIdx.x < kZeros / 4) reinterpret_cast<uint32_t*>(const_cast<T*>(zeros))[threadIdx.x] = 0;
+    if (lane == 0) {
+        for (int st = 0; st < kN; ++st) mbar_init(&bars[st], 1);
+        fence_mbar_init();
     }
-}
-
-template <typename T, bool kInterleaved> __global__ void __launch_bounds__(kThreads) qknorm_bwd_kernel(const QkArgs a) {
-    const Lane l(a, kInterleaved);
-    float w[2][8], dw[2][8];
-    l.weights(a.side[0].w, w[0]);
-    l.weights(a.side[1].w, w[1]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.0f;
-    const int64_t items = a.tokens * a.splits, step = (int64_t)gridDim.x * kWarps;
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-        const int64_t t = it / a.splits;
-        float cs[4], sn[4];
-        l.angles(a.rotary ? -a.positions[t] : 0, cs, sn);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const Side& s = a.side[k];
-            const int first = (int)(it % a.splits) - (k ? a.side[0].blocks : 0);
-            for (int b = first < 0 ? first + (-first + a.splits - 1) / a.splits * a.splits : first; b < s.blocks; b += a.splits) {
-                const int h0 = b * kRows * l.groups + l.group;
-                const T* x = static_cast<const T*>(s.x) + t * s.sx;
-                const T* dy = static_cast<const T*>(s.dy) + t * s.sdy;
-                T* dx = static_cast<T*>(s.out) + t * s.sout;
-                float v[kRows][8], g[kRows][8];
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    const int h = h0 + i * l.groups;
-                    if (l.on && h < s.heads) {
-                        load4(x + h * a.head + l.c1, v[i]);
-                        load4(x + h * a.head + l.c2, v[i] + 4);
-                        load4(dy + h * a.head + l.c1, g[i]);
-                        load4(dy + h * a.head + l.c2, g[i] + 4);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[i][j] = g[i][j] = 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    turn<kInterleaved>(g[i], cs, sn);
-                    float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ss += v[i][j] * v[i][j];
-                        dot += g[i][j] * w[k][j] * v[i][j];
-                    }
-                    for (int o = a.lanes >> 1; o > 0; o >>= 1) {
-                        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                    }
-                    const float r = rsqrtf(ss * a.inv_head + a.eps), m = dot * a.inv_head * r * r;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        dw[k][j] += g[i][j] * (v[i][j] * r);
-                        g[i][j] = r * (g[i][j] * w[k][j] - v[i][j] * m);
-                    }
-                    const int h = h0 + i * l.groups;
-                    if (l.on && h < s.heads) {
-                        store4(dx + h * a.head + l.c1, g[i]);
-                        store4(dx + h * a.head + l.c2, g[i] + 4);
-                    }
-                }
-            }
-        }
+    for (int st = 0; st < kN && ahead.it < items; ++st) {
+        if (lane == 0) fetch(st);
+        ahead.next(a, step);
     }
-    if (!a.part) return;
-    grid_launch_next();
-    // a block's sums: the groups of a warp, then the warps in turn
-    __shared__ float sums[kWarps][2][256];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            for (int o = 16; o >= a.lanes; o >>= 1) dw[k][j] += __shfl_xor_sync(0xffffffffu, dw[k][j], o);
-            if (l.group == 0 && l.on) sums[threadIdx.x >> 5][k][(j < 4 ? l.c1 : l.c2) + (j & 3)] = dw[k][j];
-        }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.head; i += kThreads) {
-        const int k = i >= a.head, c = i - k * a.head;
-        float s = 0.0f;
+    const Lane l(a, kInterleaved);
+    Pairs dw = {}, other = {};       // sums of the weights' gradients, of the side at hand and of the other
+    int summed = 0;
+    Walk at;
+    at.start(a, mine);
+    int stage = 0, parity = 0;
+    bool fresh = true, lost = false;
+    int64_t position = at.it < items && a.rotary ? a.positions[at.t] : 0;
+    f32x2 cs[2], sn[2];
+    int side = -1;
+    Pairs w, p, q;       // the side's weight; forward: what a pair's two values are multiplied by for a and for b
+    while (at.it < items) {
+        if (fresh) {
+            l.angles(position, cs, sn);
+            const int64_t after = a.shares == 1 ? at.it + step : (at.it + step) / a.shares;
+            position = at.it + step < items && a.rotary ? a.positions[after] : 0;     // the next share's
+            side = -1;
+        }
+        const int k = at.b >= a.side[0].blocks;
+        const Side& s = a.side[k];
+        if (k != side) {
+            side = k;
+            if (kBwd && k != summed) {
+                const Pairs x = dw;
+                dw = other;
+                other = x;
+                summed = k;
+            }
+            w = l.weights<kInterleaved>(s.w);
+            if constexpr (!kBwd) {
 #pragma unroll
-        for (int v = 0; v < kWarps; ++v) s += sums[v][k][c];
-        a.part[((int64_t)blockIdx.x * 2 + k) * a.head + c] = s;
+                for (int j = 0; j < 2; ++j) {
+                    p.a[j] = mul2(w.a[j], cs[j]);
+                    p.b[j] = minus(mul2(w.b[j], sn[j]));
+                    q.a[j] = mul2(w.a[j], sn[j]);
+                    q.b[j] = mul2(w.b[j], cs[j]);
+                }
+            }
+        }
+        const int b = at.b - (k ? a.side[0].blocks : 0), first = b * rows + l.group;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], parity))) {
+            lost = true;
+            break;
+        }
+        const T* const from = reinterpret_cast<const T*>(ring + stage * kStage);
+        Pairs v[kR], g[kBwd ? kR : 1];
+        const int width = l.groups * a.head;
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const bool in = l.on && first + i * l.groups < s.heads;
+            const T* const row = from + l.group * a.head + i * width;
+            v[i] = load<kInterleaved>(in ? row + l.c1 : zeros, in ? row + l.c2 : zeros);
+            if constexpr (kBwd) {
+                const T* const drow = row + kHalf / (int)sizeof(T);
+                g[i] = load<kInterleaved>(in ? drow + l.c1 : zeros, in ? drow + l.c2 : zeros);
+            }
+        }
+        __syncwarp();
+        if (ahead.it < items) {
+            if (lane == 0) fetch(stage);
+            ahead.next(a, step);
+        }
+        T* out = static_cast<T*>(s.out) + at.t * s.sout + (int64_t)first * a.head;
+        float ss[kR], gx[kR];
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            ss[i] = sum_of(dot(v[i], v[i]));
+            if constexpr (kBwd) {        // turned back; times the weight in the sum
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x2 x = fma2(g[i].b[j], sn[j], mul2(g[i].a[j], cs[j]));
+                    g[i].b[j] = fma2(minus(g[i].a[j]), sn[j], mul2(g[i].b[j], cs[j]));
+                    g[i].a[j] = x;
+                }
+                gx[i] = sum_of(dot(times(g[i], w), v[i]));
+            }
+        }
+        for (int o = a.lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+                if constexpr (kBwd) gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const float r = rsqrtf(ss[i] * a.inv_head + a.eps);
+            const Pairs xr = times(v[i], both(r));
+            Pairs y;
+            if constexpr (!kBwd) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    y.a[j] = fma2(xr.b[j], p.b[j], mul2(xr.a[j], p.a[j]));
+                    y.b[j] = fma2(xr.b[j], q.b[j], mul2(xr.a[j], q.a[j]));
+                }
+            } else {
+                const f32x2 m = both(-(gx[i] * r) * a.inv_head * r), rr = both(r);
+                const Pairs gw = times(g[i], w);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    dw.a[j] = fma2(g[i].a[j], xr.a[j], dw.a[j]);
+                    dw.b[j] = fma2(g[i].b[j], xr.b[j], dw.b[j]);
+                    y.a[j] = fma2(xr.a[j], m, mul2(gw.a[j], rr));
+                    y.b[j] = fma2(xr.b[j], m, mul2(gw.b[j], rr));
+                }
+            }
+            if (l.on && first + i * l.groups < s.heads) store<kInterleaved>(out + i * width + l.c1, out + i * width + l.c2, y);
+        }
+        if (++stage == kN) {
+            stage = 0;
+            parity ^= 1;
+        }
+        fresh = at.next(a, step);
+    }
+    if (lost)            // blocks on their way when a wait gave up
+        for (int st = 0; st < kN; ++st) mbar_wait(&bars[st], st < stage ? parity ^ 1 : parity);
+    if constexpr (kBwd) {
+        if (!a.part) return;
+        grid_launch_next();
+        // a block's sums: the groups of a warp, then the warps in turn
+        __syncthreads();
+        float* const sums = reinterpret_cast<float*>(smem);      // [kWarps][2][head]
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            Pairs d = k ? other : dw;
+            for (int o = 16; o >= a.lanes; o >>= 1) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    d.a[j] = add2(d.a[j], __shfl_xor_sync(0xffffffffu, d.a[j], o));
+                    d.b[j] = add2(d.b[j], __shfl_xor_sync(0xffffffffu, d.b[j], o));
+                }
+            }
+            if (l.group == 0 && l.on) {
+                float4 u, v;
+                columns<kInterleaved>(d, u, v);
+                float* const to = sums + (warp * 2 + (k ? 1 - summed : summed)) * a.head;
+                *reinterpret_cast<float4*>(to + l.c1) = u;
+                *reinterpret_cast<float4*>(to + l.c2) = v;
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * a.head; i += kThreads) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) s += sums[v * 2 * a.head + i];
+            a.part[(int64_t)blockIdx.x * 2 * a.head + i] = s;
+        }
     }
 }
 
@@ -311,7 +407,7 @@ kda_status check_shape(const kda_qknorm_shape* sh) {
 
 int64_t or_else(int64_t stride, int64_t width) { return stride ? stride : width; }
 
-QkArgs args_of(const kda_qknorm_shape* sh) {
+QkArgs args_of(const kda_qknorm_shape* sh, bool backward) {
     QkArgs a{};
     a.tokens = sh->tokens;
     a.head = sh->head_dim;
@@ -320,19 +416,49 @@ QkArgs args_of(const kda_qknorm_shape* sh) {
     a.inv_head = 1.0f / sh->head_dim;
     a.lanes = 1;
     while (8 * a.lanes < a.head) a.lanes *= 2;
-    const int rows = kRows * (32 / a.lanes);
+    const int rows = (backward ? kRows<true> : kRows<false>) * (32 / a.lanes);
     a.side[0].heads = sh->q_heads;
     a.side[1].heads = sh->k_heads;
     for (Side& s : a.side) s.blocks = (s.heads + rows - 1) / rows;
     // a warp for each token while these fill the GPU, else several to share a token's heads
-    const int64_t want = (int64_t)kSMs * kBlocksPerSM * kWarps, most = a.side[0].blocks + a.side[1].blocks;
+    const int64_t want = (int64_t)kSMs * (backward ? kBlocksPerSM<true> : kBlocksPerSM<false>) * kWarps;
+    const int blocks = a.side[0].blocks + a.side[1].blocks;
     const int64_t n = sh->tokens ? (want + sh->tokens - 1) / sh->tokens : 1;
-    a.splits = (int)(n < most ? n : most);
+    a.share = n >= blocks ? 1 : (int)((blocks + n - 1) / n);
+    a.shares = (blocks + a.share - 1) / a.share;
     return a;
 }
-unsigned grid_of(const QkArgs& a) {
-    const int64_t blocks = (a.tokens * a.splits + kWarps - 1) / kWarps, most = (int64_t)kSMs * kBlocksPerSM;
+unsigned grid_of(const QkArgs& a, bool backward) {
+    const int64_t blocks = (a.tokens * a.shares + kWarps - 1) / kWarps;
+    const int64_t most = (int64_t)kSMs * (backward ? kBlocksPerSM<true> : kBlocksPerSM<false>);
     return (unsigned)(blocks < most ? blocks : most);
+}
+
+constexpr size_t kSmem = (size_t)kWarps * (kRing + 4 * sizeof(uint64_t)) + kZeros;
+
+using QkKernel = void (*)(QkArgs);
+template <bool kBwd> QkKernel pick(const kda_qknorm_shape* sh) {
+    if (sh->dtype == KDA_BF16) return sh->interleaved ? qknorm_kernel<uint16_t, true, kBwd> : qknorm_kernel<uint16_t, false, kBwd>;
+    return sh->interleaved ? qknorm_kernel<float, true, kBwd> : qknorm_kernel<float, false, kBwd>;
+}
+
+// The kernels' limits on shared memory are set once for each device.
+kda_status allow_shared(const char* where) {
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return launched(where);
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return KDA_OK;
+    for (int k = 0; k < 8; ++k) {
+        kda_qknorm_shape sh{};
+        sh.dtype = k & 1 ? KDA_FP32 : KDA_BF16;
+        sh.interleaved = k >> 1 & 1;
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(k & 4 ? pick<true>(&sh) : pick<false>(&sh)),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+            return launched(where);
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return KDA_OK;
 }
 }  // namespace
 }  // namespace kda
@@ -352,23 +478,23 @@ extern "C" kda_status kda_qknorm_fwd(const kda_qknorm_shape* shape, const void* 
     for (const void* p : {k, static_cast<const void*>(k_out), static_cast<const void*>(k_weight)})
         if (keys && misaligned(p)) return KDA_ERR_ALIGN;
     if (misaligned(positions, 8)) return KDA_ERR_ALIGN;
-    QkArgs a = args_of(shape);
+    QkArgs a = args_of(shape, false);
     const int64_t wq = (int64_t)shape->q_heads * shape->head_dim, wk = (int64_t)shape->k_heads * shape->head_dim;
     a.side[0] = Side{q, nullptr, q_out, q_weight, or_else(shape->q_stride, wq), 0, or_else(shape->q_out_stride, wq), a.side[0].heads, a.side[0].blocks};
     a.side[1] = Side{k, nullptr, k_out, keys ? k_weight : nullptr, or_else(shape->k_stride, wk), 0, or_else(shape->k_out_stride, wk), a.side[1].heads, a.side[1].blocks};
     a.positions = positions;
     a.inv_freq = inv_freq;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto run = shape->dtype == KDA_BF16 ? (shape->interleaved ? qknorm_fwd_kernel<uint16_t, true> : qknorm_fwd_kernel<uint16_t, false>)
-                                        : (shape->interleaved ? qknorm_fwd_kernel<float, true> : qknorm_fwd_kernel<float, false>);
-    run<<<grid_of(a), kThreads, 0, s>>>(a);
+    const kda_status as = allow_shared("kda_qknorm_fwd");
+    if (as != KDA_OK) return as;
+    pick<false>(shape)<<<grid_of(a, false), kThreads, kSmem, s>>>(a);
     return launched("kda_qknorm_fwd launch");
 }
 
 extern "C" size_t kda_qknorm_workspace_size(const kda_qknorm_shape* shape) {
     if (check_shape(shape) != KDA_OK) return 0;
-    const QkArgs a = args_of(shape);
-    return align_up((size_t)(grid_of(a) + 1) * 2 * a.head * sizeof(float), 1024);
+    const QkArgs a = args_of(shape, true);
+    return 1024 + align_up((size_t)grid_of(a, true) * 2 * a.head * sizeof(float), 1024);
 }
 
 extern "C" kda_status kda_qknorm_bwd(const kda_qknorm_shape* shape, const void* q, const void* k, const void* dq_out,
@@ -386,23 +512,24 @@ extern "C" kda_status kda_qknorm_bwd(const kda_qknorm_shape* shape, const void* 
     for (const void* p : {k, dk_out, static_cast<const void*>(dk), static_cast<const void*>(k_weight)})
         if (keys && misaligned(p)) return KDA_ERR_ALIGN;
     if (misaligned(positions, 8)) return KDA_ERR_ALIGN;
-    QkArgs a = args_of(shape);
+    QkArgs a = args_of(shape, true);
     const int64_t wq = (int64_t)shape->q_heads * shape->head_dim, wk = (int64_t)shape->k_heads * shape->head_dim;
     a.side[0] = Side{q, dq_out, dq, q_weight, or_else(shape->q_stride, wq), or_else(shape->q_out_stride, wq), or_else(shape->dq_stride, wq), a.side[0].heads, a.side[0].blocks};
     a.side[1] = Side{k, dk_out, dk, keys ? k_weight : nullptr, or_else(shape->k_stride, wk), or_else(shape->k_out_stride, wk), or_else(shape->dk_stride, wk), a.side[1].heads, a.side[1].blocks};
     a.positions = positions;
     a.inv_freq = inv_freq;
     const bool sums = dq_weight || dk_weight;
-    a.part = sums ? static_cast<float*>(workspace) : nullptr;
+    float* const part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 1024);
+    a.part = sums ? part : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = grid_of(a);
+    const unsigned grid = grid_of(a, true);
     if (grid) {
-        auto run = shape->dtype == KDA_BF16 ? (shape->interleaved ? qknorm_bwd_kernel<uint16_t, true> : qknorm_bwd_kernel<uint16_t, false>)
-                                            : (shape->interleaved ? qknorm_bwd_kernel<float, true> : qknorm_bwd_kernel<float, false>);
-        run<<<grid, kThreads, 0, s>>>(a);
+        const kda_status as = allow_shared("kda_qknorm_bwd");
+        if (as != KDA_OK) return as;
+        pick<true>(shape)<<<grid, kThreads, kSmem, s>>>(a);
     }
     if (sums)
         launch_kernel(qknorm_sum_kernel, dim3((unsigned)((a.head + 31) / 32), 2), dim3(32, 32), 0, s, grid > 0,
-                      static_cast<const float*>(workspace), (int)grid, a.head, dq_weight, dk_weight);
+                      static_cast<const float*>(part), (int)grid, a.head, dq_weight, dk_weight);
     return launched("kda_qknorm_bwd launch");
 }
