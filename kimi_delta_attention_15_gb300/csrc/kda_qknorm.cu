@@ -12,6 +12,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 #include "kda_internal.cuh"
 #include "umma_bf16.cuh"
 
@@ -148,25 +149,47 @@ struct Lane {
     }
 };
 
-// A warp's blocks in turn: shares of tokens, it, it + step, .., and the blocks of each
-struct Walk {
-    int64_t it, t;
-    int b, end;
-    __device__ __forceinline__ void start(const QkArgs& a, int64_t item) {
-        it = item;
-        if (a.shares == 1) {
-            t = it;
-            b = 0;
-        } else {
+// A warp's blocks in turn: shares of tokens, item, item + step, .., and the blocks of each. p and q are where the
+// block's rows start in two of the side's tensors (x and dy to load from, out to store to).
+template <typename T, bool kOut> struct Walk {
+    int64_t item, t;
+    int left, k, heads;      // blocks left of the share, side, heads left of the side
+    T *p, *q;
+    __device__ __forceinline__ void open(const QkArgs& a, int side, int b, int rows) {
+        const Side& s = a.side[side];
+        k = side;
+        heads = s.heads - b * rows;
+        const int64_t at = (int64_t)b * rows * a.head;
+        p = kOut ? static_cast<T*>(s.out) + t * s.sout + at : static_cast<T*>(const_cast<void*>(s.x)) + t * s.sx + at;
+        if constexpr (!kOut) q = static_cast<T*>(const_cast<void*>(s.dy)) + t * s.sdy + at;
+    }
+    __device__ __forceinline__ void start(const QkArgs& a, int64_t it, int rows) {
+        item = it;
+        t = it;
+        int b = 0;
+        if (a.shares > 1) {
             t = it / a.shares;
             b = (int)(it - t * a.shares) * a.share;
         }
-        end = min(b + a.share, a.side[0].blocks + a.side[1].blocks);
+        const int n = a.side[0].blocks;
+        left = min(a.share, n + a.side[1].blocks - b);
+        if (b < n) open(a, 0, b, rows);
+        else open(a, 1, b - n, rows);
     }
-    __device__ __forceinline__ bool next(const QkArgs& a, int64_t step) {      // whether another share begins
-        if (++b < end) return false;
-        start(a, it + step);
-        return true;
+    __device__ __forceinline__ bool next(const QkArgs& a, int64_t step, int rows) {      // whether another share begins
+        if (--left == 0) {
+            if (item + step < a.tokens * a.shares) start(a, item + step, rows);
+            else item += step;
+            return true;
+        }
+        heads -= rows;
+        if (heads > 0) {
+            p += rows * a.head;
+            q += rows * a.head;
+        } else {
+            open(a, 1, 0, rows);
+        }
+        return false;
     }
 };
 
@@ -179,58 +202,56 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
     const T* const zeros = reinterpret_cast<const T*>(smem + kWarps * kRing + kWarps * kN * sizeof(uint64_t));
     const int rows = kR * (32 / a.lanes);            // of a block
     const int64_t items = a.tokens * a.shares, step = (int64_t)gridDim.x * kWarps, mine = (int64_t)blockIdx.x * kWarps + warp;
-    Walk ahead;
-    ahead.start(a, mine);
+    Walk<T, false> ahead;
+    ahead.item = mine;
+    if (mine < items) ahead.start(a, mine, rows);
     auto fetch = [&](int stage) {        // by one lane: the block that `ahead` stands at
-        const int k = ahead.b >= a.side[0].blocks, b = ahead.b - (k ? a.side[0].blocks : 0);
-        const Side& s = a.side[k];
-        const int count = min(rows, s.heads - b * rows);
-        const uint32_t bytes = (uint32_t)(count * a.head) * sizeof(T);
-        const int64_t at = (int64_t)b * rows * a.head;
+        const uint32_t bytes = (uint32_t)(min(rows, ahead.heads) * a.head) * sizeof(T);
         uint8_t* const to = ring + stage * kStage;
         mbar_arrive_expect_tx(&bars[stage], kBwd ? 2 * bytes : bytes);
-        bulk_g2s(to, static_cast<const T*>(s.x) + ahead.t * s.sx + at, bytes, &bars[stage]);
-        if constexpr (kBwd) bulk_g2s(to + kHalf, static_cast<const T*>(s.dy) + ahead.t * s.sdy + at, bytes, &bars[stage]);
+        bulk_g2s(to, ahead.p, bytes, &bars[stage]);
+        if constexpr (kBwd) bulk_g2s(to + kHalf, ahead.q, bytes, &bars[stage]);
     };
     if (threadIdx.x < kZeros / 4) reinterpret_cast<uint32_t*>(const_cast<T*>(zeros))[threadIdx.x] = 0;
     if (lane == 0) {
         for (int st = 0; st < kN; ++st) mbar_init(&bars[st], 1);
         fence_mbar_init();
     }
-    for (int st = 0; st < kN && ahead.it < items; ++st) {
+    for (int st = 0; st < kN && ahead.item < items; ++st) {
         if (lane == 0) fetch(st);
-        ahead.next(a, step);
+        ahead.next(a, step, rows);
     }
     __syncthreads();
     const Lane l(a, kInterleaved);
     Pairs dw = {}, other = {};       // sums of the weights' gradients, of the side at hand and of the other
     int summed = 0;
-    Walk at;
-    at.start(a, mine);
+    Walk<T, true> at;
+    at.item = mine;
+    if (mine < items) at.start(a, mine, rows);
     int stage = 0, parity = 0;
     bool fresh = true, lost = false;
-    int64_t position = at.it < items && a.rotary ? a.positions[at.t] : 0;
+    int64_t position = mine < items && a.rotary ? a.positions[at.t] : 0;
     f32x2 cs[2], sn[2];
     int side = -1;
     Pairs w, p, q;       // the side's weight; forward: what a pair's two values are multiplied by for a and for b
-    while (at.it < items) {
+    const int width = l.groups * a.head, mine1 = l.group * a.head + l.c1, mine2 = l.group * a.head + l.c2;
+    const bool whole = 8 * a.lanes == a.head;
+    while (at.item < items) {
         if (fresh) {
             l.angles(position, cs, sn);
-            const int64_t after = a.shares == 1 ? at.it + step : (at.it + step) / a.shares;
-            position = at.it + step < items && a.rotary ? a.positions[after] : 0;     // the next share's
+            const int64_t after = a.shares == 1 ? at.item + step : (at.item + step) / a.shares;
+            position = at.item + step < items && a.rotary ? a.positions[after] : 0;     // the next share's
             side = -1;
         }
-        const int k = at.b >= a.side[0].blocks;
-        const Side& s = a.side[k];
-        if (k != side) {
-            side = k;
-            if (kBwd && k != summed) {
+        if (at.k != side) {
+            side = at.k;
+            if (kBwd && side != summed) {
                 const Pairs x = dw;
                 dw = other;
                 other = x;
-                summed = k;
+                summed = side;
             }
-            w = l.weights<kInterleaved>(s.w);
+            w = l.weights<kInterleaved>(a.side[side].w);
             if constexpr (!kBwd) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -241,80 +262,83 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
                 }
             }
         }
-        const int b = at.b - (k ? a.side[0].blocks : 0), first = b * rows + l.group;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], parity))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_asleep(&bars[stage], parity))) {
             lost = true;
             break;
         }
-        const T* const from = reinterpret_cast<const T*>(ring + stage * kStage);
-        Pairs v[kR], g[kBwd ? kR : 1];
-        const int width = l.groups * a.head;
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const bool in = l.on && first + i * l.groups < s.heads;
-            const T* const row = from + l.group * a.head + i * width;
-            v[i] = load<kInterleaved>(in ? row + l.c1 : zeros, in ? row + l.c2 : zeros);
-            if constexpr (kBwd) {
-                const T* const drow = row + kHalf / (int)sizeof(T);
-                g[i] = load<kInterleaved>(in ? drow + l.c1 : zeros, in ? drow + l.c2 : zeros);
-            }
-        }
-        __syncwarp();
-        if (ahead.it < items) {
-            if (lane == 0) fetch(stage);
-            ahead.next(a, step);
-        }
-        T* out = static_cast<T*>(s.out) + at.t * s.sout + (int64_t)first * a.head;
-        float ss[kR], gx[kR];
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            ss[i] = sum_of(dot(v[i], v[i]));
-            if constexpr (kBwd) {        // turned back; times the weight in the sum
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const f32x2 x = fma2(g[i].b[j], sn[j], mul2(g[i].a[j], cs[j]));
-                    g[i].b[j] = fma2(minus(g[i].a[j]), sn[j], mul2(g[i].b[j], cs[j]));
-                    g[i].a[j] = x;
-                }
-                gx[i] = sum_of(dot(times(g[i], w), v[i]));
-            }
-        }
-        for (int o = a.lanes >> 1; o > 0; o >>= 1) {
+        // kAll: every lane has columns and every row is one of the side's heads
+        auto block = [&](auto all) {
+            constexpr bool kAll = decltype(all)::value;
+            const T* const from = reinterpret_cast<const T*>(ring + stage * kStage);
+            Pairs v[kR], g[kBwd ? kR : 1];
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
-                ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
-                if constexpr (kBwd) gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const float r = rsqrtf(ss[i] * a.inv_head + a.eps);
-            const Pairs xr = times(v[i], both(r));
-            Pairs y;
-            if constexpr (!kBwd) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    y.a[j] = fma2(xr.b[j], p.b[j], mul2(xr.a[j], p.a[j]));
-                    y.b[j] = fma2(xr.b[j], q.b[j], mul2(xr.a[j], q.a[j]));
-                }
-            } else {
-                const f32x2 m = both(-(gx[i] * r) * a.inv_head * r), rr = both(r);
-                const Pairs gw = times(g[i], w);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    dw.a[j] = fma2(g[i].a[j], xr.a[j], dw.a[j]);
-                    dw.b[j] = fma2(g[i].b[j], xr.b[j], dw.b[j]);
-                    y.a[j] = fma2(xr.a[j], m, mul2(gw.a[j], rr));
-                    y.b[j] = fma2(xr.b[j], m, mul2(gw.b[j], rr));
+                const bool in = kAll || (l.on && l.group + i * l.groups < at.heads);
+                v[i] = load<kInterleaved>(in ? from + mine1 + i * width : zeros, in ? from + mine2 + i * width : zeros);
+                if constexpr (kBwd) {
+                    const T* const dfrom = from + kHalf / (int)sizeof(T);
+                    g[i] = load<kInterleaved>(in ? dfrom + mine1 + i * width : zeros, in ? dfrom + mine2 + i * width : zeros);
                 }
             }
-            if (l.on && first + i * l.groups < s.heads) store<kInterleaved>(out + i * width + l.c1, out + i * width + l.c2, y);
-        }
+            __syncwarp();
+            if (ahead.item < items) {
+                if (lane == 0) fetch(stage);
+                ahead.next(a, step, rows);
+            }
+            float ss[kR], gx[kR];
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                ss[i] = sum_of(dot(v[i], v[i]));
+                if constexpr (kBwd) {        // turned back; times the weight in the sum
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x2 x = fma2(g[i].b[j], sn[j], mul2(g[i].a[j], cs[j]));
+                        g[i].b[j] = fma2(minus(g[i].a[j]), sn[j], mul2(g[i].b[j], cs[j]));
+                        g[i].a[j] = x;
+                    }
+                    gx[i] = sum_of(dot(times(g[i], w), v[i]));
+                }
+            }
+            for (int o = a.lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+                    if constexpr (kBwd) gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
+                }
+            }
+            T *to1 = at.p + mine1, *to2 = at.p + mine2;
+#pragma unroll
+            for (int i = 0; i < kR; ++i, to1 += width, to2 += width) {
+                const float r = rsqrtf(ss[i] * a.inv_head + a.eps);
+                const Pairs xr = times(v[i], both(r));
+                Pairs y;
+                if constexpr (!kBwd) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        y.a[j] = fma2(xr.b[j], p.b[j], mul2(xr.a[j], p.a[j]));
+                        y.b[j] = fma2(xr.b[j], q.b[j], mul2(xr.a[j], q.a[j]));
+                    }
+                } else {
+                    const f32x2 m = both(-(gx[i] * r) * a.inv_head * r), rr = both(r);
+                    const Pairs gw = times(g[i], w);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        dw.a[j] = fma2(g[i].a[j], xr.a[j], dw.a[j]);
+                        dw.b[j] = fma2(g[i].b[j], xr.b[j], dw.b[j]);
+                        y.a[j] = fma2(xr.a[j], m, mul2(gw.a[j], rr));
+                        y.b[j] = fma2(xr.b[j], m, mul2(gw.b[j], rr));
+                    }
+                }
+                if (kAll || (l.on && l.group + i * l.groups < at.heads)) store<kInterleaved>(to1, to2, y);
+            }
+        };
+        if (whole && at.heads >= rows) block(std::true_type());
+        else block(std::false_type());
         if (++stage == kN) {
             stage = 0;
             parity ^= 1;
         }
-        fresh = at.next(a, step);
+        fresh = at.next(a, step, rows);
     }
     if (lost)            // blocks on their way when a wait gave up
         for (int st = 0; st < kN; ++st) mbar_wait(&bars[st], st < stage ? parity ^ 1 : parity);

@@ -179,7 +179,7 @@ struct Waits {
     bool lost = false;
     __device__ __forceinline__ void full(uint64_t* bar, int parity, uint8_t* ws) {
         if (lost) return;
-        if (!mbar_wait(bar, parity)) {
+        if (!mbar_wait_asleep(bar, parity)) {       // its polls would take issue slots from the other warps
             lost = true;
             raise_status(ws, KDA_ERR_TIMEOUT);
         }
