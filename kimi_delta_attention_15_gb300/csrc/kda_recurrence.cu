@@ -61,10 +61,8 @@ __device__ __forceinline__ float rate(float A_log) {
 // Two channels at a time, in packed arithmetic where it exists
 __device__ __forceinline__ f32x2 both(float x) { return two(x, x); }
 __device__ __forceinline__ f32x2 exp2_of(f32x2 x) { const float2 p = parts(x); return two(exp2_of(p.x), exp2_of(p.y)); }
-__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
-    const float2 d = parts(add2(exp2_of(mul2(x, both(-kLog2e))), both(1.0f)));
-    return two(inverse(d.x), inverse(d.y));
-}
+__device__ __forceinline__ f32x2 inverse(f32x2 x) { const float2 p = parts(x); return two(inverse(p.x), inverse(p.y)); }
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) { return inverse(add2(exp2_of(mul2(x, both(-kLog2e))), both(1.0f))); }
 // exp(-x), finite: times sigmoid(x) it is 1 - sigmoid(x) without cancellation
 __device__ __forceinline__ f32x2 exp_minus(f32x2 x) {
     const float2 p = parts(mul2(x, both(-kLog2e)));
@@ -608,7 +606,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
         const bool events = ev.find(a, some ? t0 : a.total);
         T* const own = tiles + (step % kStages) * kTensors * kTile + warp * kTok * kCh;
         T *const gs = own + 2 * lane, *const dys = gs + kTile, *const xs = gs + 2 * kTile, *const is = gs + 3 * kTile;
-        f32x2 s[kTok], n[kTok], si[kTok], rs[kTok], h = 0, sum = 0, G = 0;
+        f32x2 eg[kTok], ei[kTok], n[kTok], b[kTok], h = 0, sum = 0, G = 0;
         if (some) {
             if constexpr (kVec) {
                 wait.full(&sh.full[step % kStages], step / kStages & 1, a.ws);
@@ -624,18 +622,17 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
             auto sums = [&](auto with) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
-                    s[j] = sigmoid2(pair_at(gs + j * kCh));
-                    const f32x2 v = mul2(lam2, s[j]);
+                    eg[j] = exp_minus(pair_at(gs + j * kCh));
+                    const f32x2 v = mul2(lam2, inverse(add2(eg[j], both(1.0f))));
                     n[j] = minus_decayed(v);
                     sum = add2(sum, v);
                     if constexpr (!kTotal) {
-                        const f32x2 m2 = written2(n[j]);
-                        const float2 p = parts(add2(m2, both(0x1p-125f)));      // no infinity at 0
-                        rs[j] = two(inverse_root(p.x), inverse_root(p.y));
-                        si[j] = sigmoid2(pair_at(is + j * kCh));
+                        ei[j] = exp_minus(pair_at(is + j * kCh));
+                        const float2 m2 = parts(written2(n[j]));
+                        b[j] = mul2(mul2(two(root(m2.x), root(m2.y)), inverse(add2(ei[j], both(1.0f)))), pair_at(xs + j * kCh));
                         if constexpr (with.value)
                             if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                        h = advance(h, n[j], mul2(mul2(m2, rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
+                        h = advance(h, n[j], b[j]);
                     }
                 }
 #pragma unroll
@@ -672,20 +669,22 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                         if constexpr (with.value)
                             if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
                         before[j] = h;
-                        h = advance(h, n[j], mul2(mul2(written2(n[j]), rs[j]), mul2(si[j], pair_at(xs + j * kCh))));
+                        h = advance(h, n[j], b[j]);
                     }
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
                         if constexpr (with.value)
                             if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
-                        const f32x2 t = add2(G, pair_at(dys + j * kCh)), ix = mul2(si[j], pair_at(xs + j * kCh)), d = add2(n[j], both(1.0f));
-                        const f32x2 tm = mul2(t, mul2(written2(n[j]), rs[j]));
-                        const f32x2 q = fma2(before[j], both(-1.0f), mul2(mul2(rs[j], ix), d));       // i x a / m - h, times u a below
-                        const f32x2 duu = mul2(mul2(t, mul2(lam, s[j])), mul2(d, q));
+                        // i x is b / m, 0 where m is (then u is too, and t m)
+                        const f32x2 t = add2(G, pair_at(dys + j * kCh)), d = add2(n[j], both(1.0f)), m2 = written2(n[j]);
+                        const float2 p = parts(add2(m2, both(0x1p-125f)));      // no infinity at 0
+                        const f32x2 rm = two(inverse_root(p.x), inverse_root(p.y)), ix = mul2(b[j], rm), tm = mul2(t, mul2(m2, rm));
+                        const f32x2 s = inverse(add2(eg[j], both(1.0f))), si = inverse(add2(ei[j], both(1.0f)));
+                        const f32x2 q = fma2(before[j], both(-1.0f), mul2(mul2(rm, ix), d));       // i x a / m - h, times u a below
+                        const f32x2 duu = mul2(mul2(t, mul2(lam, s)), mul2(d, q));
                         acc = add2(acc, duu);
                         G = fma2(n[j], t, t);
-                        const f32x2 dx = mul2(tm, si[j]), dg = mul2(duu, mul2(exp_minus(pair_at(gs + j * kCh)), s[j])),
-                                    di = mul2(mul2(tm, ix), mul2(exp_minus(pair_at(is + j * kCh)), si[j]));
+                        const f32x2 dx = mul2(tm, si), dg = mul2(duu, mul2(eg[j], s)), di = mul2(mul2(tm, ix), mul2(ei[j], si));
                         if constexpr (kVec) {
                             put_shared(xs + j * kCh, dx);
                             put_shared(gs + j * kCh, dg);
