@@ -22,7 +22,6 @@ namespace {
 constexpr int kBlock = KDA_RECURRENCE_BLOCK;
 constexpr int kCh = 64;              // channels of a block, two to a lane
 constexpr int kMostRanks = 8;
-constexpr int kMostSegs = 64;
 constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -97,19 +96,20 @@ struct RecArgs {
 };
 
 // ---------------------------------------------------------------- two channels of a lane
-// What a run of tokens does to a state that comes to it: a h + b. Where a sequence starts in it, which is the same for all
-// channels, b alone (not 0 h + b: a state that is no number ends with its sequence).
+// What a run of tokens does to a state that comes to it: h + n h + b, n = its decay less 1, as for a single token. Where a
+// sequence starts in it, which is the same for all channels, b alone (not 0 h + b: a state that is no number ends with
+// its sequence).
 struct Run {
-    f32x2 a, b;
+    f32x2 n, b;
 };
 __device__ __forceinline__ Run run_of(const float4& s) { return {two(s.x, s.y), two(s.z, s.w)}; }
 __device__ __forceinline__ float4 held(const Run& r) {
-    const float2 a = parts(r.a), b = parts(r.b);
-    return make_float4(a.x, a.y, b.x, b.y);
+    const float2 n = parts(r.n), b = parts(r.b);
+    return make_float4(n.x, n.y, b.x, b.y);
 }
-__device__ __forceinline__ f32x2 over(const Run& r, bool fresh, f32x2 h) { return fresh ? r.b : fma2(r.a, h, r.b); }
+__device__ __forceinline__ f32x2 over(const Run& r, bool fresh, f32x2 h) { return fresh ? r.b : advance(h, r.n, r.b); }
 // first s, then t; `fresh` is t's
-__device__ __forceinline__ Run then(const Run& s, const Run& t, bool fresh) { return {fresh ? t.a : mul2(s.a, t.a), over(t, fresh, s.b)}; }
+__device__ __forceinline__ Run then(const Run& s, const Run& t, bool fresh) { return {fresh ? t.n : advance(s.n, t.n, t.n), over(t, fresh, s.b)}; }
 
 __device__ __forceinline__ f32x2 pair_at(const uint16_t* p) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
@@ -312,8 +312,7 @@ __device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint32_t fres
     if (fresh == 0) {
 #pragma unroll 4
         for (int k = from; k < to; ++k) {
-            const Run s = run_of(runs[k][lane]);
-            h = fma2(s.a, h, s.b);
+            h = over(run_of(runs[k][lane]), false, h);
         }
     } else {
         for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), (fresh >> k & 1) != 0, h);
@@ -327,39 +326,45 @@ template <int kCount> __device__ __forceinline__ uint32_t bits_of(const uint8_t*
     return (uint32_t)(v * 0x0102040810204080ull >> 56);
 }
 
-// After a step's own sums: the state (adjoint) that comes to this warp, and in `carry` the one that leaves the step.
-// Warps and ranks follow one another in the order of the scan, `w` and `r` their places in it. kTotal: only what all
-// the steps so far do, in `total`. The blocks' sums travel over distributed shared memory with their own
-// completion: a barrier of the cluster would make every thread wait for all its stores (a third of the time).
-// Two steps' sums are kept, and nobody sends a third before all have read the first: a block's sum of the step between
-// left it after that.
-template <int kWarps, bool kTotal>
-__device__ __forceinline__ f32x2 exchange(Shares<kWarps>& sh, int step, int ranks, int r, int w, const Run& own, bool fresh, f32x2& carry,
-                                          Run& total, bool& total_fresh, Waits& wait, uint8_t* ws) {
+// A step's own sums, in two parts with room for other work between them: `post` makes them known to the block's warps
+// and sends the block's to the others of the cluster, `take` waits for theirs and gives the state (adjoint) that comes to
+// this warp, and in `carry` the one that leaves the step. Warps and ranks follow one another in the order of the scan,
+// `w` and `r` their places in it. kTotal: only what all the steps so far do, in `total`.
+// The blocks' sums travel over distributed shared memory with their own completion: a barrier of the cluster would make
+// every thread wait for all its stores (a third of the time). Two steps' sums are kept, and nobody sends a third
+// before all have read the first: a block's sum of the step between left it after that.
+template <int kWarps>
+__device__ __forceinline__ void post(Shares<kWarps>& sh, int step, int ranks, int r, int w, const Run& own, bool fresh) {
     const int lane = threadIdx.x & 31, parity = step & 1;
     sh.warp[parity][w][lane] = held(own);
     if (lane == 0) sh.warp_fresh[parity][w] = fresh;
     __syncthreads();
+    if (ranks > 1 && w == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(&sh.sent[parity], (uint32_t)ranks * (32 * sizeof(float4) + 4));
+        const uint32_t warps = bits_of<kWarps>(sh.warp_fresh[parity]);
+        Run s = own;
+        if (warps == 0) {
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), false);
+        } else {
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), (warps >> v & 1) != 0);
+        }
+        const float4 f = held(s);
+        for (int k = 0; k < ranks; ++k) {
+            const uint32_t bar = at_rank(&sh.sent[parity], k);
+            send(at_rank(&sh.rank[parity][r][lane], k), f, bar);
+            if (lane == 0) send(at_rank(&sh.rank_fresh[parity][r], k), warps != 0 ? 1u : 0u, bar);
+        }
+    }
+}
+template <int kWarps, bool kTotal>
+__device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, int r, int w, f32x2& carry, Run& total, bool& total_fresh,
+                                      Waits& wait, uint8_t* ws) {
+    const int lane = threadIdx.x & 31, parity = step & 1;
     const uint32_t warps = bits_of<kWarps>(sh.warp_fresh[parity]);
     uint32_t all = warps;
     if (ranks > 1) {
-        if (w == 0) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.sent[parity], (uint32_t)ranks * (32 * sizeof(float4) + 4));
-            Run s = own;
-            if (warps == 0) {
-#pragma unroll
-                for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), false);
-            } else {
-#pragma unroll
-                for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), (warps >> v & 1) != 0);
-            }
-            const float4 f = held(s);
-            for (int k = 0; k < ranks; ++k) {
-                const uint32_t bar = at_rank(&sh.sent[parity], k);
-                send(at_rank(&sh.rank[parity][r][lane], k), f, bar);
-                if (lane == 0) send(at_rank(&sh.rank_fresh[parity][r], k), warps != 0 ? 1u : 0u, bar);
-            }
-        }
         wait.full(&sh.sent[parity], step >> 1 & 1, ws);
         all = __ballot_sync(0xffffffffu, lane < ranks && sh.rank_fresh[parity][lane & (kMostRanks - 1)] != 0);
     }
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
     if constexpr (kTotal) grid_launch_next();
     else grid_wait_before();           // the pass that found what segments do, where there is one
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
-    Run total{both(1.0f), 0};
+    Run total{0, 0};
     bool total_fresh = false;
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
@@ -495,8 +500,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
             if (events) gates(std::true_type());
             else gates(std::false_type());
         }
-        h = exchange<kWarps, kTotal>(sh, step, a.ranks, r, warp, Run{exp2_of(sum), h}, events && ev.starts, carry, total, total_fresh, wait, a.ws);
+        post<kWarps>(sh, step, a.ranks, r, warp, Run{minus_decayed(sum), h}, events && ev.starts);
         if (kVec && threadIdx.x == 0 && !wait.lost) load(step + 1);     // every warp has read this step's
+        h = take<kWarps, kTotal>(sh, step, a.ranks, r, warp, carry, total, total_fresh, wait, a.ws);
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
             if (left > 0) {
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     if constexpr (kTotal) grid_launch_next();
     else grid_wait_before();           // the pass that found what segments do, where there is one
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
-    Run total{both(1.0f), 0};
+    Run total{0, 0};
     bool total_fresh = false;
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
@@ -598,7 +604,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     __syncthreads();
     Events<kTok> ev;
     Waits wait;
-    f32x2 acc = 0;
+    f32x2 acc = 0, kept = 0;
+    if constexpr (!kTotal)
+        if (first + r < last) kept = load_state<kVec>(a.kept, a.chunks - 1 - first - r, c, a.D);      // of the step at hand
     for (int step = 0; step < steps; ++step) {
         const int at = first + step * a.ranks + r, chunk = a.chunks - 1 - at;
         const bool some = at < last;
@@ -646,24 +654,27 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
             if (events) sums(std::true_type());
             else sums(std::false_type());
         }
-        const f32x2 decay = exp2_of(sum);
+        const f32x2 decay = minus_decayed(sum);
         if constexpr (!kTotal) {
             ahead.warp[step & 1][warp][lane] = held(Run{decay, h});
             if (lane == 0) {
                 ahead.fresh[step & 1][warp] = events && ev.starts;
                 if (kVec) bulk_wait_read_all();      // the gradients of the step before have left
             }
-            h = some ? load_state<kVec>(a.kept, chunk, c, a.D) : 0;
         }
-        G = exchange<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends, carry, total, total_fresh, wait, a.ws);
+        post<kWarps>(sh, step, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends);
+        f32x2 before[kTok];
         if constexpr (kTotal) {
             if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);
         } else {
             if (kVec && kStages == 2 && threadIdx.x == 0 && !wait.lost && step > 0) load(step + 1);    // into the other stage, which all have left
+            // the states before this warp's tokens, while the others' sums are on their way
+            h = kept;
+            const int next = chunk - a.ranks;
+            kept = next >= 0 ? load_state<kVec>(a.kept, next, c, a.D) : 0;
             if (left > 0) {
                 h = through(ahead.warp[step & 1], bits_of<kWarps>(ahead.fresh[step & 1]), 0, warp, h);
-                f32x2 before[kTok];
-                auto grads = [&](auto with) {
+                auto states = [&](auto with) {
 #pragma unroll
                     for (int j = 0; j < kTok; ++j) {
                         if constexpr (with.value)
@@ -671,6 +682,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                         before[j] = h;
                         h = advance(h, n[j], b[j]);
                     }
+                };
+                if (events) states(std::true_type());
+                else states(std::false_type());
+            }
+        }
+        G = take<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, carry, total, total_fresh, wait, a.ws);
+        if constexpr (!kTotal) {
+            if (left > 0) {
+                auto grads = [&](auto with) {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
                         if constexpr (with.value)
@@ -988,7 +1008,7 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
     const bool bf16 = sh->dtype == KDA_BF16;
     a.chunks = p.chunks; a.seg_chunks = p.seg_chunks; a.ranks = p.ranks;
     a.seg = reinterpret_cast<float4*>(a.ws + 1024);
-    a.seg_fresh = reinterpret_cast<int*>(a.ws + 64);       // kMostSegs of them
+    a.seg_fresh = reinterpret_cast<int*>(a.ws + 64);       // 64 of them at most
     Maps m{};
     if (vec && a.total > 0) {
         const int e = bf16 ? 2 : 4;
