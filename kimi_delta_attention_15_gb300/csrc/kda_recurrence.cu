@@ -111,11 +111,12 @@ __device__ __forceinline__ f32x2 over(const Run& r, bool fresh, f32x2 h) { retur
 // first s, then t; `fresh` is t's
 __device__ __forceinline__ Run then(const Run& s, const Run& t, bool fresh) { return {fresh ? t.n : advance(s.n, t.n, t.n), over(t, fresh, s.b)}; }
 
-__device__ __forceinline__ f32x2 pair_at(const uint16_t* p) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    return two(w << 16, w & 0xffff0000u);
-}
-__device__ __forceinline__ f32x2 pair_at(const float* p) { return *reinterpret_cast<const f32x2*>(p); }
+template <typename T> struct Raw;           // two channels as they are stored
+template <> struct Raw<uint16_t> { using Two = uint32_t; };
+template <> struct Raw<float> { using Two = uint64_t; };
+__device__ __forceinline__ f32x2 pair_of(uint32_t w) { return two(w << 16, w & 0xffff0000u); }
+__device__ __forceinline__ f32x2 pair_of(uint64_t w) { return w; }
+template <typename T> __device__ __forceinline__ f32x2 pair_at(const T* p) { return pair_of(*reinterpret_cast<const typename Raw<T>::Two*>(p)); }
 __device__ __forceinline__ void put_pair(uint16_t* p, f32x2 f) {
     const float2 v = parts(f);
     const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
@@ -166,12 +167,6 @@ template <int kTok, typename T> __device__ __forceinline__ void close_rows(T* gs
     for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
     if (left < kTok) fence_async_smem();       // a later tensor load writes there
 }
-__device__ __forceinline__ void put_shared(uint16_t* p, f32x2 f) {
-    const float2 v = parts(f);
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
-}
-__device__ __forceinline__ void put_shared(float* p, f32x2 f) { *reinterpret_cast<f32x2*>(p) = f; }
-
 // Waits for a stage's loads. A wait that gave up is reported and not repeated: the rest of the call computes what it finds.
 struct Waits {
     bool lost = false;
@@ -306,16 +301,33 @@ template <int kWarps> struct Shares {          // what the warps of a block and 
     uint64_t sent[2];    // the ranks' sums
 };
 
-// h through the runs from `from` to `to`; fresh: a bit for each
-__device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint32_t fresh, int from, int to, f32x2 h) {
+// h through the first `count` of kMost runs, and in `at` what it is before run w; fresh: a bit for each. The runs are read
+// four at a time, whether they count or not: one by one, each would wait for its read.
+template <int kMost>
+__device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint32_t fresh, int count, int w, f32x2 h, f32x2& at) {
     const int lane = threadIdx.x & 31;
+    at = h;
     if (fresh == 0) {
-#pragma unroll 4
-        for (int k = from; k < to; ++k) {
-            h = over(run_of(runs[k][lane]), false, h);
+#pragma unroll
+        for (int k0 = 0; k0 < kMost; k0 += 4) {
+            float4 s[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k < kMost) s[k] = runs[k0 + k][lane];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k < kMost) {
+                    const f32x2 to = over(run_of(s[k]), false, h);
+                    h = k0 + k < count ? to : h;
+                    at = k0 + k + 1 == w ? h : at;
+                }
         }
     } else {
-        for (int k = from; k < to; ++k) h = over(run_of(runs[k][lane]), (fresh >> k & 1) != 0, h);
+#pragma unroll 1
+        for (int k = 0; k < count; ++k) {
+            h = over(run_of(runs[k][lane]), (fresh >> k & 1) != 0, h);
+            if (k + 1 == w) at = h;
+        }
     }
     return h;
 }
@@ -377,13 +389,14 @@ __device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, i
         }
         return 0;
     }
+    f32x2 at;
     if (ranks > 1) {
-        const f32x2 block = through(sh.rank[parity], all, 0, r, carry);
-        carry = through(sh.rank[parity], all, r, ranks, block);
-        return through(sh.warp[parity], warps, 0, w, block);
+        f32x2 block;
+        carry = through<kMostRanks>(sh.rank[parity], all, ranks, r, carry, block);
+        through<kWarps - 1>(sh.warp[parity], warps, w, w, block, at);
+    } else {
+        carry = through<kWarps>(sh.warp[parity], warps, kWarps, w, carry, at);
     }
-    const f32x2 at = through(sh.warp[parity], warps, 0, w, carry);
-    carry = through(sh.warp[parity], warps, w, kWarps, at);
     return at;
 }
 
@@ -402,9 +415,9 @@ __device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t
     return h;
 }
 
-// The tensor maps of the inputs (boxes of a block's chunk) and outputs (boxes of a warp's rows)
+// The tensor maps of the inputs, in boxes of a block's chunk
 struct Maps {
-    CUtensorMap x, g, i, dy, out[3];      // out: y, or dx, dg_raw, di_raw
+    CUtensorMap x, g, i, dy;
 };
 constexpr int kTile = kBlock * kCh;
 
@@ -418,10 +431,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kTok = kFwdTok, kWarps = kBlock / kTok;
     Shares<kWarps>& sh = *reinterpret_cast<Shares<kWarps>*>(smem);
-    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps>>);          // x, g, i, then y
+    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps>>);          // x, g, i
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;      // the warp's, as the compiler may know
     const int own_at = warp * kTok * kCh + 2 * lane;
-    T* const out = tiles + 3 * kTile;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
     const int first = seg * a.seg_chunks, last = min(first + a.seg_chunks, a.chunks);
@@ -506,10 +518,6 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
             if (left > 0) {
-                if constexpr (kVec) {
-                    if (lane == 0) bulk_wait_read_all();        // the step before has left
-                    __syncwarp();
-                }
                 T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.sy + c;
                 auto states = [&](auto with) {
 #pragma unroll
@@ -517,8 +525,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
                         if constexpr (with.value)
                             if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
                         h = advance(h, n[j], b[j]);
-                        if constexpr (kVec) put_shared(out + own_at + j * kCh, h);
-                        else if (j < left) store_pair<kVec>(y + j * a.sy, c, a.D, h);
+                        if (!with.value || j < left) store_pair<kVec>(y, c, a.D, h);
+                        y += a.sy;
                         if constexpr (with.value)
                             if (ev.ends >> j & 1) {
                                 const int q = ev.of(j);
@@ -526,16 +534,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
                             }
                     }
                 };
-                if (events) states(std::true_type());
+                if (events || left < kTok) states(std::true_type());
                 else states(std::false_type());
-                if constexpr (kVec) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_3d(out + warp * kTok * kCh, &maps.out[0], (int)c0, t0, 0);
-                        bulk_commit();
-                    }
-                }
             }
         }
     }
@@ -544,14 +544,11 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
     if constexpr (kTotal) {
         if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
         if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
-    } else if (kVec) {
-        if (lane == 0) bulk_wait_all();
     }
     if (a.ranks > 1) cluster_wait();
 }
 
-// The same grid, tokens from the last to the first: chunks, ranks and warps in that order. The gradients take the inputs'
-// places in shared memory.
+// The same grid, tokens from the last to the first: chunks, ranks and warps in that order.
 template <typename T, bool kTotal> constexpr int kBwdStages = sizeof(T) == 2 ? 2 : 1;
 constexpr int kBwdTok = 8, kBwdThreads = kBlock / kBwdTok * 32;
 template <typename T, bool kVec, bool kTotal>
@@ -605,8 +602,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     Events<kTok> ev;
     Waits wait;
     f32x2 acc = 0, kept = 0;
-    if constexpr (!kTotal)
-        if (first + r < last) kept = load_state<kVec>(a.kept, a.chunks - 1 - first - r, c, a.D);      // of the step at hand
+    // The state before a chunk. Read a step ahead, and whether there is such a chunk and channel or not: a choice would wait.
+    const float* const kept_from = a.kept + (c < a.D ? c : 0);
+    auto kept_at = [&](int chunk) -> f32x2 {
+        const float* const p = kept_from + (int64_t)chunk * a.D;
+        if constexpr (kVec) return *reinterpret_cast<const f32x2*>(p);
+        else return two(p[0], c + 1 < a.D ? p[1] : 0.0f);
+    };
+    if (!kTotal && steps > 0) kept = kept_at(max(a.chunks - 1 - first - r, 0));
     for (int step = 0; step < steps; ++step) {
         const int at = first + step * a.ranks + r, chunk = a.chunks - 1 - at;
         const bool some = at < last;
@@ -657,10 +660,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
         const f32x2 decay = minus_decayed(sum);
         if constexpr (!kTotal) {
             ahead.warp[step & 1][warp][lane] = held(Run{decay, h});
-            if (lane == 0) {
-                ahead.fresh[step & 1][warp] = events && ev.starts;
-                if (kVec) bulk_wait_read_all();      // the gradients of the step before have left
-            }
+            if (lane == 0) ahead.fresh[step & 1][warp] = events && ev.starts;
         }
         post<kWarps>(sh, step, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends);
         f32x2 before[kTok];
@@ -670,10 +670,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
             if (kVec && kStages == 2 && threadIdx.x == 0 && !wait.lost && step > 0) load(step + 1);    // into the other stage, which all have left
             // the states before this warp's tokens, while the others' sums are on their way
             h = kept;
-            const int next = chunk - a.ranks;
-            kept = next >= 0 ? load_state<kVec>(a.kept, next, c, a.D) : 0;
+            kept = kept_at(max(chunk - a.ranks, 0));
             if (left > 0) {
-                h = through(ahead.warp[step & 1], bits_of<kWarps>(ahead.fresh[step & 1]), 0, warp, h);
+                through<kWarps - 1>(ahead.warp[step & 1], bits_of<kWarps>(ahead.fresh[step & 1]), warp, warp, h, h);
                 auto states = [&](auto with) {
 #pragma unroll
                     for (int j = 0; j < kTok; ++j) {
@@ -690,6 +689,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
         G = take<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, carry, total, total_fresh, wait, a.ws);
         if constexpr (!kTotal) {
             if (left > 0) {
+                T* to_x = static_cast<T*>(a.dx) + (int64_t)(t0 + kTok - 1) * a.sdx + c;
+                T* to_g = static_cast<T*>(a.dg) + (int64_t)(t0 + kTok - 1) * a.sdg + c;
+                T* to_i = static_cast<T*>(a.di) + (int64_t)(t0 + kTok - 1) * a.sdi + c;
                 auto grads = [&](auto with) {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
@@ -705,15 +707,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                         acc = add2(acc, duu);
                         G = fma2(n[j], t, t);
                         const f32x2 dx = mul2(tm, si), dg = mul2(duu, mul2(eg[j], s)), di = mul2(mul2(tm, ix), mul2(ei[j], si));
-                        if constexpr (kVec) {
-                            put_shared(xs + j * kCh, dx);
-                            put_shared(gs + j * kCh, dg);
-                            put_shared(is + j * kCh, di);
-                        } else if (j < left) {
-                            store_pair<kVec>(static_cast<T*>(a.dx) + (int64_t)(t0 + j) * a.sdx + c, c, a.D, dx);
-                            store_pair<kVec>(static_cast<T*>(a.dg) + (int64_t)(t0 + j) * a.sdg + c, c, a.D, dg);
-                            store_pair<kVec>(static_cast<T*>(a.di) + (int64_t)(t0 + j) * a.sdi + c, c, a.D, di);
+                        if (!with.value || j < left) {
+                            store_pair<kVec>(to_x, c, a.D, dx);
+                            store_pair<kVec>(to_g, c, a.D, dg);
+                            store_pair<kVec>(to_i, c, a.D, di);
                         }
+                        to_x -= a.sdx;
+                        to_g -= a.sdg;
+                        to_i -= a.sdi;
                         if constexpr (with.value)
                             if (ev.starts >> j & 1) {
                                 const int q0 = ev.of(j);
@@ -721,22 +722,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                             }
                     }
                 };
-                if (events) grads(std::true_type());
+                if (events || left < kTok) grads(std::true_type());
                 else grads(std::false_type());
-                if constexpr (kVec) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_3d(own + 2 * kTile, &maps.out[0], (int)c0, t0, 0);
-                        tma_store_3d(own, &maps.out[1], (int)c0, t0, 0);
-                        tma_store_3d(own + 3 * kTile, &maps.out[2], (int)c0, t0, 0);
-                        bulk_commit();
-                    }
-                }
             }
             if constexpr (kVec && kStages == 1) {
-                if (lane == 0) bulk_wait_read_all();
-                __syncthreads();
+                __syncthreads();           // every warp has read this step's
                 if (threadIdx.x == 0 && !wait.lost) load(step + 1);
             }
         }
@@ -760,7 +750,6 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                 store_state<kVec>(a.part, blockIdx.x, c, a.D, acc);
             }
         }
-        if (kVec && lane == 0) bulk_wait_all();
     }
     if (a.ranks > 1) cluster_wait();
 }
@@ -926,7 +915,7 @@ template <bool kBwd> Kernel pick(bool bf16, bool vec, bool total) {
 constexpr size_t smem_of(bool backward, size_t element, bool total) {
     const size_t tile = kTile * element;
     constexpr int fwd = kBlock / kFwdTok, bwd = kBlock / kBwdTok;
-    if (!backward) return kBytes<Shares<fwd>> + 4 * tile;
+    if (!backward) return kBytes<Shares<fwd>> + 3 * tile;
     return kBytes<Shares<bwd>> + kBytes<Ahead<bwd>> + (total ? 2 : 4) * (element == 2 ? 2 : 1) * tile;
 }
 
@@ -1012,19 +1001,16 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
     Maps m{};
     if (vec && a.total > 0) {
         const int e = bf16 ? 2 : 4;
-        auto map = [&](CUtensorMap* to, const void* p, int64_t stride, int rows) { return row_map(to, p, sh->D, a.total, stride, rows, e); };
-        kda_status ms = map(&m.x, a.x, a.sx, kBlock);
-        if (ms == KDA_OK) ms = map(&m.g, a.g, a.sg, kBlock);
-        if (ms == KDA_OK) ms = map(&m.i, a.i, a.si, kBlock);
-        if (kBwd && ms == KDA_OK) ms = map(&m.dy, a.dy, a.sy, kBlock);
-        if (ms == KDA_OK) ms = kBwd ? map(&m.out[0], a.dx, a.sdx, kBwdTok) : map(&m.out[0], a.y, a.sy, kFwdTok);
-        if (kBwd && ms == KDA_OK) ms = map(&m.out[1], a.dg, a.sdg, kBwdTok);
-        if (kBwd && ms == KDA_OK) ms = map(&m.out[2], a.di, a.sdi, kBwdTok);
+        auto map = [&](CUtensorMap* to, const void* p, int64_t stride) { return row_map(to, p, sh->D, a.total, stride, kBlock, e); };
+        kda_status ms = map(&m.x, a.x, a.sx);
+        if (ms == KDA_OK) ms = map(&m.g, a.g, a.sg);
+        if (ms == KDA_OK) ms = map(&m.i, a.i, a.si);
+        if (kBwd && ms == KDA_OK) ms = map(&m.dy, a.dy, a.sy);
         if (ms != KDA_OK) return ms;
     }
     const int threads = kBwd ? kBwdThreads : kFwdThreads;
     if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), threads, p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), false, s, a, m);
-    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), p.segs > 1, s, a, m);
+    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), !kBwd && p.segs > 1, s, a, m);
     return launched(where);
 }
 
