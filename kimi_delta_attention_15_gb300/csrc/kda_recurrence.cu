@@ -167,6 +167,11 @@ template <int kTok, typename T> __device__ __forceinline__ void close_rows(T* gs
     for (int j = max(left, 0); j < kTok; ++j) closed(gs + j * kCh);
     if (left < kTok) fence_async_smem();       // a later tensor load writes there
 }
+__device__ __forceinline__ void put_shared(uint16_t* p, f32x2 f) {
+    const float2 v = parts(f);
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
 // Waits for a stage's loads. A wait that gave up is reported and not repeated: the rest of the call computes what it finds.
 struct Waits {
     bool lost = false;
@@ -301,28 +306,18 @@ template <int kWarps> struct Shares {          // what the warps of a block and 
     uint64_t sent[2];    // the ranks' sums
 };
 
-// h through the first `count` of kMost runs, and in `at` what it is before run w; fresh: a bit for each. The runs are read
-// four at a time, whether they count or not: one by one, each would wait for its read.
-template <int kMost>
+// h through the first `count` runs, and in `at` what it is before run w; fresh: a bit for each. (All runs at once with a
+// choice for each, so that none waits for its read, is no faster: the steps are bound by what they issue.)
 __device__ __forceinline__ f32x2 through(const float4 (*runs)[32], uint32_t fresh, int count, int w, f32x2 h, f32x2& at) {
     const int lane = threadIdx.x & 31;
-    at = h;
     if (fresh == 0) {
-#pragma unroll
-        for (int k0 = 0; k0 < kMost; k0 += 4) {
-            float4 s[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k0 + k < kMost) s[k] = runs[k0 + k][lane];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k0 + k < kMost) {
-                    const f32x2 to = over(run_of(s[k]), false, h);
-                    h = k0 + k < count ? to : h;
-                    at = k0 + k + 1 == w ? h : at;
-                }
-        }
+#pragma unroll 4
+        for (int k = 0; k < w; ++k) h = over(run_of(runs[k][lane]), false, h);
+        at = h;
+#pragma unroll 4
+        for (int k = w; k < count; ++k) h = over(run_of(runs[k][lane]), false, h);
     } else {
+        at = h;
 #pragma unroll 1
         for (int k = 0; k < count; ++k) {
             h = over(run_of(runs[k][lane]), (fresh >> k & 1) != 0, h);
@@ -392,10 +387,10 @@ __device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, i
     f32x2 at;
     if (ranks > 1) {
         f32x2 block;
-        carry = through<kMostRanks>(sh.rank[parity], all, ranks, r, carry, block);
-        through<kWarps - 1>(sh.warp[parity], warps, w, w, block, at);
+        carry = through(sh.rank[parity], all, ranks, r, carry, block);
+        through(sh.warp[parity], warps, w, w, block, at);
     } else {
-        carry = through<kWarps>(sh.warp[parity], warps, kWarps, w, carry, at);
+        carry = through(sh.warp[parity], warps, kWarps, w, carry, at);
     }
     return at;
 }
@@ -417,7 +412,7 @@ __device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t
 
 // The tensor maps of the inputs, in boxes of a block's chunk
 struct Maps {
-    CUtensorMap x, g, i, dy;
+    CUtensorMap x, g, i, dy, out[3];      // out: dx, dg_raw, di_raw in boxes of a warp's tokens
 };
 constexpr int kTile = kBlock * kCh;
 
@@ -554,6 +549,7 @@ constexpr int kBwdTok = 8, kBwdThreads = kBlock / kBwdTok * 32;
 template <typename T, bool kVec, bool kTotal>
 __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
+    constexpr bool kByCopy = kVec && !kTotal && kBwdStages<T, kTotal> == 2;      // gradients leave by tensor copies, from the inputs' places
     constexpr int kTensors = kTotal ? 2 : 4, kStages = kBwdStages<T, kTotal>, kTok = kBwdTok, kWarps = kBlock / kTok;
     Shares<kWarps>& sh = *reinterpret_cast<Shares<kWarps>*>(smem);
     Ahead<kWarps>& ahead = *reinterpret_cast<Ahead<kWarps>*>(smem + kBytes<Shares<kWarps>>);      // the states' way, forwards
@@ -660,7 +656,10 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
         const f32x2 decay = minus_decayed(sum);
         if constexpr (!kTotal) {
             ahead.warp[step & 1][warp][lane] = held(Run{decay, h});
-            if (lane == 0) ahead.fresh[step & 1][warp] = events && ev.starts;
+            if (lane == 0) {
+                ahead.fresh[step & 1][warp] = events && ev.starts;
+                if (kByCopy) bulk_wait_read_all();      // the gradients of the step before have left
+            }
         }
         post<kWarps>(sh, step, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends);
         f32x2 before[kTok];
@@ -672,7 +671,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
             h = kept;
             kept = kept_at(max(chunk - a.ranks, 0));
             if (left > 0) {
-                through<kWarps - 1>(ahead.warp[step & 1], bits_of<kWarps>(ahead.fresh[step & 1]), warp, warp, h, h);
+                through(ahead.warp[step & 1], bits_of<kWarps>(ahead.fresh[step & 1]), warp, warp, h, h);
                 auto states = [&](auto with) {
 #pragma unroll
                     for (int j = 0; j < kTok; ++j) {
@@ -707,7 +706,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                         acc = add2(acc, duu);
                         G = fma2(n[j], t, t);
                         const f32x2 dx = mul2(tm, si), dg = mul2(duu, mul2(eg[j], s)), di = mul2(mul2(tm, ix), mul2(ei[j], si));
-                        if (!with.value || j < left) {
+                        if constexpr (kByCopy) {
+                            put_shared(xs + j * kCh, dx);
+                            put_shared(gs + j * kCh, dg);
+                            put_shared(is + j * kCh, di);
+                        } else if (!with.value || j < left) {
                             store_pair<kVec>(to_x, c, a.D, dx);
                             store_pair<kVec>(to_g, c, a.D, dg);
                             store_pair<kVec>(to_i, c, a.D, di);
@@ -722,8 +725,18 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                             }
                     }
                 };
-                if (events || left < kTok) grads(std::true_type());
+                if (events || (!kByCopy && left < kTok)) grads(std::true_type());
                 else grads(std::false_type());
+                if constexpr (kByCopy) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(own + 2 * kTile, &maps.out[0], (int)c0, t0, 0);
+                        tma_store_3d(own, &maps.out[1], (int)c0, t0, 0);
+                        tma_store_3d(own + 3 * kTile, &maps.out[2], (int)c0, t0, 0);
+                        bulk_commit();
+                    }
+                }
             }
             if constexpr (kVec && kStages == 1) {
                 __syncthreads();           // every warp has read this step's
@@ -750,6 +763,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                 store_state<kVec>(a.part, blockIdx.x, c, a.D, acc);
             }
         }
+        if (kByCopy && lane == 0) bulk_wait_all();
     }
     if (a.ranks > 1) cluster_wait();
 }
@@ -839,7 +853,8 @@ struct Cost {
     int per_sm;
 };
 float wave(const Cost& c, int64_t blocks, int ranks) {
-    const int64_t full = (int64_t)kSMs * c.per_sm, rest = blocks % full, m = (rest + kSMs - 1) / kSMs;
+    // a cluster's blocks are on one of 8 groups of 19 SMs
+    const int64_t full = 8 * (int64_t)(kSMs / 8 * c.per_sm / ranks * ranks), rest = blocks % full, m = (rest + kSMs - 1) / kSMs;
     const float one = c.step + (ranks > 1 ? 0.5f + c.rank * (float)(ranks - 1) : 0.0f);
     return (float)(blocks / full) * (one + c.more * (c.per_sm - 1)) + (m ? one + c.more * (float)(m - 1) : 0.0f);
 }
@@ -1002,10 +1017,14 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, 
     if (vec && a.total > 0) {
         const int e = bf16 ? 2 : 4;
         auto map = [&](CUtensorMap* to, const void* p, int64_t stride) { return row_map(to, p, sh->D, a.total, stride, kBlock, e); };
+        auto out = [&](CUtensorMap* to, const void* p, int64_t stride) { return row_map(to, p, sh->D, a.total, stride, kBwdTok, e); };
         kda_status ms = map(&m.x, a.x, a.sx);
         if (ms == KDA_OK) ms = map(&m.g, a.g, a.sg);
         if (ms == KDA_OK) ms = map(&m.i, a.i, a.si);
         if (kBwd && ms == KDA_OK) ms = map(&m.dy, a.dy, a.sy);
+        if (kBwd && bf16 && ms == KDA_OK) ms = out(&m.out[0], a.dx, a.sdx);
+        if (kBwd && bf16 && ms == KDA_OK) ms = out(&m.out[1], a.dg, a.sdg);
+        if (kBwd && bf16 && ms == KDA_OK) ms = out(&m.out[2], a.di, a.sdi);
         if (ms != KDA_OK) return ms;
     }
     const int threads = kBwd ? kBwdThreads : kFwdThreads;
