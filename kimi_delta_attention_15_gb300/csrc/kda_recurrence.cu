@@ -870,7 +870,7 @@ Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
     float least = 0.0f;
     for (int r = 1; r <= kMostRanks && r <= (p.chunks > 1 ? p.chunks : 1); ++r) {
         const int steps = (p.chunks + r - 1) / r;
-        const float t = kPass + (float)steps * wave(cost, (int64_t)p.tiles * r, r);
+        const float t = kPass + (float)steps * wave(cost, (int64_t)p.tiles * r, r) + (backward && r > 1 ? 3.0f : 0.0f);    // the sum of shares
         if (r == 1 || t < least) { least = t; p.ranks = r; }
     }
     const int64_t slots = (int64_t)kSMs * cost.per_sm, clusters = (int64_t)p.tiles * kMostRanks;
@@ -886,15 +886,14 @@ Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
     if (p.chunks == 0) p.seg_chunks = 1;
     return p;
 }
-size_t seg_bytes(const Plan& p, int64_t D) {
-    return p.segs > 1 ? align_up((size_t)p.segs * ((D + 1) / 2) * sizeof(float4), 1024) : 0;
-}
+// The workspace: the status word and the segments' flags; what segments do to states; the blocks' shares of dA_log.
+// Enough for any plan: segments times tiles are at most an eighth of the blocks that run at once, and so are their
+// shares but where there is one segment.
+constexpr size_t kSegBytes = (size_t)kSMs * 4 / kMostRanks * kCh / 2 * sizeof(float4);
 size_t bytes_of(const kda_recurrence_shape* sh, bool backward) {
-    const size_t f = seg_bytes(plan_of(sh, false), sh->D);
-    if (!backward) return 1024 + f;
-    const Plan p = plan_of(sh, true);
-    const size_t b = seg_bytes(p, sh->D) + align_up((size_t)p.segs * p.ranks * sh->D * sizeof(float), 1024);
-    return 1024 + (f > b ? f : b);
+    if (!backward) return 1024 + kSegBytes;
+    const size_t one = (size_t)kMostRanks * sh->D * sizeof(float), many = (size_t)kSMs * 2 * kCh * sizeof(float);
+    return 1024 + kSegBytes + align_up(one > many ? one : many, 1024);
 }
 
 RecArgs args_of(const kda_recurrence_shape* sh) {
@@ -1005,10 +1004,9 @@ kda_status row_map(CUtensorMap* map, const void* p, int64_t D, int64_t tokens, i
     return KDA_ERR_CUDA;
 }
 
-template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, RecArgs& a, bool vec, cudaStream_t s, const char* where) {
+template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, const Plan& p, RecArgs& a, bool vec, cudaStream_t s, const char* where) {
     const kda_status st = allow_shared(where);
     if (st != KDA_OK) return st;
-    const Plan p = plan_of(sh, kBwd);
     const bool bf16 = sh->dtype == KDA_BF16;
     a.chunks = p.chunks; a.seg_chunks = p.seg_chunks; a.ranks = p.ranks;
     a.seg = reinterpret_cast<float4*>(a.ws + 1024);
@@ -1066,7 +1064,7 @@ extern "C" kda_status kda_recurrence_fwd(const kda_recurrence_shape* shape, cons
     a.x = x; a.g = g_raw; a.i = i_raw; a.y = y; a.A_log = A_log; a.h0 = h0; a.cu = cu_seqlens; a.hT = hT; a.kept = kept;
     a.ws = static_cast<uint8_t*>(workspace);
     const bool vec = whole_units(shape, {x, g_raw, i_raw, y}, {a.sx, a.sg, a.si, a.sy});
-    return run<false>(shape, a, vec, static_cast<cudaStream_t>(stream), "kda_recurrence_fwd launch");
+    return run<false>(shape, plan_of(shape, false), a, vec, static_cast<cudaStream_t>(stream), "kda_recurrence_fwd launch");
 }
 
 extern "C" kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,
@@ -1089,11 +1087,11 @@ extern "C" kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, cons
     a.ws = static_cast<uint8_t*>(workspace);
     const Plan p = plan_of(shape, true);
     const int parts = p.segs * p.ranks;
-    float* const shares = reinterpret_cast<float*>(a.ws + 1024 + seg_bytes(p, a.D));
+    float* const shares = reinterpret_cast<float*>(a.ws + 1024 + kSegBytes);
     a.part = !dA_log || parts == 1 ? dA_log : shares;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = whole_units(shape, {x, g_raw, i_raw, dy, dx, dg_raw, di_raw}, {a.sx, a.sg, a.si, a.sy, a.sdx, a.sdg, a.sdi});
-    const kda_status rs = run<true>(shape, a, vec, s, "kda_recurrence_bwd launch");
+    const kda_status rs = run<true>(shape, p, a, vec, s, "kda_recurrence_bwd launch");
     if (rs != KDA_OK || !dA_log || parts == 1) return rs;
     launch_kernel(rec_sum_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(32, 8), 0, s, true, static_cast<const float*>(shares), parts, a.D, dA_log);
     return launched("kda_recurrence_bwd launch");
