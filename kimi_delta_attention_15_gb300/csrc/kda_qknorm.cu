@@ -26,8 +26,8 @@ constexpr int kSMs = 152;
 constexpr int kRing = 8192;      // bytes of a warp's ring
 template <bool kBwd> constexpr int kBlocksPerSM = kBwd ? 2 : 3;
 // rows of a lane in a block, blocks in a ring: 8 columns of 32 lanes each, of x and, backwards, dy
-template <bool kBwd> constexpr int kRows = kBwd ? 2 : 4;
-template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
+constexpr int kRows = 2, kMostStages = 8;
+template <typename T, bool kBwd> constexpr int kStages = kRing / (32 * 8 * kRows * (int)sizeof(T) * (kBwd ? 2 : 1));
 constexpr int kZeros = 32;       // bytes of zeros that lanes without columns read
 
 // inv_freq / 2 pi as a 64-bit fraction of a turn, truncated at 2^-64: the significand times 1 / 2 pi in 128 bits, shifted
@@ -195,7 +195,8 @@ template <typename T, bool kOut> struct Walk {
 
 template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bounds__(kThreads, kBlocksPerSM<kBwd>) qknorm_kernel(const QkArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kN = kStages<T>, kR = kRows<kBwd>, kStage = kRing / kN, kHalf = kStage / 2;
+    constexpr int kN = kStages<T, kBwd>, kR = kRows, kStage = kRing / kN, kHalf = kStage / 2;
+    static_assert(kN >= 2 && kN <= kMostStages && 32 * 8 * kR * (int)sizeof(T) <= (kBwd ? kHalf : kStage), "a block in a stage");
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* const ring = smem + warp * kRing;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kWarps * kRing) + warp * kN;
@@ -262,7 +263,7 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
                 }
             }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_asleep(&bars[stage], parity))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], parity))) {
             lost = true;
             break;
         }
@@ -270,7 +271,8 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
         auto block = [&](auto all) {
             constexpr bool kAll = decltype(all)::value;
             const T* const from = reinterpret_cast<const T*>(ring + stage * kStage);
-            Pairs v[kR], g[kBwd ? kR : 1];
+            Pairs v[kR];
+            [[maybe_unused]] Pairs g[kBwd ? kR : 1];
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
                 const bool in = kAll || (l.on && l.group + i * l.groups < at.heads);
@@ -285,7 +287,8 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
                 if (lane == 0) fetch(stage);
                 ahead.next(a, step, rows);
             }
-            float ss[kR], gx[kR];
+            float ss[kR];
+            [[maybe_unused]] float gx[kR];
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
                 ss[i] = sum_of(dot(v[i], v[i]));
@@ -440,7 +443,7 @@ QkArgs args_of(const kda_qknorm_shape* sh, bool backward) {
     a.inv_head = 1.0f / sh->head_dim;
     a.lanes = 1;
     while (8 * a.lanes < a.head) a.lanes *= 2;
-    const int rows = (backward ? kRows<true> : kRows<false>) * (32 / a.lanes);
+    const int rows = kRows * (32 / a.lanes);
     a.side[0].heads = sh->q_heads;
     a.side[1].heads = sh->k_heads;
     for (Side& s : a.side) s.blocks = (s.heads + rows - 1) / rows;
@@ -458,7 +461,7 @@ unsigned grid_of(const QkArgs& a, bool backward) {
     return (unsigned)(blocks < most ? blocks : most);
 }
 
-constexpr size_t kSmem = (size_t)kWarps * (kRing + 4 * sizeof(uint64_t)) + kZeros;
+constexpr size_t kSmem = (size_t)kWarps * (kRing + kMostStages * sizeof(uint64_t)) + kZeros;
 
 using QkKernel = void (*)(QkArgs);
 template <bool kBwd> QkKernel pick(const kda_qknorm_shape* sh) {
