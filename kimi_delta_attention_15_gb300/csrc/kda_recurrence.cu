@@ -573,6 +573,17 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
             tma_load_3d(to + 3 * kTile, &maps.i, (int)c0, t0, 0, bar);
         }
     };
+    auto fetch = [&](int step) {         // into L2, ahead of load
+        const int at = first + step * a.ranks + r;
+        if (at >= last) return;
+        const int t0 = (a.chunks - 1 - at) * kBlock;
+        tma_prefetch_3d(&maps.g, (int)c0, t0, 0);
+        tma_prefetch_3d(&maps.dy, (int)c0, t0, 0);
+        if constexpr (!kTotal) {
+            tma_prefetch_3d(&maps.x, (int)c0, t0, 0);
+            tma_prefetch_3d(&maps.i, (int)c0, t0, 0);
+        }
+    };
     if (threadIdx.x == 0) {
         for (int k = 0; k < 2; ++k) {
             mbar_init(&sh.full[k], 1);
@@ -613,6 +624,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
         const bool events = ev.find(a, some ? t0 : a.total);
         T* const own = tiles + (step % kStages) * kTensors * kTile + warp * kTok * kCh;
         T *const gs = own + 2 * lane, *const dys = gs + kTile, *const xs = gs + 2 * kTile, *const is = gs + 3 * kTile;
+        if (kVec && kStages == 1 && threadIdx.x == 0) fetch(step + 1);
         f32x2 eg[kTok], ei[kTok], n[kTok], b[kTok], h = 0, sum = 0, G = 0;
         if (some) {
             if constexpr (kVec) {
