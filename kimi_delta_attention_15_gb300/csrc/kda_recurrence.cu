@@ -160,6 +160,15 @@ __device__ __forceinline__ void load_own(T* dst, const void* src, int64_t stride
         dst[r * kCh + 1] = b[r];
     }
 }
+// The same rows into L2, a step ahead of load_own
+template <int kTok, typename T>
+__device__ __forceinline__ void fetch_own(const void* src, int64_t stride, int t0, int total, int64_t c0, int64_t D) {
+    const int r = threadIdx.x & 31;
+    if (r >= kTok || t0 + r >= total) return;
+    const T* const p = static_cast<const T*>(src) + (int64_t)(t0 + r) * stride;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c0));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + min(c0 + kCh, D) - 1));
+}
 // Rows of the decay's gate that are no tokens: a closed gate, which decays and writes nothing.
 __device__ __forceinline__ void closed(uint16_t* p) { *reinterpret_cast<uint32_t*>(p) = 0xff80ff80u; }
 __device__ __forceinline__ void closed(float* p) { *reinterpret_cast<uint64_t*>(p) = 0xff800000ff800000ull; }
@@ -489,6 +498,12 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
                 load_own<kTok>(const_cast<T*>(xs), a.x, a.sx, t0, left, c, a.D);
                 load_own<kTok>(gs, a.g, a.sg, t0, left, c, a.D);
                 load_own<kTok>(const_cast<T*>(is), a.i, a.si, t0, left, c, a.D);
+                if (chunk + a.ranks < last) {
+                    const int next = t0 + a.ranks * kBlock;
+                    fetch_own<kTok, T>(a.x, a.sx, next, a.total, c0, a.D);
+                    fetch_own<kTok, T>(a.g, a.sg, next, a.total, c0, a.D);
+                    fetch_own<kTok, T>(a.i, a.si, next, a.total, c0, a.D);
+                }
             }
             if (left < kTok) close_rows<kTok>(gs, left);
             auto gates = [&](auto with) {
@@ -635,6 +650,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                 if constexpr (!kTotal) {
                     load_own<kTok>(xs, a.x, a.sx, t0, left, c, a.D);
                     load_own<kTok>(is, a.i, a.si, t0, left, c, a.D);
+                }
+                if (at + a.ranks < last) {
+                    const int next = t0 - a.ranks * kBlock;
+                    fetch_own<kTok, T>(a.g, a.sg, next, a.total, c0, a.D);
+                    fetch_own<kTok, T>(a.dy, a.sy, next, a.total, c0, a.D);
+                    if constexpr (!kTotal) {
+                        fetch_own<kTok, T>(a.x, a.sx, next, a.total, c0, a.D);
+                        fetch_own<kTok, T>(a.i, a.si, next, a.total, c0, a.D);
+                    }
                 }
             }
             if (left < kTok) close_rows<kTok>(gs, left);
@@ -920,7 +944,7 @@ RecArgs args_of(const kda_recurrence_shape* sh) {
 // Token tensors in whole 16-byte units?
 bool whole_units(const kda_recurrence_shape* sh, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> strides) {
     const int unit = sh->dtype == KDA_BF16 ? 8 : 4;
-    bool ok = sh->D % 8 == 0;
+    bool ok = sh->D % unit == 0;
     for (const void* p : ptrs) ok = ok && !misaligned(p);
     for (const int64_t s : strides) ok = ok && s % unit == 0 && s < (int64_t(1) << 36);    // of tensor maps: 2^40 bytes
     return ok;
