@@ -324,7 +324,8 @@ kda_status kda_recurrence_decode(const kda_recurrence_shape* shape, const void* 
  * that they may be columns of one projection; all pointers 16-byte aligned. The outputs
  * are what kda_linattn_fwd and kda_linattn_bwd read. Weights [head_dim] fp32 (NULL reads as 1),
  * inv_freq [rotary_dim / 2] fp32, finite, positions [tokens] int64, any value. Sums, norms and
- * rotations are fp32, rounded once to the outputs' type. */
+ * rotations are fp32, rounded once to the outputs' type; a row's sum of squares has to be within
+ * fp32's range (values below about 1e18). */
 typedef struct {
     int64_t tokens;
     int32_t q_heads, k_heads;   /* at least one of q; k may have none (its pointers are then not read) */

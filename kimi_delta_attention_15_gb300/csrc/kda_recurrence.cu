@@ -4,8 +4,27 @@
 //   G_t = dy_t + a_{t+1} G_{t+1}   (dhT in place of the second after a sequence's last token)
 //   dx = G m i,  di_raw = G m x i (1 - i),  dh0 = a G at the first token
 //   du u = G (i x a^2 u / m - u a h_{t-1}),  dg_raw = du u (1 - s),  dA_log = sum du u
-// em = 1 - a is what the arithmetic holds: -expm1(-u), a series for small u, so that h += b - em h keeps
-// fp32's precision over memories of any length, and m = sqrt(em (2 - em)) has no cancellation.
+// n = a - 1 = expm1(-u) is what the arithmetic holds, by a polynomial for small u, so that h += n h + b keeps fp32's
+// precision over memories of any length, and m = sqrt(-n (2 + n)) has no cancellation. A run of tokens does the same to
+// a state as one token, h += N h + B with N = expm1(-sum u), so runs are joined like tokens.
+// HBM is the floor: 8 bytes a token and channel forward in bf16, 14 backward, at some 30 and 55 instructions, which
+// the SMs issue in about as long. One pass over the data, therefore, with the scan inside it:
+//  - a warp scans 16 (backward 8) tokens of 64 channels on their own and keeps their n and b in registers; the runs of a
+//    block's warps meet in shared memory, those of a cluster's blocks in distributed shared memory; from the state that
+//    so comes to it the warp then goes over its tokens once more. Tokens arrive by tensor copies, the next ones on their
+//    way meanwhile.
+//  - Sequences need no tables: the tokens are one long axis, on which a sequence's first token takes its initial state
+//    in place of the state before it. Chunks of 64 tokens are cut without regard to sequences, so ragged batches
+//    load the blocks evenly, and a warp looks up which sequence its tokens are of.
+//  - The backward needs the states before its tokens: the forward keeps the state before every 64th token (a
+//    thirty-second of a bf16 tensor), each warp's own scan forwards gives the rest.
+// Measured (us, and times the floor): forward bf16 8192 x 12288 160 (1.33), 8192 x 4096 69 (1.7), packed six sequences 8192 x
+// 4096 with states 75 (1.9), 8192 x 1024 38 (3.7), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 358 (1.7), 8192 x 4096 139 (2.0),
+// 8192 x 1024 67 (3.8), fp32 8192 x 4096 176 (1.25), 65537 x 256 141 (2.0). Rows that are not whole 16-byte units, lane by lane:
+// forward 8192 x 4001 105 (2.7), backward 197 (2.9). What bounds them is neither DRAM (half of its peak) nor a pipe (issue
+// slots 54%, MUFU a quarter, FMA a third): 16 warps of 128 registers an SM wait for one another at every step (the dependent
+// arithmetic of a warp's tokens, the block's barrier, 0.5 us of exchange in a cluster); blocks without a cluster
+// take 1.23 (forward) and 1.5 times the floor, which is what a step costs alone.
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -20,7 +39,7 @@ void set_last_error_text(const char* msg);
 
 namespace {
 constexpr int kBlock = KDA_RECURRENCE_BLOCK;
-constexpr int kCh = 64;              // channels of a block, two to a lane
+constexpr int kCh = 64;              // channels of a block, two to a lane: rows of 128 bytes in bf16
 constexpr int kMostRanks = 8;
 constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -346,9 +365,11 @@ template <int kCount> __device__ __forceinline__ uint32_t bits_of(const uint8_t*
 // and sends the block's to the others of the cluster, `take` waits for theirs and gives the state (adjoint) that comes to
 // this warp, and in `carry` the one that leaves the step. Warps and ranks follow one another in the order of the scan,
 // `w` and `r` their places in it. kTotal: only what all the steps so far do, in `total`.
-// The blocks' sums travel over distributed shared memory with their own completion: a barrier of the cluster would make
-// every thread wait for all its stores (a third of the time). Two steps' sums are kept, and nobody sends a third
-// before all have read the first: a block's sum of the step between left it after that.
+// The blocks' sums travel over distributed shared memory with their own completion: with a barrier of the cluster every
+// thread waited for all its stores (8192 x 12288 forward 224 -> 206 us, backward 493 -> 459). Two steps' sums are kept, and nobody sends
+// a third before all have read the first: a block's sum of the step between left it after that. (Waiting for no more than
+// each rank needs, so that blocks run apart, with three steps' sums, took as long; one polling warp and a barrier for the
+// others 378 instead of 359 us backward.)
 template <int kWarps>
 __device__ __forceinline__ void post(Shares<kWarps>& sh, int step, int ranks, int r, int w, const Run& own, bool fresh) {
     const int lane = threadIdx.x & 31, parity = step & 1;
@@ -429,6 +450,8 @@ constexpr int kTile = kBlock * kCh;
 // tokens, its blocks the chunks of a step next to one another, a warp kTok tokens of a chunk, a lane two channels. kVec: rows
 // in whole 16-byte units, which arrive and leave by tensor copies; else every lane moves its own channels.
 // kTotal: only what the segment does to a state, for the segments after it.
+// 16 tokens to a warp, 4 warps a block: half the joining of 8 tokens and 8 warps (206 -> 187 us); 4 blocks an SM with one stage
+// and the chunk after it fetched into L2 rather than 3 with two stages (8192 x 4096 88 -> 69 us).
 constexpr int kFwdTok = 16, kFwdThreads = kBlock / kFwdTok * 32;      // tokens of a warp
 template <typename T, bool kVec, bool kTotal>
 __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
@@ -558,7 +581,10 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
     if (a.ranks > 1) cluster_wait();
 }
 
-// The same grid, tokens from the last to the first: chunks, ranks and warps in that order.
+// The same grid, tokens from the last to the first: chunks, ranks and warps in that order. A warp's 8 tokens hold 80 of 128
+// registers (the gates' exponentials, n, b, the states before). In bf16 the gradients take the inputs' places in
+// shared memory and leave by tensor copies, with two stages (8192 x 12288 359 us; stored from registers 378); in fp32 two
+// stages have no room: one, the chunk after it fetched into L2, gradients from registers.
 template <typename T, bool kTotal> constexpr int kBwdStages = sizeof(T) == 2 ? 2 : 1;
 constexpr int kBwdTok = 8, kBwdThreads = kBlock / kBwdTok * 32;
 template <typename T, bool kVec, bool kTotal>
