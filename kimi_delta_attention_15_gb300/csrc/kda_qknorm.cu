@@ -201,6 +201,7 @@ template <typename T, bool kOut> struct Walk {
 template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bounds__(kThreads, kBlocksPerSM<kBwd>) qknorm_kernel(const QkArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kN = kStages<T, kBwd>, kR = kRows, kStage = kRing / kN, kHalf = kStage / 2;
+    static_assert(kR == 2, "the rows that `read` sums");
     static_assert(kN >= 2 && kN <= kMostStages && 32 * 8 * kR * (int)sizeof(T) <= (kBwd ? kHalf : kStage), "a block in a stage");
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* const ring = smem + warp * kRing;
@@ -287,11 +288,6 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
                     g[i] = load<kInterleaved>(in ? dfrom + mine1 + i * width : zeros, in ? dfrom + mine2 + i * width : zeros);
                 }
             }
-            __syncwarp();
-            if (ahead.item < items) {
-                if (lane == 0) fetch(stage);
-                ahead.next(a, step, rows);
-            }
             float ss[kR];
             [[maybe_unused]] float gx[kR];
 #pragma unroll
@@ -318,6 +314,16 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
                 add(8); add(4); add(2); add(1);
             } else {
                 for (int o = a.lanes >> 1; o > 0; o >>= 1) add(o);
+            }
+            // The stage takes later rows once every lane has these in registers, which the sums of all of them show. A barrier
+            // of the warp alone does not: the last reads may still be on their way when the copy is issued, and rows of
+            // two blocks were mixed (heads of 200 in fp32, one row in ten).
+            float read = ss[0] + ss[kR - 1];
+            if constexpr (kBwd) read += gx[0] + gx[kR - 1];
+            if (!__all_sync(0xffffffffu, __float_as_uint(read) != 0x7fc0deadu)) __nanosleep(1000);      // no sum has these bits
+            if (ahead.item < items) {
+                if (lane == 0) fetch(stage);
+                ahead.next(a, step, rows);
             }
             T *to1 = at.p + mine1, *to2 = at.p + mine2;
 #pragma unroll

@@ -210,6 +210,19 @@ def test_the_same_bits_and_captured():
         assert all(torch.equal(got[n], want[n]) for n in want)
 
 
+@pytest.mark.parametrize("T,Hq,Hk,head,rotary,interleaved,dtype", [
+    (387, 18, 9, 240, 240, True, F32), (198, 72, 9, 200, 0, False, F32), (387, 18, 9, 192, 192, True, F32), (900, 72, 9, 128, 128, False, F32),
+    (900, 72, 9, 256, 256, False, F32), (900, 72, 9, 128, 128, False, BF), (3000, 27, 9, 72, 72, True, BF)])
+def test_rows_stay_until_they_are_read(T, Hq, Hk, head, rotary, interleaved, dtype):
+    """Several blocks of rows to a warp, which arrive in the places of those before them, many times over."""
+    c = make(T, Hq, Hk, head, rotary, dtype, seed=5)
+    want = run(c, interleaved)
+    verify(c, want, interleaved)
+    for _ in range(60):
+        got = run(c, interleaved)
+        assert all(torch.equal(got[n], want[n]) for n in want)
+
+
 def test_on_other_streams_at_once():
     cases = [make(900, 6, 2, 128, 128, seed=s) for s in range(3)]
     want = [run(c) for c in cases]
