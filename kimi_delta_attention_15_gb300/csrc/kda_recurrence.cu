@@ -5,8 +5,9 @@
 //   dx = G m i,  di_raw = G m x i (1 - i),  dh0 = a G at the first token
 //   du u = G (i x a^2 u / m - u a h_{t-1}),  dg_raw = du u (1 - s),  dA_log = sum du u
 // n = a - 1 = expm1(-u) is what the arithmetic holds, by a polynomial for small u, so that h += n h + b keeps fp32's
-// precision over memories of any length, and m = sqrt(-n (2 + n)) has no cancellation. A run of tokens does the same to
-// a state as one token, h += N h + B with N = expm1(-sum u), so runs are joined like tokens.
+// precision over memories of any length, and m = sqrt(-n (2 + n)) has no cancellation. A run of tokens does to a state
+// what a token does, h += N h + B with N = expm1(-sum u), so runs are joined like tokens; where a run decays by more than a
+// third it is h = exp(-sum u) h + B, since h + N h would leave an error of the old state's size.
 // HBM is the floor: 8 bytes a token and channel forward in bf16, 14 backward, at some 30 and 55 instructions, which
 // the SMs issue in about as long. One pass over the data, therefore, with the scan inside it:
 //  - a warp scans 16 (backward 8) tokens of 64 channels on their own and keeps their n and b in registers; the runs of a
@@ -18,10 +19,10 @@
 //    load the blocks evenly, and a warp looks up which sequence its tokens are of.
 //  - The backward needs the states before its tokens: the forward keeps the state before every 64th token (a
 //    thirty-second of a bf16 tensor), each warp's own scan forwards gives the rest.
-// Measured (us, and times the floor): forward bf16 8192 x 12288 160 (1.33), 8192 x 4096 69 (1.7), packed six sequences 8192 x
-// 4096 with states 75 (1.9), 8192 x 1024 38 (3.7), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 358 (1.7), 8192 x 4096 139 (2.0),
-// 8192 x 1024 67 (3.8), fp32 8192 x 4096 176 (1.25), 65537 x 256 141 (2.0). Rows that are not whole 16-byte units, lane by lane:
-// forward 8192 x 4001 105 (2.7), backward 197 (2.9). What bounds them is neither DRAM (half of its peak) nor a pipe (issue
+// Measured (us, and times the floor): forward bf16 8192 x 12288 163 (1.35), 8192 x 4096 71 (1.8), packed six sequences 8192 x
+// 4096 with states 77 (1.9), 8192 x 1024 38 (3.7), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 360 (1.7), 8192 x 4096 140 (2.0),
+// 8192 x 1024 69 (3.9), fp32 8192 x 4096 174 (1.24), 65537 x 256 142 (2.0). Rows that are not whole 16-byte units, lane by lane:
+// forward 8192 x 4001 105 (2.7), backward 199 (2.9). What bounds them is neither DRAM (half of its peak) nor a pipe (issue
 // slots 54%, MUFU a quarter, FMA a third): 16 warps of 128 registers an SM wait for one another at every step (the dependent
 // arithmetic of a warp's tokens, the block's barrier, 0.5 us of exchange in a cluster); blocks without a cluster
 // take 1.23 (forward) and 1.5 times the floor, which is what a step costs alone.
@@ -107,7 +108,7 @@ struct RecArgs {
     const int64_t* cu;
     void *y, *dx, *dg, *di;
     float *hT, *kept, *dh0, *part;
-    float4* seg;         // [segments][channel pairs] what each segment does to a state
+    float4* seg;         // [segments][channel pairs] each segment's summed exponents and what it makes of a zero
     int* seg_fresh;      // [segments] whether a sequence starts (ends, backwards) in it
     uint8_t* ws;
     int64_t D, sx, sg, si, sy, sdx, sdg, sdi;
@@ -115,20 +116,29 @@ struct RecArgs {
 };
 
 // ---------------------------------------------------------------- two channels of a lane
-// What a run of tokens does to a state that comes to it: h + n h + b, n = its decay less 1, as for a single token. Where a
-// sequence starts in it, which is the same for all channels, b alone (not 0 h + b: a state that is no number ends with
-// its sequence).
+// What a run of tokens does to a state that comes to it. Where it decays little, h + (v h + b) with v < 0 its decay less 1, as for
+// a single token; where it decays much, v h + b with v >= 0 the decay itself, so that what is left of a state is as exact as
+// the state was. (The first form alone took 160 us forward at 8192 x 12288 where this takes 163; the form beside the runs, not in
+// v's sign, 170.) Where a sequence starts in it, which is the same for all channels, b alone (not 0 h + b: a state that is
+// no number ends with its sequence).
 struct Run {
-    f32x2 n, b;
+    f32x2 v, b;
 };
 __device__ __forceinline__ Run run_of(const float4& s) { return {two(s.x, s.y), two(s.z, s.w)}; }
 __device__ __forceinline__ float4 held(const Run& r) {
-    const float2 n = parts(r.n), b = parts(r.b);
-    return make_float4(n.x, n.y, b.x, b.y);
+    const float2 v = parts(r.v), b = parts(r.b);
+    return make_float4(v.x, v.y, b.x, b.y);
 }
-__device__ __forceinline__ f32x2 over(const Run& r, bool fresh, f32x2 h) { return fresh ? r.b : advance(h, r.n, r.b); }
-// first s, then t; `fresh` is t's
-__device__ __forceinline__ Run then(const Run& s, const Run& t, bool fresh) { return {fresh ? t.n : advance(s.n, t.n, t.n), over(t, fresh, s.b)}; }
+// of the summed exponents (to base 2) and what the run makes of a zero
+__device__ __forceinline__ Run run_from(f32x2 sum, f32x2 b) {
+    const float2 n = parts(minus_decayed(sum)), a = parts(exp2_of(sum)), at = parts(sum);
+    constexpr float kNone = -1.1754944e-38f;      // no decay at all is still a decay less 1
+    return {two(at.x > -0.5f ? fminf(n.x, kNone) : a.x, at.y > -0.5f ? fminf(n.y, kNone) : a.y), b};
+}
+__device__ __forceinline__ f32x2 over(const Run& r, bool fresh, f32x2 h) {
+    const float2 v = parts(r.v);
+    return fresh ? r.b : fma2(two(v.x < 0 ? 1.0f : 0.0f, v.y < 0 ? 1.0f : 0.0f), h, fma2(r.v, h, r.b));
+}
 
 template <typename T> struct Raw;           // two channels as they are stored
 template <> struct Raw<uint16_t> { using Two = uint32_t; };
@@ -321,6 +331,10 @@ __device__ __forceinline__ void send(uint32_t to, const float4& v, uint32_t bar)
                  "f"(v.z), "f"(v.w), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ void send(uint32_t to, const float2& v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(v.x), "f"(v.y), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void send(uint32_t to, uint32_t v, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(bar) : "memory");
 }
@@ -328,6 +342,7 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t v, uint32_t bar) {
 template <int kWarps> struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
     float4 warp[2][kWarps][32];
     float4 rank[2][kMostRanks][32];
+    float2 warp_sum[2][kWarps][32], rank_sum[2][kMostRanks][32];     // their summed exponents
     uint8_t warp_fresh[2][8];
     uint32_t rank_fresh[2][kMostRanks];
     uint64_t full[2];    // the stages' loads
@@ -370,34 +385,45 @@ template <int kCount> __device__ __forceinline__ uint32_t bits_of(const uint8_t*
 // a third before all have read the first: a block's sum of the step between left it after that. (Waiting for no more than
 // each rank needs, so that blocks run apart, with three steps' sums, took as long; one polling warp and a barrier for the
 // others 378 instead of 359 us backward.)
-template <int kWarps>
-__device__ __forceinline__ void post(Shares<kWarps>& sh, int step, int ranks, int r, int w, const Run& own, bool fresh) {
+template <int kWarps, bool kTotal>
+__device__ __forceinline__ void post(Shares<kWarps>& sh, int step, int ranks, int r, int w, f32x2 sum, f32x2 b, bool fresh) {
     const int lane = threadIdx.x & 31, parity = step & 1;
-    sh.warp[parity][w][lane] = held(own);
+    sh.warp[parity][w][lane] = held(run_from(sum, b));
+    sh.warp_sum[parity][w][lane] = parts(sum);
     if (lane == 0) sh.warp_fresh[parity][w] = fresh;
     __syncthreads();
     if (ranks > 1 && w == 0) {
-        if (lane == 0) mbar_arrive_expect_tx(&sh.sent[parity], (uint32_t)ranks * (32 * sizeof(float4) + 4));
+        constexpr uint32_t bytes = 32 * (sizeof(float4) + (kTotal ? sizeof(float2) : 0)) + 4;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.sent[parity], (uint32_t)ranks * bytes);
         const uint32_t warps = bits_of<kWarps>(sh.warp_fresh[parity]);
-        Run s = own;
+#pragma unroll
+        for (int v = 1; v < kWarps; ++v) {
+            const float2 more = sh.warp_sum[parity][v][lane];
+            sum = add2(sum, two(more.x, more.y));
+        }
         if (warps == 0) {
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), false);
+            for (int v = 1; v < kWarps; ++v) b = over(run_of(sh.warp[parity][v][lane]), false, b);
         } else {
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) s = then(s, run_of(sh.warp[parity][v][lane]), (warps >> v & 1) != 0);
+            for (int v = 1; v < kWarps; ++v) b = over(run_of(sh.warp[parity][v][lane]), (warps >> v & 1) != 0, b);
         }
-        const float4 f = held(s);
+        const float4 own = held(run_from(sum, b));
         for (int k = 0; k < ranks; ++k) {
             const uint32_t bar = at_rank(&sh.sent[parity], k);
-            send(at_rank(&sh.rank[parity][r][lane], k), f, bar);
+            send(at_rank(&sh.rank[parity][r][lane], k), own, bar);
+            if constexpr (kTotal) send(at_rank(&sh.rank_sum[parity][r][lane], k), parts(sum), bar);
             if (lane == 0) send(at_rank(&sh.rank_fresh[parity][r], k), warps != 0 ? 1u : 0u, bar);
         }
     }
 }
+struct Total {           // of the steps so far
+    f32x2 sum, b;
+    bool fresh;
+};
 template <int kWarps, bool kTotal>
-__device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, int r, int w, f32x2& carry, Run& total, bool& total_fresh,
-                                      Waits& wait, uint8_t* ws) {
+__device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, int r, int w, f32x2& carry, Total& total, Waits& wait,
+                                      uint8_t* ws) {
     const int lane = threadIdx.x & 31, parity = step & 1;
     const uint32_t warps = bits_of<kWarps>(sh.warp_fresh[parity]);
     uint32_t all = warps;
@@ -409,8 +435,10 @@ __device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, i
         const int count = ranks > 1 ? ranks : kWarps;
         for (int k = 0; k < count; ++k) {
             const bool f = (all >> k & 1) != 0;
-            total = then(total, run_of((ranks > 1 ? &sh.rank[parity][0] : &sh.warp[parity][0])[k][lane]), f);
-            total_fresh = total_fresh || f;
+            const float2 more = ranks > 1 ? sh.rank_sum[parity][k][lane] : sh.warp_sum[parity][k][lane];
+            total.b = over(run_of((ranks > 1 ? &sh.rank[parity][0] : &sh.warp[parity][0])[k][lane]), f, total.b);
+            total.sum = add2(total.sum, two(more.x, more.y));
+            total.fresh = total.fresh || f;
         }
         return 0;
     }
@@ -436,7 +464,10 @@ __device__ __forceinline__ f32x2 into_segment(const RecArgs& a, int seg, int64_t
     f32x2 h = 0;
     const int64_t pairs = (a.D + 1) / 2;
     if (c < a.D)
-        for (int s = 0; s < seg; ++s) h = over(run_of(a.seg[s * pairs + c / 2]), a.seg_fresh[s] != 0, h);
+        for (int s = 0; s < seg; ++s) {
+            const float4 p = a.seg[s * pairs + c / 2];
+            h = over(run_from(two(p.x, p.y), two(p.z, p.w)), a.seg_fresh[s] != 0, h);
+        }
     return h;
 }
 
@@ -495,8 +526,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
     if constexpr (kTotal) grid_launch_next();
     else grid_wait_before();           // the pass that found what segments do, where there is one
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
-    Run total{0, 0};
-    bool total_fresh = false;
+    Total total{0, 0, false};
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
         pass_empty<kWarps, kVec>(a, a.hT, a.h0, c);
@@ -545,9 +575,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
             if (events) gates(std::true_type());
             else gates(std::false_type());
         }
-        post<kWarps>(sh, step, a.ranks, r, warp, Run{minus_decayed(sum), h}, events && ev.starts);
+        post<kWarps, kTotal>(sh, step, a.ranks, r, warp, sum, h, events && ev.starts);
         if (kVec && threadIdx.x == 0 && !wait.lost) load(step + 1);     // every warp has read this step's
-        h = take<kWarps, kTotal>(sh, step, a.ranks, r, warp, carry, total, total_fresh, wait, a.ws);
+        h = take<kWarps, kTotal>(sh, step, a.ranks, r, warp, carry, total, wait, a.ws);
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
             if (left > 0) {
@@ -575,8 +605,11 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
     if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, 1);
     if (a.ranks > 1) cluster_arrive();     // no block ends before the others have sent it all
     if constexpr (kTotal) {
-        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
-        if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
+        if (warp == 0 && r == 0 && c < a.D) {
+            const float2 t = parts(total.sum), z = parts(total.b);
+            a.seg[seg * ((a.D + 1) / 2) + c / 2] = make_float4(t.x, t.y, z.x, z.y);
+        }
+        if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total.fresh;
     }
     if (a.ranks > 1) cluster_wait();
 }
@@ -639,8 +672,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     if constexpr (kTotal) grid_launch_next();
     else grid_wait_before();           // the pass that found what segments do, where there is one
     f32x2 carry = kTotal ? 0 : into_segment(a, seg, c);
-    Run total{0, 0};
-    bool total_fresh = false;
+    Total total{0, 0, false};
     if constexpr (!kTotal) {
         if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
         pass_empty<kWarps, kVec>(a, a.dh0, a.dhT, c);
@@ -715,15 +747,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
             if (events) sums(std::true_type());
             else sums(std::false_type());
         }
-        const f32x2 decay = minus_decayed(sum);
         if constexpr (!kTotal) {
-            ahead.warp[step & 1][warp][lane] = held(Run{decay, h});
+            ahead.warp[step & 1][warp][lane] = held(run_from(sum, h));
             if (lane == 0) {
                 ahead.fresh[step & 1][warp] = events && ev.starts;
                 if (kByCopy) bulk_wait_read_all();      // the gradients of the step before have left
             }
         }
-        post<kWarps>(sh, step, a.ranks, r, kWarps - 1 - warp, Run{decay, G}, events && ev.ends);
+        post<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, sum, G, events && ev.ends);
         f32x2 before[kTok];
         if constexpr (kTotal) {
             if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);
@@ -747,7 +778,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                 else states(std::false_type());
             }
         }
-        G = take<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, carry, total, total_fresh, wait, a.ws);
+        G = take<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, carry, total, wait, a.ws);
         if constexpr (!kTotal) {
             if (left > 0) {
                 T* to_x = static_cast<T*>(a.dx) + (int64_t)(t0 + kTok - 1) * a.sdx + c;
@@ -809,8 +840,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     if (kVec && threadIdx.x == 0) wait.rest(sh.full, steps, kStages);
     if (a.ranks > 1) cluster_arrive();     // no block ends before the others have sent it all
     if constexpr (kTotal) {
-        if (warp == 0 && r == 0 && c < a.D) a.seg[seg * ((a.D + 1) / 2) + c / 2] = held(total);
-        if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total_fresh;
+        if (warp == 0 && r == 0 && c < a.D) {
+            const float2 t = parts(total.sum), z = parts(total.b);
+            a.seg[seg * ((a.D + 1) / 2) + c / 2] = make_float4(t.x, t.y, z.x, z.y);
+        }
+        if (threadIdx.x == 0 && r == 0 && blockIdx.y == 0) a.seg_fresh[seg] = total.fresh;
     } else {
         if (a.part) {
             grid_launch_next();

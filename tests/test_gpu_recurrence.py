@@ -133,6 +133,24 @@ def test_memories_of_many_thousand_tokens(shift, A):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,D", [([40], 8), ([70, 130], 72), ([5000, 3], 24), ([200, 1900, 1000], 136), ([300], 2000)])
+def test_states_that_decay_by_many_orders(lens, D, dtype):
+    """A state of 1e14 and its gradient are down at 1 after some thirty tokens, and exact there: a run's decay less 1 on
+    the state before it, added to that state, would leave an absolute error of 1e-7 of it."""
+    c = make(lens, D, dtype, A=0.7, spread=0.2)
+    c["h0"], c["dhT"] = 1e14 * c["h0"], 1e14 * c["dhT"]
+    verify(c, run(c))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("A,shift", [(2.0, 4.0), (2.0, 0.0), (0.0, 4.0)])
+def test_strong_decays(A, shift, dtype):
+    for lens, D in (([2500, 64, 1436], 136), ([4000], 128), ([9000, 17], 9)):
+        c = make(lens, D, dtype, shift=shift, A=A, spread=5.0, fused=True)
+        verify(c, run(c))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("A", [-20.0, 3.0, 9.0])
 def test_wide_gates(A, dtype):
     c = make([100, 90], 32, dtype, A=A, spread=20.0)
