@@ -700,7 +700,7 @@ def recurrence_fwd(x, g_raw, i_raw, A_log, h0=None, cu_seqlens=None, *, B: int =
     if workspace is None:
         workspace = recurrence_alloc_workspace(shape, x.device)
     if y is None:
-        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+        y = torch.empty_like(x)
     if hT is None and want_hT:
         hT = torch.empty((N, D), dtype=_F32, device=x.device)
     if kept is None and want_kept:
@@ -743,8 +743,8 @@ def recurrence_bwd(x, g_raw, i_raw, A_log, dy, kept, workspace=None, h0=None, cu
     if workspace is None:
         workspace = recurrence_alloc_workspace(shape, x.device, backward=True)
     if grads is None:
-        dx, dg, di = (torch.empty(x.shape, dtype=dtype, device=x.device) for _ in range(3))
-        grads = dict(dx=dx, dg_raw=dg, di_raw=di, dA_log=torch.empty(D, dtype=_F32, device=x.device) if want_dA_log else None,
+        dx, dg, di = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        grads = dict(dx=dx, dg_raw=dg, di_raw=di, dA_log=torch.empty_like(A_log) if want_dA_log else None,
                      dh0=torch.empty((N, D), dtype=_F32, device=x.device) if want_dh0 else None)
     else:
         dx, dg, di = (grads.get(n) for n in ("dx", "dg_raw", "di_raw"))
@@ -777,7 +777,7 @@ def recurrence_decode(x, g_raw, i_raw, A_log, state, *, y=None, stream=None):
     shape = RecurrenceShape(n, 1, D, n, _NORM_DTYPES[dtype], 0, _rows("x", x, n, D, dtype, dev),
                             _rows("g_raw", g_raw, n, D, dtype, dev), _rows("i_raw", i_raw, n, D, dtype, dev))
     if y is None:
-        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+        y = torch.empty_like(x)
     else:
         shape.y_stride = _rows("y", y, n, D, dtype, dev)
     code = lib.kda_recurrence_decode(ctypes.byref(shape), x.data_ptr(), g_raw.data_ptr(), i_raw.data_ptr(), A_log.data_ptr(),
@@ -829,13 +829,13 @@ def qknorm_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq
     lib = _lib or load()
     shape, dev = _qknorm_shape_of(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, [])
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q)
     else:
         shape.q_out_stride = _rows("q_out", q_out, shape.tokens, shape.q_heads * shape.head_dim, q.dtype, dev)
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty_like(k)
     else:
         shape.k_out_stride = _rows("k_out", k_out, shape.tokens, shape.k_heads * shape.head_dim, q.dtype, dev)
     code = lib.kda_qknorm_fwd(ctypes.byref(shape), q.data_ptr(), _address(k), _address(q_weight), _address(k_weight),
@@ -870,8 +870,8 @@ def qknorm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positions=Non
     if grads is None:
         def weight(wanted):
             return torch.empty(shape.head_dim, dtype=_F32, device=q.device) if wanted else None
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+        dq = torch.empty_like(q)
+        dk = torch.empty_like(k) if k is not None else None
         grads = dict(dq=dq, dk=dk, dq_weight=weight(want_dweight), dk_weight=weight(want_dweight and k is not None))
     else:
         dq, dk = grads.get("dq"), grads.get("dk")
