@@ -20,8 +20,8 @@
 //  - The backward needs the states before its tokens: the forward keeps the state before every 64th token (a
 //    thirty-second of a bf16 tensor), each warp's own scan forwards gives the rest.
 // Measured (us, and times the floor): forward bf16 8192 x 12288 163 (1.35), 8192 x 4096 71 (1.8), packed six sequences 8192 x
-// 4096 with states 77 (1.9), 8192 x 1024 38 (3.7), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 360 (1.7), 8192 x 4096 140 (2.0),
-// 8192 x 1024 69 (3.9), fp32 8192 x 4096 174 (1.24), 65537 x 256 142 (2.0). Rows that are not whole 16-byte units, lane by lane:
+// 4096 with states 77 (1.9), 8192 x 1024 34 (3.4), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 364 (1.7), 8192 x 4096 142 (2.0),
+// 8192 x 1024 59 (3.3), fp32 8192 x 4096 174 (1.24), 65537 x 256 132 (1.9). Rows that are not whole 16-byte units, lane by lane:
 // forward 8192 x 4001 105 (2.7), backward 199 (2.9). What bounds them is neither DRAM (half of its peak) nor a pipe (issue
 // slots 54%, MUFU a quarter, FMA a third): 16 warps of 128 registers an SM wait for one another at every step (the dependent
 // arithmetic of a warp's tokens, the block's barrier, 0.5 us of exchange in a cluster); blocks without a cluster
@@ -41,7 +41,8 @@ void set_last_error_text(const char* msg);
 namespace {
 constexpr int kBlock = KDA_RECURRENCE_BLOCK;
 constexpr int kCh = 64;              // channels of a block, two to a lane: rows of 128 bytes in bf16
-constexpr int kMostRanks = 8;
+constexpr int kMostRanks = 16;       // blocks of a cluster
+constexpr int kSegRanks = 8;         // of one where segments are scanned twice
 constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -339,10 +340,9 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t v, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(bar) : "memory");
 }
 
-template <int kWarps> struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
+template <int kWarps, bool kTotal> struct Shares {          // what the warps of a block and the blocks of a cluster did, by the step's parity
     float4 warp[2][kWarps][32];
-    float4 rank[2][kMostRanks][32];
-    float2 warp_sum[2][kWarps][32], rank_sum[2][kMostRanks][32];     // their summed exponents
+    float2 warp_sum[2][kWarps][32], rank_sum[2][kTotal ? kSegRanks : 1][32];         // their summed exponents
     uint8_t warp_fresh[2][8];
     uint32_t rank_fresh[2][kMostRanks];
     uint64_t full[2];    // the stages' loads
@@ -386,8 +386,9 @@ template <int kCount> __device__ __forceinline__ uint32_t bits_of(const uint8_t*
 // each rank needs, so that blocks run apart, with three steps' sums, took as long; one polling warp and a barrier for the
 // others 378 instead of 359 us backward.)
 template <int kWarps, bool kTotal>
-__device__ __forceinline__ void post(Shares<kWarps>& sh, int step, int ranks, int r, int w, f32x2 sum, f32x2 b, bool fresh) {
+__device__ __forceinline__ void post(Shares<kWarps, kTotal>& sh, float4 (*rank)[32], int step, int ranks, int r, int w, f32x2 sum, f32x2 b, bool fresh) {
     const int lane = threadIdx.x & 31, parity = step & 1;
+    rank += parity * ranks;
     sh.warp[parity][w][lane] = held(run_from(sum, b));
     sh.warp_sum[parity][w][lane] = parts(sum);
     if (lane == 0) sh.warp_fresh[parity][w] = fresh;
@@ -411,7 +412,7 @@ __device__ __forceinline__ void post(Shares<kWarps>& sh, int step, int ranks, in
         const float4 own = held(run_from(sum, b));
         for (int k = 0; k < ranks; ++k) {
             const uint32_t bar = at_rank(&sh.sent[parity], k);
-            send(at_rank(&sh.rank[parity][r][lane], k), own, bar);
+            send(at_rank(&rank[r][lane], k), own, bar);
             if constexpr (kTotal) send(at_rank(&sh.rank_sum[parity][r][lane], k), parts(sum), bar);
             if (lane == 0) send(at_rank(&sh.rank_fresh[parity][r], k), warps != 0 ? 1u : 0u, bar);
         }
@@ -422,9 +423,10 @@ struct Total {           // of the steps so far
     bool fresh;
 };
 template <int kWarps, bool kTotal>
-__device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, int r, int w, f32x2& carry, Total& total, Waits& wait,
-                                      uint8_t* ws) {
+__device__ __forceinline__ f32x2 take(Shares<kWarps, kTotal>& sh, const float4 (*rank)[32], int step, int ranks, int r, int w, f32x2& carry,
+                                      Total& total, Waits& wait, uint8_t* ws) {
     const int lane = threadIdx.x & 31, parity = step & 1;
+    rank += parity * ranks;
     const uint32_t warps = bits_of<kWarps>(sh.warp_fresh[parity]);
     uint32_t all = warps;
     if (ranks > 1) {
@@ -436,7 +438,7 @@ __device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, i
         for (int k = 0; k < count; ++k) {
             const bool f = (all >> k & 1) != 0;
             const float2 more = ranks > 1 ? sh.rank_sum[parity][k][lane] : sh.warp_sum[parity][k][lane];
-            total.b = over(run_of((ranks > 1 ? &sh.rank[parity][0] : &sh.warp[parity][0])[k][lane]), f, total.b);
+            total.b = over(run_of((ranks > 1 ? rank : sh.warp[parity])[k][lane]), f, total.b);
             total.sum = add2(total.sum, two(more.x, more.y));
             total.fresh = total.fresh || f;
         }
@@ -445,7 +447,7 @@ __device__ __forceinline__ f32x2 take(Shares<kWarps>& sh, int step, int ranks, i
     f32x2 at;
     if (ranks > 1) {
         f32x2 block;
-        carry = through(sh.rank[parity], all, ranks, r, carry, block);
+        carry = through(rank, all, ranks, r, carry, block);
         through(sh.warp[parity], warps, w, w, block, at);
     } else {
         carry = through(sh.warp[parity], warps, kWarps, w, carry, at);
@@ -488,8 +490,9 @@ template <typename T, bool kVec, bool kTotal>
 __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kTok = kFwdTok, kWarps = kBlock / kTok;
-    Shares<kWarps>& sh = *reinterpret_cast<Shares<kWarps>*>(smem);
-    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps>>);          // x, g, i
+    Shares<kWarps, kTotal>& sh = *reinterpret_cast<Shares<kWarps, kTotal>*>(smem);
+    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps, kTotal>>);          // x, g, i
+    float4 (*const rank)[32] = reinterpret_cast<float4 (*)[32]>(tiles + 3 * kTile);       // [2][ranks], what the cluster's blocks did
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;      // the warp's, as the compiler may know
     const int own_at = warp * kTok * kCh + 2 * lane;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
@@ -575,9 +578,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4) rec_fwd_kernel(const __grid_co
             if (events) gates(std::true_type());
             else gates(std::false_type());
         }
-        post<kWarps, kTotal>(sh, step, a.ranks, r, warp, sum, h, events && ev.starts);
+        post<kWarps, kTotal>(sh, rank, step, a.ranks, r, warp, sum, h, events && ev.starts);
         if (kVec && threadIdx.x == 0 && !wait.lost) load(step + 1);     // every warp has read this step's
-        h = take<kWarps, kTotal>(sh, step, a.ranks, r, warp, carry, total, wait, a.ws);
+        h = take<kWarps, kTotal>(sh, rank, step, a.ranks, r, warp, carry, total, wait, a.ws);
         if constexpr (!kTotal) {
             if (warp == 0 && some && a.kept) store_state<kVec>(a.kept, chunk, c, a.D, h);
             if (left > 0) {
@@ -625,9 +628,10 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr bool kByCopy = kVec && !kTotal && kBwdStages<T, kTotal> == 2;      // gradients leave by tensor copies, from the inputs' places
     constexpr int kTensors = kTotal ? 2 : 4, kStages = kBwdStages<T, kTotal>, kTok = kBwdTok, kWarps = kBlock / kTok;
-    Shares<kWarps>& sh = *reinterpret_cast<Shares<kWarps>*>(smem);
-    Ahead<kWarps>& ahead = *reinterpret_cast<Ahead<kWarps>*>(smem + kBytes<Shares<kWarps>>);      // the states' way, forwards
-    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps>> + kBytes<Ahead<kWarps>>);       // kStages of g, dy, x, i
+    Shares<kWarps, kTotal>& sh = *reinterpret_cast<Shares<kWarps, kTotal>*>(smem);
+    Ahead<kWarps>& ahead = *reinterpret_cast<Ahead<kWarps>*>(smem + kBytes<Shares<kWarps, kTotal>>);      // the states' way, forwards
+    T* const tiles = reinterpret_cast<T*>(smem + kBytes<Shares<kWarps, kTotal>> + kBytes<Ahead<kWarps>>);       // kStages of g, dy, x, i
+    float4 (*const rank)[32] = reinterpret_cast<float4 (*)[32]>(tiles + kStages * kTensors * kTile);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int r = a.ranks > 1 ? cluster_rank() : 0, seg = blockIdx.x / a.ranks;
     const int64_t c0 = (int64_t)blockIdx.y * kCh, c = c0 + 2 * lane;
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                 if (kByCopy) bulk_wait_read_all();      // the gradients of the step before have left
             }
         }
-        post<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, sum, G, events && ev.ends);
+        post<kWarps, kTotal>(sh, rank, step, a.ranks, r, kWarps - 1 - warp, sum, G, events && ev.ends);
         f32x2 before[kTok];
         if constexpr (kTotal) {
             if (kVec && threadIdx.x == 0 && !wait.lost) load(step + kStages);
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                 else states(std::false_type());
             }
         }
-        G = take<kWarps, kTotal>(sh, step, a.ranks, r, kWarps - 1 - warp, carry, total, wait, a.ws);
+        G = take<kWarps, kTotal>(sh, rank, step, a.ranks, r, kWarps - 1 - warp, carry, total, wait, a.ws);
         if constexpr (!kTotal) {
             if (left > 0) {
                 T* to_x = static_cast<T*>(a.dx) + (int64_t)(t0 + kTok - 1) * a.sdx + c;
@@ -934,30 +938,41 @@ kda_status check_shape(const kda_recurrence_shape* sh, bool packed) {
     return KDA_OK;
 }
 
+// How many clusters of r blocks run at once with m blocks on an SM, as the device tells ([m - 1][r]): its groups of SMs are not all
+// of one size.
+constexpr int kMostPerSM = 4;
+constexpr int kMostSegs = 64;        // as many flags are in the workspace
+using Fits = std::atomic<int16_t>[kMostPerSM][kMostRanks + 1];
+
 // How the tokens are cut: clusters of `ranks` blocks for each tile of channels, each over one of `segs` segments.
 // Blocks of a cluster take chunks next to one another and exchange what they did over distributed shared memory,
-// one pass over the data; where the channels are too few to fill the GPU with clusters of eight, segments may, which
+// one pass over the data; where the channels are too few to fill the GPU with clusters, segments may, which
 // read the inputs of a scan twice (once to find what each does to a state).
 struct Plan {
     int tiles, chunks, ranks, segs, seg_chunks;
 };
-// A step of m blocks on an SM takes about (m = 1) + (m - 1) more + the exchange, in us, as fitted to measured times
-// (T = 8192, D = 12288 bf16 forward: 1, 2, 3, 4 ranks 249, 189, 161, 190 us, by this 276, 198, 165, 215; D = 1024 with 8
-// ranks and 1, 2, 4 segments 51, 53, 40 us, by this 47, 57, 41).
+// A step of m blocks on an SM takes about (m = 1) + (m - 1) more + the exchange, in us, as fitted to measured times of
+// 1 to 16 ranks at 256 to 12288 channels (bf16 forward at T = 8192, D = 12288: 1, 2, 3, 4 ranks 254, 192, 165, 196 us, by this 280, 190,
+// 171, 214; D = 2560: 6, 8, 10, 12, 16 ranks 67, 60, 53, 56, 69, by this 68, 63, 53, 55, 78; D = 1024: 8, 12, 16 ranks 51, 41, 37, 4 segments of 8 40).
 struct Cost {
-    float step, more, rank, passes;      // passes: what two of them take, in times of one
+    float step, more, meet, rank, passes;     // meet + rank (r - 1): the exchange; passes: what two of them take, in times of one
     int per_sm;
 };
-float wave(const Cost& c, int64_t blocks, int ranks) {
-    // a cluster's blocks are on one of 8 groups of 19 SMs
-    const int64_t full = 8 * (int64_t)(kSMs / 8 * c.per_sm / ranks * ranks), rest = blocks % full, m = (rest + kSMs - 1) / kSMs;
-    const float one = c.step + (ranks > 1 ? 0.5f + c.rank * (float)(ranks - 1) : 0.0f);
-    return (float)(blocks / full) * (one + c.more * (c.per_sm - 1)) + (m ? one + c.more * (float)(m - 1) : 0.0f);
+// `clusters` of `ranks` blocks; 0 where none fits
+float wave(const Cost& c, const Fits& fits, int clusters, int ranks) {
+    auto fit = [&](int m) { return (int)fits[m - 1][ranks].load(std::memory_order_relaxed); };
+    const int full = fit(c.per_sm);
+    if (full <= 0) return 0.0f;
+    const int rest = clusters % full;
+    const float one = c.step + (ranks > 1 ? c.meet + c.rank * (float)(ranks - 1) : 0.0f);
+    int m = 1;
+    while (m < c.per_sm && fit(m) < rest) ++m;
+    return (float)(clusters / full) * (one + c.more * (float)(c.per_sm - 1)) + (rest ? one + c.more * (float)(m - 1) : 0.0f);
 }
-Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
+Plan plan_of(const kda_recurrence_shape* sh, bool backward, const Fits& fits) {
     const bool bf16 = sh->dtype == KDA_BF16;
-    const Cost cost = backward ? (bf16 ? Cost{2.55f, 1.2f, 0.2f, 1.45f, 2} : Cost{3.75f, 1.2f, 0.2f, 1.45f, 2})
-                               : (bf16 ? Cost{1.6f, 0.55f, 0.06f, 2.0f, 4} : Cost{1.7f, 0.9f, 0.06f, 2.0f, 2});
+    const Cost cost = backward ? (bf16 ? Cost{2.6f, 1.2f, 0.1f, 0.1f, 1.45f, 2} : Cost{3.0f, 1.5f, 0.35f, 0.12f, 1.45f, 2})
+                               : (bf16 ? Cost{1.6f, 0.55f, 0.3f, 0.09f, 2.0f, 4} : Cost{1.6f, 0.75f, 0.3f, 0.09f, 2.0f, 2});
     constexpr float kPass = 5.0f;
     Plan p;
     p.tiles = (int)((sh->D + kCh - 1) / kCh);
@@ -966,15 +981,15 @@ Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
     float least = 0.0f;
     for (int r = 1; r <= kMostRanks && r <= (p.chunks > 1 ? p.chunks : 1); ++r) {
         const int steps = (p.chunks + r - 1) / r;
-        const float t = kPass + (float)steps * wave(cost, (int64_t)p.tiles * r, r) + (backward && r > 1 ? 3.0f : 0.0f);    // the sum of shares
-        if (r == 1 || t < least) { least = t; p.ranks = r; }
+        const float w = wave(cost, fits, p.tiles, r), t = kPass + (float)steps * w + (backward && r > 1 ? 3.0f : 0.0f);    // the sum of shares
+        if (w > 0.0f && (r == 1 || t < least)) { least = t; p.ranks = r; }
     }
-    const int64_t slots = (int64_t)kSMs * cost.per_sm, clusters = (int64_t)p.tiles * kMostRanks;
-    for (const int s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-        const int steps = (p.chunks + s * kMostRanks - 1) / (s * kMostRanks);
-        if (s * clusters > slots || steps < 2) break;
-        const float t = cost.passes * (kPass + (float)steps * wave(cost, clusters * s, kMostRanks));
-        if (t < least) { least = t; p.ranks = kMostRanks; p.segs = s; }
+    const int here = fits[cost.per_sm - 1][kSegRanks].load(std::memory_order_relaxed), room = kSMs * cost.per_sm / kSegRanks;
+    for (int s = 2; s <= kMostSegs && s * p.tiles <= (here < room ? here : room); ++s) {
+        const int steps = (p.chunks + s * kSegRanks - 1) / (s * kSegRanks);
+        if (steps < 2) break;
+        const float t = cost.passes * (kPass + (float)steps * wave(cost, fits, p.tiles * s, kSegRanks));
+        if (t < least) { least = t; p.ranks = kSegRanks; p.segs = s; }
     }
     const int steps = (p.chunks + p.ranks - 1) / p.ranks;
     p.seg_chunks = (steps + p.segs - 1) / p.segs * p.ranks;
@@ -985,7 +1000,7 @@ Plan plan_of(const kda_recurrence_shape* sh, bool backward) {
 // The workspace: the status word and the segments' flags; what segments do to states; the blocks' shares of dA_log.
 // Enough for any plan: segments times tiles are at most an eighth of the blocks that run at once, and so are their
 // shares but where there is one segment.
-constexpr size_t kSegBytes = (size_t)kSMs * 4 / kMostRanks * kCh / 2 * sizeof(float4);
+constexpr size_t kSegBytes = (size_t)kSMs * kMostPerSM / kSegRanks * kCh / 2 * sizeof(float4);
 size_t bytes_of(const kda_recurrence_shape* sh, bool backward) {
     if (!backward) return 1024 + kSegBytes;
     const size_t one = (size_t)kMostRanks * sh->D * sizeof(float), many = (size_t)kSMs * 2 * kCh * sizeof(float);
@@ -1022,28 +1037,56 @@ template <bool kBwd> Kernel pick(bool bf16, bool vec, bool total) {
                : (total ? kernel_of<kBwd, float, false, true>() : kernel_of<kBwd, float, false, false>());
 }
 
-constexpr size_t smem_of(bool backward, size_t element, bool total) {
-    const size_t tile = kTile * element;
+constexpr size_t smem_of(bool backward, size_t element, bool total, int ranks) {
+    const size_t tile = kTile * element, sums = ranks > 1 ? 2 * ranks * 32 * sizeof(float4) : 0;
     constexpr int fwd = kBlock / kFwdTok, bwd = kBlock / kBwdTok;
-    if (!backward) return kBytes<Shares<fwd>> + 3 * tile;
-    return kBytes<Shares<bwd>> + kBytes<Ahead<bwd>> + (total ? 2 : 4) * (element == 2 ? 2 : 1) * tile;
+    if (!backward) return (total ? kBytes<Shares<fwd, true>> : kBytes<Shares<fwd, false>>) + 3 * tile + sums;
+    return (total ? kBytes<Shares<bwd, true>> : kBytes<Shares<bwd, false>>) + kBytes<Ahead<bwd>> + (total ? 2 : 4) * (element == 2 ? 2 : 1) * tile + sums;
 }
 
-// The kernels' limits on shared memory are set once for each device.
-kda_status allow_shared(const char* where) {
+// Once for each device: the kernels' limits on shared memory and clusters, and what fits.
+kda_status set_up(const char* where, const Fits** fits) {
     static std::atomic<uint64_t> done{0};
+    static Fits of_device[64];
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return launched(where);
+    Fits& at = of_device[device & 63];
+    *fits = &at;
     const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return KDA_OK;
+    if (done.load(std::memory_order_acquire) & bit) return KDA_OK;
+    constexpr int kRoom = 200 << 10;           // of one block on an SM, beside the registers and threads of kMostPerSM of them
+    const void* const one = reinterpret_cast<const void*>(pick<false>(true, true, false));
+    if (cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom) != cudaSuccess ||
+        cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return launched(where);
+    constexpr int room[kMostPerSM] = {kRoom, 100 << 10, 70 << 10, (int)smem_of(false, 2, false, kMostRanks)};     // so that m blocks fit
+    for (int m = 1; m <= kMostPerSM; ++m)
+        for (int r = 1; r <= kMostRanks; ++r) {
+            cudaLaunchAttribute cluster{};
+            cluster.id = cudaLaunchAttributeClusterDimension;
+            cluster.val.clusterDim.x = (unsigned)r;
+            cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+            cudaLaunchConfig_t c{};
+            c.gridDim = dim3((unsigned)r);
+            c.blockDim = dim3((unsigned)kFwdThreads);
+            c.dynamicSmemBytes = (size_t)room[m - 1];
+            c.attrs = &cluster;
+            c.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, one, &c) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;                         // none of this size
+            }
+            at[m - 1][r].store((int16_t)(n < 4096 ? n : 4096), std::memory_order_relaxed);
+        }
     for (int k = 0; k < 16; ++k) {
         const bool bwd = k & 1, bf16 = k & 2, vec = k & 4, total = k & 8;
-        const Kernel f = bwd ? pick<true>(bf16, vec, total) : pick<false>(bf16, vec, total);
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_of(bwd, bf16 ? 2 : 4, total)) != cudaSuccess)
+        const void* const f = reinterpret_cast<const void*>(bwd ? pick<true>(bf16, vec, total) : pick<false>(bf16, vec, total));
+        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bwd, bf16 ? 2 : 4, total, kMostRanks)) != cudaSuccess ||
+            cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return launched(where);
     }
-    done.fetch_or(bit, std::memory_order_relaxed);
+    done.fetch_or(bit, std::memory_order_release);
     return KDA_OK;
 }
 
@@ -1101,8 +1144,6 @@ kda_status row_map(CUtensorMap* map, const void* p, int64_t D, int64_t tokens, i
 }
 
 template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, const Plan& p, RecArgs& a, bool vec, cudaStream_t s, const char* where) {
-    const kda_status st = allow_shared(where);
-    if (st != KDA_OK) return st;
     const bool bf16 = sh->dtype == KDA_BF16;
     a.chunks = p.chunks; a.seg_chunks = p.seg_chunks; a.ranks = p.ranks;
     a.seg = reinterpret_cast<float4*>(a.ws + 1024);
@@ -1122,8 +1163,8 @@ template <bool kBwd> kda_status run(const kda_recurrence_shape* sh, const Plan& 
         if (ms != KDA_OK) return ms;
     }
     const int threads = kBwd ? kBwdThreads : kFwdThreads;
-    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), threads, p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true), false, s, a, m);
-    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false), !kBwd && p.segs > 1, s, a, m);
+    if (p.segs > 1) launch_clusters(pick<kBwd>(bf16, vec, true), threads, p, p.segs - 1, smem_of(kBwd, bf16 ? 2 : 4, true, p.ranks), false, s, a, m);
+    launch_clusters(pick<kBwd>(bf16, vec, false), threads, p, p.segs, smem_of(kBwd, bf16 ? 2 : 4, false, p.ranks), !kBwd && p.segs > 1, s, a, m);
     return launched(where);
 }
 
@@ -1156,11 +1197,14 @@ extern "C" kda_status kda_recurrence_fwd(const kda_recurrence_shape* shape, cons
     for (const float* p : {A_log, h0, static_cast<const float*>(hT), static_cast<const float*>(kept)})
         if (misaligned(p)) return KDA_ERR_ALIGN;
     if (hT && hT == h0) return KDA_ERR_UNSUPPORTED;
+    const Fits* fits = nullptr;
+    const kda_status us = set_up("kda_recurrence_fwd launch", &fits);
+    if (us != KDA_OK) return us;
     RecArgs a = args_of(shape);
     a.x = x; a.g = g_raw; a.i = i_raw; a.y = y; a.A_log = A_log; a.h0 = h0; a.cu = cu_seqlens; a.hT = hT; a.kept = kept;
     a.ws = static_cast<uint8_t*>(workspace);
     const bool vec = whole_units(shape, {x, g_raw, i_raw, y}, {a.sx, a.sg, a.si, a.sy});
-    return run<false>(shape, plan_of(shape, false), a, vec, static_cast<cudaStream_t>(stream), "kda_recurrence_fwd launch");
+    return run<false>(shape, plan_of(shape, false, *fits), a, vec, static_cast<cudaStream_t>(stream), "kda_recurrence_fwd launch");
 }
 
 extern "C" kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,
@@ -1177,11 +1221,14 @@ extern "C" kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, cons
     for (const float* p : {A_log, h0, dhT, kept, static_cast<const float*>(dA_log), static_cast<const float*>(dh0)})
         if (misaligned(p)) return KDA_ERR_ALIGN;
     if (dh0 && dh0 == dhT) return KDA_ERR_UNSUPPORTED;
+    const Fits* fits = nullptr;
+    const kda_status us = set_up("kda_recurrence_bwd launch", &fits);
+    if (us != KDA_OK) return us;
     RecArgs a = args_of(shape);
     a.x = x; a.g = g_raw; a.i = i_raw; a.dy = dy; a.A_log = A_log; a.h0 = h0; a.dhT = dhT; a.cu = cu_seqlens;
     a.kept = const_cast<float*>(kept); a.dx = dx; a.dg = dg_raw; a.di = di_raw; a.dh0 = dh0;
     a.ws = static_cast<uint8_t*>(workspace);
-    const Plan p = plan_of(shape, true);
+    const Plan p = plan_of(shape, true, *fits);
     const int parts = p.segs * p.ranks;
     float* const shares = reinterpret_cast<float*>(a.ws + 1024 + kSegBytes);
     a.part = !dA_log || parts == 1 ? dA_log : shares;

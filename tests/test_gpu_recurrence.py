@@ -112,6 +112,13 @@ def test_long_sequences_of_few_channels(lens, D, dtype):
     verify(c, run(c))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,D", [([1024], 520), ([700, 0, 333, 1, 66], 1024), ([3000, 40], 1540), ([2000], 2500), ([64] * 17, 1001)])
+def test_clusters_of_many_blocks(lens, D, dtype):
+    c = make(lens, D, dtype)
+    verify(c, run(c))
+
+
 def test_many_channels():
     c = make([150, 37], 6000)
     verify(c, run(c))
