@@ -299,7 +299,8 @@ kda_status kda_recurrence_fwd(const kda_recurrence_shape* shape, const void* x, 
 
 /* Gradients of sum_t <y_t, dy_t> + <hT, dhT> with the forward's inputs and `kept`: dx, dg_raw,
  * di_raw in the tokens' type, dA_log [D] (NULL = not wanted; written, not accumulated, summed in a
- * fixed order), dh0 [N, D] (NULL = not wanted). Bitwise reproducible. dx, dg_raw, di_raw may be
+ * fixed order), dh0 [N, D] (NULL = not wanted). Bitwise reproducible on one GPU (how tokens are cut among its
+ * blocks, and so roundings, follow how its SMs are grouped). dx, dg_raw, di_raw may be
  * any of x, g_raw, i_raw, dy (same stride, each another one); otherwise outputs that overlap
  * inputs are not allowed (dh0 = dhT gives KDA_ERR_UNSUPPORTED). */
 kda_status kda_recurrence_bwd(const kda_recurrence_shape* shape, const void* x, const void* g_raw, const void* i_raw,

@@ -7,11 +7,11 @@
 // and rotary/2 + 4 p .. of unit p where pairs are half of the rotated columns apart, 8 p .. 8 p + 7 elsewhere; only the
 // row's sums go through shuffles. A warp takes a token (or a share of its heads, where tokens are few), so that sines and
 // cosines are computed once for many heads.
-// Measured (us, and times the floor): forward bf16 8192 tokens x (96 + 96) heads of 128 140 (1.17), 8192 x (32 + 8) 36 (1.45), heads
-// of 64 69 (1.16), fp32 8192 x (32 + 32) of 96 78 (1.3); backward bf16 8192 x (96 + 96) 199 (1.10), 8192 x (32 + 8) 54 (1.44), fp32 4099 x
-// (32 + 8) 50 (1.32). What bounds them: the issue slots (67% at 8192 x (32 + 8) forward, 24 instructions an element, a third of them
+// Measured (us, and times the floor): forward bf16 8192 tokens x (96 + 96) heads of 128 137 (1.14), 8192 x (32 + 8) 37 (1.5), heads
+// of 64 70 (1.17), fp32 8192 x (32 + 32) of 96 80 (1.3); backward bf16 8192 x (96 + 96) 200 (1.11), 8192 x (32 + 8) 55 (1.47), fp32 4099 x
+// (32 + 8) 50 (1.33). What bounds them: the issue slots (67% at 8192 x (32 + 8) forward, 24 instructions an element, a third of them
 // the walk over blocks and tokens) beside HBM. Loads straight to registers, 4 rows of a lane in flight, took 320 and 617 us
-// where this takes 140 and 199: two thirds of the time they waited.
+// where this takes 137 and 200: two thirds of the time they waited.
 // An angle is a fraction of a turn in 64-bit fixed point: inv_freq / 2 pi comes from its 24 bits and a 128-bit
 // constant, and position times that, modulo 2^64, is exact at any position.
 #include <atomic>

@@ -20,10 +20,10 @@
 //  - The backward needs the states before its tokens: the forward keeps the state before every 64th token (a
 //    thirty-second of a bf16 tensor), each warp's own scan forwards gives the rest.
 // Measured (us, and times the floor): forward bf16 8192 x 12288 163 (1.35), 8192 x 4096 71 (1.8), packed six sequences 8192 x
-// 4096 with states 77 (1.9), 8192 x 1024 34 (3.4), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 364 (1.7), 8192 x 4096 142 (2.0),
-// 8192 x 1024 59 (3.3), fp32 8192 x 4096 174 (1.24), 65537 x 256 132 (1.9). Rows that are not whole 16-byte units, lane by lane:
-// forward 8192 x 4001 105 (2.7), backward 199 (2.9). What bounds them is neither DRAM (half of its peak) nor a pipe (issue
-// slots 54%, MUFU a quarter, FMA a third): 16 warps of 128 registers an SM wait for one another at every step (the dependent
+// 4096 with states 76 (1.9), 8192 x 1024 34 (3.4), fp32 8192 x 4096 91 (1.13); backward bf16 8192 x 12288 361 (1.7), 8192 x 4096 140 (2.0),
+// 8192 x 1024 58 (3.3), fp32 8192 x 4096 172 (1.22), 65537 x 256 128 (1.8). Rows that are not whole 16-byte units, lane by lane:
+// forward 8192 x 4001 104 (2.6), backward 198 (2.9). What bounds them is neither DRAM (half of its peak) nor a pipe (issue
+// slots 55%, MUFU a quarter, FMA a third): 16 warps of 128 registers an SM wait for one another at every step (the dependent
 // arithmetic of a warp's tokens, the block's barrier, 0.5 us of exchange in a cluster); blocks without a cluster
 // take 1.23 (forward) and 1.5 times the floor, which is what a step costs alone.
 #include <atomic>
