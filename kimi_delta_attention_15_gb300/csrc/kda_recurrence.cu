@@ -764,12 +764,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rec_bwd_kernel(const __grid_co
                         if constexpr (!with.value) h = advance(h, n[j], b[j]);
                     }
                 }
-                if constexpr (with.value && !kTotal)
-                    at_tokens<kTok, true, false>(ev.starts, [&](int j, auto mark) {
-                        if constexpr (mark.value)
-                            if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
-                        h = advance(h, n[j], b[j]);
-                    });
+                if constexpr (!kTotal) {
+                    if constexpr (with.value)
+                        at_tokens<kTok, true, false>(ev.starts, [&](int j, auto mark) {
+                            if constexpr (mark.value)
+                                if (ev.starts >> j & 1) h = load_state<kVec>(a.h0, ev.of(j), c, a.D);
+                            h = advance(h, n[j], b[j]);
+                        });
+                }
                 at_tokens<kTok, with.value, true>(ev.ends, [&](int j, auto mark) {
                     if constexpr (mark.value)
                         if (ev.ends >> j & 1) G = load_state<kVec>(a.dhT, ev.of(j), c, a.D);
