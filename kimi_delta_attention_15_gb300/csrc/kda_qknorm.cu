@@ -8,10 +8,10 @@
 // row's sums go through shuffles. A warp takes a token (or a share of its heads, where tokens are few), so that sines and
 // cosines are computed once for many heads.
 // Measured (us, and times the floor): forward bf16 8192 tokens x (96 + 96) heads of 128 137 (1.14), 8192 x (32 + 8) 37 (1.5), heads
-// of 64 70 (1.17), fp32 8192 x (32 + 32) of 96 80 (1.3); backward bf16 8192 x (96 + 96) 200 (1.11), 8192 x (32 + 8) 55 (1.47), fp32 4099 x
-// (32 + 8) 50 (1.33). What bounds them: the issue slots (67% at 8192 x (32 + 8) forward, 24 instructions an element, a third of them
+// of 64 70 (1.17), fp32 8192 x (32 + 32) of 96 80 (1.3); backward bf16 8192 x (96 + 96) 201 (1.11), 8192 x (32 + 8) 54 (1.44), fp32 4099 x
+// (32 + 8) 50 (1.32). What bounds them: the issue slots (67% at 8192 x (32 + 8) forward, 24 instructions an element, a third of them
 // the walk over blocks and tokens) beside HBM. Loads straight to registers, 4 rows of a lane in flight, took 320 and 617 us
-// where this takes 137 and 200: two thirds of the time they waited.
+// where this takes 137 and 201: two thirds of the time they waited.
 // An angle is a fraction of a turn in 64-bit fixed point: inv_freq / 2 pi comes from its 24 bits and a 128-bit
 // constant, and position times that, modulo 2^64, is exact at any position.
 #include <atomic>
@@ -117,6 +117,7 @@ struct QkArgs {
     const float* inv_freq;
     float* part;         // [blocks of the grid][2][head] sums of the weights' gradients, or NULL
     int64_t tokens;
+    int64_t whole, items;      // backward: the tokens that are not shared, before the others; they and the shares
     int head, rotary, lanes, share, shares;   // lanes of a row, a power of two; blocks to a share of a token, shares to a token
     float eps, inv_head;
 };
@@ -154,9 +155,14 @@ struct Lane {
     }
 };
 
-// A warp's blocks in turn: shares of tokens, item, item + step, .., and the blocks of each. p and q are where the
+// The token of an item: the first a.whole tokens (backward) are items, the others' shares the ones after them.
+template <bool kBwd> __device__ __forceinline__ int64_t token_of(const QkArgs& a, int64_t it) {
+    if constexpr (!kBwd) return a.shares == 1 ? it : it / a.shares;
+    else return a.shares == 1 || it < a.whole ? it : a.whole + (it - a.whole) / a.shares;
+}
+// A warp's blocks in turn: items, item, item + step, .., and the blocks of each. p and q are where the
 // block's rows start in two of the side's tensors (x and dy to load from, out to store to).
-template <typename T, bool kOut> struct Walk {
+template <typename T, bool kBwd, bool kOut> struct Walk {
     int64_t item, t;
     int left, k, heads;      // blocks left of the share, side, heads left of the side
     T *p, *q;
@@ -172,18 +178,27 @@ template <typename T, bool kOut> struct Walk {
         item = it;
         t = it;
         int b = 0;
-        if (a.shares > 1) {
-            t = it / a.shares;
-            b = (int)(it - t * a.shares) * a.share;
-        }
         const int n = a.side[0].blocks;
-        left = min(a.share, n + a.side[1].blocks - b);
+        if constexpr (kBwd) {
+            t = token_of<true>(a, it);
+            left = n + a.side[1].blocks;
+            if (it >= a.whole) {
+                b = (int)(it - a.whole - (t - a.whole) * a.shares) * a.share;
+                left = min(a.share, left - b);
+            }
+        } else {
+            if (a.shares > 1) {
+                t = it / a.shares;
+                b = (int)(it - t * a.shares) * a.share;
+            }
+            left = min(a.share, n + a.side[1].blocks - b);
+        }
         if (b < n) open(a, 0, b, rows);
         else open(a, 1, b - n, rows);
     }
     __device__ __forceinline__ bool next(const QkArgs& a, int64_t step, int rows) {      // whether another share begins
         if (--left == 0) {
-            if (item + step < a.tokens * a.shares) start(a, item + step, rows);
+            if (item + step < (kBwd ? a.items : a.tokens * a.shares)) start(a, item + step, rows);
             else item += step;
             return true;
         }
@@ -208,8 +223,8 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kWarps * kRing) + warp * kN;
     const T* const zeros = reinterpret_cast<const T*>(smem + kWarps * kRing + kWarps * kN * sizeof(uint64_t));
     const int rows = kR * (32 / a.lanes);            // of a block
-    const int64_t items = a.tokens * a.shares, step = (int64_t)gridDim.x * kWarps, mine = (int64_t)blockIdx.x * kWarps + warp;
-    Walk<T, false> ahead;
+    const int64_t items = kBwd ? a.items : a.tokens * a.shares, step = (int64_t)gridDim.x * kWarps, mine = (int64_t)blockIdx.x * kWarps + warp;
+    Walk<T, kBwd, false> ahead;
     ahead.item = mine;
     if (mine < items) ahead.start(a, mine, rows);
     auto fetch = [&](int stage) {        // by one lane: the block that `ahead` stands at
@@ -232,7 +247,7 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
     const Lane l(a, kInterleaved);
     Pairs dw = {}, other = {};       // sums of the weights' gradients, of the side at hand and of the other
     int summed = 0;
-    Walk<T, true> at;
+    Walk<T, kBwd, true> at;
     at.item = mine;
     if (mine < items) at.start(a, mine, rows);
     int stage = 0, parity = 0;
@@ -246,7 +261,7 @@ template <typename T, bool kInterleaved, bool kBwd> __global__ void __launch_bou
     while (at.item < items) {
         if (fresh) {
             l.angles(position, cs, sn);
-            const int64_t after = a.shares == 1 ? at.item + step : (at.item + step) / a.shares;
+            const int64_t after = token_of<kBwd>(a, at.item + step);
             position = at.item + step < items && a.rotary ? a.positions[after] : 0;     // the next share's
             side = -1;
         }
@@ -464,21 +479,26 @@ QkArgs args_of(const kda_qknorm_shape* sh, bool backward) {
     a.side[1].heads = sh->k_heads;
     for (Side& s : a.side) s.blocks = (s.heads + rows - 1) / rows;
     // Shares of a token's blocks for different warps: as many as fill the GPU where tokens are few, else those that leave
-    // the least work to the warp with the most; a share costs about four blocks more, for its angles and weights. (8192
-    // tokens of 96 heads on 3648 warps, three rounds for 2.2, took 144 us, as halves, five rounds for 4.5, 141.)
+    // the least work to the warp with the most; a share costs about four blocks more, for its angles and weights. Either all
+    // tokens are cut or, backward, those that are left after rounds of whole tokens (8192 tokens of 32 + 8 heads 56 -> 54 us, of 32 + 32 80 ->
+    // 76, 3000 of 96 + 96 87 -> 80; forward, where three blocks share an SM's registers, its bookkeeping cost more than it gave,
+    // 138 -> 149 us at 8192 x (96 + 96)).
     const int64_t warps = (int64_t)kSMs * (backward ? kBlocksPerSM<true> : kBlocksPerSM<false>) * kWarps;
     const int blocks = a.side[0].blocks + a.side[1].blocks;
     int64_t least = 0;
     for (int s = 1; s <= 16 && s <= blocks; ++s) {
         const int share = (blocks + s - 1) / s, shares = (blocks + share - 1) / share;
-        const int64_t t = (a.tokens * shares + warps - 1) / warps * (share + 4);
-        if (s == 1 || t < least) { least = t; a.share = share; a.shares = shares; }
+        for (const int64_t rounds : {int64_t(0), backward ? a.tokens / warps : 0}) {
+            const int64_t t = rounds * (blocks + 4) + ((a.tokens - rounds * warps) * shares + warps - 1) / warps * (share + 4);
+            if ((s == 1 && rounds == 0) || t < least) { least = t; a.share = share; a.shares = shares; a.whole = rounds * warps; }
+        }
     }
-    if (a.tokens * blocks <= warps) a.share = 1, a.shares = blocks;
+    if (a.tokens * blocks <= warps) a.share = 1, a.shares = blocks, a.whole = 0;
+    a.items = a.whole + (a.tokens - a.whole) * a.shares;
     return a;
 }
 unsigned grid_of(const QkArgs& a, bool backward) {
-    const int64_t blocks = (a.tokens * a.shares + kWarps - 1) / kWarps;
+    const int64_t blocks = (a.items + kWarps - 1) / kWarps;
     const int64_t most = (int64_t)kSMs * (backward ? kBlocksPerSM<true> : kBlocksPerSM<false>);
     return (unsigned)(blocks < most ? blocks : most);
 }

@@ -84,6 +84,13 @@ def test_many_tokens(interleaved):
     verify(c, run(c, interleaved), interleaved)
 
 
+@pytest.mark.parametrize("T,Hq,Hk,head,dtype", [(2600, 24, 8, 64, BF), (2433, 9, 3, 128, F32), (5000, 12, 12, 72, BF)])
+def test_tokens_left_after_whole_rounds(T, Hq, Hk, head, dtype):
+    """More tokens than warps: the last ones are shared by several."""
+    c = make(T, Hq, Hk, head, head, dtype)
+    verify(c, run(c, True), True)
+
+
 @pytest.mark.parametrize("far", [1 << 31, 1 << 40])
 def test_far_positions(far):
     """Angles of many turns. A fraction of a turn is off by 2^-64 of its position, 2^-24 of a turn at 2^40: four of the eight
